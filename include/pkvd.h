@@ -54,8 +54,9 @@
  *     on the stream: they may start while a preceding kernel that signalled
  *     early completion (griddepcontrol.launch_dependents) still runs.  Before
  *     waiting for it they read only inputs that no kernel of this library
- *     writes (context lengths, block tables, q); everything else (the cache,
- *     slot_mapping, outputs, workspaces) comes after the wait.  A caller's
+ *     writes (context lengths, block tables, rotary frequencies); everything
+ *     else (q, the cache, slot_mapping, outputs, workspaces) comes after the
+ *     wait.  A caller's
  *     own kernel that signals early must not write those inputs of the call
  *     that follows it.
  */
@@ -342,6 +343,94 @@ pkvd_status pkvd_kv_store_prefill(const void* k, const void* v, const int32_t* b
                                   const int32_t* cu_seqlens_k, int32_t num_seqs, int32_t total_q,
                                   int64_t* slot_mapping, const pkvd_cache* cache, void* stream,
                                   int32_t* err_flag);
+
+/*
+ * Rotary positions.  The first rotary_dim dims of a head turn pairwise by the
+ * angle a = position * inv_freq[i] (i < rotary_dim / 2):
+ *   y1 = mscale * (x1 cos a - x2 sin a),  y2 = mscale * (x2 cos a + x1 sin a)
+ * with (x1, x2) the dims (i, i + rotary_dim / 2) (interleaved = 0) or
+ * (2i, 2i + 1) (interleaved = 1); dims from rotary_dim on are copied.  cos and
+ * sin are fp32-accurate at positions up to 2^40 (the angle is reduced in 64-bit
+ * fixed point); the products are fp32, rounded once to the dtype.  The pages
+ * name the step without a body: the rotary kernel (`rope_rotary`) of the
+ * article on a de-frameworked runtime, section 3.1, and the rotary offset of
+ * the cache in nanochat "04 · Engine".
+ */
+typedef struct {
+  const double* inv_freq;   /* device, [rotary_dim / 2], finite; written by no kernel in flight */
+  int32_t rotary_dim;       /* even, 2 .. head_dim */
+  int32_t interleaved;      /* 0 or 1 */
+  float mscale;             /* factor on cos and sin (1, or pkvd_rope_inv_freq's) */
+} pkvd_rope_desc;
+
+/*
+ * pkvd_rope -- q_out[t] and k_out[t] = rows t of q and k rotated by
+ * positions[t] (any int64, negative ones turn backwards).
+ * Inputs: q rows of num_q_heads x head_dim elements `q_stride` elements apart
+ *         (so q, k may be slices of one projected [tokens, q+k+v] tensor), k
+ *         likewise; positions int64 [num_tokens].
+ * Output: q_out, k_out rows at their own strides; each may be its input (same
+ *         pointer and stride: rotated in place), and must not overlap any of
+ *         the other rows.  num_q_heads or num_kv_heads 0: that side is absent
+ *         (NULL).
+ * Requirements: head_dim <= 512 and a multiple of 16 bytes; rows and strides
+ *         16-byte aligned, strides at least heads * head_dim.
+ */
+pkvd_status pkvd_rope(void* q_out, int64_t q_out_stride, const void* q, int64_t q_stride, void* k_out,
+                      int64_t k_out_stride, const void* k, int64_t k_stride, int32_t dtype, int32_t num_tokens,
+                      int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim, const int64_t* positions,
+                      const pkvd_rope_desc* rope, void* stream);
+
+/*
+ * pkvd_rope_store_paged -- pkvd_rope and pkvd_kv_store_paged in one kernel:
+ * row i's query and key turn by the position of its newest token
+ * (context_lens[i] - 1); the query goes to q_out, the key and the (unrotated)
+ * value to the token's cache slot.
+ * Inputs: q, k, v rows at their strides (as pkvd_rope), cache dtype;
+ *         block_tables, context_lens and slot_mapping as in
+ *         pkvd_kv_store_paged.  Slots must be distinct.
+ * Output: q_out (may be q, in place); the cache rows; slot_mapping or NULL.
+ *         A row without a position (context 0, or a negative one, which sets
+ *         PKVD_ERR_CONTEXT) gets a zero query and stores nothing.
+ * Device errors: as pkvd_kv_store_paged (bad block id or length: nothing is
+ *         stored; the query is still rotated).
+ */
+pkvd_status pkvd_rope_store_paged(void* q_out, int64_t q_out_stride, const void* q, int64_t q_stride, const void* k,
+                                  int64_t k_stride, const void* v, int64_t v_stride, int32_t num_q_heads,
+                                  const int32_t* block_tables, int32_t max_blocks_per_seq,
+                                  const int32_t* context_lens, int32_t num_seqs, const pkvd_rope_desc* rope,
+                                  int64_t* slot_mapping, const pkvd_cache* cache, void* stream, int32_t* err_flag);
+
+/*
+ * pkvd_rope_store_prefill -- the same for the rows of a varlen prefill batch
+ * (pkvd_kv_store_prefill's arguments and positions).  Rows t >=
+ * cu_seqlens_q[num_seqs] and rows of a sequence with q_len > k_len
+ * (PKVD_ERR_CONTEXT) leave q_out and the cache as they were.
+ */
+pkvd_status pkvd_rope_store_prefill(void* q_out, int64_t q_out_stride, const void* q, int64_t q_stride, const void* k,
+                                    int64_t k_stride, const void* v, int64_t v_stride, int32_t num_q_heads,
+                                    const int32_t* block_tables, int32_t max_blocks_per_seq,
+                                    const int32_t* cu_seqlens_q, const int32_t* cu_seqlens_k, int32_t num_seqs,
+                                    int32_t total_q, const pkvd_rope_desc* rope, int64_t* slot_mapping,
+                                    const pkvd_cache* cache, void* stream, int32_t* err_flag);
+
+/*
+ * pkvd_rope_inv_freq -- the inverse frequencies base^(-2i / rotary_dim),
+ * scaled for contexts `factor` times the length a model was trained on
+ * (host arrays; copy inv_freq to the device once):
+ *   PKVD_ROPE_PLAIN   as they are;
+ *   PKVD_ROPE_LINEAR  divided by factor (position interpolation);
+ *   PKVD_ROPE_NTK     base * factor^(rotary_dim / (rotary_dim - 2));
+ *   PKVD_ROPE_PARTS   by parts (Peng et al., "YaRN", 2023): pairs that turn
+ *                     more than beta_fast times over original_len tokens are
+ *                     kept, those that turn less than beta_slow times divided
+ *                     by factor, a linear ramp between; *mscale = 0.1
+ *                     ln(factor) + 1.
+ * *mscale is 1 otherwise.  Arguments a scaling does not name are ignored.
+ */
+typedef enum { PKVD_ROPE_PLAIN = 0, PKVD_ROPE_LINEAR = 1, PKVD_ROPE_NTK = 2, PKVD_ROPE_PARTS = 3 } pkvd_rope_scaling;
+pkvd_status pkvd_rope_inv_freq(double* inv_freq, float* mscale, int32_t rotary_dim, double base, int32_t scaling,
+                               double factor, int64_t original_len, double beta_fast, double beta_slow);
 
 /*
  * pkvd_prefill_attention -- varlen causal attention of a prefill batch over

@@ -1,6 +1,7 @@
 """ctypes declarations of include/pkvd.h and tensor-to-argument helpers."""
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -13,8 +14,8 @@ ERR_BLOCK_ID, ERR_SLOT, ERR_CONTEXT, ERR_TIMEOUT = 1, 2, 4, 8
 NO_SPACE = 6
 _DTYPES = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
 
-c_void_p, c_int32, c_int64, c_size_t, c_float = (ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64,
-                                                 ctypes.c_size_t, ctypes.c_float)
+c_void_p, c_int32, c_int64, c_size_t, c_float, c_double = (ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64,
+                                                           ctypes.c_size_t, ctypes.c_float, ctypes.c_double)
 
 
 class PkvdCache(ctypes.Structure):
@@ -22,6 +23,10 @@ class PkvdCache(ctypes.Structure):
                 ("block_size", c_int32), ("num_blocks", c_int64), ("num_kv_heads", c_int32),
                 ("head_dim", c_int32), ("block_stride", c_int64), ("token_stride", c_int64),
                 ("head_stride", c_int64)]
+
+
+class PkvdRope(ctypes.Structure):
+    _fields_ = [("inv_freq", c_void_p), ("rotary_dim", c_int32), ("interleaved", c_int32), ("mscale", c_float)]
 
 
 class PkvdError(RuntimeError):
@@ -42,6 +47,17 @@ SIGNATURES = {
                                       ctypes.POINTER(PkvdCache), c_void_p, c_void_p]),
     "pkvd_kv_store_prefill": (c_int32, [c_void_p, c_void_p, c_void_p, c_int32, c_void_p, c_void_p, c_int32,
                                         c_int32, c_void_p, ctypes.POINTER(PkvdCache), c_void_p, c_void_p]),
+    "pkvd_rope": (c_int32, [c_void_p, c_int64, c_void_p, c_int64, c_void_p, c_int64, c_void_p, c_int64, c_int32,
+                            c_int32, c_int32, c_int32, c_int32, c_void_p, ctypes.POINTER(PkvdRope), c_void_p]),
+    "pkvd_rope_store_paged": (c_int32, [c_void_p, c_int64, c_void_p, c_int64, c_void_p, c_int64, c_void_p, c_int64,
+                                        c_int32, c_void_p, c_int32, c_void_p, c_int32, ctypes.POINTER(PkvdRope),
+                                        c_void_p, ctypes.POINTER(PkvdCache), c_void_p, c_void_p]),
+    "pkvd_rope_store_prefill": (c_int32, [c_void_p, c_int64, c_void_p, c_int64, c_void_p, c_int64, c_void_p, c_int64,
+                                          c_int32, c_void_p, c_int32, c_void_p, c_void_p, c_int32, c_int32,
+                                          ctypes.POINTER(PkvdRope), c_void_p, ctypes.POINTER(PkvdCache), c_void_p,
+                                          c_void_p]),
+    "pkvd_rope_inv_freq": (c_int32, [c_void_p, c_void_p, c_int32, c_double, c_int32, c_double, c_int64, c_double,
+                                     c_double]),
     "pkvd_prefill_attention": (c_int32, [c_void_p, c_void_p, ctypes.POINTER(PkvdCache), c_void_p, c_int32,
                                          c_void_p, c_void_p, c_int32, c_int32, c_int32, c_int32, c_float,
                                          c_int32, c_void_p, c_void_p]),
@@ -130,6 +146,55 @@ def stream_handle(stream, like: torch.Tensor):
     if stream is None:
         stream = torch.cuda.current_stream(like.device)
     return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
+
+
+_HERE = contextlib.nullcontext()
+
+
+def on_stream(stream, device: torch.device):
+    """Context in which `device` is current and allocations and launches go to
+    `stream` (a torch stream or a raw handle; None: the device's current one),
+    so what a call allocates belongs to the stream that uses it."""
+    if stream is None:
+        return _HERE if device.index == torch.cuda.current_device() else torch.cuda.device(device)
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream), device=device) if int(stream) else \
+            torch.cuda.default_stream(device)
+    if stream.device != device:
+        raise ValueError("the stream belongs to another device than the tensors")
+    return torch.cuda.stream(stream)
+
+
+def rows3(t: torch.Tensor, name: str, like: torch.Tensor | None = None) -> int:
+    """Check [tokens, heads, dim] rows whose heads lie side by side (a token's
+    row may be a slice of a longer one); returns the token stride in elements."""
+    if t.dim() != 3 or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor [tokens, heads, dim]")
+    T, H, D = t.shape
+    if like is not None and (t.dtype != like.dtype or t.device != like.device):
+        raise ValueError(f"{name} must have the dtype and device of the other tensors")
+    st = t.stride()
+    if (D > 1 and st[2] != 1) or (H > 1 and st[1] != D):
+        raise ValueError(f"{name}: the heads of a token must be contiguous")
+    return st[0] if T > 1 else max(H * D, 1)
+
+
+def array(t: torch.Tensor, name: str, dtype: torch.dtype, device: torch.device, shape: tuple) -> int:
+    """Check a contiguous argument array (None in shape: any size) and give its pointer."""
+    if t.dtype != dtype or t.device != device or t.dim() != len(shape) or not t.is_contiguous() or \
+            any(want is not None and have != want for have, want in zip(t.shape, shape)):
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape "
+                         f"{[('any' if n is None else n) for n in shape]} on {device}")
+    return t.data_ptr()
+
+
+def err_ptr(err, device: torch.device):
+    """The optional error flag: one int32 on the call's device."""
+    if err is None:
+        return None
+    if err.dtype != torch.int32 or err.device != device or err.numel() < 1:
+        raise ValueError(f"err must be an int32 tensor on {device}")
+    return err.data_ptr()
 
 
 def cache_desc(k_cache: torch.Tensor, v_cache: torch.Tensor) -> PkvdCache:

@@ -154,6 +154,196 @@ pkvd_status pkvd_kv_store_prefill(const void* k, const void* v, const int32_t* b
                                            static_cast<cudaStream_t>(stream), err_flag));
 }
 
+}  // extern "C"
+
+namespace {
+
+// Shared checks of a rotary call; row strides are at least a row and multiples
+// of 16 bytes, and so are the row pointers.
+pkvd_status check_rope(const pkvd_rope_desc* r, int dtype, int num_q_heads, int num_kv_heads, int head_dim) {
+  if (!valid_dtype(dtype)) return PKVD_UNSUPPORTED_DTYPE;
+  if (!r || !r->inv_freq || !std::isfinite(r->mscale) || (r->interleaved != 0 && r->interleaved != 1))
+    return PKVD_INVALID_ARG;
+  if (num_q_heads < 0 || num_kv_heads < 0 || head_dim <= 0 || num_q_heads > 65536 || num_kv_heads > 65536)
+    return PKVD_INVALID_ARG;
+  if (head_dim > kRopeMaxDim || (head_dim * esize(dtype)) % 16) return PKVD_UNSUPPORTED_SHAPE;
+  if (r->rotary_dim < 2 || r->rotary_dim > head_dim) return PKVD_INVALID_ARG;
+  if (r->rotary_dim % 2) return PKVD_UNSUPPORTED_SHAPE;
+  if (reinterpret_cast<uintptr_t>(r->inv_freq) % 8) return PKVD_UNSUPPORTED_SHAPE;
+  return PKVD_OK;
+}
+
+pkvd_status check_rope_rows(const void* p, int64_t stride, int heads, int head_dim, int dtype) {
+  if (!p) return PKVD_INVALID_ARG;
+  if (stride < (int64_t)heads * head_dim) return PKVD_INVALID_ARG;
+  if (!aligned16(p) || (stride * esize(dtype)) % 16) return PKVD_UNSUPPORTED_SHAPE;
+  return PKVD_OK;
+}
+
+void rope_common(RopeArgs* a, const pkvd_rope_desc* r, int dtype, int num_q_heads, int num_kv_heads, int head_dim) {
+  *a = RopeArgs{};
+  a->dtype = dtype;
+  a->num_q_heads = num_q_heads;
+  a->num_kv_heads = num_kv_heads;
+  a->head_dim = head_dim;
+  a->rotary_dim = r->rotary_dim;
+  a->interleaved = r->interleaved;
+  a->mscale = r->mscale;
+  a->inv_freq = r->inv_freq;
+}
+
+// The rows of a fused store: q may be absent (no query heads).
+pkvd_status rope_store_args(RopeArgs* a, void* q_out, int64_t q_out_stride, const void* q, int64_t q_stride,
+                            const void* k, int64_t k_stride, const void* v, int64_t v_stride, int num_q_heads,
+                            const pkvd_rope_desc* rope, const pkvd_cache* cache) {
+  const int hkv = cache->num_kv_heads, D = cache->head_dim, dt = cache->dtype;
+  pkvd_status s;
+  if (num_q_heads > 0) {
+    if ((s = check_rope_rows(q, q_stride, num_q_heads, D, dt)) != PKVD_OK) return s;
+    if ((s = check_rope_rows(q_out, q_out_stride, num_q_heads, D, dt)) != PKVD_OK) return s;
+  }
+  if ((s = check_rope_rows(k, k_stride, hkv, D, dt)) != PKVD_OK) return s;
+  if ((s = check_rope_rows(v, v_stride, hkv, D, dt)) != PKVD_OK) return s;
+  rope_common(a, rope, dt, num_q_heads, hkv, D);
+  a->q_out = q_out;
+  a->q = q;
+  a->k_out = cache->k_base;
+  a->k = k;
+  a->v_out = cache->v_base;
+  a->v = v;
+  a->q_stride = q_stride;
+  a->q_out_stride = q_out_stride;
+  a->k_stride = k_stride;
+  a->v_stride = v_stride;
+  a->block_stride = cache->block_stride;
+  a->token_stride = cache->token_stride;
+  a->head_stride = cache->head_stride;
+  a->num_blocks = cache->num_blocks;
+  a->block_size = cache->block_size;
+  return PKVD_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+pkvd_status pkvd_rope(void* q_out, int64_t q_out_stride, const void* q, int64_t q_stride, void* k_out,
+                      int64_t k_out_stride, const void* k, int64_t k_stride, int32_t dtype, int32_t num_tokens,
+                      int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim, const int64_t* positions,
+                      const pkvd_rope_desc* rope, void* stream) {
+  if (num_tokens < 0) return PKVD_INVALID_ARG;
+  pkvd_status s = check_rope(rope, dtype, num_q_heads, num_kv_heads, head_dim);
+  if (s != PKVD_OK) return s;
+  if (num_tokens == 0 || (num_q_heads == 0 && num_kv_heads == 0)) return PKVD_OK;
+  if (!positions) return PKVD_INVALID_ARG;
+  if (reinterpret_cast<uintptr_t>(positions) % 8) return PKVD_UNSUPPORTED_SHAPE;
+  if (num_q_heads > 0) {
+    if ((s = check_rope_rows(q, q_stride, num_q_heads, head_dim, dtype)) != PKVD_OK) return s;
+    if ((s = check_rope_rows(q_out, q_out_stride, num_q_heads, head_dim, dtype)) != PKVD_OK) return s;
+  }
+  if (num_kv_heads > 0) {
+    if ((s = check_rope_rows(k, k_stride, num_kv_heads, head_dim, dtype)) != PKVD_OK) return s;
+    if ((s = check_rope_rows(k_out, k_out_stride, num_kv_heads, head_dim, dtype)) != PKVD_OK) return s;
+  }
+  RopeArgs a;
+  rope_common(&a, rope, dtype, num_q_heads, num_kv_heads, head_dim);
+  a.q_out = q_out;
+  a.q = q;
+  a.k_out = k_out;
+  a.k = k;
+  a.q_stride = q_stride;
+  a.q_out_stride = q_out_stride;
+  a.k_stride = k_stride;
+  a.k_out_stride = k_out_stride;
+  a.positions = positions;
+  return from_cuda(launch_rope(a, num_tokens, static_cast<cudaStream_t>(stream)));
+}
+
+pkvd_status pkvd_rope_store_paged(void* q_out, int64_t q_out_stride, const void* q, int64_t q_stride, const void* k,
+                                  int64_t k_stride, const void* v, int64_t v_stride, int32_t num_q_heads,
+                                  const int32_t* block_tables, int32_t max_blocks_per_seq,
+                                  const int32_t* context_lens, int32_t num_seqs, const pkvd_rope_desc* rope,
+                                  int64_t* slot_mapping, const pkvd_cache* cache, void* stream, int32_t* err_flag) {
+  if (num_seqs < 0) return PKVD_INVALID_ARG;
+  pkvd_status s = check_cache(cache, false);
+  if (s != PKVD_OK) return s;
+  if ((s = check_rope(rope, cache->dtype, num_q_heads, cache->num_kv_heads, cache->head_dim)) != PKVD_OK) return s;
+  if (num_seqs == 0) return PKVD_OK;
+  if (!block_tables || !context_lens || max_blocks_per_seq <= 0) return PKVD_INVALID_ARG;
+  RopeArgs a;
+  s = rope_store_args(&a, q_out, q_out_stride, q, q_stride, k, k_stride, v, v_stride, num_q_heads, rope, cache);
+  if (s != PKVD_OK) return s;
+  a.tables = block_tables;
+  a.max_blocks = max_blocks_per_seq;
+  a.ctx = context_lens;
+  a.num_seqs = num_seqs;
+  a.slots_out = slot_mapping;
+  a.err = err_flag;
+  return from_cuda(launch_rope(a, num_seqs, static_cast<cudaStream_t>(stream)));
+}
+
+pkvd_status pkvd_rope_store_prefill(void* q_out, int64_t q_out_stride, const void* q, int64_t q_stride, const void* k,
+                                    int64_t k_stride, const void* v, int64_t v_stride, int32_t num_q_heads,
+                                    const int32_t* block_tables, int32_t max_blocks_per_seq,
+                                    const int32_t* cu_seqlens_q, const int32_t* cu_seqlens_k, int32_t num_seqs,
+                                    int32_t total_q, const pkvd_rope_desc* rope, int64_t* slot_mapping,
+                                    const pkvd_cache* cache, void* stream, int32_t* err_flag) {
+  if (num_seqs < 0 || total_q < 0) return PKVD_INVALID_ARG;
+  pkvd_status s = check_cache(cache, false);
+  if (s != PKVD_OK) return s;
+  if ((s = check_rope(rope, cache->dtype, num_q_heads, cache->num_kv_heads, cache->head_dim)) != PKVD_OK) return s;
+  if (total_q == 0) return PKVD_OK;
+  if (!cu_seqlens_q || !cu_seqlens_k) return PKVD_INVALID_ARG;
+  if (num_seqs > 0 && (!block_tables || max_blocks_per_seq <= 0)) return PKVD_INVALID_ARG;
+  RopeArgs a;
+  s = rope_store_args(&a, q_out, q_out_stride, q, q_stride, k, k_stride, v, v_stride, num_q_heads, rope, cache);
+  if (s != PKVD_OK) return s;
+  a.tables = block_tables;
+  a.max_blocks = max_blocks_per_seq;
+  a.cu_q = cu_seqlens_q;
+  a.cu_k = cu_seqlens_k;
+  a.num_seqs = num_seqs;
+  a.slots_out = slot_mapping;
+  a.err = err_flag;
+  return from_cuda(launch_rope(a, total_q, static_cast<cudaStream_t>(stream)));
+}
+
+pkvd_status pkvd_rope_inv_freq(double* inv_freq, float* mscale, int32_t rotary_dim, double base, int32_t scaling,
+                               double factor, int64_t original_len, double beta_fast, double beta_slow) {
+  if (!inv_freq || !mscale || rotary_dim < 2 || rotary_dim % 2 || rotary_dim > kRopeMaxDim) return PKVD_INVALID_ARG;
+  if (!std::isfinite(base) || base <= 1.0) return PKVD_INVALID_ARG;
+  if (scaling < PKVD_ROPE_PLAIN || scaling > PKVD_ROPE_PARTS) return PKVD_INVALID_ARG;
+  if (scaling != PKVD_ROPE_PLAIN && !(std::isfinite(factor) && factor >= 1.0)) return PKVD_INVALID_ARG;
+  if (scaling == PKVD_ROPE_PARTS &&
+      !(original_len > 0 && std::isfinite(beta_fast) && std::isfinite(beta_slow) && beta_slow > 0 &&
+        beta_fast > beta_slow))
+    return PKVD_INVALID_ARG;
+  *mscale = 1.f;
+  if (scaling == PKVD_ROPE_NTK && rotary_dim > 2) base *= std::pow(factor, (double)rotary_dim / (rotary_dim - 2));
+  double low = 0, high = 1;
+  if (scaling == PKVD_ROPE_PARTS) {
+    // the pair whose wave turns `n` times over the original length
+    auto pair_of = [&](double n) {
+      return rotary_dim * std::log((double)original_len / (n * 6.283185307179586)) / (2 * std::log(base));
+    };
+    low = std::fmax(std::floor(pair_of(beta_fast)), 0.0);
+    high = std::fmin(std::ceil(pair_of(beta_slow)), (double)(rotary_dim - 1));
+    *mscale = (float)(0.1 * std::log(factor) + 1.0);
+  }
+  for (int i = 0; i < rotary_dim / 2; ++i) {
+    const double f = std::pow(base, -2.0 * i / rotary_dim);
+    double v = f;
+    if (scaling == PKVD_ROPE_LINEAR) v = f / factor;
+    if (scaling == PKVD_ROPE_PARTS) {
+      double ramp = (i - low) / std::fmax(high - low, 1e-3);
+      ramp = ramp < 0 ? 0 : ramp > 1 ? 1 : ramp;
+      v = f * (1 - ramp) + f / factor * ramp;
+    }
+    inv_freq[i] = v;
+  }
+  return PKVD_OK;
+}
+
 pkvd_status pkvd_prefill_attention_ex(void* out, const void* q, const pkvd_cache* cache, const int32_t* block_tables,
                                       int32_t max_blocks_per_seq, const int32_t* cu_seqlens_q,
                                       const int32_t* cu_seqlens_k, int32_t num_seqs, int32_t total_q,

@@ -418,10 +418,11 @@ __global__ void __launch_bounds__(kAttnThreads, 1) paged_decode_partition_kernel
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int cta = blockIdx.x, grid = gridDim.x;
-  // Everything up to the producer's first copy reads only inputs of this call
-  // (context lengths, block tables, q), never memory the previous kernel (the
-  // KV store) writes, so it runs before the dependency wait and overlaps that
-  // kernel; the producer waits before its first cache read.
+  // Everything up to the producer's first copy and the consumers' first q
+  // load reads only inputs of this call (context lengths, block tables), never
+  // memory the previous kernel (the KV store) writes, so it runs before the
+  // dependency wait and overlaps that kernel; the producer waits before its
+  // first cache read, the consumers before their first q load.
 
   // ---- scan the chunk counts: total, this CTA's slice, and its first row
   // (every CTA computes the same scan; CTA 0 flags bad lengths)
@@ -606,6 +607,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) paged_decode_partition_kernel
 
   // ================================== consumer warps
   if (warp >= p.active_warps) return;
+  pdl_wait();      // q may be the output of the rotary kernels, which let this grid start early
   Consumer cons;
   for (int it = 0; it < nit; ++it) {
     const int stage = it % S;

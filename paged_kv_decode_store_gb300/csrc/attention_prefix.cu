@@ -417,6 +417,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) paged_decode_prefix_kernel(co
 
   // ================================== consumer warps
   if (warp >= p.active_warps) return;
+  pdl_wait();      // q may be the output of the rotary kernels, which let this grid start early
   GroupConsumer<T, D> cons;
   for (int it = 0; it < nit; ++it) {
     const int stage = it % S;

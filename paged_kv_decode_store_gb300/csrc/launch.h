@@ -106,6 +106,37 @@ cudaError_t launch_kv_store_prefill(const void* k, const void* v, const int32_t*
                                     int64_t* slots_out, const pkvd_cache& c, int elem_bytes, cudaStream_t stream,
                                     int32_t* err);
 
+// Rotary positions, alone (positions set) or with the paged store of a decode
+// step (ctx set) or of a prefill batch (cu_q and cu_k set): rope.cu.  Strides
+// in elements; k_out and v_out are the cache bases in the store forms.
+constexpr int kRopeMaxDim = 512;      // largest head_dim
+struct RopeArgs {
+  void* q_out;
+  const void* q;
+  void* k_out;
+  const void* k;
+  void* v_out;
+  const void* v;
+  int64_t q_stride, q_out_stride, k_stride, k_out_stride, v_stride;
+  int64_t block_stride, token_stride, head_stride, num_blocks;
+  int block_size;
+  int dtype;
+  int num_q_heads, num_kv_heads, head_dim;
+  int rotary_dim, interleaved;
+  float mscale;
+  const double* inv_freq;
+  const int64_t* positions;
+  const int32_t* tables;
+  int max_blocks;
+  const int32_t* ctx;
+  const int32_t* cu_q;
+  const int32_t* cu_k;
+  int num_seqs;
+  int64_t* slots_out;
+  int32_t* err;
+};
+cudaError_t launch_rope(const RopeArgs& a, int tokens, cudaStream_t stream);
+
 // Per-row cut parameters the sampler leaves for the extras kernel:
 // [0] flags (kRowGreedy, kRowUniform, kRowTopK), [1] nucleus threshold key
 // (0 = off), [2] k-th key, [3] index of the last kept id at the k-th key

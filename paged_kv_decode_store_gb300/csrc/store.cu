@@ -12,33 +12,9 @@
 // over rows, 16-byte vector copies, 64-bit cache offsets.
 #include "common.cuh"
 #include "launch.h"
+#include "paging.cuh"
 
 namespace pkvd {
-
-// Slot of row i's newest token, or -1 (empty row or a bad length / block id,
-// which is flagged).
-__device__ __forceinline__ int64_t decode_slot(const int32_t* __restrict__ tables, int max_blocks,
-                                               const int32_t* __restrict__ ctx, int i, int block_size,
-                                               int64_t num_blocks, int32_t* err) {
-  const int c = ctx[i];
-  if (c < 0) {
-    flag_error(err, PKVD_ERR_CONTEXT);
-    return -1;
-  }
-  if (c == 0) return -1;
-  const int pos = c - 1;
-  const int logical = pos / block_size;
-  if (logical >= max_blocks) {
-    flag_error(err, PKVD_ERR_CONTEXT);
-    return -1;
-  }
-  const int phys = tables[(int64_t)i * max_blocks + logical];
-  if (phys < 0 || phys >= num_blocks) {
-    flag_error(err, PKVD_ERR_BLOCK_ID);
-    return -1;
-  }
-  return (int64_t)phys * block_size + pos % block_size;
-}
 
 __global__ void slot_mapping_kernel(int64_t* __restrict__ slots, const int32_t* __restrict__ tables,
                                     int max_blocks, const int32_t* __restrict__ ctx, int num_seqs,
@@ -47,7 +23,7 @@ __global__ void slot_mapping_kernel(int64_t* __restrict__ slots, const int32_t* 
   pdl_trigger();
   const int i = blockIdx.x * blockDim.x + threadIdx.x;
   if (i >= num_seqs) return;
-  slots[i] = decode_slot(tables, max_blocks, ctx, i, block_size, num_blocks, err);
+  slots[i] = decode_place(tables, max_blocks, ctx, i, block_size, num_blocks, err).slot;
 }
 
 // Copy token tok's K and V rows (num_heads x head_dim each, 16-byte
@@ -108,48 +84,12 @@ __global__ void kv_store_paged_kernel(const uint8_t* __restrict__ k, const uint8
   pdl_wait();
   pdl_trigger();
   const int tok = blockIdx.x;
-  const int64_t slot = decode_slot(tables, max_blocks, ctx, tok, block_size, num_blocks,
-                                   threadIdx.x == 0 ? err : nullptr);
+  const int64_t slot = decode_place(tables, max_blocks, ctx, tok, block_size, num_blocks,
+                                    threadIdx.x == 0 ? err : nullptr).slot;
   if (slots_out && threadIdx.x == 0) slots_out[tok] = slot;
   if (slot < 0) return;
   store_rows(k, v, tok, slot, kc, vc, block_size, num_heads, head_dim, block_stride, token_stride, head_stride,
              elem_bytes);
-}
-
-// Slot of new token row t of a varlen prefill batch, or -1 (a row past
-// cu_seqlens_q[num_seqs], or a bad length / block id, which is flagged).
-// nano-vllm "Model Runner" notes, section "prefix cache": sequence i owns
-// rows [cu_q[i], cu_q[i+1]) and k_len = cu_k[i+1] - cu_k[i] tokens in all,
-// so row t sits at position (k_len - q_len) + (t - cu_q[i]).
-__device__ __forceinline__ int64_t prefill_slot(const int32_t* __restrict__ tables, int max_blocks,
-                                                const int32_t* __restrict__ cu_q, const int32_t* __restrict__ cu_k,
-                                                int num_seqs, int t, int block_size, int64_t num_blocks,
-                                                int32_t* err) {
-  if (t >= cu_q[num_seqs]) return -1;
-  int lo = 0, hi = num_seqs - 1;   // the last i with cu_q[i] <= t
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (cu_q[mid] <= t) lo = mid;
-    else hi = mid - 1;
-  }
-  const int q0 = cu_q[lo], q1 = cu_q[lo + 1];
-  const int qlen = q1 - q0, klen = cu_k[lo + 1] - cu_k[lo];
-  if (t < q0 || t >= q1 || klen < qlen) {
-    flag_error(err, PKVD_ERR_CONTEXT);
-    return -1;
-  }
-  const int pos = klen - qlen + (t - q0);
-  const int logical = pos / block_size;
-  if (logical >= max_blocks) {
-    flag_error(err, PKVD_ERR_CONTEXT);
-    return -1;
-  }
-  const int phys = tables[(int64_t)lo * max_blocks + logical];
-  if (phys < 0 || phys >= num_blocks) {
-    flag_error(err, PKVD_ERR_BLOCK_ID);
-    return -1;
-  }
-  return (int64_t)phys * block_size + pos % block_size;
 }
 
 // Prefill store: one CTA per new token row finds its sequence and position,
@@ -164,8 +104,8 @@ __global__ void kv_store_prefill_kernel(const uint8_t* __restrict__ k, const uin
   pdl_wait();
   pdl_trigger();
   const int tok = blockIdx.x;
-  const int64_t slot = prefill_slot(tables, max_blocks, cu_q, cu_k, num_seqs, tok, block_size, num_blocks,
-                                    threadIdx.x == 0 ? err : nullptr);
+  const int64_t slot = prefill_place(tables, max_blocks, cu_q, cu_k, num_seqs, tok, block_size, num_blocks,
+                                     threadIdx.x == 0 ? err : nullptr).slot;
   if (slots_out && threadIdx.x == 0) slots_out[tok] = slot;
   if (slot < 0) return;
   store_rows(k, v, tok, slot, kc, vc, block_size, num_heads, head_dim, block_stride, token_stride, head_stride,
