@@ -245,6 +245,42 @@ pkvd_status pkvd_paged_decode_attention_window(void* out, const void* q, const p
                                                void* stream, int32_t* err_flag, int32_t path);
 
 /*
+ * Score modifiers of one attention call.  With s_j = scale * <q, K_j> the
+ * score of key position j for a query at position p, query head h:
+ *   softcap > 0        s_j <- softcap * tanh(s_j / softcap); 0: no cap
+ *   alibi_slopes       s_j <- s_j - alibi_slopes[h] * |p - j|; f32 device
+ *                      array [num_q_heads], finite, any sign; NULL: no bias
+ *   prefix_lens        (prefill only) every row of sequence i also attends to
+ *                      positions j < prefix_lens[i], whatever the causal order
+ *                      and the window; int32 device array [num_seqs], clamped
+ *                      to [0, k_len_i]; NULL: none.  A decode row has every
+ *                      cached position behind it, so it is ignored there (a
+ *                      window still cuts off the prefix).
+ * in this order; fp32 throughout.  The pages give no score function besides
+ * the softmax; these are the forms that engines of the kind they walk through
+ * need next to it.
+ */
+typedef struct {
+  float softcap;
+  const float* alibi_slopes;
+  const int32_t* prefix_lens;
+} pkvd_score_mod;
+
+/*
+ * pkvd_paged_decode_attention_mod -- pkvd_paged_decode_attention_window with
+ * score modifiers (the new token is at position context_lens[i] - 1); mod
+ * NULL or all off: the same call.  Same arguments, workspace, requirements,
+ * status codes and device errors; PKVD_INVALID_ARG for a softcap that is
+ * negative, not finite or so small that scale / softcap is not finite.
+ */
+pkvd_status pkvd_paged_decode_attention_mod(void* out, const void* q, const pkvd_cache* cache,
+                                            const int32_t* block_tables, int32_t max_blocks_per_seq,
+                                            const int32_t* context_lens, int32_t max_context_len,
+                                            int32_t num_seqs, int32_t num_q_heads, float scale,
+                                            int32_t window, const pkvd_score_mod* mod, void* workspace,
+                                            size_t workspace_bytes, void* stream, int32_t* err_flag, int32_t path);
+
+/*
  * pkvd_decode_prefix_workspace_bytes -- workspace bytes of
  * pkvd_paged_decode_attention_prefix for these sizes (never less than
  * pkvd_decode_workspace_bytes for the same call; sm_count <= 0: the current
@@ -486,6 +522,17 @@ pkvd_status pkvd_prefill_attention_ex(void* out, const void* q, const pkvd_cache
                                       const int32_t* cu_seqlens_k, int32_t num_seqs, int32_t total_q,
                                       int32_t max_seqlen_q, int32_t num_q_heads, float scale, int32_t window,
                                       void* stream, int32_t* err_flag, int32_t path);
+
+/* pkvd_prefill_attention_ex with score modifiers; mod NULL or all off: the
+ * same call.  A row whose sequence has a prefix also reads the cache rows of
+ * the prefix (positions past the row's own included, so the step's store has
+ * to come first).  PKVD_INVALID_ARG for a bad softcap as in
+ * pkvd_paged_decode_attention_mod. */
+pkvd_status pkvd_prefill_attention_mod(void* out, const void* q, const pkvd_cache* cache, const int32_t* block_tables,
+                                       int32_t max_blocks_per_seq, const int32_t* cu_seqlens_q,
+                                       const int32_t* cu_seqlens_k, int32_t num_seqs, int32_t total_q,
+                                       int32_t max_seqlen_q, int32_t num_q_heads, float scale, int32_t window,
+                                       const pkvd_score_mod* mod, void* stream, int32_t* err_flag, int32_t path);
 
 /* Workspace bytes of pkvd_sample_ex's optional outputs: 32 per row (host
  * only).  pkvd_sample itself needs none (it may get NULL, 0). */

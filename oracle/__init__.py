@@ -21,6 +21,7 @@ Every function restates, in the plainest form, what the pages define:
   attention over cached prefix plus new rows (nano-vllm "Model Runner",
   sections "prefix cache", "prepare Prefill", "prefill and decode").
 * ``rotary``    -- rotary positions, the angle reduced in rational arithmetic.
+* ``scores``    -- attention whose scores are capped, biased or opened to a prefix.
 * ``block_manager`` -- block allocation with prefix sharing, forks and
   copy-on-write (imported on its own by its tests).
 
@@ -29,4 +30,4 @@ worked examples the pages print, closed forms, brute force on tiny inputs,
 library routines and published known-answer vectors.  No function is left
 "parity unpinned".
 """
-from . import paging, store, attention, philox, sampler, prefill, rotary  # noqa: F401
+from . import paging, store, attention, philox, sampler, prefill, rotary, scores  # noqa: F401

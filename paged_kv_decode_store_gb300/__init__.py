@@ -21,7 +21,7 @@ import torch
 
 from ._capi import (LIB_PATH, PATH_AUTO, PATH_FMA, PATH_MMA, PATH_TC, ERR_BLOCK_ID, ERR_SLOT,  # noqa: F401
                     ERR_CONTEXT, ERR_TIMEOUT, PkvdCache, PkvdError, lib, check, dtype_code,
-                    stream_handle, cache_desc, ptr)
+                    stream_handle, cache_desc, ptr, array, err_ptr, on_stream, score_mod)
 from .step import DecodeStep  # noqa: F401
 from .rotary import rope, rope_inv_freq, rope_store_paged, rope_store_prefill  # noqa: F401
 from .block_manager import BlockManager, shared_prefix_len  # noqa: F401
@@ -89,11 +89,19 @@ def kv_store_prefill(k: torch.Tensor, v: torch.Tensor, block_tables: torch.Tenso
 def prefill_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
                       block_tables: torch.Tensor, cu_seqlens_q: torch.Tensor, cu_seqlens_k: torch.Tensor,
                       max_seqlen_q: int, scale: float, window: int = 0, out: torch.Tensor | None = None,
-                      err: torch.Tensor | None = None, stream=None, path: int = PATH_AUTO) -> torch.Tensor:
+                      err: torch.Tensor | None = None, stream=None, path: int = PATH_AUTO, softcap: float = 0.0,
+                      alibi_slopes: torch.Tensor | None = None,
+                      prefix_lens: torch.Tensor | None = None) -> torch.Tensor:
     """Causal varlen attention of the new rows q ([total_q, Hq, D]) over their
     sequences' cached prefix and new rows, read from the paged cache
-    (path: PATH_AUTO, PATH_TC for tcgen05, PATH_MMA for mma.sync)."""
+    (path: PATH_AUTO, PATH_TC for tcgen05, PATH_MMA for mma.sync).  Scores may
+    be capped (softcap * tanh(s / softcap)) and biased by distance
+    (- alibi_slopes[h] * |p - j|, float32 [Hq]); with prefix_lens (int32 [S])
+    the first prefix_lens[i] positions of a sequence are open to all its rows."""
     T, Hq, _ = q.shape
+    if softcap or alibi_slopes is not None or prefix_lens is not None:
+        return _prefill_attention_mod(q, k_cache, v_cache, block_tables, cu_seqlens_q, cu_seqlens_k, max_seqlen_q,
+                                      scale, window, out, err, stream, path, softcap, alibi_slopes, prefix_lens)
     c = cache_desc(k_cache, v_cache)
     if out is None:
         out = torch.empty_like(q)
@@ -102,6 +110,55 @@ def prefill_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Ten
                                           cu_seqlens_q.shape[0] - 1, T, max_seqlen_q, Hq,
                                           ctypes.c_float(scale), window, stream_handle(stream, q), _err_ptr(err),
                                           path))
+    return out
+
+
+def _attention_rows(q, out, k_cache):
+    """q and out of a call with score modifiers: contiguous rows of the cache's type and head_dim."""
+    if q.dim() != 3 or not q.is_contiguous() or q.dtype != k_cache.dtype or q.device != k_cache.device or \
+            q.shape[2] != k_cache.shape[3]:
+        raise ValueError("q must be contiguous [rows, heads, head_dim] of the cache's dtype and device")
+    if out is None:
+        return torch.empty_like(q)
+    if out.shape != q.shape or out.dtype != q.dtype or out.device != q.device or not out.is_contiguous():
+        raise ValueError("out must be a contiguous tensor like q")
+    return out
+
+
+def _prefill_attention_mod(q, k_cache, v_cache, block_tables, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, scale, window,
+                           out, err, stream, path, softcap, alibi_slopes, prefix_lens):
+    T, Hq, _ = q.shape
+    dev, n = q.device, cu_seqlens_q.shape[0] - 1
+    c = cache_desc(k_cache, v_cache)
+    with on_stream(stream, dev):
+        out = _attention_rows(q, out, k_cache)
+        m = score_mod(softcap, alibi_slopes, prefix_lens, Hq, n, dev)
+        check(lib().pkvd_prefill_attention_mod(
+            out.data_ptr(), q.data_ptr(), c, array(block_tables, "block_tables", torch.int32, dev, (n, None)),
+            block_tables.shape[1], array(cu_seqlens_q, "cu_seqlens_q", torch.int32, dev, (n + 1,)),
+            array(cu_seqlens_k, "cu_seqlens_k", torch.int32, dev, (n + 1,)), n, T, max_seqlen_q, Hq, scale, window, m,
+            torch.cuda.current_stream(dev).cuda_stream, err_ptr(err, dev), path))
+    return out
+
+
+def _decode_attention_mod(q, k_cache, v_cache, block_tables, context_lens, max_context_len, scale, out, workspace, err,
+                          stream, path, window, softcap, alibi_slopes):
+    B, Hq, D = q.shape
+    dev = q.device
+    c = cache_desc(k_cache, v_cache)
+    with on_stream(stream, dev):
+        out = _attention_rows(q, out, k_cache)
+        if workspace is None:
+            workspace = torch.empty(max(decode_workspace_bytes(B, Hq, D, max_context_len), 16), dtype=torch.uint8,
+                                    device=dev)
+        elif workspace.device != dev or not workspace.is_contiguous():
+            raise ValueError(f"workspace must be a contiguous tensor on {dev}")
+        m = score_mod(softcap, alibi_slopes, None, Hq, B, dev)
+        check(lib().pkvd_paged_decode_attention_mod(
+            out.data_ptr(), q.data_ptr(), c, array(block_tables, "block_tables", torch.int32, dev, (B, None)),
+            block_tables.shape[1], array(context_lens, "context_lens", torch.int32, dev, (B,)), max_context_len, B, Hq,
+            scale, window, m, workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+            torch.cuda.current_stream(dev).cuda_stream, err_ptr(err, dev), path))
     return out
 
 
@@ -126,10 +183,16 @@ def paged_decode_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torc
                            block_tables: torch.Tensor, context_lens: torch.Tensor,
                            max_context_len: int, scale: float, out: torch.Tensor | None = None,
                            workspace: torch.Tensor | None = None, err: torch.Tensor | None = None,
-                           stream=None, path: int = PATH_AUTO, window: int = 0) -> torch.Tensor:
+                           stream=None, path: int = PATH_AUTO, window: int = 0, softcap: float = 0.0,
+                           alibi_slopes: torch.Tensor | None = None) -> torch.Tensor:
     """out[i, h] = softmax(scale * q[i, h] . K_i^T) V_i over row i's paged context
-    (its newest `window` positions when window > 0)."""
+    (its newest `window` positions when window > 0).  Scores may be capped
+    (softcap * tanh(s / softcap)) and biased by distance
+    (- alibi_slopes[h] * (context - 1 - j), float32 [Hq])."""
     B, Hq, D = q.shape
+    if softcap or alibi_slopes is not None:
+        return _decode_attention_mod(q, k_cache, v_cache, block_tables, context_lens, max_context_len, scale, out,
+                                     workspace, err, stream, path, window, softcap, alibi_slopes)
     c = cache_desc(k_cache, v_cache)
     if out is None:
         out = torch.empty_like(q)

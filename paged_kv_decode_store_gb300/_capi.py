@@ -29,6 +29,10 @@ class PkvdRope(ctypes.Structure):
     _fields_ = [("inv_freq", c_void_p), ("rotary_dim", c_int32), ("interleaved", c_int32), ("mscale", c_float)]
 
 
+class PkvdScoreMod(ctypes.Structure):
+    _fields_ = [("softcap", c_float), ("alibi_slopes", c_void_p), ("prefix_lens", c_void_p)]
+
+
 class PkvdError(RuntimeError):
     def __init__(self, status: int, text: str):
         super().__init__(f"pkvd status {status}: {text}")
@@ -64,6 +68,9 @@ SIGNATURES = {
     "pkvd_prefill_attention_ex": (c_int32, [c_void_p, c_void_p, ctypes.POINTER(PkvdCache), c_void_p, c_int32,
                                             c_void_p, c_void_p, c_int32, c_int32, c_int32, c_int32, c_float,
                                             c_int32, c_void_p, c_void_p, c_int32]),
+    "pkvd_prefill_attention_mod": (c_int32, [c_void_p, c_void_p, ctypes.POINTER(PkvdCache), c_void_p, c_int32,
+                                             c_void_p, c_void_p, c_int32, c_int32, c_int32, c_int32, c_float,
+                                             c_int32, ctypes.POINTER(PkvdScoreMod), c_void_p, c_void_p, c_int32]),
     "pkvd_bm_create": (c_int32, [c_int32, c_int32, ctypes.POINTER(c_void_p)]),
     "pkvd_bm_destroy": (None, [c_void_p]),
     "pkvd_bm_num_free": (c_int32, [c_void_p]),
@@ -88,6 +95,10 @@ SIGNATURES = {
     "pkvd_paged_decode_attention_window": (c_int32, [c_void_p, c_void_p, ctypes.POINTER(PkvdCache), c_void_p,
                                                      c_int32, c_void_p, c_int32, c_int32, c_int32, c_float,
                                                      c_int32, c_void_p, c_size_t, c_void_p, c_void_p, c_int32]),
+    "pkvd_paged_decode_attention_mod": (c_int32, [c_void_p, c_void_p, ctypes.POINTER(PkvdCache), c_void_p,
+                                                  c_int32, c_void_p, c_int32, c_int32, c_int32, c_float,
+                                                  c_int32, ctypes.POINTER(PkvdScoreMod), c_void_p, c_size_t,
+                                                  c_void_p, c_void_p, c_int32]),
     "pkvd_decode_prefix_workspace_bytes": (c_int32, [c_int32, c_int32, c_int32, c_int32, c_int32, c_int32, c_int32,
                                                      ctypes.POINTER(c_size_t)]),
     "pkvd_paged_decode_attention_prefix": (c_int32, [c_void_p, c_void_p, ctypes.POINTER(PkvdCache), c_void_p, c_int32,
@@ -195,6 +206,16 @@ def err_ptr(err, device: torch.device):
     if err.dtype != torch.int32 or err.device != device or err.numel() < 1:
         raise ValueError(f"err must be an int32 tensor on {device}")
     return err.data_ptr()
+
+
+def score_mod(softcap: float, alibi_slopes, prefix_lens, num_q_heads: int, num_seqs: int, device: torch.device):
+    """The pkvd_score_mod of an attention call, or None when nothing is on."""
+    if not softcap and alibi_slopes is None and prefix_lens is None:
+        return None
+    slopes = None if alibi_slopes is None else array(alibi_slopes, "alibi_slopes", torch.float32, device,
+                                                     (num_q_heads,))
+    prefix = None if prefix_lens is None else array(prefix_lens, "prefix_lens", torch.int32, device, (num_seqs,))
+    return PkvdScoreMod(softcap, slopes, prefix)
 
 
 def cache_desc(k_cache: torch.Tensor, v_cache: torch.Tensor) -> PkvdCache:

@@ -68,6 +68,21 @@ pkvd_status check_cache(const pkvd_cache* c, bool for_attention) {
   return PKVD_OK;
 }
 
+// The kernels' form of a call's score modifiers; false if they are invalid.
+bool score_mod(const pkvd_score_mod* m, float scale, bool prefill, ScoreMod* out) {
+  *out = ScoreMod{};
+  if (!m) return true;
+  if (!(m->softcap >= 0.f) || !std::isfinite(m->softcap)) return false;
+  if (m->softcap > 0.f) {
+    out->cap_in = (float)((double)scale / m->softcap);
+    out->cap_out_log2 = (float)(m->softcap * 1.4426950408889634);
+    if (!std::isfinite(out->cap_in) || !std::isfinite(out->cap_out_log2)) return false;
+  }
+  out->slopes = m->alibi_slopes;
+  if (prefill) out->prefix = m->prefix_lens;
+  return true;
+}
+
 pkvd_status from_cuda(cudaError_t e) { return e == cudaSuccess ? PKVD_OK : PKVD_CUDA_ERROR; }
 
 }  // namespace
@@ -349,10 +364,22 @@ pkvd_status pkvd_prefill_attention_ex(void* out, const void* q, const pkvd_cache
                                       const int32_t* cu_seqlens_k, int32_t num_seqs, int32_t total_q,
                                       int32_t max_seqlen_q, int32_t num_q_heads, float scale, int32_t window,
                                       void* stream, int32_t* err_flag, int32_t path) {
+  return pkvd_prefill_attention_mod(out, q, cache, block_tables, max_blocks_per_seq, cu_seqlens_q, cu_seqlens_k,
+                                    num_seqs, total_q, max_seqlen_q, num_q_heads, scale, window, nullptr, stream,
+                                    err_flag, path);
+}
+
+pkvd_status pkvd_prefill_attention_mod(void* out, const void* q, const pkvd_cache* cache, const int32_t* block_tables,
+                                       int32_t max_blocks_per_seq, const int32_t* cu_seqlens_q,
+                                       const int32_t* cu_seqlens_k, int32_t num_seqs, int32_t total_q,
+                                       int32_t max_seqlen_q, int32_t num_q_heads, float scale, int32_t window,
+                                       const pkvd_score_mod* mod, void* stream, int32_t* err_flag, int32_t path) {
   if (path != PKVD_PATH_AUTO && path != PKVD_PATH_MMA && path != PKVD_PATH_TC && path != PKVD_PATH_FMA)
     return PKVD_INVALID_ARG;
   if (num_seqs < 0 || total_q < 0 || max_seqlen_q < 0 || window < 0) return PKVD_INVALID_ARG;
   if (!std::isfinite(scale)) return PKVD_INVALID_ARG;
+  ScoreMod sm;
+  if (!score_mod(mod, scale, true, &sm)) return PKVD_INVALID_ARG;
   const pkvd_status cs = check_cache(cache, false);
   if (cs != PKVD_OK) return cs;
   if (num_q_heads <= 0) return PKVD_INVALID_ARG;
@@ -384,6 +411,7 @@ pkvd_status pkvd_prefill_attention_ex(void* out, const void* q, const pkvd_cache
   a.num_q_heads = num_q_heads;
   a.scale = scale;
   a.window = window;
+  a.mod = sm;
   a.err = err_flag;
   const bool tc = mma && prefill_tc_supported(a);
   if (path == PKVD_PATH_TC && !tc) return PKVD_UNSUPPORTED_SHAPE;
@@ -456,7 +484,7 @@ namespace {
 AttnArgs attn_args(void* out, const void* q, const pkvd_cache* cache, const int32_t* block_tables,
                    int32_t max_blocks_per_seq, const int32_t* context_lens, int32_t max_context_len, int32_t num_seqs,
                    int32_t num_q_heads, float scale, int32_t window, void* workspace, int32_t* err_flag, int grid,
-                   int32_t path) {
+                   int32_t path, const ScoreMod& mod) {
   AttnArgs a;
   a.out = out;
   a.q = q;
@@ -482,13 +510,17 @@ AttnArgs attn_args(void* out, const void* q, const pkvd_cache* cache, const int3
   a.grid = grid;
   a.path = path;
   a.window = window > 0 ? window : 0;
+  a.mod = mod;
   return a;
 }
 
 pkvd_status attention_call(void* out, const void* q, const pkvd_cache* cache, const int32_t* block_tables,
                            int32_t max_blocks_per_seq, const int32_t* context_lens, int32_t max_context_len,
                            int32_t num_seqs, int32_t num_q_heads, float scale, int32_t window, void* workspace,
-                           size_t workspace_bytes, void* stream, int32_t* err_flag, int32_t path) {
+                           size_t workspace_bytes, void* stream, int32_t* err_flag, int32_t path,
+                           const pkvd_score_mod* mod = nullptr) {
+  ScoreMod sm;
+  if (!score_mod(mod, scale, false, &sm)) return PKVD_INVALID_ARG;
   int grid = 0;
   size_t need = 0;
   const pkvd_status vs = attention_validate(out, q, cache, block_tables, max_blocks_per_seq, context_lens,
@@ -498,7 +530,7 @@ pkvd_status attention_call(void* out, const void* q, const pkvd_cache* cache, co
   if (!workspace || workspace_bytes < need) return PKVD_WORKSPACE_TOO_SMALL;
   if (!aligned16(workspace)) return PKVD_UNSUPPORTED_SHAPE;
   const AttnArgs a = attn_args(out, q, cache, block_tables, max_blocks_per_seq, context_lens, max_context_len,
-                               num_seqs, num_q_heads, scale, window, workspace, err_flag, grid, path);
+                               num_seqs, num_q_heads, scale, window, workspace, err_flag, grid, path, sm);
   return from_cuda(launch_attention(a, static_cast<cudaStream_t>(stream)));
 }
 }  // namespace
@@ -522,6 +554,17 @@ pkvd_status pkvd_paged_decode_attention_window(void* out, const void* q, const p
   if (window < 0) return PKVD_INVALID_ARG;
   return attention_call(out, q, cache, block_tables, max_blocks_per_seq, context_lens, max_context_len, num_seqs,
                         num_q_heads, scale, window, workspace, workspace_bytes, stream, err_flag, path);
+}
+
+pkvd_status pkvd_paged_decode_attention_mod(void* out, const void* q, const pkvd_cache* cache,
+                                            const int32_t* block_tables, int32_t max_blocks_per_seq,
+                                            const int32_t* context_lens, int32_t max_context_len, int32_t num_seqs,
+                                            int32_t num_q_heads, float scale, int32_t window,
+                                            const pkvd_score_mod* mod, void* workspace, size_t workspace_bytes,
+                                            void* stream, int32_t* err_flag, int32_t path) {
+  if (window < 0) return PKVD_INVALID_ARG;
+  return attention_call(out, q, cache, block_tables, max_blocks_per_seq, context_lens, max_context_len, num_seqs,
+                        num_q_heads, scale, window, workspace, workspace_bytes, stream, err_flag, path, mod);
 }
 
 pkvd_status pkvd_decode_prefix_workspace_bytes(int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads,
@@ -565,7 +608,7 @@ pkvd_status pkvd_paged_decode_attention_prefix(void* out, const void* q, const p
   if (!workspace || workspace_bytes < need_p) return PKVD_WORKSPACE_TOO_SMALL;
   if (!aligned16(workspace)) return PKVD_UNSUPPORTED_SHAPE;
   const AttnArgs a = attn_args(out, q, cache, block_tables, max_blocks_per_seq, context_lens, max_context_len,
-                               num_seqs, num_q_heads, scale, 0, workspace, err_flag, grid, path);
+                               num_seqs, num_q_heads, scale, 0, workspace, err_flag, grid, path, ScoreMod{});
   return from_cuda(launch_attention_prefix(a, prefix_len, static_cast<cudaStream_t>(stream)));
 }
 

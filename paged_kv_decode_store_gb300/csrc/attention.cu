@@ -78,6 +78,7 @@ PartParams part_params(const AttnArgs& a, float* rec) {
   pp.rowb = pp.row_bytes + 16;
   pp.rows_contig = a.head_stride == a.head_dim ? 1 : 0;
   pp.active_warps = a.num_kv_heads == 16 ? kConsumerWarps : a.num_kv_heads;
+  pp.mod = a.mod;
   return pp;
 }
 
@@ -91,9 +92,11 @@ cudaError_t launch_attention(const AttnArgs& a, cudaStream_t stream) {
     const size_t smem = smem_header_bytes() + (size_t)pp.stages * 2 * kChunk * pp.rowb;
     const int gmax = group_bound(G);
     cudaError_t e;
-    if (a.dtype == PKVD_F32) e = partition_f32(pp, a.head_dim, hpw, gmax, a.path, a.grid, smem, stream);
-    else if (a.dtype == PKVD_F16) e = partition_f16(pp, a.head_dim, hpw, gmax, a.path, a.grid, smem, stream);
-    else e = partition_bf16(pp, a.head_dim, hpw, gmax, a.path, a.grid, smem, stream);
+    const bool mod = a.mod.on();
+    const auto run = a.dtype == PKVD_F32   ? (mod ? partition_mod_f32 : partition_f32)
+                     : a.dtype == PKVD_F16 ? (mod ? partition_mod_f16 : partition_f16)
+                                           : (mod ? partition_mod_bf16 : partition_bf16);
+    e = run(pp, a.head_dim, hpw, gmax, a.path, a.grid, smem, stream);
     if (e != cudaSuccess) return e;
   }
   if (a.num_seqs == 0) return cudaSuccess;

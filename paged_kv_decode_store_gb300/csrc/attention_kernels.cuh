@@ -38,8 +38,11 @@
 //   PKVD_ERR_TIMEOUT and the CTA leaves after draining its own copies.
 #pragma once
 
+#include <type_traits>
+
 #include "common.cuh"
 #include "launch.h"
+#include "score_mod.cuh"
 
 namespace pkvd {
 
@@ -67,6 +70,7 @@ struct PartParams {
   int row_bytes;       // hkv * D * sizeof(T)
   int rows_contig;     // heads of a token row adjacent in memory
   int active_warps;    // consumer warps that own heads
+  ScoreMod mod;        // read by the MOD consumers only
 };
 
 // The partition kernel's parameters for a call (attention.cu); `rec` is the
@@ -123,8 +127,11 @@ struct SmemHdr {
 };
 
 // ----------------------------------------------------------- consumers
-template <typename T, int D, int HPW, int GMAX>
+// Consumers come without and with score modifiers (MOD): the second kind
+// knows how far a chunk's first token lies behind the new one (dist0).
+template <typename T, int D, int HPW, int GMAX, bool MOD = false>
 struct FmaConsumer {
+  static constexpr bool kMod = MOD;
   static constexpr int ESZ = sizeof(T);
   static constexpr int VEC = 16 / ESZ;
   static constexpr int LPT = D * ESZ / 16;   // lanes per token row of one head
@@ -134,6 +141,7 @@ struct FmaConsumer {
   float q[HPW][GMAX][VEC];
   float acc[HPW][GMAX][VEC];
   float m[HPW][GMAX], l[HPW][GMAX];
+  float slope[MOD ? HPW : 1][MOD ? GMAX : 1];
 
   __device__ void begin(const PartParams& p, int seq, int warp, int lane) {
     const int li = lane % LPT;
@@ -154,9 +162,10 @@ struct FmaConsumer {
         }
 #pragma unroll
         for (int v = 0; v < VEC; ++v) {
-          q[j][g][v] = f[v] * p.scale_log2;
+          q[j][g][v] = MOD ? f[v] : f[v] * p.scale_log2;   // a capped score is scaled after the dot product
           acc[j][g][v] = 0.f;
         }
+        if constexpr (MOD) slope[j][g] = g < p.G ? bias_slope(p.mod, hk * p.G + g) : 0.f;
         m[j][g] = -INFINITY;
         l[j][g] = 0.f;
       }
@@ -164,7 +173,7 @@ struct FmaConsumer {
   }
 
   __device__ void chunk(const PartParams& p, const uint8_t* sK, const uint8_t* sV, int ntok,
-                        int warp, int lane) {
+                        int warp, int lane, int dist0) {
     const int grp = lane / LPT, li = lane % LPT;
 #pragma unroll
     for (int j = 0; j < HPW; ++j) {
@@ -184,6 +193,8 @@ struct FmaConsumer {
           for (int v = 0; v < VEC; ++v) d = fmaf(q[j][g][v], kf[v], d);
 #pragma unroll
           for (int o = LPT / 2; o > 0; o >>= 1) d += __shfl_xor_sync(FULL_MASK, d, o);
+          if constexpr (MOD)
+            d = fmaf(slope[j][g], (float)(dist0 - t), capped<std::is_same<T, float>::value>(d, p.scale_log2, p.mod));
           s[g] = d;
         }
         if (valid) {
@@ -255,8 +266,9 @@ struct FmaConsumer {
   }
 };
 
-template <typename T, int D, int HPW>
+template <typename T, int D, int HPW, bool MOD = false>
 struct MmaConsumer {
+  static constexpr bool kMod = MOD;
   static constexpr int ESZ = sizeof(T);
   static constexpr int KS = D / 16;     // k-steps of QK^T, m-tiles of V^T P^T
   static_assert(ESZ == 2, "tensor-core path is for 16-bit caches");
@@ -264,6 +276,7 @@ struct MmaConsumer {
   uint32_t qf[HPW][KS][2];
   float acc[HPW][KS][4];
   float m[HPW][2], l[HPW][2];
+  float slope[MOD ? HPW : 1][2];
 
   __device__ void begin(const PartParams& p, int seq, int warp, int lane) {
     const int lr = lane >> 2, lc = lane & 3;
@@ -281,10 +294,15 @@ struct MmaConsumer {
       }
       m[j][0] = m[j][1] = -INFINITY;
       l[j][0] = l[j][1] = 0.f;
+      if constexpr (MOD) {
+        const int lc = lane & 3;
+#pragma unroll
+        for (int e = 0; e < 2; ++e) slope[j][e] = 2 * lc + e < p.G ? bias_slope(p.mod, hk * p.G + 2 * lc + e) : 0.f;
+      }
     }
   }
 
-  __device__ void chunk(const PartParams& p, uint8_t* sK, uint8_t* sV, int ntok, int warp, int lane) {
+  __device__ void chunk(const PartParams& p, uint8_t* sK, uint8_t* sV, int ntok, int warp, int lane, int dist0) {
     const int lr = lane >> 2;
     // ldmatrix row/column providers: A = K tile (row-major, rows = tokens)
     const int a_row = (lane & 7) + ((lane >> 3) & 1) * 8;
@@ -318,10 +336,18 @@ struct MmaConsumer {
       }
       // fragment: s0,s1 -> token lr, heads 2lc,2lc+1 ; s2,s3 -> token lr+8
       const float sl = p.scale_log2;
-      const float x0 = lr < ntok ? s[0] * sl : -INFINITY;
-      const float x1 = lr < ntok ? s[1] * sl : -INFINITY;
-      const float x2 = lr + 8 < ntok ? s[2] * sl : -INFINITY;
-      const float x3 = lr + 8 < ntok ? s[3] * sl : -INFINITY;
+      if constexpr (MOD) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          s[e] = fmaf(slope[j][e & 1], (float)(dist0 - lr - (e >> 1) * 8), capped<false>(s[e], sl, p.mod));
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[e] *= sl;
+      }
+      const float x0 = lr < ntok ? s[0] : -INFINITY;
+      const float x1 = lr < ntok ? s[1] : -INFINITY;
+      const float x2 = lr + 8 < ntok ? s[2] : -INFINITY;
+      const float x3 = lr + 8 < ntok ? s[3] : -INFINITY;
       float mx0 = fmaxf(x0, x2), mx1 = fmaxf(x1, x3);
 #pragma unroll
       for (int o = 4; o < 32; o <<= 1) {
@@ -622,7 +648,12 @@ __global__ void __launch_bounds__(kAttnThreads, 1) paged_decode_partition_kernel
     if (flags & F_FIRST) cons.begin(p, seq, warp, lane);
     uint8_t* sK = stage_base + stage * stage_bytes;
     uint8_t* sV = sK + kChunk * p.rowb;
-    if (ntok > 0) cons.chunk(p, sK, sV, ntok, warp, lane);
+    int dist0 = 0;                     // from the chunk's first token to the row's newest
+    if constexpr (Consumer::kMod) {
+      const int c = min(max(p.ctx[seq], 0), p.ctx_cap);
+      dist0 = c - 1 - window_start(c, p.window) - (int)(c0 + it - row_start) * kChunk;
+    }
+    if (ntok > 0) cons.chunk(p, sK, sV, ntok, warp, lane, dist0);
     __syncwarp();
     if (lane == 0) mbar_arrive(&hdr.empty[stage]);
     if (flags & F_LAST) cons.finish(p, seq, flags, cta, warp, lane, row_start, nrow, C, grid);

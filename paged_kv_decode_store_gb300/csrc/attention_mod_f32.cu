@@ -1,0 +1,9 @@
+// Partition-kernel instantiations for float caches with score modifiers.
+#include "attention_dispatch.cuh"
+
+namespace pkvd {
+cudaError_t partition_mod_f32(const PartParams& pp, int D, int hpw, int gmax, int path, int grid, size_t smem,
+                         cudaStream_t st) {
+  return dispatch_partition<float, true>(pp, D, hpw, gmax, path, grid, smem, st);
+}
+}  // namespace pkvd

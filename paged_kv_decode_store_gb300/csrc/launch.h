@@ -17,6 +17,16 @@ constexpr int kChunk = 16;            // tokens per pipeline stage
 constexpr int kConsumerWarps = 8;
 constexpr int kAttnThreads = (kConsumerWarps + 1) * 32;
 
+// Scores capped by a tanh, biased by distance or opened to a prefix
+// (score_mod.cuh); all off by default.
+struct ScoreMod {
+  float cap_in = 0.f;            // softmax scale / cap, 0: no cap
+  float cap_out_log2 = 0.f;      // cap * log2(e)
+  const float* slopes = nullptr;     // [query heads]
+  const int32_t* prefix = nullptr;   // [sequences], prefill only
+  bool on() const { return cap_in != 0.f || slopes || prefix; }
+};
+
 struct AttnArgs {
   void* out;
   const void* q;
@@ -40,6 +50,7 @@ struct AttnArgs {
   int grid;           // partition CTAs
   int path;           // PKVD_PATH_FMA / PKVD_PATH_MMA (resolved)
   int window;         // > 0: sliding window of the newest `window` positions
+  ScoreMod mod;
 };
 
 int attention_grid(int num_seqs, int max_context_len, int sm_count);
@@ -92,6 +103,7 @@ struct PrefillArgs {
   int num_q_heads;
   float scale;
   int window;
+  ScoreMod mod;
   int32_t* err;
 };
 bool prefill_supported(int dtype, int head_dim, int group);

@@ -30,10 +30,13 @@
 //   are zero-filled, never read.
 // * The causal / window mask is only evaluated on tiles that cross a row's
 //   diagonal or window edge; a warp skips tiles none of its rows can see.
+// * MOD: scores capped or biased, or a prefix open to every row
+//   (score_mod.cuh); the kernel without it is unchanged.
 #include <cmath>
 
 #include "common.cuh"
 #include "launch.h"
+#include "score_mod.cuh"
 
 namespace pkvd {
 
@@ -70,6 +73,7 @@ struct PfParams {
   int tile_tokens;     // query tokens per CTA (kPfRows / group)
   float scale_log2;    // softmax scale * log2(e)
   int window;
+  ScoreMod mod;
   int32_t* err;
 };
 
@@ -93,7 +97,7 @@ __device__ __forceinline__ void cp_async_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-template <typename T, int D>
+template <typename T, int D, bool MOD>
 __global__ void __launch_bounds__(kPfThreads, 1) prefill_attention_kernel(const PfParams p) {
   using L = PfLayout<D>;
   extern __shared__ __align__(128) uint8_t smem[];
@@ -120,8 +124,9 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_attention_kernel(const 
   const int qrows = (tok_end - tok_begin) * G;
   const int cached = klen - qlen;
   const int pos_first = cached + tok_begin, pos_last = cached + tok_end - 1;
-  const int lo = pf_window_start(pos_first + 1, p.window);    // first key any row reads
-  const int hi = pos_last;                                      // last key any row reads
+  const int prefix = MOD ? prefix_of(p.mod, seq, klen) : 0;     // keys that every row reads
+  const int lo = prefix > 0 ? 0 : pf_window_start(pos_first + 1, p.window);   // first key any row reads
+  const int hi = max(pos_last, prefix - 1);                     // last key any row reads
   const int kt_first = lo / kPfKeys, kt_last = hi / kPfKeys;
 
   const uint32_t sQ = smem_u32(smem);
@@ -179,6 +184,9 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_attention_kernel(const 
   const int pa = pos_first + ra / G, pb = pos_first + rb / G;
   const int wsa = pf_window_start(pa + 1, p.window), wsb = pf_window_start(pb + 1, p.window);
 
+  const float slope_a = MOD ? bias_slope(p.mod, hk * G + ra % G) : 0.f;
+  const float slope_b = MOD ? bias_slope(p.mod, hk * G + rb % G) : 0.f;
+
   uint32_t qf[D / 16][4];
   float o[D / 8][4];
 #pragma unroll
@@ -207,7 +215,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_attention_kernel(const 
 
     const int kbase = kt * kPfKeys;
     // A warp works on a tile only if one of its rows can see one of its keys.
-    if (warp_live && kbase <= w_pos_max && kbase + kPfKeys - 1 >= w_ws_min) {
+    if (warp_live && ((kbase <= w_pos_max && kbase + kPfKeys - 1 >= w_ws_min) || (MOD && kbase < prefix))) {
       const uint32_t sK = sKV + st * 2 * L::kTileBytes, sV = sK + L::kTileBytes;
       float s[kPfKeys / 8][4];
 #pragma unroll
@@ -224,17 +232,19 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_attention_kernel(const 
           Mma<T>::run(s[2 * np + 1], qf[kk], b2, b3);
         }
       }
-      const bool masked = kbase + kPfKeys - 1 > w_pos_min || kbase < w_ws_max;
+      const bool masked = (kbase + kPfKeys - 1 > w_pos_min || kbase < w_ws_max) && !(MOD && kbase + kPfKeys <= prefix);
 #pragma unroll
       for (int n = 0; n < kPfKeys / 8; ++n) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          float x = s[n][e] * p.scale_log2;
-          if (masked) {
-            const int kp = kbase + n * 8 + 2 * (lane & 3) + (e & 1);
-            const int pr = e < 2 ? pa : pb, wr = e < 2 ? wsa : wsb;
-            if (kp > pr || kp < wr) x = -INFINITY;
-          }
+          const int kp = kbase + n * 8 + 2 * (lane & 3) + (e & 1);
+          const int pr = e < 2 ? pa : pb, wr = e < 2 ? wsa : wsb;
+          float x;
+          if constexpr (MOD)
+            x = fmaf(e < 2 ? slope_a : slope_b, fabsf((float)(pr - kp)), capped<false>(s[n][e], p.scale_log2, p.mod));
+          else
+            x = s[n][e] * p.scale_log2;
+          if (masked && (kp > pr || kp < wr) && !(MOD && kp < prefix)) x = -INFINITY;
           s[n][e] = x;
         }
       }
@@ -319,10 +329,10 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_attention_kernel(const 
 template <typename T, int D>
 cudaError_t launch_prefill_typed(const PfParams& prm, dim3 grid, cudaStream_t stream) {
   constexpr int smem = PfLayout<D>::kBytes;
-  cudaError_t e = cudaFuncSetAttribute(prefill_attention_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       smem);
+  const auto kernel = prm.mod.on() ? prefill_attention_kernel<T, D, true> : prefill_attention_kernel<T, D, false>;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  return launch_pdl(prefill_attention_kernel<T, D>, grid, dim3(kPfThreads), smem, stream, prm);
+  return launch_pdl(kernel, grid, dim3(kPfThreads), smem, stream, prm);
 }
 
 }  // namespace
@@ -356,6 +366,7 @@ cudaError_t launch_prefill_attention(const PrefillArgs& a, cudaStream_t stream) 
   prm.tile_tokens = prefill_tile_tokens(G);
   prm.scale_log2 = a.scale * 1.4426950408889634f;
   prm.window = a.window;
+  prm.mod = a.mod;
   prm.err = a.err;
   const int tiles = (a.max_seqlen_q + prm.tile_tokens - 1) / prm.tile_tokens;
   const dim3 grid(a.cache.num_kv_heads, a.num_seqs, tiles);

@@ -10,9 +10,11 @@
 // fp32 (padded rows: lane j reads key j without bank conflicts); lane j scores
 // key j, the warp keeps an online softmax in the log2 domain and each lane
 // accumulates D / 32 output dimensions.  Keys outside [ws(p), p] and rows of
-// bad blocks are staged as zeros and masked.  Written for coverage, not speed.
+// bad blocks are staged as zeros and masked.  MOD: with score modifiers
+// (score_mod.cuh).  Written for coverage, not speed.
 #include "common.cuh"
 #include "launch.h"
+#include "score_mod.cuh"
 
 namespace pkvd {
 
@@ -39,6 +41,7 @@ struct FmaParams {
   int group;
   float scale_log2;
   int window;
+  ScoreMod mod;
   int32_t* err;
 };
 
@@ -48,7 +51,7 @@ __device__ __forceinline__ float fma_ex2(float x) {
   return y;
 }
 
-template <typename T, int D>
+template <typename T, int D, bool MOD>
 __global__ void __launch_bounds__(32 * kFmaMaxGroup) prefill_fma_kernel(const FmaParams p) {
   __shared__ float ks[kFmaKeys][D + 1];
   __shared__ float vs[kFmaKeys][D + 1];
@@ -78,6 +81,11 @@ __global__ void __launch_bounds__(32 * kFmaMaxGroup) prefill_fma_kernel(const Fm
   const int pos = klen - qlen + (t - q0);
   const int ws = (p.window > 0 && pos + 1 > p.window) ? pos + 1 - p.window : 0;
   const int h = hk * G + warp;
+  // keys [from, to]; with a prefix those between it and the window are skipped over by the mask
+  const int prefix = MOD ? prefix_of(p.mod, seq, klen) : 0;
+  const int from = prefix > 0 ? 0 : ws, to = max(pos, prefix - 1);
+  const float slope = MOD ? bias_slope(p.mod, h) : 0.f;
+  auto visible = [&](int kp) { return (kp >= ws && kp <= pos) || (MOD && kp < prefix); };
   const T* q = static_cast<const T*>(p.q) + ((int64_t)t * p.hq + h) * D;
   for (int d = lane; d < D; d += 32) qs[warp][d] = DT<T>::to_f(q[d]);
   const int32_t* table = p.tables + (int64_t)seq * p.max_blocks;
@@ -87,13 +95,13 @@ __global__ void __launch_bounds__(32 * kFmaMaxGroup) prefill_fma_kernel(const Fm
   float m = -INFINITY, l = 0.f, o[D / 32];
 #pragma unroll
   for (int i = 0; i < D / 32; ++i) o[i] = 0.f;
-  for (int kbase = (ws / kFmaKeys) * kFmaKeys; kbase <= pos; kbase += kFmaKeys) {
+  for (int kbase = (from / kFmaKeys) * kFmaKeys; kbase <= to; kbase += kFmaKeys) {
     __syncthreads();                                       // the previous chunk is no longer read
     for (int e = threadIdx.x; e < kFmaKeys * D; e += blockDim.x) {
       const int r = e / D, d = e - (e / D) * D;
       const int kp = kbase + r;
       float kv = 0.f, vv = 0.f;
-      if (kp >= ws && kp <= pos) {
+      if (visible(kp)) {
         const int phys = table[kp / p.block_size];
         if (phys >= 0 && phys < p.num_blocks) {
           const int64_t off = (int64_t)phys * p.block_stride + (int64_t)(kp % p.block_size) * p.token_stride +
@@ -111,11 +119,15 @@ __global__ void __launch_bounds__(32 * kFmaMaxGroup) prefill_fma_kernel(const Fm
     // lane j scores key kbase + j
     const int kp = kbase + lane;
     float sc = -INFINITY;
-    if (kp >= ws && kp <= pos) {
+    if (visible(kp)) {
       float acc = 0.f;
 #pragma unroll 8
       for (int d = 0; d < D; ++d) acc = fmaf(qs[warp][d], ks[lane][d], acc);
-      sc = acc * p.scale_log2;
+      if constexpr (MOD)
+        sc = fmaf(slope, fabsf((float)(pos - kp)),
+                  capped<std::is_same<T, float>::value>(acc, p.scale_log2, p.mod));
+      else
+        sc = acc * p.scale_log2;
     }
     float mx = sc;
 #pragma unroll
@@ -145,7 +157,8 @@ __global__ void __launch_bounds__(32 * kFmaMaxGroup) prefill_fma_kernel(const Fm
 
 template <typename T, int D>
 cudaError_t launch_fma_typed(const FmaParams& prm, dim3 grid, int threads, cudaStream_t stream) {
-  return launch_pdl(prefill_fma_kernel<T, D>, grid, dim3(threads), 0, stream, prm);
+  if (prm.mod.on()) return launch_pdl(prefill_fma_kernel<T, D, true>, grid, dim3(threads), 0, stream, prm);
+  return launch_pdl(prefill_fma_kernel<T, D, false>, grid, dim3(threads), 0, stream, prm);
 }
 
 }  // namespace
@@ -177,6 +190,7 @@ cudaError_t launch_prefill_fma(const PrefillArgs& a, cudaStream_t stream) {
   prm.group = a.num_q_heads / c.num_kv_heads;
   prm.scale_log2 = a.scale * 1.4426950408889634f;
   prm.window = a.window;
+  prm.mod = a.mod;
   prm.err = a.err;
   const dim3 grid(a.total_q, c.num_kv_heads);
   const int threads = 32 * prm.group;

@@ -48,6 +48,7 @@
 
 #include "common.cuh"
 #include "launch.h"
+#include "score_mod.cuh"
 
 namespace pkvd {
 
@@ -115,6 +116,7 @@ struct TcParams {
   int64_t l2_bytes;      // the device's L2 size, for the CTA order
   float scale_log2;
   int window;
+  ScoreMod mod;          // read by the MOD kernels only
   int32_t* err;
 };
 
@@ -168,6 +170,22 @@ __device__ __forceinline__ void tc_fma2(float& d0, float& d1, float a0, float a1
   asm("mov.b64 %0, {%1, %1};" : "=l"(cc) : "f"(c));
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(bb), "l"(cc));
   asm("mov.b64 {%0, %1}, %2;" : "=f"(d0), "=f"(d1) : "l"(d));
+}
+__device__ __forceinline__ void tc_mul2(float& d0, float& d1, float a0, float a1, float b0, float b1) {
+  unsigned long long a, b, d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(a) : "f"(a0), "f"(a1));
+  asm("mov.b64 %0, {%1, %2};" : "=l"(b) : "f"(b0), "f"(b1));
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(d0), "=f"(d1) : "l"(d));
+}
+// r = r * z + c on both lanes
+__device__ __forceinline__ void tc_fma2v(float& r0, float& r1, float z0, float z1, float c) {
+  unsigned long long r, z, cc;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(r0), "f"(r1));
+  asm("mov.b64 %0, {%1, %2};" : "=l"(z) : "f"(z0), "f"(z1));
+  asm("mov.b64 %0, {%1, %1};" : "=l"(cc) : "f"(c));
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(r), "l"(z), "l"(cc));
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r0), "=f"(r1) : "l"(r));
 }
 __device__ __forceinline__ void tc_add2(float& d0, float& d1, float a0, float a1) {
   unsigned long long a, d;
@@ -280,7 +298,57 @@ __device__ __forceinline__ void st_shared_v4(uint32_t addr, uint4 v) {
                : "memory");
 }
 
-template <typename T, int D>
+// A row's 128 raw scores with cap and bias applied, in log2 units.  `off`:
+// the tile's first key minus the row's position.  Columns that the mask
+// leaves out count as 0 before the cap (their keys may hold anything) and are
+// masked by the caller afterwards.
+__device__ __forceinline__ void tc_modify(float (&v)[kTcKeys], const TcParams& p, bool row_full, const uint32_t* mw,
+                                          float nslope, float off) {
+  const ScoreMod& m = p.mod;
+  if (m.cap_in != 0.f) {
+    if (!row_full) {
+#pragma unroll
+      for (int c = 0; c < kTcKeys; ++c) v[c] = ((mw[c >> 5] >> (c & 31)) & 1u) ? v[c] : 0.f;
+    }
+    float a0 = 0.f, a1 = 0.f, a2 = 0.f, a3 = 0.f;
+#pragma unroll
+    for (int c = 0; c < kTcKeys; c += 8) {
+      a0 = tc_max3(a0, fabsf(v[c]), fabsf(v[c + 1]));
+      a1 = tc_max3(a1, fabsf(v[c + 2]), fabsf(v[c + 3]));
+      a2 = tc_max3(a2, fabsf(v[c + 4]), fabsf(v[c + 5]));
+      a3 = tc_max3(a3, fabsf(v[c + 6]), fabsf(v[c + 7]));
+    }
+    const float most = fmaxf(tc_max3(a0, a1, a2), a3) * fabsf(m.cap_in);
+    if (__all_sync(FULL_MASK, most <= 1.f)) {
+      // every score of the warp's rows within the cap: the polynomial alone
+      // (FMAs, off by 6.9e-6 of the value against 2^-9 or 2^-12 of the
+      // rounded weights), two keys an instruction
+      constexpr float kRatio[5] = PKVD_TANH_RATIO5;
+#pragma unroll
+      for (int c = 0; c < kTcKeys; c += 2) {
+        float y0, y1, z0, z1, r0 = kRatio[4], r1 = kRatio[4];
+        tc_mul2(y0, y1, v[c], v[c + 1], m.cap_in, m.cap_in);
+        tc_mul2(z0, z1, y0, y1, y0, y1);
+#pragma unroll
+        for (int k = 3; k >= 0; --k) tc_fma2v(r0, r1, z0, z1, kRatio[k]);
+        tc_mul2(y0, y1, y0, y1, m.cap_out_log2, m.cap_out_log2);
+        tc_mul2(v[c], v[c + 1], y0, y1, r0, r1);
+      }
+    } else {
+#pragma unroll
+      for (int c = 0; c < kTcKeys; ++c) v[c] = tanh_fast(v[c] * m.cap_in) * m.cap_out_log2;
+    }
+  } else {
+#pragma unroll
+    for (int c = 0; c < kTcKeys; c += 2) tc_mul2(v[c], v[c + 1], v[c], v[c + 1], p.scale_log2, p.scale_log2);
+  }
+  if (m.slopes) {
+#pragma unroll
+    for (int c = 0; c < kTcKeys; ++c) v[c] = fmaf(nslope, fabsf(off + (float)c), v[c]);
+  }
+}
+
+template <typename T, int D, bool MOD>
 // 12 warps: an SM sub-partition holds three of them, so at most 168 registers a thread
 __global__ void __launch_bounds__(kTcThreads, 1) prefill_tc_kernel(const __grid_constant__ TcParams p) {
   using L = TcLayout<D>;
@@ -327,13 +395,14 @@ __global__ void __launch_bounds__(kTcThreads, 1) prefill_tc_kernel(const __grid_
   // Q tile g = 1 holds the later tokens (tile 2 zpair counted from the end),
   // g = 0 the tile before it (may be empty).
   const int Tt = p.tile_tokens, G = p.group, cached = klen - qlen;
+  const int prefix = MOD ? prefix_of(p.mod, seq, klen) : 0;     // keys that every row reads
   int tb[2], te[2], lo_g[2], hi_g[2];
 #pragma unroll
   for (int g = 0; g < 2; ++g) {
     te[g] = qlen - (2 * zpair + 1 - g) * Tt;
     tb[g] = max(0, te[g] - Tt);
-    lo_g[g] = tc_window_start(cached + tb[g] + 1, p.window);   // first key the tile's rows read
-    hi_g[g] = cached + te[g] - 1;                               // last key
+    lo_g[g] = prefix > 0 ? 0 : tc_window_start(cached + tb[g] + 1, p.window);   // first key the tile's rows read
+    hi_g[g] = max(cached + te[g] - 1, prefix - 1);              // last key
   }
   if (te[1] <= 0) return;
   const bool has0 = te[0] > 0;
@@ -624,17 +693,23 @@ __global__ void __launch_bounds__(kTcThreads, 1) prefill_tc_kernel(const __grid_
       }
       const uint32_t s_addr = tmem + lane_base + kColS + g * kTcKeys;
       const uint32_t o_addr = tmem + lane_base + kColO + g * D;
+      const float nslope = MOD ? bias_slope(p.mod, hk * G + gi) : 0.f;
       float m_ref = -INFINITY, l = 0.f;
       bool ok = true;
       for (int j = 0; j < my_gn; ++j) {
         const int kbase = (kt_first + my_gf + j) * kTcKeys;
         const int c_lo = max(wr - kbase, 0), c_hi = min(pr - kbase, kTcKeys - 1);
-        const bool row_full = c_lo == 0 && c_hi == kTcKeys - 1;
+        const int c_pre = MOD ? prefix - kbase : 0;            // columns below it: the prefix
+        const bool row_full = (c_lo == 0 && c_hi == kTcKeys - 1) || c_pre >= kTcKeys;
         uint32_t mw[kTcKeys / 32];
 #pragma unroll
         for (int w = 0; w < kTcKeys / 32; ++w) {
           const int a = min(max(c_lo - 32 * w, 0), 32), z = min(max(c_hi + 1 - 32 * w, 0), 32);
           mw[w] = (z == 32 ? 0xffffffffu : ((1u << z) - 1u)) & ~(a == 32 ? 0xffffffffu : ((1u << a) - 1u));
+          if constexpr (MOD) {
+            const int f = min(max(c_pre - 32 * w, 0), 32);
+            mw[w] |= f == 32 ? 0xffffffffu : (1u << f) - 1u;
+          }
         }
         ok = __all_sync(FULL_MASK, mbar_wait_bounded(&bars[kSFull + g], j & 1));
         if (!ok) break;
@@ -648,7 +723,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) prefill_tc_kernel(const __grid_
           mbar_arrive(&bars[kSRead + g]);            // the next S may overwrite these columns
         }
         // raw scores: the scale (> 0) is applied inside the exponent, so the
-        // row max is taken over the raw values and scaled once
+        // row max is taken over the raw values and scaled once (MOD: the
+        // scores are already in log2 units here, scale_log2 is 1 below)
+        if constexpr (MOD) tc_modify(v, p, row_full, mw, nslope, (float)(kbase - pr));
+        const float scale_log2 = MOD ? 1.f : p.scale_log2;
         if (!row_full) {
 #pragma unroll
           for (int c = 0; c < kTcKeys; ++c)
@@ -662,7 +740,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) prefill_tc_kernel(const __grid_
           mx2 = tc_max3(mx2, v[c + 4], v[c + 5]);
           mx3 = tc_max3(mx3, v[c + 6], v[c + 7]);
         }
-        const float mt = fmaxf(tc_max3(mx0, mx1, mx2), mx3) * p.scale_log2;
+        const float mt = fmaxf(tc_max3(mx0, mx1, mx2), mx3) * scale_log2;
         const bool rebase = mt > m_ref + kRebase;
         const bool scale_o = rebase && m_ref != -INFINITY;
         const float alpha = scale_o ? tc_ex2(m_ref - mt) : 1.f;
@@ -674,8 +752,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) prefill_tc_kernel(const __grid_
         for (int c = 0; c < kTcKeys; c += 4) {
           // 2^(scale * s - mu) for two keys per packed FMA; masked keys give 2^-inf = 0
           float a0, a1, a2, a3;
-          tc_fma2(a0, a1, v[c], v[c + 1], p.scale_log2, -mu);
-          tc_fma2(a2, a3, v[c + 2], v[c + 3], p.scale_log2, -mu);
+          tc_fma2(a0, a1, v[c], v[c + 1], scale_log2, -mu);
+          tc_fma2(a2, a3, v[c + 2], v[c + 3], scale_log2, -mu);
           const float e0 = tc_ex2(a0), e1 = tc_ex2(a1), e2 = tc_ex2(a2), e3 = tc_ex2(a3);
           if (c & 4) tc_add2(rs2, rs3, e0, e1), tc_add2(rs2, rs3, e2, e3);
           else tc_add2(rs0, rs1, e0, e1), tc_add2(rs0, rs1, e2, e3);
@@ -787,9 +865,10 @@ bool encode_cache_map(CUtensorMap* map, const void* base, const pkvd_cache& c, i
 template <typename T, int D>
 cudaError_t launch_tc_typed(const TcParams& prm, dim3 grid, cudaStream_t stream) {
   constexpr int smem = TcLayout<D>::kBytes;
-  cudaError_t e = cudaFuncSetAttribute(prefill_tc_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  const auto kernel = prm.mod.on() ? prefill_tc_kernel<T, D, true> : prefill_tc_kernel<T, D, false>;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  return launch_pdl(prefill_tc_kernel<T, D>, grid, dim3(kTcThreads), smem, stream, prm);
+  return launch_pdl(kernel, grid, dim3(kTcThreads), smem, stream, prm);
 }
 
 }  // namespace
@@ -833,6 +912,7 @@ cudaError_t launch_prefill_tc(const PrefillArgs& a, cudaStream_t stream) {
   prm.tile_tokens = kTcRows / G;
   prm.scale_log2 = a.scale * 1.4426950408889634f;
   prm.window = a.window;
+  prm.mod = a.mod;
   prm.err = a.err;
   const int tiles = (a.max_seqlen_q + prm.tile_tokens - 1) / prm.tile_tokens;
   prm.pairs = (tiles + 1) / 2;                                     // two Q tiles per CTA

@@ -1,0 +1,238 @@
+"""Attention over the paged cache with capped, biased and prefix-open scores:
+decode and prefill, every path, against the float64 oracle within its counted
+bound."""
+import numpy as np
+import pytest
+import torch
+
+import oracle
+from gpu_helpers import require_gpu
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+DT = {"f32": torch.float32, "f16": torch.float16, "bf16": torch.bfloat16}
+EPS = {torch.float32: 2.0 ** -23, torch.float16: 2.0 ** -10, torch.bfloat16: 2.0 ** -7}
+
+
+def tolerances(dt, tensor_cores):
+    """Half a step for the weights where they are rounded to the cache's type, and for the output."""
+    return dict(u_p=EPS[dt] / 2 if tensor_cores else 0.0, eps=EPS[dt], tiny=2.0 ** -24 if dt == torch.float16 else 0.0)
+
+
+def cache_of(klens, hkv, d, bs, dt, seed, spare=3):
+    """Caches whose unused rows and blocks hold NaN, tables with -1 past each row's blocks."""
+    g = torch.Generator().manual_seed(seed)
+    need = [-(-n // bs) for n in klens]
+    nb, width = sum(need) + spare, max(max(need), 1) + 1
+    kc, vc = (torch.full((nb, bs, hkv, d), float("nan"), dtype=dt) for _ in range(2))
+    tables = torch.full((len(klens), width), -1, dtype=torch.int32)
+    order = torch.randperm(nb, generator=g)
+    rows, at = [], 0
+    for i, n in enumerate(klens):
+        k, v = (torch.randn(n, hkv, d, generator=g).to(dt) for _ in range(2))
+        for b in range(need[i]):
+            blk = int(order[at])
+            at += 1
+            tables[i, b] = blk
+            m = min(bs, n - b * bs)
+            kc[blk, :m], vc[blk, :m] = k[b * bs:b * bs + m], v[b * bs:b * bs + m]
+        rows.append((k.double().numpy(), v.double().numpy()))
+    return kc.to(DEV), vc.to(DEV), tables.to(DEV), rows
+
+
+def slopes_for(hq, kind):
+    if kind is None:
+        return None, np.zeros(hq)
+    s = torch.tensor([2.0 ** (-8.0 * (h + 1) / hq) for h in range(hq)])
+    if kind == "mixed":                       # zero, negative and steep ones among them
+        s[::3] = 0.0
+        s[1::4] *= -0.05
+        s[2::5] = 3.0
+    return s.to(DEV), s.double().numpy()
+
+
+DECODE = [  # dtype, hq, hkv, d, bs, path
+    ("f32", 4, 2, 64, 16, 0), ("f32", 8, 8, 64, 32, 0), ("f32", 15, 5, 64, 16, 0),
+    ("bf16", 48, 8, 128, 16, 0), ("bf16", 48, 8, 128, 16, 1), ("f16", 16, 16, 64, 256, 0), ("f16", 128, 16, 64, 16, 0),
+    ("f16", 3, 1, 128, 64, 0), ("bf16", 64, 8, 64, 16, 2), ("bf16", 12, 6, 64, 16, 0),
+]
+MODS = [(5.0, None, 0), (0.0, "geometric", 0), (2.0, "mixed", 0), (30.0, "geometric", 37), (1e5, "mixed", 1)]
+
+
+@pytest.mark.parametrize("mod", MODS, ids=lambda m: "-".join(map(str, m)))
+@pytest.mark.parametrize("case", DECODE, ids=lambda c: "-".join(map(str, c)))
+def test_decode(case, mod):
+    pk = require_gpu()
+    dt, hq, hkv, d, bs, path = case
+    dt = DT[dt]
+    cap, kind, window = mod
+    ctx = [1, 0, 16, 17, 333, 50, 700]
+    kc, vc, tables, rows = cache_of(ctx, hkv, d, bs, dt, 1)
+    q = (3 * torch.randn(len(ctx), hq, d, generator=torch.Generator().manual_seed(2))).to(dt)
+    dev_slopes, slopes = slopes_for(hq, kind)
+    scale, err = d ** -0.5, torch.zeros(1, dtype=torch.int32, device=DEV)
+    out = pk.paged_decode_attention(q.to(DEV), kc, vc, tables, torch.tensor(ctx, dtype=torch.int32, device=DEV),
+                                    max(ctx), scale, window=window, softcap=cap, alibi_slopes=dev_slopes, err=err,
+                                    path=path)
+    assert err.item() == 0
+    got = out.double().cpu().numpy()
+    tensor = dt != torch.float32 and path != 1 and hkv in (8, 16)
+    tol = tolerances(dt, tensor)
+    for i, n in enumerate(ctx):
+        for h in range(hq):
+            k, v = (x[:, h // (hq // hkv)] for x in rows[i])
+            want, bound = oracle.scores.attend(q[i, h].double().numpy(), k, v, n - 1, scale, cap, slopes[h], window,
+                                               **tol)
+            off = np.abs(got[i, h] - want)
+            assert np.all(off <= bound), (i, h, float((off - bound).max()))
+
+
+PREFILL = [  # dtype, hq, hkv, d, bs, path
+    ("bf16", 48, 8, 128, 16, 3), ("f16", 16, 16, 64, 256, 3), ("bf16", 8, 1, 64, 32, 3), ("f16", 6, 2, 128, 128, 3),
+    ("bf16", 48, 8, 128, 16, 2), ("f16", 4, 4, 64, 64, 2), ("f32", 4, 2, 64, 16, 1), ("bf16", 6, 2, 128, 16, 1),
+]
+PREFILL_MODS = [  # cap, slopes, window, prefix lengths
+    (5.0, None, 0, None), (0.0, "geometric", 0, None), (0.0, None, 0, [0, 1, 200, 40, 999]),
+    (2.0, "mixed", 19, [5, 0, 130, 64, 10]), (30.0, "geometric", 0, [33, -4, 129, 128, 0]), (1e5, "mixed", 150, None),
+]
+
+
+@pytest.mark.parametrize("mod", PREFILL_MODS, ids=lambda m: "-".join(str(x).replace(" ", "") for x in m))
+@pytest.mark.parametrize("case", PREFILL, ids=lambda c: "-".join(map(str, c)))
+def test_prefill(case, mod):
+    pk = require_gpu()
+    dt, hq, hkv, d, bs, path = case
+    dt = DT[dt]
+    cap, kind, window, prefix = mod
+    qlen, klen = [70, 1, 45, 0, 3], [70, 131, 301, 40, 257]
+    kc, vc, tables, rows = cache_of(klen, hkv, d, bs, dt, 3)
+    T, tail = sum(qlen), 2
+    q = (3 * torch.randn(T + tail, hq, d, generator=torch.Generator().manual_seed(4))).to(dt)
+    cq, ck = (torch.tensor(np.concatenate([[0], np.cumsum(x)]), dtype=torch.int32, device=DEV) for x in (qlen, klen))
+    dev_slopes, slopes = slopes_for(hq, kind)
+    scale, err = d ** -0.5, torch.zeros(1, dtype=torch.int32, device=DEV)
+    out = torch.full((T + tail, hq, d), 7.0, dtype=dt, device=DEV)
+    pl = None if prefix is None else torch.tensor(prefix, dtype=torch.int32, device=DEV)
+    pk.prefill_attention(q.to(DEV), kc, vc, tables, cq, ck, max(qlen), scale, window=window, out=out, err=err,
+                         path=path, softcap=cap, alibi_slopes=dev_slopes, prefix_lens=pl)
+    assert err.item() == 0
+    assert torch.all(out[T:] == 7.0)
+    got = out.double().cpu().numpy()
+    tol = tolerances(dt, path != 1)
+    t = 0
+    for i, n in enumerate(klen):
+        open_to = min(max(prefix[i], 0), n) if prefix else 0
+        for j in range(qlen[i]):
+            p = n - qlen[i] + j
+            for h in range(hq):
+                if (j * hq + h) % 5 and hq > 8:         # every fifth (row, head) of the wide layouts
+                    continue
+                k, v = (x[:, h // (hq // hkv)] for x in rows[i])
+                want, bound = oracle.scores.attend(q[t, h].double().numpy(), k, v, p, scale, cap, slopes[h], window,
+                                                   open_to, **tol)
+                off = np.abs(got[t, h] - want)
+                assert np.all(off <= bound), (i, j, h, float((off - bound).max()))
+            t += 1
+
+
+@pytest.mark.parametrize("path", [1, 2, 3])
+def test_modifiers_that_do_nothing_agree_with_the_plain_call(path):
+    """A zero slope array, an open prefix of nothing: the plain result within one rounding of the output."""
+    pk = require_gpu()
+    klen, qlen = [90, 200], [90, 30]
+    kc, vc, tables, _ = cache_of(klen, 8, 64, 16, torch.bfloat16, 5)
+    q = torch.randn(120, 8, 64, generator=torch.Generator().manual_seed(6)).to(torch.bfloat16).to(DEV)
+    cq, ck = (torch.tensor([0, x[0], sum(x)], dtype=torch.int32, device=DEV) for x in (qlen, klen))
+    plain = pk.prefill_attention(q, kc, vc, tables, cq, ck, 90, 0.125, path=path)
+    z = torch.zeros(8, device=DEV)
+    none = torch.zeros(2, dtype=torch.int32, device=DEV)
+    got = pk.prefill_attention(q, kc, vc, tables, cq, ck, 90, 0.125, path=path, alibi_slopes=z, prefix_lens=none)
+    assert torch.allclose(got.float(), plain.float(), rtol=2.0 ** -6, atol=2.0 ** -8)
+    ctx = torch.tensor(klen, dtype=torch.int32, device=DEV)
+    if path != 3:
+        a = pk.paged_decode_attention(q[:2], kc, vc, tables, ctx, 200, 0.125, path=path)
+        b = pk.paged_decode_attention(q[:2], kc, vc, tables, ctx, 200, 0.125, path=path, alibi_slopes=z)
+        assert torch.allclose(a.float(), b.float(), rtol=2.0 ** -6, atol=2.0 ** -8)
+
+
+def test_bad_blocks_and_lengths_are_flagged():
+    pk = require_gpu()
+    kc, vc, tables, _ = cache_of([40, 20], 8, 64, 16, torch.float16, 7)
+    q = torch.ones(2, 8, 64, dtype=torch.float16, device=DEV)
+    ctx = torch.tensor([40, 20], dtype=torch.int32, device=DEV)
+    err = torch.zeros(1, dtype=torch.int32, device=DEV)
+    bad = tables.clone()
+    bad[0, 1] = kc.shape[0]
+    for path in (1, 2):
+        err.zero_()
+        out = pk.paged_decode_attention(q, kc, vc, bad, ctx, 40, 0.1, softcap=9.0, err=err, path=path)
+        good = pk.paged_decode_attention(q, kc, vc, tables, ctx, 40, 0.1, softcap=9.0, path=path)
+        assert err.item() == pk.ERR_BLOCK_ID and torch.equal(out[1], good[1])
+    err.zero_()
+    pk.paged_decode_attention(q, kc, vc, tables, ctx, 30, 0.1, softcap=9.0, err=err)
+    assert err.item() == pk.ERR_CONTEXT
+    cq, ck = (torch.tensor(x, dtype=torch.int32, device=DEV) for x in ([0, 1, 2], [0, 40, 60]))
+    pre = torch.tensor([40, 20], dtype=torch.int32, device=DEV)
+    for path in (1, 2, 3):
+        err.zero_()
+        pk.prefill_attention(q, kc, vc, bad, cq, ck, 1, 0.1, softcap=9.0, prefix_lens=pre, err=err, path=path)
+        assert err.item() == pk.ERR_BLOCK_ID
+        err.zero_()
+        out = torch.full_like(q, 7.0)
+        pk.prefill_attention(q, kc, vc, tables, cq.flip(0).contiguous() * 0 + cq, ck * 0, 1, 0.1, softcap=9.0,
+                             prefix_lens=pre, err=err, path=path, out=out)
+        assert err.item() == pk.ERR_CONTEXT and torch.all(out == 7.0)     # more rows than tokens
+
+
+def test_refusals():
+    pk = require_gpu()
+    kc, vc, tables, _ = cache_of([40, 20], 8, 64, 16, torch.float16, 8)
+    q = torch.ones(2, 8, 64, dtype=torch.float16, device=DEV)
+    ctx = torch.tensor([40, 20], dtype=torch.int32, device=DEV)
+    cu = torch.tensor([0, 1, 2], dtype=torch.int32, device=DEV)
+    s = torch.ones(8, device=DEV)
+    call = lambda **kw: pk.paged_decode_attention(kw.pop("q", q), kc, vc, tables, kw.pop("ctx", ctx), 40, 0.1, **kw)
+    pre = lambda **kw: pk.prefill_attention(q, kc, vc, tables, cu, kw.pop("ck", cu), 1, 0.1, **kw)
+    for bad in (dict(alibi_slopes=s[:7]), dict(alibi_slopes=s.half()), dict(alibi_slopes=s.cpu()),
+                dict(softcap=5.0, out=torch.empty(2, 8, 64, device=DEV)),
+                dict(softcap=5.0, q=q.float()), dict(softcap=5.0, q=q.transpose(0, 1)), dict(softcap=5.0, ctx=ctx[:1]),
+                dict(softcap=5.0, ctx=ctx.long()), dict(softcap=5.0, err=torch.zeros(1, device=DEV))):
+        with pytest.raises(ValueError):
+            call(**bad)
+    for bad in (dict(softcap=-1.0), dict(softcap=float("nan")), dict(softcap=5.0, path=3),
+                dict(softcap=5.0, workspace=torch.empty(16, dtype=torch.uint8, device=DEV))):
+        with pytest.raises(pk.PkvdError):
+            call(**bad)
+    for bad in (dict(prefix_lens=ctx[:1]), dict(prefix_lens=ctx.long()), dict(softcap=5.0, ck=cu[:2])):
+        with pytest.raises(ValueError):
+            pre(**bad)
+    with pytest.raises(pk.PkvdError):
+        pre(softcap=-2.0)
+
+
+def test_replayed_from_a_graph_and_on_another_stream():
+    pk = require_gpu()
+    ctx0 = [40, 300]
+    kc, vc, tables, _ = cache_of([320, 320], 8, 128, 16, torch.bfloat16, 9)
+    q = torch.randn(2, 48, 128, generator=torch.Generator().manual_seed(10)).to(torch.bfloat16).to(DEV)
+    s, _ = slopes_for(48, "geometric")
+    ctx = torch.tensor(ctx0, dtype=torch.int32, device=DEV)
+    ws = torch.empty(pk.decode_workspace_bytes(2, 48, 128, 320), dtype=torch.uint8, device=DEV)
+    run = lambda **kw: pk.paged_decode_attention(q, kc, vc, tables, ctx, 320, 0.1, softcap=20.0, alibi_slopes=s, **kw)
+    want = run()
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    got = run(stream=side)
+    side.synchronize()
+    assert torch.equal(got, want)
+    out = torch.empty_like(q)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        run(out=out, workspace=ws)
+    g.replay()
+    assert torch.equal(out, want)
+    ctx += 13
+    q.mul_(-1)
+    g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, run())
