@@ -597,6 +597,43 @@ pkvd_status pkvd_sample_ex(int32_t* token_ids, const void* logits, int32_t dtype
                            void* workspace, size_t workspace_bytes, void* stream);
 
 /*
+ * Workspace bytes of pkvd_beam_search_step for these sizes (host only).
+ */
+pkvd_status pkvd_beam_workspace_bytes(int32_t num_requests, int32_t num_beams, int32_t vocab, int32_t dtype,
+                                      int32_t keep, size_t* bytes);
+
+/*
+ * pkvd_beam_search_step -- one step of beam search over every request's beams
+ * and the vocabulary.  Request r's beam b has row r * num_beams + b of the
+ * logits and the score scores[r][b]; a continuation (b, j) is worth
+ *   scores[r][b] + x_j - log(sum_i exp x_i),
+ * and the `keep` best ones of the request are returned, best first, the lowest
+ * b * vocab + j first among equal ones.  Values of different beams are
+ * compared in 64 bits (the normaliser's sum is fp32 within a 32 KB slice of a
+ * row); logits of one beam keep their own order exactly.
+ * An ended beam (finished[r][b] != 0; finished may be NULL) has one
+ * continuation: eos_id at its score unchanged; its logits are not read.
+ * Ids at -inf are never chosen.  A beam whose score or normaliser is not
+ * finite (a dead beam at -inf, a NaN or +inf logit, no logit above -inf)
+ * offers none.  Where a request has fewer than `keep`: score -inf, parent -1,
+ * token -1.
+ * Inputs: logits (dtype) rows `row_stride` elements apart; scores f32
+ *         [num_requests, num_beams]; finished u8, same shape.
+ * Output: out_scores f32, out_parents (the beam within the request) and
+ *         out_tokens int32, all [num_requests, keep].  out_scores may be
+ *         scores when keep == num_beams.  pkvd_bm_reorder moves the beams'
+ *         block tables after it.
+ * workspace: pkvd_beam_workspace_bytes(...) bytes, 8-byte aligned, no
+ *         initialisation; calls that share one must not overlap on the GPU.
+ * Requirements: 1 <= vocab <= 2^23, num_beams <= 64, 1 <= keep <= 64; with
+ *         `finished`, 0 <= eos_id < vocab.
+ */
+pkvd_status pkvd_beam_search_step(float* out_scores, int32_t* out_parents, int32_t* out_tokens, const void* logits,
+                                  int32_t dtype, int32_t num_requests, int32_t num_beams, int32_t vocab,
+                                  int64_t row_stride, const float* scores, const uint8_t* finished, int32_t eos_id,
+                                  int32_t keep, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
  * Host block manager -- the allocation side of the paged cache (nano-vllm
  * "Model Runner" notes, section "prepare Prefill": schedule-time CPU
  * bookkeeping that fills each sequence's block table and counts its
@@ -645,6 +682,21 @@ pkvd_status pkvd_bm_fork(pkvd_block_manager* bm, const int32_t* block_table, int
 
 /* A sequence ends: every block of its table loses a reference (last first). */
 pkvd_status pkvd_bm_release(pkvd_block_manager* bm, const int32_t* block_table, int32_t num_blocks);
+
+/* The rows of a batch follow their parents (a step of beam search): row i
+ * becomes a clone of row parents[i], or ends (-1: no blocks), all rows at
+ * once.  Every block of a new row gains a reference, every block of an old
+ * row loses one (rows in order, last block first), so blocks that no row
+ * follows are free again and shared ones are copied when one of their rows
+ * next appends.  HOST arrays: parents, num_blocks [num_rows], block_tables
+ * [num_rows][table_stride]; the new tables and counts must not overlap the
+ * old ones.  Table entries past a row's new count are left as they were.
+ * PKVD_INVALID_ARG (nothing changes) for a parent outside [-1, num_rows), a
+ * count outside [0, table_stride], or tables that list a block that is free
+ * or more often than it is held. */
+pkvd_status pkvd_bm_reorder(pkvd_block_manager* bm, const int32_t* parents, int32_t num_rows,
+                            const int32_t* block_tables, const int32_t* num_blocks, int32_t table_stride,
+                            int32_t* new_tables, int32_t* new_num_blocks);
 
 /* The prefix a decode batch shares, for pkvd_paged_decode_attention_prefix:
  * the longest run of leading table entries that name the same physical

@@ -10,6 +10,7 @@ kernels.  If ``libpkvd.so`` has not been built, every call raises.
     paged_decode_attention(q, k_cache, v_cache, block_tables, context_lens,
                            max_context_len, scale)
     sample(logits, temperature, top_k, top_p, seeds, offsets)
+    beam_search_step(logits, scores, keep)
     DecodeStep(...)   -- the four calls captured in one CUDA graph
 """
 from __future__ import annotations
@@ -23,13 +24,14 @@ from ._capi import (LIB_PATH, PATH_AUTO, PATH_FMA, PATH_MMA, PATH_TC, ERR_BLOCK_
                     ERR_CONTEXT, ERR_TIMEOUT, PkvdCache, PkvdError, lib, check, dtype_code,
                     stream_handle, cache_desc, ptr, array, err_ptr, on_stream, score_mod)
 from .step import DecodeStep  # noqa: F401
+from .beam import beam_search_step, beam_workspace_bytes  # noqa: F401
 from .rotary import rope, rope_inv_freq, rope_store_paged, rope_store_prefill  # noqa: F401
 from .block_manager import BlockManager, shared_prefix_len  # noqa: F401
 
 __all__ = ["BlockManager", "copy_blocks", "slot_mapping", "kv_store", "kv_store_paged", "kv_store_prefill",
            "prefill_attention", "sample_ex", "pack_mask", "paged_decode_attention", "decode_workspace_bytes",
            "paged_decode_attention_prefix", "decode_prefix_workspace_bytes", "shared_prefix_len",
-           "rope", "rope_store_paged", "rope_store_prefill", "rope_inv_freq", "sample", "DecodeStep", "PkvdError", "lib"]
+           "rope", "rope_store_paged", "rope_store_prefill", "rope_inv_freq", "beam_search_step", "beam_workspace_bytes", "sample", "DecodeStep", "PkvdError", "lib"]
 
 
 def _err_ptr(err):

@@ -71,6 +71,9 @@ SIGNATURES = {
     "pkvd_prefill_attention_mod": (c_int32, [c_void_p, c_void_p, ctypes.POINTER(PkvdCache), c_void_p, c_int32,
                                              c_void_p, c_void_p, c_int32, c_int32, c_int32, c_int32, c_float,
                                              c_int32, ctypes.POINTER(PkvdScoreMod), c_void_p, c_void_p, c_int32]),
+    "pkvd_beam_workspace_bytes": (c_int32, [c_int32, c_int32, c_int32, c_int32, c_int32, ctypes.POINTER(c_size_t)]),
+    "pkvd_beam_search_step": (c_int32, [c_void_p, c_void_p, c_void_p, c_void_p, c_int32, c_int32, c_int32, c_int32,
+                                        c_int64, c_void_p, c_void_p, c_int32, c_int32, c_void_p, c_size_t, c_void_p]),
     "pkvd_bm_create": (c_int32, [c_int32, c_int32, ctypes.POINTER(c_void_p)]),
     "pkvd_bm_destroy": (None, [c_void_p]),
     "pkvd_bm_num_free": (c_int32, [c_void_p]),
@@ -80,6 +83,7 @@ SIGNATURES = {
     "pkvd_bm_append": (c_int32, [c_void_p, c_void_p, c_int32, c_void_p, ctypes.POINTER(c_int32), c_int32,
                                  ctypes.POINTER(c_int32), ctypes.POINTER(c_int32), ctypes.POINTER(c_int32)]),
     "pkvd_bm_fork": (c_int32, [c_void_p, c_void_p, c_int32]),
+    "pkvd_bm_reorder": (c_int32, [c_void_p, c_void_p, c_int32, c_void_p, c_void_p, c_int32, c_void_p, c_void_p]),
     "pkvd_bm_shared_prefix": (c_int32, [c_void_p, c_int32, c_int32, c_void_p, c_int32, ctypes.POINTER(c_int32)]),
     "pkvd_bm_release": (c_int32, [c_void_p, c_void_p, c_int32]),
     "pkvd_copy_blocks": (c_int32, [ctypes.POINTER(PkvdCache), c_void_p, c_void_p, c_void_p, c_int32, c_void_p,

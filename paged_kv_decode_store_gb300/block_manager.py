@@ -84,6 +84,24 @@ class BlockManager:
         _capi.check(self._lib.pkvd_bm_fork(self._h, tp, len(table)))
         return list(table)
 
+    def reorder(self, tables, parents):
+        """Every row follows its parent at once (a beam step): the new tables,
+        row i a clone of tables[parents[i]] (-1: the row ends, no blocks).
+        Blocks that no row follows are released."""
+        n = len(tables)
+        if len(parents) != n:
+            raise ValueError("one parent a row")
+        stride = max((len(t) for t in tables), default=0)
+        old = np.full((max(n, 1), max(stride, 1)), -1, dtype=np.int32)
+        for i, t in enumerate(tables):
+            old[i, :len(t)] = t
+        new = np.full_like(old, -1)
+        counts, pp = _arr([len(t) for t in tables]), _arr(parents)
+        got = _arr([0] * n)
+        _capi.check(self._lib.pkvd_bm_reorder(self._h, pp[1], n, old.ctypes.data_as(ctypes.c_void_p), counts[1],
+                                              old.shape[1], new.ctypes.data_as(ctypes.c_void_p), got[1]))
+        return [new[i, :got[0][i]].tolist() for i in range(n)]
+
     def release(self, table) -> None:
         t, tp = _arr(table)
         _capi.check(self._lib.pkvd_bm_release(self._h, tp, len(table)))

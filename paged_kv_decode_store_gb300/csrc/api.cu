@@ -668,4 +668,49 @@ pkvd_status pkvd_sample(int32_t* token_ids, const void* logits, int32_t dtype, i
                         offsets, nullptr, 0, nullptr, nullptr, nullptr, workspace, workspace_bytes, stream);
 }
 
+pkvd_status pkvd_beam_workspace_bytes(int32_t num_requests, int32_t num_beams, int32_t vocab, int32_t dtype,
+                                      int32_t keep, size_t* bytes) {
+  if (!valid_dtype(dtype)) return PKVD_UNSUPPORTED_DTYPE;
+  if (!bytes || num_requests < 0 || num_beams <= 0 || vocab <= 0 || keep <= 0) return PKVD_INVALID_ARG;
+  if (num_beams > kBeamMaxBeams || keep > kBeamMaxKeep || vocab > (1 << 23)) return PKVD_UNSUPPORTED_SHAPE;
+  *bytes = beam_workspace_bytes((int64_t)num_requests * num_beams, beam_splits(dtype, vocab), keep);
+  return PKVD_OK;
+}
+
+pkvd_status pkvd_beam_search_step(float* out_scores, int32_t* out_parents, int32_t* out_tokens, const void* logits,
+                                  int32_t dtype, int32_t num_requests, int32_t num_beams, int32_t vocab,
+                                  int64_t row_stride, const float* scores, const uint8_t* finished, int32_t eos_id,
+                                  int32_t keep, void* workspace, size_t workspace_bytes, void* stream) {
+  size_t need = 0;
+  const pkvd_status s = pkvd_beam_workspace_bytes(num_requests, num_beams, vocab, dtype, keep, &need);
+  if (s != PKVD_OK) return s;
+  if (row_stride < vocab) return PKVD_INVALID_ARG;
+  if (finished && (eos_id < 0 || eos_id >= vocab)) return PKVD_INVALID_ARG;
+  if (num_requests == 0) return PKVD_OK;
+  if (!out_scores || !out_parents || !out_tokens || !logits || !scores) return PKVD_INVALID_ARG;
+  if (reinterpret_cast<uintptr_t>(logits) % esize(dtype)) return PKVD_UNSUPPORTED_SHAPE;
+  BeamArgs a;
+  a.splits = beam_splits(dtype, vocab);
+  const int64_t rows = (int64_t)num_requests * num_beams;
+  if (rows > 0x7fffffff || rows * a.splits > 0x7fffffff) return PKVD_UNSUPPORTED_SHAPE;      // the scan's grid
+  if (!workspace || workspace_bytes < need) return PKVD_WORKSPACE_TOO_SMALL;
+  if (reinterpret_cast<uintptr_t>(workspace) % 8) return PKVD_UNSUPPORTED_SHAPE;
+  a.out_scores = out_scores;
+  a.out_parents = out_parents;
+  a.out_tokens = out_tokens;
+  a.logits = logits;
+  a.dtype = dtype;
+  a.requests = num_requests;
+  a.beams = num_beams;
+  a.vocab = vocab;
+  a.keep = keep;
+  a.row_stride = row_stride;
+  a.scores = scores;
+  a.finished = finished;
+  a.eos_id = eos_id;
+  a.cands = static_cast<uint64_t*>(workspace);
+  a.sums = reinterpret_cast<float2*>(a.cands + rows * a.splits * keep);
+  return from_cuda(launch_beam(a, static_cast<cudaStream_t>(stream)));
+}
+
 }  // extern "C"

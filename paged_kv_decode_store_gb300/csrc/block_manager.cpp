@@ -40,9 +40,10 @@ struct pkvd_block_manager {
   int32_t head = -1, tail = -1, nfree = 0;
   std::vector<std::string> key_of;      // empty: not registered
   std::unordered_map<std::string, int32_t> cache;
+  std::vector<int32_t> uses;            // pkvd_bm_reorder's counts, all 0 between calls
 
   pkvd_block_manager(int32_t n, int32_t b)
-      : nb(n), bs(b), ref(n, 0), prev(n, -1), next(n, -1), in_free(n, 0), key_of(n) {
+      : nb(n), bs(b), ref(n, 0), prev(n, -1), next(n, -1), in_free(n, 0), key_of(n), uses(n, 0) {
     for (int32_t i = 0; i < n; ++i) push_back(i);
   }
   void push_back(int32_t b) {
@@ -185,6 +186,53 @@ pkvd_status pkvd_bm_fork(pkvd_block_manager* bm, const int32_t* block_table, int
   for (int32_t i = 0; i < num_blocks; ++i)
     if (block_table[i] < 0 || block_table[i] >= bm->nb || bm->ref[block_table[i]] <= 0) return PKVD_INVALID_ARG;
   for (int32_t i = 0; i < num_blocks; ++i) ++bm->ref[block_table[i]];
+  return PKVD_OK;
+}
+
+pkvd_status pkvd_bm_reorder(pkvd_block_manager* bm, const int32_t* parents, int32_t num_rows,
+                            const int32_t* block_tables, const int32_t* num_blocks, int32_t table_stride,
+                            int32_t* new_tables, int32_t* new_num_blocks) {
+  if (!bm || num_rows < 0 || table_stride < 0) return PKVD_INVALID_ARG;
+  if (num_rows == 0) return PKVD_OK;
+  if (!parents || !num_blocks || !new_num_blocks || new_num_blocks == num_blocks) return PKVD_INVALID_ARG;
+  if (table_stride > 0 && (!block_tables || !new_tables || new_tables == block_tables)) return PKVD_INVALID_ARG;
+  for (int32_t i = 0; i < num_rows; ++i)
+    if (parents[i] < -1 || parents[i] >= num_rows || num_blocks[i] < 0 || num_blocks[i] > table_stride)
+      return PKVD_INVALID_ARG;
+  // every row's blocks are live, and no block is listed more often than it is held
+  bool ok = true;
+  int32_t seen_rows = 0, seen_blocks = 0;
+  for (; ok && seen_rows < num_rows; ++seen_rows) {
+    const int32_t* t = block_tables + (int64_t)seen_rows * table_stride;
+    for (seen_blocks = 0; seen_blocks < num_blocks[seen_rows]; ++seen_blocks) {
+      const int32_t b = t[seen_blocks];
+      if (b < 0 || b >= bm->nb || bm->uses[b] >= bm->ref[b]) {
+        ok = false;
+        break;
+      }
+      ++bm->uses[b];
+    }
+    if (!ok) break;
+  }
+  for (int32_t i = 0; i < num_rows && i <= seen_rows; ++i) {   // back to 0: the rows counted, the last one in part
+    const int32_t n = i < seen_rows ? num_blocks[i] : seen_blocks;
+    for (int32_t j = 0; j < n; ++j) bm->uses[block_tables[(int64_t)i * table_stride + j]] = 0;
+  }
+  if (!ok) return PKVD_INVALID_ARG;
+  for (int32_t i = 0; i < num_rows; ++i) {
+    const int32_t p = parents[i], n = p < 0 ? 0 : num_blocks[p];
+    new_num_blocks[i] = n;
+    for (int32_t j = 0; j < n; ++j) {
+      const int32_t b = block_tables[(int64_t)p * table_stride + j];
+      new_tables[(int64_t)i * table_stride + j] = b;
+      ++bm->ref[b];
+    }
+  }
+  for (int32_t i = 0; i < num_rows; ++i)
+    for (int32_t j = num_blocks[i] - 1; j >= 0; --j) {
+      const int32_t b = block_tables[(int64_t)i * table_stride + j];
+      if (--bm->ref[b] == 0) bm->push_back(b);
+    }
   return PKVD_OK;
 }
 

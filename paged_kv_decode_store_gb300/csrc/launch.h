@@ -149,6 +149,28 @@ struct RopeArgs {
 };
 cudaError_t launch_rope(const RopeArgs& a, int tokens, cudaStream_t stream);
 
+// One step of beam search (beam.cu).
+constexpr int kBeamMaxKeep = 64;      // continuations kept per request
+constexpr int kBeamMaxBeams = 64;     // beams per request
+struct BeamArgs {
+  float* out_scores;
+  int32_t* out_parents;
+  int32_t* out_tokens;
+  const void* logits;
+  int dtype;
+  int requests, beams, vocab, keep;
+  int64_t row_stride;
+  const float* scores;
+  const uint8_t* finished;
+  int eos_id;
+  int splits;
+  uint64_t* cands;      // workspace: [rows][splits][keep]
+  float2* sums;         // then [rows][splits]: maximum, sum of exponentials
+};
+int beam_splits(int dtype, int vocab);
+size_t beam_workspace_bytes(int64_t rows, int splits, int keep);
+cudaError_t launch_beam(const BeamArgs& a, cudaStream_t stream);
+
 // Per-row cut parameters the sampler leaves for the extras kernel:
 // [0] flags (kRowGreedy, kRowUniform, kRowTopK), [1] nucleus threshold key
 // (0 = off), [2] k-th key, [3] index of the last kept id at the k-th key
