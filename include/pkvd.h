@@ -609,7 +609,7 @@ pkvd_status pkvd_beam_workspace_bytes(int32_t num_requests, int32_t num_beams, i
  *   scores[r][b] + x_j - log(sum_i exp x_i),
  * and the `keep` best ones of the request are returned, best first, the lowest
  * b * vocab + j first among equal ones.  Values of different beams are
- * compared in 64 bits (the normaliser's sum is fp32 within a 32 KB slice of a
+ * compared in 64 bits (the normaliser's sum is fp32 within at most 16 KB of a
  * row); logits of one beam keep their own order exactly.
  * An ended beam (finished[r][b] != 0; finished may be NULL) has one
  * continuation: eos_id at its score unchanged; its logits are not read.

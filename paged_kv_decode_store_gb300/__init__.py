@@ -22,7 +22,8 @@ import torch
 
 from ._capi import (LIB_PATH, PATH_AUTO, PATH_FMA, PATH_MMA, PATH_TC, ERR_BLOCK_ID, ERR_SLOT,  # noqa: F401
                     ERR_CONTEXT, ERR_TIMEOUT, PkvdCache, PkvdError, lib, check, dtype_code,
-                    stream_handle, cache_desc, ptr, array, err_ptr, on_stream, score_mod)
+                    stream_handle, cache_desc, ptr, array, current_stream, err_ptr, on_stream,
+                    score_mod)
 from .step import DecodeStep  # noqa: F401
 from .beam import beam_search_step, beam_workspace_bytes  # noqa: F401
 from .rotary import rope, rope_inv_freq, rope_store_paged, rope_store_prefill  # noqa: F401
@@ -139,7 +140,7 @@ def _prefill_attention_mod(q, k_cache, v_cache, block_tables, cu_seqlens_q, cu_s
             out.data_ptr(), q.data_ptr(), c, array(block_tables, "block_tables", torch.int32, dev, (n, None)),
             block_tables.shape[1], array(cu_seqlens_q, "cu_seqlens_q", torch.int32, dev, (n + 1,)),
             array(cu_seqlens_k, "cu_seqlens_k", torch.int32, dev, (n + 1,)), n, T, max_seqlen_q, Hq, scale, window, m,
-            torch.cuda.current_stream(dev).cuda_stream, err_ptr(err, dev), path))
+            current_stream(dev), err_ptr(err, dev), path))
     return out
 
 
@@ -160,7 +161,7 @@ def _decode_attention_mod(q, k_cache, v_cache, block_tables, context_lens, max_c
             out.data_ptr(), q.data_ptr(), c, array(block_tables, "block_tables", torch.int32, dev, (B, None)),
             block_tables.shape[1], array(context_lens, "context_lens", torch.int32, dev, (B,)), max_context_len, B, Hq,
             scale, window, m, workspace.data_ptr(), workspace.numel() * workspace.element_size(),
-            torch.cuda.current_stream(dev).cuda_stream, err_ptr(err, dev), path))
+            current_stream(dev), err_ptr(err, dev), path))
     return out
 
 

@@ -164,6 +164,7 @@ def stream_handle(stream, like: torch.Tensor):
 
 
 _HERE = contextlib.nullcontext()
+_current_device = torch._C._cuda_getDevice if hasattr(torch._C, "_cuda_getDevice") else torch.cuda.current_device
 
 
 def on_stream(stream, device: torch.device):
@@ -171,7 +172,7 @@ def on_stream(stream, device: torch.device):
     `stream` (a torch stream or a raw handle; None: the device's current one),
     so what a call allocates belongs to the stream that uses it."""
     if stream is None:
-        return _HERE if device.index == torch.cuda.current_device() else torch.cuda.device(device)
+        return _HERE if device.index == _current_device() else torch.cuda.device(device)
     if not hasattr(stream, "cuda_stream"):
         stream = torch.cuda.ExternalStream(int(stream), device=device) if int(stream) else \
             torch.cuda.default_stream(device)
@@ -180,24 +181,33 @@ def on_stream(stream, device: torch.device):
     return torch.cuda.stream(stream)
 
 
+def current_stream(device: torch.device) -> int:
+    """Handle of the device's current stream (torch's own short way to it where there is one)."""
+    return _raw_stream(device.index) if _raw_stream else torch.cuda.current_stream(device).cuda_stream
+
+
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def rows3(t: torch.Tensor, name: str, like: torch.Tensor | None = None) -> int:
     """Check [tokens, heads, dim] rows whose heads lie side by side (a token's
     row may be a slice of a longer one); returns the token stride in elements."""
     if t.dim() != 3 or not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor [tokens, heads, dim]")
-    T, H, D = t.shape
-    if like is not None and (t.dtype != like.dtype or t.device != like.device):
+    if like is not None and (t.dtype is not like.dtype or t.device != like.device):
         raise ValueError(f"{name} must have the dtype and device of the other tensors")
-    st = t.stride()
-    if (D > 1 and st[2] != 1) or (H > 1 and st[1] != D):
+    T, H, D = t.shape
+    st, sh, sd = t.stride()
+    if (sd != 1 and D > 1) or (sh != D and H > 1):
         raise ValueError(f"{name}: the heads of a token must be contiguous")
-    return st[0] if T > 1 else max(H * D, 1)
+    return st if T > 1 else max(H * D, 1)
 
 
 def array(t: torch.Tensor, name: str, dtype: torch.dtype, device: torch.device, shape: tuple) -> int:
-    """Check a contiguous argument array (None in shape: any size) and give its pointer."""
-    if t.dtype != dtype or t.device != device or t.dim() != len(shape) or not t.is_contiguous() or \
-            any(want is not None and have != want for have, want in zip(t.shape, shape)):
+    """Check a contiguous argument array (None as the last size: any) and give its pointer."""
+    have = t.shape
+    if t.dtype is not dtype or t.device != device or not t.is_contiguous() or \
+            (have != shape and (len(have) != len(shape) or shape[-1] is not None or have[:-1] != shape[:-1])):
         raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape "
                          f"{[('any' if n is None else n) for n in shape]} on {device}")
     return t.data_ptr()
@@ -224,20 +234,11 @@ def score_mod(softcap: float, alibi_slopes, prefix_lens, num_q_heads: int, num_s
 
 def cache_desc(k_cache: torch.Tensor, v_cache: torch.Tensor) -> PkvdCache:
     """Describe [num_blocks, block_size, Hkv, D] views (e.g. kv_cache[0, layer])."""
-    if k_cache.shape != v_cache.shape or k_cache.stride() != v_cache.stride():
+    shape, stride = k_cache.shape, k_cache.stride()
+    if shape != v_cache.shape or stride != v_cache.stride():
         raise ValueError("K and V caches must share shape and strides")
-    if k_cache.dim() != 4 or k_cache.stride(3) != 1:
+    if len(shape) != 4 or stride[3] != 1:
         raise ValueError("cache views must be [num_blocks, block_size, Hkv, D] with D contiguous")
-    nb, bs, H, D = k_cache.shape
-    c = PkvdCache()
-    c.k_base = ptr(k_cache)
-    c.v_base = ptr(v_cache)
-    c.dtype = dtype_code(k_cache.dtype)
-    c.block_size = bs
-    c.num_blocks = nb
-    c.num_kv_heads = H
-    c.head_dim = D
-    c.block_stride = k_cache.stride(0)
-    c.token_stride = k_cache.stride(1)
-    c.head_stride = k_cache.stride(2)
-    return c
+    nb, bs, H, D = shape
+    return PkvdCache(ptr(k_cache), ptr(v_cache), dtype_code(k_cache.dtype), bs, nb, H, D, stride[0], stride[1],
+                     stride[2])

@@ -7,7 +7,7 @@ import ctypes
 import torch
 
 from . import _capi
-from ._capi import array, check, on_stream
+from ._capi import array, check, current_stream, on_stream
 
 
 def beam_workspace_bytes(num_requests: int, num_beams: int, vocab: int, dtype: torch.dtype, keep: int) -> int:
@@ -59,5 +59,5 @@ def beam_search_step(logits: torch.Tensor, scores: torch.Tensor, keep: int, fini
             array(out[1], "out parents", torch.int32, dev, (n, keep)),
             array(out[2], "out tokens", torch.int32, dev, (n, keep)), logits.data_ptr(), code, n, b, vocab, row_stride,
             array(scores, "scores", torch.float32, dev, (n, b)), ended, eos_id, keep, workspace.data_ptr(),
-            workspace.numel() * workspace.element_size(), torch.cuda.current_stream(dev).cuda_stream))
+            workspace.numel() * workspace.element_size(), current_stream(dev)))
     return tuple(out)

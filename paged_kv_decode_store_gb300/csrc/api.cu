@@ -673,7 +673,7 @@ pkvd_status pkvd_beam_workspace_bytes(int32_t num_requests, int32_t num_beams, i
   if (!valid_dtype(dtype)) return PKVD_UNSUPPORTED_DTYPE;
   if (!bytes || num_requests < 0 || num_beams <= 0 || vocab <= 0 || keep <= 0) return PKVD_INVALID_ARG;
   if (num_beams > kBeamMaxBeams || keep > kBeamMaxKeep || vocab > (1 << 23)) return PKVD_UNSUPPORTED_SHAPE;
-  *bytes = beam_workspace_bytes((int64_t)num_requests * num_beams, beam_splits(dtype, vocab), keep);
+  *bytes = beam_workspace_bytes((int64_t)num_requests * num_beams, beam_chunks(dtype, vocab));
   return PKVD_OK;
 }
 
@@ -690,9 +690,9 @@ pkvd_status pkvd_beam_search_step(float* out_scores, int32_t* out_parents, int32
   if (!out_scores || !out_parents || !out_tokens || !logits || !scores) return PKVD_INVALID_ARG;
   if (reinterpret_cast<uintptr_t>(logits) % esize(dtype)) return PKVD_UNSUPPORTED_SHAPE;
   BeamArgs a;
-  a.splits = beam_splits(dtype, vocab);
+  a.chunks = beam_chunks(dtype, vocab);
   const int64_t rows = (int64_t)num_requests * num_beams;
-  if (rows > 0x7fffffff || rows * a.splits > 0x7fffffff) return PKVD_UNSUPPORTED_SHAPE;      // the scan's grid
+  if (rows * a.chunks > 0x7fffffff) return PKVD_UNSUPPORTED_SHAPE;      // the scan's grid
   if (!workspace || workspace_bytes < need) return PKVD_WORKSPACE_TOO_SMALL;
   if (reinterpret_cast<uintptr_t>(workspace) % 8) return PKVD_UNSUPPORTED_SHAPE;
   a.out_scores = out_scores;
@@ -708,8 +708,8 @@ pkvd_status pkvd_beam_search_step(float* out_scores, int32_t* out_parents, int32
   a.scores = scores;
   a.finished = finished;
   a.eos_id = eos_id;
-  a.cands = static_cast<uint64_t*>(workspace);
-  a.sums = reinterpret_cast<float2*>(a.cands + rows * a.splits * keep);
+  a.sums = static_cast<float2*>(workspace);
+  a.maxima = reinterpret_cast<float*>(a.sums + rows * a.chunks);
   return from_cuda(launch_beam(a, static_cast<cudaStream_t>(stream)));
 }
 

@@ -163,12 +163,13 @@ struct BeamArgs {
   const float* scores;
   const uint8_t* finished;
   int eos_id;
-  int splits;
-  uint64_t* cands;      // workspace: [rows][splits][keep]
-  float2* sums;         // then [rows][splits]: maximum, sum of exponentials
+  int chunks;           // 1 KB chunks of a row
+  int span_chunks, spans;   // chunks a warp scans, spans of a row (set by launch_beam)
+  float2* sums;         // workspace: [rows][spans] maximum, sum of exponentials
+  float* maxima;        // then (behind [rows][chunks] of the former) [rows][chunks]
 };
-int beam_splits(int dtype, int vocab);
-size_t beam_workspace_bytes(int64_t rows, int splits, int keep);
+int beam_chunks(int dtype, int vocab);
+size_t beam_workspace_bytes(int64_t rows, int chunks);
 cudaError_t launch_beam(const BeamArgs& a, cudaStream_t stream);
 
 // Per-row cut parameters the sampler leaves for the extras kernel:

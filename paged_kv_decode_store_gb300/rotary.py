@@ -12,7 +12,7 @@ import ctypes
 import torch
 
 from . import _capi
-from ._capi import array, check, err_ptr, on_stream, ptr, rows3
+from ._capi import array, check, current_stream, err_ptr, on_stream, ptr, rows3
 
 _SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "parts": 3}
 
@@ -67,8 +67,8 @@ def rope(q: torch.Tensor, k: torch.Tensor | None, positions: torch.Tensor, inv_f
         desc = _desc(inv_freq, interleaved, mscale, dev)
         check(_capi.lib().pkvd_rope(ptr(q_out), qos, ptr(q), qs, ptr(k_out), kos, ptr(k), ks,
                                     _capi.dtype_code(q.dtype), T, Hq, hk, D,
-                                    array(positions, "positions", torch.int64, dev, (T,)), ctypes.byref(desc),
-                                    torch.cuda.current_stream(dev).cuda_stream))
+                                    array(positions, "positions", torch.int64, dev, (T,)), desc,
+                                    current_stream(dev)))
     return q_out, k_out
 
 
@@ -100,9 +100,9 @@ def rope_store_paged(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, block_ta
         check(_capi.lib().pkvd_rope_store_paged(
             ptr(q_out), qos, ptr(q), qs, ptr(k), ks, ptr(v), vs, q.shape[1],
             array(block_tables, "block_tables", torch.int32, dev, (B, None)), block_tables.shape[1],
-            array(context_lens, "context_lens", torch.int32, dev, (B,)), B, ctypes.byref(desc),
+            array(context_lens, "context_lens", torch.int32, dev, (B,)), B, desc,
             None if slot_mapping is None else array(slot_mapping, "slot_mapping", torch.int64, dev, (B,)),
-            ctypes.byref(c), torch.cuda.current_stream(dev).cuda_stream, err_ptr(err, dev)))
+            c, current_stream(dev), err_ptr(err, dev)))
     return q_out
 
 
@@ -124,7 +124,7 @@ def rope_store_prefill(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, block_
             ptr(q_out), qos, ptr(q), qs, ptr(k), ks, ptr(v), vs, q.shape[1],
             array(block_tables, "block_tables", torch.int32, dev, (n, None)), block_tables.shape[1],
             array(cu_seqlens_q, "cu_seqlens_q", torch.int32, dev, (n + 1,)),
-            array(cu_seqlens_k, "cu_seqlens_k", torch.int32, dev, (n + 1,)), n, T, ctypes.byref(desc),
+            array(cu_seqlens_k, "cu_seqlens_k", torch.int32, dev, (n + 1,)), n, T, desc,
             None if slot_mapping is None else array(slot_mapping, "slot_mapping", torch.int64, dev, (T,)),
-            ctypes.byref(c), torch.cuda.current_stream(dev).cuda_stream, err_ptr(err, dev)))
+            c, current_stream(dev), err_ptr(err, dev)))
     return q_out
