@@ -608,9 +608,9 @@ pkvd_status pkvd_beam_workspace_bytes(int32_t num_requests, int32_t num_beams, i
  * logits and the score scores[r][b]; a continuation (b, j) is worth
  *   scores[r][b] + x_j - log(sum_i exp x_i),
  * and the `keep` best ones of the request are returned, best first, the lowest
- * b * vocab + j first among equal ones.  Values of different beams are
- * compared in 64 bits (the normaliser's sum is fp32 within at most 16 KB of a
- * row); logits of one beam keep their own order exactly.
+ * b * vocab + j first among equal ones.  Values are compared as pairs of fp32
+ * (to 2^-47 of themselves); a beam's normaliser, which shifts all its values
+ * alike, is good to about 10^-7.
  * An ended beam (finished[r][b] != 0; finished may be NULL) has one
  * continuation: eos_id at its score unchanged; its logits are not read.
  * Ids at -inf are never chosen.  A beam whose score or normaliser is not
@@ -623,7 +623,7 @@ pkvd_status pkvd_beam_workspace_bytes(int32_t num_requests, int32_t num_beams, i
  *         out_tokens int32, all [num_requests, keep].  out_scores may be
  *         scores when keep == num_beams.  pkvd_bm_reorder moves the beams'
  *         block tables after it.
- * workspace: pkvd_beam_workspace_bytes(...) bytes, 8-byte aligned, no
+ * workspace: pkvd_beam_workspace_bytes(...) bytes, 16-byte aligned, no
  *         initialisation; calls that share one must not overlap on the GPU.
  * Requirements: 1 <= vocab <= 2^23, num_beams <= 64, 1 <= keep <= 64; with
  *         `finished`, 0 <= eos_id < vocab.

@@ -50,7 +50,7 @@ def beam_search_step(logits: torch.Tensor, scores: torch.Tensor, keep: int, fini
                    torch.empty(n, keep, dtype=torch.int32, device=dev),
                    torch.empty(n, keep, dtype=torch.int32, device=dev))
         if workspace is None:
-            workspace = torch.empty(max(beam_workspace_bytes(n, b, vocab, logits.dtype, keep), 8), dtype=torch.uint8,
+            workspace = torch.empty(max(beam_workspace_bytes(n, b, vocab, logits.dtype, keep), 16), dtype=torch.uint8,
                                     device=dev)
         elif workspace.device != dev or not workspace.is_contiguous():
             raise ValueError(f"workspace must be a contiguous tensor on {dev}")

@@ -694,7 +694,7 @@ pkvd_status pkvd_beam_search_step(float* out_scores, int32_t* out_parents, int32
   const int64_t rows = (int64_t)num_requests * num_beams;
   if (rows * a.chunks > 0x7fffffff) return PKVD_UNSUPPORTED_SHAPE;      // the scan's grid
   if (!workspace || workspace_bytes < need) return PKVD_WORKSPACE_TOO_SMALL;
-  if (reinterpret_cast<uintptr_t>(workspace) % 8) return PKVD_UNSUPPORTED_SHAPE;
+  if (!aligned16(workspace)) return PKVD_UNSUPPORTED_SHAPE;
   a.out_scores = out_scores;
   a.out_parents = out_parents;
   a.out_tokens = out_tokens;
@@ -708,7 +708,7 @@ pkvd_status pkvd_beam_search_step(float* out_scores, int32_t* out_parents, int32
   a.scores = scores;
   a.finished = finished;
   a.eos_id = eos_id;
-  a.sums = static_cast<float2*>(workspace);
+  a.sums = static_cast<float4*>(workspace);
   a.maxima = reinterpret_cast<float*>(a.sums + rows * a.chunks);
   return from_cuda(launch_beam(a, static_cast<cudaStream_t>(stream)));
 }

@@ -165,7 +165,9 @@ struct BeamArgs {
   int eos_id;
   int chunks;           // 1 KB chunks of a row
   int span_chunks, spans;   // chunks a warp scans, spans of a row (set by launch_beam)
-  float2* sums;         // workspace: [rows][spans] maximum, sum of exponentials
+  uint32_t chunk_mul;   // n / chunks = (umulhi(n, chunk_mul) + n) >> chunk_shift
+  int chunk_shift;
+  float4* sums;         // workspace: [rows][spans] maximum, sum of exponentials (two parts)
   float* maxima;        // then (behind [rows][chunks] of the former) [rows][chunks]
 };
 int beam_chunks(int dtype, int vocab);

@@ -13,18 +13,40 @@ DT = {"f32": torch.float32, "f16": torch.float16, "bf16": torch.bfloat16}
 
 
 def check(got, logits, scores, keep, finished=None, eos=-1):
-    """Ids and parents exactly; a score is rounded once (2^-24 of it) after a
-    normaliser off by at most 2^-20 (fp32 sums of exponentials, each term off
-    by 2^-21 of itself through its argument and the exponential)."""
+    """Ids and parents, and scores rounded once (2^-24) after a normaliser off by
+    at most NORM = 2^-20: the terms of its sum are fp32 exponentials, each off
+    by at most 2^-22 and by the rounding of its argument (2^-24 of up to 6 for
+    the terms that matter), so the sum's logarithm by less than 2^-20.
+
+    A normaliser shifts all continuations of its beam alike, so the order
+    within a beam is exact (the lowest id among equal logits), and continuations
+    of different beams may only change places where their exact values are
+    within 2 NORM of each other."""
+    NORM = 2.0 ** -20
     s, p, t = (x.cpu().numpy() for x in got)
     n, b = scores.shape
     x = logits.double().cpu().numpy().reshape(n, b, -1)
     for r in range(n):
-        ws, wp, wt = oracle.beam.step(x[r], scores[r].double().cpu().numpy(), keep,
-                                      None if finished is None else finished[r].cpu().numpy(), eos)
-        assert p[r].tolist() == wp and t[r].tolist() == wt, r
-        for a, w in zip(s[r], ws):
-            assert a == w or abs(float(a) - w) <= abs(w) * 2.0 ** -24 + 2.0 ** -20, (r, a, w)
+        fin = None if finished is None else finished[r].cpu().numpy()
+        sc = scores[r].double().cpu().numpy()
+        ws, wp, wt = oracle.beam.step(x[r], sc, keep, fin, eos)
+        have = list(zip(p[r].tolist(), t[r].tolist()))
+        value = ws
+        if have != list(zip(wp, wt)):
+            value, taken = [], {}
+            for q, tok in have:
+                taken.setdefault(q, []).append(tok)
+            own = {q: oracle.beam.step(x[r, q:q + 1], sc[q:q + 1], keep, None if fin is None else fin[q:q + 1], eos)
+                   for q in taken if q >= 0}
+            for q, toks in taken.items():          # each beam's first ones, in its own order
+                assert q >= 0 and toks == own[q][2][:len(toks)], (r, q, toks)
+            count = {q: 0 for q in taken}
+            for k, (q, tok) in enumerate(have):
+                value.append(own[q][0][count[q]])
+                count[q] += 1
+                assert abs(value[k] - ws[k]) <= 2 * NORM, (r, k, have[k], value[k], ws[k])
+        for a, w in zip(s[r], value):
+            assert a == w or abs(float(a) - w) <= abs(w) * 2.0 ** -24 + NORM, (r, a, w)
 
 
 def draw(n, b, V, dt, seed, std=3.0):
@@ -123,6 +145,23 @@ def test_few_ids_left_in_every_slice_and_many_candidates():
     check(pk.beam_search_step(crowd, scores, 64), crowd, scores, 64)
     same = logits[:1].repeat(8, 1)                      # identical beams: the lower one first
     check(pk.beam_search_step(same, torch.zeros_like(scores), 64), same, torch.zeros_like(scores), 64)
+
+
+@pytest.mark.parametrize("dt", list(DT))
+@pytest.mark.parametrize("V", [1, 7, 511, 513, 33333])
+def test_equal_beams_tie_exactly_whatever_their_alignment(V, dt):
+    """Rows of the same logits that start at every offset of a 16-byte vector: the lowest beam first, always."""
+    pk = require_gpu()
+    one = draw(1, 1, V, DT[dt], 7)[0]
+    x = one.repeat(9, 1)
+    wide = torch.zeros(9, V + 2 - V % 2 + 1, dtype=DT[dt], device=DEV)      # odd row stride
+    wide[:, :V] = x
+    zero = torch.zeros(1, 9, device=DEV)
+    want = oracle.beam.step(x.double().cpu().numpy(), np.zeros(9), 20)
+    for rows in (x, wide[:, :V]):
+        s, p, t = pk.beam_search_step(rows, zero, 20)
+        assert p[0].tolist() == want[1] and t[0].tolist() == want[2]
+        assert s[0].tolist() == sorted(s[0].tolist(), reverse=True)
 
 
 def test_a_merge_of_more_candidates_than_its_list():

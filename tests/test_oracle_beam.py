@@ -71,14 +71,14 @@ def test_beam_host_checks(pk):
     assert step(scores=None) == 1
     assert step(o=None) == 1
     assert step(ws=None) == 4
-    assert step(wsb=8 * 2 * 12 - 1) == 4                    # two 1 KB chunks a row
+    assert step(wsb=8 * 2 * 20 - 1) == 4                    # two 1 KB chunks a row
     assert step(ws=P[5] + 4) == 3
     assert step(n=1 << 26, b=64, V=8, stride=8) == 3        # more rows than a grid holds
     size = ctypes.c_size_t(0)
     assert L.pkvd_beam_workspace_bytes(3, 4, 151936, 1, 8, ctypes.byref(size)) == 0
-    assert size.value == 12 * 297 * 12                       # 297 chunks of 1 KB a row
+    assert size.value == 12 * 297 * 20                       # 297 chunks of 1 KB a row
     assert L.pkvd_beam_workspace_bytes(3, 4, 512, 1, 8, ctypes.byref(size)) == 0
-    assert size.value == 12 * 2 * 12                         # one chunk, or two where the row starts unaligned
+    assert size.value == 12 * 20
     assert L.pkvd_beam_workspace_bytes(3, 4, 100, 0, 8, None) == 1
     assert pk.beam_workspace_bytes(0, 4, 100, __import__("torch").float32, 8) == 0
 
