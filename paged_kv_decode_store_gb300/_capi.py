@@ -189,18 +189,19 @@ def current_stream(device: torch.device) -> int:
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
-def rows3(t: torch.Tensor, name: str, like: torch.Tensor | None = None) -> int:
+def rows3(t: torch.Tensor, name: str, dtype: torch.dtype, device: torch.device, shape: tuple | None = None):
     """Check [tokens, heads, dim] rows whose heads lie side by side (a token's
-    row may be a slice of a longer one); returns the token stride in elements."""
-    if t.dim() != 3 or not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor [tokens, heads, dim]")
-    if like is not None and (t.dtype is not like.dtype or t.device != like.device):
-        raise ValueError(f"{name} must have the dtype and device of the other tensors")
-    T, H, D = t.shape
+    row may be a slice of a longer one): (shape, token stride in elements,
+    pointer)."""
+    have = t.shape
+    if len(have) != 3 or t.dtype is not dtype or t.device != device or (shape is not None and have != shape):
+        raise ValueError(f"{name} must be a {dtype} tensor [tokens, heads, dim] on {device}"
+                         + (f" of shape {list(shape)}" if shape is not None else ""))
+    T, H, D = have
     st, sh, sd = t.stride()
     if (sd != 1 and D > 1) or (sh != D and H > 1):
         raise ValueError(f"{name}: the heads of a token must be contiguous")
-    return st if T > 1 else max(H * D, 1)
+    return have, (st if T > 1 else max(H * D, 1)), t.data_ptr()
 
 
 def array(t: torch.Tensor, name: str, dtype: torch.dtype, device: torch.device, shape: tuple) -> int:

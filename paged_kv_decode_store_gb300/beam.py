@@ -3,6 +3,7 @@ marshalling only."""
 from __future__ import annotations
 
 import ctypes
+import functools
 
 import torch
 
@@ -10,6 +11,7 @@ from . import _capi
 from ._capi import array, check, current_stream, on_stream
 
 
+@functools.lru_cache(maxsize=256)
 def beam_workspace_bytes(num_requests: int, num_beams: int, vocab: int, dtype: torch.dtype, keep: int) -> int:
     n = ctypes.c_size_t(0)
     check(_capi.lib().pkvd_beam_workspace_bytes(num_requests, num_beams, vocab, _capi.dtype_code(dtype), keep,
@@ -46,12 +48,12 @@ def beam_search_step(logits: torch.Tensor, scores: torch.Tensor, keep: int, fini
         ended = array(finished, "finished", torch.uint8, dev, (n, b))
     with on_stream(stream, dev):
         if out is None:
-            out = (torch.empty(n, keep, dtype=torch.float32, device=dev),
-                   torch.empty(n, keep, dtype=torch.int32, device=dev),
-                   torch.empty(n, keep, dtype=torch.int32, device=dev))
+            shape = (n, max(keep, 0))
+            tokens = torch.empty(shape, dtype=torch.int32, device=dev)
+            out = torch.empty(shape, dtype=torch.float32, device=dev), torch.empty_like(tokens), tokens
         if workspace is None:
-            workspace = torch.empty(max(beam_workspace_bytes(n, b, vocab, logits.dtype, keep), 16), dtype=torch.uint8,
-                                    device=dev)
+            workspace = torch.empty(max(beam_workspace_bytes(n, b, vocab, logits.dtype, keep), 16),
+                                    dtype=torch.uint8, device=dev)
         elif workspace.device != dev or not workspace.is_contiguous():
             raise ValueError(f"workspace must be a contiguous tensor on {dev}")
         check(_capi.lib().pkvd_beam_search_step(

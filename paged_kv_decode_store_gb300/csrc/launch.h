@@ -146,6 +146,7 @@ struct RopeArgs {
   int num_seqs;
   int64_t* slots_out;
   int32_t* err;
+  int num_tokens, parts, part_heads;   // set by launch_rope: warps of a token, heads of a warp
 };
 cudaError_t launch_rope(const RopeArgs& a, int tokens, cudaStream_t stream);
 

@@ -12,7 +12,7 @@ import ctypes
 import torch
 
 from . import _capi
-from ._capi import array, check, current_stream, err_ptr, on_stream, ptr, rows3
+from ._capi import array, check, current_stream, err_ptr, on_stream, rows3
 
 _SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "parts": 3}
 
@@ -37,12 +37,13 @@ def _desc(inv_freq: torch.Tensor, interleaved: bool, mscale: float, device: torc
     return _capi.PkvdRope(p, 2 * inv_freq.shape[0], 1 if interleaved else 0, mscale)
 
 
-def _out_rows(out, x, name):
+def _out(out, x, shape, name):
+    """(tensor, token stride, pointer) of an output like x; a fresh one is contiguous."""
     if out is None:
-        return torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    if out.shape != x.shape:
-        raise ValueError(f"{name} must have its input's shape")
-    return out
+        out = torch.empty(shape, dtype=x.dtype, device=x.device)
+        return out, max(shape[1] * shape[2], 1), out.data_ptr()
+    _, stride, p = rows3(out, name, x.dtype, x.device, shape)
+    return out, stride, p
 
 
 def rope(q: torch.Tensor, k: torch.Tensor | None, positions: torch.Tensor, inv_freq: torch.Tensor,
@@ -50,38 +51,41 @@ def rope(q: torch.Tensor, k: torch.Tensor | None, positions: torch.Tensor, inv_f
          k_out: torch.Tensor | None = None, stream=None):
     """(q, k) rotated by positions (int64 [tokens]); inv_freq float64
     [rotary_dim / 2].  q_out / k_out may be q / k (in place); k may be None."""
-    dev = q.device
-    qs = rows3(q, "q")
-    T, Hq, D = q.shape
+    dt, dev = q.dtype, q.device
+    code = _capi.dtype_code(dt)
+    if not q.is_cuda:
+        raise ValueError("tensor arguments must live on a CUDA device")
+    qshape, qs, qp = rows3(q, "q", dt, dev)
+    T, Hq, D = qshape
     ks = kos = hk = 0
+    kp = kop = None
     with on_stream(stream, dev):
-        q_out = _out_rows(q_out, q, "q_out")
-        qos = rows3(q_out, "q_out", q)
+        q_out, qos, qop = _out(q_out, q, qshape, "q_out")
         if k is not None:
-            ks = rows3(k, "k", q)
-            if k.shape[0] != T or k.shape[2] != D:
+            kshape, ks, kp = rows3(k, "k", dt, dev)
+            hk = kshape[1]
+            if kshape[0] != T or kshape[2] != D:
                 raise ValueError("k must have q's tokens and head_dim")
-            hk = k.shape[1]
-            k_out = _out_rows(k_out, k, "k_out")
-            kos = rows3(k_out, "k_out", q)
+            k_out, kos, kop = _out(k_out, k, kshape, "k_out")
         desc = _desc(inv_freq, interleaved, mscale, dev)
-        check(_capi.lib().pkvd_rope(ptr(q_out), qos, ptr(q), qs, ptr(k_out), kos, ptr(k), ks,
-                                    _capi.dtype_code(q.dtype), T, Hq, hk, D,
+        check(_capi.lib().pkvd_rope(qop, qos, qp, qs, kop, kos, kp, ks, code, T, Hq, hk, D,
                                     array(positions, "positions", torch.int64, dev, (T,)), desc,
                                     current_stream(dev)))
     return q_out, k_out
 
 
-def _store_rows(q, k, v, q_out, k_cache):
-    qs, ks, vs = rows3(q, "q"), rows3(k, "k", q), rows3(v, "v", q)
-    _, _, Hkv, D = k_cache.shape
-    T = q.shape[0]
-    if k.shape != (T, Hkv, D) or v.shape != (T, Hkv, D) or q.shape[2] != D:
-        raise ValueError("k and v must be [tokens, kv heads, head_dim] rows of the cache, q of the same head_dim")
-    if k_cache.dtype != q.dtype or k_cache.device != q.device:
-        raise ValueError("the cache must have the dtype and device of the rows")
-    q_out = _out_rows(q_out, q, "q_out")
-    return q_out, rows3(q_out, "q_out", q), qs, ks, vs
+def _store(q, k, v, k_cache, v_cache):
+    """The checks of a fused store's rows: (cache, q's shape, tokens, strides and pointers)."""
+    c = _capi.cache_desc(k_cache, v_cache)
+    dt, dev = k_cache.dtype, k_cache.device
+    qshape, qs, qp = rows3(q, "q", dt, dev)
+    T = qshape[0]
+    if qshape[2] != c.head_dim:
+        raise ValueError("q must have the cache's head_dim")
+    rows = (T, c.num_kv_heads, c.head_dim)
+    _, ks, kp = rows3(k, "k", dt, dev, rows)
+    _, vs, vp = rows3(v, "v", dt, dev, rows)
+    return c, dev, qshape, T, (qp, qs, kp, ks, vp, vs)
 
 
 def rope_store_paged(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, block_tables: torch.Tensor,
@@ -92,17 +96,16 @@ def rope_store_paged(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, block_ta
     """Decode step: row i's q and k turned by position context_lens[i] - 1, the
     key and the value stored in that token's cache slot (kv_store_paged), the
     rotated q returned (q_out may be q; rows without a context get zeros)."""
-    dev, B = q.device, q.shape[0]
-    c = _capi.cache_desc(k_cache, v_cache)
+    c, dev, qshape, B, rows = _store(q, k, v, k_cache, v_cache)
     with on_stream(stream, dev):
-        q_out, qos, qs, ks, vs = _store_rows(q, k, v, q_out, k_cache)
+        q_out, qos, qop = _out(q_out, q, qshape, "q_out")
         desc = _desc(inv_freq, interleaved, mscale, dev)
+        tables = array(block_tables, "block_tables", torch.int32, dev, (B, None))
         check(_capi.lib().pkvd_rope_store_paged(
-            ptr(q_out), qos, ptr(q), qs, ptr(k), ks, ptr(v), vs, q.shape[1],
-            array(block_tables, "block_tables", torch.int32, dev, (B, None)), block_tables.shape[1],
+            qop, qos, *rows, qshape[1], tables, block_tables.shape[1],
             array(context_lens, "context_lens", torch.int32, dev, (B,)), B, desc,
-            None if slot_mapping is None else array(slot_mapping, "slot_mapping", torch.int64, dev, (B,)),
-            c, current_stream(dev), err_ptr(err, dev)))
+            None if slot_mapping is None else array(slot_mapping, "slot_mapping", torch.int64, dev, (B,)), c,
+            current_stream(dev), err_ptr(err, dev)))
     return q_out
 
 
@@ -114,17 +117,16 @@ def rope_store_prefill(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, block_
     """Varlen prefill batch (kv_store_prefill's rows and positions): q and k
     turned, k and v stored, the rotated q returned.  Rows past
     cu_seqlens_q[-1] of q_out and the cache stay as they were."""
-    dev, T = q.device, q.shape[0]
+    c, dev, qshape, T, rows = _store(q, k, v, k_cache, v_cache)
     n = cu_seqlens_q.shape[0] - 1
-    c = _capi.cache_desc(k_cache, v_cache)
     with on_stream(stream, dev):
-        q_out, qos, qs, ks, vs = _store_rows(q, k, v, q_out, k_cache)
+        q_out, qos, qop = _out(q_out, q, qshape, "q_out")
         desc = _desc(inv_freq, interleaved, mscale, dev)
+        tables = array(block_tables, "block_tables", torch.int32, dev, (n, None))
         check(_capi.lib().pkvd_rope_store_prefill(
-            ptr(q_out), qos, ptr(q), qs, ptr(k), ks, ptr(v), vs, q.shape[1],
-            array(block_tables, "block_tables", torch.int32, dev, (n, None)), block_tables.shape[1],
+            qop, qos, *rows, qshape[1], tables, block_tables.shape[1],
             array(cu_seqlens_q, "cu_seqlens_q", torch.int32, dev, (n + 1,)),
             array(cu_seqlens_k, "cu_seqlens_k", torch.int32, dev, (n + 1,)), n, T, desc,
-            None if slot_mapping is None else array(slot_mapping, "slot_mapping", torch.int64, dev, (T,)),
-            c, current_stream(dev), err_ptr(err, dev)))
+            None if slot_mapping is None else array(slot_mapping, "slot_mapping", torch.int64, dev, (T,)), c,
+            current_stream(dev), err_ptr(err, dev)))
     return q_out
