@@ -111,6 +111,7 @@ bool prefill_tc_supported(const PrefillArgs& a);
 bool prefill_fma_supported(int dtype, int head_dim, int group, int num_kv_heads);
 cudaError_t launch_prefill_fma(const PrefillArgs& a, cudaStream_t stream);
 cudaError_t launch_prefill_tc(const PrefillArgs& a, cudaStream_t stream);
+cudaError_t launch_prefill_mod(const PrefillArgs& a, cudaStream_t stream);   // with score modifiers
 int prefill_tile_tokens(int group);
 cudaError_t launch_prefill_attention(const PrefillArgs& a, cudaStream_t stream);
 cudaError_t launch_kv_store_prefill(const void* k, const void* v, const int32_t* tables, int max_blocks,

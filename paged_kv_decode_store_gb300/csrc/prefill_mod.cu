@@ -1,0 +1,916 @@
+// Varlen paged prefill attention with modified scores (score_mod.cuh) on the
+// 5th-generation tensor cores: the operation of prefill_tc.cu with
+//   s = cap * tanh(scale <q, k> / cap) - slope_h |p - j|
+// over the causal window of every row and its sequence's prefix.
+//
+// What differs from the plain kernel is the softmax, which is three times as
+// long here and would set the pace alone.  So
+// * sixteen softmax warps instead of eight: two threads share a query row, each
+//   with its half of a tile's keys.  They agree on the row's reference maximum
+//   through shared memory (their two warps meet once a tile); the sums are
+//   joined once, at the end.
+// * the CTAs are persistent: one per SM walks (sequence, KV head, pair of Q
+//   tiles) items, the longest sequences first.  The grid is one CTA an item;
+//   a running CTA takes the next one over from the CTAs still waiting to start
+//   (clusterlaunchcontrol.try_cancel), so the SMs finish together.  The Q
+//   producer does that and works the items out, one ahead, and hands them over
+//   in shared memory; K, V and the next Q tile (TMA, one box of G heads a
+//   token) arrive while the previous item is finished; barriers count on
+//   across items.
+// * keys are taken from the newest backwards, so a distance bias has its
+//   largest scores first and the running maximum hardly ever moves.
+// * a cap's tanh is a polynomial on the FMA pipe, two keys an instruction, as
+//   long as all of a warp's scores are within 0.7 of it; a warp with a larger
+//   one reads its scores again and takes the exponential form.
+// * bf16 weights have fp32's range: with a cap and no slopes every score lies
+//   in [-cap, cap], and while 2^(cap log2 e) is far inside that range no
+//   reference is needed at all -- no maximum, no exchange, no rescaling.
+//
+// Warps (20): 0-7 and 8-15 softmax of Q tile 0 and 1 (warp w of a tile: TMEM
+// lanes 32 (w % 4) .., keys 64 (w / 4) ..), 16 producer of K and V, 17 and 19
+// the products of Q tile 0 and 1 (one warp for both, polling, took 700 to 1400
+// clocks a round: beside four busy softmax warps it gets an instruction in about
+// every thirteenth clock), 18 items and Q.
+// Row = token * G + query head of the group, as in the plain kernel.
+#include <climits>
+#include <cmath>
+
+#include "common.cuh"
+#include "launch.h"
+#include "score_mod.cuh"
+#include "tcgen05.cuh"
+
+namespace pkvd {
+
+namespace {
+
+constexpr int kThreads = 640;
+constexpr int kTileWarps = 8;         // softmax warps per Q tile (two threads per row)
+constexpr int kKvWarp = 16, kMmaWarp = 17, kQWarp = 18, kMmaWarp1 = 19;
+constexpr uint32_t kTmemCols = 512;
+// TMEM columns: S of tile g at [128 g, 128 g + 128), O of tile g at [256 + g D,
+// 256 + g D + D).  head_dim 128: a half's weights overwrite the first 32 of its
+// own 64 S columns; head_dim 64: they have [384 + 64 g, 448 + 64 g), so the
+// next S may be computed while they are in use.
+constexpr uint32_t kColO = 256, kColP64 = 384;
+constexpr float kRebase = 8.f;        // re-base the running maximum when it grows by > 2^8
+
+template <int D>
+struct Layout {
+  static constexpr int kKStages = D == 64 ? 4 : 3, kVStages = D == 64 ? 4 : 2;
+  static constexpr int kHalves = D / 64;
+  static constexpr uint32_t kQ = 0;                                    // 2 Q tiles
+  static constexpr uint32_t kK = kQ + 2 * kHalves * kHalf;
+  static constexpr uint32_t kV = kK + kKStages * kHalves * kHalf;
+  static constexpr uint32_t kBar = kV + kVStages * kHalves * kHalf;
+  static constexpr uint32_t kX = kBar + 512;                           // exchange: 512 bytes a tile and buffer
+  static constexpr int kXBufs = D == 64 ? 2 : 1;
+  // + alignment slack; at least 120 KB so that one CTA (which holds all TMEM) is resident per SM
+  static constexpr uint32_t kItems = kX + kXBufs * 1024;               // ring of items
+  static constexpr uint32_t kOrder = kItems + 320;                     // sequences, longest first
+  static constexpr uint32_t kEnd = kOrder + 64 + 1024;
+  static constexpr uint32_t kBytes = kEnd > 122880u ? kEnd : 122880u;
+};
+static_assert(Layout<128>::kBytes <= 232448, "227 KB of shared memory");
+
+// mbarriers; those of a Q tile take + g, an exchange's + 4 g + the warp's
+// quarter of the rows.
+enum : int {
+  kKFull = 0, kKEmpty = 4, kVFull = 8, kVReady = 12, kVEmpty = 16, kQFull = 20, kQEmpty = 22, kSFull = 24, kPFull = 26,
+  kPVDone = 28, kSRead = 30, kOFree = 32, kExch = 34, kItemFull = 42, kItemFree = 46, kClaim = 50, kDrain = 51,
+  kNumBars = 53
+};
+constexpr uint32_t kTmemSlot = 8 * kNumBars;        // the TMEM base, then 16 bytes of a claim's answer
+constexpr uint32_t kAnswer = (kTmemSlot + 4 + 15) / 16 * 16;
+static_assert(kAnswer + 16 <= 512, "behind the barriers");
+constexpr int kItemRing = 4, kItemAhead = 1;
+constexpr int kSorted = 64;           // sequences that are put in order of length
+constexpr int kItemUsers = 3 + 2 * kTileWarps;   // K/V, two MMA and softmax warps
+
+struct ModParams {
+  CUtensorMap tmap_q, tmap_k, tmap_v;
+  void* out;
+  const int32_t* tables;
+  int max_blocks;
+  int64_t num_blocks;
+  int block_size;
+  int seg_rows;          // rows per TMA box of the cache: min(block_size, 128)
+  const int32_t* cu_q;
+  const int32_t* cu_k;
+  int total_q, hq, hkv, group, tile_tokens;
+  uint32_t q_box;        // bytes of one 64-column box of a Q tile
+  int pairs;             // Q-tile pairs per (sequence, KV head)
+  int num_seqs, items;
+  float scale_log2;
+  int window;
+  ScoreMod mod;
+  // score of a raw product s as s * polynomial in s^2, for s^2 <= poly_range (-1: not used)
+  float poly[4], poly_range;
+  int wide_out;          // out is 32-byte aligned
+  int bounded;           // every score is in [-cap, cap] and its exponential in range: no reference
+  int32_t* err;
+};
+
+// One item: the keys of a pair of Q tiles.  n = 0: nothing to do, -1: no more.
+// K/V tiles are counted from the last one backwards: tile t holds keys
+// [kt_last - t, ..) * 128.
+struct __align__(16) Item {
+  int seq, hk, q0, cached, prefix;
+  int tb[2], te[2];      // new tokens of Q tile g (0: the earlier one, may be empty)
+  int lo, hi, kt_last, n;
+  int gf[2], gn[2];      // first K/V tile and number of tiles of Q tile g
+  int pad[3];
+};
+static_assert(sizeof(Item) * kItemRing == 320, "the ring in Layout");
+
+__device__ __forceinline__ int window_first(int c, int window) { return (window > 0 && c > window) ? c - window : 0; }
+
+// Item i: the sequences in `order` (as they come without it), their pairs from
+// the end, KV heads fastest.
+__device__ __forceinline__ Item item_at(const ModParams& p, const uint8_t* order, int i) {
+  Item t;
+  t.n = t.gn[0] = t.gn[1] = 0;
+  const int nh = p.hkv, rank = i / (p.pairs * nh), rest = i - rank * (p.pairs * nh);
+  const int zpair = rest / nh;
+  t.hk = rest - zpair * nh;
+  t.seq = order ? order[rank] : rank;
+  const int q0 = p.cu_q[t.seq], q1 = p.cu_q[t.seq + 1], k0 = p.cu_k[t.seq], k1 = p.cu_k[t.seq + 1];
+  const int qlen = q1 - q0, klen = k1 - k0;
+  if (q0 < 0 || qlen < 0 || klen < qlen || q1 > p.total_q || (int64_t)klen > (int64_t)p.max_blocks * p.block_size) {
+    if (zpair == 0 && t.hk == 0) flag_error(p.err, PKVD_ERR_CONTEXT);
+    return t;
+  }
+  if (zpair == 0 && t.hk == 0 && qlen > 2 * p.pairs * p.tile_tokens)
+    flag_error(p.err, PKVD_ERR_CONTEXT);   // longer than max_seqlen_q: the earliest tokens are not computed
+  t.q0 = q0;
+  t.cached = klen - qlen;
+  t.prefix = prefix_of(p.mod, t.seq, klen);
+  int lo_g[2], hi_g[2];
+#pragma unroll
+  for (int g = 0; g < 2; ++g) {
+    t.te[g] = qlen - (2 * zpair + 1 - g) * p.tile_tokens;
+    t.tb[g] = max(0, t.te[g] - p.tile_tokens);
+    lo_g[g] = t.prefix > 0 ? 0 : window_first(t.cached + t.tb[g] + 1, p.window);
+    hi_g[g] = max(t.cached + t.te[g] - 1, t.prefix - 1);
+  }
+  if (t.te[1] <= 0) return t;                    // past the sequence's last pair
+  t.lo = t.te[0] > 0 ? lo_g[0] : lo_g[1];
+  t.hi = hi_g[1];
+  t.kt_last = t.hi / kTcKeys;
+  t.n = t.kt_last - t.lo / kTcKeys + 1;
+#pragma unroll
+  for (int g = 0; g < 2; ++g) {
+    t.gf[g] = t.kt_last - hi_g[g] / kTcKeys;
+    t.gn[g] = t.te[g] > 0 ? hi_g[g] / kTcKeys - lo_g[g] / kTcKeys + 1 : 0;
+  }
+  return t;
+}
+
+// Ask for a CTA that has not started, in its place: 16 bytes at `dst`, counted
+// on `bar`; and its index, -1 if there is none left (then not to be asked
+// again).
+__device__ __forceinline__ void claim(uint32_t dst, uint64_t* bar) {
+  asm volatile(
+      "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(dst),
+      "r"(smem_u32(bar))
+      : "memory");
+}
+__device__ __forceinline__ int claimed(uint32_t src) {
+  int x;
+  asm volatile(
+      "{\n\t.reg .b128 h;\n\t.reg .pred p;\n\t.reg .b64 lo, hi;\n\t"
+      "ld.shared.v2.b64 {lo, hi}, [%1];\n\t"
+      "mov.b128 h, {lo, hi};\n\t"
+      "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, h;\n\t"
+      "mov.b32 %0, -1;\n\t"
+      "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %0, h;\n\t}"
+      : "=r"(x)
+      : "r"(src)
+      : "memory");
+  return x;
+}
+
+__device__ __forceinline__ void tma_load3(uint32_t dst, const CUtensorMap* map, int c0, int c1, int c2, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];"
+      ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(smem_u32(bar))
+      : "memory");
+}
+
+// The issuing thread's own forms: descriptors as a varying low word and a
+// constant high one, so that an MMA costs it two or three instructions (it
+// issues everything, and a batch's first product starts when it gets there).
+constexpr uint32_t desc_hi(uint32_t sbo) { return ((sbo >> 4) & 0x3FFFu) | (1u << 14) | (2u << 29); }
+__device__ __forceinline__ uint32_t desc_lo(uint32_t addr, uint32_t lbo) {
+  return ((addr & 0x3FFFFu) >> 4) | ((lbo >> 4) << 16);
+}
+template <bool ACC>
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t hi, uint32_t idesc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
+      "mov.b64 a, {%1, %3};\n\tmov.b64 b, {%2, %3};\n\t"
+      "setp.ne.b32 p, %5, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, p;\n\t}" ::"r"(d),
+      "r"(a_lo), "r"(b_lo), "r"(hi), "r"(idesc), "n"(ACC ? 1 : 0)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b_lo, uint32_t hi, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\t"
+      "mov.b64 b, {%2, %3};\n\t"
+      "setp.ne.b32 p, %5, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(b_lo), "r"(hi), "r"(idesc), "r"(acc)
+      : "memory");
+}
+
+__device__ __forceinline__ bool elect_one() {
+  uint32_t one;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(one));
+  return one != 0;
+}
+
+// mbar_wait_bounded that looks at the timer only once the wait is a long one:
+// a reading takes about a microsecond, which every wait would pay.
+__device__ __forceinline__ bool wait_bounded(uint64_t* bar, uint32_t parity) {
+#pragma unroll 1
+  for (int i = 0; i < 64; ++i)
+    if (mbar_try_wait(bar, parity)) return true;
+  return mbar_wait_bounded(bar, parity);
+}
+
+// Packed products: d = a * b, r = r * z + c.
+__device__ __forceinline__ void mul2(float& d0, float& d1, float a0, float a1, float b0, float b1) {
+  unsigned long long a, b, d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(a) : "f"(a0), "f"(a1));
+  asm("mov.b64 %0, {%1, %2};" : "=l"(b) : "f"(b0), "f"(b1));
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(d0), "=f"(d1) : "l"(d));
+}
+__device__ __forceinline__ void horner2(float& r0, float& r1, float z0, float z1, float c) {
+  unsigned long long r, z, cc;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(r0), "f"(r1));
+  asm("mov.b64 %0, {%1, %2};" : "=l"(z) : "f"(z0), "f"(z1));
+  asm("mov.b64 %0, {%1, %1};" : "=l"(cc) : "f"(c));
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(r), "l"(z), "l"(cc));
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r0), "=f"(r1) : "l"(r));
+}
+
+__device__ __forceinline__ void fma2(float& d0, float& d1, float a0, float a1, float b0, float b1, float c0, float c1) {
+  unsigned long long a, b, c, d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(a) : "f"(a0), "f"(a1));
+  asm("mov.b64 %0, {%1, %2};" : "=l"(b) : "f"(b0), "f"(b1));
+  asm("mov.b64 %0, {%1, %2};" : "=l"(c) : "f"(c0), "f"(c1));
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(d0), "=f"(d1) : "l"(d));
+}
+
+constexpr int kCols = kTcKeys / 2;     // keys of a softmax thread
+
+// Bits [a, z) of a 32-bit word (clamped).
+__device__ __forceinline__ uint32_t span_bits(int a, int z) {
+  a = min(max(a, 0), 32);
+  z = min(max(z, 0), 32);
+  const uint32_t below_z = z == 32 ? 0xffffffffu : (1u << z) - 1u, below_a = a == 32 ? 0xffffffffu : (1u << a) - 1u;
+  return below_z & ~below_a;
+}
+
+// A thread's visible columns: [lo, end) of its 64, and those below `prefix`.
+struct Visible {
+  int lo, end, prefix;
+  __device__ bool all() const { return (lo <= 0 && end >= kCols) || prefix >= kCols; }
+  __device__ uint32_t bits(int word) const {
+    return span_bits(lo - 32 * word, end - 32 * word) | span_bits(0, prefix - 32 * word);
+  }
+  // Everything else becomes `x`, whatever it was (masked keys may hold anything).
+  __device__ void hide(float (&v)[kCols], float x) const {
+    const uint32_t m0 = bits(0), m1 = bits(1);
+#pragma unroll
+    for (int c = 0; c < kCols; ++c) v[c] = (((c < 32 ? m0 : m1) >> (c & 31)) & 1u) ? v[c] : x;
+  }
+};
+
+// s r(s^2) + add on two keys, r a polynomial of N coefficients; `most` keeps
+// the largest s^2.
+template <int N>
+__device__ __forceinline__ void odd_poly2(float& v0, float& v1, const float* coef, float add0, float add1, float& most) {
+  float z0, z1, r0 = coef[N - 1], r1 = coef[N - 1];
+  mul2(z0, z1, v0, v1, v0, v1);
+  most = tc_max3(most, z0, z1);
+#pragma unroll
+  for (int k = N - 2; k >= 0; --k) horner2(r0, r1, z0, z1, coef[k]);
+  fma2(v0, v1, v0, v1, r0, r1, add0, add1);
+}
+
+// A thread's 64 raw scores become scores in log2 units, -inf where the mask
+// leaves a column out, up to a part of the bias that is the same for eight
+// columns: column c's score is v[c] + base + (c / 8) * step.  A bias that
+// falls linearly (no key after any of the warp's rows) then costs nothing per
+// key: eight multiples of the slope ride on the last product, the rest joins
+// the reference that the exponent subtracts anyway.  `off`: the first column's
+// key minus the row's position; `again` reads the raw scores once more (a
+// warp with a score past the polynomial's range: it has computed in vain).
+template <typename Again>
+__device__ __forceinline__ void modify(float (&v)[kCols], const ModParams& p, const Visible& see, float nslope, int off,
+                                       float& base, float& step, Again again) {
+  const ScoreMod& m = p.mod;
+  const bool full = see.all();
+  const bool linear = m.slopes && __all_sync(FULL_MASK, off + kCols - 1 <= 0);
+  float k[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) k[i] = linear ? -nslope * (float)i : 0.f;
+  base = linear ? nslope * (float)-off : 0.f;
+  step = linear ? -nslope * 8.f : 0.f;
+  if (m.cap_in != 0.f) {
+    float most = 0.f;                  // largest square: the polynomial's range
+#pragma unroll
+    for (int c = 0; c < kCols; c += 2) odd_poly2<4>(v[c], v[c + 1], p.poly, k[c & 7], k[(c & 7) + 1], most);
+    if (!__all_sync(FULL_MASK, most <= p.poly_range)) {
+      again(v);
+#pragma unroll
+      for (int c = 0; c < kCols; ++c) v[c] = fmaf(tanh_fast(v[c] * m.cap_in), m.cap_out_log2, k[c & 7]);
+    }
+  } else {
+#pragma unroll
+    for (int c = 0; c < kCols; c += 2)
+      fma2(v[c], v[c + 1], v[c], v[c + 1], p.scale_log2, p.scale_log2, k[c & 7], k[(c & 7) + 1]);
+  }
+  if (m.slopes && !linear) {
+    const float first = (float)off;
+#pragma unroll
+    for (int c = 0; c < kCols; ++c) v[c] = fmaf(nslope, fabsf(first + (float)c), v[c]);
+  }
+  if (!full) see.hide(v, -INFINITY);
+}
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kThreads, 1) prefill_mod_kernel(const __grid_constant__ ModParams p) {
+  using L = Layout<D>;
+  constexpr int H = L::kHalves, kKStages = L::kKStages, kVStages = L::kVStages;
+  constexpr bool kSepP = D == 64;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  const uint32_t base = (raw + 1023u) & ~1023u;          // whole swizzle atoms
+  uint8_t* gbase = smem_raw + (base - raw);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(gbase + L::kBar);
+  const int warp = __shfl_sync(FULL_MASK, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;   // known to be uniform
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kNumBars; ++i) {
+      int arrivals = 1;
+      if ((i >= kPFull && i < kPVDone) || (i >= kSRead && i < kExch)) arrivals = kTileWarps;
+      if (i >= kExch && i < kItemFull) arrivals = 2;
+      if ((i >= kKEmpty && i < kVFull) || (i >= kVEmpty && i < kQFull)) arrivals = 2;      // both Q tiles
+      if (i >= kItemFree && i < kClaim) arrivals = kItemUsers;
+      mbar_init(&bars[i], arrivals);
+    }
+    fence_mbar_init();
+  }
+  // a Q tile's rows past its G * tile_tokens: no copy writes them, they stay zero
+  for (int i = p.group * p.tile_tokens * 8 + (int)threadIdx.x; i < kTcRows * 8; i += kThreads)
+    for (int t = 0; t < 2 * H; ++t) st_shared_v4(base + L::kQ + t * kHalf + i * 16, make_uint4(0u, 0u, 0u, 0u));
+  fence_proxy_async_smem();
+  if (warp == kMmaWarp) tmem_alloc(base + L::kBar + kTmemSlot, kTmemCols);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = __shfl_sync(FULL_MASK, *reinterpret_cast<volatile uint32_t*>(gbase + L::kBar + kTmemSlot), 0);
+
+  pdl_wait();      // the cache rows of this step come from the store kernel
+  pdl_trigger();
+  Item* ring_items = reinterpret_cast<Item*>(gbase + L::kItems);
+
+  if (warp == kKvWarp) {
+    // ------------------------------------------------------- K and V producer
+    // Lane s copies segment s of a tile (lane 0 waits for a free stage first);
+    // K runs kAhead tiles ahead of V.  A V tile with rows outside [lo, hi] is
+    // waited for and those rows zeroed before it is released, so that they
+    // never weigh in.
+    constexpr int kAhead = kKStages - 2;
+    const uint32_t box = (uint32_t)p.seg_rows * 128u;
+    const int nseg = kTcKeys / p.seg_rows;
+    if (lane == 0) {
+      asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&p.tmap_k)) : "memory");
+      asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&p.tmap_v)) : "memory");
+    }
+    constexpr int kNone = INT_MIN;             // a segment that misses [lo, hi]: nothing to load
+    bool ok = true;
+    int nk = 0, nv = 0;                        // K and V tiles so far, of all items
+    // one operand of a tile, whose block id is b in lane s; n-th of its kind
+    auto copy = [&](const CUtensorMap* map, uint32_t ring, int stages, int full0, int empty0, int n, int ks, int hk, int b) {
+      const int stg = n % stages;
+      if (n >= stages) {
+        if (lane == 0) ok = wait_bounded(&bars[empty0 + stg], ((n / stages) - 1) & 1);
+        ok = __shfl_sync(FULL_MASK, ok, 0);
+        if (!ok) return;
+      }
+      const bool good = b != kNone && b >= 0 && b < p.num_blocks;
+      const uint32_t loaded = __ballot_sync(FULL_MASK, good), bad = __ballot_sync(FULL_MASK, b != kNone && !good);
+      const uint32_t dst0 = ring + stg * H * kHalf + lane * box;
+      if (bad) {                               // a bad block id reads as zeros
+        if (lane == 0) flag_error(p.err, PKVD_ERR_BLOCK_ID);
+        if ((bad >> lane) & 1u) {
+          for (int h = 0; h < H; ++h)
+            for (uint32_t o = 0; o < box; o += 16) st_shared_v4(dst0 + h * kHalf + o, make_uint4(0u, 0u, 0u, 0u));
+          fence_proxy_async_smem();
+        }
+      }
+      __syncwarp();
+      uint64_t* bar = &bars[full0 + stg];
+      if (lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)__popc(loaded) * box * H);
+      __syncwarp();
+      if (good) {
+#pragma unroll
+        for (int h = 0; h < H; ++h) tma_load4(dst0 + h * kHalf, map, h * 64, hk, ks % p.block_size, b, bar);
+      }
+    };
+    for (int r = 0; ok; ++r) {
+      if (lane == 0) ok = wait_bounded(&bars[kItemFull + r % kItemRing], (r / kItemRing) & 1);
+      ok = __shfl_sync(FULL_MASK, ok, 0);
+      if (!ok) break;
+      const Item& cur = ring_items[r % kItemRing];
+      if (cur.n < 0) break;
+      const int32_t* table = p.tables + (int64_t)cur.seq * p.max_blocks;
+      const int n = cur.n, hk = cur.hk, lo = cur.lo, hi = cur.hi, kt_last = cur.kt_last;
+      auto key_of = [&](int t) { return (kt_last - t) * kTcKeys + lane * p.seg_rows; };
+      auto fetch = [&](int t) -> int {
+        const int ks = key_of(t);
+        if (t >= n || lane >= nseg || ks > hi || ks + p.seg_rows - 1 < lo) return kNone;
+        return __ldg(table + ks / p.block_size);
+      };
+      int b[4];                                // block ids of V tile t and the three after it
+#pragma unroll
+      for (int i = 0; i < 4; ++i) b[i] = fetch(i);
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i)
+        if (ok && i < n) copy(&p.tmap_k, base + L::kK, kKStages, kKFull, kKEmpty, nk++, key_of(i), hk, b[i]);
+      for (int t = 0; ok && t < n; ++t) {
+        if (t + kAhead < n) copy(&p.tmap_k, base + L::kK, kKStages, kKFull, kKEmpty, nk++, key_of(t + kAhead), hk, b[kAhead]);
+        if (!ok) break;
+        copy(&p.tmap_v, base + L::kV, kVStages, kVFull, kVEmpty, nv++, key_of(t), hk, b[0]);
+        if (!ok) break;
+        const int stg = (nv - 1) % kVStages, kbase = (kt_last - t) * kTcKeys;
+        if (kbase < lo || kbase + kTcKeys - 1 > hi) {
+          if (lane == 0) ok = wait_bounded(&bars[kVFull + stg], ((nv - 1) / kVStages) & 1);
+          ok = __shfl_sync(FULL_MASK, ok, 0);
+          if (!ok) break;
+          for (int rr = lane; rr < kTcKeys; rr += 32) {
+            const int kp = kbase + rr;
+            if (kp >= lo && kp <= hi) continue;
+            for (int h = 0; h < H; ++h)
+              for (int c = 0; c < 8; ++c)
+                st_shared_v4(base + L::kV + stg * H * kHalf + h * kHalf + rr * 128 + c * 16, make_uint4(0u, 0u, 0u, 0u));
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+        }
+        if (lane == 0) mbar_arrive(&bars[kVReady + stg]);
+        b[0] = b[1];
+        b[1] = b[2];
+        b[2] = b[3];
+        b[3] = fetch(t + 4);
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars[kItemFree + r % kItemRing]);
+    }
+    if (!ok && lane == 0) {
+      // gave up: let the copies still in flight land before the CTA leaves
+      flag_error(p.err, PKVD_ERR_TIMEOUT);
+      for (int u = max(0, nk - kKStages); u < nk; ++u) wait_bounded(&bars[kKFull + u % kKStages], (u / kKStages) & 1);
+      for (int u = max(0, nv - kVStages); u < nv; ++u) wait_bounded(&bars[kVFull + u % kVStages], (u / kVStages) & 1);
+    }
+  } else if (warp == kQWarp) {
+    // ------------------------------------------------- items and Q producer
+    // Items are worked out kItemAhead ahead (empty ones are left out, -1 ends
+    // the list); a tile's rows are one box per 64 columns (G heads of
+    // tile_tokens tokens), loaded once the tensor cores are done with the item
+    // before.
+    uint8_t* order = p.num_seqs <= kSorted ? gbase + L::kOrder : nullptr;
+    if (order) {                                 // a sequence's place: how many are longer, or as long and before it
+      for (int i = lane; i < p.num_seqs; i += 32) {
+        const int len = p.cu_k[i + 1] - p.cu_k[i];
+        int before = 0;
+        for (int j = 0; j < p.num_seqs; ++j) {
+          const int other = p.cu_k[j + 1] - p.cu_k[j];
+          before += other > len || (other == len && j < i);
+        }
+        order[before] = (uint8_t)i;
+      }
+      __syncwarp();
+    }
+    if (lane == 0) {
+      asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&p.tmap_q)) : "memory");
+      bool ok = true, own = true;                // first the CTA's own item
+      int made = 0, asked = 0, used[2] = {0, 0}, next = blockIdx.x;
+      auto make = [&] {                          // the next item into the ring
+        const int slot = made % kItemRing;
+        if (made >= kItemRing) ok = ok && wait_bounded(&bars[kItemFree + slot], ((made / kItemRing) - 1) & 1);
+        Item it;
+        it.n = 0;
+        while (ok && it.n == 0) {
+          if (!own) {
+            fence_proxy_async_smem();            // the last answer has been read
+            mbar_arrive_expect_tx(&bars[kClaim], 16);
+            claim(base + L::kBar + kAnswer, &bars[kClaim]);
+            ok = wait_bounded(&bars[kClaim], asked & 1);
+            ++asked;
+            if (!ok) break;
+            next = claimed(base + L::kBar + kAnswer);
+          }
+          own = false;
+          if (next < 0) it.n = -1;
+          else it = item_at(p, order, next);
+        }
+        if (!ok) return;
+        ring_items[slot] = it;
+        mbar_arrive(&bars[kItemFull + slot]);
+        ++made;
+      };
+      for (int r = 0; ok; ++r) {
+        while (ok && made <= r + kItemAhead && !(made > 0 && ring_items[(made - 1) % kItemRing].n < 0)) make();
+        if (!ok) break;
+        const Item it = ring_items[r % kItemRing];
+        if (it.n < 0) break;
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+          if (!ok || it.gn[g] == 0) continue;
+          if (used[g] > 0) ok = wait_bounded(&bars[kQEmpty + g], (used[g] - 1) & 1);
+          if (!ok) continue;
+          mbar_arrive_expect_tx(&bars[kQFull + g], p.q_box * H);
+          for (int h = 0; h < H; ++h)
+            tma_load3(base + L::kQ + (g * H + h) * kHalf, &p.tmap_q, h * 64, it.hk * p.group, it.q0 + it.tb[g],
+                      &bars[kQFull + g]);
+          ++used[g];
+        }
+      }
+      if (!ok) flag_error(p.err, PKVD_ERR_TIMEOUT);
+      for (int g = 0; g < 2; ++g)                // no copy is in flight when the CTA leaves
+        if (used[g] > 0) wait_bounded(&bars[kQFull + g], (used[g] - 1) & 1);
+    }
+  } else if (warp == kMmaWarp || warp == kMmaWarp1) {
+    // ---------------------------------------------------------------- MMA
+    // S(n) of the Q tile, n counting all its K tiles: Q and K have landed and
+    // its S columns are free (head_dim 64: S(n - 1) was read; 128: PV(n - 1)
+    // is done, its weights lie there).  PV(n): the weights, V, and for an
+    // item's first one the O columns of the item before were read.  A K or V
+    // stage is free when both Q tiles are done with it; a tile that this one
+    // does not use it waits for all the same, so that no phase of a stage is
+    // waited for before the one before it is over.
+    //
+    // The whole warp walks through this and one elected thread issues: a
+    // product takes its operands from uniform registers, which the compiler
+    // fills directly where everything is known to be the same in all lanes
+    // (hence the shuffles).  In a branch of one lane every operand was moved
+    // there for every product, 200 to 300 clocks each.
+    {
+      const bool leader = elect_one();
+      const int g = warp == kMmaWarp ? 0 : 1;
+      constexpr uint32_t fmt = std::is_same<T, __nv_bfloat16>::value ? 1u : 0u;
+      constexpr uint32_t id_s = tc_idesc(fmt, kTcKeys, 0), id_pv = tc_idesc(fmt, D, 1), hi = desc_hi(1024);
+      const uint32_t qd = desc_lo(base + L::kQ + g * H * kHalf, 16);
+      const uint32_t s_cols = tmem + g * kTcKeys, o_cols = tmem + kColO + g * D;
+      const uint32_t p_cols = kSepP ? tmem + kColP64 + g * 64 : s_cols;
+      bool ok = true;
+      auto wait = [&](int bar, uint32_t parity) {
+        if (ok) ok = __all_sync(FULL_MASK, wait_bounded(&bars[bar], parity));
+      };
+      int at = 0, n = 0, used = 0;                  // K/V tiles of all items, this tile's, its items
+      for (int r = 0; ok; ++r) {
+        wait(kItemFull + r % kItemRing, (r / kItemRing) & 1);
+        if (!ok) break;
+        const Item& it = ring_items[r % kItemRing];
+        const int all = __shfl_sync(FULL_MASK, it.n, 0);
+        if (all < 0) break;
+        const int gn = __shfl_sync(FULL_MASK, it.gn[g], 0), first = at + __shfl_sync(FULL_MASK, it.gf[g], 0);
+        auto skip = [&](int from, int to) {         // tiles that this Q tile does not use
+          for (int t = from; t < to; ++t) {
+            wait(kKFull + t % kKStages, (t / kKStages) & 1);
+            if (ok && leader) mbar_arrive(&bars[kKEmpty + t % kKStages]);
+            wait(kVFull + t % kVStages, (t / kVStages) & 1);
+            wait(kVReady + t % kVStages, (t / kVStages) & 1);
+            if (ok && leader) mbar_arrive(&bars[kVEmpty + t % kVStages]);
+          }
+        };
+        skip(at, gn > 0 ? first : at + all);
+        auto issue_s = [&](int j) {                 // the n-th of the tile is the item's j-th
+          const int t = first + j, stg = t % kKStages;
+          wait(kKFull + stg, (t / kKStages) & 1);
+          if (!ok) return;
+          tc_fence_after();
+          const uint32_t kd = desc_lo(base + L::kK + stg * H * kHalf, 16);
+          if (leader) {
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k) {
+              const uint32_t off = ((k >> 2) * kHalf + (k & 3) * 32) >> 4;
+              if (k == 0) mma_ss<false>(s_cols, qd, kd, hi, id_s);
+              else mma_ss<true>(s_cols, qd + off, kd + off, hi, id_s);
+            }
+            tc_commit(&bars[kSFull + g]);
+            tc_commit(&bars[kKEmpty + stg]);
+            if (j == gn - 1) tc_commit(&bars[kQEmpty + g]);
+          }
+          __syncwarp();
+        };
+        if (gn > 0) {
+          wait(kQFull + g, used & 1);
+          if (n > 0) wait((kSepP ? kSRead : kPVDone) + g, (n - 1) & 1);
+          if (ok) issue_s(0);
+          for (int j = 0; ok && j < gn; ++j, ++n) {
+            if (kSepP && j + 1 < gn) {
+              wait(kSRead + g, n & 1);
+              if (ok) issue_s(j + 1);
+            }
+            const int t = first + j, stg = t % kVStages;
+            wait(kPFull + g, n & 1);
+            wait(kVFull + stg, (t / kVStages) & 1);
+            wait(kVReady + stg, (t / kVStages) & 1);
+            if (j == 0 && used > 0) wait(kOFree + g, (used - 1) & 1);
+            if (!ok) break;
+            tc_fence_after();
+            const uint32_t vd = desc_lo(base + L::kV + stg * H * kHalf, kHalf);
+            if (leader) {
+#pragma unroll
+              for (int k = 0; k < kTcKeys / 16; ++k) {      // 16 keys = 8 packed columns of weights
+                const uint32_t col = kSepP ? k * 8 : (k >> 2) * kCols + (k & 3) * 8;
+                mma_ts(o_cols, p_cols + col, vd + k * 128, hi, id_pv, k > 0 ? 1u : (uint32_t)j);
+              }
+              tc_commit(&bars[kPVDone + g]);
+              tc_commit(&bars[kVEmpty + stg]);
+            }
+            __syncwarp();
+            if (!kSepP && j + 1 < gn) {
+              wait(kPVDone + g, n & 1);
+              if (ok) issue_s(j + 1);
+            }
+          }
+          ++used;
+          skip(first + gn, at + all);
+        }
+        at += all;
+        __syncwarp();
+        if (leader) mbar_arrive(&bars[kItemFree + r % kItemRing]);
+      }
+      if (!ok && leader) flag_error(p.err, PKVD_ERR_TIMEOUT);
+      if (leader) tc_commit(&bars[kDrain + g]);   // every product issued is done when the CTA leaves
+      wait_bounded(&bars[kDrain + g], 0);
+    }
+  } else {
+    // ------------------------------------------------------------ softmax
+    // Every wait is bounded; a warp whose wait gives up leaves (the others'
+    // then give up in turn).
+    const int g = warp >> 3, half = (warp >> 2) & 1, quarter = warp & 3, row = quarter * 32 + lane;
+    const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t s_addr = tmem + lane_base + g * kTcKeys + half * kCols;
+    const uint32_t p_addr = kSepP ? tmem + lane_base + kColP64 + g * 64 + half * 32 : s_addr;
+    const uint32_t o_addr = tmem + lane_base + kColO + g * D + half * (D / 2);
+    // what a row's two threads tell each other: 128 bytes a quarter of the rows
+    uint8_t* xch = gbase + L::kX + g * 512 + quarter * 128;
+    float* xsum = reinterpret_cast<float*>(xch);
+    bool ok = true;
+    auto wait = [&](int bar, uint32_t parity) {
+      if (ok) ok = __all_sync(FULL_MASK, wait_bounded(&bars[bar], parity));
+    };
+    auto arrive = [&](int bar) {                 // for the warp
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars[bar]);
+    };
+    int exchanges = 0;
+    auto exchange = [&] {                        // what the row's two warps wrote is readable by both
+      arrive(kExch + 4 * g + quarter);
+      wait(kExch + 4 * g + quarter, exchanges & 1);
+      ++exchanges;
+    };
+    int n = 0;                                   // this tile's K tiles so far, of all items
+    for (int r = 0; ok; ++r) {
+      wait(kItemFull + r % kItemRing, (r / kItemRing) & 1);
+      if (!ok) break;
+      const Item& it = ring_items[r % kItemRing];
+      if (it.n < 0) break;
+      const int tb = it.tb[g], te = it.te[g], gf = it.gf[g], gn = it.gn[g];
+      if (gn == 0) {
+        arrive(kItemFree + r % kItemRing);
+        continue;
+      }
+      const int kt_last = it.kt_last, prefix = it.prefix;
+      const bool live = row < (te - tb) * p.group;
+      const int tt = live ? row / p.group : 0, gi = live ? row - tt * p.group : 0;
+      const int pr = it.cached + tb + tt;        // padding rows mirror row 0
+      const int wr = window_first(pr + 1, p.window);
+      const float nslope = bias_slope(p.mod, it.hk * p.group + gi);
+      float m_ref = p.bounded ? 0.f : -INFINITY, l = 0.f;
+      for (int j = 0; j < gn; ++j, ++n) {
+        const int kbase = (kt_last - gf - j) * kTcKeys + half * kCols;
+        const Visible see = {wr - kbase, pr + 1 - kbase, prefix - kbase};
+        wait(kSFull + g, n & 1);
+        if (!ok) break;
+        tc_fence_after();
+        float v[kCols];
+        auto read = [&](float (&x)[kCols]) {
+          tmem_ld32(s_addr, x);
+          tmem_ld32(s_addr + 32, x + 32);
+          tmem_ld_wait();
+        };
+        read(v);
+        // head_dim 64: the next S may overwrite these columns once nobody reads them again
+        const bool capped = p.mod.cap_in != 0.f;
+        if (kSepP && !capped) {
+          tc_fence_before();
+          arrive(kSRead + g);
+        }
+        float bias, step;
+        modify(v, p, see, nslope, kbase - pr, bias, step, read);
+        if (kSepP && capped) {
+          tc_fence_before();
+          arrive(kSRead + g);
+        }
+        float alpha = 1.f;
+        bool scale_o = false;
+        if (!p.bounded) {
+          float top = -INFINITY;
+#pragma unroll
+          for (int c = 0; c < kCols; c += 8)
+            top = fmaxf(top, fmaxf(tc_max3(tc_max3(v[c], v[c + 1], v[c + 2]), v[c + 3], v[c + 4]),
+                                   tc_max3(v[c + 5], v[c + 6], v[c + 7])) + (bias + step * (c / 8)));
+          // the two halves of a row agree on a reference: any common one does,
+          // so 16 bits (rounded up) are enough
+          __nv_bfloat16* x = reinterpret_cast<__nv_bfloat16*>(xch + (kSepP ? (n & 1) * 1024 : 0));
+          const __nv_bfloat16 mine = __float2bfloat16_ru(top);
+          x[half * 32 + lane] = mine;
+          exchange();
+          const float mt = fmaxf(__bfloat162float(mine), __bfloat162float(x[(half ^ 1) * 32 + lane]));
+          const bool rebase = mt > m_ref + kRebase;
+          scale_o = rebase && m_ref != -INFINITY;
+          alpha = scale_o ? tc_ex2(m_ref - mt) : 1.f;
+          if (rebase) m_ref = mt;
+        }
+        const float mu = m_ref == -INFINITY ? 0.f : m_ref;
+        uint32_t pk[kCols / 2];
+        float s0 = 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f, shift0 = bias - mu, shift1 = shift0;
+#pragma unroll
+        for (int c = 0; c < kCols; c += 4) {
+          if (c > 0 && c % 8 == 0) tc_add2(shift0, shift1, step, step);
+          tc_add2(v[c], v[c + 1], shift0, shift1);
+          tc_add2(v[c + 2], v[c + 3], shift0, shift1);
+          const float e0 = tc_ex2(v[c]), e1 = tc_ex2(v[c + 1]), e2 = tc_ex2(v[c + 2]), e3 = tc_ex2(v[c + 3]);
+          tc_add2(s0, s1, e0, e1);
+          tc_add2(s2, s3, e2, e3);
+          pk[c / 2] = Mma<T>::pack(e0, e1);
+          pk[c / 2 + 1] = Mma<T>::pack(e2, e3);
+        }
+        l = l * alpha + ((s0 + s1) + (s2 + s3));
+        if (kSepP && j > 0) {                    // the weights' columns are free once PV(n - 1) is done
+          wait(kPVDone + g, (n - 1) & 1);
+          tc_fence_after();
+        }
+        if (__any_sync(FULL_MASK, scale_o)) {    // O too (head_dim 128: PV(n - 1) was done before S(n))
+#pragma unroll 1
+          for (int c4 = 0; c4 < D / 64; ++c4) {
+            float o[32];
+            tmem_ld32(o_addr + c4 * 32, o);
+            tmem_ld_wait();
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] *= alpha;
+            tmem_st32(o_addr + c4 * 32, o);
+          }
+        }
+        tmem_st32(p_addr, reinterpret_cast<const float*>(pk));
+        tmem_st_wait();
+        tc_fence_before();
+        arrive(kPFull + g);
+      }
+      if (!ok) break;
+      wait(kPVDone + g, (n - 1) & 1);            // and so every warp of the tile is past its last exchange
+      if (!ok) break;
+      tc_fence_after();
+      // the row's sum: half 1's part to half 0, the whole back
+      if (half == 1) xsum[lane] = l;
+      exchange();
+      if (half == 0) {
+        l += xsum[lane];
+        xsum[lane] = l;
+      }
+      exchange();
+      if (half == 1) l = xsum[lane];
+      const float inv = l > 0.f ? 1.f / l : 0.f;
+      T* dst = static_cast<T*>(p.out) + ((int64_t)(it.q0 + tb + tt) * p.hq + (int64_t)it.hk * p.group + gi) * D +
+               half * (D / 2);
+#pragma unroll
+      for (int c4 = 0; c4 < D / 64; ++c4) {
+        float o[32];
+        tmem_ld32(o_addr + c4 * 32, o);
+        tmem_ld_wait();
+        if (c4 == D / 64 - 1) {
+          tc_fence_before();
+          arrive(kOFree + g);
+        }
+        if (live) {
+          uint32_t w[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) w[e] = Mma<T>::pack(o[2 * e] * inv, o[2 * e + 1] * inv);
+          T* d = dst + c4 * 32;
+          if (p.wide_out) {                      // whole 32-byte sectors a store
+#pragma unroll
+            for (int e = 0; e < 16; e += 8)
+              asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(d + 2 * e), "r"(w[e]),
+                           "r"(w[e + 1]), "r"(w[e + 2]), "r"(w[e + 3]), "r"(w[e + 4]), "r"(w[e + 5]), "r"(w[e + 6]),
+                           "r"(w[e + 7])
+                           : "memory");
+          } else {
+#pragma unroll
+            for (int e = 0; e < 16; e += 4)
+              *reinterpret_cast<uint4*>(d + 2 * e) = make_uint4(w[e], w[e + 1], w[e + 2], w[e + 3]);
+          }
+        }
+      }
+      arrive(kItemFree + r % kItemRing);
+      exchange();                                // xsum is read before the next item's first maximum
+    }
+    if (!ok && lane == 0) flag_error(p.err, PKVD_ERR_TIMEOUT);
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+// Tensor map over q [total_q, Hq, D]: box = 64 columns x G heads x tile_tokens tokens.
+bool encode_q_map(CUtensorMap* map, const PrefillArgs& a, int group, int tile_tokens) {
+  EncodeTiled fn = encode_fn();
+  if (!fn) return false;
+  const cuuint64_t D = a.cache.head_dim;
+  const cuuint64_t dims[3] = {D, (cuuint64_t)a.num_q_heads, (cuuint64_t)a.total_q};
+  const cuuint64_t strides[2] = {D * 2, D * 2 * a.num_q_heads};
+  const cuuint32_t box[3] = {64, (cuuint32_t)group, (cuuint32_t)tile_tokens};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  const CUtensorMapDataType dt =
+      a.cache.dtype == PKVD_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+  return fn(map, dt, 3, const_cast<void*>(a.q), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
+         CUDA_SUCCESS;
+}
+
+template <typename T, int D>
+cudaError_t launch_typed(const ModParams& prm, cudaStream_t stream) {
+  constexpr int smem = Layout<D>::kBytes;
+  cudaError_t e = cudaFuncSetAttribute(prefill_mod_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(prefill_mod_kernel<T, D>, dim3((unsigned)prm.items), dim3(kThreads), smem, stream, prm);
+}
+
+}  // namespace
+
+// Calls that prefill_tc_supported takes.
+cudaError_t launch_prefill_mod(const PrefillArgs& a, cudaStream_t stream) {
+  const pkvd_cache& c = a.cache;
+  const int G = a.num_q_heads / c.num_kv_heads;
+  const int seg_rows = c.block_size < kTcKeys ? c.block_size : kTcKeys;
+  ModParams prm;
+  prm.tile_tokens = kTcRows / G;
+  if (!encode_cache_map(&prm.tmap_k, c.k_base, c, seg_rows) || !encode_cache_map(&prm.tmap_v, c.v_base, c, seg_rows) ||
+      !encode_q_map(&prm.tmap_q, a, G, prm.tile_tokens))
+    return cudaErrorInvalidValue;
+  prm.out = a.out;
+  prm.tables = a.block_tables;
+  prm.max_blocks = a.max_blocks_per_seq;
+  prm.num_blocks = c.num_blocks;
+  prm.block_size = c.block_size;
+  prm.seg_rows = seg_rows;
+  prm.cu_q = a.cu_seqlens_q;
+  prm.cu_k = a.cu_seqlens_k;
+  prm.total_q = a.total_q;
+  prm.hq = a.num_q_heads;
+  prm.hkv = c.num_kv_heads;
+  prm.group = G;
+  prm.q_box = 128u * (uint32_t)(G * prm.tile_tokens);
+  const int tiles = (a.max_seqlen_q + prm.tile_tokens - 1) / prm.tile_tokens;
+  prm.pairs = (tiles + 1) / 2;
+  prm.num_seqs = a.num_seqs;
+  const int64_t items = (int64_t)prm.pairs * c.num_kv_heads * a.num_seqs;
+  if (items > 0x7fffffff) return cudaErrorInvalidConfiguration;
+  prm.items = (int)items;
+  prm.scale_log2 = a.scale * 1.4426950408889634f;
+  prm.window = a.window;
+  prm.mod = a.mod;
+  // cap tanh(s / cap) log2 e as a polynomial in the raw product s, whose
+  // scale goes into the coefficients (not where their powers leave fp32)
+  constexpr float kRatio[4] = PKVD_TANH_RATIO4;
+  const double in = a.mod.cap_in, size = std::fabs(in);
+  const double least = std::fabs(kRatio[3]) * std::pow(size, 7) * a.mod.cap_out_log2;
+  const bool poly = size > 1e-5 && size < 1e4 && least > 1e-37 && least < 1e37;
+  for (int k = 0; k < 4; ++k) prm.poly[k] = poly ? (float)(kRatio[k] * std::pow(in, 2 * k + 1) * a.mod.cap_out_log2) : 0.f;
+  prm.poly_range = poly ? (float)(kTanhNear * kTanhNear / (size * size)) : -1.f;
+  prm.wide_out = reinterpret_cast<uintptr_t>(a.out) % 32 == 0;
+  // 2^64 times a sum of 2^23 keys and a value of 2^16 stays within fp32
+  prm.bounded = c.dtype == PKVD_BF16 && a.mod.cap_in != 0.f && a.mod.cap_out_log2 <= 64.f && !a.mod.slopes;
+  prm.err = a.err;
+  if (c.dtype == PKVD_BF16)
+    return c.head_dim == 64 ? launch_typed<__nv_bfloat16, 64>(prm, stream)
+                            : launch_typed<__nv_bfloat16, 128>(prm, stream);
+  return c.head_dim == 64 ? launch_typed<__half, 64>(prm, stream) : launch_typed<__half, 128>(prm, stream);
+}
+
+}  // namespace pkvd

@@ -39,27 +39,20 @@
 // are read K-major (stride between 8-row groups 1024 B); V is read
 // MN-major (head_dim contiguous: 1024 B between 8-key groups, one half-tile
 // between 64-column halves).
-#include <cuda.h>
-#include <cudaTypedefs.h>
-
-#include <atomic>
 #include <climits>
 #include <cmath>
 
 #include "common.cuh"
 #include "launch.h"
-#include "score_mod.cuh"
+#include "tcgen05.cuh"
 
 namespace pkvd {
 
 namespace {
 
-constexpr int kTcRows = 128;          // M: query rows per Q tile (two Q tiles per CTA)
-constexpr int kTcKeys = 128;          // keys per K/V tile
 constexpr int kTcThreads = 384;       // 2 x 4 softmax warps, K producer, MMA 0, V producer, MMA 1
 constexpr int kGroup = 128;           // softmax threads per Q tile (one per row)
 constexpr int kProducerWarp = 8, kMmaWarp = 9, kVProducerWarp = 10, kMmaWarp1 = 11;
-constexpr uint32_t kHalf = 128u * 128u;   // one 128-row x 64-column 16-bit half tile
 constexpr uint32_t kTmemCols = 512;
 // TMEM columns: S of Q tile g at [128 g, 128 g + 128) (P of that tile is written
 // over its first 64 columns once S is read); O of Q tile g at [256 + g D, 256 + g D + D)
@@ -116,239 +109,14 @@ struct TcParams {
   int64_t l2_bytes;      // the device's L2 size, for the CTA order
   float scale_log2;
   int window;
-  ScoreMod mod;          // read by the MOD kernels only
   int32_t* err;
 };
-
-// Spin (test_wait) until the phase with this parity has completed; false
-// after 2 s without it (the caller flags PKVD_ERR_TIMEOUT).
-__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity);
-__device__ __forceinline__ bool mbar_poll_bounded(uint64_t* bar, uint32_t parity) {
-  if (mbar_test(bar, parity)) return true;
-  const uint64_t t0 = globaltimer_ns();
-  for (uint32_t spin = 0;; ++spin) {
-    if (mbar_test(bar, parity)) return true;
-    if ((spin & 255u) == 255u && globaltimer_ns() - t0 > 2000000000ull) return false;
-  }
-}
-
-// Non-blocking: has the phase with this parity completed?
-__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(smem_u32(bar)), "r"(parity)
-      : "memory");
-  return ok != 0;
-}
 
 __device__ __forceinline__ int tc_window_start(int c, int window) {
   return (window > 0 && c > window) ? c - window : 0;
 }
 
-__device__ __forceinline__ float tc_ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
-// Three-input maximum (one instruction on sm_100-family parts).
-__device__ __forceinline__ float tc_max3(float a, float b, float c) {
-  float d;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
-  return d;
-}
-
-// Packed pair arithmetic on two fp32 lanes (one instruction each).
-__device__ __forceinline__ void tc_fma2(float& d0, float& d1, float a0, float a1, float b, float c) {
-  unsigned long long a, bb, cc, d;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(a) : "f"(a0), "f"(a1));
-  asm("mov.b64 %0, {%1, %1};" : "=l"(bb) : "f"(b));
-  asm("mov.b64 %0, {%1, %1};" : "=l"(cc) : "f"(c));
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(bb), "l"(cc));
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(d0), "=f"(d1) : "l"(d));
-}
-__device__ __forceinline__ void tc_mul2(float& d0, float& d1, float a0, float a1, float b0, float b1) {
-  unsigned long long a, b, d;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(a) : "f"(a0), "f"(a1));
-  asm("mov.b64 %0, {%1, %2};" : "=l"(b) : "f"(b0), "f"(b1));
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(d0), "=f"(d1) : "l"(d));
-}
-// r = r * z + c on both lanes
-__device__ __forceinline__ void tc_fma2v(float& r0, float& r1, float z0, float z1, float c) {
-  unsigned long long r, z, cc;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(r0), "f"(r1));
-  asm("mov.b64 %0, {%1, %2};" : "=l"(z) : "f"(z0), "f"(z1));
-  asm("mov.b64 %0, {%1, %1};" : "=l"(cc) : "f"(c));
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(r), "l"(z), "l"(cc));
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(r0), "=f"(r1) : "l"(r));
-}
-__device__ __forceinline__ void tc_add2(float& d0, float& d1, float a0, float a1) {
-  unsigned long long a, d;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(a) : "f"(a0), "f"(a1));
-  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(d0), "f"(d1));
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(d), "l"(a));
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(d0), "=f"(d1) : "l"(d));
-}
-
-// ------------------------------------------------------------ tcgen05 PTX
-__device__ __forceinline__ void tmem_alloc(uint32_t slot_smem, uint32_t ncols) {
-  asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(slot_smem), "r"(ncols)
-               : "memory");
-  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
-}
-
-__device__ __forceinline__ void tmem_dealloc(uint32_t taddr, uint32_t ncols) {
-  asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
-}
-
-__device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
-
-// D[tmem] (+)= A[smem desc] * B[smem desc]^T, kind::f16, one CTA.
-__device__ __forceinline__ void tc_mma(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
-                                       uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
-
-// D[tmem] (+)= A[tmem] * B[smem desc]^T, kind::f16: A (M x 16) lane i = row i,
-// 16-bit pairs along K packed in 32-bit columns.
-__device__ __forceinline__ void tc_mma_tmem_a(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
-                                              uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
-
-// Arrive once on `bar` when every tcgen05 operation this thread issued so far completes.
-__device__ __forceinline__ void tc_commit(uint64_t* bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
-               : "memory");
-}
-
-// 32 consecutive fp32 columns of this thread's TMEM lane.
-__device__ __forceinline__ void tmem_ld32(uint32_t taddr, float* v) {
-  uint32_t* r = reinterpret_cast<uint32_t*>(v);
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
-      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
-        "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
-        "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-      : "r"(taddr));
-}
-
-__device__ __forceinline__ void tmem_st32(uint32_t taddr, const float* v) {
-  const uint32_t* r = reinterpret_cast<const uint32_t*>(v);
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
-      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
-      "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
-      "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]),
-      "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]),
-      "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
-      : "memory");
-}
-
-__device__ __forceinline__ void tmem_ld_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
-__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
-
-// Shared-memory matrix descriptor: 128-byte swizzle, version 1.
-__device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lbo, uint32_t sbo) {
-  return (uint64_t)((addr & 0x3FFFFu) >> 4) | ((uint64_t)((lbo >> 4) & 0x3FFFu) << 16) |
-         ((uint64_t)((sbo >> 4) & 0x3FFFu) << 32) | (1ull << 46) | (2ull << 61);
-}
-
-// Instruction descriptor of kind::f16: fp32 accumulator, A and B of the same
-// 16-bit type (0 f16, 1 bf16), A K-major, B K-major (b_mn = 0) or MN-major.
-__host__ __device__ constexpr uint32_t tc_idesc(uint32_t fmt, uint32_t n, uint32_t b_mn) {
-  return (1u << 4) | (fmt << 7) | (fmt << 10) | (b_mn << 16) | ((n >> 3) << 17) | ((uint32_t)(kTcRows >> 4) << 24);
-}
-
-// 4-D tiled TMA load: coordinates (column, kv head, row in block, block).
-__device__ __forceinline__ void tma_load4(uint32_t dst, const CUtensorMap* map, int c0, int c1, int c2, int c3,
-                                          uint64_t* bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], "
-      "[%6];" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(smem_u32(bar))
-      : "memory");
-}
-
-// Byte offset of 16-byte chunk c (0..7) of row r inside a 128-byte-swizzled half tile.
-__device__ __forceinline__ uint32_t swz(int r, int c) { return (uint32_t)(r * 128 + ((c ^ (r & 7)) << 4)); }
-
-__device__ __forceinline__ void st_shared_v4(uint32_t addr, uint4 v) {
-  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
-               : "memory");
-}
-
-// A row's 128 raw scores with cap and bias applied, in log2 units.  `off`:
-// the tile's first key minus the row's position.  Columns that the mask
-// leaves out count as 0 before the cap (their keys may hold anything) and are
-// masked by the caller afterwards.
-__device__ __forceinline__ void tc_modify(float (&v)[kTcKeys], const TcParams& p, bool row_full, const uint32_t* mw,
-                                          float nslope, float off) {
-  const ScoreMod& m = p.mod;
-  if (m.cap_in != 0.f) {
-    if (!row_full) {
-#pragma unroll
-      for (int c = 0; c < kTcKeys; ++c) v[c] = ((mw[c >> 5] >> (c & 31)) & 1u) ? v[c] : 0.f;
-    }
-    float a0 = 0.f, a1 = 0.f, a2 = 0.f, a3 = 0.f;
-#pragma unroll
-    for (int c = 0; c < kTcKeys; c += 8) {
-      a0 = tc_max3(a0, fabsf(v[c]), fabsf(v[c + 1]));
-      a1 = tc_max3(a1, fabsf(v[c + 2]), fabsf(v[c + 3]));
-      a2 = tc_max3(a2, fabsf(v[c + 4]), fabsf(v[c + 5]));
-      a3 = tc_max3(a3, fabsf(v[c + 6]), fabsf(v[c + 7]));
-    }
-    const float most = fmaxf(tc_max3(a0, a1, a2), a3) * fabsf(m.cap_in);
-    if (__all_sync(FULL_MASK, most <= 1.f)) {
-      // every score of the warp's rows within the cap: the polynomial alone
-      // (FMAs, off by 6.9e-6 of the value against 2^-9 or 2^-12 of the
-      // rounded weights), two keys an instruction
-      constexpr float kRatio[5] = PKVD_TANH_RATIO5;
-#pragma unroll
-      for (int c = 0; c < kTcKeys; c += 2) {
-        float y0, y1, z0, z1, r0 = kRatio[4], r1 = kRatio[4];
-        tc_mul2(y0, y1, v[c], v[c + 1], m.cap_in, m.cap_in);
-        tc_mul2(z0, z1, y0, y1, y0, y1);
-#pragma unroll
-        for (int k = 3; k >= 0; --k) tc_fma2v(r0, r1, z0, z1, kRatio[k]);
-        tc_mul2(y0, y1, y0, y1, m.cap_out_log2, m.cap_out_log2);
-        tc_mul2(v[c], v[c + 1], y0, y1, r0, r1);
-      }
-    } else {
-#pragma unroll
-      for (int c = 0; c < kTcKeys; ++c) v[c] = tanh_fast(v[c] * m.cap_in) * m.cap_out_log2;
-    }
-  } else {
-#pragma unroll
-    for (int c = 0; c < kTcKeys; c += 2) tc_mul2(v[c], v[c + 1], v[c], v[c + 1], p.scale_log2, p.scale_log2);
-  }
-  if (m.slopes) {
-#pragma unroll
-    for (int c = 0; c < kTcKeys; ++c) v[c] = fmaf(nslope, fabsf(off + (float)c), v[c]);
-  }
-}
-
-template <typename T, int D, bool MOD>
+template <typename T, int D>
 // 12 warps: an SM sub-partition holds three of them, so at most 168 registers a thread
 __global__ void __launch_bounds__(kTcThreads, 1) prefill_tc_kernel(const __grid_constant__ TcParams p) {
   using L = TcLayout<D>;
@@ -395,14 +163,13 @@ __global__ void __launch_bounds__(kTcThreads, 1) prefill_tc_kernel(const __grid_
   // Q tile g = 1 holds the later tokens (tile 2 zpair counted from the end),
   // g = 0 the tile before it (may be empty).
   const int Tt = p.tile_tokens, G = p.group, cached = klen - qlen;
-  const int prefix = MOD ? prefix_of(p.mod, seq, klen) : 0;     // keys that every row reads
   int tb[2], te[2], lo_g[2], hi_g[2];
 #pragma unroll
   for (int g = 0; g < 2; ++g) {
     te[g] = qlen - (2 * zpair + 1 - g) * Tt;
     tb[g] = max(0, te[g] - Tt);
-    lo_g[g] = prefix > 0 ? 0 : tc_window_start(cached + tb[g] + 1, p.window);   // first key the tile's rows read
-    hi_g[g] = max(cached + te[g] - 1, prefix - 1);              // last key
+    lo_g[g] = tc_window_start(cached + tb[g] + 1, p.window);   // first key the tile's rows read
+    hi_g[g] = cached + te[g] - 1;                               // last key
   }
   if (te[1] <= 0) return;
   const bool has0 = te[0] > 0;
@@ -693,23 +460,17 @@ __global__ void __launch_bounds__(kTcThreads, 1) prefill_tc_kernel(const __grid_
       }
       const uint32_t s_addr = tmem + lane_base + kColS + g * kTcKeys;
       const uint32_t o_addr = tmem + lane_base + kColO + g * D;
-      const float nslope = MOD ? bias_slope(p.mod, hk * G + gi) : 0.f;
       float m_ref = -INFINITY, l = 0.f;
       bool ok = true;
       for (int j = 0; j < my_gn; ++j) {
         const int kbase = (kt_first + my_gf + j) * kTcKeys;
         const int c_lo = max(wr - kbase, 0), c_hi = min(pr - kbase, kTcKeys - 1);
-        const int c_pre = MOD ? prefix - kbase : 0;            // columns below it: the prefix
-        const bool row_full = (c_lo == 0 && c_hi == kTcKeys - 1) || c_pre >= kTcKeys;
+        const bool row_full = c_lo == 0 && c_hi == kTcKeys - 1;
         uint32_t mw[kTcKeys / 32];
 #pragma unroll
         for (int w = 0; w < kTcKeys / 32; ++w) {
           const int a = min(max(c_lo - 32 * w, 0), 32), z = min(max(c_hi + 1 - 32 * w, 0), 32);
           mw[w] = (z == 32 ? 0xffffffffu : ((1u << z) - 1u)) & ~(a == 32 ? 0xffffffffu : ((1u << a) - 1u));
-          if constexpr (MOD) {
-            const int f = min(max(c_pre - 32 * w, 0), 32);
-            mw[w] |= f == 32 ? 0xffffffffu : (1u << f) - 1u;
-          }
         }
         ok = __all_sync(FULL_MASK, mbar_wait_bounded(&bars[kSFull + g], j & 1));
         if (!ok) break;
@@ -723,10 +484,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) prefill_tc_kernel(const __grid_
           mbar_arrive(&bars[kSRead + g]);            // the next S may overwrite these columns
         }
         // raw scores: the scale (> 0) is applied inside the exponent, so the
-        // row max is taken over the raw values and scaled once (MOD: the
-        // scores are already in log2 units here, scale_log2 is 1 below)
-        if constexpr (MOD) tc_modify(v, p, row_full, mw, nslope, (float)(kbase - pr));
-        const float scale_log2 = MOD ? 1.f : p.scale_log2;
+        // row max is taken over the raw values and scaled once
         if (!row_full) {
 #pragma unroll
           for (int c = 0; c < kTcKeys; ++c)
@@ -740,7 +498,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) prefill_tc_kernel(const __grid_
           mx2 = tc_max3(mx2, v[c + 4], v[c + 5]);
           mx3 = tc_max3(mx3, v[c + 6], v[c + 7]);
         }
-        const float mt = fmaxf(tc_max3(mx0, mx1, mx2), mx3) * scale_log2;
+        const float mt = fmaxf(tc_max3(mx0, mx1, mx2), mx3) * p.scale_log2;
         const bool rebase = mt > m_ref + kRebase;
         const bool scale_o = rebase && m_ref != -INFINITY;
         const float alpha = scale_o ? tc_ex2(m_ref - mt) : 1.f;
@@ -752,8 +510,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) prefill_tc_kernel(const __grid_
         for (int c = 0; c < kTcKeys; c += 4) {
           // 2^(scale * s - mu) for two keys per packed FMA; masked keys give 2^-inf = 0
           float a0, a1, a2, a3;
-          tc_fma2(a0, a1, v[c], v[c + 1], scale_log2, -mu);
-          tc_fma2(a2, a3, v[c + 2], v[c + 3], scale_log2, -mu);
+          tc_fma2(a0, a1, v[c], v[c + 1], p.scale_log2, -mu);
+          tc_fma2(a2, a3, v[c + 2], v[c + 3], p.scale_log2, -mu);
           const float e0 = tc_ex2(a0), e1 = tc_ex2(a1), e2 = tc_ex2(a2), e3 = tc_ex2(a3);
           if (c & 4) tc_add2(rs2, rs3, e0, e1), tc_add2(rs2, rs3, e2, e3);
           else tc_add2(rs0, rs1, e0, e1), tc_add2(rs0, rs1, e2, e3);
@@ -825,50 +583,12 @@ __global__ void __launch_bounds__(kTcThreads, 1) prefill_tc_kernel(const __grid_
   }
 }
 
-using EncodeTiled = PFN_cuTensorMapEncodeTiled_v12000;
-
-// The driver's tensor-map encoder (one entry point for every device and
-// context).  Threads racing on the first lookup all store the same pointer.
-std::atomic<EncodeTiled> g_encode_fn{nullptr};
-
-EncodeTiled encode_fn() {
-  EncodeTiled fn = g_encode_fn.load(std::memory_order_acquire);
-  if (fn) return fn;
-  void* f = nullptr;
-  cudaDriverEntryPointQueryResult q;
-  if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) ==
-          cudaSuccess &&
-      q == cudaDriverEntryPointSuccess) {
-    fn = reinterpret_cast<EncodeTiled>(f);
-    g_encode_fn.store(fn, std::memory_order_release);
-  }
-  return fn;
-}
-
-// Tensor map over one cache ([num_blocks, block_size, Hkv, D] with element
-// strides), box = 64 columns x 1 head x seg_rows rows x 1 block, 128-byte swizzle.
-bool encode_cache_map(CUtensorMap* map, const void* base, const pkvd_cache& c, int seg_rows) {
-  EncodeTiled fn = encode_fn();
-  if (!fn) return false;
-  const cuuint64_t dims[4] = {(cuuint64_t)c.head_dim, (cuuint64_t)c.num_kv_heads, (cuuint64_t)c.block_size,
-                              (cuuint64_t)c.num_blocks};
-  const cuuint64_t strides[3] = {(cuuint64_t)c.head_stride * 2, (cuuint64_t)c.token_stride * 2,
-                                 (cuuint64_t)c.block_stride * 2};
-  const cuuint32_t box[4] = {64, 1, (cuuint32_t)seg_rows, 1};
-  const cuuint32_t estr[4] = {1, 1, 1, 1};
-  const CUtensorMapDataType dt = c.dtype == PKVD_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
-  return fn(map, dt, 4, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
-         CUDA_SUCCESS;
-}
-
 template <typename T, int D>
 cudaError_t launch_tc_typed(const TcParams& prm, dim3 grid, cudaStream_t stream) {
   constexpr int smem = TcLayout<D>::kBytes;
-  const auto kernel = prm.mod.on() ? prefill_tc_kernel<T, D, true> : prefill_tc_kernel<T, D, false>;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  cudaError_t e = cudaFuncSetAttribute(prefill_tc_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  return launch_pdl(kernel, grid, dim3(kTcThreads), smem, stream, prm);
+  return launch_pdl(prefill_tc_kernel<T, D>, grid, dim3(kTcThreads), smem, stream, prm);
 }
 
 }  // namespace
@@ -912,7 +632,6 @@ cudaError_t launch_prefill_tc(const PrefillArgs& a, cudaStream_t stream) {
   prm.tile_tokens = kTcRows / G;
   prm.scale_log2 = a.scale * 1.4426950408889634f;
   prm.window = a.window;
-  prm.mod = a.mod;
   prm.err = a.err;
   const int tiles = (a.max_seqlen_q + prm.tile_tokens - 1) / prm.tile_tokens;
   prm.pairs = (tiles + 1) / 2;                                     // two Q tiles per CTA

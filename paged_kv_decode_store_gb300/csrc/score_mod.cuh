@@ -29,10 +29,13 @@ __device__ __forceinline__ float tanh_large(float y) {
   return fmaf(-2.f, mod_rcp(1.f + mod_ex2(y * 2.885390081777927f)), 1.f);   // 2 log2(e)
 }
 
-// tanh(y) / y for |y| <= 1 as a polynomial in z = y^2 (relative minimax, found
-// by an exchange iteration): off by 5.9e-7 of the value with six terms and by
-// 6.9e-6 with five.  tanh's nearest pole is at z = -(pi / 2)^2, so each term
-// gains a factor of about 12 on [0, 1].
+// tanh(y) / y as a polynomial in z = y^2 (relative minimax, found by an
+// exchange iteration): off by 5.9e-7 of the value for |y| <= 1 with six terms,
+// by 7.2e-6 for |y| <= kTanhNear with four.  tanh's nearest pole is at z =
+// -(pi / 2)^2, so each term gains a factor of about 12 on [0, 1].
+#define PKVD_TANH_RATIO4 {0.999992801f, -0.332866126f, 0.128479621f, -0.0370293619f}
+constexpr float kTanhNear = 0.707f;
+
 __device__ __forceinline__ float tanh_ratio6(float z) {
   float r = fmaf(z, -0.00306706033f, 0.0167431151f);
   r = fmaf(z, r, -0.051605674f);
@@ -40,7 +43,6 @@ __device__ __forceinline__ float tanh_ratio6(float z) {
   r = fmaf(z, r, -0.333290424f);
   return fmaf(z, r, 0.999999414f);
 }
-#define PKVD_TANH_RATIO5 {0.999993089f, -0.332980653f, 0.130368113f, -0.0448175547f, 0.00903642429f}
 
 // tanh to 1e-6 of the value: a score's error stays relative to the score
 // whatever the cap.

@@ -58,22 +58,23 @@ def test_against_a_masked_softmax_of_torch(slopes):
 
 
 def test_polynomial_of_the_capped_scores():
-    """The two tanh(y) / y polynomials hold the errors that the kernels count on, over all of |y| <= 1."""
+    """The tanh(y) / y polynomials hold the errors that the kernels count on, over all of their ranges."""
     import os
     import re
     from conftest import ROOT
     text = open(os.path.join(ROOT, "paged_kv_decode_store_gb300", "csrc", "score_mod.cuh")).read()
-    five = [float(x) for x in re.findall(r"(-?[\d.]+(?:e-?\d+)?)f", text[text.index("PKVD_TANH_RATIO5 {"):].split("}")[0])]
+    four = [float(x) for x in re.findall(r"(-?[\d.]+(?:e-?\d+)?)f", text[text.index("PKVD_TANH_RATIO4 {"):].split("}")[0])]
     body = text[text.index("float tanh_ratio6"):].split("return")[0]
     lead, *rest = re.findall(r"fmaf\(z, (-?[\d.]+)f, (-?[\d.]+)f\)|r, (-?[\d.]+)f", body)
     six = [float(lead[0]), float(lead[1])] + [float(r[2]) for r in rest]
     six = six[::-1]
     six = [float(re.search(r"return fmaf\(z, r, ([\d.]+)f\);", text).group(1))] + six
-    y = np.linspace(1e-6, 1.0, 100001)
-    z = y * y
-    for coef, most in ((five, 6.95e-6), (six, 6.0e-7)):
+    near = float(re.search(r"kTanhNear = ([\d.]+)f", text).group(1))
+    for coef, n, end, most in ((four, 4, near, 7.25e-6), (six, 6, 1.0, 6.0e-7)):
+        y = np.linspace(1e-6, end, 100001)
+        z = y * y
         ratio = sum(c * z ** i for i, c in enumerate(coef))
-        assert len(coef) in (5, 6)
+        assert len(coef) == n
         assert np.abs(ratio * y / np.tanh(y) - 1).max() < most
 
 
