@@ -53,6 +53,13 @@ constexpr uint32_t kTmemCols = 512;
 // own 64 S columns; head_dim 64: they have [384 + 64 g, 448 + 64 g), so the
 // next S may be computed while they are in use.
 constexpr uint32_t kColO = 256, kColP64 = 384;
+// What a call modifies, known when compiled: the 64 keys of a thread fill its
+// registers, and every choice left to them costs instructions in each tile.
+enum : int {
+  kCap = 1,
+  kBias = 2,
+  kBounded = 4,        // every score is in [-cap, cap] and its exponential in range: no reference
+};
 constexpr float kRebase = 8.f;        // re-base the running maximum when it grows by > 2^8
 
 template <int D>
@@ -107,7 +114,6 @@ struct ModParams {
   // score of a raw product s as s * polynomial in s^2, for s^2 <= poly_range (-1: not used)
   float poly[4], poly_range;
   int wide_out;          // out is 32-byte aligned
-  int bounded;           // every score is in [-cap, cap] and its exponential in range: no reference
   int32_t* err;
 };
 
@@ -292,14 +298,15 @@ struct Visible {
 
 // s r(s^2) + add on two keys, r a polynomial of N coefficients; `most` keeps
 // the largest s^2.
-template <int N>
+template <int N, bool ADD>
 __device__ __forceinline__ void odd_poly2(float& v0, float& v1, const float* coef, float add0, float add1, float& most) {
   float z0, z1, r0 = coef[N - 1], r1 = coef[N - 1];
   mul2(z0, z1, v0, v1, v0, v1);
   most = tc_max3(most, z0, z1);
 #pragma unroll
   for (int k = N - 2; k >= 0; --k) horner2(r0, r1, z0, z1, coef[k]);
-  fma2(v0, v1, v0, v1, r0, r1, add0, add1);
+  if (ADD) fma2(v0, v1, v0, v1, r0, r1, add0, add1);
+  else mul2(v0, v1, v0, v1, r0, r1);
 }
 
 // A thread's 64 raw scores become scores in log2 units, -inf where the mask
@@ -310,21 +317,21 @@ __device__ __forceinline__ void odd_poly2(float& v0, float& v1, const float* coe
 // the reference that the exponent subtracts anyway.  `off`: the first column's
 // key minus the row's position; `again` reads the raw scores once more (a
 // warp with a score past the polynomial's range: it has computed in vain).
-template <typename Again>
+template <int MODE, typename Again>
 __device__ __forceinline__ void modify(float (&v)[kCols], const ModParams& p, const Visible& see, float nslope, int off,
                                        float& base, float& step, Again again) {
   const ScoreMod& m = p.mod;
-  const bool full = see.all();
-  const bool linear = m.slopes && __all_sync(FULL_MASK, off + kCols - 1 <= 0);
+  const bool linear = (MODE & kBias) && __all_sync(FULL_MASK, off + kCols - 1 <= 0);
   float k[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) k[i] = linear ? -nslope * (float)i : 0.f;
   base = linear ? nslope * (float)-off : 0.f;
   step = linear ? -nslope * 8.f : 0.f;
-  if (m.cap_in != 0.f) {
+  if (MODE & kCap) {
     float most = 0.f;                  // largest square: the polynomial's range
 #pragma unroll
-    for (int c = 0; c < kCols; c += 2) odd_poly2<4>(v[c], v[c + 1], p.poly, k[c & 7], k[(c & 7) + 1], most);
+    for (int c = 0; c < kCols; c += 2)
+      odd_poly2<4, (MODE & kBias) != 0>(v[c], v[c + 1], p.poly, k[c & 7], k[(c & 7) + 1], most);
     if (!__all_sync(FULL_MASK, most <= p.poly_range)) {
       again(v);
 #pragma unroll
@@ -332,18 +339,22 @@ __device__ __forceinline__ void modify(float (&v)[kCols], const ModParams& p, co
     }
   } else {
 #pragma unroll
-    for (int c = 0; c < kCols; c += 2)
-      fma2(v[c], v[c + 1], v[c], v[c + 1], p.scale_log2, p.scale_log2, k[c & 7], k[(c & 7) + 1]);
+    for (int c = 0; c < kCols; c += 2) {
+      if (MODE & kBias)
+        fma2(v[c], v[c + 1], v[c], v[c + 1], p.scale_log2, p.scale_log2, k[c & 7], k[(c & 7) + 1]);
+      else
+        mul2(v[c], v[c + 1], v[c], v[c + 1], p.scale_log2, p.scale_log2);
+    }
   }
-  if (m.slopes && !linear) {
+  if ((MODE & kBias) && !linear) {
     const float first = (float)off;
 #pragma unroll
     for (int c = 0; c < kCols; ++c) v[c] = fmaf(nslope, fabsf(first + (float)c), v[c]);
   }
-  if (!full) see.hide(v, -INFINITY);
+  if (!see.all()) see.hide(v, -INFINITY);
 }
 
-template <typename T, int D>
+template <typename T, int D, int MODE>
 __global__ void __launch_bounds__(kThreads, 1) prefill_mod_kernel(const __grid_constant__ ModParams p) {
   using L = Layout<D>;
   constexpr int H = L::kHalves, kKStages = L::kKStages, kVStages = L::kVStages;
@@ -697,7 +708,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_mod_kernel(const __grid_c
       const int pr = it.cached + tb + tt;        // padding rows mirror row 0
       const int wr = window_first(pr + 1, p.window);
       const float nslope = bias_slope(p.mod, it.hk * p.group + gi);
-      float m_ref = p.bounded ? 0.f : -INFINITY, l = 0.f;
+      float m_ref = (MODE & kBounded) ? 0.f : -INFINITY, l = 0.f;
       for (int j = 0; j < gn; ++j, ++n) {
         const int kbase = (kt_last - gf - j) * kTcKeys + half * kCols;
         const Visible see = {wr - kbase, pr + 1 - kbase, prefix - kbase};
@@ -712,25 +723,28 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_mod_kernel(const __grid_c
         };
         read(v);
         // head_dim 64: the next S may overwrite these columns once nobody reads them again
-        const bool capped = p.mod.cap_in != 0.f;
-        if (kSepP && !capped) {
+        if (kSepP && !(MODE & kCap)) {
           tc_fence_before();
           arrive(kSRead + g);
         }
         float bias, step;
-        modify(v, p, see, nslope, kbase - pr, bias, step, read);
-        if (kSepP && capped) {
+        modify<MODE>(v, p, see, nslope, kbase - pr, bias, step, read);
+        if (kSepP && (MODE & kCap)) {
           tc_fence_before();
           arrive(kSRead + g);
         }
         float alpha = 1.f;
         bool scale_o = false;
-        if (!p.bounded) {
+        if (!(MODE & kBounded)) {
           float top = -INFINITY;
 #pragma unroll
           for (int c = 0; c < kCols; c += 8)
-            top = fmaxf(top, fmaxf(tc_max3(tc_max3(v[c], v[c + 1], v[c + 2]), v[c + 3], v[c + 4]),
-                                   tc_max3(v[c + 5], v[c + 6], v[c + 7])) + (bias + step * (c / 8)));
+            if (MODE & kBias)
+              top = fmaxf(top, fmaxf(tc_max3(tc_max3(v[c], v[c + 1], v[c + 2]), v[c + 3], v[c + 4]),
+                                     tc_max3(v[c + 5], v[c + 6], v[c + 7])) + (bias + step * (c / 8)));
+            else
+              top = tc_max3(tc_max3(tc_max3(tc_max3(top, v[c], v[c + 1]), v[c + 2], v[c + 3]), v[c + 4], v[c + 5]),
+                            v[c + 6], v[c + 7]);
           // the two halves of a row agree on a reference: any common one does,
           // so 16 bits (rounded up) are enough
           __nv_bfloat16* x = reinterpret_cast<__nv_bfloat16*>(xch + (kSepP ? (n & 1) * 1024 : 0));
@@ -748,9 +762,11 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_mod_kernel(const __grid_c
         float s0 = 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f, shift0 = bias - mu, shift1 = shift0;
 #pragma unroll
         for (int c = 0; c < kCols; c += 4) {
-          if (c > 0 && c % 8 == 0) tc_add2(shift0, shift1, step, step);
-          tc_add2(v[c], v[c + 1], shift0, shift1);
-          tc_add2(v[c + 2], v[c + 3], shift0, shift1);
+          if ((MODE & kBias) && c > 0 && c % 8 == 0) tc_add2(shift0, shift1, step, step);
+          if (!(MODE & kBounded)) {
+            tc_add2(v[c], v[c + 1], shift0, shift1);
+            tc_add2(v[c + 2], v[c + 3], shift0, shift1);
+          }
           const float e0 = tc_ex2(v[c]), e1 = tc_ex2(v[c + 1]), e2 = tc_ex2(v[c + 2]), e3 = tc_ex2(v[c + 3]);
           tc_add2(s0, s1, e0, e1);
           tc_add2(s2, s3, e2, e3);
@@ -762,7 +778,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_mod_kernel(const __grid_c
           wait(kPVDone + g, (n - 1) & 1);
           tc_fence_after();
         }
-        if (__any_sync(FULL_MASK, scale_o)) {    // O too (head_dim 128: PV(n - 1) was done before S(n))
+        if (!(MODE & kBounded) && __any_sync(FULL_MASK, scale_o)) {    // O too (head_dim 128: PV(n - 1) was done before S(n))
 #pragma unroll 1
           for (int c4 = 0; c4 < D / 64; ++c4) {
             float o[32];
@@ -853,12 +869,25 @@ bool encode_q_map(CUtensorMap* map, const PrefillArgs& a, int group, int tile_to
          CUDA_SUCCESS;
 }
 
+template <typename T, int D, int MODE>
+cudaError_t launch_mode(const ModParams& prm, cudaStream_t stream) {
+  constexpr int smem = Layout<D>::kBytes;
+  cudaError_t e =
+      cudaFuncSetAttribute(prefill_mod_kernel<T, D, MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(prefill_mod_kernel<T, D, MODE>, dim3((unsigned)prm.items), dim3(kThreads), smem, stream, prm);
+}
+
 template <typename T, int D>
 cudaError_t launch_typed(const ModParams& prm, cudaStream_t stream) {
-  constexpr int smem = Layout<D>::kBytes;
-  cudaError_t e = cudaFuncSetAttribute(prefill_mod_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  if (e != cudaSuccess) return e;
-  return launch_pdl(prefill_mod_kernel<T, D>, dim3((unsigned)prm.items), dim3(kThreads), smem, stream, prm);
+  const bool cap = prm.mod.cap_in != 0.f, bias = prm.mod.slopes != nullptr;
+  if (cap && bias) return launch_mode<T, D, kCap | kBias>(prm, stream);
+  if (bias) return launch_mode<T, D, kBias>(prm, stream);
+  if (!cap) return launch_mode<T, D, 0>(prm, stream);
+  // bf16 weights of 2^64 times a sum of 2^23 keys and a value of 2^16 stay within fp32
+  if (std::is_same<T, __nv_bfloat16>::value && prm.mod.cap_out_log2 <= 64.f)
+    return launch_mode<T, D, std::is_same<T, __nv_bfloat16>::value ? kCap | kBounded : kCap>(prm, stream);
+  return launch_mode<T, D, kCap>(prm, stream);
 }
 
 }  // namespace
@@ -904,8 +933,6 @@ cudaError_t launch_prefill_mod(const PrefillArgs& a, cudaStream_t stream) {
   for (int k = 0; k < 4; ++k) prm.poly[k] = poly ? (float)(kRatio[k] * std::pow(in, 2 * k + 1) * a.mod.cap_out_log2) : 0.f;
   prm.poly_range = poly ? (float)(kTanhNear * kTanhNear / (size * size)) : -1.f;
   prm.wide_out = reinterpret_cast<uintptr_t>(a.out) % 32 == 0;
-  // 2^64 times a sum of 2^23 keys and a value of 2^16 stays within fp32
-  prm.bounded = c.dtype == PKVD_BF16 && a.mod.cap_in != 0.f && a.mod.cap_out_log2 <= 64.f && !a.mod.slopes;
   prm.err = a.err;
   if (c.dtype == PKVD_BF16)
     return c.head_dim == 64 ? launch_typed<__nv_bfloat16, 64>(prm, stream)
