@@ -80,12 +80,13 @@ struct Layout {
 };
 static_assert(Layout<128>::kBytes <= 232448, "227 KB of shared memory");
 
-// mbarriers; those of a Q tile take + g, an exchange's + 4 g + the warp's
-// quarter of the rows.
+// mbarriers; those of a Q tile take + g, S, P and PV + g + 2 half where a tile's
+// halves of keys go their own ways, an exchange's + 4 g + the warp's quarter of
+// the rows.
 enum : int {
-  kKFull = 0, kKEmpty = 4, kVFull = 8, kVReady = 12, kVEmpty = 16, kQFull = 20, kQEmpty = 22, kSFull = 24, kPFull = 26,
-  kPVDone = 28, kSRead = 30, kOFree = 32, kExch = 34, kItemFull = 42, kItemFree = 46, kClaim = 50, kDrain = 51,
-  kNumBars = 53
+  kKFull = 0, kKEmpty = 4, kVFull = 8, kVReady = 12, kVEmpty = 16, kQFull = 20, kQEmpty = 22, kSFull = 24, kPFull = 28,
+  kPVDone = 32, kSRead = 36, kOFree = 38, kExch = 40, kItemFull = 48, kItemFree = 52, kClaim = 56, kDrain = 57,
+  kNumBars = 59
 };
 constexpr uint32_t kTmemSlot = 8 * kNumBars;        // the TMEM base, then 16 bytes of a claim's answer
 constexpr uint32_t kAnswer = (kTmemSlot + 4 + 15) / 16 * 16;
@@ -239,10 +240,19 @@ __device__ __forceinline__ bool elect_one() {
 // mbar_wait_bounded that looks at the timer only once the wait is a long one:
 // a reading takes about a microsecond, which every wait would pay.
 __device__ __forceinline__ bool wait_bounded(uint64_t* bar, uint32_t parity) {
+  if (mbar_try_wait(bar, parity)) return true;
 #pragma unroll 1
   for (int i = 0; i < 64; ++i)
     if (mbar_try_wait(bar, parity)) return true;
   return mbar_wait_bounded(bar, parity);
+}
+
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
 }
 
 // Packed products: d = a * b, r = r * z + c.
@@ -284,15 +294,28 @@ __device__ __forceinline__ uint32_t span_bits(int a, int z) {
 // A thread's visible columns: [lo, end) of its 64, and those below `prefix`.
 struct Visible {
   int lo, end, prefix;
-  __device__ bool all() const { return (lo <= 0 && end >= kCols) || prefix >= kCols; }
+  template <int N>
+  __device__ bool none() const { return (end <= max(lo, 0) || lo >= N) && prefix <= 0; }
+  template <int N>
+  __device__ bool all() const { return (lo <= 0 && end >= N) || prefix >= N; }
   __device__ uint32_t bits(int word) const {
     return span_bits(lo - 32 * word, end - 32 * word) | span_bits(0, prefix - 32 * word);
   }
-  // Everything else becomes `x`, whatever it was (masked keys may hold anything).
-  __device__ void hide(float (&v)[kCols], float x) const {
-    const uint32_t m0 = bits(0), m1 = bits(1);
+  // Everything else becomes -inf, whatever it was (masked keys may hold
+  // anything).  Most groups of eight columns are visible to the whole warp,
+  // also in a tile that the mask cuts.
+  template <int N>
+  __device__ void hide(float (&v)[N]) const {
 #pragma unroll
-    for (int c = 0; c < kCols; ++c) v[c] = (((c < 32 ? m0 : m1) >> (c & 31)) & 1u) ? v[c] : x;
+    for (int w = 0; w < N / 32; ++w) {
+      const uint32_t m = bits(w), every = __reduce_and_sync(FULL_MASK, m);
+#pragma unroll
+      for (int c8 = 0; c8 < 32; c8 += 8) {
+        if (((every >> c8) & 0xffu) == 0xffu) continue;
+#pragma unroll
+        for (int c = c8; c < c8 + 8; ++c) v[32 * w + c] = ((m >> c) & 1u) ? v[32 * w + c] : -INFINITY;
+      }
+    }
   }
 };
 
@@ -317,29 +340,29 @@ __device__ __forceinline__ void odd_poly2(float& v0, float& v1, const float* coe
 // the reference that the exponent subtracts anyway.  `off`: the first column's
 // key minus the row's position; `again` reads the raw scores once more (a
 // warp with a score past the polynomial's range: it has computed in vain).
-template <int MODE, typename Again>
-__device__ __forceinline__ void modify(float (&v)[kCols], const ModParams& p, const Visible& see, float nslope, int off,
+template <int MODE, int N, typename Again>
+__device__ __forceinline__ void modify(float (&v)[N], const ModParams& p, const Visible& see, float nslope, int off,
                                        float& base, float& step, Again again) {
   const ScoreMod& m = p.mod;
-  const bool linear = (MODE & kBias) && __all_sync(FULL_MASK, off + kCols - 1 <= 0);
+  const bool linear = (MODE & kBias) && __all_sync(FULL_MASK, off + N - 1 <= 0);
   float k[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) k[i] = linear ? -nslope * (float)i : 0.f;
+  for (int i = 0; i < 8; ++i) k[i] = (linear ? -nslope : 0.f) * (float)i;
   base = linear ? nslope * (float)-off : 0.f;
   step = linear ? -nslope * 8.f : 0.f;
   if (MODE & kCap) {
     float most = 0.f;                  // largest square: the polynomial's range
 #pragma unroll
-    for (int c = 0; c < kCols; c += 2)
+    for (int c = 0; c < N; c += 2)
       odd_poly2<4, (MODE & kBias) != 0>(v[c], v[c + 1], p.poly, k[c & 7], k[(c & 7) + 1], most);
     if (!__all_sync(FULL_MASK, most <= p.poly_range)) {
       again(v);
 #pragma unroll
-      for (int c = 0; c < kCols; ++c) v[c] = fmaf(tanh_fast(v[c] * m.cap_in), m.cap_out_log2, k[c & 7]);
+      for (int c = 0; c < N; ++c) v[c] = fmaf(tanh_fast(v[c] * m.cap_in), m.cap_out_log2, k[c & 7]);
     }
   } else {
 #pragma unroll
-    for (int c = 0; c < kCols; c += 2) {
+    for (int c = 0; c < N; c += 2) {
       if (MODE & kBias)
         fma2(v[c], v[c + 1], v[c], v[c + 1], p.scale_log2, p.scale_log2, k[c & 7], k[(c & 7) + 1]);
       else
@@ -349,9 +372,9 @@ __device__ __forceinline__ void modify(float (&v)[kCols], const ModParams& p, co
   if ((MODE & kBias) && !linear) {
     const float first = (float)off;
 #pragma unroll
-    for (int c = 0; c < kCols; ++c) v[c] = fmaf(nslope, fabsf(first + (float)c), v[c]);
+    for (int c = 0; c < N; ++c) v[c] = fmaf(nslope, fabsf(first + (float)c), v[c]);
   }
-  if (!see.all()) see.hide(v, -INFINITY);
+  if (!__all_sync(FULL_MASK, see.all<N>())) see.hide(v);
 }
 
 template <typename T, int D, int MODE>
@@ -359,6 +382,10 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_mod_kernel(const __grid_c
   using L = Layout<D>;
   constexpr int H = L::kHalves, kKStages = L::kKStages, kVStages = L::kVStages;
   constexpr bool kSepP = D == 64;
+  // head_dim 128 without a reference: nothing ties the two halves of a tile's
+  // keys together, so each has its own S, P and PV and the products of one run
+  // beside the softmax of the other.
+  constexpr bool kSplit = D == 128 && (MODE & kBounded);
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;          // whole swizzle atoms
@@ -369,7 +396,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_mod_kernel(const __grid_c
   if (threadIdx.x == 0) {
     for (int i = 0; i < kNumBars; ++i) {
       int arrivals = 1;
-      if ((i >= kPFull && i < kPVDone) || (i >= kSRead && i < kExch)) arrivals = kTileWarps;
+      if (i >= kPFull && i < kPVDone) arrivals = kSplit ? kTileWarps / 2 : kTileWarps;
+      if (i >= kSRead && i < kExch) arrivals = kTileWarps;
       if (i >= kExch && i < kItemFull) arrivals = 2;
       if ((i >= kKEmpty && i < kVFull) || (i >= kVEmpty && i < kQFull)) arrivals = 2;      // both Q tiles
       if (i >= kItemFree && i < kClaim) arrivals = kItemUsers;
@@ -391,6 +419,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_mod_kernel(const __grid_c
   pdl_trigger();
   Item* ring_items = reinterpret_cast<Item*>(gbase + L::kItems);
 
+  // registers: 512 x 104 + 128 x 56 = 60416 of the 61440 that 640 threads start with
+  if (warp >= kKvWarp) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
   if (warp == kKvWarp) {
     // ------------------------------------------------------- K and V producer
     // Lane s copies segment s of a tile (lane 0 waits for a free stage first);
@@ -577,10 +607,11 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_mod_kernel(const __grid_c
       const bool leader = elect_one();
       const int g = warp == kMmaWarp ? 0 : 1;
       constexpr uint32_t fmt = std::is_same<T, __nv_bfloat16>::value ? 1u : 0u;
-      constexpr uint32_t id_s = tc_idesc(fmt, kTcKeys, 0), id_pv = tc_idesc(fmt, D, 1), hi = desc_hi(1024);
+      constexpr uint32_t id_s = tc_idesc(fmt, kSplit ? kCols : kTcKeys, 0), id_pv = tc_idesc(fmt, D, 1), hi = desc_hi(1024);
       const uint32_t qd = desc_lo(base + L::kQ + g * H * kHalf, 16);
       const uint32_t s_cols = tmem + g * kTcKeys, o_cols = tmem + kColO + g * D;
       const uint32_t p_cols = kSepP ? tmem + kColP64 + g * 64 : s_cols;
+      constexpr int kParts = kSplit ? 2 : 1;
       bool ok = true;
       auto wait = [&](int bar, uint32_t parity) {
         if (ok) ok = __all_sync(FULL_MASK, wait_bounded(&bars[bar], parity));
@@ -603,55 +634,66 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_mod_kernel(const __grid_c
           }
         };
         skip(at, gn > 0 ? first : at + all);
-        auto issue_s = [&](int j) {                 // the n-th of the tile is the item's j-th
+        auto issue_s = [&](int j, int h) {          // the n-th of the tile is the item's j-th; half h or all (0) of its keys
           const int t = first + j, stg = t % kKStages;
           wait(kKFull + stg, (t / kKStages) & 1);
           if (!ok) return;
           tc_fence_after();
-          const uint32_t kd = desc_lo(base + L::kK + stg * H * kHalf, 16);
+          const uint32_t kd = desc_lo(base + L::kK + stg * H * kHalf, 16) + h * (kCols * 128 >> 4), d = s_cols + h * kCols;
           if (leader) {
 #pragma unroll
             for (int k = 0; k < D / 16; ++k) {
               const uint32_t off = ((k >> 2) * kHalf + (k & 3) * 32) >> 4;
-              if (k == 0) mma_ss<false>(s_cols, qd, kd, hi, id_s);
-              else mma_ss<true>(s_cols, qd + off, kd + off, hi, id_s);
+              if (k == 0) mma_ss<false>(d, qd, kd, hi, id_s);
+              else mma_ss<true>(d, qd + off, kd + off, hi, id_s);
             }
-            tc_commit(&bars[kSFull + g]);
-            tc_commit(&bars[kKEmpty + stg]);
-            if (j == gn - 1) tc_commit(&bars[kQEmpty + g]);
+            tc_commit(&bars[kSFull + g + 2 * h]);
+            if (!kSplit || h == 1) {
+              tc_commit(&bars[kKEmpty + stg]);
+              if (j == gn - 1) tc_commit(&bars[kQEmpty + g]);
+            }
           }
           __syncwarp();
         };
         if (gn > 0) {
           wait(kQFull + g, used & 1);
-          if (n > 0) wait((kSepP ? kSRead : kPVDone) + g, (n - 1) & 1);
-          if (ok) issue_s(0);
+#pragma unroll
+          for (int h = 0; h < kParts; ++h) {
+            if (n > 0) wait((kSepP ? kSRead : kPVDone) + g + 2 * h, (n - 1) & 1);
+            if (ok) issue_s(0, h);
+          }
           for (int j = 0; ok && j < gn; ++j, ++n) {
             if (kSepP && j + 1 < gn) {
               wait(kSRead + g, n & 1);
-              if (ok) issue_s(j + 1);
+              if (ok) issue_s(j + 1, 0);
             }
             const int t = first + j, stg = t % kVStages;
-            wait(kPFull + g, n & 1);
-            wait(kVFull + stg, (t / kVStages) & 1);
-            wait(kVReady + stg, (t / kVStages) & 1);
-            if (j == 0 && used > 0) wait(kOFree + g, (used - 1) & 1);
-            if (!ok) break;
-            tc_fence_after();
-            const uint32_t vd = desc_lo(base + L::kV + stg * H * kHalf, kHalf);
-            if (leader) {
 #pragma unroll
-              for (int k = 0; k < kTcKeys / 16; ++k) {      // 16 keys = 8 packed columns of weights
-                const uint32_t col = kSepP ? k * 8 : (k >> 2) * kCols + (k & 3) * 8;
-                mma_ts(o_cols, p_cols + col, vd + k * 128, hi, id_pv, k > 0 ? 1u : (uint32_t)j);
+            for (int h = 0; h < kParts; ++h) {
+              wait(kPFull + g + 2 * h, n & 1);
+              if (h == 0) {
+                wait(kVFull + stg, (t / kVStages) & 1);
+                wait(kVReady + stg, (t / kVStages) & 1);
+                if (j == 0 && used > 0) wait(kOFree + g, (used - 1) & 1);
               }
-              tc_commit(&bars[kPVDone + g]);
-              tc_commit(&bars[kVEmpty + stg]);
-            }
-            __syncwarp();
-            if (!kSepP && j + 1 < gn) {
-              wait(kPVDone + g, n & 1);
-              if (ok) issue_s(j + 1);
+              if (!ok) break;
+              tc_fence_after();
+              const uint32_t vd = desc_lo(base + L::kV + stg * H * kHalf, kHalf);
+              if (leader) {
+#pragma unroll
+                for (int i = 0; i < kTcKeys / 16 / kParts; ++i) {      // 16 keys = 8 packed columns of weights
+                  const int k = h * (kTcKeys / 32) + i;
+                  const uint32_t col = kSepP ? k * 8 : (k >> 2) * kCols + (k & 3) * 8;
+                  mma_ts(o_cols, p_cols + col, vd + k * 128, hi, id_pv, k > 0 ? 1u : (uint32_t)j);
+                }
+                tc_commit(&bars[kPVDone + g + 2 * h]);
+                if (h == kParts - 1) tc_commit(&bars[kVEmpty + stg]);
+              }
+              __syncwarp();
+              if (!kSepP && j + 1 < gn) {
+                wait(kPVDone + g + 2 * h, n & 1);
+                if (ok) issue_s(j + 1, h);
+              }
             }
           }
           ++used;
@@ -666,11 +708,13 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_mod_kernel(const __grid_c
       wait_bounded(&bars[kDrain + g], 0);
     }
   } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
     // ------------------------------------------------------------ softmax
     // Every wait is bounded; a warp whose wait gives up leaves (the others'
     // then give up in turn).
     const int g = warp >> 3, half = (warp >> 2) & 1, quarter = warp & 3, row = quarter * 32 + lane;
     const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
+    const int sub = g + (kSplit ? 2 * half : 0);   // which S, P and PV
     const uint32_t s_addr = tmem + lane_base + g * kTcKeys + half * kCols;
     const uint32_t p_addr = kSepP ? tmem + lane_base + kColP64 + g * 64 + half * 32 : s_addr;
     const uint32_t o_addr = tmem + lane_base + kColO + g * D + half * (D / 2);
@@ -712,39 +756,74 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_mod_kernel(const __grid_c
       for (int j = 0; j < gn; ++j, ++n) {
         const int kbase = (kt_last - gf - j) * kTcKeys + half * kCols;
         const Visible see = {wr - kbase, pr + 1 - kbase, prefix - kbase};
-        wait(kSFull + g, n & 1);
+        wait(kSFull + sub, n & 1);
         if (!ok) break;
         tc_fence_after();
-        float v[kCols];
-        auto read = [&](float (&x)[kCols]) {
-          tmem_ld32(s_addr, x);
-          tmem_ld32(s_addr + 32, x + 32);
-          tmem_ld_wait();
-        };
-        read(v);
-        // head_dim 64: the next S may overwrite these columns once nobody reads them again
-        if (kSepP && !(MODE & kCap)) {
-          tc_fence_before();
-          arrive(kSRead + g);
-        }
-        float bias, step;
-        modify<MODE>(v, p, see, nslope, kbase - pr, bias, step, read);
-        if (kSepP && (MODE & kCap)) {
-          tc_fence_before();
-          arrive(kSRead + g);
-        }
-        float alpha = 1.f;
-        bool scale_o = false;
-        if (!(MODE & kBounded)) {
+        if constexpr ((MODE & kBounded) != 0) {
+          // nothing is needed of the whole row before its weights: 32 keys at a
+          // time, in a loop of half the code
+#pragma unroll 1
+          for (int c0 = 0; c0 < kCols; c0 += 32) {
+            uint32_t pk[16];
+            const Visible part = {see.lo - c0, see.end - c0, see.prefix - c0};
+            if (__all_sync(FULL_MASK, part.none<32>())) {
+#pragma unroll
+              for (int c = 0; c < 16; ++c) pk[c] = 0u;
+            } else {
+              float v[32], bias, step, s0 = 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f;
+              auto read = [&](float (&x)[32]) {
+                tmem_ld32(s_addr + c0, x);
+                tmem_ld_wait();
+              };
+              read(v);
+              modify<MODE>(v, p, part, 0.f, 0, bias, step, read);
+#pragma unroll
+              for (int c = 0; c < 32; c += 4) {
+                const float e0 = tc_ex2(v[c]), e1 = tc_ex2(v[c + 1]), e2 = tc_ex2(v[c + 2]), e3 = tc_ex2(v[c + 3]);
+                tc_add2(s0, s1, e0, e1);
+                tc_add2(s2, s3, e2, e3);
+                pk[c / 2] = Mma<T>::pack(e0, e1);
+                pk[c / 2 + 1] = Mma<T>::pack(e2, e3);
+              }
+              l += (s0 + s1) + (s2 + s3);
+            }
+            if (kSepP && c0 == 0 && j > 0) {
+              wait(kPVDone + g, (n - 1) & 1);
+              tc_fence_after();
+            }
+            tmem_st16(p_addr + c0 / 2, pk);
+          }
+          if (kSepP) {
+            tc_fence_before();
+            arrive(kSRead + g);
+          }
+        } else {
+          float v[kCols];
+          auto read = [&](float (&x)[kCols]) {
+            tmem_ld32(s_addr, x);
+            tmem_ld32(s_addr + 32, x + 32);
+            tmem_ld_wait();
+          };
+          read(v);
+          // head_dim 64: the next S may overwrite these columns once nobody reads them again
+          if (kSepP && !(MODE & kCap)) {
+            tc_fence_before();
+            arrive(kSRead + g);
+          }
+          float bias, step;
+          modify<MODE>(v, p, see, nslope, kbase - pr, bias, step, read);
+          if (kSepP && (MODE & kCap)) {
+            tc_fence_before();
+            arrive(kSRead + g);
+          }
           float top = -INFINITY;
 #pragma unroll
-          for (int c = 0; c < kCols; c += 8)
-            if (MODE & kBias)
-              top = fmaxf(top, fmaxf(tc_max3(tc_max3(v[c], v[c + 1], v[c + 2]), v[c + 3], v[c + 4]),
-                                     tc_max3(v[c + 5], v[c + 6], v[c + 7])) + (bias + step * (c / 8)));
-            else
-              top = tc_max3(tc_max3(tc_max3(tc_max3(top, v[c], v[c + 1]), v[c + 2], v[c + 3]), v[c + 4], v[c + 5]),
-                            v[c + 6], v[c + 7]);
+          for (int c = 0; c < kCols; c += 8) {
+            if ((MODE & kBias) && c > 0) top -= step;          // relative to the bias of these eight columns
+            top = tc_max3(tc_max3(top, v[c], v[c + 1]), tc_max3(v[c + 2], v[c + 3], v[c + 4]),
+                          tc_max3(v[c + 5], v[c + 6], v[c + 7]));
+          }
+          if (MODE & kBias) top += bias + (kCols / 8 - 1) * step;
           // the two halves of a row agree on a reference: any common one does,
           // so 16 bits (rounded up) are enough
           __nv_bfloat16* x = reinterpret_cast<__nv_bfloat16*>(xch + (kSepP ? (n & 1) * 1024 : 0));
@@ -753,49 +832,47 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_mod_kernel(const __grid_c
           exchange();
           const float mt = fmaxf(__bfloat162float(mine), __bfloat162float(x[(half ^ 1) * 32 + lane]));
           const bool rebase = mt > m_ref + kRebase;
-          scale_o = rebase && m_ref != -INFINITY;
-          alpha = scale_o ? tc_ex2(m_ref - mt) : 1.f;
+          const bool scale_o = rebase && m_ref != -INFINITY;
+          const float alpha = scale_o ? tc_ex2(m_ref - mt) : 1.f;
           if (rebase) m_ref = mt;
-        }
-        const float mu = m_ref == -INFINITY ? 0.f : m_ref;
-        uint32_t pk[kCols / 2];
-        float s0 = 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f, shift0 = bias - mu, shift1 = shift0;
+          const float mu = m_ref == -INFINITY ? 0.f : m_ref;
+          uint32_t pk[kCols / 2];
+          float s0 = 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f, shift0 = bias - mu, shift1 = shift0;
 #pragma unroll
-        for (int c = 0; c < kCols; c += 4) {
-          if ((MODE & kBias) && c > 0 && c % 8 == 0) tc_add2(shift0, shift1, step, step);
-          if (!(MODE & kBounded)) {
+          for (int c = 0; c < kCols; c += 4) {
+            if ((MODE & kBias) && c > 0 && c % 8 == 0) tc_add2(shift0, shift1, step, step);
             tc_add2(v[c], v[c + 1], shift0, shift1);
             tc_add2(v[c + 2], v[c + 3], shift0, shift1);
+            const float e0 = tc_ex2(v[c]), e1 = tc_ex2(v[c + 1]), e2 = tc_ex2(v[c + 2]), e3 = tc_ex2(v[c + 3]);
+            tc_add2(s0, s1, e0, e1);
+            tc_add2(s2, s3, e2, e3);
+            pk[c / 2] = Mma<T>::pack(e0, e1);
+            pk[c / 2 + 1] = Mma<T>::pack(e2, e3);
           }
-          const float e0 = tc_ex2(v[c]), e1 = tc_ex2(v[c + 1]), e2 = tc_ex2(v[c + 2]), e3 = tc_ex2(v[c + 3]);
-          tc_add2(s0, s1, e0, e1);
-          tc_add2(s2, s3, e2, e3);
-          pk[c / 2] = Mma<T>::pack(e0, e1);
-          pk[c / 2 + 1] = Mma<T>::pack(e2, e3);
-        }
-        l = l * alpha + ((s0 + s1) + (s2 + s3));
-        if (kSepP && j > 0) {                    // the weights' columns are free once PV(n - 1) is done
-          wait(kPVDone + g, (n - 1) & 1);
-          tc_fence_after();
-        }
-        if (!(MODE & kBounded) && __any_sync(FULL_MASK, scale_o)) {    // O too (head_dim 128: PV(n - 1) was done before S(n))
+          l = l * alpha + ((s0 + s1) + (s2 + s3));
+          if (kSepP && j > 0) {                    // the weights' columns are free once PV(n - 1) is done
+            wait(kPVDone + g, (n - 1) & 1);
+            tc_fence_after();
+          }
+          if (__any_sync(FULL_MASK, scale_o)) {    // O too (head_dim 128: PV(n - 1) was done before S(n))
 #pragma unroll 1
-          for (int c4 = 0; c4 < D / 64; ++c4) {
-            float o[32];
-            tmem_ld32(o_addr + c4 * 32, o);
-            tmem_ld_wait();
+            for (int c4 = 0; c4 < D / 64; ++c4) {
+              float o[32];
+              tmem_ld32(o_addr + c4 * 32, o);
+              tmem_ld_wait();
 #pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] *= alpha;
-            tmem_st32(o_addr + c4 * 32, o);
+              for (int e = 0; e < 32; ++e) o[e] *= alpha;
+              tmem_st32(o_addr + c4 * 32, o);
+            }
           }
+          tmem_st32(p_addr, reinterpret_cast<const float*>(pk));
         }
-        tmem_st32(p_addr, reinterpret_cast<const float*>(pk));
         tmem_st_wait();
         tc_fence_before();
-        arrive(kPFull + g);
+        arrive(kPFull + sub);
       }
       if (!ok) break;
-      wait(kPVDone + g, (n - 1) & 1);            // and so every warp of the tile is past its last exchange
+      wait(kPVDone + g + (kSplit ? 2 : 0), (n - 1) & 1);   // the last; and so every warp of the tile is past its last exchange
       if (!ok) break;
       tc_fence_after();
       // the row's sum: half 1's part to half 0, the whole back
@@ -822,7 +899,10 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_mod_kernel(const __grid_c
         if (live) {
           uint32_t w[16];
 #pragma unroll
-          for (int e = 0; e < 16; ++e) w[e] = Mma<T>::pack(o[2 * e] * inv, o[2 * e + 1] * inv);
+          for (int e = 0; e < 16; ++e) {
+            mul2(o[2 * e], o[2 * e + 1], o[2 * e], o[2 * e + 1], inv, inv);
+            w[e] = Mma<T>::pack(o[2 * e], o[2 * e + 1]);
+          }
           T* d = dst + c4 * 32;
           if (p.wide_out) {                      // whole 32-byte sectors a store
 #pragma unroll
