@@ -13,12 +13,13 @@ import numpy as np
 
 
 def log_softmax(x: np.ndarray):
-    """x - log sum exp x, or None if the normaliser is not finite."""
+    """x - log sum exp x (from the largest x: rows of huge numbers keep their
+    sum), or None if the normaliser is not finite."""
     x = np.asarray(x, dtype=np.float64)
     if np.isnan(x).any() or np.isposinf(x).any() or np.isneginf(x).all():
         return None
     m = x.max()
-    return x - (m + np.log(np.exp(x - m).sum()))
+    return (x - m) - np.log(np.exp(x - m).sum())
 
 
 def step(logits: np.ndarray, scores: np.ndarray, keep: int, finished=None, eos_id: int = -1):

@@ -15,7 +15,8 @@
 // chunks tightens the bound; what is left (some more than `keep` elements) is
 // listed and ranked against one another.  Selecting in every 32 KB slice
 // instead, as a first version did, cost 148 us for 64 x 8 rows of 151,936 f16
-// ids, most of it in barriers; this one takes 53 us (floor 23 us).
+// ids, most of it in barriers; this one takes 40 us (floor 23 us), 31 of them
+// in the scan.
 //
 // Rounding: the order within a beam is that of the logits; values of listed
 // continuations are pairs of fp32 (about 2^-48 relative), the bounds fp32 with
@@ -171,20 +172,24 @@ struct RowView {
   }
 };
 
-// Two fp32 lanes in one instruction.
-__device__ __forceinline__ void add2(float& a0, float& a1, float b0, float b1) {
-  unsigned long long a, b;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(a) : "f"(a0), "f"(a1));
-  asm("mov.b64 %0, {%1, %2};" : "=l"(b) : "f"(b0), "f"(b1));
-  asm("add.rn.f32x2 %0, %0, %1;" : "+l"(a) : "l"(b));
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(a0), "=f"(a1) : "l"(a));
+// Two fp32 lanes in one register pair.
+__device__ __forceinline__ uint64_t pair2(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
 }
-__device__ __forceinline__ void mul2(float& a0, float& a1, float b) {
-  unsigned long long a, bb;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(a) : "f"(a0), "f"(a1));
-  asm("mov.b64 %0, {%1, %1};" : "=l"(bb) : "f"(b));
-  asm("mul.rn.f32x2 %0, %0, %1;" : "+l"(a) : "l"(bb));
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(a0), "=f"(a1) : "l"(a));
+__device__ __forceinline__ void unpair2(uint64_t x, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(x));
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
 }
 
 template <typename T>
@@ -201,18 +206,29 @@ __global__ void __launch_bounds__(kScanThreads, kScanCtas) beam_scan_kernel(cons
   const RowView<T> view(p, row);
   const int c0 = span * p.span_chunks, c1 = min(c0 + p.span_chunks, p.chunks);
   if (c0 >= c1) return;
+  const int vocab = p.vocab;
   const uint4 low = make_uint4(Word<T>::kLow, Word<T>::kLow, Word<T>::kLow, Word<T>::kLow);
-  // a lane's four vectors of the pair of chunks c, c + 1
+  // a lane's four vectors of the pair of chunks c, c + 1; chunks [in0, in1) lie
+  // inside the row with the aligned vectors around them
+  const int in0 = view.lead ? 1 : 0, in1 = min(c1, (view.lead ? max(vocab - N, 0) : vocab) / (kChunkVecs * N));
+  const uint4* aligned = reinterpret_cast<const uint4*>(view.x) + lane;
   auto fetch = [&](int c, uint4* raw) {
-    if (c + 2 <= c1 && view.inside(c * kChunkVecs * N) && view.inside((c + 2) * kChunkVecs * N - N)) {
+    if (c >= in0 && c + 2 <= in1) {
+      if (view.lead == 0) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) raw[i] = view.load_inside((c * kChunkVecs + i * 32 + lane) * N);
+        for (int i = 0; i < 4; ++i) raw[i] = __ldg(aligned + c * kChunkVecs + i * 32);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) raw[i] = view.load_inside((c * kChunkVecs + i * 32 + lane) * N);
+      }
     } else {                                            // the row's edges and the span's last chunk
 #pragma unroll
       for (int i = 0; i < 4; ++i)
         raw[i] = c + (i >> 1) < c1 ? view.load((c * kChunkVecs + i * 32 + lane) * N) : low;
     }
   };
+  constexpr float kLog2e = 1.4426950408889634f;
+  const uint64_t scale2 = pair2(kLog2e, kLog2e);
   uint4 raw[4], next[4];
   fetch(c0, raw);
   float m = -INFINITY;
@@ -224,27 +240,30 @@ __global__ void __launch_bounds__(kScanThreads, kScanCtas) beam_scan_kernel(cons
     if (lane < 2 && c + lane < c1) p.maxima[(int64_t)row * p.chunks + c + lane] = lane ? most1 : most0;
     const float up = fmaxf(most0, most1);
     if (up > m) {                                       // the same in every lane
-      const float down = ex2f((m - up) * 1.4426950408889634f);   // 0 the first time
+      const float down = ex2f((m - up) * kLog2e);   // 0 the first time
       sum.x *= down;
       sum.y *= down;
       m = up;
     }
-    // a NaN or +inf logit makes the sum NaN: the merge then drops the beam
+    // x - max first, which is exact for 16-bit logits and zero for the largest:
+    // a rounding of max * log2(e) would shift every term of the span alike.  A
+    // NaN or +inf logit makes the sum NaN: the merge then drops the beam.
     const float ref = m == -INFINITY ? 0.f : m;
-    float p0 = 0.f, p1 = 0.f;
+    const uint64_t minus_ref = pair2(-ref, -ref);
+    uint64_t part = pair2(0.f, 0.f);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       float v[N];
       Vec16<T>::unpack(raw[i], v);
 #pragma unroll
       for (int j = 0; j < N; j += 2) {
-        // x - max first, which is exact for 16-bit logits: a rounding of max
-        // * log2(e) would shift every term of the span alike
-        add2(v[j], v[j + 1], -ref, -ref);
-        mul2(v[j], v[j + 1], 1.4426950408889634f);
-        add2(p0, p1, ex2f(v[j]), ex2f(v[j + 1]));
+        float a, b;
+        unpair2(mul2(add2(pair2(v[j], v[j + 1]), minus_ref), scale2), a, b);
+        part = add2(part, pair2(ex2f(a), ex2f(b)));
       }
     }
+    float p0, p1;
+    unpair2(part, p0, p1);
     const float2 t = two_sum(sum.x, p0 + p1);
     sum = make_float2(t.x, sum.y + t.y);
 #pragma unroll
@@ -284,9 +303,8 @@ __device__ __forceinline__ float2 log_pair(float2 t) {
 }
 
 struct MergeSmem {
-  float2 base[kBeamMaxBeams];            // score minus normaliser
-  float basef[kBeamMaxBeams];            // the same in fp32, -inf: no logits to look at
-  float top[kBeamMaxBeams];              // largest logit; -inf: none, or one that is not finite
+  float2 base[kBeamMaxBeams];            // score minus the log of the sum: a logit counts from its row's largest
+  float2 basef[kBeamMaxBeams];           // the same in fp32 (-inf: no logits to look at) and the row's largest logit
   float2 total[kBeamMaxBeams];           // sum of exponentials
   float group[kGroups];
   float bound;
@@ -301,9 +319,10 @@ struct MergeSmem {
 
 // The keep-th largest of the kGroups group maxima (a lower bound of the
 // keep-th largest value, -inf if fewer groups have one), less a margin for
-// the fp32 values' rounding: a beam's base and its sum with a logit are each
-// off by 2^-24 relative, for the element that bounds and the one it is held
-// against.
+// the fp32 values' rounding: a beam's base, a logit's distance from its row's
+// largest and their sum are each off by 2^-24 relative (the distance is at most
+// value and base together), for the element that bounds and the one it is held
+// against: 2^-22 of value and base, twice that to be sure.
 __device__ __forceinline__ void set_bound(MergeSmem& s, float most, int keep, float base_size) {
   const int tid = threadIdx.x;
 #pragma unroll
@@ -321,7 +340,7 @@ __device__ __forceinline__ void set_bound(MergeSmem& s, float most, int keep, fl
   }
 #pragma unroll
   for (int o = 1; o < 8; o <<= 1) before += __shfl_xor_sync(FULL_MASK, before, o);
-  if (before == keep - 1) s.bound = most - (fabsf(most) + base_size) * 0x1p-22f;
+  if (before == keep - 1) s.bound = most - (fabsf(most) + base_size) * 0x1p-21f;
   __syncthreads();
 }
 
@@ -371,22 +390,22 @@ __global__ void __launch_bounds__(kMergeThreads) beam_merge_kernel(const BeamArg
                                            __shfl_xor_sync(FULL_MASK, total.y, o)));
     if (__any_sync(FULL_MASK, bad)) m = -INFINITY;
     if (lane == 0) {
-      s.top[b] = m;
+      s.basef[b].y = m;                  // -inf: none, or one that is not finite
       s.total[b] = total;
     }
   }
   __syncthreads();
   if (tid < B) {
-    const float top = s.top[tid];
+    const float top = s.basef[tid].y;
     const bool usable = !done && top > -INFINITY && top < INFINITY;
     float2 base = make_float2(score, 0.f);
     if (usable) {
-      const float2 norm = add_parts(log_pair(s.total[tid]), make_float2(top, 0.f));
+      const float2 norm = log_pair(s.total[tid]);
       base = add_parts(base, make_float2(-norm.x, -norm.y));
     }
     const bool finite = fabsf(score) < INFINITY && (done || usable);
     s.base[tid] = base;
-    s.basef[tid] = finite && !done ? base.x : -INFINITY;
+    s.basef[tid].x = finite && !done ? base.x : -INFINITY;
     if (finite && done) {                                                // its one continuation
       const int i = atomicAdd(&s.count, 1);
       s.value[i] = pair_key(base);
@@ -396,15 +415,16 @@ __global__ void __launch_bounds__(kMergeThreads) beam_merge_kernel(const BeamArg
   __syncthreads();
   const int ended = s.count;
   float base_size = 0.f;
-  for (int b = lane; b < B; b += 32) base_size = fmaxf(base_size, s.basef[b] > -INFINITY ? fabsf(s.basef[b]) : 0.f);
+  for (int b = lane; b < B; b += 32) base_size = fmaxf(base_size, s.basef[b].x > -INFINITY ? fabsf(s.basef[b].x) : 0.f);
   base_size = warp_max(base_size);
   // ---- the chunks that may hold a winner
   // c / chunks by a product (Granlund and Montgomery, 1994); c < 2^31
   auto beam_of = [&](int c) { return (int)((__umulhi((uint32_t)c, p.chunk_mul) + (uint32_t)c) >> p.chunk_shift); };
-  auto chunk_value = [&](int c, float top) {
-    const float base = s.basef[beam_of(c)];
-    return base > -INFINITY ? base + top : -INFINITY;
+  auto value_f = [&](int b, float logit) {
+    const float2 base = s.basef[b];
+    return base.x > -INFINITY ? base.x + (logit - base.y) : -INFINITY;
   };
+  auto chunk_value = [&](int c, float top) { return value_f(beam_of(c), top); };
   float most = -INFINITY;
 #pragma unroll
   for (int i = 0; i < kHeld; ++i) {
@@ -438,7 +458,7 @@ __global__ void __launch_bounds__(kMergeThreads) beam_merge_kernel(const BeamArg
       } else {
         c.x = beam_of(ci);
         c.y = ci - c.x * p.chunks;
-        if (s.basef[c.x] == -INFINITY) continue;
+        if (s.basef[c.x].x == -INFINITY) continue;
       }
       const RowView<T> view(p, r * B + c.x);
       const int e0 = (c.y * kChunkVecs + (int)(i % kChunkVecs)) * N;
@@ -465,19 +485,18 @@ __global__ void __launch_bounds__(kMergeThreads) beam_merge_kernel(const BeamArg
   }
 #pragma unroll
   for (int k = 0; k < kKept; ++k)
-    if (kept_beam[k] >= 0) most = fmaxf(most, s.basef[kept_beam[k]] + Word<T>::most(vec_max<T>(kept[k])));
+    if (kept_beam[k] >= 0) most = fmaxf(most, value_f(kept_beam[k], Word<T>::most(vec_max<T>(kept[k]))));
   const int64_t rest = tid + (listed ? (int64_t)kKept * kMergeThreads : 0);
-  each(rest, [&](int b, int, const uint4& v) { most = fmaxf(most, s.basef[b] + Word<T>::most(vec_max<T>(v))); });
+  each(rest, [&](int b, int, const uint4& v) { most = fmaxf(most, value_f(b, Word<T>::most(vec_max<T>(v)))); });
   set_bound(s, most, K, base_size);
   bound = fmaxf(bound, s.bound);
   auto list_vec = [&](int b, int id0, const uint4& raw) {
-    const float base = s.basef[b];
-    if (!(base + Word<T>::most(vec_max<T>(raw)) >= bound)) return;
+    if (!(value_f(b, Word<T>::most(vec_max<T>(raw))) >= bound)) return;
     float v[N];
     Vec16<T>::unpack(raw, v);
 #pragma unroll
     for (int j = 0; j < N; ++j) {
-      const float x = base + v[j];
+      const float x = value_f(b, v[j]);
       if (x > -INFINITY && x >= bound) {
         const int i = atomicAdd(&s.count, 1);
         if (i < kBeamList) {
@@ -493,8 +512,7 @@ __global__ void __launch_bounds__(kMergeThreads) beam_merge_kernel(const BeamArg
   each(rest, list_vec);
   __syncthreads();
   auto value_of = [&](int b, float logit) {
-    const float2 base = s.base[b], v = two_sum(base.x, logit);
-    return pair_key(two_sum(v.x, v.y + base.y));
+    return pair_key(add_parts(s.base[b], two_sum(logit, -s.basef[b].y)));     // the difference is exact
   };
   auto emit = [&](int k, uint64_t value, uint32_t at) {
     const int64_t o = (int64_t)r * K + k;
@@ -545,7 +563,7 @@ __global__ void __launch_bounds__(kMergeThreads) beam_merge_kernel(const BeamArg
       Vec16<T>::unpack(raw, v);
 #pragma unroll
       for (int j = 0; j < N; ++j) {
-        const float x = s.basef[b] + v[j];
+        const float x = value_f(b, v[j]);
         if (x > -INFINITY && x >= bound)
           offer(value_of(b, v[j]), (uint32_t)b * p.vocab + (id0 + j));
       }

@@ -130,6 +130,28 @@ def test_ended_dead_masked_and_broken_beams():
     assert pk.beam_search_step(logits, scores, 8)[1][2].tolist() == [-1] * 8
 
 
+@pytest.mark.parametrize("dt", list(DT))
+def test_rows_of_large_numbers_and_masks_of_the_lowest_value(dt):
+    """Rows around +-2048, 30000 and (where the type has them) 10^30, ids masked
+    with the type's lowest value, and rows of nothing else: those continue with
+    every id at score - log vocab."""
+    pk = require_gpu()
+    lowest, V = torch.finfo(DT[dt]).min, 20001
+    logits, scores = draw(3, 4, V, DT[dt], 6)
+    x = logits.float()
+    far = [2040.0, -2047.0, 2049.0, -2100.0, 30000.0, -30000.0, 1e30 if dt != "f16" else 60000.0, 0.0]
+    x[:8] += torch.tensor(far, device=DEV).view(-1, 1)
+    x = x.to(DT[dt])
+    x[7, ::3] = lowest
+    x[8] = lowest
+    x[9, 100:] = lowest
+    x[10] = lowest
+    x[10, 77] = 3.0
+    scores[2, 0] = 9.0                                  # the masked row's beam is the best one
+    for keep in (4, 64):
+        check(pk.beam_search_step(x, scores, keep), x, scores, keep)
+
+
 def test_few_ids_left_in_every_slice_and_many_candidates():
     """Masks that leave a few ids a slice (fewer than keep), and slices whose best ids crowd together."""
     pk = require_gpu()
