@@ -13,10 +13,9 @@
 //   tiles) items, the longest sequences first.  The grid is one CTA an item;
 //   a running CTA takes the next one over from the CTAs still waiting to start
 //   (clusterlaunchcontrol.try_cancel), so the SMs finish together.  The Q
-//   producer does that and works the items out, one ahead, and hands them over
-//   in shared memory; K, V and the next Q tile (TMA, one box of G heads a
-//   token) arrive while the previous item is finished; barriers count on
-//   across items.
+//   producer does that near the end of the item before and hands items over in
+//   shared memory; K, V and the next Q tile (TMA, one box of G heads a token)
+//   arrive while the previous item is finished; barriers count on across items.
 // * keys are taken from the newest backwards, so a distance bias has its
 //   largest scores first and the running maximum hardly ever moves.
 // * a cap's tanh is a polynomial on the FMA pipe, two keys an instruction, as
@@ -25,6 +24,18 @@
 // * bf16 weights have fp32's range: with a cap and no slopes every score lies
 //   in [-cap, cap], and while 2^(cap log2 e) is far inside that range no
 //   reference is needed at all -- no maximum, no exchange, no rescaling.
+//
+// Measured: 8 prompts of 1024 tokens, 48 + 8 heads of 128, bf16, capped: 154 us
+// (670 TFLOP/s of visible pairs; 281 with the plain kernel's structure).  Four
+// chunks of about 1000 tokens after up to 7168, 64 + 8 heads of 64, f16, bias
+// and prefix: 469 us (818 TFLOP/s; 709).  Bound: not the tensor pipe (active
+// 33 and 36 % of the time; leaving out nearly all products saves 1 to 2 %).  At
+// head_dim 64 the softmax warps' instructions (issue slots 66 % taken, four
+// warps a scheduler; without the exponentials or the row maxima 2 to 6 % less).
+// At 128 the chain of a half tile: weights, product, next scores; there is no
+// TMEM for a second S beside 2 O and 2 S, and the next S must wait for the
+// weights that lie in it (taking whichever half is ready, by polling, was
+// slower: 174 us).
 //
 // Warps (20): 0-7 and 8-15 softmax of Q tile 0 and 1 (warp w of a tile: TMEM
 // lanes 32 (w % 4) .., keys 64 (w / 4) ..), 16 producer of K and V, 17 and 19
@@ -387,8 +398,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_mod_kernel(const __grid_c
   // beside the softmax of the other.
   constexpr bool kSplit = D == 128 && (MODE & kBounded);
   // whole swizzle atoms; an address known when linked keeps the barriers' out
-  // of the loops (rounded up at run time: 475 instead of 468 us for 2048 of
-  // 8192 tokens)
+  // of the loops (rounded up at run time: 475 instead of 468 us for four chunks
+  // of 1000 tokens after up to 7168)
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* gbase = smem_raw;
   const uint32_t base = smem_u32(smem_raw);

@@ -24,8 +24,8 @@
 // units a lane loaded ahead (four take more registers than the loads in
 // flight are worth: 8192 prefill rows of 48 + 8 + 8 heads 67 us against 53;
 // one 55).  Bound: bytes, every row read once and written once.  Those 8192
-// rows take 51 us (5.2 TB/s of rows), 18433 rows of 16 + 16 heads of 64 half
-// rotated 29 us (5.3 TB/s); one CTA a token with a barrier between angles and
+// rows take 48 us (5.5 TB/s of rows), 18433 rows of 16 + 16 heads of 64 half
+// rotated 26 us (5.7 TB/s); one CTA a token with a barrier between angles and
 // rows took 70 and 55 us.
 #include "common.cuh"
 #include "launch.h"
