@@ -125,7 +125,8 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_attention_kernel(const 
   const int cached = klen - qlen;
   const int pos_first = cached + tok_begin, pos_last = cached + tok_end - 1;
   const int prefix = MOD ? prefix_of(p.mod, seq, klen) : 0;     // keys that every row reads
-  const int lo = prefix > 0 ? 0 : pf_window_start(pos_first + 1, p.window);   // first key any row reads
+  const int ws_first = pf_window_start(pos_first + 1, p.window);
+  const int lo = prefix > 0 ? 0 : ws_first;                     // first key any row reads
   const int hi = max(pos_last, prefix - 1);                     // last key any row reads
   const int kt_first = lo / kPfKeys, kt_last = hi / kPfKeys;
 
@@ -144,7 +145,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_attention_kernel(const 
     }
   }
 
-  // ---- K/V tile kt into stage st (rows outside [lo, hi] zero-filled)
+  // ---- K/V tile kt into stage st (rows outside [lo, hi], or between prefix and window, zero-filled)
   const int32_t* table = p.tables + (int64_t)seq * p.max_blocks;
   auto load_kv = [&](int kt, int st) {
     const int kbase = kt * kPfKeys;
@@ -152,7 +153,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_attention_kernel(const 
     for (int idx = threadIdx.x; idx < kPfKeys * L::kChunks; idx += kPfThreads) {
       const int r = idx / L::kChunks, c = idx % L::kChunks;
       const int kp = kbase + r;
-      bool ok = kp >= lo && kp <= hi;
+      bool ok = kp >= lo && kp <= hi && !(MOD && kp >= prefix && kp < ws_first);
       int64_t off = 0;
       if (ok) {
         const int phys = __ldg(table + kp / p.block_size);
@@ -193,10 +194,15 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_attention_kernel(const 
   for (int i = 0; i < D / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
   float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
 
-  for (int kt = kt_first; kt <= kt_last; ++kt) {
-    const int st = (kt - kt_first) & 1;
-    if (kt < kt_last) {
-      load_kv(kt + 1, st ^ 1);
+  // the tile after kt; those between the prefix and the window are left out
+  auto next = [&](int kt) {
+    ++kt;
+    return MOD && kt * kPfKeys >= prefix && (kt + 1) * kPfKeys <= ws_first ? ws_first / kPfKeys : kt;
+  };
+  for (int kt = kt_first, st = 0, after; kt <= kt_last; kt = after, st ^= 1) {
+    after = next(kt);
+    if (after <= kt_last) {
+      load_kv(after, st ^ 1);
       cp_async_commit();
       cp_async_wait<1>();
     } else {

@@ -81,7 +81,7 @@ __global__ void __launch_bounds__(32 * kFmaMaxGroup) prefill_fma_kernel(const Fm
   const int pos = klen - qlen + (t - q0);
   const int ws = (p.window > 0 && pos + 1 > p.window) ? pos + 1 - p.window : 0;
   const int h = hk * G + warp;
-  // keys [from, to]; with a prefix those between it and the window are skipped over by the mask
+  // keys [from, to], but those between a prefix and the window
   const int prefix = MOD ? prefix_of(p.mod, seq, klen) : 0;
   const int from = prefix > 0 ? 0 : ws, to = max(pos, prefix - 1);
   const float slope = MOD ? bias_slope(p.mod, h) : 0.f;
@@ -96,6 +96,10 @@ __global__ void __launch_bounds__(32 * kFmaMaxGroup) prefill_fma_kernel(const Fm
 #pragma unroll
   for (int i = 0; i < D / 32; ++i) o[i] = 0.f;
   for (int kbase = (from / kFmaKeys) * kFmaKeys; kbase <= to; kbase += kFmaKeys) {
+    if (MOD && kbase >= prefix && kbase + kFmaKeys <= ws) {
+      kbase = (ws / kFmaKeys - 1) * kFmaKeys;              // on to the window's first chunk
+      continue;
+    }
     __syncthreads();                                       // the previous chunk is no longer read
     for (int e = threadIdx.x; e < kFmaKeys * D; e += blockDim.x) {
       const int r = e / D, d = e - (e / D) * D;

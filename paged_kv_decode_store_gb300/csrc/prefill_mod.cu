@@ -85,7 +85,7 @@ struct Layout {
   static constexpr int kXBufs = D == 64 ? 2 : 1;
   // at least 120 KB so that one CTA (which holds all TMEM) is resident per SM
   static constexpr uint32_t kItems = kX + kXBufs * 1024;               // ring of items
-  static constexpr uint32_t kOrder = kItems + 320;                     // sequences, longest first
+  static constexpr uint32_t kOrder = kItems + 384;                     // sequences, longest first
   static constexpr uint32_t kEnd = kOrder + 64;
   static constexpr uint32_t kBytes = kEnd > 122880u ? kEnd : 122880u;
 };
@@ -95,7 +95,7 @@ static_assert(Layout<128>::kBytes <= 232448, "227 KB of shared memory");
 // halves of keys go their own ways, an exchange's + 4 g + the warp's quarter of
 // the rows.
 enum : int {
-  kKFull = 0, kKEmpty = 4, kVFull = 8, kVReady = 12, kVEmpty = 16, kQFull = 20, kQEmpty = 22, kSFull = 24, kPFull = 28,
+  kKFull = 0, kKEmpty = 4, kVFull = 8, kVCut = 12, kVEmpty = 16, kQFull = 20, kQEmpty = 22, kSFull = 24, kPFull = 28,
   kPVDone = 32, kSRead = 36, kOFree = 38, kExch = 40, kItemFull = 48, kItemFree = 52, kClaim = 56, kDrain = 57,
   kNear = 59, kNumBars = 60
 };
@@ -111,8 +111,8 @@ struct ModParams {
   void* out;
   const int32_t* tables;
   int max_blocks;
-  int64_t num_blocks;
-  int block_size;
+  int block_size, block_shift;   // a power of two
+  uint32_t block_limit;  // num_blocks, at most 2^31
   int seg_rows;          // rows per TMA box of the cache: min(block_size, 128)
   const int32_t* cu_q;
   const int32_t* cu_k;
@@ -131,15 +131,19 @@ struct ModParams {
 
 // One item: the keys of a pair of Q tiles.  n = 0: nothing to do, -1: no more.
 // K/V tiles are counted from the last one backwards: tile t holds keys
-// [kt_last - t, ..) * 128.
+// [kt_last - t, ..) * 128, from tile n_main on `gap` tiles less.  Keys that no
+// row sees are not read: those outside [lo, hi] and, between the prefix and the
+// window, [hole, hole_end).
 struct __align__(16) Item {
   int seq, hk, q0, cached, prefix;
   int tb[2], te[2];      // new tokens of Q tile g (0: the earlier one, may be empty)
   int lo, hi, kt_last, n;
   int gf[2], gn[2];      // first K/V tile and number of tiles of Q tile g
+  int n_main, gap, hole, hole_end;
   int pad[3];
+  __device__ int tile(int t) const { return kt_last - t - (t >= n_main ? gap : 0); }
 };
-static_assert(sizeof(Item) * kItemRing == 320, "the ring in Layout");
+static_assert(sizeof(Item) * kItemRing == 384, "the ring in Layout");
 
 __device__ __forceinline__ int window_first(int c, int window) { return (window > 0 && c > window) ? c - window : 0; }
 
@@ -168,18 +172,27 @@ __device__ __forceinline__ Item item_at(const ModParams& p, const uint8_t* order
   for (int g = 0; g < 2; ++g) {
     t.te[g] = qlen - (2 * zpair + 1 - g) * p.tile_tokens;
     t.tb[g] = max(0, t.te[g] - p.tile_tokens);
-    lo_g[g] = t.prefix > 0 ? 0 : window_first(t.cached + t.tb[g] + 1, p.window);
+    lo_g[g] = window_first(t.cached + t.tb[g] + 1, p.window);
     hi_g[g] = max(t.cached + t.te[g] - 1, t.prefix - 1);
   }
   if (t.te[1] <= 0) return t;                    // past the sequence's last pair
   t.lo = t.te[0] > 0 ? lo_g[0] : lo_g[1];
   t.hi = hi_g[1];
   t.kt_last = t.hi / kTcKeys;
-  t.n = t.kt_last - t.lo / kTcKeys + 1;
+  t.n = t.n_main = t.kt_last - t.lo / kTcKeys + 1;
+  t.gap = t.hole = t.hole_end = 0;
+  if (t.prefix > 0) {
+    t.hole = t.prefix;
+    t.hole_end = t.lo;
+    const int last = (t.prefix - 1) / kTcKeys;             // the prefix's last tile
+    t.gap = max(0, t.lo / kTcKeys - 1 - last);
+    t.n = t.kt_last + 1 - t.gap;
+    t.lo = 0;
+  }
 #pragma unroll
   for (int g = 0; g < 2; ++g) {
     t.gf[g] = t.kt_last - hi_g[g] / kTcKeys;
-    t.gn[g] = t.te[g] > 0 ? hi_g[g] / kTcKeys - lo_g[g] / kTcKeys + 1 : 0;
+    t.gn[g] = t.te[g] <= 0 ? 0 : t.prefix > 0 ? t.n - t.gf[g] : hi_g[g] / kTcKeys - lo_g[g] / kTcKeys + 1;
   }
   return t;
 }
@@ -436,90 +449,105 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_mod_kernel(const __grid_c
   if (warp >= kKvWarp) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
   if (warp == kKvWarp) {
     // ------------------------------------------------------- K and V producer
-    // Lane s copies segment s of a tile (lane 0 waits for a free stage first);
-    // K runs kAhead tiles ahead of V.  A V tile with rows outside [lo, hi] is
-    // waited for and those rows zeroed before it is released, so that they
-    // never weigh in.
+    // Lane s copies segment s of a tile; K runs kAhead tiles ahead of V.  A V
+    // tile with rows that are not read lands on a barrier of its own (kVCut)
+    // and is released with those rows zeroed, so that they never weigh in.
+    // Every instruction here is one that the softmax warps of the same
+    // scheduler do not get, and they set the pace (with divisions, a barrier and
+    // some votes more a tile: 500 instead of 445 us for the four chunks).
     constexpr int kAhead = kKStages - 2;
     const uint32_t box = (uint32_t)p.seg_rows * 128u;
     const int nseg = kTcKeys / p.seg_rows;
+    const uint32_t whole = (1u << nseg) - 1u;  // at most 16 segments
     if (lane == 0) {
       asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&p.tmap_k)) : "memory");
       asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&p.tmap_v)) : "memory");
     }
-    constexpr int kNone = INT_MIN;             // a segment that misses [lo, hi]: nothing to load
+    constexpr int kNone = INT_MIN;             // a segment of rows that are not read: nothing to load
     bool ok = true;
-    int nk = 0, nv = 0;                        // K and V tiles so far, of all items
-    // one operand of a tile, whose block id is b in lane s; n-th of its kind
-    auto copy = [&](const CUtensorMap* map, uint32_t ring, int stages, int full0, int empty0, int n, int ks, int hk, int b) {
-      const int stg = n % stages;
-      if (n >= stages) {
-        if (lane == 0) ok = wait_bounded(&bars[empty0 + stg], ((n / stages) - 1) & 1);
-        ok = __shfl_sync(FULL_MASK, ok, 0);
-        if (!ok) return;
-      }
-      const bool good = b != kNone && b >= 0 && b < p.num_blocks;
-      const uint32_t loaded = __ballot_sync(FULL_MASK, good), bad = __ballot_sync(FULL_MASK, b != kNone && !good);
-      const uint32_t dst0 = ring + stg * H * kHalf + lane * box;
-      if (bad) {                               // a bad block id reads as zeros
-        if (lane == 0) flag_error(p.err, PKVD_ERR_BLOCK_ID);
-        if ((bad >> lane) & 1u) {
-          for (int h = 0; h < H; ++h)
-            for (uint32_t o = 0; o < box; o += 16) st_shared_v4(dst0 + h * kHalf + o, make_uint4(0u, 0u, 0u, 0u));
-          fence_proxy_async_smem();
+    int kstg = 0, vstg = 0, landed = 0;        // next stages; phases of kVCut
+    uint32_t kpar = 1, vpar = 1;               // parities of their release (nothing to wait for in the first round)
+    auto wait = [&](int bar, uint32_t parity) {
+      if (ok) ok = __all_sync(FULL_MASK, wait_bounded(&bars[bar], parity));
+    };
+    // one operand of a tile into a stage, whose block id is b in lane s
+    auto copy = [&](const CUtensorMap* map, uint32_t dst, int bar, int ks, int hk, int b) {
+      const bool good = (uint32_t)b < p.block_limit;
+      const uint32_t loaded = __ballot_sync(FULL_MASK, good);
+      uint32_t bytes = H * kHalf;
+      dst += lane * box;
+      if (loaded != whole) {
+        bytes = (uint32_t)__popc(loaded) * box * H;
+        const uint32_t bad = __ballot_sync(FULL_MASK, b != kNone && !good);
+        if (bad) {                             // a bad block id reads as zeros
+          if (lane == 0) flag_error(p.err, PKVD_ERR_BLOCK_ID);
+          if ((bad >> lane) & 1u) {
+            for (int h = 0; h < H; ++h)
+              for (uint32_t o = 0; o < box; o += 16) st_shared_v4(dst + h * kHalf + o, make_uint4(0u, 0u, 0u, 0u));
+            fence_proxy_async_smem();
+          }
+          __syncwarp();
         }
       }
-      __syncwarp();
-      uint64_t* bar = &bars[full0 + stg];
-      if (lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)__popc(loaded) * box * H);
+      if (lane == 0) mbar_arrive_expect_tx(&bars[bar], bytes);
       __syncwarp();
       if (good) {
 #pragma unroll
-        for (int h = 0; h < H; ++h) tma_load4(dst0 + h * kHalf, map, h * 64, hk, ks % p.block_size, b, bar);
+        for (int h = 0; h < H; ++h) tma_load4(dst + h * kHalf, map, h * 64, hk, ks & (p.block_size - 1), b, &bars[bar]);
       }
     };
     for (int r = 0; ok; ++r) {
-      if (lane == 0) ok = wait_bounded(&bars[kItemFull + r % kItemRing], (r / kItemRing) & 1);
-      ok = __shfl_sync(FULL_MASK, ok, 0);
+      wait(kItemFull + r % kItemRing, (r / kItemRing) & 1);
       if (!ok) break;
       const Item& cur = ring_items[r % kItemRing];
       if (cur.n < 0) break;
       const int32_t* table = p.tables + (int64_t)cur.seq * p.max_blocks;
-      const int n = cur.n, hk = cur.hk, lo = cur.lo, hi = cur.hi, kt_last = cur.kt_last;
-      auto key_of = [&](int t) { return (kt_last - t) * kTcKeys + lane * p.seg_rows; };
+      const int n = cur.n, hk = cur.hk, lo = cur.lo, hi = cur.hi, hole = cur.hole, hole_end = cur.hole_end;
+      const int kt_last = cur.kt_last, n_main = cur.n_main, gap = cur.gap, near = max(0, n - 1 - kAhead);
+      auto tile_of = [&](int t) { return kt_last - t - (t >= n_main ? gap : 0); };
+      auto key_of = [&](int t) { return tile_of(t) * kTcKeys + lane * p.seg_rows; };
       auto fetch = [&](int t) -> int {
         const int ks = key_of(t);
         if (t >= n || lane >= nseg || ks > hi || ks + p.seg_rows - 1 < lo) return kNone;
-        return __ldg(table + ks / p.block_size);
+        if (ks >= hole && ks + p.seg_rows <= hole_end) return kNone;
+        return __ldg(table + (ks >> p.block_shift));
+      };
+      auto copy_k = [&](int t, int b) {
+        wait(kKEmpty + kstg, kpar);
+        if (!ok) return;
+        copy(&p.tmap_k, base + L::kK + kstg * H * kHalf, kKFull + kstg, key_of(t), hk, b);
+        if (++kstg == kKStages) kstg = 0, kpar ^= 1;
       };
       int b[4];                                // block ids of V tile t and the three after it
 #pragma unroll
       for (int i = 0; i < 4; ++i) b[i] = fetch(i);
 #pragma unroll
       for (int i = 0; i < kAhead; ++i)
-        if (ok && i < n) copy(&p.tmap_k, base + L::kK, kKStages, kKFull, kKEmpty, nk++, key_of(i), hk, b[i]);
+        if (i < n) copy_k(i, b[i]);
       for (int t = 0; ok && t < n; ++t) {
-        if (t + kAhead < n) copy(&p.tmap_k, base + L::kK, kKStages, kKFull, kKEmpty, nk++, key_of(t + kAhead), hk, b[kAhead]);
+        if (t + kAhead < n) copy_k(t + kAhead, b[kAhead]);
+        if (lane == 0 && t == near) mbar_arrive(&bars[kNear]);
+        wait(kVEmpty + vstg, vpar);
         if (!ok) break;
-        if (lane == 0 && t == max(0, n - 1 - kAhead)) mbar_arrive(&bars[kNear]);
-        copy(&p.tmap_v, base + L::kV, kVStages, kVFull, kVEmpty, nv++, key_of(t), hk, b[0]);
-        if (!ok) break;
-        const int stg = (nv - 1) % kVStages, kbase = (kt_last - t) * kTcKeys;
-        if (kbase < lo || kbase + kTcKeys - 1 > hi) {
-          if (lane == 0) ok = wait_bounded(&bars[kVFull + stg], ((nv - 1) / kVStages) & 1);
-          ok = __shfl_sync(FULL_MASK, ok, 0);
+        const int kbase = tile_of(t) * kTcKeys;
+        const bool cut = kbase < lo || kbase + kTcKeys - 1 > hi || max(kbase, hole) < min(kbase + kTcKeys, hole_end);
+        const uint32_t dst = base + L::kV + vstg * H * kHalf;
+        copy(&p.tmap_v, dst, (cut ? kVCut : kVFull) + vstg, kbase + lane * p.seg_rows, hk, b[0]);
+        if (cut) {
+          wait(kVCut + vstg, (landed >> vstg) & 1);
+          landed ^= 1 << vstg;
           if (!ok) break;
           for (int rr = lane; rr < kTcKeys; rr += 32) {
             const int kp = kbase + rr;
-            if (kp >= lo && kp <= hi) continue;
+            if (kp >= lo && kp <= hi && !(kp >= hole && kp < hole_end)) continue;
             for (int h = 0; h < H; ++h)
-              for (int c = 0; c < 8; ++c)
-                st_shared_v4(base + L::kV + stg * H * kHalf + h * kHalf + rr * 128 + c * 16, make_uint4(0u, 0u, 0u, 0u));
+              for (int c = 0; c < 8; ++c) st_shared_v4(dst + h * kHalf + rr * 128 + c * 16, make_uint4(0u, 0u, 0u, 0u));
           }
           fence_proxy_async_smem();
           __syncwarp();
+          if (lane == 0) mbar_arrive(&bars[kVFull + vstg]);
         }
-        if (lane == 0) mbar_arrive(&bars[kVReady + stg]);
+        if (++vstg == kVStages) vstg = 0, vpar ^= 1;
         b[0] = b[1];
         b[1] = b[2];
         b[2] = b[3];
@@ -531,8 +559,9 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_mod_kernel(const __grid_c
     if (!ok && lane == 0) {
       // gave up: let the copies still in flight land before the CTA leaves
       flag_error(p.err, PKVD_ERR_TIMEOUT);
-      for (int u = max(0, nk - kKStages); u < nk; ++u) wait_bounded(&bars[kKFull + u % kKStages], (u / kKStages) & 1);
-      for (int u = max(0, nv - kVStages); u < nv; ++u) wait_bounded(&bars[kVFull + u % kVStages], (u / kVStages) & 1);
+      // (a stage's full barrier is behind its release, or one phase ahead of it)
+      for (int u = 0; u < kKStages; ++u) wait_bounded(&bars[kKFull + u], (kpar ^ (u < kstg ? 0u : 1u)) ^ 1u);
+      for (int u = 0; u < kVStages; ++u) wait_bounded(&bars[kVFull + u], (vpar ^ (u < vstg ? 0u : 1u)) ^ 1u);
     }
   } else if (warp == kQWarp) {
     // ------------------------------------------------- items and Q producer
@@ -646,7 +675,6 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_mod_kernel(const __grid_c
             wait(kKFull + t % kKStages, (t / kKStages) & 1);
             if (ok && leader) mbar_arrive(&bars[kKEmpty + t % kKStages]);
             wait(kVFull + t % kVStages, (t / kVStages) & 1);
-            wait(kVReady + t % kVStages, (t / kVStages) & 1);
             if (ok && leader) mbar_arrive(&bars[kVEmpty + t % kVStages]);
           }
         };
@@ -690,7 +718,6 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_mod_kernel(const __grid_c
               wait(kPFull + g + 2 * h, n & 1);
               if (h == 0) {
                 wait(kVFull + stg, (t / kVStages) & 1);
-                wait(kVReady + stg, (t / kVStages) & 1);
                 if (j == 0 && used > 0) wait(kOFree + g, (used - 1) & 1);
               }
               if (!ok) break;
@@ -763,15 +790,17 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_mod_kernel(const __grid_c
         arrive(kItemFree + r % kItemRing);
         continue;
       }
-      const int kt_last = it.kt_last, prefix = it.prefix;
+      const int prefix = it.prefix;
       const bool live = row < (te - tb) * p.group;
       const int tt = live ? row / p.group : 0, gi = live ? row - tt * p.group : 0;
       const int pr = it.cached + tb + tt;        // padding rows mirror row 0
       const int wr = window_first(pr + 1, p.window);
       const float nslope = bias_slope(p.mod, it.hk * p.group + gi);
       float m_ref = (MODE & kBounded) ? 0.f : -INFINITY, l = 0.f;
-      for (int j = 0; j < gn; ++j, ++n) {
-        const int kbase = (kt_last - gf - j) * kTcKeys + half * kCols;
+      int kbase = it.tile(gf) * kTcKeys + half * kCols;
+      const int jump = gf < it.n_main ? it.n_main - gf : -1;
+      for (int j = 0; j < gn; ++j, ++n, kbase -= kTcKeys) {
+        if (j == jump) kbase -= it.gap * kTcKeys;
         const Visible see = {wr - kbase, pr + 1 - kbase, prefix - kbase};
         wait(kSFull + sub, n & 1);
         if (!ok) break;
@@ -1002,8 +1031,10 @@ cudaError_t launch_prefill_mod(const PrefillArgs& a, cudaStream_t stream) {
   prm.out = a.out;
   prm.tables = a.block_tables;
   prm.max_blocks = a.max_blocks_per_seq;
-  prm.num_blocks = c.num_blocks;
+  prm.block_limit = (uint32_t)(c.num_blocks < 0x80000000ll ? c.num_blocks : 0x80000000ll);
   prm.block_size = c.block_size;
+  prm.block_shift = 0;
+  while ((1 << prm.block_shift) < c.block_size) ++prm.block_shift;
   prm.seg_rows = seg_rows;
   prm.cu_q = a.cu_seqlens_q;
   prm.cu_k = a.cu_seqlens_k;

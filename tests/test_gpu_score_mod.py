@@ -236,3 +236,35 @@ def test_replayed_from_a_graph_and_on_another_stream():
     g.replay()
     torch.cuda.synchronize()
     assert torch.equal(out, run())
+
+
+@pytest.mark.parametrize("path", [1, 2, 3])
+@pytest.mark.parametrize("prefix", [1, 128, 129, 500, 1200, 1301])
+def test_prefill_prefix_far_before_the_window(prefix, path):
+    """Blocks between the prefix and the window (none, one, whole tiles of them) are not read: they hold NaN, or
+    are no longer in the table."""
+    pk = require_gpu()
+    hq, hkv, d, bs, klen, qlen, window, scale = 4, 2, 64, 16, 1400, 90, 70, 0.125
+    kc, vc, tables, rows = cache_of([klen, 300], hkv, d, bs, torch.bfloat16, 7)
+    first = klen - qlen + 1 - window                     # the first key in any row's window
+    for b in range(-(-prefix // bs), first // bs):
+        kc[tables[0, b].item()] = float("nan")
+        vc[tables[0, b].item()] = float("nan")
+        if b % 2:
+            tables[0, b] = -1
+    err = torch.zeros(1, dtype=torch.int32, device=DEV)
+    q = torch.randn(qlen + 20, hq, d, generator=torch.Generator().manual_seed(8)).to(torch.bfloat16)
+    slopes = torch.full((hq,), 0.01, device=DEV)
+    cq, ck = (torch.tensor(x, dtype=torch.int32, device=DEV) for x in ([0, qlen, qlen + 20], [0, klen, klen + 300]))
+    out = pk.prefill_attention(q.to(DEV), kc, vc, tables, cq, ck, qlen, scale, window=window, path=path, softcap=9.0,
+                               alibi_slopes=slopes, prefix_lens=torch.tensor([prefix, 64], dtype=torch.int32, device=DEV),
+                               err=err)
+    assert err.item() == 0
+    got, tol = out.double().cpu().numpy(), tolerances(torch.bfloat16, path != 1)
+    for t in range(qlen + 20):
+        i, p, n = (0, klen - qlen + t, klen) if t < qlen else (1, 300 - 20 + t - qlen, 300)
+        for h in range(0, hq, 3):
+            k, v = (x[:, h // (hq // hkv)] for x in rows[i])
+            want, bound = oracle.scores.attend(q[t, h].double().numpy(), k, v, p, scale, 9.0, float(slopes[h]), window,
+                                               (prefix, 64)[i], **tol)
+            assert np.all(np.abs(got[t, h] - want) <= bound), (t, h)
