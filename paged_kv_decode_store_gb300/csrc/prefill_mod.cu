@@ -662,88 +662,100 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_mod_kernel(const __grid_c
       auto wait = [&](int bar, uint32_t parity) {
         if (ok) ok = __all_sync(FULL_MASK, wait_bounded(&bars[bar], parity));
       };
-      int at = 0, n = 0, used = 0;                  // K/V tiles of all items, this tile's, its items
+      int n = 0, used = 0;                          // this tile's K tiles of all items, its items
+      int kstg = 0, vstg = 0;                       // next stages and their phases, every tile of every item
+      uint32_t kpar = 0, vpar = 0;
+      auto next_k = [&] {
+        if (++kstg == kKStages) kstg = 0, kpar ^= 1;
+      };
+      auto next_v = [&] {
+        if (++vstg == kVStages) vstg = 0, vpar ^= 1;
+      };
+      auto skip = [&](int tiles) {                  // that this Q tile does not use
+        for (int t = 0; t < tiles; ++t) {
+          wait(kKFull + kstg, kpar);
+          if (ok && leader) mbar_arrive(&bars[kKEmpty + kstg]);
+          next_k();
+          wait(kVFull + vstg, vpar);
+          if (ok && leader) mbar_arrive(&bars[kVEmpty + vstg]);
+          next_v();
+        }
+      };
+      // S of the next K stage: half h or all (0) of its keys
+      auto issue_s = [&](int h, bool last) {
+        tc_fence_after();
+        const uint32_t kd = desc_lo(base + L::kK + kstg * H * kHalf, 16) + h * (kCols * 128 >> 4), d = s_cols + h * kCols;
+        if (leader) {
+#pragma unroll
+          for (int k = 0; k < D / 16; ++k) {
+            const uint32_t off = ((k >> 2) * kHalf + (k & 3) * 32) >> 4;
+            if (k == 0) mma_ss<false>(d, qd, kd, hi, id_s);
+            else mma_ss<true>(d, qd + off, kd + off, hi, id_s);
+          }
+          tc_commit(&bars[kSFull + g + 2 * h]);
+          if (h == kParts - 1) {
+            tc_commit(&bars[kKEmpty + kstg]);
+            if (last) tc_commit(&bars[kQEmpty + g]);
+          }
+        }
+        __syncwarp();
+        if (h == kParts - 1) next_k();
+      };
+      auto issue_pv = [&](int h, uint32_t add) {    // half h or all of the next V stage
+        tc_fence_after();
+        const uint32_t vd = desc_lo(base + L::kV + vstg * H * kHalf, kHalf);
+        if (leader) {
+#pragma unroll
+          for (int i = 0; i < kTcKeys / 16 / kParts; ++i) {        // 16 keys = 8 packed columns of weights
+            const int k = h * (kTcKeys / 32) + i;
+            const uint32_t col = kSepP ? k * 8 : (k >> 2) * kCols + (k & 3) * 8;
+            mma_ts(o_cols, p_cols + col, vd + k * 128, hi, id_pv, k > 0 ? 1u : add);
+          }
+          tc_commit(&bars[kPVDone + g + 2 * h]);
+          if (h == kParts - 1) tc_commit(&bars[kVEmpty + vstg]);
+        }
+        __syncwarp();
+        if (h == kParts - 1) next_v();
+      };
       for (int r = 0; ok; ++r) {
         wait(kItemFull + r % kItemRing, (r / kItemRing) & 1);
         if (!ok) break;
         const Item& it = ring_items[r % kItemRing];
         const int all = __shfl_sync(FULL_MASK, it.n, 0);
         if (all < 0) break;
-        const int gn = __shfl_sync(FULL_MASK, it.gn[g], 0), first = at + __shfl_sync(FULL_MASK, it.gf[g], 0);
-        auto skip = [&](int from, int to) {         // tiles that this Q tile does not use
-          for (int t = from; t < to; ++t) {
-            wait(kKFull + t % kKStages, (t / kKStages) & 1);
-            if (ok && leader) mbar_arrive(&bars[kKEmpty + t % kKStages]);
-            wait(kVFull + t % kVStages, (t / kVStages) & 1);
-            if (ok && leader) mbar_arrive(&bars[kVEmpty + t % kVStages]);
-          }
-        };
-        skip(at, gn > 0 ? first : at + all);
-        auto issue_s = [&](int j, int h) {          // the n-th of the tile is the item's j-th; half h or all (0) of its keys
-          const int t = first + j, stg = t % kKStages;
-          wait(kKFull + stg, (t / kKStages) & 1);
-          if (!ok) return;
-          tc_fence_after();
-          const uint32_t kd = desc_lo(base + L::kK + stg * H * kHalf, 16) + h * (kCols * 128 >> 4), d = s_cols + h * kCols;
-          if (leader) {
-#pragma unroll
-            for (int k = 0; k < D / 16; ++k) {
-              const uint32_t off = ((k >> 2) * kHalf + (k & 3) * 32) >> 4;
-              if (k == 0) mma_ss<false>(d, qd, kd, hi, id_s);
-              else mma_ss<true>(d, qd + off, kd + off, hi, id_s);
-            }
-            tc_commit(&bars[kSFull + g + 2 * h]);
-            if (!kSplit || h == 1) {
-              tc_commit(&bars[kKEmpty + stg]);
-              if (j == gn - 1) tc_commit(&bars[kQEmpty + g]);
-            }
-          }
-          __syncwarp();
-        };
+        const int gn = __shfl_sync(FULL_MASK, it.gn[g], 0), before = __shfl_sync(FULL_MASK, it.gf[g], 0);
+        skip(gn > 0 ? before : all);
         if (gn > 0) {
+          // what arrives last (the softmax warps' part) is waited for last
           wait(kQFull + g, used & 1);
+          wait(kKFull + kstg, kpar);
 #pragma unroll
           for (int h = 0; h < kParts; ++h) {
             if (n > 0) wait((kSepP ? kSRead : kPVDone) + g + 2 * h, (n - 1) & 1);
-            if (ok) issue_s(0, h);
+            if (ok) issue_s(h, gn == 1);
           }
           for (int j = 0; ok && j < gn; ++j, ++n) {
-            if (kSepP && j + 1 < gn) {
+            const bool more = j + 1 < gn;
+            if (more) wait(kKFull + kstg, kpar);
+            if (kSepP && more) {
               wait(kSRead + g, n & 1);
-              if (ok) issue_s(j + 1, 0);
+              if (ok) issue_s(0, j + 2 == gn);
             }
-            const int t = first + j, stg = t % kVStages;
+            wait(kVFull + vstg, vpar);
+            if (j == 0 && used > 0) wait(kOFree + g, (used - 1) & 1);
 #pragma unroll
             for (int h = 0; h < kParts; ++h) {
               wait(kPFull + g + 2 * h, n & 1);
-              if (h == 0) {
-                wait(kVFull + stg, (t / kVStages) & 1);
-                if (j == 0 && used > 0) wait(kOFree + g, (used - 1) & 1);
-              }
-              if (!ok) break;
-              tc_fence_after();
-              const uint32_t vd = desc_lo(base + L::kV + stg * H * kHalf, kHalf);
-              if (leader) {
-#pragma unroll
-                for (int i = 0; i < kTcKeys / 16 / kParts; ++i) {      // 16 keys = 8 packed columns of weights
-                  const int k = h * (kTcKeys / 32) + i;
-                  const uint32_t col = kSepP ? k * 8 : (k >> 2) * kCols + (k & 3) * 8;
-                  mma_ts(o_cols, p_cols + col, vd + k * 128, hi, id_pv, k > 0 ? 1u : (uint32_t)j);
-                }
-                tc_commit(&bars[kPVDone + g + 2 * h]);
-                if (h == kParts - 1) tc_commit(&bars[kVEmpty + stg]);
-              }
-              __syncwarp();
-              if (!kSepP && j + 1 < gn) {
+              if (ok) issue_pv(h, j);
+              if (!kSepP && more) {
                 wait(kPVDone + g + 2 * h, n & 1);
-                if (ok) issue_s(j + 1, h);
+                if (ok) issue_s(h, j + 2 == gn);
               }
             }
           }
           ++used;
-          skip(first + gn, at + all);
+          skip(all - before - gn);
         }
-        at += all;
         __syncwarp();
         if (leader) mbar_arrive(&bars[kItemFree + r % kItemRing]);
       }
