@@ -287,13 +287,25 @@ __device__ __forceinline__ void mul2(float& d0, float& d1, float a0, float a1, f
   asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
   asm("mov.b64 {%0, %1}, %2;" : "=f"(d0), "=f"(d1) : "l"(d));
 }
-__device__ __forceinline__ void horner2(float& r0, float& r1, float z0, float z1, float c) {
-  unsigned long long r, z, cc;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(r0), "f"(r1));
-  asm("mov.b64 %0, {%1, %2};" : "=l"(z) : "f"(z0), "f"(z1));
-  asm("mov.b64 %0, {%1, %1};" : "=l"(cc) : "f"(c));
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(r), "l"(z), "l"(cc));
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(r0), "=f"(r1) : "l"(r));
+// A factor for both of a pair.  Volatile, so that it is made once: left to
+// itself the compiler makes it anew for every product.
+__device__ __forceinline__ uint64_t both(float c) {
+  uint64_t r;
+  asm volatile("mov.b64 %0, {%1, %1};" : "=l"(r) : "f"(c));
+  return r;
+}
+__device__ __forceinline__ void scale2(float& d0, float& d1, uint64_t b) {
+  uint64_t a;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(a) : "f"(d0), "f"(d1));
+  asm("mul.rn.f32x2 %0, %0, %1;" : "+l"(a) : "l"(b));
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(d0), "=f"(d1) : "l"(a));
+}
+__device__ __forceinline__ void scale_add2(float& d0, float& d1, uint64_t b, float c0, float c1) {
+  uint64_t a, c;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(a) : "f"(d0), "f"(d1));
+  asm("mov.b64 %0, {%1, %2};" : "=l"(c) : "f"(c0), "f"(c1));
+  asm("fma.rn.f32x2 %0, %0, %1, %2;" : "+l"(a) : "l"(b), "l"(c));
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(d0), "=f"(d1) : "l"(a));
 }
 
 __device__ __forceinline__ void fma2(float& d0, float& d1, float a0, float a1, float b0, float b1, float c0, float c1) {
@@ -343,15 +355,23 @@ struct Visible {
   }
 };
 
-// s r(s^2) + add on two keys, r a polynomial of N coefficients; `most` keeps
-// the largest s^2.
-template <int N, bool ADD>
-__device__ __forceinline__ void odd_poly2(float& v0, float& v1, const float* coef, float add0, float add1, float& most) {
-  float z0, z1, r0 = coef[N - 1], r1 = coef[N - 1];
+// The factors of a thread's products: the softmax scale, the cap's polynomial.
+struct Factors {
+  uint64_t scale, poly[4];
+};
+
+// s r(s^2) + add on two keys, r the polynomial; `most` keeps the largest s^2.
+template <bool ADD>
+__device__ __forceinline__ void odd_poly2(float& v0, float& v1, const uint64_t (&coef)[4], float add0, float add1,
+                                          float& most) {
+  float z0, z1, r0, r1;
   mul2(z0, z1, v0, v1, v0, v1);
   most = tc_max3(most, z0, z1);
+  uint64_t z, r = coef[3];
+  asm("mov.b64 %0, {%1, %2};" : "=l"(z) : "f"(z0), "f"(z1));
 #pragma unroll
-  for (int k = N - 2; k >= 0; --k) horner2(r0, r1, z0, z1, coef[k]);
+  for (int k = 2; k >= 0; --k) asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(r), "l"(z), "l"(coef[k]));
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r0), "=f"(r1) : "l"(r));
   if (ADD) fma2(v0, v1, v0, v1, r0, r1, add0, add1);
   else mul2(v0, v1, v0, v1, r0, r1);
 }
@@ -365,7 +385,7 @@ __device__ __forceinline__ void odd_poly2(float& v0, float& v1, const float* coe
 // key minus the row's position; `again` reads the raw scores once more (a
 // warp with a score past the polynomial's range: it has computed in vain).
 template <int MODE, int N, typename Again>
-__device__ __forceinline__ void modify(float (&v)[N], const ModParams& p, const Visible& see, float nslope, int off,
+__device__ __forceinline__ void modify(float (&v)[N], const ModParams& p, const Factors& f, const Visible& see, float nslope, int off,
                                        float& base, float& step, Again again) {
   const ScoreMod& m = p.mod;
   const bool linear = (MODE & kBias) && __all_sync(FULL_MASK, off + N - 1 <= 0);
@@ -378,7 +398,7 @@ __device__ __forceinline__ void modify(float (&v)[N], const ModParams& p, const 
     float most = 0.f;                  // largest square: the polynomial's range
 #pragma unroll
     for (int c = 0; c < N; c += 2)
-      odd_poly2<4, (MODE & kBias) != 0>(v[c], v[c + 1], p.poly, k[c & 7], k[(c & 7) + 1], most);
+      odd_poly2<(MODE & kBias) != 0>(v[c], v[c + 1], f.poly, k[c & 7], k[(c & 7) + 1], most);
     if (!__all_sync(FULL_MASK, most <= p.poly_range)) {
       again(v);
 #pragma unroll
@@ -388,9 +408,9 @@ __device__ __forceinline__ void modify(float (&v)[N], const ModParams& p, const 
 #pragma unroll
     for (int c = 0; c < N; c += 2) {
       if (MODE & kBias)
-        fma2(v[c], v[c + 1], v[c], v[c + 1], p.scale_log2, p.scale_log2, k[c & 7], k[(c & 7) + 1]);
+        scale_add2(v[c], v[c + 1], f.scale, k[c & 7], k[(c & 7) + 1]);
       else
-        mul2(v[c], v[c + 1], v[c], v[c + 1], p.scale_log2, p.scale_log2);
+        scale2(v[c], v[c + 1], f.scale);
     }
   }
   if ((MODE & kBias) && !linear) {
@@ -777,6 +797,10 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_mod_kernel(const __grid_c
     // what a row's two threads tell each other: 128 bytes a quarter of the rows
     uint8_t* xch = gbase + L::kX + g * 512 + quarter * 128;
     float* xsum = reinterpret_cast<float*>(xch);
+    Factors f;
+    f.scale = both(p.scale_log2);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) f.poly[k] = both(p.poly[k]);
     bool ok = true;
     auto wait = [&](int bar, uint32_t parity) {
       if (ok) ok = __all_sync(FULL_MASK, wait_bounded(&bars[bar], parity));
@@ -834,7 +858,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_mod_kernel(const __grid_c
                 tmem_ld_wait();
               };
               read(v);
-              modify<MODE>(v, p, part, 0.f, 0, bias, step, read);
+              modify<MODE>(v, p, f, part, 0.f, 0, bias, step, read);
 #pragma unroll
               for (int c = 0; c < 32; c += 4) {
                 const float e0 = tc_ex2(v[c]), e1 = tc_ex2(v[c + 1]), e2 = tc_ex2(v[c + 2]), e3 = tc_ex2(v[c + 3]);
@@ -869,7 +893,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_mod_kernel(const __grid_c
             arrive(kSRead + g);
           }
           float bias, step;
-          modify<MODE>(v, p, see, nslope, kbase - pr, bias, step, read);
+          modify<MODE>(v, p, f, see, nslope, kbase - pr, bias, step, read);
           if (kSepP && (MODE & kCap)) {
             tc_fence_before();
             arrive(kSRead + g);
