@@ -330,10 +330,6 @@ __device__ __forceinline__ uint32_t span_bits(int a, int z) {
 // A thread's visible columns: [lo, end) of its 64, and those below `prefix`.
 struct Visible {
   int lo, end, prefix;
-  template <int N>
-  __device__ bool none() const { return (end <= max(lo, 0) || lo >= N) && prefix <= 0; }
-  template <int N>
-  __device__ bool all() const { return (lo <= 0 && end >= N) || prefix >= N; }
   __device__ uint32_t bits(int word) const {
     return span_bits(lo - 32 * word, end - 32 * word) | span_bits(0, prefix - 32 * word);
   }
@@ -381,14 +377,15 @@ __device__ __forceinline__ void odd_poly2(float& v0, float& v1, const uint64_t (
 // columns: column c's score is v[c] + base + (c / 8) * step.  A bias that
 // falls linearly (no key after any of the warp's rows) then costs nothing per
 // key: eight multiples of the slope ride on the last product, the rest joins
-// the reference that the exponent subtracts anyway.  `off`: the first column's
+// the reference that the exponent subtracts anyway.  The same for the whole
+// warp: `whole`, every row sees every column, and `linear`.  `off`: the first column's
 // key minus the row's position; `again` reads the raw scores once more (a
 // warp with a score past the polynomial's range: it has computed in vain).
 template <int MODE, int N, typename Again>
-__device__ __forceinline__ void modify(float (&v)[N], const ModParams& p, const Factors& f, const Visible& see, float nslope, int off,
-                                       float& base, float& step, Again again) {
+__device__ __forceinline__ void modify(float (&v)[N], const ModParams& p, const Factors& f, const Visible& see,
+                                       bool whole, bool linear, float nslope, int off, float& base, float& step,
+                                       Again again) {
   const ScoreMod& m = p.mod;
-  const bool linear = (MODE & kBias) && __all_sync(FULL_MASK, off + N - 1 <= 0);
   float k[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) k[i] = (linear ? -nslope : 0.f) * (float)i;
@@ -418,7 +415,7 @@ __device__ __forceinline__ void modify(float (&v)[N], const ModParams& p, const 
 #pragma unroll
     for (int c = 0; c < N; ++c) v[c] = fmaf(nslope, fabsf(first + (float)c), v[c]);
   }
-  if (!__all_sync(FULL_MASK, see.all<N>())) see.hide(v);
+  if (!whole) see.hide(v);
 }
 
 template <typename T, int D, int MODE>
@@ -821,23 +818,26 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_mod_kernel(const __grid_c
       if (!ok) break;
       const Item& it = ring_items[r % kItemRing];
       if (it.n < 0) break;
-      const int tb = it.tb[g], te = it.te[g], gf = it.gf[g], gn = it.gn[g];
+      // (the shuffles: known to be uniform, and so is what the masks make of a tile)
+      auto uniform = [](int x) { return __shfl_sync(FULL_MASK, x, 0); };
+      const int tb = uniform(it.tb[g]), te = uniform(it.te[g]), gf = uniform(it.gf[g]), gn = uniform(it.gn[g]);
       if (gn == 0) {
         arrive(kItemFree + r % kItemRing);
         continue;
       }
-      const int prefix = it.prefix;
+      const int prefix = uniform(it.prefix);
       const bool live = row < (te - tb) * p.group;
       const int tt = live ? row / p.group : 0, gi = live ? row - tt * p.group : 0;
       const int pr = it.cached + tb + tt;        // padding rows mirror row 0
       const int wr = window_first(pr + 1, p.window);
+      const int pr_min = __reduce_min_sync(FULL_MASK, pr), wr_max = __reduce_max_sync(FULL_MASK, wr);
+      const int pr_max = __reduce_max_sync(FULL_MASK, pr), wr_min = __reduce_min_sync(FULL_MASK, wr);
       const float nslope = bias_slope(p.mod, it.hk * p.group + gi);
       float m_ref = (MODE & kBounded) ? 0.f : -INFINITY, l = 0.f;
-      int kbase = it.tile(gf) * kTcKeys + half * kCols;
-      const int jump = gf < it.n_main ? it.n_main - gf : -1;
+      int kbase = uniform(it.tile(gf)) * kTcKeys + half * kCols;
+      const int jump = uniform(it.n_main) - gf, gap = uniform(it.gap) * kTcKeys;
       for (int j = 0; j < gn; ++j, ++n, kbase -= kTcKeys) {
-        if (j == jump) kbase -= it.gap * kTcKeys;
-        const Visible see = {wr - kbase, pr + 1 - kbase, prefix - kbase};
+        if (j == jump && j > 0) kbase -= gap;     // (a first tile behind the gap: tile() knows)
         wait(kSFull + sub, n & 1);
         if (!ok) break;
         tc_fence_after();
@@ -847,8 +847,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_mod_kernel(const __grid_c
 #pragma unroll 1
           for (int c0 = 0; c0 < kCols; c0 += 32) {
             uint32_t pk[16];
-            const Visible part = {see.lo - c0, see.end - c0, see.prefix - c0};
-            if (__all_sync(FULL_MASK, part.none<32>())) {
+            const int k0 = kbase + c0;
+            if ((k0 > pr_max || k0 + 31 < wr_min) && k0 >= prefix) {       // no row sees any
 #pragma unroll
               for (int c = 0; c < 16; ++c) pk[c] = 0u;
             } else {
@@ -858,7 +858,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_mod_kernel(const __grid_c
                 tmem_ld_wait();
               };
               read(v);
-              modify<MODE>(v, p, f, part, 0.f, 0, bias, step, read);
+              const bool whole = (k0 + 31 <= pr_min && k0 >= wr_max) || k0 + 32 <= prefix;
+              modify<MODE>(v, p, f, Visible{wr - k0, pr + 1 - k0, prefix - k0}, whole, false, 0.f, 0, bias, step, read);
 #pragma unroll
               for (int c = 0; c < 32; c += 4) {
                 const float e0 = tc_ex2(v[c]), e1 = tc_ex2(v[c + 1]), e2 = tc_ex2(v[c + 2]), e3 = tc_ex2(v[c + 3]);
@@ -893,7 +894,10 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_mod_kernel(const __grid_c
             arrive(kSRead + g);
           }
           float bias, step;
-          modify<MODE>(v, p, f, see, nslope, kbase - pr, bias, step, read);
+          const bool before = kbase + kCols - 1 <= pr_min;
+          const bool whole = (before && kbase >= wr_max) || kbase + kCols <= prefix;
+          modify<MODE>(v, p, f, Visible{wr - kbase, pr + 1 - kbase, prefix - kbase}, whole, (MODE & kBias) && before, nslope,
+                       kbase - pr, bias, step, read);
           if (kSepP && (MODE & kCap)) {
             tc_fence_before();
             arrive(kSRead + g);
