@@ -25,17 +25,17 @@
 //   in [-cap, cap], and while 2^(cap log2 e) is far inside that range no
 //   reference is needed at all -- no maximum, no exchange, no rescaling.
 //
-// Measured: 8 prompts of 1024 tokens, 48 + 8 heads of 128, bf16, capped: 154 us
-// (670 TFLOP/s of visible pairs; 281 with the plain kernel's structure).  Four
+// Measured: 8 prompts of 1024 tokens, 48 + 8 heads of 128, bf16, capped: 131 us
+// (788 TFLOP/s of visible pairs; 281 with the plain kernel's structure).  Four
 // chunks of about 1000 tokens after up to 7168, 64 + 8 heads of 64, f16, bias
-// and prefix: 469 us (818 TFLOP/s; 709).  Bound: not the tensor pipe (active
-// 33 and 36 % of the time; leaving out nearly all products saves 1 to 2 %).  At
-// head_dim 64 the softmax warps' instructions (issue slots 66 % taken, four
-// warps a scheduler; without the exponentials or the row maxima 2 to 6 % less).
-// At 128 the chain of a half tile: weights, product, next scores; there is no
-// TMEM for a second S beside 2 O and 2 S, and the next S must wait for the
-// weights that lie in it (taking whichever half is ready, by polling, was
-// slower: 174 us).
+// and prefix: 418 us (918 TFLOP/s; 709).  Bound: not the tensor pipe (active
+// 39 % of the time; leaving out nearly all products saved 1 to 2 %).  At
+// head_dim 64 the instructions (issue slots 70 % taken; a scheduler has four
+// softmax warps and one of the others, and the slowest scheduler sets the
+// pace).  At 128 the chain of a half tile: weights, product, next scores; there
+// is no TMEM for a second S beside 2 O and 2 S, and the next S must wait for
+// the weights that lie in it (taking whichever half is ready, by polling, was
+// slower: 174 instead of 160 us).
 //
 // Warps (20): 0-7 and 8-15 softmax of Q tile 0 and 1 (warp w of a tile: TMEM
 // lanes 32 (w % 4) .., keys 64 (w / 4) ..), 16 producer of K and V, 17 and 19
@@ -892,17 +892,13 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_mod_kernel(const __grid_c
             tmem_ld_wait();
           };
           read(v);
-          // head_dim 64: the next S may overwrite these columns once nobody reads them again
-          if (kSepP && !(MODE & kCap)) {
-            tc_fence_before();
-            arrive(kSRead + g);
-          }
           float bias, step;
           const bool before = kbase + kCols - 1 <= pr_min;
           const bool whole = (before && kbase >= wr_max) || kbase + kCols <= prefix;
           modify<MODE>(v, p, f, Visible{wr - kbase, pr + 1 - kbase, prefix - kbase}, whole, (MODE & kBias) && before, nslope,
                        kbase - pr, bias, step, read);
-          if (kSepP && (MODE & kCap)) {
+          // head_dim 64: the next S may overwrite these columns once nobody reads them again
+          if (kSepP) {
             tc_fence_before();
             arrive(kSRead + g);
           }
