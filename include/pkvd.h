@@ -406,8 +406,8 @@ typedef struct {
  *         (so q, k may be slices of one projected [tokens, q+k+v] tensor), k
  *         likewise; positions int64 [num_tokens].
  * Output: q_out, k_out rows at their own strides; each may be its input (same
- *         pointer and stride: rotated in place), and must not overlap any of
- *         the other rows.  num_q_heads or num_kv_heads 0: that side is absent
+ *         pointer and stride: rotated in place; the pointer with another stride
+ *         is refused), and must not overlap any of the other rows.  num_q_heads or num_kv_heads 0: that side is absent
  *         (NULL).
  * Requirements: head_dim <= 512 and a multiple of 16 bytes; rows and strides
  *         16-byte aligned, strides at least heads * head_dim.

@@ -195,6 +195,11 @@ pkvd_status check_rope_rows(const void* p, int64_t stride, int heads, int head_d
   return PKVD_OK;
 }
 
+// Rows turned in place keep their places.
+bool in_place_elsewhere(const void* out, int64_t out_stride, const void* in, int64_t in_stride, int rows) {
+  return out == in && out_stride != in_stride && rows > 1;
+}
+
 void rope_common(RopeArgs* a, const pkvd_rope_desc* r, int dtype, int num_q_heads, int num_kv_heads, int head_dim) {
   *a = RopeArgs{};
   a->dtype = dtype;
@@ -210,12 +215,13 @@ void rope_common(RopeArgs* a, const pkvd_rope_desc* r, int dtype, int num_q_head
 // The rows of a fused store: q may be absent (no query heads).
 pkvd_status rope_store_args(RopeArgs* a, void* q_out, int64_t q_out_stride, const void* q, int64_t q_stride,
                             const void* k, int64_t k_stride, const void* v, int64_t v_stride, int num_q_heads,
-                            const pkvd_rope_desc* rope, const pkvd_cache* cache) {
+                            int rows, const pkvd_rope_desc* rope, const pkvd_cache* cache) {
   const int hkv = cache->num_kv_heads, D = cache->head_dim, dt = cache->dtype;
   pkvd_status s;
   if (num_q_heads > 0) {
     if ((s = check_rope_rows(q, q_stride, num_q_heads, D, dt)) != PKVD_OK) return s;
     if ((s = check_rope_rows(q_out, q_out_stride, num_q_heads, D, dt)) != PKVD_OK) return s;
+    if (in_place_elsewhere(q_out, q_out_stride, q, q_stride, rows)) return PKVD_INVALID_ARG;
   }
   if ((s = check_rope_rows(k, k_stride, hkv, D, dt)) != PKVD_OK) return s;
   if ((s = check_rope_rows(v, v_stride, hkv, D, dt)) != PKVD_OK) return s;
@@ -255,10 +261,12 @@ pkvd_status pkvd_rope(void* q_out, int64_t q_out_stride, const void* q, int64_t 
   if (num_q_heads > 0) {
     if ((s = check_rope_rows(q, q_stride, num_q_heads, head_dim, dtype)) != PKVD_OK) return s;
     if ((s = check_rope_rows(q_out, q_out_stride, num_q_heads, head_dim, dtype)) != PKVD_OK) return s;
+    if (in_place_elsewhere(q_out, q_out_stride, q, q_stride, num_tokens)) return PKVD_INVALID_ARG;
   }
   if (num_kv_heads > 0) {
     if ((s = check_rope_rows(k, k_stride, num_kv_heads, head_dim, dtype)) != PKVD_OK) return s;
     if ((s = check_rope_rows(k_out, k_out_stride, num_kv_heads, head_dim, dtype)) != PKVD_OK) return s;
+    if (in_place_elsewhere(k_out, k_out_stride, k, k_stride, num_tokens)) return PKVD_INVALID_ARG;
   }
   RopeArgs a;
   rope_common(&a, rope, dtype, num_q_heads, num_kv_heads, head_dim);
@@ -286,7 +294,8 @@ pkvd_status pkvd_rope_store_paged(void* q_out, int64_t q_out_stride, const void*
   if (num_seqs == 0) return PKVD_OK;
   if (!block_tables || !context_lens || max_blocks_per_seq <= 0) return PKVD_INVALID_ARG;
   RopeArgs a;
-  s = rope_store_args(&a, q_out, q_out_stride, q, q_stride, k, k_stride, v, v_stride, num_q_heads, rope, cache);
+  s = rope_store_args(&a, q_out, q_out_stride, q, q_stride, k, k_stride, v, v_stride, num_q_heads, num_seqs, rope,
+                      cache);
   if (s != PKVD_OK) return s;
   a.tables = block_tables;
   a.max_blocks = max_blocks_per_seq;
@@ -311,7 +320,8 @@ pkvd_status pkvd_rope_store_prefill(void* q_out, int64_t q_out_stride, const voi
   if (!cu_seqlens_q || !cu_seqlens_k) return PKVD_INVALID_ARG;
   if (num_seqs > 0 && (!block_tables || max_blocks_per_seq <= 0)) return PKVD_INVALID_ARG;
   RopeArgs a;
-  s = rope_store_args(&a, q_out, q_out_stride, q, q_stride, k, k_stride, v, v_stride, num_q_heads, rope, cache);
+  s = rope_store_args(&a, q_out, q_out_stride, q, q_stride, k, k_stride, v, v_stride, num_q_heads, total_q, rope,
+                      cache);
   if (s != PKVD_OK) return s;
   a.tables = block_tables;
   a.max_blocks = max_blocks_per_seq;

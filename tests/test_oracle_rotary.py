@@ -147,3 +147,18 @@ def test_rope_store_host_checks(L):
     assert prefill(ck=None) == 1
     assert prefill(q=P[1] + 2) == 3
     assert prefill(desc=_desc(-2)) == 1
+
+
+def test_rows_turned_in_place_keep_their_stride(L):
+    def rope(q=P[1], qs=512, qo=P[2], qos=512, k=P[3], ks=256, ko=P[4], kos=256, T=4):
+        return L.pkvd_rope(qo, qos, q, qs, ko, kos, k, ks, 2, T, 4, 2, 128, P[5], _desc(), None)
+    assert rope(qo=P[1], qos=520) == 1
+    assert rope(ko=P[3], kos=264) == 1
+    def paged(qos, n):
+        return L.pkvd_rope_store_paged(P[1], qos, P[1], 48 * 128, P[3], 1024, P[4], 1024, 48, P[5], 8, P[6], n,
+                                       _desc(128), None, ctypes.byref(_cache()), None, None)
+    assert paged(48 * 128 + 8, 2) == 1
+    def prefill(qos, T):
+        return L.pkvd_rope_store_prefill(P[1], qos, P[1], 48 * 128, P[3], 1024, P[4], 1024, 48, P[5], 8, P[6], P[7], 2, T,
+                                         _desc(128), None, ctypes.byref(_cache()), None, None)
+    assert prefill(48 * 128 + 8, 9) == 1
