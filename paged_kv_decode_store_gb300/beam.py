@@ -51,15 +51,19 @@ def beam_search_step(logits: torch.Tensor, scores: torch.Tensor, keep: int, fini
             shape = (n, max(keep, 0))
             tokens = torch.empty(shape, dtype=torch.int32, device=dev)
             out = torch.empty(shape, dtype=torch.float32, device=dev), torch.empty_like(tokens), tokens
+            pointers = [t.data_ptr() for t in out]
+        else:
+            shape = (n, keep)
+            pointers = [array(out[0], "out scores", torch.float32, dev, shape),
+                        array(out[1], "out parents", torch.int32, dev, shape),
+                        array(out[2], "out tokens", torch.int32, dev, shape)]
         if workspace is None:
             workspace = torch.empty(max(beam_workspace_bytes(n, b, vocab, logits.dtype, keep), 16),
                                     dtype=torch.uint8, device=dev)
         elif workspace.device != dev or not workspace.is_contiguous():
             raise ValueError(f"workspace must be a contiguous tensor on {dev}")
         check(_capi.lib().pkvd_beam_search_step(
-            array(out[0], "out scores", torch.float32, dev, (n, keep)),
-            array(out[1], "out parents", torch.int32, dev, (n, keep)),
-            array(out[2], "out tokens", torch.int32, dev, (n, keep)), logits.data_ptr(), code, n, b, vocab, row_stride,
+            *pointers, logits.data_ptr(), code, n, b, vocab, row_stride,
             array(scores, "scores", torch.float32, dev, (n, b)), ended, eos_id, keep, workspace.data_ptr(),
             workspace.numel() * workspace.element_size(), current_stream(dev)))
     return tuple(out)
