@@ -119,6 +119,7 @@ struct ModParams {
   int total_q, hq, hkv, group, tile_tokens;
   uint32_t q_box;        // bytes of one 64-column box of a Q tile
   int pairs;             // Q-tile pairs per (sequence, KV head)
+  int pair;              // tiles of a pair: 2, or 1 (only tile 1)
   int num_seqs, items;
   float scale_log2;
   int window;
@@ -162,7 +163,7 @@ __device__ __forceinline__ Item item_at(const ModParams& p, const uint8_t* order
     if (zpair == 0 && t.hk == 0) flag_error(p.err, PKVD_ERR_CONTEXT);
     return t;
   }
-  if (zpair == 0 && t.hk == 0 && qlen > 2 * p.pairs * p.tile_tokens)
+  if (zpair == 0 && t.hk == 0 && qlen > p.pair * p.pairs * p.tile_tokens)
     flag_error(p.err, PKVD_ERR_CONTEXT);   // longer than max_seqlen_q: the earliest tokens are not computed
   t.q0 = q0;
   t.cached = klen - qlen;
@@ -170,7 +171,7 @@ __device__ __forceinline__ Item item_at(const ModParams& p, const uint8_t* order
   int lo_g[2], hi_g[2];
 #pragma unroll
   for (int g = 0; g < 2; ++g) {
-    t.te[g] = qlen - (2 * zpair + 1 - g) * p.tile_tokens;
+    t.te[g] = p.pair == 2 ? qlen - (2 * zpair + 1 - g) * p.tile_tokens : g ? qlen - zpair * p.tile_tokens : 0;
     t.tb[g] = max(0, t.te[g] - p.tile_tokens);
     lo_g[g] = window_first(t.cached + t.tb[g] + 1, p.window);
     hi_g[g] = max(t.cached + t.te[g] - 1, t.prefix - 1);
@@ -1091,7 +1092,15 @@ cudaError_t launch_prefill_mod(const PrefillArgs& a, cudaStream_t stream) {
   prm.group = G;
   prm.q_box = 128u * (uint32_t)(G * prm.tile_tokens);
   const int tiles = (a.max_seqlen_q + prm.tile_tokens - 1) / prm.tile_tokens;
-  prm.pairs = (tiles + 1) / 2;
+  // With an SM for every Q tile, each has one: a chain of K tiles is shorter
+  // with half the softmax warps on it (one prompt of 734 tokens, 12 + 2 heads of
+  // 128: 21 instead of 27 us; four chunks of 14 to 116 tokens after 1467, 8 + 4
+  // heads of 64: 27 instead of 35).  Otherwise two share a CTA, so that one's
+  // products run beside the other's softmax.
+  const int sms = device_sm_count();
+  if (sms <= 0) return cudaErrorInvalidDevice;
+  prm.pair = (int64_t)tiles * c.num_kv_heads * a.num_seqs <= sms ? 1 : 2;
+  prm.pairs = (tiles + prm.pair - 1) / prm.pair;
   prm.num_seqs = a.num_seqs;
   const int64_t items = (int64_t)prm.pairs * c.num_kv_heads * a.num_seqs;
   if (items > 0x7fffffff) return cudaErrorInvalidConfiguration;

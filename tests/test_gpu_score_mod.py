@@ -268,3 +268,36 @@ def test_prefill_prefix_far_before_the_window(prefix, path):
             want, bound = oracle.scores.attend(q[t, h].double().numpy(), k, v, p, scale, 9.0, float(slopes[h]), window,
                                                (prefix, 64)[i], **tol)
             assert np.all(np.abs(got[t, h] - want) <= bound), (t, h)
+
+
+@pytest.mark.parametrize("mod", [(4.0, None, 0, False), (0.0, "geometric", 0, True), (3.0, "mixed", 100, True)],
+                         ids=["cap", "bias-prefix", "all"])
+@pytest.mark.parametrize("case", [("f16", 16, 16, 64, 64), ("bf16", 64, 8, 64, 16), ("bf16", 48, 8, 128, 32),
+                                  ("f16", 20, 10, 128, 16)], ids=lambda c: "-".join(map(str, c)))
+def test_prefill_of_more_tiles_than_sms(case, mod):
+    """Batches whose Q tiles outnumber the SMs several times: pairs of tiles, CTAs that take over further items."""
+    pk = require_gpu()
+    dt, hq, hkv, d, bs = case
+    cap, kind, window, open_prefix = mod
+    dt = DT[dt]
+    qlen = [300, 129, 1, 0, 200, 257, 33, 280, 64, 128]
+    klen = [n + c for n, c in zip(qlen, [0, 50, 700, 9, 0, 130, 400, 300, 64, 0])]
+    kc, vc, tables, rows = cache_of(klen, hkv, d, bs, dt, 11)
+    q = (2 * torch.randn(sum(qlen), hq, d, generator=torch.Generator().manual_seed(12))).to(dt)
+    cq, ck = (torch.tensor(np.concatenate([[0], np.cumsum(x)]), dtype=torch.int32, device=DEV) for x in (qlen, klen))
+    dev_slopes, slopes = slopes_for(hq, kind)
+    prefix = [(97 * i) % (n + 40) if open_prefix else 0 for i, n in enumerate(klen)]
+    pl = torch.tensor(prefix, dtype=torch.int32, device=DEV) if open_prefix else None
+    err = torch.zeros(1, dtype=torch.int32, device=DEV)
+    out = pk.prefill_attention(q.to(DEV), kc, vc, tables, cq, ck, max(qlen), d ** -0.5, window=window, err=err, path=3,
+                               softcap=cap, alibi_slopes=dev_slopes, prefix_lens=pl)
+    assert err.item() == 0
+    got, tol, t0 = out.double().cpu().numpy(), tolerances(dt, True), 0
+    for i, n in enumerate(klen):
+        for j in sorted({0, qlen[i] - 1, *range(i, qlen[i], 23)} if qlen[i] else ()):
+            for h in ((j + i) % hq, hq - 1 - j % hq):
+                k, v = (x[:, h // (hq // hkv)] for x in rows[i])
+                want, bound = oracle.scores.attend(q[t0 + j, h].double().numpy(), k, v, n - qlen[i] + j, d ** -0.5, cap,
+                                                   slopes[h], window, min(prefix[i], n), **tol)
+                assert np.all(np.abs(got[t0 + j, h] - want) <= bound), (i, j, h)
+        t0 += qlen[i]
