@@ -121,6 +121,7 @@ struct ModParams {
   int pairs;             // Q-tile pairs per (sequence, KV head)
   int pair;              // tiles of a pair: 2, or 1 (only tile 1)
   int num_seqs, items;
+  int waves;             // more items than SMs: they are put in order and taken over
   float scale_log2;
   int window;
   ScoreMod mod;
@@ -589,7 +590,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_mod_kernel(const __grid_c
     // to eight tiles); empty ones are left out, -1 ends the list.  A tile's rows are one box per 64 columns (G heads of
     // tile_tokens tokens), loaded once the tensor cores are done with the item
     // before.
-    uint8_t* order = p.num_seqs <= kSorted ? gbase + L::kOrder : nullptr;
+    uint8_t* order = p.waves && p.num_seqs <= kSorted ? gbase + L::kOrder : nullptr;
     if (order) {                                 // a sequence's place: how many are longer, or as long and before it
       for (int i = lane; i < p.num_seqs; i += 32) {
         const int len = p.cu_k[i + 1] - p.cu_k[i];
@@ -613,7 +614,9 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_mod_kernel(const __grid_c
         Item it;
         it.n = 0;
         while (ok && it.n == 0) {
-          if (!own) {
+          if (!own && !p.waves) {
+            next = -1;
+          } else if (!own) {
             fence_proxy_async_smem();            // the last answer has been read
             mbar_arrive_expect_tx(&bars[kClaim], 16);
             claim(base + L::kBar + kAnswer, &bars[kClaim]);
@@ -1105,6 +1108,7 @@ cudaError_t launch_prefill_mod(const PrefillArgs& a, cudaStream_t stream) {
   const int64_t items = (int64_t)prm.pairs * c.num_kv_heads * a.num_seqs;
   if (items > 0x7fffffff) return cudaErrorInvalidConfiguration;
   prm.items = (int)items;
+  prm.waves = items > sms;
   prm.scale_log2 = a.scale * 1.4426950408889634f;
   prm.window = a.window;
   prm.mod = a.mod;
