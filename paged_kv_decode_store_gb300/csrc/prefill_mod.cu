@@ -335,11 +335,11 @@ struct Visible {
   __device__ uint32_t bits(int word) const {
     return span_bits(lo - 32 * word, end - 32 * word) | span_bits(0, prefix - 32 * word);
   }
-  // Everything else becomes -inf, whatever it was (masked keys may hold
+  // Everything else becomes `x`, whatever it was (masked keys may hold
   // anything).  Most groups of eight columns are visible to the whole warp,
   // also in a tile that the mask cuts.
   template <int N>
-  __device__ void hide(float (&v)[N]) const {
+  __device__ void hide(float (&v)[N], float x) const {
 #pragma unroll
     for (int w = 0; w < N / 32; ++w) {
       const uint32_t m = bits(w), every = __reduce_and_sync(FULL_MASK, m);
@@ -347,7 +347,7 @@ struct Visible {
       for (int c8 = 0; c8 < 32; c8 += 8) {
         if (((every >> c8) & 0xffu) == 0xffu) continue;
 #pragma unroll
-        for (int c = c8; c < c8 + 8; ++c) v[32 * w + c] = ((m >> c) & 1u) ? v[32 * w + c] : -INFINITY;
+        for (int c = c8; c < c8 + 8; ++c) v[32 * w + c] = ((m >> c) & 1u) ? v[32 * w + c] : x;
       }
     }
   }
@@ -380,13 +380,14 @@ __device__ __forceinline__ void odd_poly2(float& v0, float& v1, const uint64_t (
 // falls linearly (no key after any of the warp's rows) then costs nothing per
 // key: eight multiples of the slope ride on the last product, the rest joins
 // the reference that the exponent subtracts anyway.  The same for the whole
-// warp: `whole`, every row sees every column, and `linear`.  `off`: the first column's
+// warp: `whole`, every row sees every column, and `linear`.  `range`: of the
+// polynomial, in squares of the raw score.  `off`: the first column's
 // key minus the row's position; `again` reads the raw scores once more (a
 // warp with a score past the polynomial's range: it has computed in vain).
 template <int MODE, int N, typename Again>
 __device__ __forceinline__ void modify(float (&v)[N], const ModParams& p, const Factors& f, const Visible& see,
-                                       bool whole, bool linear, float nslope, int off, float& base, float& step,
-                                       Again again) {
+                                       bool whole, bool linear, float range, float nslope, int off, float& base,
+                                       float& step, Again again) {
   const ScoreMod& m = p.mod;
   float k[8];
 #pragma unroll
@@ -394,11 +395,14 @@ __device__ __forceinline__ void modify(float (&v)[N], const ModParams& p, const 
   base = linear ? nslope * (float)-off : 0.f;
   step = linear ? -nslope * 8.f : 0.f;
   if (MODE & kCap) {
+    // the form is chosen by the scores that count: with what else lies in the
+    // stages and in other rows the last bit would change from run to run
+    if (!whole) see.hide(v, 0.f);
     float most = 0.f;                  // largest square: the polynomial's range
 #pragma unroll
     for (int c = 0; c < N; c += 2)
       odd_poly2<(MODE & kBias) != 0>(v[c], v[c + 1], f.poly, k[c & 7], k[(c & 7) + 1], most);
-    if (!__all_sync(FULL_MASK, most <= p.poly_range)) {
+    if (!__all_sync(FULL_MASK, most <= range)) {
       again(v);
 #pragma unroll
       for (int c = 0; c < N; ++c) v[c] = fmaf(tanh_fast(v[c] * m.cap_in), m.cap_out_log2, k[c & 7]);
@@ -417,7 +421,7 @@ __device__ __forceinline__ void modify(float (&v)[N], const ModParams& p, const 
 #pragma unroll
     for (int c = 0; c < N; ++c) v[c] = fmaf(nslope, fabsf(first + (float)c), v[c]);
   }
-  if (!whole) see.hide(v);
+  if (!whole) see.hide(v, -INFINITY);
 }
 
 template <typename T, int D, int MODE>
@@ -841,6 +845,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_mod_kernel(const __grid_c
       const int pr_min = __reduce_min_sync(FULL_MASK, pr), wr_max = __reduce_max_sync(FULL_MASK, wr);
       const int pr_max = __reduce_max_sync(FULL_MASK, pr), wr_min = __reduce_min_sync(FULL_MASK, wr);
       const float nslope = bias_slope(p.mod, it.hk * p.group + gi);
+      const float range = live ? p.poly_range : INFINITY;   // padding rows have no say
       float m_ref = (MODE & kBounded) ? 0.f : -INFINITY, l = 0.f;
       int kbase = uniform(it.tile(gf)) * kTcKeys + half * kCols;
       const int jump = uniform(it.n_main) - gf, gap = uniform(it.gap) * kTcKeys;
@@ -867,7 +872,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_mod_kernel(const __grid_c
               };
               read(v);
               const bool whole = (k0 + 31 <= pr_min && k0 >= wr_max) || k0 + 32 <= prefix;
-              modify<MODE>(v, p, f, Visible{wr - k0, pr + 1 - k0, prefix - k0}, whole, false, 0.f, 0, bias, step, read);
+              modify<MODE>(v, p, f, Visible{wr - k0, pr + 1 - k0, prefix - k0}, whole, false, range, 0.f, 0, bias, step, read);
 #pragma unroll
               for (int c = 0; c < 32; c += 4) {
                 const float e0 = tc_ex2(v[c]), e1 = tc_ex2(v[c + 1]), e2 = tc_ex2(v[c + 2]), e3 = tc_ex2(v[c + 3]);
@@ -899,8 +904,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_mod_kernel(const __grid_c
           float bias, step;
           const bool before = kbase + kCols - 1 <= pr_min;
           const bool whole = (before && kbase >= wr_max) || kbase + kCols <= prefix;
-          modify<MODE>(v, p, f, Visible{wr - kbase, pr + 1 - kbase, prefix - kbase}, whole, (MODE & kBias) && before, nslope,
-                       kbase - pr, bias, step, read);
+          modify<MODE>(v, p, f, Visible{wr - kbase, pr + 1 - kbase, prefix - kbase}, whole, (MODE & kBias) && before, range,
+                       nslope, kbase - pr, bias, step, read);
           // head_dim 64: the next S may overwrite these columns once nobody reads them again
           if (kSepP) {
             tc_fence_before();

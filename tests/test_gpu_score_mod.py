@@ -301,3 +301,35 @@ def test_prefill_of_more_tiles_than_sms(case, mod):
                                                    slopes[h], window, min(prefix[i], n), **tol)
                 assert np.all(np.abs(got[t0 + j, h] - want) <= bound), (i, j, h)
         t0 += qlen[i]
+
+
+def test_calls_on_two_streams_at_once():
+    """Prefill and decode calls of different shapes on two streams, launched in turn: each result as when it runs alone."""
+    pk = require_gpu()
+    calls = []
+    for seed, (dt, hq, hkv, d, bs, mod) in enumerate([
+            ("bf16", 48, 8, 128, 16, dict(softcap=5.0)), ("f16", 32, 8, 64, 64, dict(prefix=True, alibi=True)),
+            ("bf16", 64, 8, 64, 16, dict(softcap=9.0, alibi=True)), ("f16", 16, 8, 128, 32, dict(alibi=True))]):
+        dt = DT[dt]
+        qlen, klen = [200, 150, 77, 1], [900, 150, 300, 513]
+        kc, vc, tables, _ = cache_of(klen, hkv, d, bs, dt, 20 + seed)
+        q = torch.randn(sum(qlen), hq, d, generator=torch.Generator().manual_seed(seed)).to(dt).to(DEV)
+        cq, ck = (torch.tensor(np.concatenate([[0], np.cumsum(x)]), dtype=torch.int32, device=DEV) for x in (qlen, klen))
+        ctx = torch.tensor(klen, dtype=torch.int32, device=DEV)
+        kw = dict(softcap=mod.get("softcap", 0.0), alibi_slopes=slopes_for(hq, "geometric")[0] if mod.get("alibi") else None)
+        pl = torch.tensor([64, 0, 200, 513], dtype=torch.int32, device=DEV) if mod.get("prefix") else None
+        calls.append(lambda s, a=(kc, vc, tables), q=q, cq=cq, ck=ck, kw=kw, pl=pl, d=d, m=max(qlen): pk.prefill_attention(
+            q, *a, cq, ck, m, d ** -0.5, stream=s, prefix_lens=pl, **kw))
+        calls.append(lambda s, a=(kc, vc, tables), q=q[:4].contiguous(), ctx=ctx, kw=kw, d=d: pk.paged_decode_attention(
+            q, *a, ctx, 1000, d ** -0.5, stream=s, **dict(kw, softcap=kw["softcap"] or 3.0)))
+    alone = [c(None).clone() for c in calls]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    got = []
+    for turn in range(6):
+        for i in range(len(calls)):
+            j = (i + turn) % len(calls)
+            got.append((j, calls[j](streams[(i + turn // 3) % 2])))
+    torch.cuda.synchronize()
+    for j, out in got:
+        assert torch.equal(out, alone[j]), j
