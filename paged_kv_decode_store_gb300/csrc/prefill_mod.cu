@@ -272,6 +272,14 @@ __device__ __forceinline__ bool wait_bounded(uint64_t* bar, uint32_t parity) {
     if (mbar_try_wait(bar, parity)) return true;
   return mbar_wait_bounded(bar, parity);
 }
+// The same for the two waits that last as long as an item does: twenty times
+// the limit (ten seconds), some 10^9 keys.
+__device__ __forceinline__ bool wait_item(uint64_t* bar, uint32_t parity) {
+#pragma unroll 1
+  for (int i = 0; i < 20; ++i)
+    if (wait_bounded(bar, parity)) return true;
+  return false;
+}
 
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
   asm volatile(
@@ -613,7 +621,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_mod_kernel(const __grid_c
       int made = 0, asked = 0, used[2] = {0, 0}, next = blockIdx.x;
       auto make = [&] {                          // the next item into the ring
         const int slot = made % kItemRing;
-        if (made > 0) ok = wait_bounded(&bars[kNear], (made - 1) & 1);
+        if (made > 0) ok = wait_item(&bars[kNear], (made - 1) & 1);
         if (made >= kItemRing) ok = ok && wait_bounded(&bars[kItemFree + slot], ((made / kItemRing) - 1) & 1);
         Item it;
         it.n = 0;
@@ -826,7 +834,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_mod_kernel(const __grid_c
     };
     int n = 0;                                   // this tile's K tiles so far, of all items
     for (int r = 0; ok; ++r) {
-      wait(kItemFull + r % kItemRing, (r / kItemRing) & 1);
+      ok = __all_sync(FULL_MASK, wait_item(&bars[kItemFull + r % kItemRing], (r / kItemRing) & 1));
       if (!ok) break;
       const Item& it = ring_items[r % kItemRing];
       if (it.n < 0) break;
