@@ -333,3 +333,61 @@ def test_calls_on_two_streams_at_once():
     torch.cuda.synchronize()
     for j, out in got:
         assert torch.equal(out, alone[j]), j
+
+
+def test_blocks_past_32_bit_offsets():
+    """The same rows in a small pool and at the end of one of 2^31 elements and more: stores and both attentions alike."""
+    pk = require_gpu()
+    hq, hkv, d, bs, dt = 16, 8, 128, 16, torch.bfloat16
+    nb = 2 ** 31 // (bs * hkv * d) + 64
+    kc, vc, tables, _ = cache_of([300, 77], hkv, d, bs, dt, 31)
+    big = [torch.empty(nb, bs, hkv, d, dtype=dt, device=DEV) for _ in range(2)]
+    for small, b in zip((kc, vc), big):
+        b[nb - small.shape[0]:] = small
+    far = torch.where(tables >= 0, tables + (nb - kc.shape[0]), tables)
+    g = torch.Generator().manual_seed(32)
+    q = torch.randn(90, hq, d, generator=g).to(dt).to(DEV)
+    k, v = (torch.randn(90, hkv, d, generator=g).to(dt).to(DEV) for _ in range(2))
+    cq, ck = (torch.tensor(x, dtype=torch.int32, device=DEV) for x in ([0, 60, 90], [0, 300, 377]))
+    ctx = torch.tensor([300, 77], dtype=torch.int32, device=DEV)
+    inv, _ = pk.rope_inv_freq(d, device=DEV)
+    s = slopes_for(hq, "geometric")[0]
+    got = []
+    for kk, vv, t in ((kc, vc, tables), (*big, far)):
+        a = pk.rope_store_prefill(q, k, v, t, cq, ck, inv, kk, vv)
+        b = pk.rope_store_paged(q[:2].contiguous(), k[:2].contiguous(), v[:2].contiguous(), t, ctx, inv, kk, vv)
+        got.append([a, b, *(pk.prefill_attention(a, kk, vv, t, cq, ck, 60, 0.1, path=path, softcap=4.0, alibi_slopes=s)
+                            for path in (1, 2, 3)),
+                    *(pk.paged_decode_attention(b, kk, vv, t, ctx, 300, 0.1, path=path, softcap=4.0, alibi_slopes=s)
+                      for path in (1, 2))])
+    for small, large in zip(*got):
+        assert torch.equal(small, large)
+    assert torch.equal(kc[tables[0, 0].item()], big[0][far[0, 0].item()])
+    assert torch.equal(vc[tables[1, 4].item()][:13], big[1][far[1, 4].item()][:13])     # the row stored last among them
+
+
+@pytest.mark.parametrize("mod", [(3.0, None, 0, 0), (0.0, 2.0 ** -12, 0, 70000), (20.0, 2.0 ** -14, 90000, 500)],
+                         ids=["cap", "bias", "all"])
+def test_a_long_context(mod):
+    """150,000 keys: the chain of K tiles, a prefix and a window of thousands of tiles, and decode over the same rows."""
+    pk = require_gpu()
+    cap, slope, window, prefix = mod
+    n, qn, hq, d, bs, dt = 150001, 40, 2, 64, 64, torch.float16
+    kc, vc, tables, rows = cache_of([n], 1, d, bs, dt, 41, spare=0)
+    q = (3 * torch.randn(qn, hq, d, generator=torch.Generator().manual_seed(42))).to(dt)
+    cq, ck = (torch.tensor(x, dtype=torch.int32, device=DEV) for x in ([0, qn], [0, n]))
+    slopes = None if slope is None else torch.tensor([slope, 2 * slope], device=DEV)
+    pl = torch.tensor([prefix], dtype=torch.int32, device=DEV) if prefix else None
+    out = pk.prefill_attention(q.to(DEV), kc, vc, tables, cq, ck, qn, 0.125, window=window, path=3, softcap=cap,
+                               alibi_slopes=slopes, prefix_lens=pl).double().cpu().numpy()
+    one = pk.paged_decode_attention(q[-1:].to(DEV), kc, vc, tables, ck[1:], n, 0.125, window=window, softcap=cap or 1e4,
+                                    alibi_slopes=slopes).double().cpu().numpy()
+    k, v = (x[:, 0] for x in rows[0])
+    tol = tolerances(dt, True)
+    for h in range(hq):
+        sl = (slope or 0.0) * (h + 1)
+        for t in (0, 17, qn - 1):
+            want, bound = oracle.scores.attend(q[t, h].double().numpy(), k, v, n - qn + t, 0.125, cap, sl, window, prefix, **tol)
+            assert np.all(np.abs(out[t, h] - want) <= bound), (h, t)
+        want, bound = oracle.scores.attend(q[-1, h].double().numpy(), k, v, n - 1, 0.125, cap or 1e4, sl, window, **tolerances(dt, False))
+        assert np.all(np.abs(one[0, h] - want) <= bound), h
