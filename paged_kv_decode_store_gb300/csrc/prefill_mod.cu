@@ -935,10 +935,15 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_mod_kernel(const __grid_c
           exchange();
           if (!ok) break;
           const float mt = fmaxf(__bfloat162float(mine), __bfloat162float(x[(half ^ 1) * 32 + lane]));
-          const bool rebase = mt > m_ref + kRebase;
+          // f16 weights are normal down to 2^-14: with the reference 7 below the
+          // largest score they have seven bits more before they lose any (2^15 at
+          // most, as the reference lets scores grow by 2^8), and many small ones
+          // beside a large one add up to what they are
+          constexpr float kLift = std::is_same<T, __half>::value ? 7.f : 0.f;
+          const bool rebase = mt > m_ref + (kLift + kRebase);
           const bool scale_o = rebase && m_ref != -INFINITY;
-          const float alpha = scale_o ? tc_ex2(m_ref - mt) : 1.f;
-          if (rebase) m_ref = mt;
+          const float alpha = scale_o ? tc_ex2(m_ref - (mt - kLift)) : 1.f;
+          if (rebase) m_ref = mt - kLift;
           const float mu = m_ref == -INFINITY ? 0.f : m_ref;
           uint32_t pk[kCols / 2];
           float s0 = 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f, shift0 = bias - mu, shift1 = shift0;

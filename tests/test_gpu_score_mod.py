@@ -391,3 +391,28 @@ def test_a_long_context(mod):
             assert np.all(np.abs(out[t, h] - want) <= bound), (h, t)
         want, bound = oracle.scores.attend(q[-1, h].double().numpy(), k, v, n - 1, 0.125, cap or 1e4, sl, window, **tolerances(dt, False))
         assert np.all(np.abs(one[0, h] - want) <= bound), h
+
+
+@pytest.mark.parametrize("large", [0, 30000, 59990])
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+def test_many_small_weights_beside_a_large_one(dt, large):
+    """One key e^11 above 60,000 equal ones, which together outweigh it: each of their weights is 2^-16 of the largest."""
+    pk = require_gpu()
+    n, d, bs, dt = 60000, 64, 256, DT[dt]
+    kc, vc, tables, rows = cache_of([n], 1, d, bs, dt, 51, spare=0)
+    k = torch.zeros(n, d, dtype=dt)
+    k[large, 0] = 22.0
+    v = (1.0 + 0.25 * torch.randn(n, 1, d, generator=torch.Generator().manual_seed(52))).to(dt)
+    for b in range(-(-n // bs)):
+        m = min(bs, n - b * bs)
+        kc[tables[0, b].item(), :m, 0], vc[tables[0, b].item(), :m] = k[b * bs:b * bs + m].to(DEV), v[b * bs:b * bs + m].to(DEV)
+    q = torch.zeros(9, 1, d, dtype=dt)
+    q[:, 0, 0] = 4.0
+    cq, ck = (torch.tensor(x, dtype=torch.int32, device=DEV) for x in ([0, 9], [0, n]))
+    for cap in (0.0, 100.0):
+        out = pk.prefill_attention(q.to(DEV), kc, vc, tables, cq, ck, 9, 0.125, path=3, softcap=cap,
+                                   alibi_slopes=torch.zeros(1, device=DEV)).double().cpu().numpy()
+        for t in (0, 8):
+            want, bound = oracle.scores.attend(q[t, 0].double().numpy(), k.double().numpy(), v[:, 0].double().numpy(),
+                                               n - 9 + t, 0.125, cap, **tolerances(dt, True))
+            assert np.all(np.abs(out[t, 0] - want) <= bound), (cap, t, np.abs(out[t, 0] - want).max(), bound.max())
