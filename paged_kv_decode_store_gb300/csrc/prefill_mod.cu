@@ -23,7 +23,8 @@
 //   one reads its scores again and takes the exponential form.
 // * bf16 weights have fp32's range: with a cap and no slopes every score lies
 //   in [-cap, cap], and while 2^(cap log2 e) is far inside that range no
-//   reference is needed at all -- no maximum, no exchange, no rescaling.
+//   reference is needed at all -- no maximum, no exchange, no rescaling (169
+//   instead of 132 us for 8 capped prompts of 1024 tokens with one).
 //
 // Measured: 8 prompts of 1024 tokens, 48 + 8 heads of 128, bf16, capped: 131 us
 // (788 TFLOP/s of visible pairs; 281 with the plain kernel's structure).  Four
@@ -121,13 +122,14 @@ struct ModParams {
   int pairs;             // Q-tile pairs per (sequence, KV head)
   int pair;              // tiles of a pair: 2, or 1 (only tile 1)
   int num_seqs, items;
-  int waves;             // more items than SMs: they are put in order and taken over
+  int waves;             // more items than SMs: they are put in order (418 us; 424 as they come) and taken
+                         // over; fewer: neither (10 to 12 us calls 1 to 2 us shorter)
   float scale_log2;
   int window;
   ScoreMod mod;
   // score of a raw product s as s * polynomial in s^2, for s^2 <= poly_range (-1: not used)
   float poly[4], poly_range;
-  int wide_out;          // out is 32-byte aligned
+  int wide_out;          // out is 32-byte aligned: stores of 32 bytes (132 us; 142 in 16)
   int32_t* err;
 };
 
@@ -439,7 +441,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_mod_kernel(const __grid_c
   constexpr bool kSepP = D == 64;
   // head_dim 128 without a reference: nothing ties the two halves of a tile's
   // keys together, so each has its own S, P and PV and the products of one run
-  // beside the softmax of the other.
+  // beside the softmax of the other (132 us; 142 together).
   constexpr bool kSplit = D == 128 && (MODE & kBounded);
   // whole swizzle atoms; an address known when linked keeps the barriers' out
   // of the loops (rounded up at run time: 475 instead of 468 us for four chunks
