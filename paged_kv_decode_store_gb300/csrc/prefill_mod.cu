@@ -26,8 +26,8 @@
 //   reference is needed at all -- no maximum, no exchange, no rescaling (169
 //   instead of 132 us for 8 capped prompts of 1024 tokens with one).
 //
-// Measured: 8 prompts of 1024 tokens, 48 + 8 heads of 128, bf16, capped: 131 us
-// (788 TFLOP/s of visible pairs; 281 with the plain kernel's structure).  Four
+// Measured: 8 prompts of 1024 tokens, 48 + 8 heads of 128, bf16, capped: 132 us
+// (782 TFLOP/s of visible pairs; 281 with the plain kernel's structure).  Four
 // chunks of about 1000 tokens after up to 7168, 64 + 8 heads of 64, f16, bias
 // and prefix: 418 us (918 TFLOP/s; 709).  Bound: not the tensor pipe (active
 // 39 % of the time; leaving out nearly all products saved 1 to 2 %).  At
