@@ -12,7 +12,8 @@ With every output comes a bound on how far fp32 arithmetic may be from it,
 counted from the roundings:
     weights   u_p each (half a step of the type they are rounded to, 0 for fp32)
     scores    an error of e in s_j is a relative error of e in its weight:
-              the dot product (D + 2 roundings of 2^-24 of sum |q||k| scale),
+              the dot product (D + 2 roundings of 2^-24 of sum |q||k| scale;
+              `dot_rounds` of them where a test's products and sums are exact),
               the cap (`cap_error` of the value), the bias and the exponent's
               argument (4 roundings of 2^-24 of the largest |s|), 2^-22 of the
               exponential
@@ -32,7 +33,8 @@ def visible_keys(p: int, klen: int, window: int = 0, prefix: int = 0) -> np.ndar
 
 
 def attend(q, K, V, p: int, scale: float, cap: float = 0.0, slope: float = 0.0, window: int = 0, prefix: int = 0,
-           u_p: float = 0.0, eps: float = 2.0 ** -23, tiny: float = 0.0, cap_error: float = 7e-6):
+           u_p: float = 0.0, eps: float = 2.0 ** -23, tiny: float = 0.0, cap_error: float = 7e-6,
+           dot_rounds: int | None = None):
     """(output [D], bound [D]) of one query over its sequence's keys K [klen, D]."""
     seen = visible_keys(p, K.shape[0], window, prefix)
     j = np.nonzero(seen)[0]
@@ -41,7 +43,8 @@ def attend(q, K, V, p: int, scale: float, cap: float = 0.0, slope: float = 0.0, 
         return z, z
     k, v = K[j].astype(np.float64), V[j].astype(np.float64)
     s = scale * (k @ q)
-    dot = abs(scale) * (np.abs(k) @ np.abs(q)) * (q.shape[0] + 2) * 2.0 ** -24
+    dot = abs(scale) * (np.abs(k) @ np.abs(q)) * 2.0 ** -24
+    dot *= q.shape[0] + 2 if dot_rounds is None else dot_rounds
     if cap > 0:
         s = cap * np.tanh(s / cap)
         dot = dot + np.abs(s) * cap_error

@@ -82,10 +82,10 @@ struct Layout {
   static constexpr uint32_t kK = kQ + 2 * kHalves * kHalf;
   static constexpr uint32_t kV = kK + kKStages * kHalves * kHalf;
   static constexpr uint32_t kBar = kV + kVStages * kHalves * kHalf;
-  static constexpr uint32_t kX = kBar + 512;                           // exchange: 512 bytes a tile and buffer
+  static constexpr uint32_t kX = kBar + 512;                           // exchange: 1024 bytes a tile and buffer
   static constexpr int kXBufs = D == 64 ? 2 : 1;
   // at least 120 KB so that one CTA (which holds all TMEM) is resident per SM
-  static constexpr uint32_t kItems = kX + kXBufs * 1024;               // ring of items
+  static constexpr uint32_t kItems = kX + kXBufs * 2048;               // ring of items
   static constexpr uint32_t kOrder = kItems + 384;                     // sequences, longest first
   static constexpr uint32_t kGaveUp = kOrder + 64;                     // one word a pair of softmax warps
   static constexpr uint32_t kEnd = kGaveUp + 32;
@@ -813,9 +813,9 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_mod_kernel(const __grid_c
     const uint32_t s_addr = tmem + lane_base + g * kTcKeys + half * kCols;
     const uint32_t p_addr = kSepP ? tmem + lane_base + kColP64 + g * 64 + half * 32 : s_addr;
     const uint32_t o_addr = tmem + lane_base + kColO + g * D + half * (D / 2);
-    // what a row's two threads tell each other: 128 bytes a quarter of the rows
-    uint8_t* xch = gbase + L::kX + g * 512 + quarter * 128;
-    float* xsum = reinterpret_cast<float*>(xch);
+    // what a row's two threads tell each other: 256 bytes a quarter of the rows
+    float* xch = reinterpret_cast<float*>(gbase + L::kX + g * 1024 + quarter * 256);
+    float* xsum = xch;
     Factors f;
     f.scale = both(p.scale_log2);
 #pragma unroll
@@ -929,14 +929,14 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_mod_kernel(const __grid_c
                           tc_max3(v[c + 5], v[c + 6], v[c + 7]));
           }
           if (MODE & kBias) top += bias + (kCols / 8 - 1) * step;
-          // the two halves of a row agree on a reference: any common one does,
-          // so 16 bits (rounded up) are enough
-          __nv_bfloat16* x = reinterpret_cast<__nv_bfloat16*>(xch + (kSepP ? (n & 1) * 1024 : 0));
-          const __nv_bfloat16 mine = __float2bfloat16_ru(top);
-          x[half * 32 + lane] = mine;
+          // the two halves of a row agree on a reference, the larger maximum to
+          // all its bits: rounded up to 16 of them it would lie 2^-8 of a score
+          // above it, which at thousands is more than the weights' exponents have
+          float* x = xch + (kSepP ? (n & 1) * 512 : 0);
+          x[half * 32 + lane] = top;
           exchange();
           if (!ok) break;
-          const float mt = fmaxf(__bfloat162float(mine), __bfloat162float(x[(half ^ 1) * 32 + lane]));
+          const float mt = fmaxf(top, x[(half ^ 1) * 32 + lane]);
           // f16 weights are normal down to 2^-14: with the reference 7 below the
           // largest score they have seven bits more before they lose any (2^15 at
           // most, as the reference lets scores grow by 2^8), and many small ones

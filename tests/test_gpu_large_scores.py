@@ -1,0 +1,116 @@
+"""Attention with modified scores where the scores themselves are large: rows
+all of whose scores lie thousands above or below zero, by their products or by
+a distance bias.  Only differences within a row count, so the weights are as
+those of any other row.  The products and their sums are whole numbers that
+fp32 holds exactly: what is left of the oracle's bound are the roundings of
+the score's own arithmetic."""
+import numpy as np
+import pytest
+import torch
+
+import oracle
+from gpu_helpers import require_gpu
+from test_gpu_score_mod import DEV, DT, tolerances
+
+pytestmark = pytest.mark.gpu
+
+
+def place(keys, values, bs, dt, seed):
+    """One sequence's rows [n, Hkv, D] in shuffled blocks: (K cache, V cache, table)."""
+    n, hkv, d = keys.shape
+    nb = -(-n // bs)
+    order = torch.randperm(nb + 2, generator=torch.Generator().manual_seed(seed))
+    kc, vc = (torch.full((nb + 2, bs, hkv, d), float("nan"), dtype=dt) for _ in range(2))
+    for b in range(nb):
+        m = min(bs, n - b * bs)
+        kc[order[b], :m], vc[order[b], :m] = keys[b * bs:b * bs + m], values[b * bs:b * bs + m]
+    return kc.to(DEV), vc.to(DEV), order[:nb].to(torch.int32).view(1, nb).to(DEV)
+
+
+def rows_around(offset, n, qn, hq, hkv, d, dt, seed):
+    """q [qn, hq, d], k, v [n, hkv, d] whose scores at scale 1/8 lie about `offset` (log2 units), some units apart."""
+    g = torch.Generator().manual_seed(seed)
+    raw = offset * 8 * np.log(2.0) / 128                # of the first component, eight bits of it
+    step = 2.0 ** max(np.floor(np.log2(abs(raw))) - 7, 0)
+    k = torch.zeros(n, hkv, d)
+    k[:, :, 0] = abs(round(raw / step)) * step
+    k[:, :, 1] = torch.randint(0, 25, (n, hkv), generator=g).float()
+    q = torch.zeros(qn, hq, d)
+    q[:, :, 0] = 128.0 if offset > 0 else -128.0
+    q[:, :, 1] = torch.randint(0, 3, (qn, hq), generator=g).float()
+    v = 1.0 + 0.25 * torch.randn(n, hkv, d, generator=g)
+    return q.to(dt), k.to(dt), v.to(dt)
+
+
+def check(got, q, k, v, positions, cap, slopes, prefix, tol):
+    G = q.shape[1] // k.shape[1]
+    qd, kd, vd = (x.double().numpy() for x in (q, k, v))
+    for t, p in enumerate(positions):
+        for h in range(q.shape[1]):
+            want, bound = oracle.scores.attend(qd[t, h], kd[:, h // G], vd[:, h // G], p, 0.125, cap, slopes[h],
+                                               prefix=prefix, dot_rounds=0, **tol)
+            off = np.abs(got[t, h] - want)
+            assert np.all(off <= bound), (t, h, float(off.max()), float(bound.max()))
+
+
+OFFSETS = [1e3, -1e3, 5e3, -5e3, 9e3, -9e3, 2e4, -2e4, 5e4, -5e4]
+MODES = {"prefix": (0.0, None), "cap": (2.0 ** 22, None), "bias": (0.0, 2.0 ** -6), "cap-bias": (2.0 ** 22, 2.0 ** -6)}
+
+
+@pytest.mark.parametrize("mode", MODES)
+@pytest.mark.parametrize("offset", OFFSETS)
+@pytest.mark.parametrize("dt,d", [("f16", 64), ("f16", 128), ("bf16", 64), ("bf16", 128)])
+def test_prefill_rows_of_large_scores(dt, d, offset, mode):
+    pk = require_gpu()
+    dt, (cap, slope) = DT[dt], MODES[mode]
+    n, qn, hq, hkv, bs = 300, 21, 4, 2, 16
+    q, k, v = rows_around(offset, n, qn, hq, hkv, d, dt, 1)
+    kc, vc, table = place(k, v, bs, dt, 2)
+    cq, ck = (torch.tensor(x, dtype=torch.int32, device=DEV) for x in ([0, qn], [0, n]))
+    slopes = np.zeros(hq) if slope is None else slope * np.arange(1, hq + 1)
+    prefix = 40 if mode == "prefix" else 0
+    for path in (1, 2, 3):
+        out = pk.prefill_attention(
+            q.to(DEV), kc, vc, table, cq, ck, qn, 0.125, path=path, softcap=cap,
+            alibi_slopes=None if slope is None else torch.tensor(slopes, dtype=torch.float32, device=DEV),
+            prefix_lens=torch.tensor([prefix], dtype=torch.int32, device=DEV) if prefix else None)
+        check(out.double().cpu().numpy(), q, k, v, range(n - qn, n), cap, slopes, prefix, tolerances(dt, path != 1))
+
+
+@pytest.mark.parametrize("cap", [0.0, 2.0 ** 22])
+@pytest.mark.parametrize("slope", [-1.0, 1.0])
+@pytest.mark.parametrize("dt,d", [("f16", 64), ("f16", 128), ("bf16", 64), ("bf16", 128)])
+def test_prefill_bias_over_a_long_row(dt, d, slope, cap):
+    """8,000 keys that a slope of -1 puts up to 11,500 log2 units above the row's own key."""
+    pk = require_gpu()
+    dt = DT[dt]
+    n, qn, hq, hkv, bs = 8000, 9, 2, 1, 64
+    g = torch.Generator().manual_seed(3)
+    q, k = torch.zeros(qn, hq, d), torch.zeros(n, hkv, d)
+    q[:, :, 0], k[:, :, 0] = 1.0, torch.randint(0, 33, (n, hkv), generator=g).float()
+    q, k = q.to(dt), k.to(dt)
+    v = (1.0 + 0.25 * torch.randn(n, hkv, d, generator=g)).to(dt)
+    kc, vc, table = place(k, v, bs, dt, 4)
+    cq, ck = (torch.tensor(x, dtype=torch.int32, device=DEV) for x in ([0, qn], [0, n]))
+    slopes = np.array([slope, slope / 4])
+    for path in (1, 2, 3):
+        out = pk.prefill_attention(q.to(DEV), kc, vc, table, cq, ck, qn, 0.125, path=path, softcap=cap,
+                                   alibi_slopes=torch.tensor(slopes, dtype=torch.float32, device=DEV))
+        check(out.double().cpu().numpy(), q, k, v, range(n - qn, n), cap, slopes, 0, tolerances(dt, path != 1))
+
+
+@pytest.mark.parametrize("mode", ["cap", "bias", "cap-bias"])
+@pytest.mark.parametrize("offset", OFFSETS)
+@pytest.mark.parametrize("dt,d", [("f16", 64), ("bf16", 128)])
+def test_decode_rows_of_large_scores(dt, d, offset, mode):
+    pk = require_gpu()
+    dt, (cap, slope) = DT[dt], MODES[mode]
+    n, hq, hkv, bs = 300, 16, 8, 16
+    q, k, v = rows_around(offset, n, 1, hq, hkv, d, dt, 5)
+    kc, vc, table = place(k, v, bs, dt, 6)
+    slopes = np.zeros(hq) if slope is None else slope * np.arange(1, hq + 1)
+    for path in (1, 2):
+        out = pk.paged_decode_attention(
+            q.to(DEV), kc, vc, table, torch.tensor([n], dtype=torch.int32, device=DEV), n, 0.125, path=path,
+            softcap=cap, alibi_slopes=None if slope is None else torch.tensor(slopes, dtype=torch.float32, device=DEV))
+        check(out.double().cpu().numpy(), q, k, v, [n - 1], cap, slopes, 0, tolerances(dt, path != 1))
