@@ -73,6 +73,11 @@ enum : int {
   kBounded = 4,        // every score is in [-cap, cap] and its exponential in range: no reference
 };
 constexpr float kRebase = 8.f;        // re-base the running maximum when it grows by > 2^8
+// Largest bias (log2 units) that is put together from parts: their sums round
+// at the bias's own size, several times and in the maximum otherwise than in
+// the weights, so from 2^22 on a weight would pass f16's range (and from 2^30
+// on all of a row could vanish).  Up to 2^14 it is at most a few 2^-10.
+constexpr float kLinear = 16384.f;
 
 template <int D>
 struct Layout {
@@ -389,7 +394,8 @@ __device__ __forceinline__ void odd_poly2(float& v0, float& v1, const uint64_t (
 // columns: column c's score is v[c] + base + (c / 8) * step.  A bias that
 // falls linearly (no key after any of the warp's rows) then costs nothing per
 // key: eight multiples of the slope ride on the last product, the rest joins
-// the reference that the exponent subtracts anyway.  The same for the whole
+// the reference that the exponent subtracts anyway.  A large bias (kLinear) is
+// added to each score in one rounding instead.  The same for the whole
 // warp: `whole`, every row sees every column, and `linear`.  `range`: of the
 // polynomial, in squares of the raw score.  `off`: the first column's
 // key minus the row's position; `again` reads the raw scores once more (a
@@ -855,6 +861,11 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_mod_kernel(const __grid_c
       const int pr_min = __reduce_min_sync(FULL_MASK, pr), wr_max = __reduce_max_sync(FULL_MASK, wr);
       const int pr_max = __reduce_max_sync(FULL_MASK, pr), wr_min = __reduce_min_sync(FULL_MASK, wr);
       const float nslope = bias_slope(p.mod, it.hk * p.group + gi);
+      int near = 0;                              // the first key whose bias may be put together from parts (kLinear)
+      if (MODE & kBias) {
+        const float steepest = __uint_as_float(__reduce_max_sync(FULL_MASK, __float_as_uint(fabsf(nslope))));
+        near = uniform(pr_max - (int)fminf(kLinear / steepest, 1e9f));
+      }
       const float range = live ? p.poly_range : INFINITY;   // padding rows have no say
       float m_ref = (MODE & kBounded) ? 0.f : -INFINITY, l = 0.f;
       int kbase = uniform(it.tile(gf)) * kTcKeys + half * kCols;
@@ -914,7 +925,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_mod_kernel(const __grid_c
           float bias, step;
           const bool before = kbase + kCols - 1 <= pr_min;
           const bool whole = (before && kbase >= wr_max) || kbase + kCols <= prefix;
-          modify<MODE>(v, p, f, Visible{wr - kbase, pr + 1 - kbase, prefix - kbase}, whole, (MODE & kBias) && before, range,
+          const bool linear = (MODE & kBias) && before && kbase >= near;
+          modify<MODE>(v, p, f, Visible{wr - kbase, pr + 1 - kbase, prefix - kbase}, whole, linear, range,
                        nslope, kbase - pr, bias, step, read);
           // head_dim 64: the next S may overwrite these columns once nobody reads them again
           if (kSepP) {

@@ -114,3 +114,68 @@ def test_decode_rows_of_large_scores(dt, d, offset, mode):
             q.to(DEV), kc, vc, table, torch.tensor([n], dtype=torch.int32, device=DEV), n, 0.125, path=path,
             softcap=cap, alibi_slopes=None if slope is None else torch.tensor(slopes, dtype=torch.float32, device=DEV))
         check(out.double().cpu().numpy(), q, k, v, [n - 1], cap, slopes, 0, tolerances(dt, path != 1))
+
+
+def steep_case(slope, n, qn, hq, hkv, d, dt, seed):
+    """Scores of a few units under a slope so steep that a row's nearest key (a negative slope: its farthest) has all
+    the weight."""
+    g = torch.Generator().manual_seed(seed)
+    q = torch.randn(qn, hq, d, generator=g).to(dt)
+    k = torch.randn(n, hkv, d, generator=g).to(dt)
+    v = (1.0 + 0.25 * torch.randn(n, hkv, d, generator=g)).to(dt)
+    return q, k, v, np.float32(slope) * np.ones(hq, dtype=np.float32)
+
+
+def check_steep(got, v, hq, positions, prefix, steep, tol):
+    """Each row is one key's values: its weight, rounded once, over a sum of that weight, rounded once more."""
+    G, vd = hq // v.shape[1], v.double().numpy()
+    for t, p in enumerate(positions):
+        j = p if steep > 0 else 0 if p >= max(prefix - 1 - p, 0) else prefix - 1
+        for h in range(hq):
+            want = vd[j, h // G]
+            bound = np.abs(want) * (tol["u_p"] + tol["eps"] / 2 + 2.0 ** -20)
+            assert np.all(np.abs(got[t, h] - want) <= bound), (t, h, float(np.abs(got[t, h] - want).max()))
+
+
+STEEP = [300.0, 1e4, 1e6, 1e9, 1e20]
+
+
+@pytest.mark.parametrize("slope", [s * x for x in STEEP for s in (1, -1)])
+@pytest.mark.parametrize("dt,d", [("f16", 64), ("f16", 128), ("bf16", 64), ("bf16", 128)])
+def test_prefill_of_steep_slopes(dt, d, slope):
+    prefill_of_steep_slopes(dt, d, slope)
+
+
+def prefill_of_steep_slopes(dt, d, slope):
+    pk = require_gpu()
+    dt = DT[dt]
+    n, qn, hq, hkv, bs = 300, 41, 4, 2, 16
+    q, k, v, slopes = steep_case(slope, n, qn, hq, hkv, d, dt, 7)
+    kc, vc, table = place(k, v, bs, dt, 8)
+    cq, ck = (torch.tensor(x, dtype=torch.int32, device=DEV) for x in ([0, qn], [0, n]))
+    for prefix in (0, 100):
+        for cap in (0.0, 50.0):
+            for path in (1, 2, 3):
+                out = pk.prefill_attention(q.to(DEV), kc, vc, table, cq, ck, qn, 0.125, path=path, softcap=cap,
+                                           alibi_slopes=torch.from_numpy(slopes).to(DEV),
+                                           prefix_lens=torch.tensor([prefix], dtype=torch.int32, device=DEV))
+                check_steep(out.double().cpu().numpy(), v, hq, range(n - qn, n), prefix, slope,
+                            tolerances(dt, path != 1))
+
+
+@pytest.mark.parametrize("slope", [s * x for x in STEEP for s in (1, -1)])
+@pytest.mark.parametrize("dt,d", [("f16", 64), ("bf16", 128), ("f32", 64)])
+def test_decode_of_steep_slopes(dt, d, slope):
+    decode_of_steep_slopes(dt, d, slope)
+
+
+def decode_of_steep_slopes(dt, d, slope):
+    pk = require_gpu()
+    dt = DT[dt]
+    n, hq, hkv, bs = 300, 16, 8, 16
+    q, k, v, slopes = steep_case(slope, n, 1, hq, hkv, d, dt, 9)
+    kc, vc, table = place(k, v, bs, dt, 10)
+    for path in (1,) if dt == torch.float32 else (1, 2):
+        out = pk.paged_decode_attention(q.to(DEV), kc, vc, table, torch.tensor([n], dtype=torch.int32, device=DEV), n,
+                                        0.125, path=path, alibi_slopes=torch.from_numpy(slopes).to(DEV))
+        check_steep(out.double().cpu().numpy(), v, hq, [n - 1], 0, slope, tolerances(dt, path != 1))
