@@ -954,7 +954,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_mod_kernel(const __grid_c
           // most, as the reference lets scores grow by 2^8), and many small ones
           // beside a large one add up to what they are
           constexpr float kLift = std::is_same<T, __half>::value ? 7.f : 0.f;
-          const bool rebase = mt > m_ref + (kLift + kRebase);
+          // (the difference is exact where it counts; the sum m_ref + 15 is not from 2^24 on)
+          const bool rebase = mt - m_ref > kLift + kRebase;
           const bool scale_o = rebase && m_ref != -INFINITY;
           const float alpha = scale_o ? tc_ex2(m_ref - (mt - kLift)) : 1.f;
           if (rebase) m_ref = mt - kLift;

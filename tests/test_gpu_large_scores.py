@@ -179,3 +179,27 @@ def decode_of_steep_slopes(dt, d, slope):
         out = pk.paged_decode_attention(q.to(DEV), kc, vc, table, torch.tensor([n], dtype=torch.int32, device=DEV), n,
                                         0.125, path=path, alibi_slopes=torch.from_numpy(slopes).to(DEV))
         check_steep(out.double().cpu().numpy(), v, hq, [n - 1], 0, slope, tolerances(dt, path != 1))
+
+
+@pytest.mark.parametrize("large", [2.0 ** 24, 2.0 ** 25, 2.0 ** 26, 2.0 ** 28, -2.0 ** 25])
+@pytest.mark.parametrize("d", [64, 128])
+def test_f16_weights_of_scores_without_a_fraction(d, large):
+    """Scores so large that fp32 holds them in steps of 2 to 32: what grows from tile to tile without a new reference
+    still has to be a weight that f16 can hold."""
+    pk = require_gpu()
+    n, qn, hq, hkv, bs, dt = 1100, 5, 2, 1, 16, torch.float16
+    g = torch.Generator().manual_seed(11)
+    q, k = torch.zeros(qn, hq, d), torch.zeros(n, hkv, d)
+    q[:, :, 0], k[:, :, 0] = large / 2.0 ** 13, 2.0 ** 15
+    q[:, :, 1] = 8.0
+    k[:, :, 1] = torch.randint(0, 8, (n, hkv), generator=g).float() + torch.arange(n, 0, -1)[:, None] // 32
+    q, k = q.to(dt), k.to(dt)
+    v = (1.0 + 0.25 * torch.randn(n, hkv, d, generator=g)).to(dt)
+    kc, vc, table = place(k, v, bs, dt, 12)
+    cq, ck = (torch.tensor(x, dtype=torch.int32, device=DEV) for x in ([0, qn], [0, n]))
+    scale = 0.25 / np.log2(np.e)                       # the first component comes to `large` in log2 units
+    for path in (1, 2, 3):
+        out = pk.prefill_attention(q.to(DEV), kc, vc, table, cq, ck, qn, float(scale), path=path,
+                                   prefix_lens=torch.tensor([3], dtype=torch.int32, device=DEV)).double().cpu().numpy()
+        lo, hi = float(v.min()), float(v.max())
+        assert np.all(out >= lo - abs(lo) * 2.0 ** -9) and np.all(out <= hi + abs(hi) * 2.0 ** -9), path
