@@ -60,9 +60,12 @@ __device__ __forceinline__ float capped(float raw, float scale_log2, const Score
   return (EXACT ? tanhf(y) : tanh_fast(y)) * m.cap_out_log2;
 }
 
-// -slope * log2(e) of a query head, 0 without slopes.
+// -slope * log2(e) of a query head, 0 without slopes.  At most 2^90 either way,
+// so that its product with any distance is finite (an infinite one makes NaN at
+// distance 0, or where a row starts with keys at -inf): a key is then 2^90
+// ahead of the next, which no other score makes up for.
 __device__ __forceinline__ float bias_slope(const ScoreMod& m, int head) {
-  return m.slopes ? -m.slopes[head] * 1.4426950408889634f : 0.f;
+  return m.slopes ? fminf(fmaxf(-m.slopes[head] * 1.4426950408889634f, -0x1p90f), 0x1p90f) : 0.f;
 }
 
 // Tokens of sequence `seq` that every row may see, clamped to its length.

@@ -181,6 +181,16 @@ def decode_of_steep_slopes(dt, d, slope):
         check_steep(out.double().cpu().numpy(), v, hq, [n - 1], 0, slope, tolerances(dt, path != 1))
 
 
+HUGE = [1e33, 1e36, 3e38]
+
+
+@pytest.mark.parametrize("slope", [s * x for x in HUGE for s in (1, -1)])
+@pytest.mark.parametrize("dt,d", [("f16", 64), ("bf16", 128)])
+def test_slopes_whose_bias_is_past_fp32(dt, d, slope):
+    prefill_of_steep_slopes(dt, d, slope)
+    decode_of_steep_slopes(dt, d, slope)
+
+
 @pytest.mark.parametrize("large", [2.0 ** 24, 2.0 ** 25, 2.0 ** 26, 2.0 ** 28, -2.0 ** 25])
 @pytest.mark.parametrize("d", [64, 128])
 def test_f16_weights_of_scores_without_a_fraction(d, large):
