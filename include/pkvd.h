@@ -393,7 +393,8 @@ pkvd_status pkvd_kv_store_prefill(const void* k, const void* v, const int32_t* b
  * the cache in nanochat "04 · Engine".
  */
 typedef struct {
-  const double* inv_freq;   /* device, [rotary_dim / 2], finite; written by no kernel in flight */
+  const double* inv_freq;   /* device, [rotary_dim / 2], finite (2^64 and more in size count as 0);
+                               written by no kernel in flight */
   int32_t rotary_dim;       /* even, 2 .. head_dim */
   int32_t interleaved;      /* 0 or 1 */
   float mscale;             /* factor on cos and sin (1, or pkvd_rope_inv_freq's) */

@@ -58,8 +58,8 @@ __device__ __forceinline__ float2 turn(int64_t pos, uint64_t step, float mscale)
 // inv_freq / 2 pi modulo one turn, in units of 2^-64 turns, rounded to nearest:
 // the double is M 2^E with an integer M, 1 / 2 pi is C 2^-128, and the bits of
 // M C from 64 - E up are the result (those of FP64 arithmetic would take its
-// pipe, which has a sixtieth of the rate).  Frequencies of 2^64 and more,
-// which no position tells apart, count as 0.
+// pipe, which has a sixtieth of the rate).  Frequencies of 2^64 and more count
+// as 0: their products would need more bits than C has.
 __device__ __forceinline__ uint64_t turn_step(double inv_freq) {
   constexpr uint64_t kC1 = 0x28be60db9391054aull, kC0 = 0x7f09d5f47d4d3770ull;
   const uint64_t bits = (uint64_t)__double_as_longlong(inv_freq);
@@ -75,7 +75,7 @@ __device__ __forceinline__ uint64_t turn_step(double inv_freq) {
     const uint64_t lo = w == 0 ? p0 : w == 1 ? p1 : w == 2 ? p2 : 0, hi = w == 0 ? p1 : w == 1 ? p2 : 0;
     return r ? (lo >> r) | (hi << (64 - r)) : lo;
   };
-  uint64_t t = s > 0 && s < 192 ? from(s) + (from(s - 1) & 1u) : 0;
+  uint64_t t = ex < 1023 + 64 && s < 192 ? from(s) + (from(s - 1) & 1u) : 0;
   return (bits >> 63) ? 0 - t : t;
 }
 
