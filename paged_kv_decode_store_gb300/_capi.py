@@ -238,6 +238,8 @@ def cache_desc(k_cache: torch.Tensor, v_cache: torch.Tensor) -> PkvdCache:
     shape, stride = k_cache.shape, k_cache.stride()
     if shape != v_cache.shape or stride != v_cache.stride():
         raise ValueError("K and V caches must share shape and strides")
+    if k_cache.dtype is not v_cache.dtype or k_cache.device != v_cache.device:
+        raise ValueError("K and V caches must share dtype and device")
     if len(shape) != 4 or stride[3] != 1:
         raise ValueError("cache views must be [num_blocks, block_size, Hkv, D] with D contiguous")
     nb, bs, H, D = shape
