@@ -254,8 +254,10 @@ pkvd_status pkvd_paged_decode_attention_window(void* out, const void* q, const p
  *                      positions j < prefix_lens[i], whatever the causal order
  *                      and the window; int32 device array [num_seqs], clamped
  *                      to [0, k_len_i]; NULL: none.  A decode row has every
- *                      cached position behind it, so it is ignored there (a
- *                      window still cuts off the prefix).
+ *                      cached position behind it and sees the prefix anyway;
+ *                      decode with prefix_lens and a window shorter than
+ *                      max_context_len, which would cut the prefix off, is
+ *                      refused.
  * in this order; fp32 throughout.  The pages give no score function besides
  * the softmax; these are the forms that engines of the kind they walk through
  * need next to it.
@@ -271,7 +273,9 @@ typedef struct {
  * score modifiers (the new token is at position context_lens[i] - 1); mod
  * NULL or all off: the same call.  Same arguments, workspace, requirements,
  * status codes and device errors; PKVD_INVALID_ARG for a softcap that is
- * negative, not finite or so small that scale / softcap is not finite.
+ * negative, not finite or so small that scale / softcap is not finite (or so
+ * large that softcap * log2(e) is not), and for prefix_lens with
+ * 0 < window < max_context_len.
  */
 pkvd_status pkvd_paged_decode_attention_mod(void* out, const void* q, const pkvd_cache* cache,
                                             const int32_t* block_tables, int32_t max_blocks_per_seq,

@@ -191,7 +191,8 @@ def paged_decode_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torc
     """out[i, h] = softmax(scale * q[i, h] . K_i^T) V_i over row i's paged context
     (its newest `window` positions when window > 0).  Scores may be capped
     (softcap * tanh(s / softcap)) and biased by distance
-    (- alibi_slopes[h] * (context - 1 - j), float32 [Hq])."""
+    (- alibi_slopes[h] * (context - 1 - j), float32 [Hq]).  A window also cuts
+    off a prefix that prefill_attention opened with prefix_lens."""
     B, Hq, D = q.shape
     if softcap or alibi_slopes is not None:
         return _decode_attention_mod(q, k_cache, v_cache, block_tables, context_lens, max_context_len, scale, out,

@@ -573,6 +573,8 @@ pkvd_status pkvd_paged_decode_attention_mod(void* out, const void* q, const pkvd
                                             const pkvd_score_mod* mod, void* workspace, size_t workspace_bytes,
                                             void* stream, int32_t* err_flag, int32_t path) {
   if (window < 0) return PKVD_INVALID_ARG;
+  // the prompt's rows saw the prefix past their windows; a decode row would not
+  if (mod && mod->prefix_lens && window > 0 && window < max_context_len) return PKVD_INVALID_ARG;
   return attention_call(out, q, cache, block_tables, max_blocks_per_seq, context_lens, max_context_len, num_seqs,
                         num_q_heads, scale, window, workspace, workspace_bytes, stream, err_flag, path, mod);
 }
