@@ -77,7 +77,7 @@ typedef enum {
   PKVD_UNSUPPORTED_SHAPE = 3,    /* head_dim, group size, block size, alignment */
   PKVD_WORKSPACE_TOO_SMALL = 4,
   PKVD_CUDA_ERROR = 5,           /* a CUDA runtime call failed (launch, query) */
-  PKVD_NO_SPACE = 6              /* block manager: not enough free blocks (nothing changed) */
+  PKVD_NO_SPACE = 6              /* block manager: not enough free blocks or host memory (nothing changed) */
 } pkvd_status;
 
 typedef enum { PKVD_F32 = 0, PKVD_F16 = 1, PKVD_BF16 = 2 } pkvd_dtype;

@@ -25,6 +25,7 @@
 // * a request that needs more free blocks than there are changes nothing.
 #include <cstdint>
 #include <cstring>
+#include <exception>
 #include <new>
 #include <string>
 #include <unordered_map>
@@ -80,11 +81,16 @@ struct pkvd_block_manager {
     ref[b] = 1;
     return b;
   }
-  void register_block(int32_t b, int32_t parent, const int32_t* tokens) {
-    std::string k = key(parent, tokens);
-    if (cache.count(k)) return;         // an equal block is registered: keep the first
-    key_of[b] = k;
-    cache.emplace(std::move(k), b);
+  // Without memory for its key a block stays unregistered: no later prompt finds it.
+  void register_block(int32_t b, int32_t parent, const int32_t* tokens) noexcept {
+    try {
+      std::string k = key(parent, tokens);
+      if (cache.count(k)) return;       // an equal block is registered: keep the first
+      key_of[b] = k;
+      cache.emplace(std::move(k), b);
+    } catch (const std::bad_alloc&) {
+      key_of[b].clear();
+    }
   }
 };
 
@@ -93,9 +99,11 @@ extern "C" {
 pkvd_status pkvd_bm_create(int32_t num_blocks, int32_t block_size, pkvd_block_manager** out) {
   if (!out || num_blocks <= 0 || block_size <= 0) return PKVD_INVALID_ARG;
   *out = nullptr;
-  pkvd_block_manager* bm = new (std::nothrow) pkvd_block_manager(num_blocks, block_size);
-  if (!bm) return PKVD_NO_SPACE;
-  *out = bm;
+  try {                                 // the arrays' allocations throw
+    *out = new pkvd_block_manager(num_blocks, block_size);
+  } catch (const std::exception&) {
+    return PKVD_NO_SPACE;
+  }
   return PKVD_OK;
 }
 
@@ -118,11 +126,15 @@ pkvd_status pkvd_bm_allocate(pkvd_block_manager* bm, const int32_t* tokens, int3
   // prefix lookups: full blocks with at least one prompt token after them
   std::vector<int32_t> hits;
   int32_t parent = -1;
-  for (int32_t i = 0; i < nblk && (int64_t)(i + 1) * bs <= num_tokens - 1; ++i) {
-    auto it = bm->cache.find(bm->key(parent, tokens + (int64_t)i * bs));
-    if (it == bm->cache.end()) break;
-    hits.push_back(it->second);
-    parent = it->second;
+  try {                                 // nothing has changed yet
+    for (int32_t i = 0; i < nblk && (int64_t)(i + 1) * bs <= num_tokens - 1; ++i) {
+      auto it = bm->cache.find(bm->key(parent, tokens + (int64_t)i * bs));
+      if (it == bm->cache.end()) break;
+      hits.push_back(it->second);
+      parent = it->second;
+    }
+  } catch (const std::bad_alloc&) {
+    return PKVD_NO_SPACE;
   }
   int32_t need = nblk - (int32_t)hits.size();
   for (int32_t b : hits) need += bm->ref[b] == 0;
