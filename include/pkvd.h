@@ -202,7 +202,8 @@ pkvd_status pkvd_decode_workspace_bytes(int32_t num_seqs, int32_t num_q_heads,
  *         clamped).  Entries past a row's last block and cache rows past its
  *         context are never read.
  * Output: out [num_seqs, num_q_heads, head_dim], cache dtype, fp32 softmax
- *         and accumulation.
+ *         and accumulation (the tensor-core path rounds the softmax weights
+ *         to the cache dtype for the second product).
  * workspace: device scratch of at least pkvd_decode_workspace_bytes(...)
  *         bytes (16-byte aligned), used for split-context partial results;
  *         its contents need no initialisation.  Calls that share a
@@ -258,9 +259,13 @@ pkvd_status pkvd_paged_decode_attention_window(void* out, const void* q, const p
  *                      decode with prefix_lens and a window shorter than
  *                      max_context_len, which would cut the prefix off, is
  *                      refused.
- * in this order; fp32 throughout.  The pages give no score function besides
- * the softmax; these are the forms that engines of the kind they walk through
- * need next to it.
+ * in this order.  Scores, softmax statistics and sums are fp32.  A capped score
+ * is off by a few 2^-24 of itself with an f32 cache, by 10^-6 with a 16-bit one
+ * and by 7.2 * 10^-6 in prefill on the tcgen05 path (tanh as a polynomial), plus
+ * those roundings; the tensor-core paths round the softmax weights to the
+ * cache's type for the product with V, as without modifiers.  The pages give
+ * no score function besides the softmax; these are the forms that engines of
+ * the kind they walk through need next to it.
  */
 typedef struct {
   float softcap;
@@ -532,7 +537,10 @@ pkvd_status pkvd_prefill_attention_ex(void* out, const void* q, const pkvd_cache
  * same call.  A row whose sequence has a prefix also reads the cache rows of
  * the prefix (positions past the row's own included, so the step's store has
  * to come first).  PKVD_INVALID_ARG for a bad softcap as in
- * pkvd_paged_decode_attention_mod. */
+ * pkvd_paged_decode_attention_mod.  bf16 caches, a cap of at most 44 and no
+ * slopes, on the tcgen05 path: the weights are not taken relative to the row's
+ * largest score, so values should lie between 2^-60 and 2^40 in size (beyond
+ * they may be lost or overflow in the fp32 sums). */
 pkvd_status pkvd_prefill_attention_mod(void* out, const void* q, const pkvd_cache* cache, const int32_t* block_tables,
                                        int32_t max_blocks_per_seq, const int32_t* cu_seqlens_q,
                                        const int32_t* cu_seqlens_k, int32_t num_seqs, int32_t total_q,
@@ -615,7 +623,7 @@ pkvd_status pkvd_beam_workspace_bytes(int32_t num_requests, int32_t num_beams, i
  * and the `keep` best ones of the request are returned, best first, the lowest
  * b * vocab + j first among equal ones.  Values are compared as pairs of fp32
  * (to 2^-47 of themselves); a beam's normaliser, which shifts all its values
- * alike, is good to about 10^-7.
+ * alike, is good to 2^-20 (its sum is of fp32 exponentials).
  * An ended beam (finished[r][b] != 0; finished may be NULL) has one
  * continuation: eos_id at its score unchanged; its logits are not read.
  * Ids at -inf are never chosen.  A beam whose score or normaliser is not

@@ -14,7 +14,7 @@ counted from the roundings:
     scores    an error of e in s_j is a relative error of e in its weight:
               the dot product (D + 2 roundings of 2^-24 of sum |q||k| scale;
               `dot_rounds` of them where a test's products and sums are exact),
-              the cap (`cap_error` of the value), the bias and the exponent's
+              the cap (`cap_error` of the value, see CAP_ERROR), the bias and the exponent's
               argument (4 roundings of 2^-24 of the largest |s|), 2^-22 of the
               exponential
     sums      one rounding of 2^-24 per key in the numerator and denominator
@@ -25,6 +25,12 @@ from __future__ import annotations
 
 import numpy as np
 
+# How far a capped score may be off, relative to itself.  fp32 caches: the
+# argument and the factor behind (4 roundings of 2^-24) and tanh itself, 2 ulp
+# of at most 2^-23.  16-bit caches: the same roundings and tanh to 1e-6; by
+# tcgen05 a polynomial off by 7.2e-6.
+CAP_ERROR = {"f32": 8 * 2.0 ** -24, "16-bit": 1e-6 + 4 * 2.0 ** -24, "tcgen05": 7.2e-6 + 4 * 2.0 ** -24}
+
 
 def visible_keys(p: int, klen: int, window: int = 0, prefix: int = 0) -> np.ndarray:
     j = np.arange(klen)
@@ -33,7 +39,7 @@ def visible_keys(p: int, klen: int, window: int = 0, prefix: int = 0) -> np.ndar
 
 
 def attend(q, K, V, p: int, scale: float, cap: float = 0.0, slope: float = 0.0, window: int = 0, prefix: int = 0,
-           u_p: float = 0.0, eps: float = 2.0 ** -23, tiny: float = 0.0, cap_error: float = 7e-6,
+           u_p: float = 0.0, eps: float = 2.0 ** -23, tiny: float = 0.0, cap_error: float = CAP_ERROR["tcgen05"],
            dot_rounds: int | None = None):
     """(output [D], bound [D]) of one query over its sequence's keys K [klen, D]."""
     seen = visible_keys(p, K.shape[0], window, prefix)
