@@ -427,7 +427,9 @@ pkvd_status pkvd_prefill_attention_mod(void* out, const void* q, const pkvd_cach
   if (path == PKVD_PATH_TC && !tc) return PKVD_UNSUPPORTED_SHAPE;
   if (path == PKVD_PATH_AUTO) path = tc ? PKVD_PATH_TC : mma ? PKVD_PATH_MMA : PKVD_PATH_FMA;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (path == PKVD_PATH_TC) return from_cuda(sm.on() ? launch_prefill_mod(a, st) : launch_prefill_tc(a, st));
+  // the plain tcgen05 kernel takes the maximum of the unscaled products, which needs a scale above 0
+  const bool plain = !sm.on() && scale > 0.f;
+  if (path == PKVD_PATH_TC) return from_cuda(plain ? launch_prefill_tc(a, st) : launch_prefill_mod(a, st));
   if (path == PKVD_PATH_MMA) return from_cuda(launch_prefill_attention(a, st));
   return from_cuda(launch_prefill_fma(a, st));
 }

@@ -1,7 +1,9 @@
 // Varlen paged prefill attention with modified scores (score_mod.cuh) on the
 // 5th-generation tensor cores: the operation of prefill_tc.cu with
 //   s = cap * tanh(scale <q, k> / cap) - slope_h |p - j|
-// over the causal window of every row and its sequence's prefix.
+// over the causal window of every row and its sequence's prefix; and without
+// any of these where the scale is not positive (prefill_tc.cu takes maxima
+// before it scales).
 //
 // What differs from the plain kernel is the softmax, which is three times as
 // long here and would set the pace alone.  So
