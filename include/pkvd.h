@@ -250,7 +250,8 @@ pkvd_status pkvd_paged_decode_attention_window(void* out, const void* q, const p
  * score of key position j for a query at position p, query head h:
  *   softcap > 0        s_j <- softcap * tanh(s_j / softcap); 0: no cap
  *   alibi_slopes       s_j <- s_j - alibi_slopes[h] * |p - j|; f32 device
- *                      array [num_q_heads], finite, any sign; NULL: no bias
+ *                      array [num_q_heads], finite, any sign (counts as at
+ *                      most 2^90 / log2(e) in size); NULL: no bias
  *   prefix_lens        (prefill only) every row of sequence i also attends to
  *                      positions j < prefix_lens[i], whatever the causal order
  *                      and the window; int32 device array [num_seqs], clamped
@@ -638,6 +639,9 @@ pkvd_status pkvd_beam_workspace_bytes(int32_t num_requests, int32_t num_beams, i
  *         block tables after it.
  * workspace: pkvd_beam_workspace_bytes(...) bytes, 16-byte aligned, no
  *         initialisation; calls that share one must not overlap on the GPU.
+ * Time: a request in which more than some 2000 continuations tie with the last
+ *         one kept, or nearly so (uniform rows), is read once more for every
+ *         one kept, by one thread block.
  * Requirements: 1 <= vocab <= 2^23, num_beams <= 64, 1 <= keep <= 64; with
  *         `finished`, 0 <= eos_id < vocab.
  */

@@ -25,19 +25,24 @@
 //   one reads its scores again and takes the exponential form.
 // * bf16 weights have fp32's range: with a cap and no slopes every score lies
 //   in [-cap, cap], and while 2^(cap log2 e) is far inside that range no
-//   reference is needed at all -- no maximum, no exchange, no rescaling (169
-//   instead of 132 us for 8 capped prompts of 1024 tokens with one).
+//   reference is needed at all -- no maximum, no exchange, no rescaling (167
+//   instead of 130 us for 8 capped prompts of 1024 tokens with one).
+// * weights are rounded to the cache's type for the product with V: its two
+//   operands have one type, and a second product for the bits below would
+//   double that part.  It costs half a step a weight, as in the plain kernel
+//   (error of the capped prompts 2.3e-3 of the result, 1.7e-3 of them the
+//   output's own rounding).
 //
-// Measured: 8 prompts of 1024 tokens, 48 + 8 heads of 128, bf16, capped: 132 us
-// (782 TFLOP/s of visible pairs; 281 with the plain kernel's structure).  Four
+// Measured: 8 prompts of 1024 tokens, 48 + 8 heads of 128, bf16, capped: 130 us
+// (794 TFLOP/s of visible pairs; 281 us with the plain kernel's structure).  Four
 // chunks of about 1000 tokens after up to 7168, 64 + 8 heads of 64, f16, bias
-// and prefix: 418 us (918 TFLOP/s; 709).  Bound: not the tensor pipe (active
+// and prefix: 415 us (924 TFLOP/s; 709 us).  Bound: not the tensor pipe (active
 // 39 % of the time; leaving out nearly all products saved 1 to 2 %).  At
 // head_dim 64 the instructions (issue slots 70 % taken; a scheduler has four
 // softmax warps and one of the others, and the slowest scheduler sets the
-// pace).  At 128 the chain of a half tile: weights, product, next scores; there
-// is no TMEM for a second S beside 2 O and 2 S, and the next S must wait for
-// the weights that lie in it (taking whichever half is ready, by polling, was
+// pace).  At 128 the chain of a half tile: weights, product, next scores; with
+// two Q tiles a CTA there is no TMEM for a second S beside 2 O and 2 S, and the
+// next S must wait for the weights that lie in it (taking whichever half is ready, by polling, was
 // slower: 174 instead of 160 us).
 //
 // Warps (20): 0-7 and 8-15 softmax of Q tile 0 and 1 (warp w of a tile: TMEM

@@ -22,8 +22,8 @@
 // into the warp's shared memory, then share out units of two 16-byte vectors
 // (the two halves of eight or four pairs, or two neighbouring vectors), two
 // units a lane loaded ahead (four take more registers than the loads in
-// flight are worth: 8192 prefill rows of 48 + 8 + 8 heads 67 us against 53;
-// one 55).  Bound: bytes, every row read once and written once.  Those 8192
+// flight are worth: 8192 prefill rows of 48 + 8 + 8 heads 60 us against 48;
+// one 48 there, but 27 us for the half-rotated rows below).  Bound: bytes, every row read once and written once.  Those 8192
 // rows take 48 us (5.5 TB/s of rows), 18433 rows of 16 + 16 heads of 64 half
 // rotated 26 us (5.7 TB/s); one CTA a token with a barrier between angles and
 // rows took 70 and 55 us.
@@ -216,7 +216,7 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeCtas) rope_kernel(const Rop
   if constexpr (VECTOR) {
     // cos and sin of a unit's VEC pairs; a lane whose units are the same one of
     // every head keeps them (reading them a unit at a time from shared memory,
-    // four lanes to a bank, took 59 us instead of 53 for 8192 prefill rows)
+    // four lanes to a bank, takes 55 us instead of 48 for 8192 prefill rows)
     float2 t[VEC];
     auto pairs_of = [&](int u) {
 #pragma unroll
