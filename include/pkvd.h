@@ -264,7 +264,9 @@ pkvd_status pkvd_paged_decode_attention_window(void* out, const void* q, const p
  * is off by a few 2^-24 of itself with an f32 cache, by 10^-6 with a 16-bit one
  * and by 7.2 * 10^-6 in prefill on the tcgen05 path (tanh as a polynomial), plus
  * those roundings; the tensor-core paths round the softmax weights to the
- * cache's type for the product with V, as without modifiers.  The pages give
+ * cache's type for the product with V, as without modifiers (f16 ones are
+ * scaled first: they keep their bits down to 2^-29 of the row's largest, to
+ * 2^-21 on the tcgen05 path).  The pages give
  * no score function besides the softmax; these are the forms that engines of
  * the kind they walk through need next to it.
  */

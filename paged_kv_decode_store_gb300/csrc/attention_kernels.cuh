@@ -356,8 +356,9 @@ struct MmaConsumer {
       }
       const float mn0 = fmaxf(m[j][0], mx0), mn1 = fmaxf(m[j][1], mx1);
       const float c0 = exp2f(m[j][0] - mn0), c1 = exp2f(m[j][1] - mn1);
-      const float p0 = exp2f(x0 - mn0), p1 = exp2f(x1 - mn1);
-      const float p2 = exp2f(x2 - mn0), p3 = exp2f(x3 - mn1);
+      constexpr float lift = MOD ? kWeightLift<T> : 0.f;
+      const float p0 = exp2f(x0 - mn0 + lift), p1 = exp2f(x1 - mn1 + lift);
+      const float p2 = exp2f(x2 - mn0 + lift), p3 = exp2f(x3 - mn1 + lift);
       l[j][0] = l[j][0] * c0 + p0 + p2;
       l[j][1] = l[j][1] * c1 + p1 + p3;
       m[j][0] = mn0;

@@ -272,10 +272,11 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_attention_kernel(const 
       float rs0 = 0.f, rs1 = 0.f;
 #pragma unroll
       for (int n = 0; n < kPfKeys / 8; ++n) {
-        s[n][0] = ex2(s[n][0] - u0);
-        s[n][1] = ex2(s[n][1] - u0);
-        s[n][2] = ex2(s[n][2] - u1);
-        s[n][3] = ex2(s[n][3] - u1);
+        constexpr float lift = MOD ? kWeightLift<T> : 0.f;
+        s[n][0] = ex2(s[n][0] - u0 + lift);
+        s[n][1] = ex2(s[n][1] - u0 + lift);
+        s[n][2] = ex2(s[n][2] - u1 + lift);
+        s[n][3] = ex2(s[n][3] - u1 + lift);
         rs0 += s[n][0] + s[n][1];
         rs1 += s[n][2] + s[n][3];
       }

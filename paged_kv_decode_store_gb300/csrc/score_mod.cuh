@@ -6,6 +6,8 @@
 // scale and 1 / cap are one factor on the raw dot product.
 #pragma once
 
+#include <type_traits>
+
 #include "common.cuh"
 #include "launch.h"
 
@@ -67,6 +69,13 @@ __device__ __forceinline__ float capped(float raw, float scale_log2, const Score
 __device__ __forceinline__ float bias_slope(const ScoreMod& m, int head) {
   return m.slopes ? fminf(fmaxf(-m.slopes[head] * 1.4426950408889634f, -0x1p90f), 0x1p90f) : 0.f;
 }
+
+// Exponent that the mma.sync paths add to a weight of at most 1 before it is
+// rounded to the cache's type (the sum of the weights has it too, so it
+// cancels): f16 is normal down to 2^-14 only, and many small weights beside a
+// large one have to add up to what they are.
+template <typename T>
+constexpr float kWeightLift = std::is_same<T, __half>::value ? 15.f : 0.f;
 
 // Tokens of sequence `seq` that every row may see, clamped to its length.
 __device__ __forceinline__ int prefix_of(const ScoreMod& m, int seq, int klen) {

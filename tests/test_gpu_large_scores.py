@@ -213,3 +213,35 @@ def test_f16_weights_of_scores_without_a_fraction(d, large):
                                    prefix_lens=torch.tensor([3], dtype=torch.int32, device=DEV)).double().cpu().numpy()
         lo, hi = float(v.min()), float(v.max())
         assert np.all(out >= lo - abs(lo) * 2.0 ** -9) and np.all(out <= hi + abs(hi) * 2.0 ** -9), path
+
+
+@pytest.mark.parametrize("steps", [9.5, 1.49, 0.3])
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+def test_small_weights_beside_one_whose_value_is_zero(dt, steps):
+    """All but one key of a row have `steps` of f16's smallest step (2^-24) of the largest one's weight, and that one's
+    values are zero: the small weights are the whole result."""
+    pk = require_gpu()
+    n, qn, hq, hkv, d, bs, dt = 3000, 5, 8, 8, 64, 64, DT[dt]
+    g = torch.Generator().manual_seed(15)
+    k = torch.zeros(n, hkv, d)
+    k[n - 20, :, 0] = 1.0
+    q = torch.zeros(qn, hq, d)
+    q[:, :, 0] = 1.0
+    k, q = k.to(dt), q.to(dt)
+    v = 64 * (1.0 + 0.25 * torch.randn(n, hkv, d, generator=g))
+    v[n - 20] = 0.0
+    v = v.to(dt)
+    scale = float(-np.log(steps * 2.0 ** -24))
+    kc, vc, table = place(k, v, bs, dt, 16)
+    cq, ck = (torch.tensor(x, dtype=torch.int32, device=DEV) for x in ([0, qn], [0, n]))
+    zero = torch.zeros(hq, device=DEV)
+    # the tcgen05 path's reference may lag 2^8 behind the largest weight, which leaves it seven bits below 2^-14
+    got = [pk.prefill_attention(q.to(DEV), kc, vc, table, cq, ck, qn, scale, path=path, alibi_slopes=zero)[qn - 1]
+           for path in ((2, 3) if dt == torch.bfloat16 or steps > 8 else (2,))]
+    got.append(pk.paged_decode_attention(q[:1].to(DEV), kc, vc, table, ck[1:], n, scale, path=2, alibi_slopes=zero)[0])
+    for h in range(hq):
+        want, bound = oracle.scores.attend(q[0, h].double().numpy(), k[:, h].double().numpy(), v[:, h].double().numpy(),
+                                           n - 1, scale, dot_rounds=0, **tolerances(dt, True))
+        for i, o in enumerate(got):
+            off = np.abs(o[h].double().cpu().numpy() - want)
+            assert np.all(off <= bound), (i, h, float((off / bound).max()))
