@@ -54,11 +54,12 @@
  *     on the stream: they may start while a preceding kernel that signalled
  *     early completion (griddepcontrol.launch_dependents) still runs.  Before
  *     waiting for it they read only inputs that no kernel of this library
- *     writes (context lengths, block tables, rotary frequencies); everything
- *     else (q, the cache, slot_mapping, outputs, workspaces) comes after the
- *     wait.  A caller's
- *     own kernel that signals early must not write those inputs of the call
- *     that follows it.
+ *     writes while a later one may start (context lengths, cu_seqlens, parents,
+ *     block tables, rotary frequencies; pkvd_evict_select, whose counts are
+ *     lengths, does not signal early); everything else (q, the cache,
+ *     slot_mapping, outputs, workspaces) comes after the wait.  A caller's own
+ *     kernel that signals early must not write those inputs of the call that
+ *     follows it.
  */
 #ifndef PKVD_H
 #define PKVD_H
@@ -87,6 +88,7 @@ typedef enum { PKVD_F32 = 0, PKVD_F16 = 1, PKVD_BF16 = 2 } pkvd_dtype;
 #define PKVD_ERR_SLOT        2   /* slot >= num_blocks * block_size           */
 #define PKVD_ERR_CONTEXT     4   /* context_len < 0 or > the stated bound     */
 #define PKVD_ERR_TIMEOUT     8   /* a pipeline wait gave up (never expected)  */
+#define PKVD_ERR_TREE       16   /* a drafted node whose parent is not an earlier node or -1 */
 
 /* Attention path selector for pkvd_paged_decode_attention_ex and
  * pkvd_prefill_attention_ex. */
@@ -550,6 +552,147 @@ pkvd_status pkvd_prefill_attention_mod(void* out, const void* q, const pkvd_cach
                                        int32_t max_seqlen_q, int32_t num_q_heads, float scale, int32_t window,
                                        const pkvd_score_mod* mod, void* stream, int32_t* err_flag, int32_t path);
 
+/*
+ * Trees of drafted tokens (speculative decoding).  Sequence i's n_i drafted rows
+ * [cu_seqlens_q[i], cu_seqlens_q[i+1]) are stored behind its cached_i = k_len_i -
+ * n_i cached tokens (pkvd_kv_store_prefill does that); node t of the tree is its
+ * t-th drafted row, parents[cu_seqlens_q[i] + t] an earlier node (< t) or -1 for
+ * one that follows the cached context directly.  A node's token position is
+ * cached_i + its depth (its ancestors' number): pkvd_rope takes those positions.
+ *
+ * pkvd_tree_attention -- every drafted row attends to the cached context, its
+ * ancestors and itself.  For node t, query head h, kv head hk = h / G:
+ *   out[t,h,:] = sum_j softmax(s)_j V_j,  s_j = scale * <q[t,h,:], K_j>,
+ * modified as in pkvd_score_mod (distances and the window count token positions:
+ * a key `window` or more positions behind is not seen).  mod->prefix_lens has to
+ * be NULL.  The same scores as decoding the path to t token by token.
+ * Inputs: q [total_q, num_q_heads, head_dim] contiguous, cache dtype, 16-byte
+ *         aligned; parents int32 [total_q]; cu_seqlens_q, cu_seqlens_k,
+ *         block_tables as in pkvd_prefill_attention; max_seqlen_q >= every n_i.
+ *         Cache rows before every node's window and past k_len_i are never
+ *         weighed; drafted rows of the same tree must be stored (finite).
+ * Output: out [total_q, num_q_heads, head_dim], 16-byte aligned; rows t >=
+ *         cu_seqlens_q[num_seqs] are not written.
+ * workspace: pkvd_tree_workspace_bytes(...) bytes, 256-byte aligned, no
+ *         initialisation; calls that share one must not overlap on the GPU.
+ * path:   PKVD_PATH_TC (tcgen05; 16-bit caches with block_size >= 8 whose strides
+ *         nest head < token < block), PKVD_PATH_FMA (fp32 arithmetic, any
+ *         dtype), PKVD_PATH_AUTO (TC where it can run the call).
+ * Requirements: head_dim 64 or 128, num_q_heads % num_kv_heads == 0, group size
+ *         <= 128, max_seqlen_q <= 256, num_seqs <= 65535, window >= 0.
+ * Device errors: n_i > k_len_i or > max_seqlen_q, cu_seqlens_q[i+1] > total_q,
+ *         k_len_i past the table set PKVD_ERR_CONTEXT (that sequence's rows are
+ *         not written); a parent that is not -1 or an earlier node sets
+ *         PKVD_ERR_TREE and counts as -1; a bad block id sets
+ *         PKVD_ERR_BLOCK_ID (its rows read as zeros).
+ */
+pkvd_status pkvd_tree_workspace_bytes(int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
+                                      int32_t max_seqlen_q, int32_t sm_count, size_t* bytes);
+pkvd_status pkvd_tree_attention(void* out, const void* q, const pkvd_cache* cache, const int32_t* block_tables,
+                                int32_t max_blocks_per_seq, const int32_t* cu_seqlens_q, const int32_t* cu_seqlens_k,
+                                const int32_t* parents, int32_t num_seqs, int32_t total_q, int32_t max_seqlen_q,
+                                int32_t num_q_heads, float scale, int32_t window, const pkvd_score_mod* mod,
+                                void* workspace, size_t workspace_bytes, void* stream, int32_t* err_flag, int32_t path);
+
+/*
+ * pkvd_tree_accept -- which drafted nodes the target's own choices follow.
+ * Node 0 of every tree is the token chosen last (its row is new, but it is no
+ * draft); target[t] is the token that the target chooses after node t's path
+ * (pkvd_sample on the logits of row t, say).  From node 0 on, the path goes to
+ * the lowest node whose parent is the path's last one and whose drafted id is
+ * the target's choice there, until there is none or the path has max_path nodes.
+ * Inputs: drafted, parents, target int32 [total_q]; cu_seqlens_q, cu_seqlens_k as
+ *         above, trees of at most 256 nodes.
+ * Output: positions int32 [num_seqs, max_path], the path's cache positions
+ *         (cached_i + node), -1 behind; first int32 [num_seqs] = cached_i; counts
+ *         int32 [num_seqs], the path's nodes (0 for an empty tree); tokens int32
+ *         [num_seqs, max_path] = target of the path's nodes, the new tokens of
+ *         this step (the last one is the next tree's node 0), -1 behind.
+ *         pkvd_compact_cache(positions, first, counts) then moves the path's rows
+ *         to where the sequence goes on.
+ * Device errors: as pkvd_tree_attention (such a sequence gets counts 0, first 0).
+ */
+pkvd_status pkvd_tree_accept(int32_t* positions, int32_t* first, int32_t* counts, int32_t* tokens,
+                             const int32_t* drafted, const int32_t* parents, const int32_t* target,
+                             const int32_t* cu_seqlens_q, const int32_t* cu_seqlens_k, int32_t num_seqs,
+                             int32_t total_q, int32_t max_path, void* stream, int32_t* err_flag);
+
+/*
+ * pkvd_compact_cache -- rows of the cache close up: for r < counts[i], row
+ * first[i] + r of sequence i in new_tables becomes row positions[i][r] of it in
+ * block_tables, K and V, an exact bit copy; every head alike (positions
+ * [num_seqs, max_count], head stride 0) or each KV head by its own list
+ * ([num_seqs, num_kv_heads, max_count]).  Rows from first[i] + counts[i] on are
+ * left as they were.
+ * new_tables == block_tables: in place.  Every position must then be at least
+ *         first[i] + r (ascending lists are; any order and repeats are fine).
+ * Other tables: no block that is written may be read by this call.
+ * Blocks that other sequences share are written like any other: cut a shared
+ * sequence into fresh blocks (new_tables), or copy its blocks first.
+ * Inputs: positions int32, rows `pos_stride`, heads `pos_head_stride` elements
+ *         apart; counts int32 [num_seqs] <= max_count; first int32 [num_seqs] or
+ *         NULL (0).
+ * Device errors: a position outside the table, a count outside [0, max_count]
+ *         (clamped), a negative first (the sequence is skipped), a position
+ *         below its place in place: PKVD_ERR_CONTEXT; a bad block id:
+ *         PKVD_ERR_BLOCK_ID.  Such rows are not copied.
+ */
+pkvd_status pkvd_compact_cache(const pkvd_cache* cache, const int32_t* block_tables, int32_t max_blocks_per_seq,
+                               const int32_t* new_tables, int32_t new_max_blocks_per_seq, const int32_t* positions,
+                               int64_t pos_stride, int64_t pos_head_stride, const int32_t* counts, const int32_t* first,
+                               int32_t num_seqs, int32_t max_count, void* stream, int32_t* err_flag);
+
+/*
+ * pkvd_paged_decode_attention_weights -- pkvd_paged_decode_attention_mod that
+ * also counts what each cached position was given: for j < context_lens[i]
+ *   weights_out[i][h][j] = weights[i][h][j] + sum of softmax_j over the query
+ *   heads of KV head h (weight_heads == num_kv_heads) or over all query heads
+ *   (weight_heads == 1); 0 is added before a window.
+ * Entries from context_lens[i] on are left as they were.  A buffer that starts
+ * with zeros adds up a sequence's decode steps; pkvd_evict_select reads it.
+ * Inputs: weights f32, element (i, h, j) at i * seq_stride + h * head_stride + j,
+ *         rows of at least max_context_len; mod as for the decode call.
+ * Output: out as the decode call's; weights_out at the same strides, may be
+ *         weights (in place), else must not overlap it.  Sums are fp32 in a
+ *         fixed order: the same bits in every run.
+ * workspace: pkvd_decode_weights_workspace_bytes(...) bytes (4 bytes per query
+ *         head and key of max_context_len beside the decode call's), 256-byte
+ *         aligned, no initialisation; calls that share one must not overlap.
+ * Requirements, status codes and device errors of the decode call; keys of a bad
+ *         block are given 0.  PKVD_INVALID_ARG for other weight_heads.
+ */
+pkvd_status pkvd_decode_weights_workspace_bytes(int32_t num_seqs, int32_t num_q_heads, int32_t head_dim,
+                                                int32_t max_context_len, int32_t sm_count, size_t* bytes);
+pkvd_status pkvd_paged_decode_attention_weights(void* out, const void* q, const pkvd_cache* cache,
+                                                const int32_t* block_tables, int32_t max_blocks_per_seq,
+                                                const int32_t* context_lens, int32_t max_context_len, int32_t num_seqs,
+                                                int32_t num_q_heads, float scale, int32_t window,
+                                                const pkvd_score_mod* mod, float* weights_out, const float* weights,
+                                                int64_t seq_stride, int64_t head_stride, int32_t weight_heads,
+                                                void* workspace, size_t workspace_bytes, void* stream,
+                                                int32_t* err_flag, int32_t path);
+
+/*
+ * pkvd_evict_select -- which positions of a sequence stay in a cache of `keep`
+ * rows.  Row (i, h) of weights: a sequence of at most `keep` tokens keeps all;
+ * a longer one its first `sink`, its last `recent` and the heaviest of the
+ * others, keep in all, the lowest position first among equal weights (-0 equals
+ * 0, a NaN is above all numbers).
+ * Inputs: weights f32 as above, rows of `length`; context_lens int32 [num_seqs]
+ *         <= length; sink, recent >= 0, sink + recent <= keep.
+ * Output: positions int32 [num_seqs, heads, keep], ascending, -1 behind; counts
+ *         int32 [num_seqs] = min(context_lens[i], keep); weights_out (or NULL) at
+ *         the same strides: the weights that stay, closed up in the same order,
+ *         zeros behind them up to `length`.  It may be weights (in place), else
+ *         must not overlap it.
+ * Device errors: a length outside [0, length] sets PKVD_ERR_CONTEXT and is
+ *         clamped.
+ */
+pkvd_status pkvd_evict_select(int32_t* positions, int32_t* counts, float* weights_out, const float* weights,
+                              int64_t seq_stride, int64_t head_stride, int32_t length, const int32_t* context_lens,
+                              int32_t num_seqs, int32_t heads, int32_t keep, int32_t sink, int32_t recent, void* stream,
+                              int32_t* err_flag);
+
 /* Workspace bytes of pkvd_sample_ex's optional outputs: 32 per row (host
  * only).  pkvd_sample itself needs none (it may get NULL, 0). */
 pkvd_status pkvd_sample_workspace_bytes(int32_t num_rows, int32_t vocab, size_t* bytes);
@@ -701,6 +844,32 @@ pkvd_status pkvd_bm_fork(pkvd_block_manager* bm, const int32_t* block_table, int
 
 /* A sequence ends: every block of its table loses a reference (last first). */
 pkvd_status pkvd_bm_release(pkvd_block_manager* bm, const int32_t* block_table, int32_t num_blocks);
+
+/* Room for drafts: the table of a sequence of num_tokens tokens grows to hold
+ * `drafts` more rows behind them (fresh blocks, which are not registered).  When
+ * the first of them lands in a shared block, *copy_src / *copy_dst / *copy_rows
+ * name the copy-on-write copy to run before the store (else -1, -1, 0).
+ * PKVD_NO_SPACE (nothing changes) without enough free blocks. */
+pkvd_status pkvd_bm_reserve(pkvd_block_manager* bm, int32_t num_tokens, int32_t drafts, int32_t* block_table,
+                            int32_t* num_blocks, int32_t max_blocks, int32_t* copy_src, int32_t* copy_dst,
+                            int32_t* copy_rows);
+
+/* What stays of it: the sequence now holds num_tokens tokens (`tokens`: all their
+ * ids), the first old_tokens of which it held before pkvd_bm_reserve.  Blocks
+ * behind its last one are released (last first), blocks that the accepted
+ * tokens filled are registered. */
+pkvd_status pkvd_bm_trim(pkvd_block_manager* bm, const int32_t* tokens, int32_t num_tokens, int32_t old_tokens,
+                         const int32_t* block_table, int32_t* num_blocks);
+
+/* After an eviction: the sequence keeps num_tokens >= 1 rows, which are no
+ * prompt's any more.  Its blocks' keys are forgotten, none of those that stay, nor
+ * what is appended behind them, is registered until it is handed out again;
+ * blocks behind the last one are released (last first).  PKVD_INVALID_ARG (nothing
+ * changes) if a block is shared: in place the eviction would have rewritten
+ * another sequence's rows.  Check with pkvd_bm_ref_count, and cut such a sequence
+ * into fresh blocks: pkvd_bm_reserve from an empty table, pkvd_compact_cache into
+ * it, this call on it, pkvd_bm_release of the old table. */
+pkvd_status pkvd_bm_evict(pkvd_block_manager* bm, int32_t num_tokens, const int32_t* block_table, int32_t* num_blocks);
 
 /* The rows of a batch follow their parents (a step of beam search): row i
  * becomes a clone of row parents[i], or ends (-1: no blocks), all rows at

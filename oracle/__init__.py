@@ -23,6 +23,7 @@ Every function restates, in the plainest form, what the pages define:
 * ``rotary``    -- rotary positions, the angle reduced in rational arithmetic.
 * ``scores``    -- attention whose scores are capped, biased or opened to a prefix.
 * ``beam``      -- one step of beam search over beams and vocabulary.
+* ``drafts``    -- trees of drafted tokens, and eviction by attention weight.
 * ``block_manager`` -- block allocation with prefix sharing, forks and
   copy-on-write (imported on its own by its tests).
 
@@ -31,4 +32,4 @@ worked examples the pages print, closed forms, brute force on tiny inputs,
 library routines and published known-answer vectors.  No function is left
 "parity unpinned".
 """
-from . import paging, store, attention, philox, sampler, prefill, rotary, scores, beam  # noqa: F401
+from . import paging, store, attention, philox, sampler, prefill, rotary, scores, beam, drafts  # noqa: F401

@@ -42,6 +42,7 @@ class BlockManager:
         self.ref = [0] * self.nb
         self.key_of = [None] * self.nb          # key a block is registered under
         self.cache = {}                         # key -> block
+        self.opaque = [False] * self.nb         # rows that are no prompt's
 
     def _key(self, parent: int, tokens) -> tuple:
         return (int(parent),) + tuple(int(t) for t in tokens)
@@ -51,10 +52,15 @@ class BlockManager:
         if self.key_of[b] is not None:          # stale content: forget it
             del self.cache[self.key_of[b]]
             self.key_of[b] = None
+        self.opaque[b] = False
         self.ref[b] = 1
         return b
 
     def _register(self, b: int, parent: int, tokens) -> None:
+        if parent >= 0 and self.opaque[parent]:
+            self.opaque[b] = True
+        if self.opaque[b]:
+            return
         k = self._key(parent, tokens)
         if k in self.cache:                     # an equal block exists: keep the first
             return
@@ -113,6 +119,7 @@ class BlockManager:
                 if not self.free:
                     return None, None
                 b = self._take()
+                self.opaque[b] = self.opaque[last]
                 self.ref[last] -= 1
                 copy = (last, b, p % bs)
                 table[-1] = b
@@ -121,6 +128,44 @@ class BlockManager:
             parent = table[i - 1] if i > 0 else -1
             self._register(table[i], parent, tokens[i * bs:(i + 1) * bs])
         return table, copy
+
+    def reserve(self, num_tokens: int, drafts: int, table):
+        """Room for drafted rows behind a sequence: (table, copy) as append, fresh
+        blocks that are not registered; (None, None) when too few are free."""
+        table, copy = list(table), None
+        want = -(-(num_tokens + drafts) // self.bs)
+        shared = drafts > 0 and num_tokens % self.bs != 0 and self.ref[table[-1]] > 1
+        if want - len(table) + shared > len(self.free):
+            return None, None
+        if shared:
+            last, b = table[-1], self._take()
+            self.ref[last] -= 1
+            self.opaque[b] = self.opaque[last]
+            copy, table[-1] = (last, b, num_tokens % self.bs), b
+        while len(table) < want:
+            table.append(self._take())
+        return table, copy
+
+    def trim(self, tokens, old_tokens: int, table) -> list:
+        """The accepted tokens stay: blocks they filled are registered, those behind released."""
+        table, n = list(table), len(tokens)
+        for i in range(old_tokens // self.bs, n // self.bs):
+            self._register(table[i], table[i - 1] if i > 0 else -1, tokens[i * self.bs:(i + 1) * self.bs])
+        stay = -(-n // self.bs)
+        self.release(table[stay:])
+        return table[:stay]
+
+    def evict(self, num_tokens: int, table) -> list:
+        """num_tokens rows of no prompt stay: keys forgotten, nothing registered from here on."""
+        table, stay = list(table), -(-num_tokens // self.bs)
+        assert all(self.ref[b] == 1 for b in table)
+        for i, b in enumerate(table):
+            if self.key_of[b] is not None:
+                del self.cache[self.key_of[b]]
+                self.key_of[b] = None
+            self.opaque[b] = i < stay
+        self.release(table[stay:])
+        return table[:stay]
 
     def fork(self, table) -> list:
         """A clone of the sequence: every block gains a reference."""

@@ -11,6 +11,13 @@ kernels.  If ``libpkvd.so`` has not been built, every call raises.
                            max_context_len, scale)
     sample(logits, temperature, top_k, top_p, seeds, offsets)
     beam_search_step(logits, scores, keep)
+    tree_attention(q, k_cache, v_cache, block_tables, cu_seqlens_q, cu_seqlens_k, parents,
+                   max_seqlen_q, scale)
+    tree_accept(drafted, parents, target, cu_seqlens_q, cu_seqlens_k, max_path)
+    paged_decode_attention_weights(q, k_cache, v_cache, block_tables, context_lens,
+                                   max_context_len, scale, weights)
+    evict_select(weights, context_lens, keep)
+    compact_cache(k_cache, v_cache, block_tables, positions, counts)
     DecodeStep(...)   -- the four calls captured in one CUDA graph
 """
 from __future__ import annotations
@@ -22,17 +29,22 @@ import torch
 
 from ._capi import (LIB_PATH, PATH_AUTO, PATH_FMA, PATH_MMA, PATH_TC, ERR_BLOCK_ID, ERR_SLOT,  # noqa: F401
                     ERR_CONTEXT, ERR_TIMEOUT, PkvdCache, PkvdError, lib, check, dtype_code,
-                    stream_handle, cache_desc, ptr, array, current_stream, err_ptr, on_stream,
-                    score_mod)
+                    ERR_TREE, stream_handle, cache_desc, ptr, array, current_stream, err_ptr, on_stream,
+                    score_mod, rows_like)
 from .step import DecodeStep  # noqa: F401
 from .beam import beam_search_step, beam_workspace_bytes  # noqa: F401
+from .drafts import tree_accept, tree_attention, tree_workspace_bytes  # noqa: F401
+from .eviction import (compact_cache, decode_weights_workspace_bytes, evict_select,  # noqa: F401
+                       paged_decode_attention_weights)
 from .rotary import rope, rope_inv_freq, rope_store_paged, rope_store_prefill  # noqa: F401
 from .block_manager import BlockManager, shared_prefix_len  # noqa: F401
 
 __all__ = ["BlockManager", "copy_blocks", "slot_mapping", "kv_store", "kv_store_paged", "kv_store_prefill",
            "prefill_attention", "sample_ex", "pack_mask", "paged_decode_attention", "decode_workspace_bytes",
            "paged_decode_attention_prefix", "decode_prefix_workspace_bytes", "shared_prefix_len",
-           "rope", "rope_store_paged", "rope_store_prefill", "rope_inv_freq", "beam_search_step", "beam_workspace_bytes", "sample", "DecodeStep", "PkvdError", "lib"]
+           "rope", "rope_store_paged", "rope_store_prefill", "rope_inv_freq", "beam_search_step", "beam_workspace_bytes",
+           "tree_attention", "tree_accept", "tree_workspace_bytes", "compact_cache", "paged_decode_attention_weights",
+           "decode_weights_workspace_bytes", "evict_select", "sample", "DecodeStep", "PkvdError", "lib"]
 
 
 def _err_ptr(err):
@@ -116,25 +128,13 @@ def prefill_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Ten
     return out
 
 
-def _attention_rows(q, out, k_cache):
-    """q and out of a call with score modifiers: contiguous rows of the cache's type and head_dim."""
-    if q.dim() != 3 or not q.is_contiguous() or q.dtype != k_cache.dtype or q.device != k_cache.device or \
-            q.shape[2] != k_cache.shape[3]:
-        raise ValueError("q must be contiguous [rows, heads, head_dim] of the cache's dtype and device")
-    if out is None:
-        return torch.empty_like(q)
-    if out.shape != q.shape or out.dtype != q.dtype or out.device != q.device or not out.is_contiguous():
-        raise ValueError("out must be a contiguous tensor like q")
-    return out
-
-
 def _prefill_attention_mod(q, k_cache, v_cache, block_tables, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, scale, window,
                            out, err, stream, path, softcap, alibi_slopes, prefix_lens):
     T, Hq, _ = q.shape
     dev, n = q.device, cu_seqlens_q.shape[0] - 1
     c = cache_desc(k_cache, v_cache)
     with on_stream(stream, dev):
-        out = _attention_rows(q, out, k_cache)
+        out = rows_like(q, out, k_cache)
         m = score_mod(softcap, alibi_slopes, prefix_lens, Hq, n, dev)
         check(lib().pkvd_prefill_attention_mod(
             out.data_ptr(), q.data_ptr(), c, array(block_tables, "block_tables", torch.int32, dev, (n, None)),
@@ -150,7 +150,7 @@ def _decode_attention_mod(q, k_cache, v_cache, block_tables, context_lens, max_c
     dev = q.device
     c = cache_desc(k_cache, v_cache)
     with on_stream(stream, dev):
-        out = _attention_rows(q, out, k_cache)
+        out = rows_like(q, out, k_cache)
         if workspace is None:
             workspace = torch.empty(max(decode_workspace_bytes(B, Hq, D, max_context_len), 16), dtype=torch.uint8,
                                     device=dev)

@@ -10,7 +10,7 @@ import torch
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libpkvd.so")
 
 PATH_AUTO, PATH_FMA, PATH_MMA, PATH_TC = 0, 1, 2, 3
-ERR_BLOCK_ID, ERR_SLOT, ERR_CONTEXT, ERR_TIMEOUT = 1, 2, 4, 8
+ERR_BLOCK_ID, ERR_SLOT, ERR_CONTEXT, ERR_TIMEOUT, ERR_TREE = 1, 2, 4, 8, 16
 NO_SPACE = 6
 _DTYPES = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
 
@@ -111,6 +111,28 @@ SIGNATURES = {
     "pkvd_paged_decode_attention_noalloc": (c_int32, [c_void_p, c_void_p, ctypes.POINTER(PkvdCache), c_void_p,
                                                       c_int32, c_void_p, c_int32, c_int32, c_int32, c_float,
                                                       c_void_p, c_void_p]),
+    "pkvd_tree_workspace_bytes": (c_int32, [c_int32, c_int32, c_int32, c_int32, c_int32, c_int32,
+                                            ctypes.POINTER(c_size_t)]),
+    "pkvd_tree_attention": (c_int32, [c_void_p, c_void_p, ctypes.POINTER(PkvdCache), c_void_p, c_int32, c_void_p,
+                                      c_void_p, c_void_p, c_int32, c_int32, c_int32, c_int32, c_float, c_int32,
+                                      ctypes.POINTER(PkvdScoreMod), c_void_p, c_size_t, c_void_p, c_void_p, c_int32]),
+    "pkvd_tree_accept": (c_int32, [c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p,
+                                   c_void_p, c_int32, c_int32, c_int32, c_void_p, c_void_p]),
+    "pkvd_compact_cache": (c_int32, [ctypes.POINTER(PkvdCache), c_void_p, c_int32, c_void_p, c_int32, c_void_p, c_int64,
+                                     c_int64, c_void_p, c_void_p, c_int32, c_int32, c_void_p, c_void_p]),
+    "pkvd_decode_weights_workspace_bytes": (c_int32, [c_int32, c_int32, c_int32, c_int32, c_int32,
+                                                      ctypes.POINTER(c_size_t)]),
+    "pkvd_paged_decode_attention_weights": (c_int32, [c_void_p, c_void_p, ctypes.POINTER(PkvdCache), c_void_p, c_int32,
+                                                      c_void_p, c_int32, c_int32, c_int32, c_float, c_int32,
+                                                      ctypes.POINTER(PkvdScoreMod), c_void_p, c_void_p, c_int64,
+                                                      c_int64, c_int32, c_void_p, c_size_t, c_void_p, c_void_p,
+                                                      c_int32]),
+    "pkvd_evict_select": (c_int32, [c_void_p, c_void_p, c_void_p, c_void_p, c_int64, c_int64, c_int32, c_void_p,
+                                    c_int32, c_int32, c_int32, c_int32, c_int32, c_void_p, c_void_p]),
+    "pkvd_bm_reserve": (c_int32, [c_void_p, c_int32, c_int32, c_void_p, ctypes.POINTER(c_int32), c_int32,
+                                  ctypes.POINTER(c_int32), ctypes.POINTER(c_int32), ctypes.POINTER(c_int32)]),
+    "pkvd_bm_trim": (c_int32, [c_void_p, c_void_p, c_int32, c_int32, c_void_p, ctypes.POINTER(c_int32)]),
+    "pkvd_bm_evict": (c_int32, [c_void_p, c_int32, c_void_p, ctypes.POINTER(c_int32)]),
     "pkvd_sample_workspace_bytes": (c_int32, [c_int32, c_int32, ctypes.POINTER(c_size_t)]),
     "pkvd_sample": (c_int32, [c_void_p, c_void_p, c_int32, c_int32, c_int32, c_int64, c_void_p, c_void_p,
                               c_void_p, c_void_p, c_void_p, c_void_p, c_size_t, c_void_p]),
@@ -231,6 +253,27 @@ def score_mod(softcap: float, alibi_slopes, prefix_lens, num_q_heads: int, num_s
                                                      (num_q_heads,))
     prefix = None if prefix_lens is None else array(prefix_lens, "prefix_lens", torch.int32, device, (num_seqs,))
     return PkvdScoreMod(softcap, slopes, prefix)
+
+
+def rows_like(q, out, k_cache):
+    """q and out of an attention call: contiguous rows of the cache's type and head_dim."""
+    if q.dim() != 3 or not q.is_contiguous() or q.dtype != k_cache.dtype or q.device != k_cache.device or \
+            q.shape[2] != k_cache.shape[3]:
+        raise ValueError("q must be contiguous [rows, heads, head_dim] of the cache's dtype and device")
+    if out is None:
+        return torch.empty_like(q)
+    if out.shape != q.shape or out.dtype != q.dtype or out.device != q.device or not out.is_contiguous():
+        raise ValueError("out must be a contiguous tensor like q")
+    return out
+
+
+def scratch(workspace, nbytes: int, device: torch.device):
+    """A call's workspace: the caller's, or one of its own."""
+    if workspace is None:
+        return torch.empty(max(nbytes, 16), dtype=torch.uint8, device=device)
+    if workspace.device != device or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on {device}")
+    return workspace
 
 
 def cache_desc(k_cache: torch.Tensor, v_cache: torch.Tensor) -> PkvdCache:

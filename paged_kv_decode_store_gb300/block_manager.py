@@ -102,6 +102,38 @@ class BlockManager:
                                               old.shape[1], new.ctypes.data_as(ctypes.c_void_p), got[1]))
         return [new[i, :got[0][i]].tolist() for i in range(n)]
 
+    def reserve(self, num_tokens: int, drafts: int, table):
+        """Room for `drafts` rows behind a sequence's num_tokens: (new table,
+        (src, dst, rows) or None), or (None, None) when too few blocks are free.
+        The blocks are not registered; trim() says what stays."""
+        total = -(-(num_tokens + drafts) // self.bs)
+        t, tptr = _arr(table, max(total - len(table), 0))
+        n = ctypes.c_int32(len(table))
+        cs, cd, cr = ctypes.c_int32(0), ctypes.c_int32(0), ctypes.c_int32(0)
+        st = self._lib.pkvd_bm_reserve(self._h, num_tokens, drafts, tptr, ctypes.byref(n), max(total, len(table)),
+                                       ctypes.byref(cs), ctypes.byref(cd), ctypes.byref(cr))
+        if st == _capi.NO_SPACE:
+            return None, None
+        _capi.check(st)
+        return t[:n.value].tolist(), ((cs.value, cd.value, cr.value) if cs.value >= 0 else None)
+
+    def trim(self, tokens, old_tokens: int, table):
+        """The sequence holds `tokens`, the first old_tokens of which it held before
+        reserve(): the table without the blocks behind them."""
+        t, tptr = _arr(table)
+        toks, tp = _arr(tokens)
+        n = ctypes.c_int32(len(table))
+        _capi.check(self._lib.pkvd_bm_trim(self._h, tp, len(tokens), old_tokens, tptr, ctypes.byref(n)))
+        return t[:n.value].tolist()
+
+    def evict(self, num_tokens: int, table):
+        """The sequence keeps num_tokens rows of no prompt (after an eviction): the
+        table without the blocks behind them.  Refused if a block is shared."""
+        t, tptr = _arr(table)
+        n = ctypes.c_int32(len(table))
+        _capi.check(self._lib.pkvd_bm_evict(self._h, num_tokens, tptr, ctypes.byref(n)))
+        return t[:n.value].tolist()
+
     def release(self, table) -> None:
         t, tp = _arr(table)
         _capi.check(self._lib.pkvd_bm_release(self._h, tp, len(table)))

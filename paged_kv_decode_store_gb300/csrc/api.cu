@@ -636,6 +636,226 @@ pkvd_status pkvd_paged_decode_attention(void* out, const void* q, const pkvd_cac
                                         stream, err_flag, PKVD_PATH_AUTO);
 }
 
+// ------------------------------------------------- drafted trees, eviction
+pkvd_status pkvd_tree_workspace_bytes(int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
+                                      int32_t max_seqlen_q, int32_t sm_count, size_t* bytes) {
+  if (!bytes || num_seqs < 0 || num_q_heads <= 0 || num_kv_heads <= 0 || head_dim <= 0 || max_seqlen_q < 0)
+    return PKVD_INVALID_ARG;
+  if (num_q_heads % num_kv_heads || num_q_heads / num_kv_heads > 128 || max_seqlen_q > kTreeMaxNodes)
+    return PKVD_UNSUPPORTED_SHAPE;
+  if (sm_count <= 0) sm_count = device_sm_count();
+  if (sm_count <= 0) return PKVD_CUDA_ERROR;
+  *bytes = max_seqlen_q == 0 ? 0 : tree_workspace_bytes(num_seqs, num_q_heads, num_kv_heads, head_dim, max_seqlen_q, sm_count);
+  return PKVD_OK;
+}
+
+pkvd_status pkvd_tree_attention(void* out, const void* q, const pkvd_cache* cache, const int32_t* block_tables,
+                                int32_t max_blocks_per_seq, const int32_t* cu_seqlens_q, const int32_t* cu_seqlens_k,
+                                const int32_t* parents, int32_t num_seqs, int32_t total_q, int32_t max_seqlen_q,
+                                int32_t num_q_heads, float scale, int32_t window, const pkvd_score_mod* mod,
+                                void* workspace, size_t workspace_bytes, void* stream, int32_t* err_flag, int32_t path) {
+  if (path != PKVD_PATH_AUTO && path != PKVD_PATH_TC && path != PKVD_PATH_FMA)
+    return path == PKVD_PATH_MMA ? PKVD_UNSUPPORTED_SHAPE : PKVD_INVALID_ARG;
+  if (num_seqs < 0 || total_q < 0 || max_seqlen_q < 0 || window < 0 || !std::isfinite(scale)) return PKVD_INVALID_ARG;
+  ScoreMod sm;
+  if (!score_mod(mod, scale, false, &sm) || (mod && mod->prefix_lens)) return PKVD_INVALID_ARG;
+  const pkvd_status cs = check_cache(cache, false);
+  if (cs != PKVD_OK) return cs;
+  if (num_q_heads <= 0) return PKVD_INVALID_ARG;
+  if (num_q_heads % cache->num_kv_heads || num_q_heads / cache->num_kv_heads > 128) return PKVD_UNSUPPORTED_SHAPE;
+  if (max_seqlen_q > kTreeMaxNodes || num_seqs > 65535) return PKVD_UNSUPPORTED_SHAPE;
+  if (path == PKVD_PATH_TC && cache->dtype == PKVD_F32) return PKVD_UNSUPPORTED_DTYPE;
+  if (num_seqs == 0 || total_q == 0 || max_seqlen_q == 0) return PKVD_OK;
+  if (!out || !q || !block_tables || !cu_seqlens_q || !cu_seqlens_k || !parents || max_blocks_per_seq <= 0)
+    return PKVD_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(out)) return PKVD_UNSUPPORTED_SHAPE;
+  TreeArgs a;
+  a.sms = device_sm_count();
+  if (a.sms <= 0) return PKVD_CUDA_ERROR;
+  const size_t need =
+      tree_workspace_bytes(num_seqs, num_q_heads, cache->num_kv_heads, cache->head_dim, max_seqlen_q, a.sms);
+  if (!workspace || workspace_bytes < need) return PKVD_WORKSPACE_TOO_SMALL;
+  if (reinterpret_cast<uintptr_t>(workspace) & 255u) return PKVD_UNSUPPORTED_SHAPE;
+  a.out = out;
+  a.q = q;
+  a.cache = *cache;
+  a.block_tables = block_tables;
+  a.max_blocks_per_seq = max_blocks_per_seq;
+  a.cu_seqlens_q = cu_seqlens_q;
+  a.cu_seqlens_k = cu_seqlens_k;
+  a.parents = parents;
+  a.num_seqs = num_seqs;
+  a.total_q = total_q;
+  a.max_seqlen_q = max_seqlen_q;
+  a.num_q_heads = num_q_heads;
+  a.scale = scale;
+  a.window = window;
+  a.mod = sm;
+  a.workspace = workspace;
+  a.err = err_flag;
+  const bool tc = path != PKVD_PATH_FMA && tree_tc_supported(a);
+  if (path == PKVD_PATH_TC && !tc) return PKVD_UNSUPPORTED_SHAPE;
+  a.path = tc ? PKVD_PATH_TC : PKVD_PATH_FMA;
+  return from_cuda(launch_tree(a, static_cast<cudaStream_t>(stream)));
+}
+
+pkvd_status pkvd_tree_accept(int32_t* positions, int32_t* first, int32_t* counts, int32_t* tokens,
+                             const int32_t* drafted, const int32_t* parents, const int32_t* target,
+                             const int32_t* cu_seqlens_q, const int32_t* cu_seqlens_k, int32_t num_seqs,
+                             int32_t total_q, int32_t max_path, void* stream, int32_t* err_flag) {
+  if (num_seqs < 0 || total_q < 0 || max_path <= 0) return PKVD_INVALID_ARG;
+  if (num_seqs == 0) return PKVD_OK;
+  if (!positions || !first || !counts || !tokens || !cu_seqlens_q || !cu_seqlens_k) return PKVD_INVALID_ARG;
+  if (total_q > 0 && (!drafted || !parents || !target)) return PKVD_INVALID_ARG;
+  AcceptArgs a;
+  a.drafted = drafted;
+  a.parents = parents;
+  a.target = target;
+  a.cu_q = cu_seqlens_q;
+  a.cu_k = cu_seqlens_k;
+  a.total_q = total_q;
+  a.max_path = max_path;
+  a.positions = positions;
+  a.first = first;
+  a.counts = counts;
+  a.tokens = tokens;
+  a.err = err_flag;
+  return from_cuda(launch_tree_accept(a, num_seqs, static_cast<cudaStream_t>(stream)));
+}
+
+pkvd_status pkvd_compact_cache(const pkvd_cache* cache, const int32_t* block_tables, int32_t max_blocks_per_seq,
+                               const int32_t* new_tables, int32_t new_max_blocks_per_seq, const int32_t* positions,
+                               int64_t pos_stride, int64_t pos_head_stride, const int32_t* counts, const int32_t* first,
+                               int32_t num_seqs, int32_t max_count, void* stream, int32_t* err_flag) {
+  if (num_seqs < 0 || max_count < 0 || pos_stride < 0 || pos_head_stride < 0) return PKVD_INVALID_ARG;
+  const pkvd_status cs = check_cache(cache, false);
+  if (cs != PKVD_OK) return cs;
+  if (num_seqs > 65535 || cache->num_kv_heads > 65535) return PKVD_UNSUPPORTED_SHAPE;
+  if (num_seqs == 0 || max_count == 0) return PKVD_OK;
+  if (!block_tables || !new_tables || !positions || !counts || max_blocks_per_seq <= 0 || new_max_blocks_per_seq <= 0)
+    return PKVD_INVALID_ARG;
+  if (block_tables == new_tables && max_blocks_per_seq != new_max_blocks_per_seq) return PKVD_INVALID_ARG;
+  CompactArgs a;
+  a.k_base = cache->k_base;
+  a.v_base = cache->v_base;
+  a.block_stride = cache->block_stride;
+  a.token_stride = cache->token_stride;
+  a.head_stride = cache->head_stride;
+  a.num_blocks = cache->num_blocks;
+  a.block_size = cache->block_size;
+  a.block_shift = 0;
+  while ((1 << a.block_shift) < cache->block_size) ++a.block_shift;
+  a.head_dim = cache->head_dim;
+  a.elem_bytes = esize(cache->dtype);
+  a.tables = block_tables;
+  a.new_tables = new_tables;
+  a.max_blocks = max_blocks_per_seq;
+  a.new_max_blocks = new_max_blocks_per_seq;
+  auto tokens = [&](int32_t blocks) {
+    const int64_t n = (int64_t)blocks * cache->block_size;
+    return (int)(n < 0x7fffffff ? n : 0x7fffffff);
+  };
+  a.max_tokens = tokens(max_blocks_per_seq);
+  a.new_max_tokens = tokens(new_max_blocks_per_seq);
+  a.positions = positions;
+  a.pos_stride = pos_stride;
+  a.pos_head_stride = pos_head_stride;
+  a.counts = counts;
+  a.first = first;
+  a.max_count = max_count;
+  a.err = err_flag;
+  return from_cuda(launch_compact(a, num_seqs, cache->num_kv_heads, static_cast<cudaStream_t>(stream)));
+}
+
+namespace {
+// The decode call's records, then the rows' statistics, then the scores.
+struct WeightsLayout {
+  size_t stats, scores, bytes;
+  WeightsLayout(size_t records, int64_t rows, int max_context_len) {
+    auto up = [](size_t x) { return (x + 255) / 256 * 256; };
+    stats = up(records);
+    scores = stats + up((size_t)rows * 2 * sizeof(float));
+    bytes = scores + (size_t)rows * (size_t)score_row(max_context_len) * sizeof(float);
+  }
+};
+}  // namespace
+
+pkvd_status pkvd_decode_weights_workspace_bytes(int32_t num_seqs, int32_t num_q_heads, int32_t head_dim,
+                                                int32_t max_context_len, int32_t sm_count, size_t* bytes) {
+  size_t records = 0;
+  const pkvd_status s = pkvd_decode_workspace_bytes(num_seqs, num_q_heads, head_dim, max_context_len, sm_count, &records);
+  if (s != PKVD_OK || !bytes) return s == PKVD_OK ? PKVD_INVALID_ARG : s;
+  *bytes = WeightsLayout(records, (int64_t)num_seqs * num_q_heads, max_context_len).bytes;
+  return PKVD_OK;
+}
+
+pkvd_status pkvd_paged_decode_attention_weights(void* out, const void* q, const pkvd_cache* cache,
+                                                const int32_t* block_tables, int32_t max_blocks_per_seq,
+                                                const int32_t* context_lens, int32_t max_context_len, int32_t num_seqs,
+                                                int32_t num_q_heads, float scale, int32_t window,
+                                                const pkvd_score_mod* mod, float* weights_out, const float* weights,
+                                                int64_t seq_stride, int64_t head_stride, int32_t weight_heads,
+                                                void* workspace, size_t workspace_bytes, void* stream,
+                                                int32_t* err_flag, int32_t path) {
+  if (window < 0) return PKVD_INVALID_ARG;
+  if (mod && mod->prefix_lens && window > 0 && window < max_context_len) return PKVD_INVALID_ARG;
+  ScoreMod sm;
+  if (!score_mod(mod, scale, false, &sm)) return PKVD_INVALID_ARG;
+  int grid = 0;
+  size_t records = 0;
+  const pkvd_status vs = attention_validate(out, q, cache, block_tables, max_blocks_per_seq, context_lens,
+                                            max_context_len, num_seqs, num_q_heads, scale, window, &path, &grid,
+                                            &records);
+  if (vs != PKVD_OK) return vs;
+  if (weight_heads != 1 && weight_heads != cache->num_kv_heads) return PKVD_INVALID_ARG;
+  if (num_seqs == 0) return PKVD_OK;
+  if (num_seqs > 65535) return PKVD_UNSUPPORTED_SHAPE;
+  if (!weights || !weights_out || seq_stride < 0 || head_stride < 0) return PKVD_INVALID_ARG;
+  if ((num_seqs > 1 && seq_stride < max_context_len) || (weight_heads > 1 && head_stride < max_context_len))
+    return PKVD_INVALID_ARG;
+  if (reinterpret_cast<uintptr_t>(weights) % 4 || reinterpret_cast<uintptr_t>(weights_out) % 4) return PKVD_UNSUPPORTED_SHAPE;
+  const int64_t rows = (int64_t)num_seqs * num_q_heads;
+  const WeightsLayout lay(records, rows, max_context_len);
+  if (!workspace || workspace_bytes < lay.bytes) return PKVD_WORKSPACE_TOO_SMALL;
+  if (reinterpret_cast<uintptr_t>(workspace) & 255u) return PKVD_UNSUPPORTED_SHAPE;
+  AttnArgs a = attn_args(out, q, cache, block_tables, max_blocks_per_seq, context_lens, max_context_len, num_seqs,
+                         num_q_heads, scale, window, workspace, err_flag, grid, path, sm);
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  a.stats = reinterpret_cast<float*>(ws + lay.stats);
+  a.scores = reinterpret_cast<float*>(ws + lay.scores);
+  a.score_ld = score_row(max_context_len);
+  const WeightArgs w{weights, weights_out, seq_stride, head_stride, weight_heads};
+  return from_cuda(launch_attention_weights(a, w, static_cast<cudaStream_t>(stream)));
+}
+
+pkvd_status pkvd_evict_select(int32_t* positions, int32_t* counts, float* weights_out, const float* weights,
+                              int64_t seq_stride, int64_t head_stride, int32_t length, const int32_t* context_lens,
+                              int32_t num_seqs, int32_t heads, int32_t keep, int32_t sink, int32_t recent, void* stream,
+                              int32_t* err_flag) {
+  if (num_seqs < 0 || heads <= 0 || length <= 0 || keep <= 0 || sink < 0 || recent < 0 || seq_stride < 0 || head_stride < 0)
+    return PKVD_INVALID_ARG;
+  if ((int64_t)sink + recent > keep) return PKVD_INVALID_ARG;
+  if (num_seqs > 65535) return PKVD_UNSUPPORTED_SHAPE;
+  if (num_seqs == 0) return PKVD_OK;
+  if (!positions || !counts || !weights || !context_lens) return PKVD_INVALID_ARG;
+  if ((num_seqs > 1 && seq_stride < length) || (heads > 1 && head_stride < length)) return PKVD_INVALID_ARG;
+  if (reinterpret_cast<uintptr_t>(weights) % 4 || reinterpret_cast<uintptr_t>(weights_out) % 4) return PKVD_UNSUPPORTED_SHAPE;
+  EvictArgs a;
+  a.weights = weights;
+  a.weights_out = weights_out;
+  a.seq_stride = seq_stride;
+  a.head_stride = head_stride;
+  a.length = length;
+  a.context_lens = context_lens;
+  a.keep = keep;
+  a.sink = sink;
+  a.recent = recent;
+  a.positions = positions;
+  a.counts = counts;
+  a.err = err_flag;
+  return from_cuda(launch_evict_select(a, num_seqs, heads, static_cast<cudaStream_t>(stream)));
+}
+
 pkvd_status pkvd_sample_workspace_bytes(int32_t num_rows, int32_t vocab, size_t* bytes) {
   if (!bytes || num_rows < 0 || vocab <= 0) return PKVD_INVALID_ARG;
   *bytes = (size_t)num_rows * kRowInfo * sizeof(int32_t);     // per-row cut parameters (extras only)

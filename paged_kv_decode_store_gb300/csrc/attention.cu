@@ -79,6 +79,9 @@ PartParams part_params(const AttnArgs& a, float* rec) {
   pp.rows_contig = a.head_stride == a.head_dim ? 1 : 0;
   pp.active_warps = a.num_kv_heads == 16 ? kConsumerWarps : a.num_kv_heads;
   pp.mod = a.mod;
+  pp.scores = a.scores;
+  pp.score_ld = a.score_ld;
+  pp.stats = reinterpret_cast<float2*>(a.stats);
   return pp;
 }
 
@@ -87,13 +90,17 @@ cudaError_t launch_attention(const AttnArgs& a, cudaStream_t stream) {
   const int G = a.num_q_heads / a.num_kv_heads;
   float* rec = static_cast<float*>(a.workspace);
   if (a.grid > 0) {
-    PartParams pp = part_params(a, rec);    const int hpw = a.num_kv_heads == 16 ? 2 : 1;
+    PartParams pp = part_params(a, rec);
+    const int hpw = a.num_kv_heads == 16 ? 2 : 1;
     pp.active_warps = hpw == 2 ? kConsumerWarps : a.num_kv_heads;
     const size_t smem = smem_header_bytes() + (size_t)pp.stages * 2 * kChunk * pp.rowb;
     const int gmax = group_bound(G);
     cudaError_t e;
     const bool mod = a.mod.on();
-    const auto run = a.dtype == PKVD_F32   ? (mod ? partition_mod_f32 : partition_f32)
+    const auto run = a.scores ? (a.dtype == PKVD_F32   ? partition_scores_f32
+                                 : a.dtype == PKVD_F16 ? partition_scores_f16
+                                                       : partition_scores_bf16)
+                     : a.dtype == PKVD_F32 ? (mod ? partition_mod_f32 : partition_f32)
                      : a.dtype == PKVD_F16 ? (mod ? partition_mod_f16 : partition_f16)
                                            : (mod ? partition_mod_bf16 : partition_bf16);
     e = run(pp, a.head_dim, hpw, gmax, a.path, a.grid, smem, stream);
@@ -113,14 +120,15 @@ cudaError_t launch_attention(const AttnArgs& a, cudaStream_t stream) {
   const int parts = pieces > 16 ? 4 : pieces > 8 ? 2 : 1;
   const int groups = (a.num_q_heads * (a.head_dim / 4) * parts + 255) / 256;
   const dim3 mg((unsigned)a.num_seqs, (unsigned)groups), mb(256);
-  if (a.dtype == PKVD_F32)
-    return launch_pdl(lse_merge_kernel<float>, mg, mb, 0, stream, static_cast<float*>(a.out), (const float*)rec,
-                      a.context_lens, ctx_cap, a.window, a.num_seqs, a.num_q_heads, a.head_dim, a.grid, parts);
-  if (a.dtype == PKVD_F16)
-    return launch_pdl(lse_merge_kernel<__half>, mg, mb, 0, stream, static_cast<__half*>(a.out), (const float*)rec,
-                      a.context_lens, ctx_cap, a.window, a.num_seqs, a.num_q_heads, a.head_dim, a.grid, parts);
-  return launch_pdl(lse_merge_kernel<__nv_bfloat16>, mg, mb, 0, stream, static_cast<__nv_bfloat16*>(a.out),
-                    (const float*)rec, a.context_lens, ctx_cap, a.window, a.num_seqs, a.num_q_heads, a.head_dim, a.grid, parts);
+  const auto merge = [&](auto type) {
+    using T = decltype(type);
+    return launch_pdl(a.scores ? lse_merge_kernel<T, true> : lse_merge_kernel<T, false>, mg, mb, 0, stream,
+                      static_cast<T*>(a.out), (const float*)rec, a.context_lens, ctx_cap, a.window, a.num_seqs,
+                      a.num_q_heads, a.head_dim, a.grid, parts, reinterpret_cast<float2*>(a.stats));
+  };
+  if (a.dtype == PKVD_F32) return merge(float());
+  if (a.dtype == PKVD_F16) return merge(__half());
+  return merge(__nv_bfloat16());
 }
 
 }  // namespace pkvd

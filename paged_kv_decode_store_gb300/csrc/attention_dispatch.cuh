@@ -1,13 +1,13 @@
 // Per-dtype instantiation of the partition kernel for every supported
 // (head_dim, heads-per-warp, group bound, path) combination, without and with
-// score modifiers (MOD).  Each dtype lives in its own translation unit so the build compiles them in parallel.
+// score modifiers (MOD = 0, 1) and with the scores handed on (2).  Each dtype lives in its own translation unit so the build compiles them in parallel.
 #pragma once
 
 #include "attention_kernels.cuh"
 
 namespace pkvd {
 
-template <typename T, int D, int HPW, bool MOD>
+template <typename T, int D, int HPW, int MOD>
 cudaError_t dispatch_fma_g(const PartParams& pp, int gmax, int grid, size_t smem, cudaStream_t st) {
   switch (gmax) {
     case 1: return launch_partition<T, D, FmaConsumer<T, D, HPW, 1, MOD>>(pp, grid, smem, st);
@@ -17,7 +17,7 @@ cudaError_t dispatch_fma_g(const PartParams& pp, int gmax, int grid, size_t smem
   }
 }
 
-template <typename T, int D, bool MOD>
+template <typename T, int D, int MOD>
 cudaError_t dispatch_d(const PartParams& pp, int hpw, int gmax, int path, int grid, size_t smem,
                        cudaStream_t st) {
   if constexpr (sizeof(T) == 2) {
@@ -33,7 +33,7 @@ cudaError_t dispatch_d(const PartParams& pp, int hpw, int gmax, int path, int gr
   }
 }
 
-template <typename T, bool MOD>
+template <typename T, int MOD>
 cudaError_t dispatch_partition(const PartParams& pp, int D, int hpw, int gmax, int path, int grid,
                                size_t smem, cudaStream_t st) {
   return D == 64 ? dispatch_d<T, 64, MOD>(pp, hpw, gmax, path, grid, smem, st)
@@ -47,5 +47,9 @@ cudaError_t partition_bf16(const PartParams&, int, int, int, int, int, size_t, c
 cudaError_t partition_mod_f32(const PartParams&, int, int, int, int, int, size_t, cudaStream_t);
 cudaError_t partition_mod_f16(const PartParams&, int, int, int, int, int, size_t, cudaStream_t);
 cudaError_t partition_mod_bf16(const PartParams&, int, int, int, int, int, size_t, cudaStream_t);
+// and with every key's score handed on
+cudaError_t partition_scores_f32(const PartParams&, int, int, int, int, int, size_t, cudaStream_t);
+cudaError_t partition_scores_f16(const PartParams&, int, int, int, int, int, size_t, cudaStream_t);
+cudaError_t partition_scores_bf16(const PartParams&, int, int, int, int, int, size_t, cudaStream_t);
 
 }  // namespace pkvd

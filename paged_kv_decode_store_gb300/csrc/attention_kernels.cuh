@@ -71,6 +71,11 @@ struct PartParams {
   int rows_contig;     // heads of a token row adjacent in memory
   int active_warps;    // consumer warps that own heads
   ScoreMod mod;        // read by the MOD consumers only
+  // read by the consumers that hand their scores on (MOD = 2): scores
+  // [num_seqs][hq][score_ld] in log2 units, and every row's statistics [num_seqs][hq]
+  float* scores;
+  int64_t score_ld;
+  float2* stats;
 };
 
 // The partition kernel's parameters for a call (attention.cu); `rec` is the
@@ -126,12 +131,22 @@ struct SmemHdr {
   int abort_flag;
 };
 
+// A row's statistics as the keys' weights need them: the maximum and one over
+// the sum; a row without a readable key gives its keys nothing.
+__device__ __forceinline__ float2 row_stats(float m, float l) {
+  return l > 0.f ? make_float2(m, 1.f / l) : make_float2(0.f, 0.f);
+}
+
 // ----------------------------------------------------------- consumers
-// Consumers come without and with score modifiers (MOD): the second kind
-// knows how far a chunk's first token lies behind the new one (dist0).
-template <typename T, int D, int HPW, int GMAX, bool MOD = false>
+// Consumers come without (MOD = 0) and with score modifiers (1, 2): these
+// know how far a chunk's first token lies behind the new one (dist0).  MOD = 2
+// also leaves every key's score (`srow`: of the chunk's first token, head 0)
+// and a row's maximum and sum, from which attention_weights.cu counts what each
+// key was given.
+template <typename T, int D, int HPW, int GMAX, int MOD = 0>
 struct FmaConsumer {
-  static constexpr bool kMod = MOD;
+  static constexpr bool kMod = MOD != 0;
+  static constexpr bool kScores = MOD == 2;
   static constexpr int ESZ = sizeof(T);
   static constexpr int VEC = 16 / ESZ;
   static constexpr int LPT = D * ESZ / 16;   // lanes per token row of one head
@@ -173,7 +188,7 @@ struct FmaConsumer {
   }
 
   __device__ void chunk(const PartParams& p, const uint8_t* sK, const uint8_t* sV, int ntok,
-                        int warp, int lane, int dist0) {
+                        int warp, int lane, int dist0, float* srow) {
     const int grp = lane / LPT, li = lane % LPT;
 #pragma unroll
     for (int j = 0; j < HPW; ++j) {
@@ -196,6 +211,9 @@ struct FmaConsumer {
           if constexpr (MOD)
             d = fmaf(slope[j][g], (float)(dist0 - t), capped<std::is_same<T, float>::value>(d, p.scale_log2, p.mod));
           s[g] = d;
+          if constexpr (kScores) {
+            if (valid && li == 0 && g < p.G) srow[(hk * p.G + g) * p.score_ld + t] = d;
+          }
         }
         if (valid) {
           float vf[VEC];
@@ -250,6 +268,9 @@ struct FmaConsumer {
 #pragma unroll
             for (int v = 0; v < VEC; ++v) tmp[v] = DT<T>::from_f(acc[j][g][v] * inv);
             *reinterpret_cast<uint4*>(o) = *reinterpret_cast<const uint4*>(tmp);
+            if constexpr (kScores) {
+              if (li == 0) p.stats[(int64_t)seq * p.hq + h] = row_stats(m[j][g], l[j][g]);
+            }
           } else {
             const int slot = (flags & F_SLOT1) ? 1 : 0;
             float* r = p.rec + ((int64_t)(cta * 2 + slot) * p.hq + h) * (D + 4);
@@ -266,9 +287,10 @@ struct FmaConsumer {
   }
 };
 
-template <typename T, int D, int HPW, bool MOD = false>
+template <typename T, int D, int HPW, int MOD = 0>
 struct MmaConsumer {
-  static constexpr bool kMod = MOD;
+  static constexpr bool kMod = MOD != 0;
+  static constexpr bool kScores = MOD == 2;
   static constexpr int ESZ = sizeof(T);
   static constexpr int KS = D / 16;     // k-steps of QK^T, m-tiles of V^T P^T
   static_assert(ESZ == 2, "tensor-core path is for 16-bit caches");
@@ -302,7 +324,8 @@ struct MmaConsumer {
     }
   }
 
-  __device__ void chunk(const PartParams& p, uint8_t* sK, uint8_t* sV, int ntok, int warp, int lane, int dist0) {
+  __device__ void chunk(const PartParams& p, uint8_t* sK, uint8_t* sV, int ntok, int warp, int lane, int dist0,
+                        float* srow) {
     const int lr = lane >> 2;
     // ldmatrix row/column providers: A = K tile (row-major, rows = tokens)
     const int a_row = (lane & 7) + ((lane >> 3) & 1) * 8;
@@ -343,6 +366,13 @@ struct MmaConsumer {
       } else {
 #pragma unroll
         for (int e = 0; e < 4; ++e) s[e] *= sl;
+      }
+      if constexpr (kScores) {         // eight tokens of a head: a whole 32-byte sector
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int g = 2 * (lane & 3) + (e & 1), t = lr + (e >> 1) * 8;
+          if (g < p.G && t < ntok) srow[(hk * p.G + g) * p.score_ld + t] = s[e];
+        }
       }
       const float x0 = lr < ntok ? s[0] : -INFINITY;
       const float x1 = lr < ntok ? s[1] : -INFINITY;
@@ -408,6 +438,13 @@ struct MmaConsumer {
           if (gB < p.G) {
             ob[gB * D + d0] = DT<T>::from_f(acc[j][mt][1] * iB);
             ob[gB * D + d0 + 8] = DT<T>::from_f(acc[j][mt][3] * iB);
+          }
+        }
+        if constexpr (kScores) {
+          if (lr == 0) {
+            float2* st = p.stats + (int64_t)seq * p.hq + hk * p.G;
+            if (gA < p.G) st[gA] = row_stats(m[j][0], lA);
+            if (gB < p.G) st[gB] = row_stats(m[j][1], lB);
           }
         }
       } else {
@@ -650,11 +687,20 @@ __global__ void __launch_bounds__(kAttnThreads, 1) paged_decode_partition_kernel
     uint8_t* sK = stage_base + stage * stage_bytes;
     uint8_t* sV = sK + kChunk * p.rowb;
     int dist0 = 0;                     // from the chunk's first token to the row's newest
+    float* srow = nullptr;
     if constexpr (Consumer::kMod) {
       const int c = min(max(p.ctx[seq], 0), p.ctx_cap);
       dist0 = c - 1 - window_start(c, p.window) - (int)(c0 + it - row_start) * kChunk;
+      if constexpr (Consumer::kScores) {
+        srow = p.scores + (int64_t)seq * p.hq * p.score_ld + (c - 1 - dist0);
+        if (ntok == 0) {               // a bad block: its keys are given nothing
+          const int heads = p.hq / p.active_warps, n = min(dist0 + 1, kChunk);
+          for (int k = lane; k < heads * kChunk; k += 32)
+            if (k % kChunk < n) srow[(warp * heads + k / kChunk) * p.score_ld + k % kChunk] = -INFINITY;
+        }
+      }
     }
-    if (ntok > 0) cons.chunk(p, sK, sV, ntok, warp, lane, dist0);
+    if (ntok > 0) cons.chunk(p, sK, sV, ntok, warp, lane, dist0, srow);
     __syncwarp();
     if (lane == 0) mbar_arrive(&hdr.empty[stage]);
     if (flags & F_LAST) cons.finish(p, seq, flags, cta, warp, lane, row_start, nrow, C, grid);
@@ -672,10 +718,12 @@ __global__ void __launch_bounds__(kAttnThreads, 1) paged_decode_partition_kernel
 // loads are issued before any is used (one L2 round trip per chunk).
 constexpr int kMaxMergeRecords = 1024;     // >= any partition grid (one CTA per SM)
 
-template <typename T>
+// STATS: the merged rows' statistics go to `stats` too.
+template <typename T, bool STATS = false>
 __global__ void __launch_bounds__(256) lse_merge_kernel(T* __restrict__ out, const float* __restrict__ rec,
                                                         const int32_t* __restrict__ ctx, int ctx_cap, int window,
-                                                        int num_seqs, int hq, int D, int grid, int parts) {
+                                                        int num_seqs, int hq, int D, int grid, int parts,
+                                                        float2* __restrict__ stats) {
   __shared__ int s_rec[kMaxMergeRecords];
   __shared__ int s_n;
   __shared__ long long s_part[2][8];
@@ -803,6 +851,9 @@ __global__ void __launch_bounds__(256) lse_merge_kernel(T* __restrict__ out, con
     }
     if (live && part == 0) {
       const float inv = 1.f / L;
+      if constexpr (STATS) {
+        if (d4 == 0) stats[(int64_t)i * hq + h] = row_stats(M, L);
+      }
       T* dst = orow + h * D + d4;
       dst[0] = DT<T>::from_f(o.x * inv);
       dst[1] = DT<T>::from_f(o.y * inv);

@@ -4,6 +4,6 @@
 namespace pkvd {
 cudaError_t partition_mod_f32(const PartParams& pp, int D, int hpw, int gmax, int path, int grid, size_t smem,
                          cudaStream_t st) {
-  return dispatch_partition<float, true>(pp, D, hpw, gmax, path, grid, smem, st);
+  return dispatch_partition<float, 1>(pp, D, hpw, gmax, path, grid, smem, st);
 }
 }  // namespace pkvd

@@ -22,6 +22,9 @@
 // * a token written into a shared last block (count > 1) first gets a fresh
 //   copy of it (the caller copies the rows with pkvd_copy_blocks); a block
 //   that becomes full registers its key.
+// * drafted rows get blocks that are registered only when accepted tokens fill
+//   them; what an eviction leaves is no prompt's: its blocks and those filled
+//   behind them are never registered (opaque) until they are handed out again.
 // * a request that needs more free blocks than there are changes nothing.
 #include <cstdint>
 #include <cstring>
@@ -42,9 +45,10 @@ struct pkvd_block_manager {
   std::vector<std::string> key_of;      // empty: not registered
   std::unordered_map<std::string, int32_t> cache;
   std::vector<int32_t> uses;            // pkvd_bm_reorder's counts, all 0 between calls
+  std::vector<uint8_t> opaque;          // rows that are no prompt's (an eviction's, or behind such a block)
 
   pkvd_block_manager(int32_t n, int32_t b)
-      : nb(n), bs(b), ref(n, 0), prev(n, -1), next(n, -1), in_free(n, 0), key_of(n), uses(n, 0) {
+      : nb(n), bs(b), ref(n, 0), prev(n, -1), next(n, -1), in_free(n, 0), key_of(n), uses(n, 0), opaque(n, 0) {
     for (int32_t i = 0; i < n; ++i) push_back(i);
   }
   void push_back(int32_t b) {
@@ -78,11 +82,20 @@ struct pkvd_block_manager {
       cache.erase(key_of[b]);
       key_of[b].clear();
     }
+    opaque[b] = 0;
     ref[b] = 1;
     return b;
   }
+  void forget(int32_t b) {              // its key no longer says what it holds
+    if (key_of[b].empty()) return;
+    cache.erase(key_of[b]);
+    key_of[b].clear();
+  }
   // Without memory for its key a block stays unregistered: no later prompt finds it.
+  // One that follows an opaque block is opaque itself.
   void register_block(int32_t b, int32_t parent, const int32_t* tokens) noexcept {
+    if (parent >= 0 && opaque[parent]) opaque[b] = 1;
+    if (opaque[b]) return;
     try {
       std::string k = key(parent, tokens);
       if (cache.count(k)) return;       // an equal block is registered: keep the first
@@ -179,6 +192,7 @@ pkvd_status pkvd_bm_append(pkvd_block_manager* bm, const int32_t* tokens, int32_
     if (bm->ref[last] > 1) {            // shared: copy before writing
       if (bm->nfree == 0) return PKVD_NO_SPACE;
       const int32_t b = bm->take();
+      bm->opaque[b] = bm->opaque[last];
       --bm->ref[last];
       *copy_src = last;
       *copy_dst = b;
@@ -190,6 +204,73 @@ pkvd_status pkvd_bm_append(pkvd_block_manager* bm, const int32_t* tokens, int32_
     const int32_t i = p / bs;
     bm->register_block(block_table[i], i > 0 ? block_table[i - 1] : -1, tokens + (int64_t)i * bs);
   }
+  return PKVD_OK;
+}
+
+// Every block of a table is held.
+static bool held(const pkvd_block_manager* bm, const int32_t* block_table, int32_t n) {
+  for (int32_t i = 0; i < n; ++i)
+    if (block_table[i] < 0 || block_table[i] >= bm->nb || bm->ref[block_table[i]] <= 0) return false;
+  return true;
+}
+
+pkvd_status pkvd_bm_reserve(pkvd_block_manager* bm, int32_t num_tokens, int32_t drafts, int32_t* block_table,
+                            int32_t* num_blocks, int32_t max_blocks, int32_t* copy_src, int32_t* copy_dst,
+                            int32_t* copy_rows) {
+  if (!bm || !block_table || !num_blocks || !copy_src || !copy_dst || !copy_rows || num_tokens < 0 || drafts < 0)
+    return PKVD_INVALID_ARG;
+  const int32_t bs = bm->bs, n = *num_blocks;
+  const int64_t have = ((int64_t)num_tokens + bs - 1) / bs, want = ((int64_t)num_tokens + drafts + bs - 1) / bs;
+  if (n != have || want > max_blocks || !held(bm, block_table, n)) return PKVD_INVALID_ARG;
+  *copy_src = *copy_dst = -1;
+  *copy_rows = 0;
+  if (drafts == 0) return PKVD_OK;
+  const bool partial = num_tokens % bs != 0, copy = partial && bm->ref[block_table[n - 1]] > 1;
+  if (want - have + (copy ? 1 : 0) > bm->nfree) return PKVD_NO_SPACE;
+  if (copy) {
+    const int32_t last = block_table[n - 1], b = bm->take();
+    --bm->ref[last];
+    bm->opaque[b] = bm->opaque[last];
+    *copy_src = last;
+    *copy_dst = b;
+    *copy_rows = num_tokens % bs;
+    block_table[n - 1] = b;
+  }
+  for (int64_t i = have; i < want; ++i) block_table[i] = bm->take();
+  *num_blocks = (int32_t)want;
+  return PKVD_OK;
+}
+
+pkvd_status pkvd_bm_trim(pkvd_block_manager* bm, const int32_t* tokens, int32_t num_tokens, int32_t old_tokens,
+                         const int32_t* block_table, int32_t* num_blocks) {
+  if (!bm || !block_table || !num_blocks || num_tokens < 0 || old_tokens < 0 || old_tokens > num_tokens ||
+      (num_tokens > 0 && !tokens))
+    return PKVD_INVALID_ARG;
+  const int32_t bs = bm->bs, n = *num_blocks;
+  const int32_t stay = (int32_t)(((int64_t)num_tokens + bs - 1) / bs);
+  if (n < stay || !held(bm, block_table, n)) return PKVD_INVALID_ARG;
+  for (int32_t i = old_tokens / bs; i < num_tokens / bs; ++i)
+    bm->register_block(block_table[i], i > 0 ? block_table[i - 1] : -1, tokens + (int64_t)i * bs);
+  for (int32_t i = n - 1; i >= stay; --i)
+    if (--bm->ref[block_table[i]] == 0) bm->push_back(block_table[i]);
+  *num_blocks = stay;
+  return PKVD_OK;
+}
+
+pkvd_status pkvd_bm_evict(pkvd_block_manager* bm, int32_t num_tokens, const int32_t* block_table, int32_t* num_blocks) {
+  if (!bm || !num_blocks || num_tokens < 1 || *num_blocks < 0 || !block_table) return PKVD_INVALID_ARG;
+  const int32_t n = *num_blocks, stay = (int32_t)(((int64_t)num_tokens + bm->bs - 1) / bm->bs);
+  if (n < stay || !held(bm, block_table, n)) return PKVD_INVALID_ARG;
+  for (int32_t i = 0; i < n; ++i)
+    if (bm->ref[block_table[i]] != 1) return PKVD_INVALID_ARG;
+  // (a block that stays is opaque; one behind them followed rows that are gone)
+  for (int32_t i = 0; i < n; ++i) {
+    bm->forget(block_table[i]);
+    bm->opaque[block_table[i]] = i < stay;
+  }
+  for (int32_t i = n - 1; i >= stay; --i)
+    if (--bm->ref[block_table[i]] == 0) bm->push_back(block_table[i]);
+  *num_blocks = stay;
   return PKVD_OK;
 }
 

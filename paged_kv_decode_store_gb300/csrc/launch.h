@@ -51,7 +51,96 @@ struct AttnArgs {
   int path;           // PKVD_PATH_FMA / PKVD_PATH_MMA (resolved)
   int window;         // > 0: sliding window of the newest `window` positions
   ScoreMod mod;
+  // Set where every key's score is handed on (launch_attention_weights): scores
+  // [num_seqs][num_q_heads][score_ld], pairs (maximum, 1 / sum) [num_seqs][num_q_heads]
+  float* scores = nullptr;
+  int64_t score_ld = 0;
+  float* stats = nullptr;
 };
+
+// Decode attention that also counts what each key was given (attention_weights.cu).
+struct WeightArgs {
+  const float* in;         // [num_seqs][heads][length], rows at these strides
+  float* out;
+  int64_t seq_stride, head_stride;
+  int heads;               // 1 or the KV heads
+};
+int64_t score_row(int max_context_len);      // scores of one head's row in the workspace
+cudaError_t launch_attention_weights(const AttnArgs& a, const WeightArgs& w, cudaStream_t stream);
+
+// Rows of the cache close up (compact.cu).
+struct CompactArgs {
+  void* k_base;
+  void* v_base;
+  int64_t block_stride, token_stride, head_stride, num_blocks;   // elements
+  int block_size, block_shift, head_dim, elem_bytes;
+  const int32_t* tables;
+  const int32_t* new_tables;    // the same pointer: in place
+  int max_blocks, new_max_blocks;
+  int max_tokens, new_max_tokens;
+  const int32_t* positions;     // strides in elements; head stride 0: alike for all heads
+  int64_t pos_stride, pos_head_stride;
+  const int32_t* counts;
+  const int32_t* first;         // or null: 0
+  int max_count;
+  int32_t* err;
+};
+cudaError_t launch_compact(const CompactArgs& a, int num_seqs, int num_kv_heads, cudaStream_t stream);
+
+// Which positions stay (evict.cu).
+struct EvictArgs {
+  const float* weights;         // [num_seqs][heads][length]
+  float* weights_out;           // or null
+  int64_t seq_stride, head_stride;
+  int length;
+  const int32_t* context_lens;
+  int keep, sink, recent;
+  int32_t* positions;           // [num_seqs][heads][keep]
+  int32_t* counts;              // [num_seqs]
+  int32_t* err;
+};
+cudaError_t launch_evict_select(const EvictArgs& a, int num_seqs, int heads, cudaStream_t stream);
+
+// Attention of drafted trees (tree.cu, tree_tc.cu).
+constexpr int kTreeMaxNodes = 256;    // nodes of a sequence's tree
+constexpr int kTreeKeys = 128;        // keys of a tile
+struct TreeArgs {
+  void* out;
+  const void* q;
+  pkvd_cache cache;
+  const int32_t* block_tables;
+  int max_blocks_per_seq;
+  const int32_t* cu_seqlens_q;
+  const int32_t* cu_seqlens_k;
+  const int32_t* parents;
+  int num_seqs, total_q, max_seqlen_q, num_q_heads;
+  float scale;
+  int window;
+  ScoreMod mod;
+  void* workspace;
+  int32_t* err;
+  int path;                // PKVD_PATH_FMA / PKVD_PATH_TC (resolved)
+  int sms;
+};
+bool tree_tc_supported(const TreeArgs& a);
+size_t tree_workspace_bytes(int num_seqs, int num_q_heads, int num_kv_heads, int head_dim, int max_seqlen_q, int sms);
+cudaError_t launch_tree(const TreeArgs& a, cudaStream_t stream);
+
+// Which drafted nodes the target's choices follow (tree.cu).
+struct AcceptArgs {
+  const int32_t* drafted;
+  const int32_t* parents;
+  const int32_t* target;
+  const int32_t* cu_q;
+  const int32_t* cu_k;
+  int total_q, max_path;
+  int32_t* positions;      // [num_seqs][max_path]
+  int32_t* first;
+  int32_t* counts;
+  int32_t* tokens;         // [num_seqs][max_path]
+  int32_t* err;
+};
+cudaError_t launch_tree_accept(const AcceptArgs& a, int num_seqs, cudaStream_t stream);
 
 int attention_grid(int num_seqs, int max_context_len, int sm_count);
 size_t attention_workspace_bytes(int num_seqs, int num_q_heads, int head_dim, int grid);

@@ -1,0 +1,549 @@
+// Attention for trees of drafted tokens over the paged cache: the plan, the
+// fp32 kernel and the merge; and the walk that says which drafts stay.
+//
+// Node t of sequence i's tree is its drafted row t, stored behind the cached
+// tokens (position cached_i + t of the block table); parents[t] < t, or -1 for
+// one that follows the cached context directly.  With depth(t) its ancestors'
+// number, query head h of KV head hk = h / G:
+//   out[t,h] = sum_j softmax_j(mod(scale <q[t,h], K_j>)) V_j
+// over the cached keys (j < cached_i) and t's ancestors and t itself.  Token
+// positions are cached_i + depth; a window and a distance bias count those.
+//
+// The plan kernel turns parents into one bit a (node, ancestor) -- the window
+// applied, so that a set bit is a visible key and the number of bits above one
+// is its distance -- and sums up the batch's pieces (tree_plan.cuh).
+//
+// The fp32 kernel (fp32 caches, 16-bit ones whose layout the tensor cores'
+// copies cannot walk) keeps 32 keys of K and V in shared memory and four query
+// rows a warp: lane j scores key j, then owns D / 32 dims of the sums.  Bound by
+// shared-memory reads (eight per sixteen multiply-adds).
+#include "score_mod.cuh"
+#include "tree_plan.cuh"
+
+namespace pkvd {
+
+cudaError_t launch_tree_tc(const TreeArgs& a, const TreePlan& plan, cudaStream_t stream);   // tree_tc.cu
+
+namespace {
+
+constexpr int kPlanThreads = 256;
+static_assert(kPlanThreads >= kTreeMaxNodes, "a thread a node");
+
+// CTA i < num_seqs: sequence i's ancestors.  The last one: the pieces before
+// every sequence.
+__global__ void __launch_bounds__(kPlanThreads) tree_plan_kernel(const TreePlan p, const int32_t* __restrict__ parents,
+                                                                 int32_t* err) {
+  __shared__ int up[kTreeMaxNodes];
+  __shared__ uint32_t bits[kTreeMaxNodes][kTreeMaxNodes / 32 + 1];
+  __shared__ int64_t warp_sum[kPlanThreads / 32];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if ((int)blockIdx.x == p.num_seqs) {
+    pdl_wait();        // a call before this one may still read the workspace
+    pdl_trigger();
+    int64_t running = 0;
+    for (int base = 0; base < p.num_seqs; base += kPlanThreads) {
+      const int i = base + tid;
+      const int64_t mine = i < p.num_seqs ? tree_seq(p, i).pieces(p.hkv) : 0;
+      int64_t upto = mine;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int64_t t = __shfl_up_sync(FULL_MASK, upto, o);
+        if (lane >= o) upto += t;
+      }
+      if (lane == 31) warp_sum[warp] = upto;
+      __syncthreads();
+      int64_t before = running;
+      for (int w = 0; w < kPlanThreads / 32; ++w) {
+        if (w < warp) before += warp_sum[w];
+        running += warp_sum[w];
+      }
+      if (i < p.num_seqs) p.starts[i] = before + upto - mine;
+      __syncthreads();
+    }
+    if (tid == 0) p.starts[p.num_seqs] = running;
+    return;
+  }
+  const int i = blockIdx.x;
+  const TreeSeq s = tree_seq(p, i);
+  if (s.n < 0 && tid == 0) flag_error(err, PKVD_ERR_CONTEXT);
+  int depth = -1;
+  if (tid < s.n) {
+    int u = parents[s.q0 + tid];
+    if (u < -1 || u >= tid) {
+      flag_error(err, PKVD_ERR_TREE);
+      u = -1;
+    }
+    up[tid] = u;
+  }
+  for (int w = 0; w < p.words; ++w) bits[tid][w] = 0u;
+  __syncthreads();
+  if (tid < s.n)
+    for (int u = tid; u >= 0; u = up[u]) {
+      ++depth;
+      if (p.window <= 0 || depth < p.window) bits[tid][u >> 5] |= 1u << (u & 31);
+    }
+  pdl_wait();
+  pdl_trigger();
+  if (tid < s.n) {
+    const int64_t row = (int64_t)i * p.max_q + tid;
+    p.depth[row] = depth;
+    for (int w = 0; w < p.words; ++w) p.anc[row * p.words + w] = bits[tid][w];
+  }
+}
+
+// ------------------------------------------------------------- fp32 kernel
+constexpr int kFmaThreads = 256, kFmaWarps = kFmaThreads / 32;
+constexpr int kRowsPerWarp = 4, kPassRows = kFmaWarps * kRowsPerWarp;
+constexpr int kChunkKeys = 32;
+
+struct TreeFma {
+  TreePlan plan;
+  void* out;
+  const void* q;
+  const uint8_t* kc;
+  const uint8_t* vc;
+  int64_t num_blocks, block_stride, token_stride, head_stride;   // strides in elements
+  int block_size;
+  const int32_t* tables;
+  int max_blocks;
+  float scale_log2;
+  ScoreMod mod;
+  int32_t* err;
+};
+
+// Is node u among the visible ancestors of a row, and how many lie after it?
+__device__ __forceinline__ bool tree_sees(const uint32_t* anc, int words, int u, int& after) {
+  const int w = u >> 5;
+  const uint32_t x = anc[w];
+  after = __popc(u % 32 == 31 ? 0u : x >> (u % 32 + 1));
+  for (int k = w + 1; k < words; ++k) after += __popc(anc[k]);
+  return (x >> (u & 31)) & 1u;
+}
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kFmaThreads) tree_fma_kernel(const TreeFma p) {
+  constexpr int LD = D + 4, DL = D / 32;
+  extern __shared__ __align__(16) float sm[];
+  float* ks = sm;                                   // [32][LD]
+  float* vs = ks + kChunkKeys * LD;
+  float* qs = vs + kChunkKeys * LD;                 // [kPassRows][D]
+  float* ps = qs + kPassRows * D;                   // [kPassRows][32]
+  const TreePlan& pl = p.plan;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  pdl_wait();
+  pdl_trigger();
+  const int64_t total = pl.starts[pl.num_seqs], slices = tree_slices(pl, total);
+  if ((int64_t)blockIdx.x >= slices) return;
+  TreeWalk walk;
+  walk.start(pl, blockIdx.x, total, slices);
+  TreeSegment g;
+  while (walk.next(pl, g)) {
+    const TreeSeq& s = walk.s;
+    const int tb = g.unit * pl.unit_tokens, rows = (min(tb + pl.unit_tokens, s.n) - tb) * pl.group;
+    const int k0 = max(s.lo, (s.lo_tile + g.t0) * kTreeKeys), k1 = min(s.klen, (s.lo_tile + g.t1) * kTreeKeys);
+    for (int pass = 0; pass < rows; pass += kPassRows) {
+      float acc[kRowsPerWarp][DL], m[kRowsPerWarp], l[kRowsPerWarp], slope[kRowsPerWarp];
+      int pos[kRowsPerWarp];
+      const uint32_t* anc[kRowsPerWarp];
+      __syncthreads();
+      for (int idx = tid; idx < kPassRows * (D / 4); idx += kFmaThreads) {
+        const int r = idx / (D / 4), c = idx % (D / 4) * 4;
+        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (pass + r < rows) {
+          const int t = (pass + r) / pl.group, gi = (pass + r) % pl.group;
+          const T* src = static_cast<const T*>(p.q) +
+                         ((int64_t)(s.q0 + tb + t) * pl.hq + (int64_t)g.head * pl.group + gi) * D + c;
+          x = make_float4(DT<T>::to_f(src[0]), DT<T>::to_f(src[1]), DT<T>::to_f(src[2]), DT<T>::to_f(src[3]));
+        }
+        *reinterpret_cast<float4*>(qs + r * D + c) = x;
+      }
+#pragma unroll
+      for (int r = 0; r < kRowsPerWarp; ++r) {
+        const int row = min(pass + warp * kRowsPerWarp + r, rows - 1), t = row / pl.group;   // rows past the last mirror it
+        const int64_t node = (int64_t)g.seq * pl.max_q + tb + t;
+        pos[r] = s.cached + pl.depth[node];
+        anc[r] = pl.anc + node * pl.words;
+        slope[r] = bias_slope(p.mod, g.head * pl.group + row % pl.group);
+        m[r] = -INFINITY;
+        l[r] = 0.f;
+#pragma unroll
+        for (int d = 0; d < DL; ++d) acc[r][d] = 0.f;
+      }
+      for (int kb = k0; kb < k1; kb += kChunkKeys) {
+        __syncthreads();
+        for (int idx = tid; idx < kChunkKeys * (D / 4); idx += kFmaThreads) {
+          const int r = idx / (D / 4), c = idx % (D / 4) * 4, j = kb + r;
+          float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
+          if (j < k1) {
+            const int b = __ldg(p.tables + (int64_t)g.seq * p.max_blocks + j / p.block_size);
+            if (b >= 0 && b < p.num_blocks) {
+              const int64_t off = (int64_t)b * p.block_stride + (int64_t)(j % p.block_size) * p.token_stride +
+                                  (int64_t)g.head * p.head_stride + c;
+              const T* kp = reinterpret_cast<const T*>(p.kc) + off;
+              const T* vp = reinterpret_cast<const T*>(p.vc) + off;
+              x = make_float4(DT<T>::to_f(kp[0]), DT<T>::to_f(kp[1]), DT<T>::to_f(kp[2]), DT<T>::to_f(kp[3]));
+              y = make_float4(DT<T>::to_f(vp[0]), DT<T>::to_f(vp[1]), DT<T>::to_f(vp[2]), DT<T>::to_f(vp[3]));
+            } else if (c == 0) {
+              flag_error(p.err, PKVD_ERR_BLOCK_ID);              // its keys read as zeros
+            }
+          }
+          *reinterpret_cast<float4*>(ks + r * LD + c) = x;
+          *reinterpret_cast<float4*>(vs + r * LD + c) = y;
+        }
+        __syncthreads();
+        if (pass + warp * kRowsPerWarp >= rows) continue;
+        float sc[kRowsPerWarp] = {};
+        const float* qw = qs + warp * kRowsPerWarp * D;
+#pragma unroll 8
+        for (int c = 0; c < D; c += 4) {
+          const float4 k = *reinterpret_cast<const float4*>(ks + lane * LD + c);
+#pragma unroll
+          for (int r = 0; r < kRowsPerWarp; ++r) {
+            const float4 x = *reinterpret_cast<const float4*>(qw + r * D + c);
+            sc[r] = fmaf(x.x, k.x, fmaf(x.y, k.y, fmaf(x.z, k.z, fmaf(x.w, k.w, sc[r]))));
+          }
+        }
+        const int j = kb + lane;
+#pragma unroll
+        for (int r = 0; r < kRowsPerWarp; ++r) {
+          int back = pos[r] - j;
+          bool sees = j < k1 && (pl.window <= 0 || back < pl.window);
+          if (j >= s.cached && j < k1) sees = tree_sees(anc[r], pl.words, j - s.cached, back);
+          float x = -INFINITY;
+          if (sees) x = fmaf(slope[r], (float)back, capped<std::is_same<T, float>::value>(sc[r], p.scale_log2, p.mod));
+          float top = x;
+#pragma unroll
+          for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(FULL_MASK, top, o));
+          const float mn = fmaxf(m[r], top), base = mn == -INFINITY ? 0.f : mn;
+          const float corr = exp2f(m[r] - base), e = exp2f(x - base);
+          float sum = e;
+#pragma unroll
+          for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(FULL_MASK, sum, o);
+          l[r] = l[r] * corr + sum;
+          m[r] = mn;
+#pragma unroll
+          for (int d = 0; d < DL; ++d) acc[r][d] *= corr;
+          ps[(warp * kRowsPerWarp + r) * 32 + lane] = e;
+        }
+        __syncwarp();
+#pragma unroll 4
+        for (int k = 0; k < kChunkKeys; k += 4) {
+          float4 w[kRowsPerWarp];
+#pragma unroll
+          for (int r = 0; r < kRowsPerWarp; ++r)
+            w[r] = *reinterpret_cast<const float4*>(ps + (warp * kRowsPerWarp + r) * 32 + k);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            float v[DL];
+#pragma unroll
+            for (int d = 0; d < DL; ++d) v[d] = vs[(k + e) * LD + lane * DL + d];
+#pragma unroll
+            for (int r = 0; r < kRowsPerWarp; ++r) {
+              const float x = e == 0 ? w[r].x : e == 1 ? w[r].y : e == 2 ? w[r].z : w[r].w;
+              // a key that this row does not see weighs nothing, whatever its value holds
+#pragma unroll
+              for (int d = 0; d < DL; ++d) acc[r][d] = x == 0.f ? acc[r][d] : fmaf(x, v[d], acc[r][d]);
+            }
+          }
+        }
+        __syncwarp();
+      }
+#pragma unroll
+      for (int r = 0; r < kRowsPerWarp; ++r) {
+        const int row = pass + warp * kRowsPerWarp + r;
+        if (row >= rows) continue;
+        if (g.slot < 0) {
+          const int t = row / pl.group, gi = row % pl.group;
+          T* dst = static_cast<T*>(p.out) + ((int64_t)(s.q0 + tb + t) * pl.hq + (int64_t)g.head * pl.group + gi) * D;
+          const float inv = l[r] > 0.f ? 1.f / l[r] : 0.f;
+#pragma unroll
+          for (int d = 0; d < DL; ++d) dst[lane * DL + d] = DT<T>::from_f(acc[r][d] * inv);
+        } else {
+          const int64_t at = (int64_t)g.slot * pl.unit_rows + row;
+#pragma unroll
+          for (int d = 0; d < DL; ++d) pl.rec[at * D + lane * DL + d] = acc[r][d];
+          if (lane == 0) pl.rec_ml[at] = make_float2(m[r], l[r]);
+        }
+      }
+    }
+  }
+}
+
+// ------------------------------------------------------------------- merge
+// Joins the records of a (unit, head) that more than one CTA worked on:
+//   M = max m_k, out = sum 2^(m_k - M) acc_k / sum 2^(m_k - M) l_k.
+// PARTS = 1: a warp a row (eight rows a CTA).  PARTS = 8, for few rows cut into
+// many pieces: the CTA's eight warps share a row's records.
+template <typename T, int D, int PARTS>
+__global__ void __launch_bounds__(256) tree_merge_kernel(const TreePlan p, T* __restrict__ out) {
+  constexpr int R = 8;                                   // records on their way
+  __shared__ float part[PARTS == 1 ? 1 : 8 * (D + 2)];
+  pdl_wait();
+  pdl_trigger();
+  const int seq = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int units = (p.max_q + p.unit_tokens - 1) / p.unit_tokens;
+  const int item = blockIdx.x % (units * p.hkv), group = blockIdx.x / (units * p.hkv);
+  const int unit = item / p.hkv, head = item % p.hkv;
+  const TreeSeq s = tree_seq(p, seq);
+  if (unit >= s.units) return;
+  const int tb = unit * p.unit_tokens, rows = (min(tb + p.unit_tokens, s.n) - tb) * p.group;
+  const int row = PARTS == 1 ? group * 8 + warp : group;
+  if ((PARTS == 1 ? group * 8 : group) >= rows) return;
+  const int64_t total = p.starts[p.num_seqs], slices = tree_slices(p, total);
+  const int64_t f = p.starts[seq] + ((int64_t)unit * p.hkv + head) * s.tiles;
+  const int a = (int)tree_slice_of(total, slices, f), b = (int)tree_slice_of(total, slices, f + s.tiles - 1);
+  if (a == b) return;                                    // one CTA had it all
+  const int slot_a = tree_slice_begin(total, slices, a) == f ? 0 : 1;
+  constexpr int Q = D / 4, SUB = 32 / Q;                 // lanes of a row's float4 slices; records a warp takes at once
+  const int d4 = lane % Q * 4, sub = lane / Q;
+  const int step = SUB * (PARTS == 1 ? 1 : 8), k_first = PARTS == 1 ? sub : warp * SUB + sub;
+  float M = -INFINITY, L = 0.f;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  const bool live = row < rows;
+  for (int k0 = a + k_first; live && k0 <= b; k0 += R * step) {
+    float2 ml[R];
+    float4 x[R];
+#pragma unroll
+    for (int e = 0; e < R; ++e) {
+      const int k = k0 + e * step;
+      ml[e] = make_float2(-INFINITY, 0.f);
+      x[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (k <= b) {
+        const int64_t at = (int64_t)(2 * k + (k == a ? slot_a : 0)) * p.unit_rows + row;
+        ml[e] = p.rec_ml[at];
+        x[e] = *reinterpret_cast<const float4*>(p.rec + at * D + d4);
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < R; ++e) {
+      if (ml[e].x == -INFINITY) continue;                // saw none of the keys
+      const float Mn = fmaxf(M, ml[e].x), cs = exp2f(M - Mn), cr = exp2f(ml[e].x - Mn);
+      L = L * cs + ml[e].y * cr;
+      o.x = o.x * cs + x[e].x * cr;
+      o.y = o.y * cs + x[e].y * cr;
+      o.z = o.z * cs + x[e].z * cr;
+      o.w = o.w * cs + x[e].w * cr;
+      M = Mn;
+    }
+  }
+  auto join = [&](float Mo, float Lo, float4 x) {
+    const float Mn = fmaxf(M, Mo), base = Mn == -INFINITY ? 0.f : Mn;
+    const float ca = exp2f(M - base), cb = exp2f(Mo - base);
+    L = L * ca + Lo * cb;
+    o = make_float4(o.x * ca + x.x * cb, o.y * ca + x.y * cb, o.z * ca + x.z * cb, o.w * ca + x.w * cb);
+    M = Mn;
+  };
+#pragma unroll
+  for (int off = Q; off < 32; off <<= 1) {
+    const float Mo = __shfl_xor_sync(FULL_MASK, M, off), Lo = __shfl_xor_sync(FULL_MASK, L, off);
+    const float4 x = make_float4(__shfl_xor_sync(FULL_MASK, o.x, off), __shfl_xor_sync(FULL_MASK, o.y, off),
+                                 __shfl_xor_sync(FULL_MASK, o.z, off), __shfl_xor_sync(FULL_MASK, o.w, off));
+    join(Mo, Lo, x);
+  }
+  if constexpr (PARTS > 1) {
+    float* mine = part + warp * (D + 2);
+    if (sub == 0) {
+      mine[d4] = o.x, mine[d4 + 1] = o.y, mine[d4 + 2] = o.z, mine[d4 + 3] = o.w;
+      if (d4 == 0) mine[D] = M, mine[D + 1] = L;
+    }
+    __syncthreads();
+    if (warp > 0) return;
+    for (int w = 1; w < 8; ++w) {
+      const float* x = part + w * (D + 2);
+      join(x[D], x[D + 1], make_float4(x[d4], x[d4 + 1], x[d4 + 2], x[d4 + 3]));
+    }
+  }
+  if (!live || sub > 0) return;
+  const int t = row / p.group, gi = row % p.group;
+  T* dst = out + ((int64_t)(s.q0 + tb + t) * p.hq + (int64_t)head * p.group + gi) * D + d4;
+  const float inv = L > 0.f ? 1.f / L : 0.f;
+  dst[0] = DT<T>::from_f(o.x * inv);
+  dst[1] = DT<T>::from_f(o.y * inv);
+  dst[2] = DT<T>::from_f(o.z * inv);
+  dst[3] = DT<T>::from_f(o.w * inv);
+}
+
+// ------------------------------------------------------------------ accept
+// A warp a sequence.  Node 0 is the token that the target chose last; from a
+// node on the path the walk goes to the lowest child that drafts the target's
+// choice there, eight nodes a lane in registers.
+constexpr int kAcceptWarps = 4;
+
+__global__ void __launch_bounds__(kAcceptWarps * 32) tree_accept_kernel(const AcceptArgs a, int num_seqs) {
+  constexpr int PER = kTreeMaxNodes / 32;
+  pdl_wait();          // the target's choices come from the sampler (no early trigger: counts may be lengths)
+  const int i = blockIdx.x * kAcceptWarps + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  if (i >= num_seqs) return;
+  const int q0 = a.cu_q[i], n = a.cu_q[i + 1] - q0, cached = a.cu_k[i + 1] - a.cu_k[i] - n;
+  int count = 0;
+  const bool ok = q0 >= 0 && n >= 0 && n <= kTreeMaxNodes && cached >= 0 && (int64_t)q0 + n <= a.total_q;
+  if (!ok && lane == 0) flag_error(a.err, PKVD_ERR_CONTEXT);
+  int32_t* pos = a.positions + (int64_t)i * a.max_path;
+  int32_t* tok = a.tokens + (int64_t)i * a.max_path;
+  if (ok && n > 0) {
+    int up[PER], id[PER], choice[PER];
+#pragma unroll
+    for (int k = 0; k < PER; ++k) {
+      const int t = k * 32 + lane;
+      up[k] = id[k] = choice[k] = -1;
+      if (t < n) {
+        up[k] = a.parents[q0 + t];
+        id[k] = a.drafted[q0 + t];
+        choice[k] = a.target[q0 + t];
+        if (up[k] < -1 || up[k] >= t) {
+          flag_error(a.err, PKVD_ERR_TREE);
+          up[k] = -1;
+        }
+      }
+    }
+    int here = 0;
+    while (count < a.max_path) {
+      int want = 0;
+#pragma unroll
+      for (int k = 0; k < PER; ++k) {
+        const int c = __shfl_sync(FULL_MASK, choice[k], here & 31);
+        if (k == here >> 5) want = c;
+      }
+      if (lane == 0) {
+        pos[count] = cached + here;
+        tok[count] = want;
+      }
+      ++count;
+      int child = -1;
+#pragma unroll
+      for (int k = PER - 1; k >= 0; --k) {
+        const uint32_t fits = __ballot_sync(FULL_MASK, up[k] == here && id[k] == want && k * 32 + lane < n);
+        if (fits) child = k * 32 + __ffs(fits) - 1;
+      }
+      if (child < 0) break;
+      here = child;
+    }
+  }
+  for (int k = count + lane; k < a.max_path; k += 32) pos[k] = tok[k] = -1;
+  if (lane == 0) {
+    a.first[i] = ok ? cached : 0;
+    a.counts[i] = count;
+    __threadfence();
+  }
+}
+
+// ------------------------------------------------------------------- host
+size_t up256(size_t x) { return (x + 255) / 256 * 256; }
+
+int unit_tokens_of(int path, int group, int max_q) {
+  if (path == PKVD_PATH_FMA) return kPassRows / group > 1 ? kPassRows / group : 1;
+  const int tile = 128 / group;                          // two Q tiles, or one where that holds every tree
+  return max_q > tile ? 2 * tile : tile;
+}
+
+int grid_of(int path, int sms) { return path == PKVD_PATH_FMA ? 2 * sms : sms; }
+
+struct WorkspaceLayout {
+  size_t starts, anc, depth, rec, rec_ml, bytes;
+  WorkspaceLayout(int path, int num_seqs, int group, int head_dim, int max_q, int sms) {
+    const int words = (max_q + 31) / 32;
+    const size_t rows = (size_t)2 * grid_of(path, sms) * unit_tokens_of(path, group, max_q) * group;
+    starts = 0;
+    anc = starts + up256(sizeof(int64_t) * ((size_t)num_seqs + 1));
+    depth = anc + up256(sizeof(uint32_t) * (size_t)num_seqs * max_q * words);
+    rec_ml = depth + up256(sizeof(int32_t) * (size_t)num_seqs * max_q);
+    rec = rec_ml + up256(sizeof(float2) * rows);
+    bytes = rec + up256(sizeof(float) * rows * head_dim);
+  }
+};
+
+template <typename T, int D>
+cudaError_t launch_fma(const TreeFma& p, cudaStream_t stream) {
+  constexpr int smem = (2 * kChunkKeys * (D + 4) + kPassRows * (D + 32)) * (int)sizeof(float);
+  cudaError_t e = cudaFuncSetAttribute(tree_fma_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(tree_fma_kernel<T, D>, dim3(p.plan.grid), dim3(kFmaThreads), smem, stream, p);
+}
+
+template <typename T, int D>
+cudaError_t launch_merge(const TreePlan& p, void* out, cudaStream_t stream) {
+  const int64_t items = (int64_t)((p.max_q + p.unit_tokens - 1) / p.unit_tokens) * p.hkv;
+  const int rows = (p.max_q < p.unit_tokens ? p.max_q : p.unit_tokens) * p.group;
+  // pieces of an item: about grid / items; a warp takes eight records a round
+  const bool many = p.grid > 8 * items * p.num_seqs;
+  const int64_t groups = many ? rows : (rows + 7) / 8;
+  const dim3 grid((unsigned)(items * groups), (unsigned)p.num_seqs);
+  return many ? launch_pdl(tree_merge_kernel<T, D, 8>, grid, dim3(256), 0, stream, p, static_cast<T*>(out))
+              : launch_pdl(tree_merge_kernel<T, D, 1>, grid, dim3(256), 0, stream, p, static_cast<T*>(out));
+}
+
+}  // namespace
+
+// Enough for either path: a call whose layout the tensor cores cannot read falls back.
+size_t tree_workspace_bytes(int num_seqs, int num_q_heads, int num_kv_heads, int head_dim, int max_seqlen_q, int sms) {
+  const int group = num_q_heads / num_kv_heads;
+  const size_t a = WorkspaceLayout(PKVD_PATH_FMA, num_seqs, group, head_dim, max_seqlen_q, sms).bytes;
+  const size_t b = WorkspaceLayout(PKVD_PATH_TC, num_seqs, group, head_dim, max_seqlen_q, sms).bytes;
+  return a > b ? a : b;
+}
+
+cudaError_t launch_tree(const TreeArgs& a, cudaStream_t stream) {
+  const pkvd_cache& c = a.cache;
+  const int group = a.num_q_heads / c.num_kv_heads;
+  const WorkspaceLayout lay(a.path, a.num_seqs, group, c.head_dim, a.max_seqlen_q, a.sms);
+  uint8_t* ws = static_cast<uint8_t*>(a.workspace);
+  TreePlan p;
+  p.cu_q = a.cu_seqlens_q;
+  p.cu_k = a.cu_seqlens_k;
+  p.num_seqs = a.num_seqs;
+  p.total_q = a.total_q;
+  p.max_q = a.max_seqlen_q;
+  p.words = (a.max_seqlen_q + 31) / 32;
+  p.unit_tokens = unit_tokens_of(a.path, group, a.max_seqlen_q);
+  p.unit_rows = p.unit_tokens * group;
+  p.hkv = c.num_kv_heads;
+  p.hq = a.num_q_heads;
+  p.group = group;
+  p.window = a.window;
+  p.table_tokens = (int64_t)a.max_blocks_per_seq * c.block_size;
+  p.grid = grid_of(a.path, a.sms);
+  p.starts = reinterpret_cast<int64_t*>(ws + lay.starts);
+  p.anc = reinterpret_cast<uint32_t*>(ws + lay.anc);
+  p.depth = reinterpret_cast<int32_t*>(ws + lay.depth);
+  p.rec = reinterpret_cast<float*>(ws + lay.rec);
+  p.rec_ml = reinterpret_cast<float2*>(ws + lay.rec_ml);
+  cudaError_t e = launch_pdl(tree_plan_kernel, dim3(a.num_seqs + 1), dim3(kPlanThreads), 0, stream, p, a.parents, a.err);
+  if (e != cudaSuccess) return e;
+  if (a.path == PKVD_PATH_TC) {
+    e = launch_tree_tc(a, p, stream);
+  } else {
+    TreeFma f;
+    f.plan = p;
+    f.out = a.out;
+    f.q = a.q;
+    f.kc = static_cast<const uint8_t*>(c.k_base);
+    f.vc = static_cast<const uint8_t*>(c.v_base);
+    f.num_blocks = c.num_blocks;
+    f.block_stride = c.block_stride;
+    f.token_stride = c.token_stride;
+    f.head_stride = c.head_stride;
+    f.block_size = c.block_size;
+    f.tables = a.block_tables;
+    f.max_blocks = a.max_blocks_per_seq;
+    f.scale_log2 = a.scale * 1.4426950408889634f;
+    f.mod = a.mod;
+    f.err = a.err;
+    const bool wide = c.head_dim == 128;
+    if (c.dtype == PKVD_F32) e = wide ? launch_fma<float, 128>(f, stream) : launch_fma<float, 64>(f, stream);
+    else if (c.dtype == PKVD_F16) e = wide ? launch_fma<__half, 128>(f, stream) : launch_fma<__half, 64>(f, stream);
+    else e = wide ? launch_fma<__nv_bfloat16, 128>(f, stream) : launch_fma<__nv_bfloat16, 64>(f, stream);
+  }
+  if (e != cudaSuccess) return e;
+  const bool wide = c.head_dim == 128;
+  if (c.dtype == PKVD_F32) return wide ? launch_merge<float, 128>(p, a.out, stream) : launch_merge<float, 64>(p, a.out, stream);
+  if (c.dtype == PKVD_F16) return wide ? launch_merge<__half, 128>(p, a.out, stream) : launch_merge<__half, 64>(p, a.out, stream);
+  return wide ? launch_merge<__nv_bfloat16, 128>(p, a.out, stream) : launch_merge<__nv_bfloat16, 64>(p, a.out, stream);
+}
+
+cudaError_t launch_tree_accept(const AcceptArgs& a, int num_seqs, cudaStream_t stream) {
+  if (num_seqs == 0) return cudaSuccess;
+  return launch_pdl(tree_accept_kernel, dim3((num_seqs + kAcceptWarps - 1) / kAcceptWarps), dim3(kAcceptWarps * 32), 0,
+                    stream, a, num_seqs);
+}
+
+}  // namespace pkvd

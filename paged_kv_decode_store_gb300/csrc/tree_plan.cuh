@@ -1,0 +1,127 @@
+// Attention of drafted trees: how its work is cut, shared by the kernels that
+// compute it (tree.cu in fp32, tree_tc.cu on the tensor cores) and the merge.
+//
+// Sequence i has n_i drafted rows behind cached_i = k_len_i - n_i cached tokens.
+// A unit is a run of its nodes (all query heads of one KV head: unit_rows
+// rows); a unit, KV head and tile of 128 keys is the smallest piece of work.
+// The pieces of the batch, sequence by sequence, unit by unit, head by head,
+// tile by tile, are one list; slices of equal length go to the CTAs.  A CTA
+// whose slice holds a (unit, head)'s tiles in part leaves a record (sums,
+// maximum, sum of weights), which the merge kernel joins; whole ones are
+// written at once.
+#pragma once
+
+#include "common.cuh"
+#include "launch.h"
+
+namespace pkvd {
+
+struct TreePlan {
+  const int32_t* cu_q;
+  const int32_t* cu_k;
+  int num_seqs, total_q, max_q, words;      // words: 32 ancestors each
+  int unit_tokens, unit_rows;
+  int hkv, hq, group;
+  int window;
+  int64_t table_tokens;                     // tokens a block table can hold
+  int grid;                                 // CTAs; slices are at most as many
+  // the workspace
+  int64_t* starts;                          // [num_seqs + 1]: pieces before a sequence
+  uint32_t* anc;                            // [num_seqs][max_q][words]: a node's visible ancestors and itself
+  int32_t* depth;                           // [num_seqs][max_q]
+  float* rec;                               // [2 grid][unit_rows][D]: sums of a slice's first and last segment
+  float2* rec_ml;                           // [2 grid][unit_rows]: maximum (log2 units), sum of weights
+};
+
+// A slice has at least so many tiles: a record more costs what a tile does.
+constexpr int kTreeMinTiles = 2;
+
+struct TreeSeq {
+  int q0, n, klen, cached;
+  int lo, lo_tile, tiles, units;            // first key any node sees, its tile, tiles of keys, units
+  __device__ int64_t pieces(int hkv) const { return (int64_t)units * hkv * tiles; }
+};
+
+__device__ __forceinline__ TreeSeq tree_seq(const TreePlan& p, int i) {
+  TreeSeq s;
+  s.q0 = p.cu_q[i];
+  s.n = p.cu_q[i + 1] - s.q0;
+  s.klen = p.cu_k[i + 1] - p.cu_k[i];
+  s.cached = s.klen - s.n;
+  s.units = s.tiles = s.lo = s.lo_tile = 0;
+  const bool ok = s.q0 >= 0 && s.n >= 0 && s.n <= p.max_q && s.cached >= 0 && (int64_t)s.q0 + s.n <= p.total_q &&
+                  s.klen <= p.table_tokens;
+  if (!ok) s.n = -1;
+  if (s.n <= 0) return s;
+  s.lo = p.window > 0 ? max(0, s.cached + 1 - p.window) : 0;
+  s.lo_tile = s.lo / kTreeKeys;
+  s.tiles = (s.klen - 1) / kTreeKeys - s.lo_tile + 1;
+  s.units = (s.n + p.unit_tokens - 1) / p.unit_tokens;
+  return s;
+}
+
+// Slices of a batch of `total` pieces, and where one begins.
+__device__ __forceinline__ int64_t tree_slices(const TreePlan& p, int64_t total) {
+  const int64_t most = total / kTreeMinTiles;
+  return most < 1 ? (total > 0 ? 1 : 0) : most < p.grid ? most : p.grid;
+}
+__device__ __forceinline__ int64_t tree_slice_begin(int64_t total, int64_t slices, int64_t c) { return total * c / slices; }
+// The slice that holds piece f.
+__device__ __forceinline__ int64_t tree_slice_of(int64_t total, int64_t slices, int64_t f) {
+  return ((f + 1) * slices - 1) / total;
+}
+
+// The sequence that holds piece f, for a whole warp: the last i with starts[i] <= f.
+__device__ __forceinline__ int tree_find(const TreePlan& p, int64_t f) {
+  const int lane = threadIdx.x & 31;
+  int lo = 0, hi = p.num_seqs;
+  while (hi - lo > 1) {
+    const int step = (hi - lo + 31) / 32, probe = lo + lane * step;
+    const uint32_t below = __ballot_sync(FULL_MASK, probe < hi && p.starts[min(probe, hi - 1)] <= f);
+    lo += (31 - __clz(below)) * step;      // lane 0's is always below
+    hi = min(hi, lo + step);
+  }
+  return lo;
+}
+
+// One segment of a slice: tiles [t0, t1) of a (unit, head).
+struct TreeSegment {
+  int seq, unit, head;
+  int t0, t1;
+  int slot;                                 // of its record; -1: the whole (unit, head)
+};
+
+// Walks a slice's segments (every thread of the caller alike).
+struct TreeWalk {
+  int64_t at, end, begin;
+  int cta, seq;
+  TreeSeq s;
+  __device__ void start(const TreePlan& p, int c, int64_t total, int64_t slices) {
+    cta = c;
+    at = begin = tree_slice_begin(total, slices, c);
+    end = tree_slice_begin(total, slices, c + 1);
+    seq = tree_find(p, at);
+    s = tree_seq(p, seq);
+  }
+  __device__ bool next(const TreePlan& p, TreeSegment& g) {
+    if (at >= end) return false;
+    int64_t in = at - p.starts[seq];
+    while (in >= s.pieces(p.hkv)) {         // the next sequence with any
+      if (++seq >= p.num_seqs) return false;
+      in = 0;
+      s = tree_seq(p, seq);
+    }
+    const int64_t item = in / s.tiles;
+    g.seq = seq;
+    g.unit = (int)(item / p.hkv);
+    g.head = (int)(item % p.hkv);
+    g.t0 = (int)(in - item * s.tiles);
+    g.t1 = (int)(end - at < s.tiles - g.t0 ? g.t0 + (end - at) : s.tiles);
+    const bool whole = g.t0 == 0 && g.t1 == s.tiles;
+    g.slot = whole ? -1 : 2 * cta + (at == begin ? 0 : 1);
+    at += g.t1 - g.t0;
+    return true;
+  }
+};
+
+}  // namespace pkvd

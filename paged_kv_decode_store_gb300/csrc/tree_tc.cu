@@ -1,0 +1,863 @@
+// Attention for trees of drafted tokens on the 5th-generation tensor cores
+// (the mathematics: tree.cu; how the work is cut: tree_plan.cuh).
+//
+// A drafted tree is a handful of query rows over a long cache: the keys decide
+// the time, so every CTA streams an equal share of all of them (one persistent
+// CTA an SM, a slice of the batch's list of 128-key tiles), and a (unit, KV
+// head) that is cut leaves records that the merge kernel joins.
+//
+// Rows are (node, query head of the group) pairs, up to 128 a Q tile.  The CTA
+// has two streams, each with its S, P and O in tensor memory and eight softmax
+// warps (two threads a row, 64 keys each):
+//   a unit of two Q tiles: stream g takes Q tile g, both use each K/V tile;
+//   a unit of one Q tile: both take it, stream g every second K/V tile, and
+//   their sums are joined from tensor memory at the end of the segment.
+// So the chain score product -> softmax -> value product of a tile runs beside
+// another one whatever the tree's size, and the K/V copies set the pace while a
+// unit has one Q tile.  Keys go from the newest backwards; the drafted ones, which
+// are masked by a bit a (row, node), come first.
+//
+// Warps (20): 0-7 and 8-15 softmax of stream 0 and 1 (warp w of a stream: TMEM
+// lanes 32 (w % 4) .., keys 64 (w / 4) ..), 16 copies of K and V, 17 and 19 the
+// products of stream 0 and 1, 18 the segments and Q.
+#include <climits>
+
+#include "common.cuh"
+#include "launch.h"
+#include "score_mod.cuh"
+#include "tc_softmax.cuh"
+#include "tcgen05.cuh"
+#include "tree_plan.cuh"
+
+namespace pkvd {
+
+namespace {
+
+constexpr int kThreads = 640;
+constexpr int kStreamWarps = 8;
+constexpr int kKvWarp = 16, kMmaWarp = 17, kQWarp = 18, kMmaWarp1 = 19;
+constexpr uint32_t kTmemCols = 512;
+// TMEM columns: S of stream g at [128 g, 128 g + 128), O at [256 + g D, 256 + g D
+// + D).  head_dim 128: a half's weights overwrite the first 32 of its own 64 S
+// columns; head_dim 64: they have [384 + 64 g, 448 + 64 g), so the next S may be
+// computed while they are in use.
+constexpr uint32_t kColO = 256, kColP64 = 384;
+enum : int { kCap = 1, kBias = 2 };       // what a call modifies, known when compiled
+constexpr float kRebase = 8.f;            // re-base the running maximum when it grows by > 2^8
+constexpr float kLinear = 16384.f;        // largest bias (log2 units) put together from parts
+
+template <int D>
+struct Layout {
+  static constexpr int kKStages = D == 64 ? 4 : 3, kVStages = D == 64 ? 4 : 2;
+  static constexpr int kHalves = D / 64;
+  static constexpr uint32_t kQ = 0;                                    // 2 Q tiles
+  static constexpr uint32_t kK = kQ + 2 * kHalves * kHalf;
+  static constexpr uint32_t kV = kK + kKStages * kHalves * kHalf;
+  static constexpr uint32_t kBar = kV + kVStages * kHalves * kHalf;
+  static constexpr uint32_t kX = kBar + 512;                           // exchange: 1024 bytes a stream and buffer
+  static constexpr int kXBufs = D == 64 ? 2 : 1;
+  static constexpr uint32_t kItems = kX + kXBufs * 2048;               // ring of segments
+  static constexpr uint32_t kGaveUp = kItems + 256;                    // one word a pair of softmax warps
+  static constexpr uint32_t kEnd = kGaveUp + 32;
+  // at least 120 KB so that one CTA (which holds all TMEM) is resident per SM
+  static constexpr uint32_t kBytes = kEnd > 122880u ? kEnd : 122880u;
+};
+static_assert(Layout<128>::kBytes <= 232448, "227 KB of shared memory");
+
+// mbarriers; those of a stream take + g
+enum : int {
+  kKFull = 0, kKEmpty = 4, kVFull = 8, kVCut = 12, kVEmpty = 16, kQFull = 20, kQEmpty = 22, kSFull = 24, kPFull = 26,
+  kPVDone = 28, kSRead = 30, kOFree = 32, kItemFull = 34, kItemFree = 38, kDrain = 42, kJoin = 44, kNumBars = 48
+};
+constexpr uint32_t kTmemSlot = 8 * kNumBars;
+static_assert(kTmemSlot + 4 <= 512, "behind the barriers");
+constexpr int kItemRing = 4;
+constexpr int kItemUsers = 3 + 2 * kStreamWarps;   // K/V, two MMA and softmax warps
+
+struct TcTree {
+  CUtensorMap tmap_q, tmap_k, tmap_v;
+  TreePlan plan;
+  void* out;
+  const int32_t* tables;
+  int max_blocks;
+  int block_size, block_shift;   // a power of two
+  uint32_t block_limit;          // num_blocks, at most 2^31
+  int seg_rows;                  // rows per TMA box of the cache: min(block_size, 128)
+  int tile_tokens;               // nodes of a Q tile
+  uint32_t q_box;                // bytes of one 64-column box of a Q tile
+  float scale_log2;
+  ScoreMod mod;
+  float poly[4], poly_range;     // cap_poly
+  int wide_out;                  // out is 32-byte aligned: stores of 32 bytes
+  int32_t* err;
+};
+
+// A segment: n tiles of a (unit, KV head) from tile kt_last down.  n = -1: no more.
+struct __align__(16) Item {
+  int seq, hk, q0, tokens;       // q0: the unit's first row of q
+  int node0, cached, lo, hi;     // node0: its place in the plan's arrays; keys outside [lo, hi] are not read
+  int kt_last, n, slot, two;     // two Q tiles?
+  int qbuf, pad[3];              // where a single Q tile lies
+};
+static_assert(sizeof(Item) * kItemRing == 256, "the ring in Layout");
+
+__device__ __forceinline__ int window_first(int c, int window) { return (window > 0 && c > window) ? c - window : 0; }
+
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, float* v) {
+  uint32_t* r = reinterpret_cast<uint32_t*>(v);
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
+
+__device__ __forceinline__ void st_global_v8(void* dst, const uint32_t* w) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+               "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+               : "memory");
+}
+
+// Which of a thread's 64 columns its row sees: two words, and how many visible
+// nodes lie after the last column.
+struct Seen {
+  uint32_t word[2];
+  int after;
+};
+
+// Columns of a tile that reaches into the tree (first key kbase, `cut` of the
+// columns before the first node).
+__device__ __forceinline__ Seen tree_columns(const uint32_t* anc, int words, int first, int cut) {
+  Seen s;
+  s.after = 0;
+  for (int k = 0; k < words; ++k) {                  // nodes at 64 - cut and later
+    const int from = 64 - cut - 32 * k;
+    const uint32_t x = anc[k];
+    s.after += __popc(from <= 0 ? x : from >= 32 ? 0u : x >> from);
+  }
+#pragma unroll
+  for (int w = 0; w < 2; ++w) {
+    const int b = 32 * w - cut;                      // the node of the word's first column
+    uint32_t x = 0u;
+    if (b >= 0) {
+      const int k = b >> 5;
+      const uint32_t lo = k < words ? anc[k] : 0u, hi = k + 1 < words ? anc[k + 1] : 0u;
+      x = __funnelshift_r(lo, hi, b & 31);
+    } else if (b > -32) {
+      x = anc[0] << -b;
+    }
+    s.word[w] = x | span_bits(first - 32 * w, cut - 32 * w);
+  }
+  return s;
+}
+
+// Everything a row does not see becomes `x`, whatever it was.  Most groups of
+// eight columns are visible to the whole warp.
+__device__ __forceinline__ void hide(float (&v)[kCols], const uint32_t (&seen)[2], float x) {
+#pragma unroll
+  for (int w = 0; w < 2; ++w) {
+    const uint32_t m = seen[w], every = __reduce_and_sync(FULL_MASK, m);
+#pragma unroll
+    for (int c8 = 0; c8 < 32; c8 += 8) {
+      if (((every >> c8) & 0xffu) == 0xffu) continue;
+#pragma unroll
+      for (int c = c8; c < c8 + 8; ++c) v[32 * w + c] = ((m >> c) & 1u) ? v[32 * w + c] : x;
+    }
+  }
+}
+
+template <typename T, int D, int MODE>
+__global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const __grid_constant__ TcTree p) {
+  using L = Layout<D>;
+  constexpr int H = L::kHalves, kKStages = L::kKStages, kVStages = L::kVStages;
+  constexpr bool kSepP = D == 64;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* gbase = smem_raw;
+  const uint32_t base = smem_u32(smem_raw);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(gbase + L::kBar);
+  const TreePlan& pl = p.plan;
+  const int warp = __shfl_sync(FULL_MASK, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;   // known to be uniform
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kNumBars; ++i) {
+      int arrivals = 1;
+      if ((i >= kPFull && i < kPVDone) || (i >= kSRead && i < kOFree)) arrivals = kStreamWarps;
+      if (i >= kOFree && i < kItemFull) arrivals = 2 * kStreamWarps + 1;
+      if ((i >= kKEmpty && i < kVFull) || (i >= kVEmpty && i < kQFull) || i == kQEmpty || i == kQEmpty + 1) arrivals = 2;
+      if (i >= kItemFree && i < kDrain) arrivals = kItemUsers;
+      if (i >= kJoin) arrivals = 4;
+      mbar_init(&bars[i], arrivals);
+    }
+    fence_mbar_init();
+  }
+  if (threadIdx.x < 8) reinterpret_cast<uint32_t*>(gbase + L::kGaveUp)[threadIdx.x] = 0;
+  // a Q tile's rows past its G * tile_tokens: no copy writes them, they stay zero
+  for (int i = pl.group * p.tile_tokens * 8 + (int)threadIdx.x; i < kTcRows * 8; i += kThreads)
+    for (int t = 0; t < 2 * H; ++t) st_shared_v4(base + L::kQ + t * kHalf + i * 16, make_uint4(0u, 0u, 0u, 0u));
+  fence_proxy_async_smem();
+  if (warp == kMmaWarp) tmem_alloc(base + L::kBar + kTmemSlot, kTmemCols);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = __shfl_sync(FULL_MASK, *reinterpret_cast<volatile uint32_t*>(gbase + L::kBar + kTmemSlot), 0);
+
+  pdl_wait();      // the plan, and the cache rows of this step
+  pdl_trigger();
+  Item* ring_items = reinterpret_cast<Item*>(gbase + L::kItems);
+
+  // registers: 512 x 104 + 128 x 56 = 60416 of the 61440 that 640 threads start with
+  if (warp >= kKvWarp) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+  if (warp == kKvWarp) {
+    // ------------------------------------------------------- K and V copies
+    // Lane s copies segment s of a tile; K runs kAhead tiles ahead of V.  A V
+    // tile with rows that are not read lands on a barrier of its own (kVCut)
+    // and is released with those rows zeroed, so that they never weigh in.
+    constexpr int kAhead = kKStages - 2;
+    const uint32_t box = (uint32_t)p.seg_rows * 128u;
+    const int nseg = kTcKeys / p.seg_rows;
+    const uint32_t whole = (1u << nseg) - 1u;  // at most 16 segments
+    if (lane == 0) {
+      asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&p.tmap_k)) : "memory");
+      asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&p.tmap_v)) : "memory");
+    }
+    constexpr int kNone = INT_MIN;             // a segment of rows that are not read: nothing to load
+    bool ok = true;
+    int kstg = 0, vstg = 0, landed = 0;        // next stages; phases of kVCut
+    uint32_t kpar = 1, vpar = 1;               // parities of their release (nothing to wait for in the first round)
+    auto wait = [&](int bar, uint32_t parity) {
+      if (ok) ok = __all_sync(FULL_MASK, wait_bounded(&bars[bar], parity));
+    };
+    // one operand of a tile into a stage, whose block id is b in lane s
+    auto copy = [&](const CUtensorMap* map, uint32_t dst, int bar, int ks, int hk, int b) {
+      const bool good = (uint32_t)b < p.block_limit;
+      const uint32_t loaded = __ballot_sync(FULL_MASK, good);
+      uint32_t bytes = H * kHalf;
+      dst += lane * box;
+      if (loaded != whole) {
+        bytes = (uint32_t)__popc(loaded) * box * H;
+        const uint32_t bad = __ballot_sync(FULL_MASK, b != kNone && !good);
+        if (bad) {                             // a bad block id reads as zeros
+          if (lane == 0) flag_error(p.err, PKVD_ERR_BLOCK_ID);
+          if ((bad >> lane) & 1u) {
+            for (int h = 0; h < H; ++h)
+              for (uint32_t o = 0; o < box; o += 16) st_shared_v4(dst + h * kHalf + o, make_uint4(0u, 0u, 0u, 0u));
+            fence_proxy_async_smem();
+          }
+          __syncwarp();
+        }
+      }
+      if (lane == 0) mbar_arrive_expect_tx(&bars[bar], bytes);
+      __syncwarp();
+      if (good) {
+#pragma unroll
+        for (int h = 0; h < H; ++h) tma_load4(dst + h * kHalf, map, h * 64, hk, ks & (p.block_size - 1), b, &bars[bar]);
+      }
+    };
+    for (int r = 0; ok; ++r) {
+      ok = __all_sync(FULL_MASK, wait_item(&bars[kItemFull + r % kItemRing], (r / kItemRing) & 1));
+      if (!ok) break;
+      const Item& cur = ring_items[r % kItemRing];
+      if (cur.n < 0) break;
+      const int32_t* table = p.tables + (int64_t)cur.seq * p.max_blocks;
+      const int n = cur.n, hk = cur.hk, lo = cur.lo, hi = cur.hi, kt_last = cur.kt_last;
+      auto key_of = [&](int t) { return (kt_last - t) * kTcKeys + lane * p.seg_rows; };
+      auto fetch = [&](int t) -> int {
+        const int ks = key_of(t);
+        if (t >= n || lane >= nseg || ks > hi || ks + p.seg_rows - 1 < lo) return kNone;
+        return __ldg(table + (ks >> p.block_shift));
+      };
+      auto copy_k = [&](int t, int b) {
+        wait(kKEmpty + kstg, kpar);
+        if (!ok) return;
+        copy(&p.tmap_k, base + L::kK + kstg * H * kHalf, kKFull + kstg, key_of(t), hk, b);
+        if (++kstg == kKStages) kstg = 0, kpar ^= 1;
+      };
+      int b[4];                                // block ids of V tile t and the three after it
+#pragma unroll
+      for (int i = 0; i < 4; ++i) b[i] = fetch(i);
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i)
+        if (i < n) copy_k(i, b[i]);
+      for (int t = 0; ok && t < n; ++t) {
+        if (t + kAhead < n) copy_k(t + kAhead, b[kAhead]);
+        wait(kVEmpty + vstg, vpar);
+        if (!ok) break;
+        const int kbase = (kt_last - t) * kTcKeys;
+        const bool cut = kbase < lo || kbase + kTcKeys - 1 > hi;
+        const uint32_t dst = base + L::kV + vstg * H * kHalf;
+        copy(&p.tmap_v, dst, (cut ? kVCut : kVFull) + vstg, kbase + lane * p.seg_rows, hk, b[0]);
+        if (cut) {
+          wait(kVCut + vstg, (landed >> vstg) & 1);
+          landed ^= 1 << vstg;
+          if (!ok) break;
+          for (int rr = lane; rr < kTcKeys; rr += 32) {
+            const int kp = kbase + rr;
+            if (kp >= lo && kp <= hi) continue;
+            for (int h = 0; h < H; ++h)
+              for (int c = 0; c < 8; ++c) st_shared_v4(dst + h * kHalf + rr * 128 + c * 16, make_uint4(0u, 0u, 0u, 0u));
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bars[kVFull + vstg]);
+        }
+        if (++vstg == kVStages) vstg = 0, vpar ^= 1;
+        b[0] = b[1];
+        b[1] = b[2];
+        b[2] = b[3];
+        b[3] = fetch(t + 4);
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars[kItemFree + r % kItemRing]);
+    }
+    if (!ok && lane == 0) {
+      // gave up: let the copies still in flight land before the CTA leaves
+      flag_error(p.err, PKVD_ERR_TIMEOUT);
+      // (a stage's full barrier is behind its release, or one phase ahead of it)
+      for (int u = 0; u < kKStages; ++u) wait_bounded(&bars[kKFull + u], (kpar ^ (u < kstg ? 0u : 1u)) ^ 1u);
+      for (int u = 0; u < kVStages; ++u) wait_bounded(&bars[kVFull + u], (vpar ^ (u < vstg ? 0u : 1u)) ^ 1u);
+    }
+  } else if (warp == kQWarp) {
+    // ------------------------------------------------------- segments and Q
+    // A Q tile's rows are one box per 64 columns (G heads of tile_tokens nodes).
+    // Two tiles of a unit fill both buffers; single ones take them in turn, so
+    // the next is loaded while the last is in use.
+    const int64_t total = pl.starts[pl.num_seqs], slices = tree_slices(pl, total);
+    TreeWalk walk;
+    walk.at = walk.end = 0;
+    if ((int64_t)blockIdx.x < slices) walk.start(pl, blockIdx.x, total, slices);
+    if (lane == 0) {
+      asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&p.tmap_q)) : "memory");
+      bool ok = true;
+      int used[2] = {0, 0}, turn = 0;
+      for (int r = 0; ok; ++r) {
+        const int slot = r % kItemRing;
+        if (r >= kItemRing) ok = wait_item(&bars[kItemFree + slot], ((r / kItemRing) - 1) & 1);
+        if (!ok) break;
+        Item it;
+        TreeSegment g;
+        it.n = -1;
+        if (walk.next(pl, g)) {
+          const int tb = g.unit * pl.unit_tokens;
+          it.seq = g.seq;
+          it.hk = g.head;
+          it.q0 = walk.s.q0 + tb;
+          it.tokens = min(pl.unit_tokens, walk.s.n - tb);
+          it.node0 = g.seq * pl.max_q + tb;
+          it.cached = walk.s.cached;
+          it.lo = walk.s.lo;
+          it.hi = walk.s.klen - 1;
+          it.kt_last = walk.s.lo_tile + g.t1 - 1;
+          it.n = g.t1 - g.t0;
+          it.slot = g.slot;
+          it.two = it.tokens > p.tile_tokens;
+          it.qbuf = turn;
+          if (!it.two) turn ^= 1;
+        }
+        ring_items[slot] = it;
+        mbar_arrive(&bars[kItemFull + slot]);
+        if (it.n < 0) break;
+#pragma unroll
+        for (int g2 = 0; g2 < 2; ++g2) {
+          if (!ok || !(it.two || it.qbuf == g2)) continue;
+          if (used[g2] > 0) ok = wait_item(&bars[kQEmpty + g2], (used[g2] - 1) & 1);
+          if (!ok) continue;
+          mbar_arrive_expect_tx(&bars[kQFull + g2], p.q_box * H);
+          for (int h = 0; h < H; ++h)
+            tma_load3(base + L::kQ + (g2 * H + h) * kHalf, &p.tmap_q, h * 64, it.hk * pl.group,
+                      it.q0 + (it.two ? g2 * p.tile_tokens : 0), &bars[kQFull + g2]);
+          ++used[g2];
+        }
+      }
+      if (!ok) flag_error(p.err, PKVD_ERR_TIMEOUT);
+      for (int g2 = 0; g2 < 2; ++g2)             // no copy is in flight when the CTA leaves
+        if (used[g2] > 0) wait_bounded(&bars[kQFull + g2], (used[g2] - 1) & 1);
+    }
+  } else if (warp == kMmaWarp || warp == kMmaWarp1) {
+    // ---------------------------------------------------------------- MMA
+    // S(n) of the stream, n counting all its K tiles: Q and K have landed and
+    // its S columns are free (head_dim 64: S(n - 1) was read; 128: PV(n - 1)
+    // is done, its weights lie there).  PV(n): the weights, V, and for a
+    // segment's first one the O columns of the segment before were read.  A
+    // stage of K, V or Q is free when both streams are done with it; one that
+    // this stream does not use it waits for all the same, so that no phase of a
+    // stage is waited for before the one before it is over.  The whole warp
+    // walks through this and one elected thread issues.
+    const bool leader = elect_one();
+    const int g = warp == kMmaWarp ? 0 : 1;
+    constexpr uint32_t fmt = std::is_same<T, __nv_bfloat16>::value ? 1u : 0u;
+    constexpr uint32_t id_s = tc_idesc(fmt, kTcKeys, 0), id_pv = tc_idesc(fmt, D, 1), hi = desc_hi(1024);
+    const uint32_t s_cols = tmem + g * kTcKeys, o_cols = tmem + kColO + g * D;
+    const uint32_t p_cols = kSepP ? tmem + kColP64 + g * 64 : s_cols;
+    bool ok = true;
+    auto wait = [&](int bar, uint32_t parity) {
+      if (ok) ok = __all_sync(FULL_MASK, wait_bounded(&bars[bar], parity));
+    };
+    int n = 0, used[2] = {0, 0};                   // this stream's K tiles of all segments; uses of the Q buffers
+    int kstg = 0, vstg = 0;                        // next stages and their phases, every tile of every segment
+    uint32_t kpar = 0, vpar = 0;
+    auto next_k = [&] {
+      if (++kstg == kKStages) kstg = 0, kpar ^= 1;
+    };
+    auto next_v = [&] {
+      if (++vstg == kVStages) vstg = 0, vpar ^= 1;
+    };
+    auto release = [&](int full, int empty, uint32_t parity) {     // of what this stream does not use
+      wait(full, parity);
+      if (ok && leader) mbar_arrive(&bars[empty]);
+    };
+    for (int r = 0; ok; ++r) {
+      ok = __all_sync(FULL_MASK, wait_item(&bars[kItemFull + r % kItemRing], (r / kItemRing) & 1));
+      if (!ok) break;
+      const Item& it = ring_items[r % kItemRing];
+      const int all = __shfl_sync(FULL_MASK, it.n, 0);
+      if (all < 0) break;
+      const int two = __shfl_sync(FULL_MASK, it.two, 0), qbuf = two ? g : __shfl_sync(FULL_MASK, it.qbuf, 0);
+      const int gn = two ? all : (all + 1 - g) >> 1;
+      const uint32_t qd = desc_lo(base + L::kQ + qbuf * H * kHalf, 16);
+      int kt = 0, vt = 0;                          // tiles of the segment that the rings have passed
+      auto tile = [&](int j) { return two ? j : 2 * j + g; };
+      auto to_k = [&](int t) {
+        for (; ok && kt < t; ++kt) {
+          release(kKFull + kstg, kKEmpty + kstg, kpar);
+          next_k();
+        }
+      };
+      auto to_v = [&](int t) {
+        for (; ok && vt < t; ++vt) {
+          release(kVFull + vstg, kVEmpty + vstg, vpar);
+          next_v();
+        }
+      };
+      auto issue_s = [&](bool last) {
+        tc_fence_after();
+        const uint32_t kd = desc_lo(base + L::kK + kstg * H * kHalf, 16);
+        if (leader) {
+#pragma unroll
+          for (int k = 0; k < D / 16; ++k) {
+            const uint32_t off = ((k >> 2) * kHalf + (k & 3) * 32) >> 4;
+            if (k == 0) mma_ss<false>(s_cols, qd, kd, hi, id_s);
+            else mma_ss<true>(s_cols, qd + off, kd + off, hi, id_s);
+          }
+          tc_commit(&bars[kSFull + g]);
+          tc_commit(&bars[kKEmpty + kstg]);
+          if (last) tc_commit(&bars[kQEmpty + qbuf]);
+        }
+        __syncwarp();
+        next_k();
+        ++kt;
+      };
+      auto issue_pv = [&](uint32_t add) {
+        tc_fence_after();
+        const uint32_t vd = desc_lo(base + L::kV + vstg * H * kHalf, kHalf);
+        if (leader) {
+#pragma unroll
+          for (int k = 0; k < kTcKeys / 16; ++k) {         // 16 keys = 8 packed columns of weights
+            const uint32_t col = kSepP ? k * 8 : (k >> 2) * kCols + (k & 3) * 8;
+            mma_ts(o_cols, p_cols + col, vd + k * 128, hi, id_pv, k > 0 ? 1u : add);
+          }
+          tc_commit(&bars[kPVDone + g]);
+          tc_commit(&bars[kVEmpty + vstg]);
+        }
+        __syncwarp();
+        next_v();
+        ++vt;
+      };
+      // The O columns of the segment before were read.  This warp's own arrival
+      // for the segment keeps the softmax warps of a segment in which the stream
+      // has no tile from completing a phase that is still to be waited for.
+      auto pass_o = [&] {
+        if (r > 0) wait(kOFree + g, (r - 1) & 1);
+        if (ok && leader) mbar_arrive(&bars[kOFree + g]);
+      };
+      if (gn > 0) {
+        // what arrives last (the softmax warps' part) is waited for last
+        to_k(tile(0));
+        wait(kQFull + qbuf, used[qbuf] & 1);
+        wait(kKFull + kstg, kpar);
+        if (n > 0) wait((kSepP ? kSRead : kPVDone) + g, (n - 1) & 1);
+        if (ok) issue_s(gn == 1);
+        for (int j = 0; ok && j < gn; ++j, ++n) {
+          const bool more = j + 1 < gn;
+          if (more) {
+            to_k(tile(j + 1));
+            wait(kKFull + kstg, kpar);
+          }
+          if (kSepP && more) {
+            wait(kSRead + g, n & 1);
+            if (ok) issue_s(j + 2 == gn);
+          }
+          to_v(tile(j));
+          wait(kVFull + vstg, vpar);
+          if (j == 0) pass_o();
+          wait(kPFull + g, n & 1);
+          if (ok) issue_pv(j);
+          if (!kSepP && more) {
+            wait(kPVDone + g, n & 1);
+            if (ok) issue_s(j + 2 == gn);
+          }
+        }
+      } else {
+        pass_o();
+        release(kQFull + qbuf, kQEmpty + qbuf, used[qbuf] & 1);
+      }
+      if (two) release(kQFull + (g ^ 1), kQEmpty + (g ^ 1), used[g ^ 1] & 1);
+      to_k(all);
+      to_v(all);
+      if (two) ++used[0], ++used[1];
+      else ++used[qbuf];
+      __syncwarp();
+      if (ok && leader) mbar_arrive(&bars[kItemFree + r % kItemRing]);
+    }
+    if (!ok && leader) flag_error(p.err, PKVD_ERR_TIMEOUT);
+    if (leader) tc_commit(&bars[kDrain + g]);     // every product issued is done when the CTA leaves
+    wait_bounded(&bars[kDrain + g], 0);
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
+    // ------------------------------------------------------------ softmax
+    // Every wait is bounded; a warp whose wait gives up leaves (the others'
+    // then give up in turn).  The two warps of a quarter of a stream's rows meet
+    // at a named barrier, which does not give up, but always brings both: each
+    // passes the same ones, a last one when it leaves, and one that gave up says
+    // so at their next meeting, where both leave.  The two streams' warps of a
+    // quarter meet at an mbarrier (kJoin), whose wait is bounded too.
+    const int g = warp >> 3, half = (warp >> 2) & 1, quarter = warp & 3, row = quarter * 32 + lane;
+    const uint32_t lane_base = (uint32_t)(quarter * 32) << 16;
+    const uint32_t s_addr = tmem + lane_base + g * kTcKeys + half * kCols;
+    const uint32_t p_addr = kSepP ? tmem + lane_base + kColP64 + g * 64 + half * 32 : s_addr;
+    const uint32_t o_addr = tmem + lane_base + kColO + g * D + half * (D / 2);
+    // what a row's threads tell each other: 256 bytes a quarter of a stream's rows
+    float* const x0 = reinterpret_cast<float*>(gbase + L::kX + quarter * 256);
+    float* const xch = x0 + g * 256;
+    Factors f;
+    f.scale = both(p.scale_log2);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) f.poly[k] = both(p.poly[k]);
+    bool ok = true;
+    auto wait = [&](int bar, uint32_t parity) {
+      if (ok) ok = __all_sync(FULL_MASK, wait_bounded(&bars[bar], parity));
+    };
+    auto arrive = [&](int bar) {                 // for the warp
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars[bar]);
+    };
+    volatile uint32_t* gave_up = reinterpret_cast<volatile uint32_t*>(gbase + L::kGaveUp) + g * 4 + quarter;
+    bool told = false;
+    auto exchange = [&] {                        // what the row's two warps wrote is readable by both
+      asm volatile("bar.sync %0, 64;" ::"r"(1 + g * 4 + quarter) : "memory");
+      if (*gave_up) ok = false, told = true;     // the same word in every lane
+    };
+    int joins = 0;
+    auto join = [&] {                            // the same for the row's four warps of both streams
+      arrive(kJoin + quarter);
+      wait(kJoin + quarter, joins & 1);
+      ++joins;
+    };
+    int n = 0;                                   // this stream's K tiles so far, of all segments
+    for (int r = 0; ok; ++r) {
+      ok = __all_sync(FULL_MASK, wait_item(&bars[kItemFull + r % kItemRing], (r / kItemRing) & 1));
+      if (!ok) break;
+      const Item& it = ring_items[r % kItemRing];
+      if (it.n < 0) break;
+      // (the shuffles: known to be uniform, and so is what the masks make of a tile)
+      auto uniform = [](int x) { return __shfl_sync(FULL_MASK, x, 0); };
+      const int all = uniform(it.n), two = uniform(it.two), cached = uniform(it.cached), slot = uniform(it.slot);
+      const int gn = two ? all : (all + 1 - g) >> 1, tb = two ? g * p.tile_tokens : 0;
+      const bool live = row < min(p.tile_tokens, it.tokens - tb) * pl.group;
+      const int tt = live ? row / pl.group : 0, gi = live ? row - tt * pl.group : 0;   // padding rows mirror row 0
+      const int64_t node = it.node0 + tb + tt;
+      const uint32_t* anc = pl.anc + node * pl.words;
+      const int pr = cached + ((MODE & kBias) || pl.window > 0 ? pl.depth[node] : 0);
+      const int wr = window_first(pr + 1, pl.window);
+      const int wr_max = __reduce_max_sync(FULL_MASK, wr);
+      const float nslope = bias_slope(p.mod, it.hk * pl.group + gi);
+      int near = 0;                              // the first key whose bias may be put together from parts (kLinear)
+      if (MODE & kBias) {
+        const float steepest = __uint_as_float(__reduce_max_sync(FULL_MASK, __float_as_uint(fabsf(nslope))));
+        near = uniform(__reduce_max_sync(FULL_MASK, pr) - (int)fminf(kLinear / steepest, 1e9f));
+      }
+      const float range = live ? p.poly_range : INFINITY;   // padding rows have no say
+      float m_ref = -INFINITY, l = 0.f;
+      const int step_keys = two ? kTcKeys : 2 * kTcKeys;
+      int kbase = (uniform(it.kt_last) - (two ? 0 : g)) * kTcKeys + half * kCols;
+      for (int j = 0; j < gn; ++j, ++n, kbase -= step_keys) {
+        // masks first: their loads run beside the product
+        const bool tree = kbase + kCols > cached;
+        const bool whole = !tree && kbase >= wr_max;
+        const int cut = min(max(cached - kbase, -INT_MAX), kCols);
+        Seen seen;
+        seen.word[0] = seen.word[1] = 0xffffffffu;
+        seen.after = 0;
+        if (tree) {
+          seen = tree_columns(anc, pl.words, wr - kbase, cut);
+        } else if (!whole) {
+          seen.word[0] = span_bits(wr - kbase, 32);
+          seen.word[1] = span_bits(wr - kbase - 32, 32);
+        }
+        wait(kSFull + g, n & 1);
+        if (!ok) break;
+        tc_fence_after();
+        float v[kCols];
+        auto read = [&] {
+          tmem_ld32(s_addr, v);
+          tmem_ld32(s_addr + 32, v + 32);
+          tmem_ld_wait();
+        };
+        read();
+        // raw scores become scores in log2 units, up to a part of a linear bias
+        // that is the same for eight columns: column c's is v[c] + bias + (c / 8) step
+        const bool linear = (MODE & kBias) && !tree && kbase >= near;
+        float kk[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) kk[i] = linear ? -nslope * (float)i : 0.f;
+        const float bias = linear ? nslope * (float)(pr - kbase) : 0.f, step = linear ? -nslope * 8.f : 0.f;
+        if (MODE & kCap) {
+          // the form is chosen by the scores that count: with what else lies in
+          // the stages the last bit would change from run to run
+          if (!whole) hide(v, seen.word, 0.f);
+          float most = 0.f;              // largest square: the polynomial's range
+#pragma unroll
+          for (int c = 0; c < kCols; c += 2)
+            odd_poly2<(MODE & kBias) != 0>(v[c], v[c + 1], f.poly, kk[c & 7], kk[(c & 7) + 1], most);
+          if (!__all_sync(FULL_MASK, most <= range)) {
+            read();
+#pragma unroll
+            for (int c = 0; c < kCols; ++c) v[c] = fmaf(tanh_fast(v[c] * p.mod.cap_in), p.mod.cap_out_log2, kk[c & 7]);
+          }
+        } else {
+#pragma unroll
+          for (int c = 0; c < kCols; c += 2) {
+            if (MODE & kBias) scale_add2(v[c], v[c + 1], f.scale, kk[c & 7], kk[(c & 7) + 1]);
+            else scale2(v[c], v[c + 1], f.scale);
+          }
+        }
+        if ((MODE & kBias) && !linear) {
+          const float first = (float)(pr - kbase);
+          int after = seen.after;
+#pragma unroll
+          for (int c = kCols - 1; c >= 0; --c) {
+            float back = first - (float)c;
+            if (tree && c >= cut) {      // a node: as far as there are visible ones after it
+              back = (float)after;
+              after += (seen.word[c >> 5] >> (c & 31)) & 1u;
+            }
+            v[c] = fmaf(nslope, back, v[c]);
+          }
+        }
+        if (!whole) hide(v, seen.word, -INFINITY);
+        // head_dim 64: the next S may overwrite these columns once nobody reads them again
+        if (kSepP) {
+          tc_fence_before();
+          arrive(kSRead + g);
+        }
+        float top = -INFINITY;
+#pragma unroll
+        for (int c = 0; c < kCols; c += 8) {
+          if ((MODE & kBias) && c > 0) top -= step;          // relative to the bias of these eight columns
+          top = tc_max3(tc_max3(top, v[c], v[c + 1]), tc_max3(v[c + 2], v[c + 3], v[c + 4]),
+                        tc_max3(v[c + 5], v[c + 6], v[c + 7]));
+        }
+        if (MODE & kBias) top += bias + (kCols / 8 - 1) * step;
+        // the two halves of a row agree on a reference, the larger maximum
+        float* x = xch + (kSepP ? (n & 1) * 512 : 0);
+        x[half * 32 + lane] = top;
+        exchange();
+        if (!ok) break;
+        const float mt = fmaxf(top, x[(half ^ 1) * 32 + lane]);
+        // f16 weights are normal down to 2^-14: with the reference 7 below the
+        // largest score they keep seven bits more
+        constexpr float kLift = std::is_same<T, __half>::value ? 7.f : 0.f;
+        const bool rebase = mt - m_ref > kLift + kRebase;
+        const bool scale_o = rebase && m_ref != -INFINITY;
+        const float alpha = scale_o ? tc_ex2(m_ref - (mt - kLift)) : 1.f;
+        if (rebase) m_ref = mt - kLift;
+        const float mu = m_ref == -INFINITY ? 0.f : m_ref;
+        uint32_t pk[kCols / 2];
+        float s0 = 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f, shift0 = bias - mu, shift1 = shift0;
+#pragma unroll
+        for (int c = 0; c < kCols; c += 4) {
+          if ((MODE & kBias) && c > 0 && c % 8 == 0) tc_add2(shift0, shift1, step, step);
+          tc_add2(v[c], v[c + 1], shift0, shift1);
+          tc_add2(v[c + 2], v[c + 3], shift0, shift1);
+          const float e0 = tc_ex2(v[c]), e1 = tc_ex2(v[c + 1]), e2 = tc_ex2(v[c + 2]), e3 = tc_ex2(v[c + 3]);
+          tc_add2(s0, s1, e0, e1);
+          tc_add2(s2, s3, e2, e3);
+          pk[c / 2] = Mma<T>::pack(e0, e1);
+          pk[c / 2 + 1] = Mma<T>::pack(e2, e3);
+        }
+        l = l * alpha + ((s0 + s1) + (s2 + s3));
+        if (kSepP && j > 0) {                    // the weights' columns are free once PV(n - 1) is done
+          wait(kPVDone + g, (n - 1) & 1);
+          tc_fence_after();
+        }
+        if (__any_sync(FULL_MASK, scale_o)) {    // O too (head_dim 128: PV(n - 1) was done before S(n))
+#pragma unroll 1
+          for (int c4 = 0; c4 < D / 64; ++c4) {
+            float o[32];
+            tmem_ld32(o_addr + c4 * 32, o);
+            tmem_ld_wait();
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] *= alpha;
+            tmem_st32(o_addr + c4 * 32, o);
+          }
+        }
+        tmem_st32(p_addr, reinterpret_cast<const float*>(pk));
+        tmem_st_wait();
+        tc_fence_before();
+        arrive(kPFull + g);
+      }
+      if (!ok) break;
+      // the last product; and so every warp of the stream is past its last exchange
+      if (gn > 0) wait(kPVDone + g, (n - 1) & 1);
+      if (!ok) break;
+      tc_fence_after();
+      // the row's sum: half 1's part to half 0, the whole and the reference back
+      if (half == 1) xch[lane] = l;
+      exchange();
+      if (!ok) break;
+      if (half == 0) {
+        l += xch[lane];
+        xch[lane] = l;
+        xch[32 + lane] = m_ref;
+      }
+      tc_fence_before();
+      if (two) exchange();
+      else join();
+      if (!ok) break;
+      tc_fence_after();
+      // factors of this row's sums in both streams' O (two: of this stream's alone)
+      float f0 = 1.f, f1 = 0.f, sum = xch[lane], top = m_ref;
+      bool has1 = false;
+      if (!two) {
+        const float l0 = x0[lane], m0 = x0[32 + lane], l1 = x0[256 + lane], m1 = x0[256 + 32 + lane];
+        top = fmaxf(m0, m1);
+        const float ref = top == -INFINITY ? 0.f : top;
+        f0 = tc_ex2(m0 - ref);
+        f1 = tc_ex2(m1 - ref);
+        sum = l0 * f0 + l1 * f1;
+        has1 = all > 1;
+      }
+      const int cols = two ? D / 2 : D / 4, col0 = two ? half * (D / 2) : (2 * g + half) * (D / 4);
+      const uint32_t o0 = tmem + lane_base + kColO + (two ? g * D : 0) + col0, o1 = tmem + lane_base + kColO + D + col0;
+      const float inv = slot >= 0 ? 1.f : sum > 0.f ? 1.f / sum : 0.f;
+      f0 *= inv;
+      f1 *= inv;
+      const int64_t rec_row = (int64_t)slot * pl.unit_rows + (tb + tt) * pl.group + gi;
+      T* dst = static_cast<T*>(p.out) + ((int64_t)(it.q0 + tb + tt) * pl.hq + (int64_t)it.hk * pl.group + gi) * D + col0;
+      float* rec = pl.rec + rec_row * D + col0;
+#pragma unroll 1
+      for (int c = 0; c < cols; c += 16) {
+        float o[16];
+        tmem_ld16(o0 + c, o);
+        if (has1) {
+          float y[16];
+          tmem_ld16(o1 + c, y);
+          tmem_ld_wait();
+          // a stream whose keys this row sees none of has zeros there
+#pragma unroll
+          for (int e = 0; e < 16; ++e) o[e] = fmaf(y[e], f1, o[e] * f0);
+        } else {
+          tmem_ld_wait();
+#pragma unroll
+          for (int e = 0; e < 16; ++e) o[e] *= f0;
+        }
+        if (!live) continue;
+        if (slot >= 0) {
+          st_global_v8(rec + c, reinterpret_cast<const uint32_t*>(o));
+          st_global_v8(rec + c + 8, reinterpret_cast<const uint32_t*>(o) + 8);
+        } else {
+          uint32_t w[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) w[e] = Mma<T>::pack(o[2 * e], o[2 * e + 1]);
+          if (p.wide_out) {
+            st_global_v8(dst + c, w);
+          } else {
+            *reinterpret_cast<uint4*>(dst + c) = make_uint4(w[0], w[1], w[2], w[3]);
+            *reinterpret_cast<uint4*>(dst + c + 8) = make_uint4(w[4], w[5], w[6], w[7]);
+          }
+        }
+      }
+      if (slot >= 0 && live && half == 0 && (two || g == 0)) pl.rec_ml[rec_row] = make_float2(top, sum);
+      tc_fence_before();
+      arrive(kOFree);
+      arrive(kOFree + 1);
+      arrive(kItemFree + r % kItemRing);
+      if (two) exchange();                       // the exchanged values are read before the next segment's
+      else join();
+    }
+    if (!told) {
+      if (!ok) *gave_up = 1;
+      exchange();
+    }
+    if (!ok && lane == 0) flag_error(p.err, PKVD_ERR_TIMEOUT);
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+template <typename T, int D, int MODE>
+cudaError_t launch_mode(const TcTree& prm, cudaStream_t stream) {
+  constexpr int smem = Layout<D>::kBytes;
+  cudaError_t e = cudaFuncSetAttribute(tree_tc_kernel<T, D, MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(tree_tc_kernel<T, D, MODE>, dim3((unsigned)prm.plan.grid), dim3(kThreads), smem, stream, prm);
+}
+
+template <typename T, int D>
+cudaError_t launch_typed(const TcTree& prm, cudaStream_t stream) {
+  const bool cap = prm.mod.cap_in != 0.f, bias = prm.mod.slopes != nullptr;
+  if (cap && bias) return launch_mode<T, D, kCap | kBias>(prm, stream);
+  if (bias) return launch_mode<T, D, kBias>(prm, stream);
+  return cap ? launch_mode<T, D, kCap>(prm, stream) : launch_mode<T, D, 0>(prm, stream);
+}
+
+}  // namespace
+
+// What the tensor copies need: the cache's strides nest, rows on 16 bytes.
+bool tree_tc_supported(const TreeArgs& a) {
+  const pkvd_cache& c = a.cache;
+  if (c.dtype != PKVD_F16 && c.dtype != PKVD_BF16) return false;
+  if (c.block_size < 8) return false;            // a box fills whole 8-row swizzle atoms
+  if ((reinterpret_cast<uintptr_t>(a.out) & 15u) || (reinterpret_cast<uintptr_t>(a.q) & 15u)) return false;
+  if (c.head_stride < c.head_dim || c.token_stride < c.head_stride * c.num_kv_heads ||
+      c.block_stride < c.token_stride * c.block_size)
+    return false;
+  CUtensorMap m;
+  return encode_cache_map(&m, c.k_base, c, c.block_size < kTcKeys ? c.block_size : kTcKeys);
+}
+
+cudaError_t launch_tree_tc(const TreeArgs& a, const TreePlan& plan, cudaStream_t stream) {
+  const pkvd_cache& c = a.cache;
+  TcTree prm;
+  prm.plan = plan;
+  prm.seg_rows = c.block_size < kTcKeys ? c.block_size : kTcKeys;
+  prm.tile_tokens = kTcRows / plan.group;
+  if (!encode_cache_map(&prm.tmap_k, c.k_base, c, prm.seg_rows) ||
+      !encode_cache_map(&prm.tmap_v, c.v_base, c, prm.seg_rows) ||
+      !encode_q_map(&prm.tmap_q, a.q, c.dtype, c.head_dim, a.num_q_heads, a.total_q, plan.group, prm.tile_tokens))
+    return cudaErrorInvalidValue;
+  prm.out = a.out;
+  prm.tables = a.block_tables;
+  prm.max_blocks = a.max_blocks_per_seq;
+  prm.block_limit = (uint32_t)(c.num_blocks < 0x80000000ll ? c.num_blocks : 0x80000000ll);
+  prm.block_size = c.block_size;
+  prm.block_shift = 0;
+  while ((1 << prm.block_shift) < c.block_size) ++prm.block_shift;
+  prm.q_box = 128u * (uint32_t)(plan.group * prm.tile_tokens);
+  prm.scale_log2 = a.scale * 1.4426950408889634f;
+  prm.mod = a.mod;
+  prm.poly_range = cap_poly(a.mod, prm.poly);
+  prm.wide_out = reinterpret_cast<uintptr_t>(a.out) % 32 == 0;
+  prm.err = a.err;
+  if (c.dtype == PKVD_BF16)
+    return c.head_dim == 64 ? launch_typed<__nv_bfloat16, 64>(prm, stream) : launch_typed<__nv_bfloat16, 128>(prm, stream);
+  return c.head_dim == 64 ? launch_typed<__half, 64>(prm, stream) : launch_typed<__half, 128>(prm, stream);
+}
+
+}  // namespace pkvd
