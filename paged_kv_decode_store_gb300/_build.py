@@ -19,7 +19,7 @@ LIB = os.path.join(PKG, "libpkvd.so")
 
 SOURCES = ["api.cu", "api_noalloc.cu", "store.cu", "rope.cu", "attention.cu", "attention_f32.cu", "attention_f16.cu",
            "attention_bf16.cu", "attention_mod_f32.cu", "attention_mod_f16.cu", "attention_mod_bf16.cu", "attention_prefix.cu", "sampler.cu", "sampler512.cu", "beam.cu", "prefill.cu", "prefill_tc.cu", "prefill_mod.cu", "prefill_fma.cu",
-           "tree.cu", "tree_tc.cu", "attention_scores_f32.cu", "attention_scores_f16.cu", "attention_scores_bf16.cu",
+           "tree.cu", "tree_tc.cu", "tree_few.cu", "attention_scores_f32.cu", "attention_scores_f16.cu", "attention_scores_bf16.cu",
            "attention_weights.cu", "evict.cu", "compact.cu", "block_manager.cpp"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC",

@@ -745,6 +745,7 @@ pkvd_status pkvd_compact_cache(const pkvd_cache* cache, const int32_t* block_tab
   a.block_size = cache->block_size;
   a.block_shift = 0;
   while ((1 << a.block_shift) < cache->block_size) ++a.block_shift;
+  a.num_kv_heads = cache->num_kv_heads;
   a.head_dim = cache->head_dim;
   a.elem_bytes = esize(cache->dtype);
   a.tables = block_tables;
@@ -764,7 +765,7 @@ pkvd_status pkvd_compact_cache(const pkvd_cache* cache, const int32_t* block_tab
   a.first = first;
   a.max_count = max_count;
   a.err = err_flag;
-  return from_cuda(launch_compact(a, num_seqs, cache->num_kv_heads, static_cast<cudaStream_t>(stream)));
+  return from_cuda(launch_compact(a, num_seqs, static_cast<cudaStream_t>(stream)));
 }
 
 namespace {

@@ -42,7 +42,7 @@ __global__ void __launch_bounds__(kThreads) add_weights_kernel(const float* scor
     before[k] = j < c ? w[j] : 0.f;
   }
   const int64_t row0 = (int64_t)i * hq + (int64_t)h * group;
-#pragma unroll 4
+#pragma unroll 8
   for (int g = 0; g < group; ++g) {
     const float2 st = stats[row0 + g];
     const float* s = scores + (row0 + g) * score_ld;

@@ -73,7 +73,7 @@ struct CompactArgs {
   void* k_base;
   void* v_base;
   int64_t block_stride, token_stride, head_stride, num_blocks;   // elements
-  int block_size, block_shift, head_dim, elem_bytes;
+  int block_size, block_shift, num_kv_heads, head_dim, elem_bytes;
   const int32_t* tables;
   const int32_t* new_tables;    // the same pointer: in place
   int max_blocks, new_max_blocks;
@@ -85,7 +85,7 @@ struct CompactArgs {
   int max_count;
   int32_t* err;
 };
-cudaError_t launch_compact(const CompactArgs& a, int num_seqs, int num_kv_heads, cudaStream_t stream);
+cudaError_t launch_compact(const CompactArgs& a, int num_seqs, cudaStream_t stream);
 
 // Which positions stay (evict.cu).
 struct EvictArgs {
@@ -104,6 +104,7 @@ cudaError_t launch_evict_select(const EvictArgs& a, int num_seqs, int heads, cud
 // Attention of drafted trees (tree.cu, tree_tc.cu).
 constexpr int kTreeMaxNodes = 256;    // nodes of a sequence's tree
 constexpr int kTreeKeys = 128;        // keys of a tile
+constexpr int kTreeFewRows = 64;      // (node, query head) rows of a tree that tree_few.cu takes
 struct TreeArgs {
   void* out;
   const void* q;

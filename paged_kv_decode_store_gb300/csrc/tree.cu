@@ -22,11 +22,12 @@
 
 namespace pkvd {
 
-cudaError_t launch_tree_tc(const TreeArgs& a, const TreePlan& plan, cudaStream_t stream);   // tree_tc.cu
+cudaError_t launch_tree_tc(const TreeArgs& a, const TreePlan& plan, cudaStream_t stream);    // tree_tc.cu
+cudaError_t launch_tree_few(const TreeArgs& a, const TreePlan& plan, cudaStream_t stream);   // tree_few.cu
 
 namespace {
 
-constexpr int kPlanThreads = 256;
+constexpr int kPlanThreads = 256, kNearSeqs = 1024;
 static_assert(kPlanThreads >= kTreeMaxNodes, "a thread a node");
 
 // CTA i < num_seqs: sequence i's ancestors.  The last one: the pieces before
@@ -36,6 +37,7 @@ __global__ void __launch_bounds__(kPlanThreads) tree_plan_kernel(const TreePlan 
   __shared__ int up[kTreeMaxNodes];
   __shared__ uint32_t bits[kTreeMaxNodes][kTreeMaxNodes / 32 + 1];
   __shared__ int64_t warp_sum[kPlanThreads / 32];
+  __shared__ int64_t near[kNearSeqs];                // pieces before the first sequences
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   if ((int)blockIdx.x == p.num_seqs) {
     pdl_wait();        // a call before this one may still read the workspace
@@ -58,9 +60,23 @@ __global__ void __launch_bounds__(kPlanThreads) tree_plan_kernel(const TreePlan 
         running += warp_sum[w];
       }
       if (i < p.num_seqs) p.starts[i] = before + upto - mine;
+      if (i < min(p.num_seqs, kNearSeqs)) near[i] = before + upto - mine;
       __syncthreads();
     }
     if (tid == 0) p.starts[p.num_seqs] = running;
+    // where the slices begin: the last sequence with no more pieces before it
+    const int64_t* starts = p.num_seqs <= kNearSeqs ? near : p.starts;
+    const int64_t slices = tree_slices(p, running);
+    for (int c = tid; c < slices; c += kPlanThreads) {
+      const int64_t f = tree_slice_begin(running, slices, c);
+      int lo = 0, hi = p.num_seqs;
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (starts[mid] <= f) lo = mid;
+        else hi = mid;
+      }
+      p.slice_seq[c] = lo;
+    }
     return;
   }
   const int i = blockIdx.x;
@@ -80,8 +96,11 @@ __global__ void __launch_bounds__(kPlanThreads) tree_plan_kernel(const TreePlan 
   if (tid < s.n)
     for (int u = tid; u >= 0; u = up[u]) {
       ++depth;
-      if (p.window <= 0 || depth < p.window) bits[tid][u >> 5] |= 1u << (u & 31);
+      if (p.window > 0 && depth >= p.window) continue;
+      if (p.by_key) atomicOr(&bits[u][tid >> 5], 1u << (tid & 31));
+      else bits[tid][u >> 5] |= 1u << (u & 31);
     }
+  if (p.by_key) __syncthreads();
   pdl_wait();
   pdl_trigger();
   if (tid < s.n) {
@@ -272,11 +291,15 @@ __global__ void __launch_bounds__(kFmaThreads) tree_fma_kernel(const TreeFma p) 
 // ------------------------------------------------------------------- merge
 // Joins the records of a (unit, head) that more than one CTA worked on:
 //   M = max m_k, out = sum 2^(m_k - M) acc_k / sum 2^(m_k - M) l_k.
-// PARTS = 1: a warp a row (eight rows a CTA).  PARTS = 8, for few rows cut into
-// many pieces: the CTA's eight warps share a row's records.
+// PARTS = 1: a warp has kMergeRows rows, whose records are on their way together
+// (one row a warp: 36 instead of see the table for 64 nodes of 8 heads a KV head,
+// where rows are cut in two or three).  PARTS = 8, for few rows cut into many
+// pieces: the CTA's eight warps share a row's records.
+constexpr int kMergeRows = 4;
+
 template <typename T, int D, int PARTS>
 __global__ void __launch_bounds__(256) tree_merge_kernel(const TreePlan p, T* __restrict__ out) {
-  constexpr int R = 8;                                   // records on their way
+  constexpr int ROWS = PARTS == 1 ? kMergeRows : 1, R = PARTS == 1 ? 3 : 8;   // rows, records of each on their way
   __shared__ float part[PARTS == 1 ? 1 : 8 * (D + 2)];
   pdl_wait();
   pdl_trigger();
@@ -284,83 +307,98 @@ __global__ void __launch_bounds__(256) tree_merge_kernel(const TreePlan p, T* __
   const int units = (p.max_q + p.unit_tokens - 1) / p.unit_tokens;
   const int item = blockIdx.x % (units * p.hkv), group = blockIdx.x / (units * p.hkv);
   const int unit = item / p.hkv, head = item % p.hkv;
+  const int64_t total = p.starts[p.num_seqs], start = p.starts[seq];
   const TreeSeq s = tree_seq(p, seq);
   if (unit >= s.units) return;
   const int tb = unit * p.unit_tokens, rows = (min(tb + p.unit_tokens, s.n) - tb) * p.group;
-  const int row = PARTS == 1 ? group * 8 + warp : group;
-  if ((PARTS == 1 ? group * 8 : group) >= rows) return;
-  const int64_t total = p.starts[p.num_seqs], slices = tree_slices(p, total);
-  const int64_t f = p.starts[seq] + ((int64_t)unit * p.hkv + head) * s.tiles;
+  const int row0 = PARTS == 1 ? (group * 8 + warp) * ROWS : group;
+  if ((PARTS == 1 ? group * 8 * ROWS : group) >= rows) return;
+  const int64_t slices = tree_slices(p, total);
+  const int64_t f = start + ((int64_t)unit * p.hkv + head) * s.tiles;
   const int a = (int)tree_slice_of(total, slices, f), b = (int)tree_slice_of(total, slices, f + s.tiles - 1);
   if (a == b) return;                                    // one CTA had it all
   const int slot_a = tree_slice_begin(total, slices, a) == f ? 0 : 1;
   constexpr int Q = D / 4, SUB = 32 / Q;                 // lanes of a row's float4 slices; records a warp takes at once
   const int d4 = lane % Q * 4, sub = lane / Q;
-  const int step = SUB * (PARTS == 1 ? 1 : 8), k_first = PARTS == 1 ? sub : warp * SUB + sub;
-  float M = -INFINITY, L = 0.f;
-  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-  const bool live = row < rows;
-  for (int k0 = a + k_first; live && k0 <= b; k0 += R * step) {
-    float2 ml[R];
-    float4 x[R];
+  const int step = SUB * PARTS, k_first = PARTS == 1 ? sub : warp * SUB + sub;
+  float M[ROWS], L[ROWS];
+  float4 o[ROWS];
+#pragma unroll
+  for (int i = 0; i < ROWS; ++i) M[i] = -INFINITY, L[i] = 0.f, o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int k0 = a + k_first; row0 < rows && k0 <= b; k0 += R * step) {
+    float2 ml[R][ROWS];
+    float4 x[R][ROWS];
 #pragma unroll
     for (int e = 0; e < R; ++e) {
       const int k = k0 + e * step;
-      ml[e] = make_float2(-INFINITY, 0.f);
-      x[e] = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (k <= b) {
-        const int64_t at = (int64_t)(2 * k + (k == a ? slot_a : 0)) * p.unit_rows + row;
-        ml[e] = p.rec_ml[at];
-        x[e] = *reinterpret_cast<const float4*>(p.rec + at * D + d4);
+      const int64_t at = (int64_t)(2 * k + (k == a ? slot_a : 0)) * p.unit_rows + row0;
+#pragma unroll
+      for (int i = 0; i < ROWS; ++i) {
+        ml[e][i] = make_float2(-INFINITY, 0.f);
+        x[e][i] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (k <= b && row0 + i < rows) {
+          ml[e][i] = p.rec_ml[at + i];
+          x[e][i] = *reinterpret_cast<const float4*>(p.rec + (at + i) * D + d4);
+        }
       }
     }
 #pragma unroll
-    for (int e = 0; e < R; ++e) {
-      if (ml[e].x == -INFINITY) continue;                // saw none of the keys
-      const float Mn = fmaxf(M, ml[e].x), cs = exp2f(M - Mn), cr = exp2f(ml[e].x - Mn);
-      L = L * cs + ml[e].y * cr;
-      o.x = o.x * cs + x[e].x * cr;
-      o.y = o.y * cs + x[e].y * cr;
-      o.z = o.z * cs + x[e].z * cr;
-      o.w = o.w * cs + x[e].w * cr;
-      M = Mn;
-    }
+    for (int e = 0; e < R; ++e)
+#pragma unroll
+      for (int i = 0; i < ROWS; ++i) {
+        if (ml[e][i].x == -INFINITY) continue;           // saw none of the keys
+        const float Mn = fmaxf(M[i], ml[e][i].x), cs = exp2f(M[i] - Mn), cr = exp2f(ml[e][i].x - Mn);
+        L[i] = L[i] * cs + ml[e][i].y * cr;
+        o[i].x = o[i].x * cs + x[e][i].x * cr;
+        o[i].y = o[i].y * cs + x[e][i].y * cr;
+        o[i].z = o[i].z * cs + x[e][i].z * cr;
+        o[i].w = o[i].w * cs + x[e][i].w * cr;
+        M[i] = Mn;
+      }
   }
-  auto join = [&](float Mo, float Lo, float4 x) {
-    const float Mn = fmaxf(M, Mo), base = Mn == -INFINITY ? 0.f : Mn;
-    const float ca = exp2f(M - base), cb = exp2f(Mo - base);
-    L = L * ca + Lo * cb;
-    o = make_float4(o.x * ca + x.x * cb, o.y * ca + x.y * cb, o.z * ca + x.z * cb, o.w * ca + x.w * cb);
-    M = Mn;
+  auto join = [&](int i, float Mo, float Lo, float4 x) {
+    const float Mn = fmaxf(M[i], Mo), base = Mn == -INFINITY ? 0.f : Mn;
+    const float ca = exp2f(M[i] - base), cb = exp2f(Mo - base);
+    L[i] = L[i] * ca + Lo * cb;
+    o[i] = make_float4(o[i].x * ca + x.x * cb, o[i].y * ca + x.y * cb, o[i].z * ca + x.z * cb, o[i].w * ca + x.w * cb);
+    M[i] = Mn;
   };
 #pragma unroll
-  for (int off = Q; off < 32; off <<= 1) {
-    const float Mo = __shfl_xor_sync(FULL_MASK, M, off), Lo = __shfl_xor_sync(FULL_MASK, L, off);
-    const float4 x = make_float4(__shfl_xor_sync(FULL_MASK, o.x, off), __shfl_xor_sync(FULL_MASK, o.y, off),
-                                 __shfl_xor_sync(FULL_MASK, o.z, off), __shfl_xor_sync(FULL_MASK, o.w, off));
-    join(Mo, Lo, x);
-  }
+  for (int i = 0; i < ROWS; ++i)
+#pragma unroll
+    for (int off = Q; off < 32; off <<= 1) {
+      const float Mo = __shfl_xor_sync(FULL_MASK, M[i], off), Lo = __shfl_xor_sync(FULL_MASK, L[i], off);
+      const float4 x = make_float4(__shfl_xor_sync(FULL_MASK, o[i].x, off), __shfl_xor_sync(FULL_MASK, o[i].y, off),
+                                   __shfl_xor_sync(FULL_MASK, o[i].z, off), __shfl_xor_sync(FULL_MASK, o[i].w, off));
+      join(i, Mo, Lo, x);
+    }
   if constexpr (PARTS > 1) {
     float* mine = part + warp * (D + 2);
     if (sub == 0) {
-      mine[d4] = o.x, mine[d4 + 1] = o.y, mine[d4 + 2] = o.z, mine[d4 + 3] = o.w;
-      if (d4 == 0) mine[D] = M, mine[D + 1] = L;
+      mine[d4] = o[0].x, mine[d4 + 1] = o[0].y, mine[d4 + 2] = o[0].z, mine[d4 + 3] = o[0].w;
+      if (d4 == 0) mine[D] = M[0], mine[D + 1] = L[0];
     }
     __syncthreads();
     if (warp > 0) return;
     for (int w = 1; w < 8; ++w) {
       const float* x = part + w * (D + 2);
-      join(x[D], x[D + 1], make_float4(x[d4], x[d4 + 1], x[d4 + 2], x[d4 + 3]));
+      join(0, x[D], x[D + 1], make_float4(x[d4], x[d4 + 1], x[d4 + 2], x[d4 + 3]));
     }
   }
-  if (!live || sub > 0) return;
-  const int t = row / p.group, gi = row % p.group;
-  T* dst = out + ((int64_t)(s.q0 + tb + t) * p.hq + (int64_t)head * p.group + gi) * D + d4;
-  const float inv = L > 0.f ? 1.f / L : 0.f;
-  dst[0] = DT<T>::from_f(o.x * inv);
-  dst[1] = DT<T>::from_f(o.y * inv);
-  dst[2] = DT<T>::from_f(o.z * inv);
-  dst[3] = DT<T>::from_f(o.w * inv);
+  if (sub > 0) return;
+#pragma unroll
+  for (int i = 0; i < ROWS; ++i) {
+    const int row = row0 + i;
+    if (row >= rows) break;
+    const int t = row / p.group, gi = row % p.group;
+    T* dst = out + ((int64_t)(s.q0 + tb + t) * p.hq + (int64_t)head * p.group + gi) * D + d4;
+    const float inv = L[i] > 0.f ? 1.f / L[i] : 0.f;
+    if constexpr (sizeof(T) == 2) {                      // out is 16-byte aligned, rows of 128 bytes and more
+      *reinterpret_cast<uint2*>(dst) = make_uint2(Mma<T>::pack(o[i].x * inv, o[i].y * inv), Mma<T>::pack(o[i].z * inv, o[i].w * inv));
+    } else {
+      *reinterpret_cast<float4*>(dst) = make_float4(o[i].x * inv, o[i].y * inv, o[i].z * inv, o[i].w * inv);
+    }
+  }
 }
 
 // ------------------------------------------------------------------ accept
@@ -430,8 +468,12 @@ __global__ void __launch_bounds__(kAcceptWarps * 32) tree_accept_kernel(const Ac
 // ------------------------------------------------------------------- host
 size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 
+bool few_rows(int group, int max_q) { return group * max_q <= kTreeFewRows; }
+
 int unit_tokens_of(int path, int group, int max_q) {
   if (path == PKVD_PATH_FMA) return kPassRows / group > 1 ? kPassRows / group : 1;
+  // trees of few rows: a unit is a whole tree, its rows the columns of tree_few.cu
+  if (few_rows(group, max_q)) return max_q;
   const int tile = 128 / group;                          // two Q tiles, or one where that holds every tree
   return max_q > tile ? 2 * tile : tile;
 }
@@ -439,12 +481,13 @@ int unit_tokens_of(int path, int group, int max_q) {
 int grid_of(int path, int sms) { return path == PKVD_PATH_FMA ? 2 * sms : sms; }
 
 struct WorkspaceLayout {
-  size_t starts, anc, depth, rec, rec_ml, bytes;
+  size_t starts, slice_seq, anc, depth, rec, rec_ml, bytes;
   WorkspaceLayout(int path, int num_seqs, int group, int head_dim, int max_q, int sms) {
     const int words = (max_q + 31) / 32;
     const size_t rows = (size_t)2 * grid_of(path, sms) * unit_tokens_of(path, group, max_q) * group;
     starts = 0;
-    anc = starts + up256(sizeof(int64_t) * ((size_t)num_seqs + 1));
+    slice_seq = starts + up256(sizeof(int64_t) * ((size_t)num_seqs + 1));
+    anc = slice_seq + up256(sizeof(int32_t) * (size_t)grid_of(path, sms));
     depth = anc + up256(sizeof(uint32_t) * (size_t)num_seqs * max_q * words);
     rec_ml = depth + up256(sizeof(int32_t) * (size_t)num_seqs * max_q);
     rec = rec_ml + up256(sizeof(float2) * rows);
@@ -466,7 +509,7 @@ cudaError_t launch_merge(const TreePlan& p, void* out, cudaStream_t stream) {
   const int rows = (p.max_q < p.unit_tokens ? p.max_q : p.unit_tokens) * p.group;
   // pieces of an item: about grid / items; a warp takes eight records a round
   const bool many = p.grid > 8 * items * p.num_seqs;
-  const int64_t groups = many ? rows : (rows + 7) / 8;
+  const int64_t groups = many ? rows : (rows + 8 * kMergeRows - 1) / (8 * kMergeRows);
   const dim3 grid((unsigned)(items * groups), (unsigned)p.num_seqs);
   return many ? launch_pdl(tree_merge_kernel<T, D, 8>, grid, dim3(256), 0, stream, p, static_cast<T*>(out))
               : launch_pdl(tree_merge_kernel<T, D, 1>, grid, dim3(256), 0, stream, p, static_cast<T*>(out));
@@ -502,7 +545,9 @@ cudaError_t launch_tree(const TreeArgs& a, cudaStream_t stream) {
   p.window = a.window;
   p.table_tokens = (int64_t)a.max_blocks_per_seq * c.block_size;
   p.grid = grid_of(a.path, a.sms);
+  p.by_key = a.path == PKVD_PATH_TC && few_rows(group, a.max_seqlen_q);
   p.starts = reinterpret_cast<int64_t*>(ws + lay.starts);
+  p.slice_seq = reinterpret_cast<int32_t*>(ws + lay.slice_seq);
   p.anc = reinterpret_cast<uint32_t*>(ws + lay.anc);
   p.depth = reinterpret_cast<int32_t*>(ws + lay.depth);
   p.rec = reinterpret_cast<float*>(ws + lay.rec);
@@ -510,7 +555,7 @@ cudaError_t launch_tree(const TreeArgs& a, cudaStream_t stream) {
   cudaError_t e = launch_pdl(tree_plan_kernel, dim3(a.num_seqs + 1), dim3(kPlanThreads), 0, stream, p, a.parents, a.err);
   if (e != cudaSuccess) return e;
   if (a.path == PKVD_PATH_TC) {
-    e = launch_tree_tc(a, p, stream);
+    e = few_rows(group, a.max_seqlen_q) ? launch_tree_few(a, p, stream) : launch_tree_tc(a, p, stream);
   } else {
     TreeFma f;
     f.plan = p;

@@ -27,14 +27,15 @@ struct TreePlan {
   int grid;                                 // CTAs; slices are at most as many
   // the workspace
   int64_t* starts;                          // [num_seqs + 1]: pieces before a sequence
-  uint32_t* anc;                            // [num_seqs][max_q][words]: a node's visible ancestors and itself
+  int32_t* slice_seq;                       // [grid]: the sequence that a slice begins in
+  // [num_seqs][max_q][words]: a node's visible ancestors and itself; by_key: the
+  // nodes that see it, itself among them
+  uint32_t* anc;
+  int by_key;
   int32_t* depth;                           // [num_seqs][max_q]
   float* rec;                               // [2 grid][unit_rows][D]: sums of a slice's first and last segment
   float2* rec_ml;                           // [2 grid][unit_rows]: maximum (log2 units), sum of weights
 };
-
-// A slice has at least so many tiles: a record more costs what a tile does.
-constexpr int kTreeMinTiles = 2;
 
 struct TreeSeq {
   int q0, n, klen, cached;
@@ -62,26 +63,12 @@ __device__ __forceinline__ TreeSeq tree_seq(const TreePlan& p, int i) {
 
 // Slices of a batch of `total` pieces, and where one begins.
 __device__ __forceinline__ int64_t tree_slices(const TreePlan& p, int64_t total) {
-  const int64_t most = total / kTreeMinTiles;
-  return most < 1 ? (total > 0 ? 1 : 0) : most < p.grid ? most : p.grid;
+  return total < p.grid ? total : p.grid;
 }
 __device__ __forceinline__ int64_t tree_slice_begin(int64_t total, int64_t slices, int64_t c) { return total * c / slices; }
 // The slice that holds piece f.
 __device__ __forceinline__ int64_t tree_slice_of(int64_t total, int64_t slices, int64_t f) {
   return ((f + 1) * slices - 1) / total;
-}
-
-// The sequence that holds piece f, for a whole warp: the last i with starts[i] <= f.
-__device__ __forceinline__ int tree_find(const TreePlan& p, int64_t f) {
-  const int lane = threadIdx.x & 31;
-  int lo = 0, hi = p.num_seqs;
-  while (hi - lo > 1) {
-    const int step = (hi - lo + 31) / 32, probe = lo + lane * step;
-    const uint32_t below = __ballot_sync(FULL_MASK, probe < hi && p.starts[min(probe, hi - 1)] <= f);
-    lo += (31 - __clz(below)) * step;      // lane 0's is always below
-    hi = min(hi, lo + step);
-  }
-  return lo;
 }
 
 // One segment of a slice: tiles [t0, t1) of a (unit, head).
@@ -91,7 +78,7 @@ struct TreeSegment {
   int slot;                                 // of its record; -1: the whole (unit, head)
 };
 
-// Walks a slice's segments (every thread of the caller alike).
+// Walks a slice's segments.
 struct TreeWalk {
   int64_t at, end, begin;
   int cta, seq;
@@ -100,7 +87,7 @@ struct TreeWalk {
     cta = c;
     at = begin = tree_slice_begin(total, slices, c);
     end = tree_slice_begin(total, slices, c + 1);
-    seq = tree_find(p, at);
+    seq = p.slice_seq[c];
     s = tree_seq(p, seq);
   }
   __device__ bool next(const TreePlan& p, TreeSegment& g) {

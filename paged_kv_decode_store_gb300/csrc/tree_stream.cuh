@@ -1,0 +1,277 @@
+// What the tensor-core kernels of drafted trees share (tree_tc.cu: up to two Q
+// tiles of 128 rows; tree_few.cu: up to 64 rows): a slice's segments, the copies
+// of K, V and Q, and the barriers between them.
+#pragma once
+
+#include <climits>
+
+#include "common.cuh"
+#include "launch.h"
+#include "score_mod.cuh"
+#include "tc_softmax.cuh"
+#include "tcgen05.cuh"
+#include "tree_plan.cuh"
+
+namespace pkvd {
+
+constexpr int kTreeThreads = 640;
+constexpr int kStreamWarps = 8;           // softmax warps of a stream
+constexpr int kKvWarp = 16, kMmaWarp = 17, kQWarp = 18, kMmaWarp1 = 19;
+constexpr uint32_t kTmemCols = 512;
+enum : int { kCap = 1, kBias = 2 };       // what a call modifies, known when compiled
+constexpr float kRebase = 8.f;            // a new reference when the maximum grows by > 2^8
+
+// mbarriers: six for each stage of K and V; those of a stream take + g
+enum : int {
+  kKFull = 0, kKEmpty = 6, kVFull = 12, kVCut = 18, kVEmpty = 24, kQFull = 30, kQEmpty = 32, kItemFull = 34,
+  kItemFree = 38, kDrain = 42, kOFree = 44, kJoin = 46, kSFull = 50, kSRead = 54, kPFull = 58, kPVDone = 60, kNumBars = 62
+};
+constexpr uint32_t kBarBytes = 512, kTmemSlot = 8 * kNumBars;
+static_assert(kTmemSlot + 4 <= kBarBytes, "behind the barriers");
+constexpr int kItemRing = 4;
+constexpr int kItemUsers = 3 + 2 * kStreamWarps;   // K/V, two MMA and softmax warps
+
+struct TcTree {
+  CUtensorMap tmap_q, tmap_k, tmap_v;
+  TreePlan plan;
+  void* out;
+  const int32_t* tables;
+  int max_blocks;
+  int block_size, block_shift;   // a power of two
+  uint32_t block_limit;          // num_blocks, at most 2^31
+  int seg_rows;                  // rows per TMA box of the cache: min(block_size, 128)
+  int tile_tokens;               // nodes of a Q tile
+  uint32_t q_box;                // bytes of one 64-column box of a Q tile
+  float scale_log2;
+  ScoreMod mod;
+  float poly[4], poly_range;     // cap_poly
+  int wide_out;                  // out is 32-byte aligned: stores of 32 bytes
+  int32_t* err;
+};
+
+// A segment: n tiles of a (unit, KV head) from tile kt_last down.  n = -1: no more.
+struct __align__(16) Item {
+  int seq, hk, q0, tokens;       // q0: the unit's first row of q
+  int node0, cached, lo, hi;     // node0: its place in the plan's arrays; keys outside [lo, hi] are not read
+  int kt_last, n, slot, two;     // two Q tiles?
+  int qbuf, late, pad[2];        // where a single Q tile lies; more than the unit's last tile, and that
+};
+constexpr uint32_t kItemBytes = sizeof(Item) * kItemRing;
+
+__device__ __forceinline__ int window_first(int c, int window) { return (window > 0 && c > window) ? c - window : 0; }
+
+// Barriers and what a kernel's layout L says of its arrivals.
+template <typename L>
+__device__ __forceinline__ void tree_init_barriers(uint64_t* bars) {
+  for (int i = 0; i < kNumBars; ++i) {
+    int arrivals = 1;
+    if ((i >= kPFull && i < kPVDone) || (i >= kSRead && i < kPFull)) arrivals = kStreamWarps;
+    if (i >= kOFree && i < kJoin) arrivals = 2 * kStreamWarps + 1;
+    if ((i >= kKEmpty && i < kVFull) || (i >= kVEmpty && i < kQFull) || i == kQEmpty || i == kQEmpty + 1) arrivals = 2;
+    if (i >= kItemFree && i < kDrain) arrivals = kItemUsers;
+    if (i >= kJoin && i < kSFull) arrivals = L::kJoinWarps;
+    mbar_init(&bars[i], arrivals);
+  }
+  fence_mbar_init();
+}
+
+// K and V (one warp).  Lane s copies segment s of a tile; K runs kAhead tiles
+// ahead of V.  A V tile with rows that are not read lands on a barrier of its own
+// (kVCut) and is released with those rows zeroed, so that they never weigh in.
+template <typename L>
+__device__ __forceinline__ void tree_copy_kv(const TcTree& p, uint64_t* bars, uint32_t base, const Item* ring_items, int lane) {
+  constexpr int H = L::kHalves, kKStages = L::kKStages, kVStages = L::kVStages;
+  constexpr int kAhead = kKStages - 2;
+  const uint32_t box = (uint32_t)p.seg_rows * 128u;
+  const int nseg = kTcKeys / p.seg_rows;
+  const uint32_t whole = (1u << nseg) - 1u;  // at most 16 segments
+  if (lane == 0) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&p.tmap_k)) : "memory");
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&p.tmap_v)) : "memory");
+  }
+  constexpr int kNone = INT_MIN;             // a segment of rows that are not read: nothing to load
+  bool ok = true;
+  int kstg = 0, vstg = 0, landed = 0;        // next stages; phases of kVCut
+  uint32_t kpar = 1, vpar = 1;               // parities of their release (nothing to wait for in the first round)
+  auto wait = [&](int bar, uint32_t parity) {
+    if (ok) ok = __all_sync(FULL_MASK, wait_bounded(&bars[bar], parity));
+  };
+  // one operand of a tile into a stage, whose block id is b in lane s
+  auto copy = [&](const CUtensorMap* map, uint32_t dst, int bar, int ks, int hk, int b) {
+    const bool good = (uint32_t)b < p.block_limit;
+    const uint32_t loaded = __ballot_sync(FULL_MASK, good);
+    uint32_t bytes = H * kHalf;
+    dst += lane * box;
+    if (loaded != whole) {
+      bytes = (uint32_t)__popc(loaded) * box * H;
+      const uint32_t bad = __ballot_sync(FULL_MASK, b != kNone && !good);
+      if (bad) {                             // a bad block id reads as zeros
+        if (lane == 0) flag_error(p.err, PKVD_ERR_BLOCK_ID);
+        if ((bad >> lane) & 1u) {
+          for (int h = 0; h < H; ++h)
+            for (uint32_t o = 0; o < box; o += 16) st_shared_v4(dst + h * kHalf + o, make_uint4(0u, 0u, 0u, 0u));
+          fence_proxy_async_smem();
+        }
+        __syncwarp();
+      }
+    }
+    if (lane == 0) mbar_arrive_expect_tx(&bars[bar], bytes);
+    __syncwarp();
+    if (good) {
+#pragma unroll
+      for (int h = 0; h < H; ++h) tma_load4(dst + h * kHalf, map, h * 64, hk, ks & (p.block_size - 1), b, &bars[bar]);
+    }
+  };
+  for (int r = 0; ok; ++r) {
+    ok = __all_sync(FULL_MASK, wait_item(&bars[kItemFull + r % kItemRing], (r / kItemRing) & 1));
+    if (!ok) break;
+    const Item& cur = ring_items[r % kItemRing];
+    if (cur.n < 0) break;
+    const int32_t* table = p.tables + (int64_t)cur.seq * p.max_blocks;
+    const int n = cur.n, hk = cur.hk, lo = cur.lo, hi = cur.hi, kt_last = cur.kt_last;
+    auto key_of = [&](int t) { return (kt_last - t) * kTcKeys + lane * p.seg_rows; };
+    auto fetch = [&](int t) -> int {
+      const int ks = key_of(t);
+      if (t >= n || lane >= nseg || ks > hi || ks + p.seg_rows - 1 < lo) return kNone;
+      return __ldg(table + (ks >> p.block_shift));
+    };
+    auto copy_k = [&](int t, int b) {
+      wait(kKEmpty + kstg, kpar);
+      if (!ok) return;
+      copy(&p.tmap_k, base + L::kK + kstg * H * kHalf, kKFull + kstg, key_of(t), hk, b);
+      if (++kstg == kKStages) kstg = 0, kpar ^= 1;
+    };
+    int b[4];                                // block ids of V tile t and the three after it
+#pragma unroll
+    for (int i = 0; i < 4; ++i) b[i] = fetch(i);
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i)
+      if (i < n) copy_k(i, b[i]);
+    for (int t = 0; ok && t < n; ++t) {
+      if (t + kAhead < n) copy_k(t + kAhead, b[kAhead]);
+      wait(kVEmpty + vstg, vpar);
+      if (!ok) break;
+      const int kbase = (kt_last - t) * kTcKeys;
+      const bool cut = kbase < lo || kbase + kTcKeys - 1 > hi;
+      const uint32_t dst = base + L::kV + vstg * H * kHalf;
+      copy(&p.tmap_v, dst, (cut ? kVCut : kVFull) + vstg, kbase + lane * p.seg_rows, hk, b[0]);
+      if (cut) {
+        wait(kVCut + vstg, (landed >> vstg) & 1);
+        landed ^= 1 << vstg;
+        if (!ok) break;
+        for (int rr = lane; rr < kTcKeys; rr += 32) {
+          const int kp = kbase + rr;
+          if (kp >= lo && kp <= hi) continue;
+          for (int h = 0; h < H; ++h)
+            for (int c = 0; c < 8; ++c) st_shared_v4(dst + h * kHalf + rr * 128 + c * 16, make_uint4(0u, 0u, 0u, 0u));
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars[kVFull + vstg]);
+      }
+      if (++vstg == kVStages) vstg = 0, vpar ^= 1;
+      b[0] = b[1];
+      b[1] = b[2];
+      b[2] = b[3];
+      b[3] = fetch(t + 4);
+    }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&bars[kItemFree + r % kItemRing]);
+  }
+  if (!ok && lane == 0) {
+    // gave up: let the copies still in flight land before the CTA leaves
+    flag_error(p.err, PKVD_ERR_TIMEOUT);
+    // (a stage's full barrier is behind its release, or one phase ahead of it)
+    for (int u = 0; u < kKStages; ++u) wait_bounded(&bars[kKFull + u], (kpar ^ (u < kstg ? 0u : 1u)) ^ 1u);
+    for (int u = 0; u < kVStages; ++u) wait_bounded(&bars[kVFull + u], (vpar ^ (u < vstg ? 0u : 1u)) ^ 1u);
+  }
+}
+
+// Segments and Q (one warp).  A Q tile's rows are one box per 64 columns (G heads
+// of tile_tokens nodes).  Two tiles of a unit fill both buffers; single ones take
+// them in turn (L::kQBufs), so the next is loaded while the last is in use.
+template <typename L>
+__device__ __forceinline__ void tree_segments(const TcTree& p, uint64_t* bars, uint32_t base, Item* ring_items, int lane) {
+  constexpr int H = L::kHalves;
+  const TreePlan& pl = p.plan;
+  const int64_t total = pl.starts[pl.num_seqs], slices = tree_slices(pl, total);
+  TreeWalk walk;
+  walk.at = walk.end = 0;
+  if ((int64_t)blockIdx.x < slices) walk.start(pl, blockIdx.x, total, slices);
+  if (lane == 0) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&p.tmap_q)) : "memory");
+    bool ok = true;
+    int used[2] = {0, 0}, turn = 0;
+    for (int r = 0; ok; ++r) {
+      const int slot = r % kItemRing;
+      if (r >= kItemRing) ok = wait_item(&bars[kItemFree + slot], ((r / kItemRing) - 1) & 1);
+      if (!ok) break;
+      Item it;
+      TreeSegment g;
+      it.n = -1;
+      if (walk.next(pl, g)) {
+        const int tb = g.unit * pl.unit_tokens;
+        it.seq = g.seq;
+        it.hk = g.head;
+        it.q0 = walk.s.q0 + tb;
+        it.tokens = min(pl.unit_tokens, walk.s.n - tb);
+        it.node0 = g.seq * pl.max_q + tb;
+        it.cached = walk.s.cached;
+        it.lo = walk.s.lo;
+        it.hi = walk.s.klen - 1;
+        it.kt_last = walk.s.lo_tile + g.t1 - 1;
+        it.n = g.t1 - g.t0;
+        it.slot = g.slot;
+      it.late = g.t1 == walk.s.tiles && it.n > 1;
+        it.two = it.tokens > p.tile_tokens;
+        it.qbuf = turn;
+        if (!it.two && L::kQBufs == 2) turn ^= 1;
+      }
+      ring_items[slot] = it;
+      mbar_arrive(&bars[kItemFull + slot]);
+      if (it.n < 0) break;
+#pragma unroll
+      for (int g2 = 0; g2 < 2; ++g2) {
+        if (!ok || !(it.two || it.qbuf == g2)) continue;
+        if (used[g2] > 0) ok = wait_item(&bars[kQEmpty + g2], (used[g2] - 1) & 1);
+        if (!ok) continue;
+        mbar_arrive_expect_tx(&bars[kQFull + g2], p.q_box * H);
+        for (int h = 0; h < H; ++h)
+          tma_load3(base + L::kQ + (g2 * H + h) * L::kQHalf, &p.tmap_q, h * 64, it.hk * pl.group,
+                    it.q0 + (it.two ? g2 * p.tile_tokens : 0), &bars[kQFull + g2]);
+        ++used[g2];
+      }
+    }
+    if (!ok) flag_error(p.err, PKVD_ERR_TIMEOUT);
+    for (int g2 = 0; g2 < 2; ++g2)             // no copy is in flight when the CTA leaves
+      if (used[g2] > 0) wait_bounded(&bars[kQFull + g2], (used[g2] - 1) & 1);
+  }
+}
+
+// Host: the parameters, without the shape of a Q tile's rows.
+inline bool tree_tc_params(const TreeArgs& a, const TreePlan& plan, int tile_tokens, TcTree* prm) {
+  const pkvd_cache& c = a.cache;
+  prm->plan = plan;
+  prm->seg_rows = c.block_size < kTcKeys ? c.block_size : kTcKeys;
+  prm->tile_tokens = tile_tokens;
+  if (!encode_cache_map(&prm->tmap_k, c.k_base, c, prm->seg_rows) ||
+      !encode_cache_map(&prm->tmap_v, c.v_base, c, prm->seg_rows) ||
+      !encode_q_map(&prm->tmap_q, a.q, c.dtype, c.head_dim, a.num_q_heads, a.total_q, plan.group, tile_tokens))
+    return false;
+  prm->out = a.out;
+  prm->tables = a.block_tables;
+  prm->max_blocks = a.max_blocks_per_seq;
+  prm->block_limit = (uint32_t)(c.num_blocks < 0x80000000ll ? c.num_blocks : 0x80000000ll);
+  prm->block_size = c.block_size;
+  prm->block_shift = 0;
+  while ((1 << prm->block_shift) < c.block_size) ++prm->block_shift;
+  prm->q_box = 128u * (uint32_t)(plan.group * tile_tokens);
+  prm->scale_log2 = a.scale * 1.4426950408889634f;
+  prm->mod = a.mod;
+  prm->poly_range = cap_poly(a.mod, prm->poly);
+  prm->wide_out = reinterpret_cast<uintptr_t>(a.out) % 32 == 0;
+  prm->err = a.err;
+  return true;
+}
+
+}  // namespace pkvd

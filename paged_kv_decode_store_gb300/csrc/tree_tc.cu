@@ -20,30 +20,17 @@
 // Warps (20): 0-7 and 8-15 softmax of stream 0 and 1 (warp w of a stream: TMEM
 // lanes 32 (w % 4) .., keys 64 (w / 4) ..), 16 copies of K and V, 17 and 19 the
 // products of stream 0 and 1, 18 the segments and Q.
-#include <climits>
-
-#include "common.cuh"
-#include "launch.h"
-#include "score_mod.cuh"
-#include "tc_softmax.cuh"
-#include "tcgen05.cuh"
-#include "tree_plan.cuh"
+#include "tree_stream.cuh"
 
 namespace pkvd {
 
 namespace {
 
-constexpr int kThreads = 640;
-constexpr int kStreamWarps = 8;
-constexpr int kKvWarp = 16, kMmaWarp = 17, kQWarp = 18, kMmaWarp1 = 19;
-constexpr uint32_t kTmemCols = 512;
 // TMEM columns: S of stream g at [128 g, 128 g + 128), O at [256 + g D, 256 + g D
 // + D).  head_dim 128: a half's weights overwrite the first 32 of its own 64 S
 // columns; head_dim 64: they have [384 + 64 g, 448 + 64 g), so the next S may be
 // computed while they are in use.
 constexpr uint32_t kColO = 256, kColP64 = 384;
-enum : int { kCap = 1, kBias = 2 };       // what a call modifies, known when compiled
-constexpr float kRebase = 8.f;            // re-base the running maximum when it grows by > 2^8
 constexpr float kLinear = 16384.f;        // largest bias (log2 units) put together from parts
 
 template <int D>
@@ -54,54 +41,17 @@ struct Layout {
   static constexpr uint32_t kK = kQ + 2 * kHalves * kHalf;
   static constexpr uint32_t kV = kK + kKStages * kHalves * kHalf;
   static constexpr uint32_t kBar = kV + kVStages * kHalves * kHalf;
-  static constexpr uint32_t kX = kBar + 512;                           // exchange: 1024 bytes a stream and buffer
+  static constexpr uint32_t kQHalf = kHalf;                            // bytes of a Q tile's 64 columns
+  static constexpr int kQBufs = 2, kJoinWarps = 4;                                // a quarter of the rows, both streams
+  static constexpr uint32_t kX = kBar + kBarBytes;                         // exchange: 1024 bytes a stream and buffer
   static constexpr int kXBufs = D == 64 ? 2 : 1;
   static constexpr uint32_t kItems = kX + kXBufs * 2048;               // ring of segments
-  static constexpr uint32_t kGaveUp = kItems + 256;                    // one word a pair of softmax warps
+  static constexpr uint32_t kGaveUp = kItems + kItemBytes;                    // one word a pair of softmax warps
   static constexpr uint32_t kEnd = kGaveUp + 32;
   // at least 120 KB so that one CTA (which holds all TMEM) is resident per SM
   static constexpr uint32_t kBytes = kEnd > 122880u ? kEnd : 122880u;
 };
 static_assert(Layout<128>::kBytes <= 232448, "227 KB of shared memory");
-
-// mbarriers; those of a stream take + g
-enum : int {
-  kKFull = 0, kKEmpty = 4, kVFull = 8, kVCut = 12, kVEmpty = 16, kQFull = 20, kQEmpty = 22, kSFull = 24, kPFull = 26,
-  kPVDone = 28, kSRead = 30, kOFree = 32, kItemFull = 34, kItemFree = 38, kDrain = 42, kJoin = 44, kNumBars = 48
-};
-constexpr uint32_t kTmemSlot = 8 * kNumBars;
-static_assert(kTmemSlot + 4 <= 512, "behind the barriers");
-constexpr int kItemRing = 4;
-constexpr int kItemUsers = 3 + 2 * kStreamWarps;   // K/V, two MMA and softmax warps
-
-struct TcTree {
-  CUtensorMap tmap_q, tmap_k, tmap_v;
-  TreePlan plan;
-  void* out;
-  const int32_t* tables;
-  int max_blocks;
-  int block_size, block_shift;   // a power of two
-  uint32_t block_limit;          // num_blocks, at most 2^31
-  int seg_rows;                  // rows per TMA box of the cache: min(block_size, 128)
-  int tile_tokens;               // nodes of a Q tile
-  uint32_t q_box;                // bytes of one 64-column box of a Q tile
-  float scale_log2;
-  ScoreMod mod;
-  float poly[4], poly_range;     // cap_poly
-  int wide_out;                  // out is 32-byte aligned: stores of 32 bytes
-  int32_t* err;
-};
-
-// A segment: n tiles of a (unit, KV head) from tile kt_last down.  n = -1: no more.
-struct __align__(16) Item {
-  int seq, hk, q0, tokens;       // q0: the unit's first row of q
-  int node0, cached, lo, hi;     // node0: its place in the plan's arrays; keys outside [lo, hi] are not read
-  int kt_last, n, slot, two;     // two Q tiles?
-  int qbuf, pad[3];              // where a single Q tile lies
-};
-static_assert(sizeof(Item) * kItemRing == 256, "the ring in Layout");
-
-__device__ __forceinline__ int window_first(int c, int window) { return (window > 0 && c > window) ? c - window : 0; }
 
 __device__ __forceinline__ void tmem_ld16(uint32_t taddr, float* v) {
   uint32_t* r = reinterpret_cast<uint32_t*>(v);
@@ -168,7 +118,7 @@ __device__ __forceinline__ void hide(float (&v)[kCols], const uint32_t (&seen)[2
 }
 
 template <typename T, int D, int MODE>
-__global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const __grid_constant__ TcTree p) {
+__global__ void __launch_bounds__(kTreeThreads, 1) tree_tc_kernel(const __grid_constant__ TcTree p) {
   using L = Layout<D>;
   constexpr int H = L::kHalves, kKStages = L::kKStages, kVStages = L::kVStages;
   constexpr bool kSepP = D == 64;
@@ -179,21 +129,10 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const __grid_const
   const TreePlan& pl = p.plan;
   const int warp = __shfl_sync(FULL_MASK, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;   // known to be uniform
 
-  if (threadIdx.x == 0) {
-    for (int i = 0; i < kNumBars; ++i) {
-      int arrivals = 1;
-      if ((i >= kPFull && i < kPVDone) || (i >= kSRead && i < kOFree)) arrivals = kStreamWarps;
-      if (i >= kOFree && i < kItemFull) arrivals = 2 * kStreamWarps + 1;
-      if ((i >= kKEmpty && i < kVFull) || (i >= kVEmpty && i < kQFull) || i == kQEmpty || i == kQEmpty + 1) arrivals = 2;
-      if (i >= kItemFree && i < kDrain) arrivals = kItemUsers;
-      if (i >= kJoin) arrivals = 4;
-      mbar_init(&bars[i], arrivals);
-    }
-    fence_mbar_init();
-  }
+  if (threadIdx.x == 0) tree_init_barriers<L>(bars);
   if (threadIdx.x < 8) reinterpret_cast<uint32_t*>(gbase + L::kGaveUp)[threadIdx.x] = 0;
   // a Q tile's rows past its G * tile_tokens: no copy writes them, they stay zero
-  for (int i = pl.group * p.tile_tokens * 8 + (int)threadIdx.x; i < kTcRows * 8; i += kThreads)
+  for (int i = pl.group * p.tile_tokens * 8 + (int)threadIdx.x; i < kTcRows * 8; i += kTreeThreads)
     for (int t = 0; t < 2 * H; ++t) st_shared_v4(base + L::kQ + t * kHalf + i * 16, make_uint4(0u, 0u, 0u, 0u));
   fence_proxy_async_smem();
   if (warp == kMmaWarp) tmem_alloc(base + L::kBar + kTmemSlot, kTmemCols);
@@ -209,170 +148,9 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(const __grid_const
   // registers: 512 x 104 + 128 x 56 = 60416 of the 61440 that 640 threads start with
   if (warp >= kKvWarp) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
   if (warp == kKvWarp) {
-    // ------------------------------------------------------- K and V copies
-    // Lane s copies segment s of a tile; K runs kAhead tiles ahead of V.  A V
-    // tile with rows that are not read lands on a barrier of its own (kVCut)
-    // and is released with those rows zeroed, so that they never weigh in.
-    constexpr int kAhead = kKStages - 2;
-    const uint32_t box = (uint32_t)p.seg_rows * 128u;
-    const int nseg = kTcKeys / p.seg_rows;
-    const uint32_t whole = (1u << nseg) - 1u;  // at most 16 segments
-    if (lane == 0) {
-      asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&p.tmap_k)) : "memory");
-      asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&p.tmap_v)) : "memory");
-    }
-    constexpr int kNone = INT_MIN;             // a segment of rows that are not read: nothing to load
-    bool ok = true;
-    int kstg = 0, vstg = 0, landed = 0;        // next stages; phases of kVCut
-    uint32_t kpar = 1, vpar = 1;               // parities of their release (nothing to wait for in the first round)
-    auto wait = [&](int bar, uint32_t parity) {
-      if (ok) ok = __all_sync(FULL_MASK, wait_bounded(&bars[bar], parity));
-    };
-    // one operand of a tile into a stage, whose block id is b in lane s
-    auto copy = [&](const CUtensorMap* map, uint32_t dst, int bar, int ks, int hk, int b) {
-      const bool good = (uint32_t)b < p.block_limit;
-      const uint32_t loaded = __ballot_sync(FULL_MASK, good);
-      uint32_t bytes = H * kHalf;
-      dst += lane * box;
-      if (loaded != whole) {
-        bytes = (uint32_t)__popc(loaded) * box * H;
-        const uint32_t bad = __ballot_sync(FULL_MASK, b != kNone && !good);
-        if (bad) {                             // a bad block id reads as zeros
-          if (lane == 0) flag_error(p.err, PKVD_ERR_BLOCK_ID);
-          if ((bad >> lane) & 1u) {
-            for (int h = 0; h < H; ++h)
-              for (uint32_t o = 0; o < box; o += 16) st_shared_v4(dst + h * kHalf + o, make_uint4(0u, 0u, 0u, 0u));
-            fence_proxy_async_smem();
-          }
-          __syncwarp();
-        }
-      }
-      if (lane == 0) mbar_arrive_expect_tx(&bars[bar], bytes);
-      __syncwarp();
-      if (good) {
-#pragma unroll
-        for (int h = 0; h < H; ++h) tma_load4(dst + h * kHalf, map, h * 64, hk, ks & (p.block_size - 1), b, &bars[bar]);
-      }
-    };
-    for (int r = 0; ok; ++r) {
-      ok = __all_sync(FULL_MASK, wait_item(&bars[kItemFull + r % kItemRing], (r / kItemRing) & 1));
-      if (!ok) break;
-      const Item& cur = ring_items[r % kItemRing];
-      if (cur.n < 0) break;
-      const int32_t* table = p.tables + (int64_t)cur.seq * p.max_blocks;
-      const int n = cur.n, hk = cur.hk, lo = cur.lo, hi = cur.hi, kt_last = cur.kt_last;
-      auto key_of = [&](int t) { return (kt_last - t) * kTcKeys + lane * p.seg_rows; };
-      auto fetch = [&](int t) -> int {
-        const int ks = key_of(t);
-        if (t >= n || lane >= nseg || ks > hi || ks + p.seg_rows - 1 < lo) return kNone;
-        return __ldg(table + (ks >> p.block_shift));
-      };
-      auto copy_k = [&](int t, int b) {
-        wait(kKEmpty + kstg, kpar);
-        if (!ok) return;
-        copy(&p.tmap_k, base + L::kK + kstg * H * kHalf, kKFull + kstg, key_of(t), hk, b);
-        if (++kstg == kKStages) kstg = 0, kpar ^= 1;
-      };
-      int b[4];                                // block ids of V tile t and the three after it
-#pragma unroll
-      for (int i = 0; i < 4; ++i) b[i] = fetch(i);
-#pragma unroll
-      for (int i = 0; i < kAhead; ++i)
-        if (i < n) copy_k(i, b[i]);
-      for (int t = 0; ok && t < n; ++t) {
-        if (t + kAhead < n) copy_k(t + kAhead, b[kAhead]);
-        wait(kVEmpty + vstg, vpar);
-        if (!ok) break;
-        const int kbase = (kt_last - t) * kTcKeys;
-        const bool cut = kbase < lo || kbase + kTcKeys - 1 > hi;
-        const uint32_t dst = base + L::kV + vstg * H * kHalf;
-        copy(&p.tmap_v, dst, (cut ? kVCut : kVFull) + vstg, kbase + lane * p.seg_rows, hk, b[0]);
-        if (cut) {
-          wait(kVCut + vstg, (landed >> vstg) & 1);
-          landed ^= 1 << vstg;
-          if (!ok) break;
-          for (int rr = lane; rr < kTcKeys; rr += 32) {
-            const int kp = kbase + rr;
-            if (kp >= lo && kp <= hi) continue;
-            for (int h = 0; h < H; ++h)
-              for (int c = 0; c < 8; ++c) st_shared_v4(dst + h * kHalf + rr * 128 + c * 16, make_uint4(0u, 0u, 0u, 0u));
-          }
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&bars[kVFull + vstg]);
-        }
-        if (++vstg == kVStages) vstg = 0, vpar ^= 1;
-        b[0] = b[1];
-        b[1] = b[2];
-        b[2] = b[3];
-        b[3] = fetch(t + 4);
-      }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&bars[kItemFree + r % kItemRing]);
-    }
-    if (!ok && lane == 0) {
-      // gave up: let the copies still in flight land before the CTA leaves
-      flag_error(p.err, PKVD_ERR_TIMEOUT);
-      // (a stage's full barrier is behind its release, or one phase ahead of it)
-      for (int u = 0; u < kKStages; ++u) wait_bounded(&bars[kKFull + u], (kpar ^ (u < kstg ? 0u : 1u)) ^ 1u);
-      for (int u = 0; u < kVStages; ++u) wait_bounded(&bars[kVFull + u], (vpar ^ (u < vstg ? 0u : 1u)) ^ 1u);
-    }
+    tree_copy_kv<L>(p, bars, base, ring_items, lane);
   } else if (warp == kQWarp) {
-    // ------------------------------------------------------- segments and Q
-    // A Q tile's rows are one box per 64 columns (G heads of tile_tokens nodes).
-    // Two tiles of a unit fill both buffers; single ones take them in turn, so
-    // the next is loaded while the last is in use.
-    const int64_t total = pl.starts[pl.num_seqs], slices = tree_slices(pl, total);
-    TreeWalk walk;
-    walk.at = walk.end = 0;
-    if ((int64_t)blockIdx.x < slices) walk.start(pl, blockIdx.x, total, slices);
-    if (lane == 0) {
-      asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&p.tmap_q)) : "memory");
-      bool ok = true;
-      int used[2] = {0, 0}, turn = 0;
-      for (int r = 0; ok; ++r) {
-        const int slot = r % kItemRing;
-        if (r >= kItemRing) ok = wait_item(&bars[kItemFree + slot], ((r / kItemRing) - 1) & 1);
-        if (!ok) break;
-        Item it;
-        TreeSegment g;
-        it.n = -1;
-        if (walk.next(pl, g)) {
-          const int tb = g.unit * pl.unit_tokens;
-          it.seq = g.seq;
-          it.hk = g.head;
-          it.q0 = walk.s.q0 + tb;
-          it.tokens = min(pl.unit_tokens, walk.s.n - tb);
-          it.node0 = g.seq * pl.max_q + tb;
-          it.cached = walk.s.cached;
-          it.lo = walk.s.lo;
-          it.hi = walk.s.klen - 1;
-          it.kt_last = walk.s.lo_tile + g.t1 - 1;
-          it.n = g.t1 - g.t0;
-          it.slot = g.slot;
-          it.two = it.tokens > p.tile_tokens;
-          it.qbuf = turn;
-          if (!it.two) turn ^= 1;
-        }
-        ring_items[slot] = it;
-        mbar_arrive(&bars[kItemFull + slot]);
-        if (it.n < 0) break;
-#pragma unroll
-        for (int g2 = 0; g2 < 2; ++g2) {
-          if (!ok || !(it.two || it.qbuf == g2)) continue;
-          if (used[g2] > 0) ok = wait_item(&bars[kQEmpty + g2], (used[g2] - 1) & 1);
-          if (!ok) continue;
-          mbar_arrive_expect_tx(&bars[kQFull + g2], p.q_box * H);
-          for (int h = 0; h < H; ++h)
-            tma_load3(base + L::kQ + (g2 * H + h) * kHalf, &p.tmap_q, h * 64, it.hk * pl.group,
-                      it.q0 + (it.two ? g2 * p.tile_tokens : 0), &bars[kQFull + g2]);
-          ++used[g2];
-        }
-      }
-      if (!ok) flag_error(p.err, PKVD_ERR_TIMEOUT);
-      for (int g2 = 0; g2 < 2; ++g2)             // no copy is in flight when the CTA leaves
-        if (used[g2] > 0) wait_bounded(&bars[kQFull + g2], (used[g2] - 1) & 1);
-    }
+    tree_segments<L>(p, bars, base, ring_items, lane);
   } else if (warp == kMmaWarp || warp == kMmaWarp1) {
     // ---------------------------------------------------------------- MMA
     // S(n) of the stream, n counting all its K tiles: Q and K have landed and
@@ -806,7 +584,7 @@ cudaError_t launch_mode(const TcTree& prm, cudaStream_t stream) {
   constexpr int smem = Layout<D>::kBytes;
   cudaError_t e = cudaFuncSetAttribute(tree_tc_kernel<T, D, MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  return launch_pdl(tree_tc_kernel<T, D, MODE>, dim3((unsigned)prm.plan.grid), dim3(kThreads), smem, stream, prm);
+  return launch_pdl(tree_tc_kernel<T, D, MODE>, dim3((unsigned)prm.plan.grid), dim3(kTreeThreads), smem, stream, prm);
 }
 
 template <typename T, int D>
@@ -833,31 +611,12 @@ bool tree_tc_supported(const TreeArgs& a) {
 }
 
 cudaError_t launch_tree_tc(const TreeArgs& a, const TreePlan& plan, cudaStream_t stream) {
-  const pkvd_cache& c = a.cache;
   TcTree prm;
-  prm.plan = plan;
-  prm.seg_rows = c.block_size < kTcKeys ? c.block_size : kTcKeys;
-  prm.tile_tokens = kTcRows / plan.group;
-  if (!encode_cache_map(&prm.tmap_k, c.k_base, c, prm.seg_rows) ||
-      !encode_cache_map(&prm.tmap_v, c.v_base, c, prm.seg_rows) ||
-      !encode_q_map(&prm.tmap_q, a.q, c.dtype, c.head_dim, a.num_q_heads, a.total_q, plan.group, prm.tile_tokens))
-    return cudaErrorInvalidValue;
-  prm.out = a.out;
-  prm.tables = a.block_tables;
-  prm.max_blocks = a.max_blocks_per_seq;
-  prm.block_limit = (uint32_t)(c.num_blocks < 0x80000000ll ? c.num_blocks : 0x80000000ll);
-  prm.block_size = c.block_size;
-  prm.block_shift = 0;
-  while ((1 << prm.block_shift) < c.block_size) ++prm.block_shift;
-  prm.q_box = 128u * (uint32_t)(plan.group * prm.tile_tokens);
-  prm.scale_log2 = a.scale * 1.4426950408889634f;
-  prm.mod = a.mod;
-  prm.poly_range = cap_poly(a.mod, prm.poly);
-  prm.wide_out = reinterpret_cast<uintptr_t>(a.out) % 32 == 0;
-  prm.err = a.err;
-  if (c.dtype == PKVD_BF16)
-    return c.head_dim == 64 ? launch_typed<__nv_bfloat16, 64>(prm, stream) : launch_typed<__nv_bfloat16, 128>(prm, stream);
-  return c.head_dim == 64 ? launch_typed<__half, 64>(prm, stream) : launch_typed<__half, 128>(prm, stream);
+  if (!tree_tc_params(a, plan, kTcRows / plan.group, &prm)) return cudaErrorInvalidValue;
+  const bool wide = a.cache.head_dim == 128;
+  if (a.cache.dtype == PKVD_BF16)
+    return wide ? launch_typed<__nv_bfloat16, 128>(prm, stream) : launch_typed<__nv_bfloat16, 64>(prm, stream);
+  return wide ? launch_typed<__half, 128>(prm, stream) : launch_typed<__half, 64>(prm, stream);
 }
 
 }  // namespace pkvd
