@@ -2,23 +2,22 @@
 //
 // Row (sequence i, head h) of `weights` holds what each cached position was
 // given so far.  With c = context_lens[i] > keep the first `sink` and the last
-// `recent` positions stay, and of the others the heaviest, keep in all; the
+// `recent` positions stay, and of those between the heaviest, keep in all; the
 // lowest position first among equal weights.  Positions come out in ascending
 // order, the weights that stay close up beside them, zeros behind.
 //
-// A CTA a row.  Its weights are read once (rows up to 32,768: half in
-// registers, half in shared memory; a longer one again for each pass, 32,768
-// at a time) and looked at four times: the keep-th weight by radix selection
-// over order-preserving whole numbers (11, 11 and 10 bits, a histogram in
-// shared memory each, four copies of it so that lanes with equal digits do not
-// all wait for one another), then what stays is written in order.  Every warp
-// has a contiguous part of the row, so the order needs two prefix sums over
-// warps and ballots within one, no barrier an element.  Exact: whole-number
-// arithmetic on the weights' bits.
+// A CTA a row, two on an SM.  The weights between are read once (24,576 of them;
+// more of them again for each pass, as many at a time) into shared memory as
+// whole numbers in the order of the numbers, and looked at five times: a radix
+// selection of the last one that stays (11, 11 and 10 bits, a histogram each, two
+// copies of it so that lanes with equal digits wait less for one another), a
+// count and the writing, in order.  Every warp has a contiguous part of the row,
+// so the order needs prefix sums over warps once and ballots within one, no
+// barrier an element.  Exact: whole-number arithmetic on the weights' bits.
 //
-// Bound by bytes and, beside them, by the passes' instructions: with 1024
-// threads a row, weights read again for every pass and one histogram, 64 rows
-// of 8 heads of 4,096 to 32,768 weights took 135 us.
+// The loops are short code on purpose: a form with half of the weights in
+// registers, its passes written out, took 14 us for a row of 50 (and 70 us for 64
+// x 8 rows of 4,096 to 32,768): it waited for instructions.
 #include "common.cuh"
 #include "launch.h"
 
@@ -26,129 +25,152 @@ namespace pkvd {
 
 namespace {
 
-constexpr int kThreads = 512, kWarps = kThreads / 32;
-constexpr int kInRegs = 32, kInSmem = 32;                  // weights of a thread
-constexpr int kSpan = (kInRegs + kInSmem) * kThreads;      // positions of a round
-constexpr int kBins = 2048, kCopies = 4;
-constexpr int kSmemBytes = kInSmem * kThreads * 4 + kBins * kCopies * 4;
+constexpr int kBins = 2048, kCopies = 2;
+template <int THREADS>
+struct Size {
+  static constexpr int kWarps = THREADS / 32;
+  static constexpr int kSpan = 48 * THREADS;                       // positions of a round
+  static constexpr int kStack = kBins * kCopies / kWarps / 2;      // positions and weights that a warp gathers
+  static constexpr int kSmemBytes = kSpan * 4 + kBins * kCopies * 4;
+};
 
-// Keys in the order of the numbers: -0 as 0, NaN above all.  `special`: the row
-// has a -0 or a NaN.
-__device__ __forceinline__ uint32_t key_of(uint32_t u, bool special) {
-  const uint32_t k = u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
-  if (special) {
-    if (u == 0x80000000u) return 0x80000000u;
-    if ((u & 0x7fffffffu) > 0x7f800000u) return 0xffffffffu;
+// A weight's bits in the order of the numbers, and back.  Any NaN becomes the quiet
+// one, above all numbers; 0 is left for no weight.
+__device__ __forceinline__ uint32_t ordered_bits(uint32_t u) {
+  if ((u & 0x7fffffffu) > 0x7f800000u) u = 0x7fc00000u;
+  return u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
+}
+__device__ __forceinline__ uint32_t number_bits(uint32_t k) { return k ^ (~(uint32_t)((int32_t)k >> 31) | 0x80000000u); }
+// What is compared: -0 and 0, next to each other, as one.
+__device__ __forceinline__ uint32_t key_of(uint32_t k) { return k - (k >> 31); }
+
+struct Row {
+  const float* w;
+  float* wo;
+  int32_t* out;
+  int lo, hi, left;                    // [lo, hi) compete for `left` places behind the first lo
+};
+
+// This warp's part of a round: positions [first, n), 32 at a time.
+template <int kThreads>
+struct Part {
+  static constexpr int kWarps = Size<kThreads>::kWarps, kSpan = Size<kThreads>::kSpan;
+  int first, n, steps;                 // steps: a multiple of four
+  __device__ Part(const Row& row, int r, int warp) {
+    const int base = row.lo + r * kSpan, span = min(row.hi - base, kSpan);
+    const int seg = ((span + kWarps - 1) / kWarps + 31) / 32 * 32;
+    first = base + min(warp * seg, span);
+    n = base + min(warp * seg + seg, span);
+    steps = ((n - first + 31) / 32 + 3) / 4 * 4;
   }
-  return k;
+};
+
+// The weights of a round, 0 where there is none: step i's at held[i * kThreads],
+// each thread's its own.
+template <int kThreads>
+__device__ __forceinline__ void fetch(const Row& row, const Part<kThreads>& part, uint32_t* held, int lane) {
+  const float* src = row.w + part.first + lane;
+  const int mine = part.n - part.first - lane;             // positions from this lane's first to the end
+#pragma unroll 4
+  for (int i = 0; i < part.steps; ++i) {
+    if (i * 32 < mine)
+      asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(held + i * kThreads)), "l"(src + i * 32)
+                   : "memory");
+  }
+  asm volatile("cp.async.commit_group;\n\tcp.async.wait_group 0;" ::: "memory");
+#pragma unroll 4
+  for (int i = 0; i < part.steps; ++i) held[i * kThreads] = i * 32 < mine ? ordered_bits(held[i * kThreads]) : 0u;
 }
 
-__global__ void __launch_bounds__(kThreads, 2) evict_select_kernel(const EvictArgs a) {
+template <int kThreads>
+__global__ void __launch_bounds__(kThreads, 1024 / kThreads) evict_select_kernel(const EvictArgs a) {
+  constexpr int kWarps = Size<kThreads>::kWarps, kSpan = Size<kThreads>::kSpan, kStack = Size<kThreads>::kStack;
   extern __shared__ __align__(16) uint32_t sm[];
-  uint32_t* held = sm;                                     // [kInSmem][kThreads]
-  uint32_t* hist = sm + kInSmem * kThreads;                // [kBins][kCopies]
   __shared__ int warp_sum[2][kWarps];
   __shared__ uint32_t found_digit;
   __shared__ int found_left;
+  uint32_t* const hist = sm;                               // [kBins][kCopies]
   pdl_wait();          // (and no early trigger: counts are the next call's lengths, which it reads before it waits)
   const int h = blockIdx.x, seq = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  uint32_t* const held = sm + kBins * kCopies + tid;
   int c = a.context_lens[seq];
   if (c < 0 || c > a.length) {
     if (tid == 0 && h == 0) flag_error(a.err, PKVD_ERR_CONTEXT);
     c = min(max(c, 0), a.length);
   }
-  const float* w = a.weights + (int64_t)seq * a.seq_stride + (int64_t)h * a.head_stride;
-  float* wo = a.weights_out ? a.weights_out + (int64_t)seq * a.seq_stride + (int64_t)h * a.head_stride : nullptr;
-  int32_t* out = a.positions + ((int64_t)seq * gridDim.x + h) * a.keep;
+  Row row;
+  row.w = a.weights + (int64_t)seq * a.seq_stride + (int64_t)h * a.head_stride;
+  row.wo = a.weights_out ? a.weights_out + (int64_t)seq * a.seq_stride + (int64_t)h * a.head_stride : nullptr;
+  row.out = a.positions + ((int64_t)seq * gridDim.x + h) * a.keep;
   const int count = min(c, a.keep);
   if (h == 0 && tid == 0) {
     a.counts[seq] = count;
     __threadfence();
   }
-  // what competes: positions [lo, hi) for `left` places
-  const bool all = c <= a.keep;
-  const int lo = all ? 0 : a.sink, hi = all ? 0 : c - a.recent;
-  int left = all ? 0 : a.keep - a.sink - a.recent;
-
-  // A round: positions [base, base + span), every warp `seg` of them, 32 at a time.
-  const int rounds = (c + kSpan - 1) / kSpan;
-  uint32_t reg[kInRegs];
-  int first = 0, n = 0, steps = 0;                         // this warp's part: position of lane 0's first, end, steps
-  auto place = [&](int r) {
-    const int base = r * kSpan, span = min(c - base, kSpan);
-    const int seg = ((span + kWarps - 1) / kWarps + 31) / 32 * 32;
-    first = base + min(warp * seg, span);
-    n = base + min(warp * seg + seg, span);
-    steps = (n - first + 31) / 32;
-  };
-  auto fetch = [&](int r) {
-    place(r);
-    bool odd = false;
-    const float* src = w + first + lane;
-    const int mine = n - first - lane;                     // positions from this lane's first to the end
-#pragma unroll
-    for (int i = 0; i < kInRegs; ++i) {
-      reg[i] = i * 32 < mine ? __float_as_uint(src[i * 32]) : 0u;
+  // behind what stays; in place only when everything has been read
+  auto behind = [&] {
+    if (!row.wo) return;
+    int r = count;
+    if ((reinterpret_cast<uintptr_t>(row.wo) & 15u) == 0) {      // whole 16 bytes from the next boundary on
+      const int from = min((count + 3) / 4 * 4, a.length), to = a.length / 4 * 4;
+      if (count + tid < from) row.wo[count + tid] = 0.f;
+#pragma unroll 1
+      for (int i = from + 4 * tid; i < to; i += 4 * kThreads) *reinterpret_cast<float4*>(row.wo + i) = make_float4(0.f, 0.f, 0.f, 0.f);
+      r = max(from, to);
     }
-    for (int i = kInRegs; i < steps; i += 8) {
-      uint32_t x[8];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) x[e] = (i + e) * 32 < mine ? __float_as_uint(src[(i + e) * 32]) : 0u;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        if (i + e < steps) held[(i + e - kInRegs) * kThreads + tid] = x[e];
-        odd |= x[e] == 0x80000000u || (x[e] & 0x7fffffffu) > 0x7f800000u;
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < kInRegs; ++i) odd |= reg[i] == 0x80000000u || (reg[i] & 0x7fffffffu) > 0x7f800000u;
-    return odd;
+#pragma unroll 1
+    for (int i = r + tid; i < a.length; i += kThreads) row.wo[i] = 0.f;
   };
-  // f(position, bits, there) for this thread's places in order; every lane of the warp comes along
-  auto each = [&](auto f) {
-    if (steps >= kInRegs) {
-#pragma unroll
-      for (int i = 0; i < kInRegs; ++i) f(first + i * 32 + lane, reg[i], first + i * 32 + lane < n);
-      for (int i = kInRegs; i < steps; ++i)
-        f(first + i * 32 + lane, held[(i - kInRegs) * kThreads + tid], first + i * 32 + lane < n);
-    } else {
-#pragma unroll
-      for (int i = 0; i < kInRegs; ++i) {
-        if (i >= steps) break;
-        f(first + i * 32 + lane, reg[i], first + i * 32 + lane < n);
-      }
-    }
-  };
-
-  bool special = false;
-  uint32_t kth = 0xffffffffu;          // the key of the last one that stays, `left` of those equal to it do
-  for (int r = 0; r < rounds; ++r) special |= fetch(r);    // (one round: kept from here on)
-  special = __syncthreads_or(special);
-  if (left > 0) {
-    uint32_t prefix = 0, mask = 0;
-    for (int shift = 21; shift >= 0; shift = shift == 21 ? 10 : shift == 10 ? 0 : -1) {
-      const uint32_t digits = shift == 0 ? 1023u : 2047u;
+  // the first ones stay where they are (all of a row that is short enough)
+  const int sink = c > a.keep ? a.sink : c, recent = c > a.keep ? a.recent : 0;
+  row.lo = sink;
+  row.hi = c - recent;
+  row.left = count - sink - recent;
+  const int rounds = row.left > 0 ? (row.hi - row.lo + kSpan - 1) / kSpan : 0;
+  if (rounds == 1) fetch(row, Part<kThreads>(row, 0, warp), held, lane);
+  if (row.wo != row.w) behind();
+#pragma unroll 1
+  for (int j = count + tid; j < a.keep; j += kThreads) row.out[j] = -1;
+#pragma unroll 1
+  for (int j = tid; j < sink; j += kThreads) {
+    row.out[j] = j;
+    if (row.wo && row.wo != row.w) row.wo[j] = row.w[j];
+  }
+  if (rounds > 0) {
+    int left = row.left;
+    uint32_t kth = 0;                  // the last key that stays, so far its upper bits
+#pragma unroll 1
+    for (int pass = 0; pass < 3; ++pass) {
+      const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, above = pass == 0 ? 31 : pass == 1 ? 21 : 10;
+      const uint32_t digits = pass == 2 ? 1023u : 2047u;
       for (int i = tid; i < kBins * kCopies / 4; i += kThreads) reinterpret_cast<uint4*>(hist)[i] = make_uint4(0, 0, 0, 0);
       __syncthreads();
+      uint32_t* const bins = hist + (lane & (kCopies - 1));
+#pragma unroll 1
       for (int r = 0; r < rounds; ++r) {
-        if (rounds > 1) fetch(r);
-        each([&](int j, uint32_t u, bool there) {
-          const uint32_t k = key_of(u, special);
-          if (there && j >= lo && j < hi && (k & mask) == prefix)
-            atomicAdd(&hist[((k >> shift) & digits) * kCopies + (lane & (kCopies - 1))], 1u);
-        });
+        const Part<kThreads> part(row, r, warp);
+        if (rounds > 1) fetch(row, part, held, lane);
+        // (no weight: key 0, the lowest digit, below every one that is looked for; it
+        // counts nowhere, so that rows of few do not pile up there)
+#pragma unroll 4
+        for (int i = 0; i < part.steps; ++i) {
+          const uint32_t k = key_of(held[i * kThreads]);
+          if (k != 0u && (pass == 0 || k >> above == kth >> above)) atomicAdd(bins + ((k >> shift) & digits) * kCopies, 1u);
+        }
       }
       __syncthreads();
-      // from the largest digit down: thread t has the kPer bins below kBins - kPer t
-      constexpr int kPer = kBins / kThreads;
-      int bin[kPer], mine = 0;
+      // from the largest digit down: thread t has the kEach bins below kBins - kEach t
+      constexpr int kEach = kBins / kThreads;
+      int bin[kEach], sum = 0;
+      const uint4* mine = reinterpret_cast<const uint4*>(hist) + (kBins / kEach - 1 - tid) * (kEach * kCopies / 4);
 #pragma unroll
-      for (int i = 0; i < kPer; ++i) {
-        const uint4 x = reinterpret_cast<const uint4*>(hist)[kBins - 1 - (tid * kPer + i)];
-        bin[i] = (int)(x.x + x.y + x.z + x.w);
-        mine += bin[i];
+      for (int i = 0; i < kEach / 2; ++i) {                // (two bins of two copies each)
+        const uint4 x = mine[kEach / 2 - 1 - i];
+        bin[2 * i] = (int)(x.z + x.w);
+        bin[2 * i + 1] = (int)(x.x + x.y);
+        sum += (int)(x.x + x.y + x.z + x.w);
       }
-      int upto = mine;
+      int upto = sum;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const int t = __shfl_up_sync(FULL_MASK, upto, o);
@@ -156,91 +178,119 @@ __global__ void __launch_bounds__(kThreads, 2) evict_select_kernel(const EvictAr
       }
       if (lane == 31) warp_sum[0][warp] = upto;
       __syncthreads();
-      int before = upto - mine;
+      // the warps before: a lane each
+      int before = lane < warp ? warp_sum[0][lane % kWarps] : 0;
+      before = __reduce_add_sync(FULL_MASK, before) + upto - sum;
+      if (before < left && left <= before + sum) {
 #pragma unroll
-      for (int v = 0; v < kWarps; ++v) before += v < warp ? warp_sum[0][v] : 0;
-      if (before < left && left <= before + mine) {
-#pragma unroll
-        for (int i = 0; i < kPer; ++i) {
+        for (int i = 0; i < kEach; ++i) {
           if (before < left && left <= before + bin[i]) {
-            found_digit = kBins - 1 - (tid * kPer + i);
+            found_digit = kBins - 1 - (tid * kEach + i);
             found_left = left - before;
           }
           before += bin[i];
         }
       }
       __syncthreads();
-      prefix |= found_digit << shift;
-      mask |= digits << shift;
+      kth |= found_digit << shift;
       left = found_left;
     }
-    kth = prefix;
-  }
-  // in order: what stays, and of those equal to the last one the first `left`
-  int kept = 0, ties = 0;              // of the rounds before
-  for (int r = 0; r < rounds; ++r) {
-    if (rounds > 1) fetch(r);
-    int more = 0, tie = 0;             // of this thread, then of the warps before
-    auto stays = [&](int j, uint32_t u, bool there, bool& m, bool& t) {
-      const bool inside = j >= lo && j < hi;
-      const uint32_t k = key_of(u, special);
-      m = there && (!inside || (left > 0 && k > kth));
-      t = there && inside && left > 0 && k == kth;
-    };
-    each([&](int j, uint32_t u, bool there) {
-      bool m, t;
-      stays(j, u, there, m, t);
-      more += m;
-      tie += t;
-    });
-    more = __reduce_add_sync(FULL_MASK, more);
-    tie = __reduce_add_sync(FULL_MASK, tie);
-    if (lane == 0) warp_sum[0][warp] = more, warp_sum[1][warp] = tie;
-    __syncthreads();                   // (and every weight of the round is read: in place it may be overwritten)
-    int m_before = 0, t_before = ties, m_all = 0, t_all = ties;
-#pragma unroll
-    for (int v = 0; v < kWarps; ++v) {
-      const int m = warp_sum[0][v], t = warp_sum[1][v];
-      if (v < warp) m_before += m, t_before += t;
-      m_all += m;
-      t_all += t;
-    }
-    // the place of this warp's next one: those before it, ties as far as there are places for them
-    int at = kept + m_before + min(t_before, left) - min(ties, left);
-    int rank = t_before;
-    if (more > 0 || (tie > 0 && rank < left)) {
+    // in order: what is larger, and of those equal to the last one the first `left`
+    int kept = row.lo, ties = 0;       // of the rounds before
+#pragma unroll 1
+    for (int r = 0; r < rounds; ++r) {
+      const Part<kThreads> part(row, r, warp);
+      if (rounds > 1) fetch(row, part, held, lane);
+      int more = 0, tie = 0;           // of this thread, then of the warp
+#pragma unroll 4
+      for (int i = 0; i < part.steps; ++i) {
+        const uint32_t k = key_of(held[i * kThreads]);
+        more += k > kth;
+        tie += k == kth;
+      }
+      more = __reduce_add_sync(FULL_MASK, more);
+      tie = __reduce_add_sync(FULL_MASK, tie);
+      if (lane == 0) warp_sum[0][warp] = more, warp_sum[1][warp] = tie;
+      __syncthreads();                 // (and every weight of the round is read: in place it may be overwritten)
+      const int m = lane < kWarps ? warp_sum[0][lane % kWarps] : 0, t = lane < kWarps ? warp_sum[1][lane % kWarps] : 0;
+      const int m_before = __reduce_add_sync(FULL_MASK, lane < warp ? m : 0), m_all = __reduce_add_sync(FULL_MASK, m);
+      const int t_before = ties + __reduce_add_sync(FULL_MASK, lane < warp ? t : 0), t_all = ties + __reduce_add_sync(FULL_MASK, t);
+      // the place of this warp's next one: those before it, ties as far as there are places for them
+      int at = kept + m_before + min(t_before, left) - min(ties, left), rank = t_before;
       const uint32_t below = (1u << lane) - 1u;
-      each([&](int j, uint32_t u, bool there) {
-        bool m, t;
-        stays(j, u, there, m, t);
-        const uint32_t tb = __ballot_sync(FULL_MASK, t);
-        const bool stay = m || (t && rank + __popc(tb & below) < left);
-        const uint32_t sb = __ballot_sync(FULL_MASK, stay);
-        if (stay) {
-          const int to = at + __popc(sb & below);
-          out[to] = j;
-          if (wo) wo[to] = __uint_as_float(u);             // to <= j: not of a later round
+      // what stays is gathered in the warp's part of the histogram's memory, so that
+      // it leaves 32 side by side
+      uint32_t* const stack = hist + warp * (2 * kStack);
+      int fill = 0;
+      if (more > 0 || (tie > 0 && rank < left)) {
+#pragma unroll 1
+        for (int i = 0; i < part.steps; ++i) {
+          const uint32_t number = held[i * kThreads], k = key_of(number);
+          bool stay = k >= kth;
+          uint32_t sb = __ballot_sync(FULL_MASK, stay);
+          if (sb != 0u) {
+            const uint32_t tb = __ballot_sync(FULL_MASK, k == kth);
+            if (tb) {
+              stay = k > kth || (k == kth && rank + __popc(tb & below) < left);
+              sb = __ballot_sync(FULL_MASK, stay);
+              rank += __popc(tb);
+            }
+            if (stay) {
+              const int to = fill + __popc(sb & below);
+              stack[to] = (uint32_t)(part.first + i * 32 + lane);
+              stack[kStack + to] = number_bits(number);
+            }
+            fill += __popc(sb);
+          }
+          if (fill > kStack - 32 || i == part.steps - 1) {
+            __syncwarp();
+#pragma unroll 1
+            for (int e = lane; e < fill; e += 32) {
+              row.out[at + e] = (int)stack[e];
+              if (row.wo) row.wo[at + e] = __uint_as_float(stack[kStack + e]);   // to <= the position: not of a later round
+            }
+            __syncwarp();
+            at += fill;
+            fill = 0;
+          }
         }
-        at += __popc(sb);
-        rank += __popc(tb);
-      });
+      }
+      kept += m_all + min(t_all, left) - min(ties, left);
+      ties = t_all;
+      __syncthreads();
     }
-    kept += m_all + min(t_all, left) - min(ties, left);
-    ties = t_all;
-    __syncthreads();
   }
-  for (int r = count + tid; r < a.keep; r += kThreads) out[r] = -1;
-  if (wo)
-    for (int r = count + tid; r < a.length; r += kThreads) wo[r] = 0.f;
+  // the last ones: to <= from, a stretch read before it is written
+  const int to = count - recent;
+#pragma unroll 1
+  for (int base = 0; base < recent; base += kThreads) {
+    const int i = base + tid;
+    const float x = i < recent && row.wo ? row.w[row.hi + i] : 0.f;
+    __syncthreads();
+    if (i < recent) {
+      row.out[to + i] = row.hi + i;
+      if (row.wo) row.wo[to + i] = x;
+    }
+  }
+  if (row.wo == row.w) {
+    __syncthreads();
+    behind();
+  }
+}
+
+template <int kThreads>
+cudaError_t launch(const EvictArgs& a, int num_seqs, int heads, cudaStream_t stream) {
+  constexpr int smem = Size<kThreads>::kSmemBytes;
+  cudaError_t e = cudaFuncSetAttribute(evict_select_kernel<kThreads>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(evict_select_kernel<kThreads>, dim3(heads, num_seqs), dim3(kThreads), smem, stream, a);
 }
 
 }  // namespace
 
 cudaError_t launch_evict_select(const EvictArgs& a, int num_seqs, int heads, cudaStream_t stream) {
   if (num_seqs == 0 || heads == 0) return cudaSuccess;
-  cudaError_t e = cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
-  if (e != cudaSuccess) return e;
-  return launch_pdl(evict_select_kernel, dim3(heads, num_seqs), dim3(kThreads), kSmemBytes, stream, a);
+  return a.length > Size<512>::kSpan ? launch<1024>(a, num_seqs, heads, stream) : launch<512>(a, num_seqs, heads, stream);
 }
 
 }  // namespace pkvd

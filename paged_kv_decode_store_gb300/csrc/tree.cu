@@ -64,18 +64,28 @@ __global__ void __launch_bounds__(kPlanThreads) tree_plan_kernel(const TreePlan 
       __syncthreads();
     }
     if (tid == 0) p.starts[p.num_seqs] = running;
-    // where the slices begin: the last sequence with no more pieces before it
+    // where the slices begin: in the last sequence with no more pieces before it
     const int64_t* starts = p.num_seqs <= kNearSeqs ? near : p.starts;
     const int64_t slices = tree_slices(p, running);
-    for (int c = tid; c < slices; c += kPlanThreads) {
-      const int64_t f = tree_slice_begin(running, slices, c);
+    for (int c = tid; c < p.grid; c += kPlanThreads) {
+      const bool any = c < slices;
+      const int64_t f = any ? tree_slice_begin(running, slices, c) : 0;
       int lo = 0, hi = p.num_seqs;
       while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
         if (starts[mid] <= f) lo = mid;
         else hi = mid;
       }
-      p.slice_seq[c] = lo;
+      TreeStart s;
+      s.at = f;
+      s.end = any ? tree_slice_begin(running, slices, c + 1) : 0;
+      s.in = any ? f - starts[lo] : 0;
+      s.seq = lo;
+      s.q0 = p.cu_q[lo];
+      s.n = p.cu_q[lo + 1] - s.q0;
+      s.klen = p.cu_k[lo + 1] - p.cu_k[lo];
+      s.pad[0] = s.pad[1] = 0;
+      p.slice[c] = s;
     }
     return;
   }
@@ -97,8 +107,12 @@ __global__ void __launch_bounds__(kPlanThreads) tree_plan_kernel(const TreePlan 
     for (int u = tid; u >= 0; u = up[u]) {
       ++depth;
       if (p.window > 0 && depth >= p.window) continue;
-      if (p.by_key) atomicOr(&bits[u][tid >> 5], 1u << (tid & 31));
-      else bits[tid][u >> 5] |= 1u << (u & 31);
+      if (p.by_key) {        // the node's rows
+        const int r = tid * p.group;
+        const uint64_t m = (p.group == 64 ? ~0ull : (1ull << p.group) - 1ull) << r;
+        if ((uint32_t)m) atomicOr(&bits[u][0], (uint32_t)m);
+        if (m >> 32) atomicOr(&bits[u][1], (uint32_t)(m >> 32));
+      } else bits[tid][u >> 5] |= 1u << (u & 31);
     }
   if (p.by_key) __syncthreads();
   pdl_wait();
@@ -151,10 +165,8 @@ __global__ void __launch_bounds__(kFmaThreads) tree_fma_kernel(const TreeFma p) 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   pdl_wait();
   pdl_trigger();
-  const int64_t total = pl.starts[pl.num_seqs], slices = tree_slices(pl, total);
-  if ((int64_t)blockIdx.x >= slices) return;
   TreeWalk walk;
-  walk.start(pl, blockIdx.x, total, slices);
+  walk.start(pl, blockIdx.x);
   TreeSegment g;
   while (walk.next(pl, g)) {
     const TreeSeq& s = walk.s;
@@ -468,6 +480,8 @@ __global__ void __launch_bounds__(kAcceptWarps * 32) tree_accept_kernel(const Ac
 // ------------------------------------------------------------------- host
 size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 
+int words_of(int max_q) { return max_q <= 64 ? 2 : (max_q + 31) / 32; }   // two at least: by_key
+
 bool few_rows(int group, int max_q) { return group * max_q <= kTreeFewRows; }
 
 int unit_tokens_of(int path, int group, int max_q) {
@@ -481,13 +495,13 @@ int unit_tokens_of(int path, int group, int max_q) {
 int grid_of(int path, int sms) { return path == PKVD_PATH_FMA ? 2 * sms : sms; }
 
 struct WorkspaceLayout {
-  size_t starts, slice_seq, anc, depth, rec, rec_ml, bytes;
+  size_t starts, slice, anc, depth, rec, rec_ml, bytes;
   WorkspaceLayout(int path, int num_seqs, int group, int head_dim, int max_q, int sms) {
-    const int words = (max_q + 31) / 32;
+    const int words = words_of(max_q);
     const size_t rows = (size_t)2 * grid_of(path, sms) * unit_tokens_of(path, group, max_q) * group;
     starts = 0;
-    slice_seq = starts + up256(sizeof(int64_t) * ((size_t)num_seqs + 1));
-    anc = slice_seq + up256(sizeof(int32_t) * (size_t)grid_of(path, sms));
+    slice = starts + up256(sizeof(int64_t) * ((size_t)num_seqs + 1));
+    anc = slice + up256(sizeof(TreeStart) * (size_t)grid_of(path, sms));
     depth = anc + up256(sizeof(uint32_t) * (size_t)num_seqs * max_q * words);
     rec_ml = depth + up256(sizeof(int32_t) * (size_t)num_seqs * max_q);
     rec = rec_ml + up256(sizeof(float2) * rows);
@@ -536,7 +550,7 @@ cudaError_t launch_tree(const TreeArgs& a, cudaStream_t stream) {
   p.num_seqs = a.num_seqs;
   p.total_q = a.total_q;
   p.max_q = a.max_seqlen_q;
-  p.words = (a.max_seqlen_q + 31) / 32;
+  p.words = words_of(a.max_seqlen_q);
   p.unit_tokens = unit_tokens_of(a.path, group, a.max_seqlen_q);
   p.unit_rows = p.unit_tokens * group;
   p.hkv = c.num_kv_heads;
@@ -547,7 +561,7 @@ cudaError_t launch_tree(const TreeArgs& a, cudaStream_t stream) {
   p.grid = grid_of(a.path, a.sms);
   p.by_key = a.path == PKVD_PATH_TC && few_rows(group, a.max_seqlen_q);
   p.starts = reinterpret_cast<int64_t*>(ws + lay.starts);
-  p.slice_seq = reinterpret_cast<int32_t*>(ws + lay.slice_seq);
+  p.slice = reinterpret_cast<TreeStart*>(ws + lay.slice);
   p.anc = reinterpret_cast<uint32_t*>(ws + lay.anc);
   p.depth = reinterpret_cast<int32_t*>(ws + lay.depth);
   p.rec = reinterpret_cast<float*>(ws + lay.rec);
@@ -579,6 +593,7 @@ cudaError_t launch_tree(const TreeArgs& a, cudaStream_t stream) {
     else e = wide ? launch_fma<__nv_bfloat16, 128>(f, stream) : launch_fma<__nv_bfloat16, 64>(f, stream);
   }
   if (e != cudaSuccess) return e;
+  if (p.table_tokens <= kTreeKeys) return cudaSuccess;     // a tile of keys each: nothing is cut
   const bool wide = c.head_dim == 128;
   if (c.dtype == PKVD_F32) return wide ? launch_merge<float, 128>(p, a.out, stream) : launch_merge<float, 64>(p, a.out, stream);
   if (c.dtype == PKVD_F16) return wide ? launch_merge<__half, 128>(p, a.out, stream) : launch_merge<__half, 64>(p, a.out, stream);

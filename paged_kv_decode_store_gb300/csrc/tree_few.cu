@@ -49,8 +49,7 @@ struct Layout {
   static constexpr uint32_t kNeg = kRef + 256;                         // [64] what is added to a score: -reference
   static constexpr uint32_t kPos = kNeg + 256;                         // [64] positions of the columns' rows
   static constexpr uint32_t kSlope = kPos + 256;                       // [64]
-  static constexpr uint32_t kNode = kSlope + 256;                      // [64] the columns' nodes
-  static constexpr uint32_t kItems = kNode + 64;
+  static constexpr uint32_t kItems = kSlope + 256;
   static constexpr uint32_t kGaveUp = kItems + kItemBytes;
   static constexpr uint32_t kEnd = kGaveUp + 16;
   // at least 120 KB so that one CTA is resident per SM
@@ -350,7 +349,6 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_few_kernel(const __grid_
     float* neg = reinterpret_cast<float*>(gbase + L::kNeg);
     int* pos = reinterpret_cast<int*>(gbase + L::kPos);
     float* slope = reinterpret_cast<float*>(gbase + L::kSlope);
-    uint8_t* node = gbase + L::kNode;
     // while the weights' buffer is free: the largest scores and rescaling factors
     // of a new reference; the sums at the end
     int* most_of = reinterpret_cast<int*>(gbase + L::kP);
@@ -406,7 +404,6 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_few_kernel(const __grid_
         ref[me] = -INFINITY;
         neg[me] = me < live ? kNoRef : -kNoRef;                // (no column: its scores never ask)
         most_of[me] = ordered(-INFINITY);
-        node[me] = (uint8_t)t;
         if ((MODE & kBias) || pl.window > 0) {
           pos[me] = cached + pl.depth[it.node0 + t];
           slope[me] = bias_slope(p.mod, it.hk * pl.group + c - t * pl.group);
@@ -415,9 +412,9 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_few_kernel(const __grid_
       meet(false);
       if (!ok) break;
       const uint32_t mine = span_bits(0, live - c0);           // this thread's columns that are rows
-      float l[C];
+      float l[C], less[C];                 // sums of weights; what is added to a column's scores (neg)
 #pragma unroll
-      for (int c = 0; c < C; ++c) l[c] = 0.f;
+      for (int c = 0; c < C; ++c) l[c] = 0.f, less[c] = 0.f;
       const int kt_last = uniform(it.kt_last), late = uniform(it.late);
       for (int j = 0; j < all; ++j, ++n) {
         const int kbase = tile_at(kt_last, all, late, j) * kTcKeys;
@@ -430,22 +427,21 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_few_kernel(const __grid_
         uint32_t see = seen ? mine : 0u;
         int at = key;
         if (tree || edge) {
-          uint32_t d0 = 0xffffffffu, d1 = d0;        // the nodes that see it
           if (u >= 0 && seen) {
             const int64_t k = (int64_t)it.seq * pl.max_q + u;
-            d0 = pl.anc[k * pl.words];
-            d1 = pl.words > 1 ? pl.anc[k * pl.words + 1] : 0u;
-            at = cached + pl.depth[k];
+            see &= pl.anc[k * 2 + c0 / 32] >> (c0 & 31);
+            if ((MODE & kBias) || edge) at = cached + pl.depth[k];
           }
-          see = 0u;
+          if (edge) {
+            const int oldest = at + pl.window;               // of the positions that see it
 #pragma unroll
-          for (int c = 0; c < C; ++c) {
-            const int t = node[c0 + c];
-            bool s = seen && (((t & 32 ? d1 : d0) >> (t & 31)) & 1u);
-            if (edge) s = s && at > pos[c0 + c] - pl.window;
-            see |= (uint32_t)s << c;
+            for (int c = 0; c < C; c += 4) {
+              const int4 q = *reinterpret_cast<const int4*>(pos + c0 + c);
+              const uint32_t m = (uint32_t)(q.x < oldest) | (uint32_t)(q.y < oldest) << 1 | (uint32_t)(q.z < oldest) << 2 |
+                                 (uint32_t)(q.w < oldest) << 3;
+              see &= ~(15u << c) | m << c;
+            }
           }
-          see &= mine;
         }
         wait(kSFull + buf, (n >> 1) & 1);
         if (!ok) break;
@@ -484,24 +480,23 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_few_kernel(const __grid_
         }
         // (a segment's first tile has no references yet)
         bool rebase = j == 0;
+        float x[C];
         if (j > 0) {
           float top = -INFINITY;
 #pragma unroll
           for (int c = 0; c < C; c += 4) {
-            const float4 s = *reinterpret_cast<const float4*>(neg + c0 + c);
-            float x0, x1, x2, x3;
-            add2(x0, x1, v[c], v[c + 1], s.x, s.y);
-            add2(x2, x3, v[c + 2], v[c + 3], s.z, s.w);
-            top = tc_max3(tc_max3(top, x0, x1), x2, x3);
+            add2(x[c], x[c + 1], v[c], v[c + 1], less[c], less[c + 1]);
+            add2(x[c + 2], x[c + 3], v[c + 2], v[c + 3], less[c + 2], less[c + 3]);
+            top = tc_max3(tc_max3(top, x[c], x[c + 1]), x[c + 2], x[c + 3]);
           }
           rebase = meet(top > kLimit);
           if (!ok) break;
-          wait(kPVDone, (n - 1) & 1);    // the weights' buffer, and O^T
-          if (ok) tc_fence_after();
         }
         if (rebase) {
           // ---- new references for the columns that passed theirs
           if (j > 0) {
+            wait(kPVDone, (n - 1) & 1);                        // the weights' buffer and O^T are free
+            if (ok) tc_fence_after();
             if (me < N) most_of[me] = ordered(-INFINITY);      // (a segment starts with that)
             meet(false);
             if (!ok) break;
@@ -539,24 +534,26 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_few_kernel(const __grid_
             meet(false);                 // the factors are read before the weights take their place
             if (!ok) break;
           }
-        }
 #pragma unroll
-        for (int c = 0; c < C; c += 8) { // 16 bytes of weights
-          uint32_t pk[4];
-#pragma unroll
-          for (int i = 0; i < 8; i += 4) {
-            const float4 s = *reinterpret_cast<const float4*>(neg + c0 + c + i);
-            float x0, x1, x2, x3;
-            add2(x0, x1, v[c + i], v[c + i + 1], s.x, s.y);
-            add2(x2, x3, v[c + i + 2], v[c + i + 3], s.z, s.w);
-            x0 = tc_ex2(x0), x1 = tc_ex2(x1), x2 = tc_ex2(x2), x3 = tc_ex2(x3);
-            tc_add2(l[c + i], l[c + i + 1], x0, x1);
-            tc_add2(l[c + i + 2], l[c + i + 3], x2, x3);
-            pk[i / 2] = Mma<T>::pack(x0, x1);
-            pk[i / 2 + 1] = Mma<T>::pack(x2, x3);
+          for (int c = 0; c < C; c += 4) {
+            const float4 s = *reinterpret_cast<const float4*>(neg + c0 + c);
+            less[c] = s.x, less[c + 1] = s.y, less[c + 2] = s.z, less[c + 3] = s.w;
+            add2(x[c], x[c + 1], v[c], v[c + 1], s.x, s.y);
+            add2(x[c + 2], x[c + 3], v[c + 2], v[c + 3], s.z, s.w);
           }
-          st_shared_v4(p_row + swz(krow, (c0 + c) / 8), make_uint4(pk[0], pk[1], pk[2], pk[3]));
         }
+        uint32_t pk[C / 2];
+#pragma unroll
+        for (int c = 0; c < C; c += 2) {
+          const float e0 = tc_ex2(x[c]), e1 = tc_ex2(x[c + 1]);
+          tc_add2(l[c], l[c + 1], e0, e1);
+          pk[c / 2] = Mma<T>::pack(e0, e1);
+        }
+        if (j > 0 && !rebase) wait(kPVDone, (n - 1) & 1);      // the weights' buffer is free
+        if (!ok) break;
+#pragma unroll
+        for (int c = 0; c < C; c += 8)
+          st_shared_v4(p_row + swz(krow, (c0 + c) / 8), make_uint4(pk[c / 2], pk[c / 2 + 1], pk[c / 2 + 2], pk[c / 2 + 3]));
         fence_proxy_async_smem();
         tc_fence_before();
         arrive(kPFull);
@@ -590,24 +587,27 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_few_kernel(const __grid_
       tc_fence_before();
       arrive(kOFree);
       const int64_t rec0 = (int64_t)slot * pl.unit_rows;
-      if (slot >= 0 && me < live)
-        pl.rec_ml[rec0 + me] = make_float2(ref[me], (sums[me] + sums[64 + me]) + (sums[128 + me] + sums[192 + me]));
+      // lane c: the sum of column c (mod C), then one over it
+      const int mycol = c0 + lane % C;
+      const float sum = (sums[mycol] + sums[64 + mycol]) + (sums[128 + mycol] + sums[192 + mycol]);
+      if (slot >= 0 && quarter == 0 && lane < C && mycol < live) pl.rec_ml[rec0 + mycol] = make_float2(ref[mycol], sum);
+      const float inv = sum > 0.f ? 1.f / sum : 0.f;
       if (quarter * 32 < D && c0 < live) {
         int t = c0 / pl.group, gi = c0 - t * pl.group;
         const int64_t row_stride = (int64_t)pl.hq * D;
-        T* dst = static_cast<T*>(p.out) + (int64_t)it.q0 * row_stride + (int64_t)it.hk * pl.group * D + krow;
-        float* rec = pl.rec + rec0 * D + krow;
+        T* dst = static_cast<T*>(p.out) + (int64_t)(it.q0 + t) * row_stride + ((int64_t)it.hk * pl.group + gi) * D + krow;
+        float* rec = pl.rec + (rec0 + c0) * D + krow;
 #pragma unroll
         for (int c = 0; c < C; ++c) {
           const int col = c0 + c;
           if (col >= live) break;
           if (slot >= 0) {
-            rec[(int64_t)col * D] = o[c];
+            rec[c * D] = o[c];
           } else {
-            const float sum = (sums[col] + sums[64 + col]) + (sums[128 + col] + sums[192 + col]);
-            dst[t * row_stride + (int64_t)gi * D] = DT<T>::from_f(o[c] * (sum > 0.f ? 1.f / sum : 0.f));
+            *dst = DT<T>::from_f(o[c] * __shfl_sync(FULL_MASK, inv, c));
           }
-          if (++gi == pl.group) gi = 0, ++t;
+          dst += D;
+          if (++gi == pl.group) gi = 0, dst += row_stride - (int64_t)pl.group * D;
         }
       }
       arrive(kItemFree + r % kItemRing);

@@ -27,9 +27,9 @@ struct TreePlan {
   int grid;                                 // CTAs; slices are at most as many
   // the workspace
   int64_t* starts;                          // [num_seqs + 1]: pieces before a sequence
-  int32_t* slice_seq;                       // [grid]: the sequence that a slice begins in
-  // [num_seqs][max_q][words]: a node's visible ancestors and itself; by_key: the
-  // nodes that see it, itself among them
+  struct TreeStart* slice;                  // [grid]: where a slice begins
+  // [num_seqs][max_q][words]: a node's visible ancestors and itself, a bit each;
+  // by_key (at most 64 rows a tree): the rows of the nodes that see it, two words
   uint32_t* anc;
   int by_key;
   int32_t* depth;                           // [num_seqs][max_q]
@@ -43,11 +43,11 @@ struct TreeSeq {
   __device__ int64_t pieces(int hkv) const { return (int64_t)units * hkv * tiles; }
 };
 
-__device__ __forceinline__ TreeSeq tree_seq(const TreePlan& p, int i) {
+__device__ __forceinline__ TreeSeq tree_seq(const TreePlan& p, int q0, int n, int klen) {
   TreeSeq s;
-  s.q0 = p.cu_q[i];
-  s.n = p.cu_q[i + 1] - s.q0;
-  s.klen = p.cu_k[i + 1] - p.cu_k[i];
+  s.q0 = q0;
+  s.n = n;
+  s.klen = klen;
   s.cached = s.klen - s.n;
   s.units = s.tiles = s.lo = s.lo_tile = 0;
   const bool ok = s.q0 >= 0 && s.n >= 0 && s.n <= p.max_q && s.cached >= 0 && (int64_t)s.q0 + s.n <= p.total_q &&
@@ -61,6 +61,10 @@ __device__ __forceinline__ TreeSeq tree_seq(const TreePlan& p, int i) {
   return s;
 }
 
+__device__ __forceinline__ TreeSeq tree_seq(const TreePlan& p, int i) {
+  return tree_seq(p, p.cu_q[i], p.cu_q[i + 1] - p.cu_q[i], p.cu_k[i + 1] - p.cu_k[i]);
+}
+
 // Slices of a batch of `total` pieces, and where one begins.
 __device__ __forceinline__ int64_t tree_slices(const TreePlan& p, int64_t total) {
   return total < p.grid ? total : p.grid;
@@ -71,6 +75,16 @@ __device__ __forceinline__ int64_t tree_slice_of(int64_t total, int64_t slices, 
   return ((f + 1) * slices - 1) / total;
 }
 
+// Where a slice begins, as the plan kernel leaves it: one load instead of a
+// search and the sequence's lengths.
+struct __align__(16) TreeStart {
+  int64_t at, end;                          // the slice's pieces
+  int64_t in;                               // the first one's place in its sequence
+  int seq, q0;
+  int n, klen;
+  int pad[2];
+};
+
 // One segment of a slice: tiles [t0, t1) of a (unit, head).
 struct TreeSegment {
   int seq, unit, head;
@@ -80,33 +94,38 @@ struct TreeSegment {
 
 // Walks a slice's segments.
 struct TreeWalk {
-  int64_t at, end, begin;
+  int64_t at, end, begin, in;               // in: `at` within its sequence
   int cta, seq;
   TreeSeq s;
-  __device__ void start(const TreePlan& p, int c, int64_t total, int64_t slices) {
+  __device__ void start(const TreePlan& p, int c) {
+    const TreeStart f = p.slice[c];
     cta = c;
-    at = begin = tree_slice_begin(total, slices, c);
-    end = tree_slice_begin(total, slices, c + 1);
-    seq = p.slice_seq[c];
-    s = tree_seq(p, seq);
+    at = begin = f.at;
+    end = f.end;
+    in = f.in;
+    seq = f.seq;
+    s = tree_seq(p, f.q0, f.n, f.klen);
   }
   __device__ bool next(const TreePlan& p, TreeSegment& g) {
     if (at >= end) return false;
-    int64_t in = at - p.starts[seq];
     while (in >= s.pieces(p.hkv)) {         // the next sequence with any
       if (++seq >= p.num_seqs) return false;
       in = 0;
       s = tree_seq(p, seq);
     }
-    const int64_t item = in / s.tiles;
+    // (in 32 bits where that holds it: a 64-bit division takes hundreds of clocks)
+    int64_t item;
+    if (in <= 0xffffffffll) item = (uint32_t)in / (uint32_t)s.tiles;
+    else item = in / s.tiles;
     g.seq = seq;
-    g.unit = (int)(item / p.hkv);
-    g.head = (int)(item % p.hkv);
+    g.unit = (int)item / p.hkv;
+    g.head = (int)item - g.unit * p.hkv;
     g.t0 = (int)(in - item * s.tiles);
     g.t1 = (int)(end - at < s.tiles - g.t0 ? g.t0 + (end - at) : s.tiles);
     const bool whole = g.t0 == 0 && g.t1 == s.tiles;
     g.slot = whole ? -1 : 2 * cta + (at == begin ? 0 : 1);
     at += g.t1 - g.t0;
+    in += g.t1 - g.t0;
     return true;
   }
 };

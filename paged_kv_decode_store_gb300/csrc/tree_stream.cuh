@@ -21,10 +21,11 @@ constexpr uint32_t kTmemCols = 512;
 enum : int { kCap = 1, kBias = 2 };       // what a call modifies, known when compiled
 constexpr float kRebase = 8.f;            // a new reference when the maximum grows by > 2^8
 
-// mbarriers: six for each stage of K and V; those of a stream take + g
+// mbarriers: five for each stage of K and V; those of a stream take + g, S, P and
+// PV + g + 2 half
 enum : int {
-  kKFull = 0, kKEmpty = 6, kVFull = 12, kVCut = 18, kVEmpty = 24, kQFull = 30, kQEmpty = 32, kItemFull = 34,
-  kItemFree = 38, kDrain = 42, kOFree = 44, kJoin = 46, kSFull = 50, kSRead = 54, kPFull = 58, kPVDone = 60, kNumBars = 62
+  kKFull = 0, kKEmpty = 5, kVFull = 10, kVCut = 15, kVEmpty = 20, kQFull = 25, kQEmpty = 27, kItemFull = 29,
+  kItemFree = 33, kDrain = 37, kOFree = 39, kJoin = 41, kSFull = 45, kSRead = 49, kPFull = 51, kPVDone = 55, kNumBars = 59
 };
 constexpr uint32_t kBarBytes = 512, kTmemSlot = 8 * kNumBars;
 static_assert(kTmemSlot + 4 <= kBarBytes, "behind the barriers");
@@ -194,10 +195,8 @@ template <typename L>
 __device__ __forceinline__ void tree_segments(const TcTree& p, uint64_t* bars, uint32_t base, Item* ring_items, int lane) {
   constexpr int H = L::kHalves;
   const TreePlan& pl = p.plan;
-  const int64_t total = pl.starts[pl.num_seqs], slices = tree_slices(pl, total);
   TreeWalk walk;
-  walk.at = walk.end = 0;
-  if ((int64_t)blockIdx.x < slices) walk.start(pl, blockIdx.x, total, slices);
+  walk.start(pl, blockIdx.x);
   if (lane == 0) {
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&p.tmap_q)) : "memory");
     bool ok = true;

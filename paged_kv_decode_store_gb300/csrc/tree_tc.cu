@@ -1,36 +1,38 @@
 // Attention for trees of drafted tokens on the 5th-generation tensor cores
 // (the mathematics: tree.cu; how the work is cut: tree_plan.cuh).
 //
-// A drafted tree is a handful of query rows over a long cache: the keys decide
-// the time, so every CTA streams an equal share of all of them (one persistent
-// CTA an SM, a slice of the batch's list of 128-key tiles), and a (unit, KV
-// head) that is cut leaves records that the merge kernel joins.
+// A drafted tree is a handful of query rows over a long cache, so every CTA
+// streams an equal share of all keys (one persistent CTA an SM, a slice of the
+// batch's list of 128-key tiles), and a (unit, KV head) that is cut leaves records
+// that the merge kernel joins.
 //
 // Rows are (node, query head of the group) pairs, up to 128 a Q tile.  The CTA
 // has two streams, each with its S, P and O in tensor memory and eight softmax
-// warps (two threads a row, 64 keys each):
+// warps (two threads a row):
 //   a unit of two Q tiles: stream g takes Q tile g, both use each K/V tile;
 //   a unit of one Q tile: both take it, stream g every second K/V tile, and
 //   their sums are joined from tensor memory at the end of the segment.
-// So the chain score product -> softmax -> value product of a tile runs beside
-// another one whatever the tree's size, and the K/V copies set the pace while a
-// unit has one Q tile.  Keys go from the newest backwards; the drafted ones, which
-// are masked by a bit a (row, node), come first.
+// A stream takes a tile's keys 64 at a time, in two S buffers: the next scores are
+// there when a softmax ends, and the product with V and the one after next run
+// beside it.  (All 128 at once, weights over their scores, left the tensor pipe
+// idle while a softmax ran and the softmax while products did: 4,200 clocks a tile.)
+// A row's reference moves only when a score passes it by far (bf16 weights have
+// fp32's range), by a vote of the row's two warps.  Keys go from the newest
+// backwards; the drafted ones, which are masked by a bit a (row, node), come first.
 //
 // Warps (20): 0-7 and 8-15 softmax of stream 0 and 1 (warp w of a stream: TMEM
-// lanes 32 (w % 4) .., keys 64 (w / 4) ..), 16 copies of K and V, 17 and 19 the
-// products of stream 0 and 1, 18 the segments and Q.
+// lanes 32 (w % 4) .., keys 32 (w / 4) .. of 64), 16 copies of K and V, 17 and 19
+// the products of stream 0 and 1, 18 the segments and Q.
 #include "tree_stream.cuh"
 
 namespace pkvd {
 
 namespace {
 
-// TMEM columns: S of stream g at [128 g, 128 g + 128), O at [256 + g D, 256 + g D
-// + D).  head_dim 128: a half's weights overwrite the first 32 of its own 64 S
-// columns; head_dim 64: they have [384 + 64 g, 448 + 64 g), so the next S may be
-// computed while they are in use.
-constexpr uint32_t kColO = 256, kColP64 = 384;
+// TMEM columns: S of stream g, keys of half h, at [128 g + 64 h, ..), its weights
+// over the first 16 of each thread's 32; O at [256 + g D, 256 + g D + D).
+constexpr uint32_t kColO = 256;
+constexpr int kThreadKeys = 32;           // keys of a softmax thread
 constexpr float kLinear = 16384.f;        // largest bias (log2 units) put together from parts
 
 template <int D>
@@ -42,11 +44,10 @@ struct Layout {
   static constexpr uint32_t kV = kK + kKStages * kHalves * kHalf;
   static constexpr uint32_t kBar = kV + kVStages * kHalves * kHalf;
   static constexpr uint32_t kQHalf = kHalf;                            // bytes of a Q tile's 64 columns
-  static constexpr int kQBufs = 2, kJoinWarps = 4;                                // a quarter of the rows, both streams
-  static constexpr uint32_t kX = kBar + kBarBytes;                         // exchange: 1024 bytes a stream and buffer
-  static constexpr int kXBufs = D == 64 ? 2 : 1;
-  static constexpr uint32_t kItems = kX + kXBufs * 2048;               // ring of segments
-  static constexpr uint32_t kGaveUp = kItems + kItemBytes;                    // one word a pair of softmax warps
+  static constexpr int kQBufs = 2, kJoinWarps = 4;                     // kJoin: a quarter of the rows, both streams
+  static constexpr uint32_t kX = kBar + kBarBytes;                     // exchange: 1024 bytes a stream
+  static constexpr uint32_t kItems = kX + 2048;                        // ring of segments
+  static constexpr uint32_t kGaveUp = kItems + kItemBytes;             // one word a pair of softmax warps
   static constexpr uint32_t kEnd = kGaveUp + 32;
   // at least 120 KB so that one CTA (which holds all TMEM) is resident per SM
   static constexpr uint32_t kBytes = kEnd > 122880u ? kEnd : 122880u;
@@ -69,51 +70,44 @@ __device__ __forceinline__ void st_global_v8(void* dst, const uint32_t* w) {
                : "memory");
 }
 
-// Which of a thread's 64 columns its row sees: two words, and how many visible
-// nodes lie after the last column.
+// Which of a thread's 32 keys its row sees, and how many visible nodes lie after
+// the last of them.
 struct Seen {
-  uint32_t word[2];
+  uint32_t word;
   int after;
 };
 
-// Columns of a tile that reaches into the tree (first key kbase, `cut` of the
-// columns before the first node).
-__device__ __forceinline__ Seen tree_columns(const uint32_t* anc, int words, int first, int cut) {
+// Keys that reach into the tree: `cut` of them lie before the first node (below 0:
+// the first is a later node), the first `first` before the row's window.
+__device__ __forceinline__ Seen tree_keys(const uint32_t* anc, int words, int first, int cut) {
   Seen s;
   s.after = 0;
-  for (int k = 0; k < words; ++k) {                  // nodes at 64 - cut and later
-    const int from = 64 - cut - 32 * k;
+  for (int k = 0; k < words; ++k) {                  // nodes at 32 - cut and later
+    const int from = kThreadKeys - cut - 32 * k;
     const uint32_t x = anc[k];
     s.after += __popc(from <= 0 ? x : from >= 32 ? 0u : x >> from);
   }
-#pragma unroll
-  for (int w = 0; w < 2; ++w) {
-    const int b = 32 * w - cut;                      // the node of the word's first column
-    uint32_t x = 0u;
-    if (b >= 0) {
-      const int k = b >> 5;
-      const uint32_t lo = k < words ? anc[k] : 0u, hi = k + 1 < words ? anc[k + 1] : 0u;
-      x = __funnelshift_r(lo, hi, b & 31);
-    } else if (b > -32) {
-      x = anc[0] << -b;
-    }
-    s.word[w] = x | span_bits(first - 32 * w, cut - 32 * w);
+  uint32_t x = 0u;
+  if (cut <= 0) {
+    const int k = -cut >> 5;
+    const uint32_t lo = k < words ? anc[k] : 0u, hi = k + 1 < words ? anc[k + 1] : 0u;
+    x = __funnelshift_r(lo, hi, -cut & 31);
+  } else if (cut < 32) {
+    x = anc[0] << cut;
   }
+  s.word = x | span_bits(first, cut);
   return s;
 }
 
 // Everything a row does not see becomes `x`, whatever it was.  Most groups of
-// eight columns are visible to the whole warp.
-__device__ __forceinline__ void hide(float (&v)[kCols], const uint32_t (&seen)[2], float x) {
+// eight keys are visible to the whole warp.
+__device__ __forceinline__ void hide(float (&v)[kThreadKeys], uint32_t seen, float x) {
+  const uint32_t every = __reduce_and_sync(FULL_MASK, seen);
 #pragma unroll
-  for (int w = 0; w < 2; ++w) {
-    const uint32_t m = seen[w], every = __reduce_and_sync(FULL_MASK, m);
+  for (int c8 = 0; c8 < 32; c8 += 8) {
+    if (((every >> c8) & 0xffu) == 0xffu) continue;
 #pragma unroll
-    for (int c8 = 0; c8 < 32; c8 += 8) {
-      if (((every >> c8) & 0xffu) == 0xffu) continue;
-#pragma unroll
-      for (int c = c8; c < c8 + 8; ++c) v[32 * w + c] = ((m >> c) & 1u) ? v[32 * w + c] : x;
-    }
+    for (int c = c8; c < c8 + 8; ++c) v[c] = (seen >> c) & 1u ? v[c] : x;
   }
 }
 
@@ -121,7 +115,6 @@ template <typename T, int D, int MODE>
 __global__ void __launch_bounds__(kTreeThreads, 1) tree_tc_kernel(const __grid_constant__ TcTree p) {
   using L = Layout<D>;
   constexpr int H = L::kHalves, kKStages = L::kKStages, kVStages = L::kVStages;
-  constexpr bool kSepP = D == 64;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* gbase = smem_raw;
   const uint32_t base = smem_u32(smem_raw);
@@ -153,20 +146,19 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_tc_kernel(const __grid_c
     tree_segments<L>(p, bars, base, ring_items, lane);
   } else if (warp == kMmaWarp || warp == kMmaWarp1) {
     // ---------------------------------------------------------------- MMA
-    // S(n) of the stream, n counting all its K tiles: Q and K have landed and
-    // its S columns are free (head_dim 64: S(n - 1) was read; 128: PV(n - 1)
-    // is done, its weights lie there).  PV(n): the weights, V, and for a
-    // segment's first one the O columns of the segment before were read.  A
-    // stage of K, V or Q is free when both streams are done with it; one that
-    // this stream does not use it waits for all the same, so that no phase of a
-    // stage is waited for before the one before it is over.  The whole warp
-    // walks through this and one elected thread issues.
+    // S(n, h) of the stream, n counting all its K tiles, h = 1 (the newer 64
+    // keys) before 0: Q and K have landed and PV(n - 1, h), whose weights lie in
+    // the same columns, is done.  PV(n, h): the weights, V, and for a segment's
+    // first one the O columns of the segment before were read.  A stage of K, V or
+    // Q is free when both streams are done with it; one that this stream does not
+    // use it waits for all the same, so that no phase of a stage is waited for
+    // before the one before it is over.  The whole warp walks through this and one
+    // elected thread issues.
     const bool leader = elect_one();
     const int g = warp == kMmaWarp ? 0 : 1;
     constexpr uint32_t fmt = std::is_same<T, __nv_bfloat16>::value ? 1u : 0u;
-    constexpr uint32_t id_s = tc_idesc(fmt, kTcKeys, 0), id_pv = tc_idesc(fmt, D, 1), hi = desc_hi(1024);
-    const uint32_t s_cols = tmem + g * kTcKeys, o_cols = tmem + kColO + g * D;
-    const uint32_t p_cols = kSepP ? tmem + kColP64 + g * 64 : s_cols;
+    constexpr uint32_t id_s = tc_idesc(fmt, 64, 0), id_pv = tc_idesc(fmt, D, 1), hi = desc_hi(1024);
+    const uint32_t s_cols = tmem + g * 128, o_cols = tmem + kColO + g * D;
     bool ok = true;
     auto wait = [&](int bar, uint32_t parity) {
       if (ok) ok = __all_sync(FULL_MASK, wait_bounded(&bars[bar], parity));
@@ -207,39 +199,31 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_tc_kernel(const __grid_c
           next_v();
         }
       };
-      auto issue_s = [&](bool last) {
+      // S(m, h) of the segment's j-th tile, m its count of all
+      auto scores = [&](int m, int j, int h) {
+        if (h == 1) {
+          to_k(tile(j));
+          wait(kKFull + kstg, kpar);
+        }
+        if (m > 0) wait(kPVDone + g + 2 * h, (m - 1) & 1);
+        if (!ok) return;
         tc_fence_after();
-        const uint32_t kd = desc_lo(base + L::kK + kstg * H * kHalf, 16);
+        const uint32_t kd = desc_lo(base + L::kK + kstg * H * kHalf, 16) + h * (64 * 128 >> 4), d = s_cols + h * 64;
         if (leader) {
 #pragma unroll
           for (int k = 0; k < D / 16; ++k) {
             const uint32_t off = ((k >> 2) * kHalf + (k & 3) * 32) >> 4;
-            if (k == 0) mma_ss<false>(s_cols, qd, kd, hi, id_s);
-            else mma_ss<true>(s_cols, qd + off, kd + off, hi, id_s);
+            if (k == 0) mma_ss<false>(d, qd, kd, hi, id_s);
+            else mma_ss<true>(d, qd + off, kd + off, hi, id_s);
           }
-          tc_commit(&bars[kSFull + g]);
-          tc_commit(&bars[kKEmpty + kstg]);
-          if (last) tc_commit(&bars[kQEmpty + qbuf]);
+          tc_commit(&bars[kSFull + g + 2 * h]);
+          if (h == 0) {
+            tc_commit(&bars[kKEmpty + kstg]);
+            if (j == gn - 1) tc_commit(&bars[kQEmpty + qbuf]);
+          }
         }
         __syncwarp();
-        next_k();
-        ++kt;
-      };
-      auto issue_pv = [&](uint32_t add) {
-        tc_fence_after();
-        const uint32_t vd = desc_lo(base + L::kV + vstg * H * kHalf, kHalf);
-        if (leader) {
-#pragma unroll
-          for (int k = 0; k < kTcKeys / 16; ++k) {         // 16 keys = 8 packed columns of weights
-            const uint32_t col = kSepP ? k * 8 : (k >> 2) * kCols + (k & 3) * 8;
-            mma_ts(o_cols, p_cols + col, vd + k * 128, hi, id_pv, k > 0 ? 1u : add);
-          }
-          tc_commit(&bars[kPVDone + g]);
-          tc_commit(&bars[kVEmpty + vstg]);
-        }
-        __syncwarp();
-        next_v();
-        ++vt;
+        if (h == 0) next_k(), ++kt;
       };
       // The O columns of the segment before were read.  This warp's own arrival
       // for the segment keeps the softmax warps of a segment in which the stream
@@ -248,31 +232,36 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_tc_kernel(const __grid_c
         if (r > 0) wait(kOFree + g, (r - 1) & 1);
         if (ok && leader) mbar_arrive(&bars[kOFree + g]);
       };
-      if (gn > 0) {
-        // what arrives last (the softmax warps' part) is waited for last
-        to_k(tile(0));
-        wait(kQFull + qbuf, used[qbuf] & 1);
-        wait(kKFull + kstg, kpar);
-        if (n > 0) wait((kSepP ? kSRead : kPVDone) + g, (n - 1) & 1);
-        if (ok) issue_s(gn == 1);
-        for (int j = 0; ok && j < gn; ++j, ++n) {
-          const bool more = j + 1 < gn;
-          if (more) {
-            to_k(tile(j + 1));
-            wait(kKFull + kstg, kpar);
-          }
-          if (kSepP && more) {
-            wait(kSRead + g, n & 1);
-            if (ok) issue_s(j + 2 == gn);
-          }
+      auto values = [&](int j, int h) {
+        if (h == 1) {
           to_v(tile(j));
           wait(kVFull + vstg, vpar);
           if (j == 0) pass_o();
-          wait(kPFull + g, n & 1);
-          if (ok) issue_pv(j);
-          if (!kSepP && more) {
-            wait(kPVDone + g, n & 1);
-            if (ok) issue_s(j + 2 == gn);
+        }
+        wait(kPFull + g + 2 * h, n & 1);
+        if (!ok) return;
+        tc_fence_after();
+        const uint32_t vd = desc_lo(base + L::kV + vstg * H * kHalf, kHalf) + h * 4 * 128;
+        if (leader) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k)                      // 16 keys = 8 packed columns of weights
+            mma_ts(o_cols, s_cols + h * 64 + (k >> 1) * kThreadKeys + (k & 1) * 8, vd + k * 128, hi, id_pv,
+                   j > 0 || h == 0 || k > 0 ? 1u : 0u);
+          tc_commit(&bars[kPVDone + g + 2 * h]);
+          if (h == 0) tc_commit(&bars[kVEmpty + vstg]);
+        }
+        __syncwarp();
+        if (h == 0) next_v(), ++vt;
+      };
+      if (gn > 0) {
+        wait(kQFull + qbuf, used[qbuf] & 1);
+        scores(n, 0, 1);
+        scores(n, 0, 0);
+        for (int j = 0; ok && j < gn; ++j, ++n) {
+#pragma unroll
+          for (int h = 1; h >= 0; --h) {
+            values(j, h);
+            if (j + 1 < gn) scores(n + 1, j + 1, h);
           }
         }
       } else {
@@ -301,8 +290,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_tc_kernel(const __grid_c
     // quarter meet at an mbarrier (kJoin), whose wait is bounded too.
     const int g = warp >> 3, half = (warp >> 2) & 1, quarter = warp & 3, row = quarter * 32 + lane;
     const uint32_t lane_base = (uint32_t)(quarter * 32) << 16;
-    const uint32_t s_addr = tmem + lane_base + g * kTcKeys + half * kCols;
-    const uint32_t p_addr = kSepP ? tmem + lane_base + kColP64 + g * 64 + half * 32 : s_addr;
+    const uint32_t s_addr = tmem + lane_base + g * 128 + half * kThreadKeys;
     const uint32_t o_addr = tmem + lane_base + kColO + g * D + half * (D / 2);
     // what a row's threads tell each other: 256 bytes a quarter of a stream's rows
     float* const x0 = reinterpret_cast<float*>(gbase + L::kX + quarter * 256);
@@ -321,9 +309,16 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_tc_kernel(const __grid_c
     };
     volatile uint32_t* gave_up = reinterpret_cast<volatile uint32_t*>(gbase + L::kGaveUp) + g * 4 + quarter;
     bool told = false;
-    auto exchange = [&] {                        // what the row's two warps wrote is readable by both
-      asm volatile("bar.sync %0, 64;" ::"r"(1 + g * 4 + quarter) : "memory");
+    auto meet = [&](bool mine) -> bool {         // any thread's of the row's two warps?
+      uint32_t any;
+      asm volatile(
+          "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 q, %1, 0;\n\t"
+          "barrier.cta.red.or.pred p, %2, 64, q;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+          : "=r"(any)
+          : "r"((uint32_t)mine), "r"(1 + g * 4 + quarter)
+          : "memory");
       if (*gave_up) ok = false, told = true;     // the same word in every lane
+      return any != 0;
     };
     int joins = 0;
     auto join = [&] {                            // the same for the row's four warps of both streams
@@ -331,6 +326,10 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_tc_kernel(const __grid_c
       wait(kJoin + quarter, joins & 1);
       ++joins;
     };
+    // How far a score may pass its reference before that moves: tree_few.cu.  f16
+    // weights keep their bits down to 2^-21 of the row's largest.
+    constexpr bool kNarrow = std::is_same<T, __half>::value;
+    constexpr float kLift = kNarrow ? 7.f : 0.f, kLimit = kNarrow ? 15.f : 64.f;
     int n = 0;                                   // this stream's K tiles so far, of all segments
     for (int r = 0; ok; ++r) {
       ok = __all_sync(FULL_MASK, wait_item(&bars[kItemFull + r % kItemRing], (r / kItemRing) & 1));
@@ -355,143 +354,144 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_tc_kernel(const __grid_c
         near = uniform(__reduce_max_sync(FULL_MASK, pr) - (int)fminf(kLinear / steepest, 1e9f));
       }
       const float range = live ? p.poly_range : INFINITY;   // padding rows have no say
-      float m_ref = -INFINITY, l = 0.f;
+      float m_ref = -INFINITY, less = 0.f, limit = -3e38f, l = 0.f;   // no reference yet: any visible key asks for one
       const int step_keys = two ? kTcKeys : 2 * kTcKeys;
-      int kbase = (uniform(it.kt_last) - (two ? 0 : g)) * kTcKeys + half * kCols;
+      int kbase = (uniform(it.kt_last) - (two ? 0 : g)) * kTcKeys + half * kThreadKeys;
       for (int j = 0; j < gn; ++j, ++n, kbase -= step_keys) {
-        // masks first: their loads run beside the product
-        const bool tree = kbase + kCols > cached;
-        const bool whole = !tree && kbase >= wr_max;
-        const int cut = min(max(cached - kbase, -INT_MAX), kCols);
-        Seen seen;
-        seen.word[0] = seen.word[1] = 0xffffffffu;
-        seen.after = 0;
-        if (tree) {
-          seen = tree_columns(anc, pl.words, wr - kbase, cut);
-        } else if (!whole) {
-          seen.word[0] = span_bits(wr - kbase, 32);
-          seen.word[1] = span_bits(wr - kbase - 32, 32);
-        }
-        wait(kSFull + g, n & 1);
-        if (!ok) break;
-        tc_fence_after();
-        float v[kCols];
-        auto read = [&] {
-          tmem_ld32(s_addr, v);
-          tmem_ld32(s_addr + 32, v + 32);
-          tmem_ld_wait();
-        };
-        read();
-        // raw scores become scores in log2 units, up to a part of a linear bias
-        // that is the same for eight columns: column c's is v[c] + bias + (c / 8) step
-        const bool linear = (MODE & kBias) && !tree && kbase >= near;
-        float kk[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) kk[i] = linear ? -nslope * (float)i : 0.f;
-        const float bias = linear ? nslope * (float)(pr - kbase) : 0.f, step = linear ? -nslope * 8.f : 0.f;
-        if (MODE & kCap) {
-          // the form is chosen by the scores that count: with what else lies in
-          // the stages the last bit would change from run to run
-          if (!whole) hide(v, seen.word, 0.f);
-          float most = 0.f;              // largest square: the polynomial's range
-#pragma unroll
-          for (int c = 0; c < kCols; c += 2)
-            odd_poly2<(MODE & kBias) != 0>(v[c], v[c + 1], f.poly, kk[c & 7], kk[(c & 7) + 1], most);
-          if (!__all_sync(FULL_MASK, most <= range)) {
-            read();
-#pragma unroll
-            for (int c = 0; c < kCols; ++c) v[c] = fmaf(tanh_fast(v[c] * p.mod.cap_in), p.mod.cap_out_log2, kk[c & 7]);
-          }
-        } else {
-#pragma unroll
-          for (int c = 0; c < kCols; c += 2) {
-            if (MODE & kBias) scale_add2(v[c], v[c + 1], f.scale, kk[c & 7], kk[(c & 7) + 1]);
-            else scale2(v[c], v[c + 1], f.scale);
-          }
-        }
-        if ((MODE & kBias) && !linear) {
-          const float first = (float)(pr - kbase);
-          int after = seen.after;
-#pragma unroll
-          for (int c = kCols - 1; c >= 0; --c) {
-            float back = first - (float)c;
-            if (tree && c >= cut) {      // a node: as far as there are visible ones after it
-              back = (float)after;
-              after += (seen.word[c >> 5] >> (c & 31)) & 1u;
-            }
-            v[c] = fmaf(nslope, back, v[c]);
-          }
-        }
-        if (!whole) hide(v, seen.word, -INFINITY);
-        // head_dim 64: the next S may overwrite these columns once nobody reads them again
-        if (kSepP) {
-          tc_fence_before();
-          arrive(kSRead + g);
-        }
-        float top = -INFINITY;
-#pragma unroll
-        for (int c = 0; c < kCols; c += 8) {
-          if ((MODE & kBias) && c > 0) top -= step;          // relative to the bias of these eight columns
-          top = tc_max3(tc_max3(top, v[c], v[c + 1]), tc_max3(v[c + 2], v[c + 3], v[c + 4]),
-                        tc_max3(v[c + 5], v[c + 6], v[c + 7]));
-        }
-        if (MODE & kBias) top += bias + (kCols / 8 - 1) * step;
-        // the two halves of a row agree on a reference, the larger maximum
-        float* x = xch + (kSepP ? (n & 1) * 512 : 0);
-        x[half * 32 + lane] = top;
-        exchange();
-        if (!ok) break;
-        const float mt = fmaxf(top, x[(half ^ 1) * 32 + lane]);
-        // f16 weights are normal down to 2^-14: with the reference 7 below the
-        // largest score they keep seven bits more
-        constexpr float kLift = std::is_same<T, __half>::value ? 7.f : 0.f;
-        const bool rebase = mt - m_ref > kLift + kRebase;
-        const bool scale_o = rebase && m_ref != -INFINITY;
-        const float alpha = scale_o ? tc_ex2(m_ref - (mt - kLift)) : 1.f;
-        if (rebase) m_ref = mt - kLift;
-        const float mu = m_ref == -INFINITY ? 0.f : m_ref;
-        uint32_t pk[kCols / 2];
-        float s0 = 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f, shift0 = bias - mu, shift1 = shift0;
-#pragma unroll
-        for (int c = 0; c < kCols; c += 4) {
-          if ((MODE & kBias) && c > 0 && c % 8 == 0) tc_add2(shift0, shift1, step, step);
-          tc_add2(v[c], v[c + 1], shift0, shift1);
-          tc_add2(v[c + 2], v[c + 3], shift0, shift1);
-          const float e0 = tc_ex2(v[c]), e1 = tc_ex2(v[c + 1]), e2 = tc_ex2(v[c + 2]), e3 = tc_ex2(v[c + 3]);
-          tc_add2(s0, s1, e0, e1);
-          tc_add2(s2, s3, e2, e3);
-          pk[c / 2] = Mma<T>::pack(e0, e1);
-          pk[c / 2 + 1] = Mma<T>::pack(e2, e3);
-        }
-        l = l * alpha + ((s0 + s1) + (s2 + s3));
-        if (kSepP && j > 0) {                    // the weights' columns are free once PV(n - 1) is done
-          wait(kPVDone + g, (n - 1) & 1);
-          tc_fence_after();
-        }
-        if (__any_sync(FULL_MASK, scale_o)) {    // O too (head_dim 128: PV(n - 1) was done before S(n))
 #pragma unroll 1
-          for (int c4 = 0; c4 < D / 64; ++c4) {
-            float o[32];
-            tmem_ld32(o_addr + c4 * 32, o);
-            tmem_ld_wait();
+        for (int h = 1; h >= 0; --h) {
+          const int k0 = kbase + h * 64;                   // this thread's first key
+          // masks first: their loads run beside the product
+          const bool tree = k0 + kThreadKeys > cached;
+          const bool whole = !tree && k0 >= wr_max;
+          const int cut = min(cached - k0, kThreadKeys);
+          Seen seen;
+          seen.word = 0xffffffffu;
+          seen.after = 0;
+          if (tree) seen = tree_keys(anc, pl.words, wr - k0, cut);
+          else if (!whole) seen.word = span_bits(wr - k0, 32);
+          wait(kSFull + g + 2 * h, n & 1);
+          if (!ok) break;
+          tc_fence_after();
+          float v[kThreadKeys];
+          tmem_ld32(s_addr + h * 64, v);
+          tmem_ld_wait();
+          // raw scores become scores in log2 units, up to a part of a linear bias
+          // that is the same for eight keys: key c's is v[c] + bias + (c / 8) step
+          const bool linear = (MODE & kBias) && !tree && k0 >= near;
+          float kk[8];
 #pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] *= alpha;
-            tmem_st32(o_addr + c4 * 32, o);
+          for (int i = 0; i < 8; ++i) kk[i] = linear ? -nslope * (float)i : 0.f;
+          const float bias = linear ? nslope * (float)(pr - k0) : 0.f, step = linear ? -nslope * 8.f : 0.f;
+          if (MODE & kCap) {
+            // the form is chosen by the scores that count: with what else lies in
+            // the stages the last bit would change from run to run
+            if (!whole) hide(v, seen.word, 0.f);
+            float most = 0.f;            // largest square: the polynomial's range
+#pragma unroll
+            for (int c = 0; c < kThreadKeys; c += 2)
+              odd_poly2<(MODE & kBias) != 0>(v[c], v[c + 1], f.poly, kk[c & 7], kk[(c & 7) + 1], most);
+            if (!__all_sync(FULL_MASK, most <= range)) {
+              tmem_ld32(s_addr + h * 64, v);
+              tmem_ld_wait();
+#pragma unroll
+              for (int c = 0; c < kThreadKeys; ++c)
+                v[c] = fmaf(tanh_fast(v[c] * p.mod.cap_in), p.mod.cap_out_log2, kk[c & 7]);
+            }
+          } else {
+#pragma unroll
+            for (int c = 0; c < kThreadKeys; c += 2) {
+              if (MODE & kBias) scale_add2(v[c], v[c + 1], f.scale, kk[c & 7], kk[(c & 7) + 1]);
+              else scale2(v[c], v[c + 1], f.scale);
+            }
           }
+          if ((MODE & kBias) && !linear) {
+            const float first = (float)(pr - k0);
+            int after = seen.after;
+#pragma unroll
+            for (int c = kThreadKeys - 1; c >= 0; --c) {
+              float back = first - (float)c;
+              if (tree && c >= cut) {    // a node: as far as there are visible ones after it
+                back = (float)after;
+                after += (seen.word >> c) & 1u;
+              }
+              v[c] = fmaf(nslope, back, v[c]);
+            }
+          }
+          if (!whole) hide(v, seen.word, -INFINITY);
+          // relative to the row's reference
+          float top = -INFINITY, shift0 = bias + less, shift1 = shift0;
+#pragma unroll
+          for (int c = 0; c < kThreadKeys; c += 4) {
+            if ((MODE & kBias) && c > 0 && c % 8 == 0) tc_add2(shift0, shift1, step, step);
+            tc_add2(v[c], v[c + 1], shift0, shift1);
+            tc_add2(v[c + 2], v[c + 3], shift0, shift1);
+            top = tc_max3(tc_max3(top, v[c], v[c + 1]), v[c + 2], v[c + 3]);
+          }
+          const bool rebase = meet(live && top > limit);
+          if (!ok) break;
+          if (rebase) {
+            // ---- new references for the rows that passed theirs: the row's two
+            // threads agree on the largest score
+            xch[half * 32 + lane] = top - less;
+            meet(false);
+            if (!ok) break;
+            const float most = fmaxf(top - less, xch[(half ^ 1) * 32 + lane]);
+            const bool unset = m_ref == -INFINITY;
+            const bool moves = unset ? most > -INFINITY : most - m_ref > kLimit;
+            const float now = moves ? most - kLift : m_ref, alpha = moves && !unset ? tc_ex2(m_ref - now) : 1.f;
+            if (moves) {
+              m_ref = now;
+              limit = kLimit;
+              l *= alpha;
+              const float by = -now - less;
+              less = -now;
+#pragma unroll
+              for (int c = 0; c < kThreadKeys; ++c) v[c] += by;
+            }
+            if (__any_sync(FULL_MASK, alpha != 1.f)) {     // O too, when every product before this one is done
+              if (h == 0) wait(kPVDone + g + 2, n & 1);
+              else wait(kPVDone + g, (n - 1) & 1);
+              if (ok) tc_fence_after();
+#pragma unroll 1
+              for (int c4 = 0; c4 < D / 64; ++c4) {
+                float o[32];
+                tmem_ld32(o_addr + c4 * 32, o);
+                tmem_ld_wait();
+#pragma unroll
+                for (int e = 0; e < 32; ++e) o[e] *= alpha;
+                tmem_st32(o_addr + c4 * 32, o);
+              }
+            }
+            meet(false);                 // both have read
+            if (!ok) break;
+          }
+          uint32_t pk[kThreadKeys / 2];
+          float s0 = 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f;
+#pragma unroll
+          for (int c = 0; c < kThreadKeys; c += 4) {
+            const float e0 = tc_ex2(v[c]), e1 = tc_ex2(v[c + 1]), e2 = tc_ex2(v[c + 2]), e3 = tc_ex2(v[c + 3]);
+            tc_add2(s0, s1, e0, e1);
+            tc_add2(s2, s3, e2, e3);
+            pk[c / 2] = Mma<T>::pack(e0, e1);
+            pk[c / 2 + 1] = Mma<T>::pack(e2, e3);
+          }
+          l += (s0 + s1) + (s2 + s3);
+          tmem_st16(s_addr + h * 64, pk);
+          tmem_st_wait();
+          tc_fence_before();
+          arrive(kPFull + g + 2 * h);
         }
-        tmem_st32(p_addr, reinterpret_cast<const float*>(pk));
-        tmem_st_wait();
-        tc_fence_before();
-        arrive(kPFull + g);
+        if (!ok) break;
       }
       if (!ok) break;
-      // the last product; and so every warp of the stream is past its last exchange
+      // the last product
       if (gn > 0) wait(kPVDone + g, (n - 1) & 1);
       if (!ok) break;
       tc_fence_after();
       // the row's sum: half 1's part to half 0, the whole and the reference back
       if (half == 1) xch[lane] = l;
-      exchange();
+      meet(false);
       if (!ok) break;
       if (half == 0) {
         l += xch[lane];
@@ -499,7 +499,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_tc_kernel(const __grid_c
         xch[32 + lane] = m_ref;
       }
       tc_fence_before();
-      if (two) exchange();
+      if (two) meet(false);
       else join();
       if (!ok) break;
       tc_fence_after();
@@ -560,12 +560,12 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_tc_kernel(const __grid_c
       arrive(kOFree);
       arrive(kOFree + 1);
       arrive(kItemFree + r % kItemRing);
-      if (two) exchange();                       // the exchanged values are read before the next segment's
+      if (two) meet(false);                      // the exchanged values are read before the next segment's
       else join();
     }
     if (!told) {
       if (!ok) *gave_up = 1;
-      exchange();
+      meet(false);
     }
     if (!ok && lane == 0) flag_error(p.err, PKVD_ERR_TIMEOUT);
   }

@@ -66,10 +66,11 @@ def tree_accept(drafted: torch.Tensor, parents: torch.Tensor, target: torch.Tens
     tokens.  tokens are the step's new ids, the last of which is no draft."""
     dev, T, n = drafted.device, drafted.shape[0], cu_seqlens_q.shape[0] - 1
     with on_stream(stream, dev):
-        lists = torch.empty(2, n, max(max_path, 0), dtype=torch.int32, device=dev)
-        heads = torch.empty(2, n, dtype=torch.int32, device=dev)
-        positions, tokens = lists.unbind(0)
-        first, counts = heads.unbind(0)
+        width = max(max_path, 0)
+        positions = torch.empty(n, width, dtype=torch.int32, device=dev)
+        first = torch.empty(n, dtype=torch.int32, device=dev)
+        counts = torch.empty(n, dtype=torch.int32, device=dev)
+        tokens = torch.empty(n, width, dtype=torch.int32, device=dev)
         check(_capi.lib().pkvd_tree_accept(
             positions.data_ptr(), first.data_ptr(), counts.data_ptr(), tokens.data_ptr(),
             array(drafted, "drafted", torch.int32, dev, (T,)), array(parents, "parents", torch.int32, dev, (T,)),
