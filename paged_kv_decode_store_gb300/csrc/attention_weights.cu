@@ -27,48 +27,48 @@ __global__ void __launch_bounds__(kThreads) add_weights_kernel(const float* scor
                                                                int ctx_cap, int window, int hq, int group, int wide) {
   const int h = blockIdx.y, i = blockIdx.z;
   const int c = min(max(ctx[i], 0), ctx_cap);
-  const int j = ((int)blockIdx.x * kThreads + (int)threadIdx.x) * kPer;
   pdl_wait();
   pdl_trigger();
-  if (j >= c) return;
   const int first = window_start(c, window);
-  const float* w = win + (int64_t)i * seq_stride + (int64_t)h * head_stride + j;
-  float* o = wout + (int64_t)i * seq_stride + (int64_t)h * head_stride + j;
-  const bool whole = j + kPer <= c;
-  float sum[kPer] = {}, before[kPer] = {};
-  if (wide && whole) {
-    const float4 x = *reinterpret_cast<const float4*>(w);
-    before[0] = x.x, before[1] = x.y, before[2] = x.z, before[3] = x.w;
-  } else {
+  for (int j = ((int)blockIdx.x * kThreads + (int)threadIdx.x) * kPer; j < c; j += (int)gridDim.x * kThreads * kPer) {
+    const float* w = win + (int64_t)i * seq_stride + (int64_t)h * head_stride + j;
+    float* o = wout + (int64_t)i * seq_stride + (int64_t)h * head_stride + j;
+    const bool whole = j + kPer <= c;
+    float sum[kPer] = {}, before[kPer] = {};
+    if (wide && whole) {
+      const float4 x = *reinterpret_cast<const float4*>(w);
+      before[0] = x.x, before[1] = x.y, before[2] = x.z, before[3] = x.w;
+    } else {
 #pragma unroll
-    for (int k = 0; k < kPer; ++k)
-      if (j + k < c) before[k] = w[k];
-  }
-  if (j + kPer > first) {
-    const int64_t row0 = (int64_t)i * hq + (int64_t)h * group;
-    // rows of whole groups of eight: a group of four behind the context or before
-    // the window may hold anything, and is left out below
-    const float* s = scores + row0 * score_ld + j;
-#pragma unroll 8
-    for (int g = 0; g < group; ++g) {
-      const float2 st = stats[row0 + g];
-      const float4 x = *reinterpret_cast<const float4*>(s + g * score_ld);
-      const float m = st.x - lift;
-      const float y[kPer] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-      for (int k = 0; k < kPer; ++k) sum[k] = fmaf(exp2f(y[k] - m), st.y, sum[k]);
+      for (int k = 0; k < kPer; ++k)
+        if (j + k < c) before[k] = w[k];
     }
+    if (j + kPer > first) {
+      const int64_t row0 = (int64_t)i * hq + (int64_t)h * group;
+      // rows of whole groups of eight: a group of four behind the context or before
+      // the window may hold anything, and is left out below
+      const float* s = scores + row0 * score_ld + j;
+#pragma unroll 8
+      for (int g = 0; g < group; ++g) {
+        const float2 st = stats[row0 + g];
+        const float4 x = *reinterpret_cast<const float4*>(s + g * score_ld);
+        const float m = st.x - lift;
+        const float y[kPer] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-    for (int k = 0; k < kPer; ++k)
-      if (j + k < first) sum[k] = 0.f;
-  }
-  if (wide && whole) {
-    *reinterpret_cast<float4*>(o) =
-        make_float4(before[0] + sum[0], before[1] + sum[1], before[2] + sum[2], before[3] + sum[3]);
-  } else {
+        for (int k = 0; k < kPer; ++k) sum[k] = fmaf(exp2f(y[k] - m), st.y, sum[k]);
+      }
 #pragma unroll
-    for (int k = 0; k < kPer; ++k)
-      if (j + k < c) o[k] = before[k] + sum[k];
+      for (int k = 0; k < kPer; ++k)
+        if (j + k < first) sum[k] = 0.f;
+    }
+    if (wide && whole) {
+      *reinterpret_cast<float4*>(o) =
+          make_float4(before[0] + sum[0], before[1] + sum[1], before[2] + sum[2], before[3] + sum[3]);
+    } else {
+#pragma unroll
+      for (int k = 0; k < kPer; ++k)
+        if (j + k < c) o[k] = before[k] + sum[k];
+    }
   }
 }
 
@@ -87,7 +87,10 @@ cudaError_t launch_attention_weights(const AttnArgs& a, const WeightArgs& w, cud
   const int wide = whole16((int64_t)reinterpret_cast<uintptr_t>(w.in)) && whole16((int64_t)reinterpret_cast<uintptr_t>(w.out)) &&
                    whole16(w.seq_stride * 4) && whole16(w.head_stride * 4);
   const int span = kThreads * kPer;
-  const dim3 grid((unsigned)((ctx_cap + span - 1) / span), (unsigned)w.heads, (unsigned)a.num_seqs);
+  // rows are of all lengths: few CTAs each that walk it, rather than many of which most find nothing
+  const int64_t rows = (int64_t)w.heads * a.num_seqs, most = (ctx_cap + span - 1) / span;
+  const int64_t each = 48 * 152 / rows + 1;
+  const dim3 grid((unsigned)(each < most ? each : most), (unsigned)w.heads, (unsigned)a.num_seqs);
   return launch_pdl(add_weights_kernel, grid, dim3(kThreads), 0, stream, (const float*)a.scores, a.score_ld,
                     (const float2*)a.stats, lift, w.in, w.out, w.seq_stride, w.head_stride, a.context_lens, ctx_cap,
                     a.window, a.num_q_heads, a.num_q_heads / w.heads, wide);

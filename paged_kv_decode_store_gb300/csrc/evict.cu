@@ -6,9 +6,9 @@
 // lowest position first among equal weights.  Positions come out in ascending
 // order, the weights that stay close up beside them, zeros behind.
 //
-// A CTA a row, two on an SM.  The weights between are read once (24,576 of them;
-// more of them again for each pass, as many at a time) into shared memory as
-// whole numbers in the order of the numbers, and looked at five times: a radix
+// A CTA a row, two on an SM.  The weights between are read once into shared
+// memory (24,576 of them; what is beyond is read again for each pass) as whole
+// numbers in the order of the numbers, and looked at five times: a radix
 // selection of the last one that stays (11, 11 and 10 bits, a histogram each, two
 // copies of it so that lanes with equal digits wait less for one another), a
 // count and the writing, in order.  Every warp has a contiguous part of the row,
@@ -25,14 +25,11 @@ namespace pkvd {
 
 namespace {
 
+constexpr int kThreads = 512, kWarps = kThreads / 32;
+constexpr int kPer = 48;                                   // weights of a thread in shared memory
 constexpr int kBins = 2048, kCopies = 2;
-template <int THREADS>
-struct Size {
-  static constexpr int kWarps = THREADS / 32;
-  static constexpr int kSpan = 48 * THREADS;                       // positions of a round
-  static constexpr int kStack = kBins * kCopies / kWarps / 2;      // positions and weights that a warp gathers
-  static constexpr int kSmemBytes = kSpan * 4 + kBins * kCopies * 4;
-};
+constexpr int kStack = kBins * kCopies / kWarps / 2;       // positions and weights that a warp gathers
+constexpr int kSmemBytes = kPer * kThreads * 4 + kBins * kCopies * 4;
 
 // A weight's bits in the order of the numbers, and back.  Any NaN becomes the quiet
 // one, above all numbers; 0 is left for no weight.
@@ -51,40 +48,52 @@ struct Row {
   int lo, hi, left;                    // [lo, hi) compete for `left` places behind the first lo
 };
 
-// This warp's part of a round: positions [first, n), 32 at a time.
-template <int kThreads>
+// This warp's part: positions [first, n), 32 at a time; step i's of this thread is
+// held[i * kThreads] for i < kPer, behind that it is read where it lies.
 struct Part {
-  static constexpr int kWarps = Size<kThreads>::kWarps, kSpan = Size<kThreads>::kSpan;
-  int first, n, steps;                 // steps: a multiple of four
-  __device__ Part(const Row& row, int r, int warp) {
-    const int base = row.lo + r * kSpan, span = min(row.hi - base, kSpan);
-    const int seg = ((span + kWarps - 1) / kWarps + 31) / 32 * 32;
-    first = base + min(warp * seg, span);
-    n = base + min(warp * seg + seg, span);
+  const float* src;                    // this lane's first
+  uint32_t* held;
+  int first, mine, steps;              // positions from this lane's first to the end; steps: a multiple of four
+  __device__ Part(const Row& row, uint32_t* held, int warp, int lane) : held(held) {
+    const int span = row.hi - row.lo, seg = ((span + kWarps - 1) / kWarps + 31) / 32 * 32;
+    first = row.lo + (int)min((int64_t)warp * seg, (int64_t)span);
+    const int n = row.lo + (int)min((int64_t)warp * seg + seg, (int64_t)span);
+    src = row.w + first + lane;
+    mine = n - first - lane;
     steps = ((n - first + 31) / 32 + 3) / 4 * 4;
+  }
+  // 0 where there is none
+  __device__ uint32_t read(int i) const { return (int64_t)i * 32 < mine ? ordered_bits(__float_as_uint(src[(int64_t)i * 32])) : 0u; }
+  __device__ void fetch() {
+    const int n = min(steps, kPer);
+#pragma unroll 4
+    for (int i = 0; i < n; ++i) {
+      if (i * 32 < mine)
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(held + i * kThreads)), "l"(src + i * 32)
+                     : "memory");
+    }
+    asm volatile("cp.async.commit_group;\n\tcp.async.wait_group 0;" ::: "memory");
+#pragma unroll 4
+    for (int i = 0; i < n; ++i) held[i * kThreads] = i * 32 < mine ? ordered_bits(held[i * kThreads]) : 0u;
+  }
+  // f(step, bits in order), every lane of the warp alike
+  template <typename F>
+  __device__ void each(F f) const {
+    const int n = min(steps, kPer);
+#pragma unroll 4
+    for (int i = 0; i < n; ++i) f(i, held[i * kThreads]);
+#pragma unroll 1
+    for (int i = kPer; i < steps; i += 4) {
+      uint32_t x[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) x[e] = read(i + e);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) f(i + e, x[e]);
+    }
   }
 };
 
-// The weights of a round, 0 where there is none: step i's at held[i * kThreads],
-// each thread's its own.
-template <int kThreads>
-__device__ __forceinline__ void fetch(const Row& row, const Part<kThreads>& part, uint32_t* held, int lane) {
-  const float* src = row.w + part.first + lane;
-  const int mine = part.n - part.first - lane;             // positions from this lane's first to the end
-#pragma unroll 4
-  for (int i = 0; i < part.steps; ++i) {
-    if (i * 32 < mine)
-      asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(held + i * kThreads)), "l"(src + i * 32)
-                   : "memory");
-  }
-  asm volatile("cp.async.commit_group;\n\tcp.async.wait_group 0;" ::: "memory");
-#pragma unroll 4
-  for (int i = 0; i < part.steps; ++i) held[i * kThreads] = i * 32 < mine ? ordered_bits(held[i * kThreads]) : 0u;
-}
-
-template <int kThreads>
-__global__ void __launch_bounds__(kThreads, 1024 / kThreads) evict_select_kernel(const EvictArgs a) {
-  constexpr int kWarps = Size<kThreads>::kWarps, kSpan = Size<kThreads>::kSpan, kStack = Size<kThreads>::kStack;
+__global__ void __launch_bounds__(kThreads, 2) evict_select_kernel(const EvictArgs a) {
   extern __shared__ __align__(16) uint32_t sm[];
   __shared__ int warp_sum[2][kWarps];
   __shared__ uint32_t found_digit;
@@ -126,8 +135,12 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) evict_select_kernel
   row.lo = sink;
   row.hi = c - recent;
   row.left = count - sink - recent;
-  const int rounds = row.left > 0 ? (row.hi - row.lo + kSpan - 1) / kSpan : 0;
-  if (rounds == 1) fetch(row, Part<kThreads>(row, 0, warp), held, lane);
+  const bool selects = row.left > 0;
+  Part part(row, held, warp, lane);
+  if (selects) part.fetch();
+  // rows that are read again while they are written in place: the weights follow
+  // when every position is known
+  const bool later = row.wo == row.w && selects && row.hi - row.lo > kPer * kThreads;
   if (row.wo != row.w) behind();
 #pragma unroll 1
   for (int j = count + tid; j < a.keep; j += kThreads) row.out[j] = -1;
@@ -136,7 +149,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) evict_select_kernel
     row.out[j] = j;
     if (row.wo && row.wo != row.w) row.wo[j] = row.w[j];
   }
-  if (rounds > 0) {
+  if (selects) {
     int left = row.left;
     uint32_t kth = 0;                  // the last key that stays, so far its upper bits
 #pragma unroll 1
@@ -146,18 +159,12 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) evict_select_kernel
       for (int i = tid; i < kBins * kCopies / 4; i += kThreads) reinterpret_cast<uint4*>(hist)[i] = make_uint4(0, 0, 0, 0);
       __syncthreads();
       uint32_t* const bins = hist + (lane & (kCopies - 1));
-#pragma unroll 1
-      for (int r = 0; r < rounds; ++r) {
-        const Part<kThreads> part(row, r, warp);
-        if (rounds > 1) fetch(row, part, held, lane);
-        // (no weight: key 0, the lowest digit, below every one that is looked for; it
-        // counts nowhere, so that rows of few do not pile up there)
-#pragma unroll 4
-        for (int i = 0; i < part.steps; ++i) {
-          const uint32_t k = key_of(held[i * kThreads]);
-          if (k != 0u && (pass == 0 || k >> above == kth >> above)) atomicAdd(bins + ((k >> shift) & digits) * kCopies, 1u);
-        }
-      }
+      // (no weight: key 0, the lowest digit, below every one that is looked for; it
+      // counts nowhere, so that rows of few do not pile up there)
+      part.each([&](int, uint32_t x) {
+        const uint32_t k = key_of(x);
+        if (k != 0u && (pass == 0 || k >> above == kth >> above)) atomicAdd(bins + ((k >> shift) & digits) * kCopies, 1u);
+      });
       __syncthreads();
       // from the largest digit down: thread t has the kEach bins below kBins - kEach t
       constexpr int kEach = kBins / kThreads;
@@ -196,69 +203,75 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) evict_select_kernel
       left = found_left;
     }
     // in order: what is larger, and of those equal to the last one the first `left`
-    int kept = row.lo, ties = 0;       // of the rounds before
+    int more = 0, tie = 0;             // of this thread, then of the warp
+    part.each([&](int, uint32_t x) {
+      const uint32_t k = key_of(x);
+      more += k > kth;
+      tie += k == kth;
+    });
+    more = __reduce_add_sync(FULL_MASK, more);
+    tie = __reduce_add_sync(FULL_MASK, tie);
+    if (lane == 0) warp_sum[0][warp] = more, warp_sum[1][warp] = tie;
+    __syncthreads();                   // (and every weight was read: in place it may be overwritten, or follows later)
+    const int m = lane < warp ? warp_sum[0][lane % kWarps] : 0, t = lane < warp ? warp_sum[1][lane % kWarps] : 0;
+    const int m_before = __reduce_add_sync(FULL_MASK, m), t_before = __reduce_add_sync(FULL_MASK, t);
+    // the place of this warp's next one: those before it, ties as far as there are places for them
+    int at = row.lo + m_before + min(t_before, left), rank = t_before;
+    const uint32_t below = (1u << lane) - 1u;
+    // what stays is gathered in the warp's part of the histogram's memory, so that
+    // it leaves 32 side by side
+    uint32_t* const stack = hist + warp * (2 * kStack);
+    int fill = 0;
+    auto flush = [&] {
+      __syncwarp();
 #pragma unroll 1
-    for (int r = 0; r < rounds; ++r) {
-      const Part<kThreads> part(row, r, warp);
-      if (rounds > 1) fetch(row, part, held, lane);
-      int more = 0, tie = 0;           // of this thread, then of the warp
-#pragma unroll 4
-      for (int i = 0; i < part.steps; ++i) {
-        const uint32_t k = key_of(held[i * kThreads]);
-        more += k > kth;
-        tie += k == kth;
+      for (int e = lane; e < fill; e += 32) {
+        row.out[at + e] = (int)stack[e];
+        if (row.wo && !later) row.wo[at + e] = __uint_as_float(stack[kStack + e]);
       }
-      more = __reduce_add_sync(FULL_MASK, more);
-      tie = __reduce_add_sync(FULL_MASK, tie);
-      if (lane == 0) warp_sum[0][warp] = more, warp_sum[1][warp] = tie;
-      __syncthreads();                 // (and every weight of the round is read: in place it may be overwritten)
-      const int m = lane < kWarps ? warp_sum[0][lane % kWarps] : 0, t = lane < kWarps ? warp_sum[1][lane % kWarps] : 0;
-      const int m_before = __reduce_add_sync(FULL_MASK, lane < warp ? m : 0), m_all = __reduce_add_sync(FULL_MASK, m);
-      const int t_before = ties + __reduce_add_sync(FULL_MASK, lane < warp ? t : 0), t_all = ties + __reduce_add_sync(FULL_MASK, t);
-      // the place of this warp's next one: those before it, ties as far as there are places for them
-      int at = kept + m_before + min(t_before, left) - min(ties, left), rank = t_before;
-      const uint32_t below = (1u << lane) - 1u;
-      // what stays is gathered in the warp's part of the histogram's memory, so that
-      // it leaves 32 side by side
-      uint32_t* const stack = hist + warp * (2 * kStack);
-      int fill = 0;
-      if (more > 0 || (tie > 0 && rank < left)) {
-#pragma unroll 1
-        for (int i = 0; i < part.steps; ++i) {
-          const uint32_t number = held[i * kThreads], k = key_of(number);
-          bool stay = k >= kth;
-          uint32_t sb = __ballot_sync(FULL_MASK, stay);
-          if (sb != 0u) {
-            const uint32_t tb = __ballot_sync(FULL_MASK, k == kth);
-            if (tb) {
-              stay = k > kth || (k == kth && rank + __popc(tb & below) < left);
-              sb = __ballot_sync(FULL_MASK, stay);
-              rank += __popc(tb);
-            }
-            if (stay) {
-              const int to = fill + __popc(sb & below);
-              stack[to] = (uint32_t)(part.first + i * 32 + lane);
-              stack[kStack + to] = number_bits(number);
-            }
-            fill += __popc(sb);
-          }
-          if (fill > kStack - 32 || i == part.steps - 1) {
-            __syncwarp();
-#pragma unroll 1
-            for (int e = lane; e < fill; e += 32) {
-              row.out[at + e] = (int)stack[e];
-              if (row.wo) row.wo[at + e] = __uint_as_float(stack[kStack + e]);   // to <= the position: not of a later round
-            }
-            __syncwarp();
-            at += fill;
-            fill = 0;
-          }
-        }
+      __syncwarp();
+      at += fill;
+      fill = 0;
+    };
+    auto take = [&](int i, uint32_t x) {
+      const uint32_t k = key_of(x);
+      bool stay = k >= kth;
+      uint32_t sb = __ballot_sync(FULL_MASK, stay);
+      if (sb == 0u) return;
+      const uint32_t tb = __ballot_sync(FULL_MASK, k == kth);
+      if (tb) {
+        stay = k > kth || (k == kth && rank + __popc(tb & below) < left);
+        sb = __ballot_sync(FULL_MASK, stay);
+        rank += __popc(tb);
       }
-      kept += m_all + min(t_all, left) - min(ties, left);
-      ties = t_all;
-      __syncthreads();
+      if (stay) {
+        const int to = fill + __popc(sb & below);
+        stack[to] = (uint32_t)(part.first + i * 32 + lane);
+        stack[kStack + to] = number_bits(x);
+      }
+      fill += __popc(sb);
+      if (fill > kStack - 32) flush();
+    };
+    if (more > 0 || (tie > 0 && rank < left)) {
+      const int n = min(part.steps, kPer);
+#pragma unroll 1
+      for (int i = 0; i < n; ++i) take(i, part.held[i * kThreads]);
+#pragma unroll 1
+      for (int i = kPer; i < part.steps; ++i) take(i, part.read(i));
+      flush();
     }
+    if (later) {                       // position r comes from r or behind it: a stretch read before it is written
+      const int to = row.lo + row.left;
+#pragma unroll 1
+      for (int base = row.lo; base < to; base += kThreads) {
+        const int r = base + tid;
+        __syncthreads();
+        const float x = r < to ? row.w[row.out[r]] : 0.f;
+        __syncthreads();
+        if (r < to) row.wo[r] = x;
+      }
+    }
+    __syncthreads();
   }
   // the last ones: to <= from, a stretch read before it is written
   const int to = count - recent;
@@ -278,19 +291,13 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) evict_select_kernel
   }
 }
 
-template <int kThreads>
-cudaError_t launch(const EvictArgs& a, int num_seqs, int heads, cudaStream_t stream) {
-  constexpr int smem = Size<kThreads>::kSmemBytes;
-  cudaError_t e = cudaFuncSetAttribute(evict_select_kernel<kThreads>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  if (e != cudaSuccess) return e;
-  return launch_pdl(evict_select_kernel<kThreads>, dim3(heads, num_seqs), dim3(kThreads), smem, stream, a);
-}
-
 }  // namespace
 
 cudaError_t launch_evict_select(const EvictArgs& a, int num_seqs, int heads, cudaStream_t stream) {
   if (num_seqs == 0 || heads == 0) return cudaSuccess;
-  return a.length > Size<512>::kSpan ? launch<1024>(a, num_seqs, heads, stream) : launch<512>(a, num_seqs, heads, stream);
+  cudaError_t e = cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(evict_select_kernel, dim3(heads, num_seqs), dim3(kThreads), kSmemBytes, stream, a);
 }
 
 }  // namespace pkvd

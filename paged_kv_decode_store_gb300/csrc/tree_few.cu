@@ -339,8 +339,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_few_kernel(const __grid_
     // ------------------------------------------------------------ softmax
     // Every wait is bounded.  The warps meet at a named barrier, which does not
     // give up, but always brings all: each passes the same ones, a last one when
-    // it leaves, and one that gave up says so at their next meeting, where all
-    // leave.
+    // it leaves, where one that gave up asks, so that all learn of it and leave.
     const int quarter = warp & 3, c0 = (warp >> 2) * C, krow = quarter * 32 + lane, me = threadIdx.x;
     const uint32_t lane_base = (uint32_t)(quarter * 32) << 16;
     const uint32_t s_addr = tmem + lane_base + c0, o_addr = s_addr + kColO;
@@ -368,7 +367,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_few_kernel(const __grid_
     };
     volatile uint32_t* gave_up = reinterpret_cast<volatile uint32_t*>(gbase + L::kGaveUp);
     bool told = false;
-    auto meet = [&](bool mine) -> bool {         // any thread's?
+    auto vote = [&](bool mine) -> bool {         // any thread's?
       uint32_t any;
       asm volatile(
           "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 q, %1, 0;\n\t"
@@ -376,8 +375,10 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_few_kernel(const __grid_
           : "=r"(any)
           : "r"((uint32_t)mine)
           : "memory");
-      if (*gave_up) ok = false, told = true;     // the same word in every lane
       return any != 0;
+    };
+    auto meet = [&] {                            // where nobody asks for anything: one that does gave up
+      if (vote(false)) ok = false, told = true;
     };
     // How far a score may pass its reference before that moves.  bf16 weights
     // have fp32's range: 2^64 times 2^23 keys and values of 2^30 stay within it.
@@ -409,7 +410,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_few_kernel(const __grid_
           slope[me] = bias_slope(p.mod, it.hk * pl.group + c - t * pl.group);
         }
       }
-      meet(false);
+      meet();
       if (!ok) break;
       const uint32_t mine = span_bits(0, live - c0);           // this thread's columns that are rows
       float l[C], less[C];                 // sums of weights; what is added to a column's scores (neg)
@@ -489,7 +490,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_few_kernel(const __grid_
             add2(x[c + 2], x[c + 3], v[c + 2], v[c + 3], less[c + 2], less[c + 3]);
             top = tc_max3(tc_max3(top, x[c], x[c + 1]), x[c + 2], x[c + 3]);
           }
-          rebase = meet(top > kLimit);
+          rebase = vote(top > kLimit);
+          if (rebase && *gave_up) ok = false, told = true;     // (the same word for all)
           if (!ok) break;
         }
         if (rebase) {
@@ -498,7 +500,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_few_kernel(const __grid_
             wait(kPVDone, (n - 1) & 1);                        // the weights' buffer and O^T are free
             if (ok) tc_fence_after();
             if (me < N) most_of[me] = ordered(-INFINITY);      // (a segment starts with that)
-            meet(false);
+            meet();
             if (!ok) break;
           }
           int most = 0;                  // lane c: of column c (mod C) over the warp's keys
@@ -508,7 +510,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_few_kernel(const __grid_
             most = lane % C == c ? m : most;
           }
           if (lane < C) atomicMax(&most_of[c0 + lane], most);
-          meet(false);
+          meet();
           if (!ok) break;
           if (me < N) {
             const float before = ref[me], top_of = unordered(most_of[me]);
@@ -519,7 +521,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_few_kernel(const __grid_
             ref[me] = now;
             if (now > -INFINITY) neg[me] = -now;
           }
-          meet(false);
+          meet();
           if (!ok) break;
           if (j > 0) {
 #pragma unroll
@@ -531,7 +533,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_few_kernel(const __grid_
             for (int c = 0; c < C; ++c) o[c] *= alpha_of[c0 + c];
             tmem_st<C>(o_addr, o);
             tmem_st_wait();
-            meet(false);                 // the factors are read before the weights take their place
+            meet();                 // the factors are read before the weights take their place
             if (!ok) break;
           }
 #pragma unroll
@@ -576,7 +578,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_few_kernel(const __grid_
       if (!ok) break;
       tc_fence_after();
       if (lane < C) sums[quarter * 64 + c0 + lane] = l[0];     // (the weights were read)
-      meet(false);
+      meet();
       if (!ok) break;
       // a warp: 32 dims of its columns
       float o[C];
@@ -611,11 +613,11 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_few_kernel(const __grid_
         }
       }
       arrive(kItemFree + r % kItemRing);
-      meet(false);                       // the sums and references are read before the next segment's
+      meet();                       // the sums and references are read before the next segment's
     }
     if (!told) {
       if (!ok) *gave_up = 1;
-      meet(false);
+      vote(!ok);
     }
     if (!ok && lane == 0) flag_error(p.err, PKVD_ERR_TIMEOUT);
   }

@@ -285,8 +285,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_tc_kernel(const __grid_c
     // Every wait is bounded; a warp whose wait gives up leaves (the others'
     // then give up in turn).  The two warps of a quarter of a stream's rows meet
     // at a named barrier, which does not give up, but always brings both: each
-    // passes the same ones, a last one when it leaves, and one that gave up says
-    // so at their next meeting, where both leave.  The two streams' warps of a
+    // passes the same ones, a last one when it leaves, where one that gave up asks,
+    // so that both learn of it and leave.  The two streams' warps of a
     // quarter meet at an mbarrier (kJoin), whose wait is bounded too.
     const int g = warp >> 3, half = (warp >> 2) & 1, quarter = warp & 3, row = quarter * 32 + lane;
     const uint32_t lane_base = (uint32_t)(quarter * 32) << 16;
@@ -309,7 +309,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_tc_kernel(const __grid_c
     };
     volatile uint32_t* gave_up = reinterpret_cast<volatile uint32_t*>(gbase + L::kGaveUp) + g * 4 + quarter;
     bool told = false;
-    auto meet = [&](bool mine) -> bool {         // any thread's of the row's two warps?
+    auto vote = [&](bool mine) -> bool {         // any thread's of the row's two warps?
       uint32_t any;
       asm volatile(
           "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 q, %1, 0;\n\t"
@@ -317,8 +317,10 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_tc_kernel(const __grid_c
           : "=r"(any)
           : "r"((uint32_t)mine), "r"(1 + g * 4 + quarter)
           : "memory");
-      if (*gave_up) ok = false, told = true;     // the same word in every lane
       return any != 0;
+    };
+    auto meet = [&] {                            // where nobody asks for anything: one that does gave up
+      if (vote(false)) ok = false, told = true;
     };
     int joins = 0;
     auto join = [&] {                            // the same for the row's four warps of both streams
@@ -428,13 +430,14 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_tc_kernel(const __grid_c
             tc_add2(v[c + 2], v[c + 3], shift0, shift1);
             top = tc_max3(tc_max3(top, v[c], v[c + 1]), v[c + 2], v[c + 3]);
           }
-          const bool rebase = meet(live && top > limit);
+          const bool rebase = vote(live && top > limit);
+          if (rebase && *gave_up) ok = false, told = true;     // (the same word for both)
           if (!ok) break;
           if (rebase) {
             // ---- new references for the rows that passed theirs: the row's two
             // threads agree on the largest score
             xch[half * 32 + lane] = top - less;
-            meet(false);
+            meet();
             if (!ok) break;
             const float most = fmaxf(top - less, xch[(half ^ 1) * 32 + lane]);
             const bool unset = m_ref == -INFINITY;
@@ -463,7 +466,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_tc_kernel(const __grid_c
                 tmem_st32(o_addr + c4 * 32, o);
               }
             }
-            meet(false);                 // both have read
+            meet();                 // both have read
             if (!ok) break;
           }
           uint32_t pk[kThreadKeys / 2];
@@ -491,7 +494,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_tc_kernel(const __grid_c
       tc_fence_after();
       // the row's sum: half 1's part to half 0, the whole and the reference back
       if (half == 1) xch[lane] = l;
-      meet(false);
+      meet();
       if (!ok) break;
       if (half == 0) {
         l += xch[lane];
@@ -499,7 +502,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_tc_kernel(const __grid_c
         xch[32 + lane] = m_ref;
       }
       tc_fence_before();
-      if (two) meet(false);
+      if (two) meet();
       else join();
       if (!ok) break;
       tc_fence_after();
@@ -560,12 +563,12 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_tc_kernel(const __grid_c
       arrive(kOFree);
       arrive(kOFree + 1);
       arrive(kItemFree + r % kItemRing);
-      if (two) meet(false);                      // the exchanged values are read before the next segment's
+      if (two) meet();                      // the exchanged values are read before the next segment's
       else join();
     }
     if (!told) {
       if (!ok) *gave_up = 1;
-      meet(false);
+      vote(!ok);
     }
     if (!ok && lane == 0) flag_error(p.err, PKVD_ERR_TIMEOUT);
   }
