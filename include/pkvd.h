@@ -571,8 +571,12 @@ pkvd_status pkvd_prefill_attention_mod(void* out, const void* q, const pkvd_cach
  *         block_tables as in pkvd_prefill_attention; max_seqlen_q >= every n_i.
  *         Cache rows before every node's window and past k_len_i are never
  *         weighed; drafted rows of the same tree must be stored (finite).
- * Output: out [total_q, num_q_heads, head_dim], 16-byte aligned; rows t >=
- *         cu_seqlens_q[num_seqs] are not written.
+ * Output: out [total_q, num_q_heads, head_dim], 16-byte aligned, not q; rows t
+ *         >= cu_seqlens_q[num_seqs] are not written.  Scores, softmax statistics
+ *         and sums are fp32; PKVD_PATH_TC rounds the softmax weights to the cache's
+ *         type for the product with V (f16 ones keep their bits down to 2^-17 of
+ *         the row's largest; bf16 ones are taken against a reference up to 2^24
+ *         below the largest, so values should be below 2^80 in size).
  * workspace: pkvd_tree_workspace_bytes(...) bytes, 256-byte aligned, no
  *         initialisation; calls that share one must not overlap on the GPU.
  * path:   PKVD_PATH_TC (tcgen05; 16-bit caches with block_size >= 8 whose strides

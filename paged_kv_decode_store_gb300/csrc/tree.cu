@@ -40,8 +40,10 @@ __global__ void __launch_bounds__(kPlanThreads) tree_plan_kernel(const TreePlan 
   __shared__ int64_t near[kNearSeqs];                // pieces before the first sequences
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   if ((int)blockIdx.x == p.num_seqs) {
-    pdl_wait();        // a call before this one may still read the workspace
-    pdl_trigger();
+    // the lengths are inputs: summed up while the kernel before still runs (a call
+    // before this one may still read the workspace: written behind the wait)
+    const bool in_smem = p.num_seqs <= kNearSeqs;
+    if (!in_smem) pdl_wait();
     int64_t running = 0;
     for (int base = 0; base < p.num_seqs; base += kPlanThreads) {
       const int i = base + tid;
@@ -59,15 +61,13 @@ __global__ void __launch_bounds__(kPlanThreads) tree_plan_kernel(const TreePlan 
         if (w < warp) before += warp_sum[w];
         running += warp_sum[w];
       }
-      if (i < p.num_seqs) p.starts[i] = before + upto - mine;
-      if (i < min(p.num_seqs, kNearSeqs)) near[i] = before + upto - mine;
+      if (i < p.num_seqs) (in_smem ? near : p.starts)[i] = before + upto - mine;
       __syncthreads();
     }
-    if (tid == 0) p.starts[p.num_seqs] = running;
     // where the slices begin: in the last sequence with no more pieces before it
-    const int64_t* starts = p.num_seqs <= kNearSeqs ? near : p.starts;
+    const int64_t* starts = in_smem ? near : p.starts;
     const int64_t slices = tree_slices(p, running);
-    for (int c = tid; c < p.grid; c += kPlanThreads) {
+    auto begins = [&](int c) {
       const bool any = c < slices;
       const int64_t f = any ? tree_slice_begin(running, slices, c) : 0;
       int lo = 0, hi = p.num_seqs;
@@ -85,8 +85,16 @@ __global__ void __launch_bounds__(kPlanThreads) tree_plan_kernel(const TreePlan 
       s.n = p.cu_q[lo + 1] - s.q0;
       s.klen = p.cu_k[lo + 1] - p.cu_k[lo];
       s.pad[0] = s.pad[1] = 0;
-      p.slice[c] = s;
-    }
+      return s;
+    };
+    const TreeStart first = begins(tid);
+    if (in_smem) pdl_wait();
+    pdl_trigger();
+    if (in_smem)
+      for (int i = tid; i < p.num_seqs; i += kPlanThreads) p.starts[i] = near[i];
+    if (tid == 0) p.starts[p.num_seqs] = running;
+    if (tid < p.grid) p.slice[tid] = first;
+    for (int c = tid + kPlanThreads; c < p.grid; c += kPlanThreads) p.slice[c] = begins(c);
     return;
   }
   const int i = blockIdx.x;
@@ -313,22 +321,27 @@ template <typename T, int D, int PARTS>
 __global__ void __launch_bounds__(256) tree_merge_kernel(const TreePlan p, T* __restrict__ out) {
   constexpr int ROWS = PARTS == 1 ? kMergeRows : 1, R = PARTS == 1 ? 3 : 8;   // rows, records of each on their way
   __shared__ float part[PARTS == 1 ? 1 : 8 * (D + 2)];
-  pdl_wait();
-  pdl_trigger();
+  // The plan was complete before the kernel with the records let this one start;
+  // its records come behind the wait.
   const int seq = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int units = (p.max_q + p.unit_tokens - 1) / p.unit_tokens;
   const int item = blockIdx.x % (units * p.hkv), group = blockIdx.x / (units * p.hkv);
   const int unit = item / p.hkv, head = item % p.hkv;
-  const int64_t total = p.starts[p.num_seqs], start = p.starts[seq];
+  const int64_t total = __ldcg(reinterpret_cast<const long long*>(p.starts + p.num_seqs));
+  const int64_t start = __ldcg(reinterpret_cast<const long long*>(p.starts + seq));
   const TreeSeq s = tree_seq(p, seq);
-  if (unit >= s.units) return;
-  const int tb = unit * p.unit_tokens, rows = (min(tb + p.unit_tokens, s.n) - tb) * p.group;
+  const int tb = unit * p.unit_tokens, rows = unit < s.units ? (min(tb + p.unit_tokens, s.n) - tb) * p.group : 0;
   const int row0 = PARTS == 1 ? (group * 8 + warp) * ROWS : group;
-  if ((PARTS == 1 ? group * 8 * ROWS : group) >= rows) return;
-  const int64_t slices = tree_slices(p, total);
-  const int64_t f = start + ((int64_t)unit * p.hkv + head) * s.tiles;
-  const int a = (int)tree_slice_of(total, slices, f), b = (int)tree_slice_of(total, slices, f + s.tiles - 1);
-  if (a == b) return;                                    // one CTA had it all
+  int a = 0, b = 0;
+  int64_t slices = 0, f = 0;
+  if ((PARTS == 1 ? group * 8 * ROWS : group) < rows) {
+    slices = tree_slices(p, total);
+    f = start + ((int64_t)unit * p.hkv + head) * s.tiles;
+    a = (int)tree_slice_of(total, slices, f), b = (int)tree_slice_of(total, slices, f + s.tiles - 1);
+  }
+  pdl_wait();
+  pdl_trigger();
+  if (a == b) return;                                    // no rows, or one CTA had them all
   const int slot_a = tree_slice_begin(total, slices, a) == f ? 0 : 1;
   constexpr int Q = D / 4, SUB = 32 / Q;                 // lanes of a row's float4 slices; records a warp takes at once
   const int d4 = lane % Q * 4, sub = lane / Q;

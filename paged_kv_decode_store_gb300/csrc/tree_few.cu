@@ -381,13 +381,13 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_few_kernel(const __grid_
       if (vote(false)) ok = false, told = true;
     };
     // How far a score may pass its reference before that moves.  bf16 weights
-    // have fp32's range: 2^64 times 2^23 keys and values of 2^30 stay within it.
+    // have fp32's range: 2^24 times 2^23 keys and values of 2^80 stay within it.
     // f16 ones end at 2^16 and are normal from 2^-14 on: the first tile's
     // reference lies 3 below its largest score (later tiles usually have larger
     // ones), a later one 7, so weights keep their bits down to 2^-17 of the row's
     // largest at least.
     constexpr bool kNarrow = std::is_same<T, __half>::value;
-    constexpr float kLift = kNarrow ? 7.f : 0.f, kFirst = kNarrow ? 4.f : 0.f, kLimit = kNarrow ? 15.f : 64.f;
+    constexpr float kLift = kNarrow ? 7.f : 0.f, kFirst = kNarrow ? 4.f : 0.f, kLimit = kNarrow ? 15.f : 24.f;
     int n = 0;                                   // tiles so far, of all segments
     for (int r = 0; ok; ++r) {
       ok = __all_sync(FULL_MASK, wait_item(&bars[kItemFull + r % kItemRing], (r / kItemRing) & 1));

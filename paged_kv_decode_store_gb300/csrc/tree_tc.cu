@@ -331,7 +331,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_tc_kernel(const __grid_c
     // How far a score may pass its reference before that moves: tree_few.cu.  f16
     // weights keep their bits down to 2^-21 of the row's largest.
     constexpr bool kNarrow = std::is_same<T, __half>::value;
-    constexpr float kLift = kNarrow ? 7.f : 0.f, kLimit = kNarrow ? 15.f : 64.f;
+    constexpr float kLift = kNarrow ? 7.f : 0.f, kLimit = kNarrow ? 15.f : 24.f;
     int n = 0;                                   // this stream's K tiles so far, of all segments
     for (int r = 0; ok; ++r) {
       ok = __all_sync(FULL_MASK, wait_item(&bars[kItemFull + r % kItemRing], (r / kItemRing) & 1));

@@ -241,7 +241,7 @@ def test_tree_attention_refusals(pk):
     assert go() == OK and go(seqs=3, total=0) == OK and go(seqs=3, max_q=0) == OK
     for kw in (dict(seqs=-1), dict(total=-1), dict(max_q=-1), dict(window=-1), dict(scale=float("nan")), dict(path=9), dict(hq=0),
                dict(mod=_capi.PkvdScoreMod(-1.0, None, None)), dict(mod=_capi.PkvdScoreMod(0.0, None, P)),
-               dict(cache=cache(_capi, k_base=0)), dict(seqs=2, q=None), dict(seqs=2, parents=None), dict(seqs=2, max_blocks=0)):
+               dict(cache=cache(_capi, k_base=0)), dict(seqs=2, q=None), dict(seqs=2, parents=None), dict(seqs=2, max_blocks=0), dict(seqs=2)):
         assert go(**kw) == INVALID, kw
     for kw in (dict(hq=44), dict(hq=8 * 129), dict(max_q=257), dict(seqs=65536), dict(path=2), dict(cache=cache(_capi, head_dim=96)),
                dict(cache=cache(_capi, block_size=24)), dict(seqs=2, q=P + 8), dict(seqs=2, out=P + 4)):
