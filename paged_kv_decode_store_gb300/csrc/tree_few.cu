@@ -122,10 +122,10 @@ __device__ __forceinline__ int tile_at(int kt_last, int n, int late, int j) {
 }
 
 // K or V of every segment (a warp each): lane s copies 8 to 128 rows of a tile.  A
-// V tile with rows that are not read lands on a barrier of its own (kVCut) and is
-// released with those rows zeroed, so that they never weigh in.
-template <typename L, bool IS_V>
-__device__ __forceinline__ void copy_tiles(const TcTree& p, uint64_t* bars, uint32_t base, const Item* ring_items, int lane) {
+// V tile with keys that not every row sees lands on a barrier of its own (kVCut)
+// and is released when tidy_values has seen to it.
+template <typename T, typename L, bool IS_V>
+__device__ __forceinline__ void copy_tiles(const TcTree& p, uint64_t* bars, uint32_t base, Item* ring_items, int lane) {
   constexpr int H = L::kHalves, kStages = IS_V ? L::kVStages : L::kKStages;
   constexpr int full = IS_V ? kVFull : kKFull, empty = IS_V ? kVEmpty : kKEmpty;
   const CUtensorMap* map = IS_V ? &p.tmap_v : &p.tmap_k;
@@ -143,8 +143,9 @@ __device__ __forceinline__ void copy_tiles(const TcTree& p, uint64_t* bars, uint
   for (int r = 0; ok; ++r) {
     ok = __all_sync(FULL_MASK, wait_item(&bars[kItemFull + r % kItemRing], (r / kItemRing) & 1));
     if (!ok) break;
-    const Item& cur = ring_items[r % kItemRing];
+    Item& cur = ring_items[r % kItemRing];
     if (cur.n < 0) break;
+    const Sight sight(cur, p.plan.window);
     const int32_t* table = p.tables + (int64_t)cur.seq * p.max_blocks;
     const int n = cur.n, hk = cur.hk, lo = cur.lo, hi = cur.hi, kt_last = cur.kt_last, late = cur.late;
     auto fetch = [&](int t) -> int {
@@ -159,7 +160,7 @@ __device__ __forceinline__ void copy_tiles(const TcTree& p, uint64_t* bars, uint
       wait(empty + stg, par);
       if (!ok) break;
       const int kbase = tile_at(kt_last, n, late, t) * kTcKeys, ks = kbase + lane * p.seg_rows;
-      const bool cut = IS_V && (kbase < lo || kbase + kTcKeys - 1 > hi);
+      const bool cut = IS_V && !sight.whole(kbase);
       uint64_t* bar = &bars[(cut ? kVCut : full) + stg];
       const uint32_t tile = ring + stg * H * kHalf, dst = tile + lane * box;
       const bool good = (uint32_t)b[0] < p.block_limit;
@@ -188,12 +189,7 @@ __device__ __forceinline__ void copy_tiles(const TcTree& p, uint64_t* bars, uint
         wait(kVCut + stg, (landed >> stg) & 1);
         landed ^= 1 << stg;
         if (!ok) break;
-        for (int rr = lane; rr < kTcKeys; rr += 32) {
-          const int kp = kbase + rr;
-          if (kp >= lo && kp <= hi) continue;
-          for (int h = 0; h < H; ++h)
-            for (int c = 0; c < 8; ++c) st_shared_v4(tile + h * kHalf + rr * 128 + c * 16, make_uint4(0u, 0u, 0u, 0u));
-        }
+        if (tidy_values<T, H>(tile, kbase, sight, lane) && lane == 0) cur.odd = 1;
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars[kVFull + stg]);
@@ -257,9 +253,9 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_few_kernel(const __grid_
   // registers: 512 x 104 + 128 x 56 = 60416 of the 61440 that 640 threads start with
   if (warp >= kWarps) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
   if (warp == kKvWarp) {
-    copy_tiles<L, false>(p, bars, base, ring_items, lane);
+    copy_tiles<T, L, false>(p, bars, base, ring_items, lane);
   } else if (warp == kVWarp) {
-    copy_tiles<L, true>(p, bars, base, ring_items, lane);
+    copy_tiles<T, L, true>(p, bars, base, ring_items, lane);
   } else if (warp == kQWarp) {
     tree_segments<L>(p, bars, base, ring_items, lane);
   } else if (warp == kMmaWarp) {
@@ -588,6 +584,16 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_few_kernel(const __grid_
       }
       tc_fence_before();
       arrive(kOFree);
+      if (*static_cast<const volatile int*>(&it.odd) && quarter * 32 < D) {
+        odd_keys(p, it, Sight(it, pl.window), kt_last - all + 1, kt_last, [&](int k, const uint16_t* v) {
+          const float x = odd_value<T>(v + krow);
+          uint32_t see = 0u;
+          if (k >= cached) see = pl.anc[((int64_t)it.seq * pl.max_q + k - cached) * 2 + c0 / 32] >> (c0 & 31);
+#pragma unroll
+          for (int c = 0; c < C; ++c)
+            if (k >= cached ? (see >> c) & 1u : pos[c0 + c] < k + pl.window) o[c] += x;
+        });
+      }
       const int64_t rec0 = (int64_t)slot * pl.unit_rows;
       // lane c: the sum of column c (mod C), then one over it
       const int mycol = c0 + lane % C;

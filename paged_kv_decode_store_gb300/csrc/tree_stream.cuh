@@ -46,6 +46,8 @@ struct TcTree {
   float scale_log2;
   ScoreMod mod;
   float poly[4], poly_range;     // cap_poly
+  const uint16_t* values;        // V of the cache, and its strides in elements
+  int64_t block_stride, token_stride, head_stride;
   int wide_out;                  // out is 32-byte aligned: stores of 32 bytes
   int32_t* err;
 };
@@ -55,11 +57,96 @@ struct __align__(16) Item {
   int seq, hk, q0, tokens;       // q0: the unit's first row of q
   int node0, cached, lo, hi;     // node0: its place in the plan's arrays; keys outside [lo, hi] are not read
   int kt_last, n, slot, two;     // two Q tiles?
-  int qbuf, late, pad[2];        // where a single Q tile lies; more than the unit's last tile, and that
+  int qbuf, late;                // where a single Q tile lies; more than the unit's last tile, and that
+  int odd, pad;                  // set by the copies of V: values that are no numbers (tidy_values)
 };
 constexpr uint32_t kItemBytes = sizeof(Item) * kItemRing;
 
 __device__ __forceinline__ int window_first(int c, int window) { return (window > 0 && c > window) ? c - window : 0; }
+
+// Which keys no row sees, and which ones perhaps some: drafted ones, and those
+// that a window has left behind for some of the rows.
+struct Sight {
+  int lo, hi, cached, edge;      // keys outside [lo, hi]: no row; cached keys from `edge` on: all rows
+  __device__ Sight(const Item& it, int window)
+      : lo(it.lo), hi(it.hi), cached(it.cached), edge(window_first(it.hi + 1, window)) {}
+  __device__ bool whole(int kbase) const {     // of a tile: all rows see every key
+    return kbase >= lo && kbase >= edge && kbase + kTcKeys <= min(cached, hi + 1);
+  }
+};
+
+__device__ __forceinline__ uint4 ld_shared_v4(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
+  return v;
+}
+
+// A V tile (H boxes of 64 dims), by a warp, where not all rows see every key: a
+// weight of 0 times an infinity or a NaN would be a NaN.  Rows that no row of Q
+// sees become zeros; in those that some see, every element that is no finite
+// number does.  Returns whether there was one: the sums get it afterwards, where
+// it is seen (odd_keys).
+template <typename T, int H>
+__device__ __forceinline__ bool tidy_values(uint32_t tile, int kbase, const Sight& s, int lane) {
+  constexpr uint32_t kExp = std::is_same<T, __half>::value ? 0x7c007c00u : 0x7f807f80u;
+  constexpr uint32_t kOne = std::is_same<T, __half>::value ? 0x04000400u : 0x00800080u;
+  const int first = max(s.lo - kbase, 0), end = min(s.hi - kbase + 1, kTcKeys);
+  bool odd = false;
+#pragma unroll
+  for (int h = 0; h < H; ++h) {
+    const uint32_t at = tile + h * kHalf;      // a key: 128 bytes, whose order does not matter here
+    for (int i = lane; i < first * 8; i += 32) st_shared_v4(at + i * 16, make_uint4(0u, 0u, 0u, 0u));
+    for (int i = end * 8 + lane; i < kTcKeys * 8; i += 32) st_shared_v4(at + i * 16, make_uint4(0u, 0u, 0u, 0u));
+    auto look = [&](int from, int to) {
+      uint32_t any = 0u;
+#pragma unroll 4
+      for (int i = from * 8 + lane; i < to * 8; i += 32) {
+        const uint4 x = ld_shared_v4(at + i * 16);          // (a carry into the sign: all ones in the exponent)
+        any |= ((x.x & kExp) + kOne) | ((x.y & kExp) + kOne) | ((x.z & kExp) + kOne) | ((x.w & kExp) + kOne);
+      }
+      if (!(any & 0x80008000u)) return;
+      for (int i = from * 8 + lane; i < to * 8; i += 32) {
+        const uint4 x = ld_shared_v4(at + i * 16);
+        const uint32_t a = __vcmpeq2(x.x & kExp, kExp), b = __vcmpeq2(x.y & kExp, kExp),
+                       c = __vcmpeq2(x.z & kExp, kExp), d = __vcmpeq2(x.w & kExp, kExp);
+        if (a | b | c | d) {
+          odd = true;
+          st_shared_v4(at + i * 16, make_uint4(x.x & ~a, x.y & ~b, x.z & ~c, x.w & ~d));
+        }
+      }
+    };
+    look(first, min(s.edge - kbase, end));
+    look(max(s.cached - kbase, first), end);
+  }
+  return __any_sync(FULL_MASK, odd);
+}
+
+// The keys of tiles [kt0, kt1] that tidy_values looks at, for sums that miss a
+// value (softmax weights are above 0, so an infinity or a NaN goes into them as it
+// is): f(key, its row of V).
+template <typename F>
+__device__ __forceinline__ void odd_keys(const TcTree& p, const Item& it, const Sight& s, int kt0, int kt1, F f) {
+  const int k0 = max(s.lo, kt0 * kTcKeys), k1 = min(s.hi, kt1 * kTcKeys + kTcKeys - 1);
+#pragma unroll 1
+  for (int k = k0; k <= k1; ++k) {
+    if (k >= s.edge && k < s.cached) {         // on to the drafted ones
+      k = max(k, min(s.cached, k1 + 1) - 1);
+      continue;
+    }
+    const uint32_t b = (uint32_t)__ldg(p.tables + (int64_t)it.seq * p.max_blocks + (k >> p.block_shift));
+    if (b >= p.block_limit) continue;
+    f(k, p.values + (int64_t)b * p.block_stride + (int64_t)(k & (p.block_size - 1)) * p.token_stride +
+             (int64_t)it.hk * p.head_stride);
+  }
+}
+template <typename T>
+__device__ __forceinline__ float odd_value(const uint16_t* at) {   // 0 for a finite number
+  constexpr uint32_t kExp = std::is_same<T, __half>::value ? 0x7c00u : 0x7f80u;
+  const uint16_t x = *at;
+  T t;
+  memcpy(&t, &x, 2);
+  return (x & kExp) == kExp ? DT<T>::to_f(t) : 0.f;
+}
 
 // Barriers and what a kernel's layout L says of its arrivals.
 template <typename L>
@@ -77,10 +164,10 @@ __device__ __forceinline__ void tree_init_barriers(uint64_t* bars) {
 }
 
 // K and V (one warp).  Lane s copies segment s of a tile; K runs kAhead tiles
-// ahead of V.  A V tile with rows that are not read lands on a barrier of its own
-// (kVCut) and is released with those rows zeroed, so that they never weigh in.
-template <typename L>
-__device__ __forceinline__ void tree_copy_kv(const TcTree& p, uint64_t* bars, uint32_t base, const Item* ring_items, int lane) {
+// ahead of V.  A V tile with keys that not every row sees lands on a barrier of
+// its own (kVCut) and is released when tidy_values has seen to it.
+template <typename T, typename L>
+__device__ __forceinline__ void tree_copy_kv(const TcTree& p, uint64_t* bars, uint32_t base, Item* ring_items, int lane) {
   constexpr int H = L::kHalves, kKStages = L::kKStages, kVStages = L::kVStages;
   constexpr int kAhead = kKStages - 2;
   const uint32_t box = (uint32_t)p.seg_rows * 128u;
@@ -126,10 +213,11 @@ __device__ __forceinline__ void tree_copy_kv(const TcTree& p, uint64_t* bars, ui
   for (int r = 0; ok; ++r) {
     ok = __all_sync(FULL_MASK, wait_item(&bars[kItemFull + r % kItemRing], (r / kItemRing) & 1));
     if (!ok) break;
-    const Item& cur = ring_items[r % kItemRing];
+    Item& cur = ring_items[r % kItemRing];
     if (cur.n < 0) break;
     const int32_t* table = p.tables + (int64_t)cur.seq * p.max_blocks;
     const int n = cur.n, hk = cur.hk, lo = cur.lo, hi = cur.hi, kt_last = cur.kt_last;
+    const Sight sight(cur, p.plan.window);
     auto key_of = [&](int t) { return (kt_last - t) * kTcKeys + lane * p.seg_rows; };
     auto fetch = [&](int t) -> int {
       const int ks = key_of(t);
@@ -153,19 +241,14 @@ __device__ __forceinline__ void tree_copy_kv(const TcTree& p, uint64_t* bars, ui
       wait(kVEmpty + vstg, vpar);
       if (!ok) break;
       const int kbase = (kt_last - t) * kTcKeys;
-      const bool cut = kbase < lo || kbase + kTcKeys - 1 > hi;
+      const bool cut = !sight.whole(kbase);
       const uint32_t dst = base + L::kV + vstg * H * kHalf;
       copy(&p.tmap_v, dst, (cut ? kVCut : kVFull) + vstg, kbase + lane * p.seg_rows, hk, b[0]);
       if (cut) {
         wait(kVCut + vstg, (landed >> vstg) & 1);
         landed ^= 1 << vstg;
         if (!ok) break;
-        for (int rr = lane; rr < kTcKeys; rr += 32) {
-          const int kp = kbase + rr;
-          if (kp >= lo && kp <= hi) continue;
-          for (int h = 0; h < H; ++h)
-            for (int c = 0; c < 8; ++c) st_shared_v4(dst + h * kHalf + rr * 128 + c * 16, make_uint4(0u, 0u, 0u, 0u));
-        }
+        if (tidy_values<T, H>(dst, kbase, sight, lane) && lane == 0) cur.odd = 1;
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars[kVFull + vstg]);
@@ -221,7 +304,8 @@ __device__ __forceinline__ void tree_segments(const TcTree& p, uint64_t* bars, u
         it.kt_last = walk.s.lo_tile + g.t1 - 1;
         it.n = g.t1 - g.t0;
         it.slot = g.slot;
-      it.late = g.t1 == walk.s.tiles && it.n > 1;
+        it.late = g.t1 == walk.s.tiles && it.n > 1;
+        it.odd = 0;
         it.two = it.tokens > p.tile_tokens;
         it.qbuf = turn;
         if (!it.two && L::kQBufs == 2) turn ^= 1;
@@ -257,6 +341,10 @@ inline bool tree_tc_params(const TreeArgs& a, const TreePlan& plan, int tile_tok
       !encode_cache_map(&prm->tmap_v, c.v_base, c, prm->seg_rows) ||
       !encode_q_map(&prm->tmap_q, a.q, c.dtype, c.head_dim, a.num_q_heads, a.total_q, plan.group, tile_tokens))
     return false;
+  prm->values = static_cast<const uint16_t*>(c.v_base);
+  prm->block_stride = c.block_stride;
+  prm->token_stride = c.token_stride;
+  prm->head_stride = c.head_stride;
   prm->out = a.out;
   prm->tables = a.block_tables;
   prm->max_blocks = a.max_blocks_per_seq;

@@ -141,7 +141,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_tc_kernel(const __grid_c
   // registers: 512 x 104 + 128 x 56 = 60416 of the 61440 that 640 threads start with
   if (warp >= kKvWarp) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
   if (warp == kKvWarp) {
-    tree_copy_kv<L>(p, bars, base, ring_items, lane);
+    tree_copy_kv<T, L>(p, bars, base, ring_items, lane);
   } else if (warp == kQWarp) {
     tree_segments<L>(p, bars, base, ring_items, lane);
   } else if (warp == kMmaWarp || warp == kMmaWarp1) {
@@ -518,6 +518,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_tc_kernel(const __grid_c
         sum = l0 * f0 + l1 * f1;
         has1 = all > 1;
       }
+      const bool odd = *static_cast<const volatile int*>(&it.odd);
       const int cols = two ? D / 2 : D / 4, col0 = two ? half * (D / 2) : (2 * g + half) * (D / 4);
       const uint32_t o0 = tmem + lane_base + kColO + (two ? g * D : 0) + col0, o1 = tmem + lane_base + kColO + D + col0;
       const float inv = slot >= 0 ? 1.f : sum > 0.f ? 1.f / sum : 0.f;
@@ -541,6 +542,15 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_tc_kernel(const __grid_c
           tmem_ld_wait();
 #pragma unroll
           for (int e = 0; e < 16; ++e) o[e] *= f0;
+        }
+        if (odd) {
+          const int kt_last = it.kt_last;
+          odd_keys(p, it, Sight(it, pl.window), kt_last - all + 1, kt_last, [&](int k, const uint16_t* at) {
+            const int u = k - cached;
+            if (u >= 0 ? !((anc[u >> 5] >> (u & 31)) & 1u) : k < wr) return;
+#pragma unroll
+            for (int e = 0; e < 16; ++e) o[e] += odd_value<T>(at + col0 + c + e);
+          });
         }
         if (!live) continue;
         if (slot >= 0) {

@@ -305,3 +305,56 @@ def test_accept_errors_in_device_data():
     err.zero_()
     _, _, counts, _ = pk.tree_accept(*args(one - 1, [0, 3, 301], [0, 3, 301]), err=err)           # past the rows
     assert err.item() == pk.ERR_CONTEXT and counts.tolist() == [1, 0]
+
+
+@pytest.mark.parametrize("case", [("bf16", 48, 8, 128, 16, 3), ("f16", 4, 2, 64, 64, 3), ("bf16", 64, 2, 128, 16, 3),
+                                  ("f16", 80, 2, 64, 16, 3), ("bf16", 8, 2, 64, 16, 1), ("f32", 4, 2, 128, 16, 1)],
+                         ids=lambda c: "-".join(map(str, c)))
+@pytest.mark.parametrize("window", [0, 20])
+def test_values_that_are_no_numbers(case, window):
+    """A NaN or an infinity in the V row of a draft, or of a token that a window has left behind for some, reaches
+    the nodes that see it in its own column alone, and no other node at all; in K, a draft nobody else sees."""
+    pk = require_gpu()
+    dt, hq, hkv, d, bs, path = case
+    dt, G = DT[dt], hq // hkv
+    rng = np.random.default_rng(11)
+    qlen, cached = [9, 5, 40, 1, 20], [300, 0, 121, 64, 700]
+    klen = [c + n for c, n in zip(cached, qlen)]
+    kc, vc, tables, _ = cache_of(klen, hkv, d, bs, dt, 12)
+    trees = [a_tree(n, k, rng) for n, k in zip(qlen, ["tree", "star", "forest", "tree", "chain"])]
+    q = torch.randn(sum(qlen), hq, d, generator=torch.Generator().manual_seed(13)).to(dt).to(DEV)
+
+    def go(k, v):
+        return pk.tree_attention(q, k, v, tables, cumulative(qlen), cumulative(klen), ints([u for t in trees for u in t]),
+                                 max(qlen), d ** -0.5, window=window, path=path)
+
+    plain = go(kc, vc).float()
+    want, k2, v2 = plain.clone(), kc.clone(), vc.clone()
+    host = tables.cpu()
+    first = np.cumsum([0] + qlen)
+
+    def positions(i):                       # keys that node j sees
+        for j in range(qlen[i]):
+            up = oracle.drafts.path_of(trees[i], j)
+            pos = cached[i] + len(up) - 1
+            keys = [(c, c) for c in range(cached[i])] + [(cached[i] + u, cached[i] + n) for n, u in enumerate(up)]
+            yield j, {key for key, at in keys if not window or at > pos - window}
+
+    for i in range(len(qlen)):
+        sees = dict(positions(i))
+        for n, bad in enumerate([float("inf"), float("nan"), float("-inf"), float("inf")]):
+            key = cached[i] + int(rng.integers(0, qlen[i])) if n < 3 or not window else max(0, cached[i] - window + 4)
+            hk, col = int(rng.integers(0, hkv)), int(rng.integers(0, d))
+            v2[host[i, key // bs], key % bs, hk, col] = bad
+            for j, seen in sees.items():
+                if key in seen:
+                    want[first[i] + j, hk * G:(hk + 1) * G, col] += bad
+        leaf = qlen[i] - 1                  # the last node: nobody's ancestor
+        key = cached[i] + leaf
+        k2[host[i, key // bs], key % bs, 0, 3] = float("nan")
+        want[first[i] + leaf, :G] = float("nan")
+    assert torch.equal(plain.isfinite().all(), torch.tensor(True, device=DEV)) and not want.isfinite().all()
+    got = go(k2, v2).float()
+    number = want.isfinite()
+    assert torch.equal(got[number], plain[number])
+    assert torch.equal(got.isnan(), want.isnan()) and torch.equal(got[~want.isnan()], want[~want.isnan()])
