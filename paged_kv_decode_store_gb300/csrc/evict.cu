@@ -7,17 +7,23 @@
 // order, the weights that stay close up beside them, zeros behind.
 //
 // A CTA a row, two on an SM.  The weights between are read once into shared
-// memory (24,576 of them; what is beyond is read again for each pass) as whole
-// numbers in the order of the numbers, and looked at five times: a radix
-// selection of the last one that stays (11, 11 and 10 bits, a histogram each, two
-// copies of it so that lanes with equal digits wait less for one another), a
-// count and the writing, in order.  Every warp has a contiguous part of the row,
-// so the order needs prefix sums over warps once and ballots within one, no
-// barrier an element.  Exact: whole-number arithmetic on the weights' bits.
+// memory (22,528 of them; what is beyond is read again for each pass) as whole
+// numbers in the order of the numbers, and looked at three times: for a histogram
+// of their first 11 bits (two copies of it, so that lanes with equal digits wait
+// less for one another), which says what digit the last one that stays has; for
+// a list of the keys with that digit, in which the other 11 and 10 bits are found
+// the same way (rows whose list would be longer than its place look at all of
+// them again); and for the writing, in order.  Every warp has a contiguous part of
+// the row, so the order needs prefix sums over warps once and ballots within one,
+// no barrier an element.  Exact: whole-number arithmetic on the weights' bits.
 //
-// The loops are short code on purpose: a form with half of the weights in
-// registers, its passes written out, took 14 us for a row of 50 (and 70 us for 64
-// x 8 rows of 4,096 to 32,768): it waited for instructions.
+// Bound by instructions (59 % of the issue slots) and the barriers between the
+// passes: 64 x 8 rows of 4,096 to 32,768 take 51 us, of which their bytes are 15;
+// 62 with every pass over the whole row and rows in order.  The loops are short
+// code on purpose: a form with half of the weights in registers, its passes
+// written out, took 14 us for a row of 50 instead of 8: it waited for instructions.
+#include <climits>
+
 #include "common.cuh"
 #include "launch.h"
 
@@ -26,10 +32,14 @@ namespace pkvd {
 namespace {
 
 constexpr int kThreads = 512, kWarps = kThreads / 32;
-constexpr int kPer = 48;                                   // weights of a thread in shared memory
+constexpr int kPer = 44;                                   // weights of a thread in shared memory
 constexpr int kBins = 2048, kCopies = 2;
+constexpr int kList = 256;                                 // a warp's keys with the first digit (behind one copy)
 constexpr int kStack = kBins * kCopies / kWarps / 2;       // positions and weights that a warp gathers
-constexpr int kSmemBytes = kPer * kThreads * 4 + kBins * kCopies * 4;
+constexpr int kHist = kBins + kWarps * kList;              // words of all of these, one use after the other
+static_assert(kHist >= kBins * kCopies, "two copies of the histogram");
+constexpr int kRanked = 256;
+constexpr int kSmemBytes = (kPer * kThreads + kHist) * 4;
 
 // A weight's bits in the order of the numbers, and back.  Any NaN becomes the quiet
 // one, above all numbers; 0 is left for no weight.
@@ -64,7 +74,7 @@ struct Part {
   }
   // 0 where there is none
   __device__ uint32_t read(int i) const { return (int64_t)i * 32 < mine ? ordered_bits(__float_as_uint(src[(int64_t)i * 32])) : 0u; }
-  __device__ void fetch() {
+  __device__ void ask() const {
     const int n = min(steps, kPer);
 #pragma unroll 4
     for (int i = 0; i < n; ++i) {
@@ -72,9 +82,21 @@ struct Part {
         asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(held + i * kThreads)), "l"(src + i * 32)
                      : "memory");
     }
-    asm volatile("cp.async.commit_group;\n\tcp.async.wait_group 0;" ::: "memory");
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  }
+  // what was asked for has come: f(bits in order) of every one
+  template <typename F>
+  __device__ void take_in(F f) const {
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+    const int n = min(steps, kPer);
 #pragma unroll 4
-    for (int i = 0; i < n; ++i) held[i * kThreads] = i * 32 < mine ? ordered_bits(held[i * kThreads]) : 0u;
+    for (int i = 0; i < n; ++i) {
+      const uint32_t x = i * 32 < mine ? ordered_bits(held[i * kThreads]) : 0u;
+      held[i * kThreads] = x;
+      f(x);
+    }
+#pragma unroll 4
+    for (int i = kPer; i < steps; ++i) f(read(i));
   }
   // f(step, bits in order), every lane of the warp alike
   template <typename F>
@@ -93,15 +115,39 @@ struct Part {
   }
 };
 
-__global__ void __launch_bounds__(kThreads, 2) evict_select_kernel(const EvictArgs a) {
+// The sequence with the y-th longest context (of equal ones the first).
+// len: kRanked + 1 words, in memory used later (more of it would leave one CTA on an SM).
+__device__ __forceinline__ int by_length(const int32_t* __restrict__ lens, int n, int y, int* len) {
+  const int tid = threadIdx.x;
+  if (tid < kRanked) len[tid] = tid < n ? lens[tid] : INT_MIN;
+  __syncthreads();
+  if (tid < n) {
+    const int mine = len[tid];
+    int rank = 0;
+    for (int j = 0; j < n; j += 4) {
+      const int4 x = *reinterpret_cast<const int4*>(len + j);
+      rank += (x.x > mine || (x.x == mine && j < tid)) + (x.y > mine || (x.y == mine && j + 1 < tid)) +
+              (x.z > mine || (x.z == mine && j + 2 < tid)) + (x.w > mine || (x.w == mine && j + 3 < tid));
+    }
+    if (rank == y) len[kRanked] = tid;
+  }
+  __syncthreads();
+  const int at = len[kRanked];
+  __syncthreads();
+  return at;
+}
+
+__global__ void __launch_bounds__(kThreads, 2) evict_select_kernel(const EvictArgs a, int ranked) {
   extern __shared__ __align__(16) uint32_t sm[];
   __shared__ int warp_sum[2][kWarps];
   __shared__ uint32_t found_digit;
   __shared__ int found_left;
-  uint32_t* const hist = sm;                               // [kBins][kCopies]
+  uint32_t* const hist = sm;                               // [kBins][copies]
+  const int seq = ranked ? by_length(a.context_lens, (int)gridDim.y, (int)blockIdx.y, reinterpret_cast<int*>(sm)) : (int)blockIdx.y;
   pdl_wait();          // (and no early trigger: counts are the next call's lengths, which it reads before it waits)
-  const int h = blockIdx.x, seq = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  uint32_t* const held = sm + kBins * kCopies + tid;
+  const int h = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  uint32_t* const held = sm + kHist + tid;
+  uint32_t* const list = sm + kBins + warp * kList;
   int c = a.context_lens[seq];
   if (c < 0 || c > a.length) {
     if (tid == 0 && h == 0) flag_error(a.err, PKVD_ERR_CONTEXT);
@@ -137,7 +183,10 @@ __global__ void __launch_bounds__(kThreads, 2) evict_select_kernel(const EvictAr
   row.left = count - sink - recent;
   const bool selects = row.left > 0;
   Part part(row, held, warp, lane);
-  if (selects) part.fetch();
+  if (selects) {
+    part.ask();
+    for (int i = tid; i < kBins * kCopies / 4; i += kThreads) reinterpret_cast<uint4*>(hist)[i] = make_uint4(0, 0, 0, 0);
+  }
   // rows that are read again while they are written in place: the weights follow
   // when every position is known
   const bool later = row.wo == row.w && selects && row.hi - row.lo > kPer * kThreads;
@@ -152,31 +201,53 @@ __global__ void __launch_bounds__(kThreads, 2) evict_select_kernel(const EvictAr
   if (selects) {
     int left = row.left;
     uint32_t kth = 0;                  // the last key that stays, so far its upper bits
+    int more = 0, tie = 0;             // of this thread, then of the warp: larger keys, equal ones
+    int fill = 0;                      // of this warp's list
+    bool listed = false;               // the keys with the first digit are there
 #pragma unroll 1
     for (int pass = 0; pass < 3; ++pass) {
       const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, above = pass == 0 ? 31 : pass == 1 ? 21 : 10;
       const uint32_t digits = pass == 2 ? 1023u : 2047u;
-      for (int i = tid; i < kBins * kCopies / 4; i += kThreads) reinterpret_cast<uint4*>(hist)[i] = make_uint4(0, 0, 0, 0);
-      __syncthreads();
       uint32_t* const bins = hist + (lane & (kCopies - 1));
       // (no weight: key 0, the lowest digit, below every one that is looked for; it
       // counts nowhere, so that rows of few do not pile up there)
-      part.each([&](int, uint32_t x) {
-        const uint32_t k = key_of(x);
-        if (k != 0u && (pass == 0 || k >> above == kth >> above)) atomicAdd(bins + ((k >> shift) & digits) * kCopies, 1u);
-      });
+      if (pass == 0) {
+        __syncthreads();               // (emptied above)
+        part.take_in([&](uint32_t x) {
+          const uint32_t k = key_of(x);
+          if (k != 0u) atomicAdd(bins + (k >> 21) * kCopies, 1u);
+        });
+      } else {
+        for (int i = tid; i < (listed ? kBins / 4 : kBins * kCopies / 4); i += kThreads)
+          reinterpret_cast<uint4*>(hist)[i] = make_uint4(0, 0, 0, 0);
+        __syncthreads();
+        if (listed) {
+          for (int i = lane; i < fill; i += 32) {
+            const uint32_t k = list[i];
+            if (k >> above == kth >> above) atomicAdd(hist + ((k >> shift) & digits), 1u);
+          }
+        } else {
+          part.each([&](int, uint32_t x) {
+            const uint32_t k = key_of(x);
+            if (k != 0u && k >> above == kth >> above) atomicAdd(bins + ((k >> shift) & digits) * kCopies, 1u);
+          });
+        }
+      }
       __syncthreads();
       // from the largest digit down: thread t has the kEach bins below kBins - kEach t
       constexpr int kEach = kBins / kThreads;
+      static_assert(kEach == 4 && kCopies == 2, "two loads of two bins, or one of four");
       int bin[kEach], sum = 0;
-      const uint4* mine = reinterpret_cast<const uint4*>(hist) + (kBins / kEach - 1 - tid) * (kEach * kCopies / 4);
-#pragma unroll
-      for (int i = 0; i < kEach / 2; ++i) {                // (two bins of two copies each)
-        const uint4 x = mine[kEach / 2 - 1 - i];
-        bin[2 * i] = (int)(x.z + x.w);
-        bin[2 * i + 1] = (int)(x.x + x.y);
-        sum += (int)(x.x + x.y + x.z + x.w);
+      const int top = kBins / kEach - 1 - tid;
+      if (listed) {
+        const uint4 x = reinterpret_cast<const uint4*>(hist)[top];
+        bin[0] = (int)x.w, bin[1] = (int)x.z, bin[2] = (int)x.y, bin[3] = (int)x.x;
+      } else {
+        const uint4 x = reinterpret_cast<const uint4*>(hist)[2 * top + 1], y = reinterpret_cast<const uint4*>(hist)[2 * top];
+        bin[0] = (int)(x.z + x.w), bin[1] = (int)(x.x + x.y), bin[2] = (int)(y.z + y.w), bin[3] = (int)(y.x + y.y);
       }
+#pragma unroll
+      for (int i = 0; i < kEach; ++i) sum += bin[i];
       int upto = sum;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -201,14 +272,33 @@ __global__ void __launch_bounds__(kThreads, 2) evict_select_kernel(const EvictAr
       __syncthreads();
       kth |= found_digit << shift;
       left = found_left;
+      if (pass > 0) continue;
+      // The keys with that digit, usually a few in a hundred, on a list: the other
+      // two digits are looked for there.  (Digit 0 has what is no weight.)
+      const uint32_t first = found_digit;
+      if (first != 0u)
+        part.each([&](int, uint32_t x) {
+          const uint32_t k = key_of(x), d = k >> 21;
+          more += d > first;
+          const uint32_t b = __ballot_sync(FULL_MASK, d == first);
+          if (b == 0u) return;
+          const int to = fill + __popc(b & ((1u << lane) - 1u));
+          if (d == first && to < kList) list[to] = k;
+          fill += __popc(b);
+        });
+      listed = !__syncthreads_or(first == 0u || fill > kList);
     }
     // in order: what is larger, and of those equal to the last one the first `left`
-    int more = 0, tie = 0;             // of this thread, then of the warp
-    part.each([&](int, uint32_t x) {
-      const uint32_t k = key_of(x);
-      more += k > kth;
-      tie += k == kth;
-    });
+    if (listed) {
+      for (int i = lane; i < fill; i += 32) more += list[i] > kth, tie += list[i] == kth;
+    } else {
+      more = 0;
+      part.each([&](int, uint32_t x) {
+        const uint32_t k = key_of(x);
+        more += k > kth;
+        tie += k == kth;
+      });
+    }
     more = __reduce_add_sync(FULL_MASK, more);
     tie = __reduce_add_sync(FULL_MASK, tie);
     if (lane == 0) warp_sum[0][warp] = more, warp_sum[1][warp] = tie;
@@ -221,7 +311,7 @@ __global__ void __launch_bounds__(kThreads, 2) evict_select_kernel(const EvictAr
     // what stays is gathered in the warp's part of the histogram's memory, so that
     // it leaves 32 side by side
     uint32_t* const stack = hist + warp * (2 * kStack);
-    int fill = 0;
+    fill = 0;
     auto flush = [&] {
       __syncwarp();
 #pragma unroll 1
@@ -254,8 +344,13 @@ __global__ void __launch_bounds__(kThreads, 2) evict_select_kernel(const EvictAr
     };
     if (more > 0 || (tie > 0 && rank < left)) {
       const int n = min(part.steps, kPer);
+      uint32_t next = part.held[0];    // (a step is 32 of this warp's: n > 0)
 #pragma unroll 1
-      for (int i = 0; i < n; ++i) take(i, part.held[i * kThreads]);
+      for (int i = 0; i < n; ++i) {
+        const uint32_t x = next;
+        next = part.held[min(i + 1, kPer - 1) * kThreads];
+        take(i, x);
+      }
 #pragma unroll 1
       for (int i = kPer; i < part.steps; ++i) take(i, part.read(i));
       flush();
@@ -297,7 +392,11 @@ cudaError_t launch_evict_select(const EvictArgs& a, int num_seqs, int heads, cud
   if (num_seqs == 0 || heads == 0) return cudaSuccess;
   cudaError_t e = cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
   if (e != cudaSuccess) return e;
-  return launch_pdl(evict_select_kernel, dim3(heads, num_seqs), dim3(kThreads), kSmemBytes, stream, a);
+  // More rows than fit on the card at once start with the longest ones, so that
+  // none of those is left for the end (64 x 8 rows of 4,096 to 32,768: 58 us in
+  // order, 51 so); the ranks cost a comparison with every sequence.
+  const int ranked = (int64_t)heads * num_seqs > 2 * device_sm_count() && num_seqs > 1 && num_seqs <= kRanked;
+  return launch_pdl(evict_select_kernel, dim3(heads, num_seqs), dim3(kThreads), kSmemBytes, stream, a, ranked);
 }
 
 }  // namespace pkvd

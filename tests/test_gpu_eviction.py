@@ -220,6 +220,32 @@ def test_select_values(kind):
         run_select(pk, w, [n, 2200], keep, sink, recent)
 
 
+@pytest.mark.parametrize("near", [1, 255, 256, 257, 512])
+@pytest.mark.parametrize("keep", [1, 100, 255, 300])
+def test_select_crowded_weights(near, keep):
+    """Many weights that differ in late bits alone, in one stretch of a row: as many as are kept aside, and more."""
+    pk = require_gpu()
+    g = torch.Generator().manual_seed(near)
+    w = 0.1 * torch.rand(2, 2, 8192, generator=g)
+    w[:, :, :near] = 1 + 0.25 * torch.rand(2, 2, near, generator=g)
+    w[1, :, 4096:4096 + near] = 1 + 0.25 * torch.rand(2, near, generator=g)
+    w[:, 1, 5000:5003] = 7.0
+    run_select(pk, w, [8192, 8192], keep, 0, 0)
+    run_select(pk, w, [8192, 8100], keep, 0, 0, in_place=True)
+
+
+@pytest.mark.parametrize("seqs", [2, 45, 256, 257])
+def test_select_of_many_rows(seqs):
+    """More rows than run at once, of all lengths, equal and none among them: every row in its own place."""
+    pk = require_gpu()
+    rng = np.random.default_rng(seqs)
+    heads = 200 if seqs == 2 else 8 if seqs == 45 else 2
+    ctx = rng.choice([0, 1, 17, 64, 65, 100, 199, 200], seqs).tolist()
+    w = torch.rand(seqs, heads, 200, generator=torch.Generator().manual_seed(seqs))
+    run_select(pk, w, ctx, 60, 3, 10)
+    run_select(pk, w, ctx[::-1], 60, 3, 10, in_place=True)
+
+
 def test_select_long_rows_of_other_strides():
     """Rows longer than one pass over shared memory would hold, inside a wider buffer at an odd offset."""
     pk = require_gpu()
