@@ -30,11 +30,37 @@ namespace {
 constexpr int kPlanThreads = 256, kNearSeqs = 1024;
 static_assert(kPlanThreads >= kTreeMaxNodes, "a thread a node");
 
+// A tree's visible ancestors, a bit each, and depths, by a CTA of a thread a node:
+// what a thread leaves is its own node's (others read it behind a barrier).
+__device__ __forceinline__ void tree_ancestors(const TreePlan& p, const int32_t* __restrict__ parents, const TreeSeq& s,
+                                               uint32_t (*bits)[kTreeMaxNodes / 32 + 1], int* up, int* depths, int32_t* err) {
+  const int tid = threadIdx.x;
+  if (tid < s.n) {
+    int u = parents[s.q0 + tid];
+    if (u < -1 || u >= tid) {
+      flag_error(err, PKVD_ERR_TREE);
+      u = -1;
+    }
+    up[tid] = u;
+  }
+  for (int w = 0; w < p.words; ++w) bits[tid][w] = 0u;
+  __syncthreads();
+  if (tid >= s.n) return;
+  int depth = -1;
+  for (int u = tid; u >= 0; u = up[u]) {
+    ++depth;
+    if (p.window > 0 && depth >= p.window) continue;
+    bits[tid][u >> 5] |= 1u << (u & 31);
+  }
+  depths[tid] = depth;
+}
+
 // CTA i < num_seqs: sequence i's ancestors.  The last one: the pieces before
-// every sequence.
+// every sequence.  It runs where it is needed: for tree_tc.cu's masks, and for
+// batches of more than kOwnSeqs sequences.
 __global__ void __launch_bounds__(kPlanThreads) tree_plan_kernel(const TreePlan p, const int32_t* __restrict__ parents,
                                                                  int32_t* err) {
-  __shared__ int up[kTreeMaxNodes];
+  __shared__ int up[kTreeMaxNodes], depths[kTreeMaxNodes];
   __shared__ uint32_t bits[kTreeMaxNodes][kTreeMaxNodes / 32 + 1];
   __shared__ int64_t warp_sum[kPlanThreads / 32];
   __shared__ int64_t near[kNearSeqs];                // pieces before the first sequences
@@ -100,34 +126,12 @@ __global__ void __launch_bounds__(kPlanThreads) tree_plan_kernel(const TreePlan 
   const int i = blockIdx.x;
   const TreeSeq s = tree_seq(p, i);
   if (s.n < 0 && tid == 0) flag_error(err, PKVD_ERR_CONTEXT);
-  int depth = -1;
-  if (tid < s.n) {
-    int u = parents[s.q0 + tid];
-    if (u < -1 || u >= tid) {
-      flag_error(err, PKVD_ERR_TREE);
-      u = -1;
-    }
-    up[tid] = u;
-  }
-  for (int w = 0; w < p.words; ++w) bits[tid][w] = 0u;
-  __syncthreads();
-  if (tid < s.n)
-    for (int u = tid; u >= 0; u = up[u]) {
-      ++depth;
-      if (p.window > 0 && depth >= p.window) continue;
-      if (p.by_key) {        // the node's rows
-        const int r = tid * p.group;
-        const uint64_t m = (p.group == 64 ? ~0ull : (1ull << p.group) - 1ull) << r;
-        if ((uint32_t)m) atomicOr(&bits[u][0], (uint32_t)m);
-        if (m >> 32) atomicOr(&bits[u][1], (uint32_t)(m >> 32));
-      } else bits[tid][u >> 5] |= 1u << (u & 31);
-    }
-  if (p.by_key) __syncthreads();
+  tree_ancestors(p, parents, s, bits, up, depths, err);
   pdl_wait();
   pdl_trigger();
   if (tid < s.n) {
     const int64_t row = (int64_t)i * p.max_q + tid;
-    p.depth[row] = depth;
+    p.depth[row] = depths[tid];
     for (int w = 0; w < p.words; ++w) p.anc[row * p.words + w] = bits[tid][w];
   }
 }
@@ -139,6 +143,7 @@ constexpr int kChunkKeys = 32;
 
 struct TreeFma {
   TreePlan plan;
+  const int32_t* parents;
   void* out;
   const void* q;
   const uint8_t* kc;
@@ -169,15 +174,33 @@ __global__ void __launch_bounds__(kFmaThreads) tree_fma_kernel(const TreeFma p) 
   float* vs = ks + kChunkKeys * LD;
   float* qs = vs + kChunkKeys * LD;                 // [kPassRows][D]
   float* ps = qs + kPassRows * D;                   // [kPassRows][32]
+  uint32_t (*bits)[kTreeMaxNodes / 32 + 1] = reinterpret_cast<uint32_t (*)[kTreeMaxNodes / 32 + 1]>(ps + kPassRows * 32);
+  int* up = reinterpret_cast<int*>(bits + kTreeMaxNodes);      // [kTreeMaxNodes]
+  int* depths = up + kTreeMaxNodes;
   const TreePlan& pl = p.plan;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  pdl_wait();
-  pdl_trigger();
   TreeWalk walk;
-  walk.start(pl, blockIdx.x);
+  if (pl.num_seqs <= kOwnSeqs) {
+    const OwnStart own(pl, blockIdx.x, lane);
+    pdl_wait();
+    pdl_trigger();
+    walk.start(pl, blockIdx.x, own.first);
+    if (blockIdx.x == 0 && warp == 0) OwnStart::tell(pl, lane, p.err, own.before, own.total, own.bad);
+  } else {
+    pdl_wait();
+    pdl_trigger();
+    walk.start(pl, blockIdx.x, pl.slice[blockIdx.x]);
+  }
   TreeSegment g;
+  int tree_of = -1;                                 // whose ancestors are at hand
   while (walk.next(pl, g)) {
     const TreeSeq& s = walk.s;
+    if (g.seq != tree_of) {
+      tree_of = g.seq;
+      __syncthreads();
+      tree_ancestors(pl, p.parents, s, bits, up, depths, p.err);
+      __syncthreads();
+    }
     const int tb = g.unit * pl.unit_tokens, rows = (min(tb + pl.unit_tokens, s.n) - tb) * pl.group;
     const int k0 = max(s.lo, (s.lo_tile + g.t0) * kTreeKeys), k1 = min(s.klen, (s.lo_tile + g.t1) * kTreeKeys);
     for (int pass = 0; pass < rows; pass += kPassRows) {
@@ -199,9 +222,8 @@ __global__ void __launch_bounds__(kFmaThreads) tree_fma_kernel(const TreeFma p) 
 #pragma unroll
       for (int r = 0; r < kRowsPerWarp; ++r) {
         const int row = min(pass + warp * kRowsPerWarp + r, rows - 1), t = row / pl.group;   // rows past the last mirror it
-        const int64_t node = (int64_t)g.seq * pl.max_q + tb + t;
-        pos[r] = s.cached + pl.depth[node];
-        anc[r] = pl.anc + node * pl.words;
+        pos[r] = s.cached + depths[tb + t];
+        anc[r] = bits[tb + t];
         slope[r] = bias_slope(p.mod, g.head * pl.group + row % pl.group);
         m[r] = -INFINITY;
         l[r] = 0.f;
@@ -327,6 +349,7 @@ __global__ void __launch_bounds__(256) tree_merge_kernel(const TreePlan p, T* __
   const int units = (p.max_q + p.unit_tokens - 1) / p.unit_tokens;
   const int item = blockIdx.x % (units * p.hkv), group = blockIdx.x / (units * p.hkv);
   const int unit = item / p.hkv, head = item % p.hkv;
+  if (!p.planned) pdl_wait();                            // (its first lines then come from that kernel too)
   const int64_t total = __ldcg(reinterpret_cast<const long long*>(p.starts + p.num_seqs));
   const int64_t start = __ldcg(reinterpret_cast<const long long*>(p.starts + seq));
   const TreeSeq s = tree_seq(p, seq);
@@ -339,7 +362,7 @@ __global__ void __launch_bounds__(256) tree_merge_kernel(const TreePlan p, T* __
     f = start + ((int64_t)unit * p.hkv + head) * s.tiles;
     a = (int)tree_slice_of(total, slices, f), b = (int)tree_slice_of(total, slices, f + s.tiles - 1);
   }
-  pdl_wait();
+  if (p.planned) pdl_wait();
   pdl_trigger();
   if (a == b) return;                                    // no rows, or one CTA had them all
   const int slot_a = tree_slice_begin(total, slices, a) == f ? 0 : 1;
@@ -493,7 +516,7 @@ __global__ void __launch_bounds__(kAcceptWarps * 32) tree_accept_kernel(const Ac
 // ------------------------------------------------------------------- host
 size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 
-int words_of(int max_q) { return max_q <= 64 ? 2 : (max_q + 31) / 32; }   // two at least: by_key
+int words_of(int max_q) { return max_q <= 64 ? 2 : (max_q + 31) / 32; }   // an even number
 
 bool few_rows(int group, int max_q) { return group * max_q <= kTreeFewRows; }
 
@@ -524,7 +547,7 @@ struct WorkspaceLayout {
 
 template <typename T, int D>
 cudaError_t launch_fma(const TreeFma& p, cudaStream_t stream) {
-  constexpr int smem = (2 * kChunkKeys * (D + 4) + kPassRows * (D + 32)) * (int)sizeof(float);
+  constexpr int smem = (2 * kChunkKeys * (D + 4) + kPassRows * (D + 32) + kTreeMaxNodes * (kTreeMaxNodes / 32 + 3)) * (int)sizeof(float);
   cudaError_t e = cudaFuncSetAttribute(tree_fma_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   return launch_pdl(tree_fma_kernel<T, D>, dim3(p.plan.grid), dim3(kFmaThreads), smem, stream, p);
@@ -572,20 +595,22 @@ cudaError_t launch_tree(const TreeArgs& a, cudaStream_t stream) {
   p.window = a.window;
   p.table_tokens = (int64_t)a.max_blocks_per_seq * c.block_size;
   p.grid = grid_of(a.path, a.sms);
-  p.by_key = a.path == PKVD_PATH_TC && few_rows(group, a.max_seqlen_q);
+  p.planned = a.num_seqs > kOwnSeqs || (a.path == PKVD_PATH_TC && !few_rows(group, a.max_seqlen_q));
   p.starts = reinterpret_cast<int64_t*>(ws + lay.starts);
   p.slice = reinterpret_cast<TreeStart*>(ws + lay.slice);
   p.anc = reinterpret_cast<uint32_t*>(ws + lay.anc);
   p.depth = reinterpret_cast<int32_t*>(ws + lay.depth);
   p.rec = reinterpret_cast<float*>(ws + lay.rec);
   p.rec_ml = reinterpret_cast<float2*>(ws + lay.rec_ml);
-  cudaError_t e = launch_pdl(tree_plan_kernel, dim3(a.num_seqs + 1), dim3(kPlanThreads), 0, stream, p, a.parents, a.err);
+  cudaError_t e = cudaSuccess;
+  if (p.planned) e = launch_pdl(tree_plan_kernel, dim3(a.num_seqs + 1), dim3(kPlanThreads), 0, stream, p, a.parents, a.err);
   if (e != cudaSuccess) return e;
   if (a.path == PKVD_PATH_TC) {
     e = few_rows(group, a.max_seqlen_q) ? launch_tree_few(a, p, stream) : launch_tree_tc(a, p, stream);
   } else {
     TreeFma f;
     f.plan = p;
+    f.parents = a.parents;
     f.out = a.out;
     f.q = a.q;
     f.kc = static_cast<const uint8_t*>(c.k_base);

@@ -50,7 +50,9 @@ struct Layout {
   static constexpr uint32_t kPos = kNeg + 256;                         // [64] positions of the columns' rows
   static constexpr uint32_t kSlope = kPos + 256;                       // [64]
   static constexpr uint32_t kItems = kSlope + 256;
-  static constexpr uint32_t kGaveUp = kItems + kItemBytes;
+  static constexpr int kItemRing = 2;
+  static constexpr uint32_t kTree = kItems + sizeof(Item) * kItemRing; // of each segment: which rows see a drafted key
+  static constexpr uint32_t kGaveUp = kTree + kTreeBytes * kItemRing;
   static constexpr uint32_t kEnd = kGaveUp + 16;
   // at least 120 KB so that one CTA is resident per SM
   static constexpr uint32_t kBytes = kEnd > 122880u ? kEnd : 122880u;
@@ -126,7 +128,7 @@ __device__ __forceinline__ int tile_at(int kt_last, int n, int late, int j) {
 // and is released when tidy_values has seen to it.
 template <typename T, typename L, bool IS_V>
 __device__ __forceinline__ void copy_tiles(const TcTree& p, uint64_t* bars, uint32_t base, Item* ring_items, int lane) {
-  constexpr int H = L::kHalves, kStages = IS_V ? L::kVStages : L::kKStages;
+  constexpr int H = L::kHalves, kStages = IS_V ? L::kVStages : L::kKStages, kItemRing = L::kItemRing;
   constexpr int full = IS_V ? kVFull : kKFull, empty = IS_V ? kVEmpty : kKEmpty;
   const CUtensorMap* map = IS_V ? &p.tmap_v : &p.tmap_k;
   const uint32_t ring = base + (IS_V ? L::kV : L::kK), box = (uint32_t)p.seg_rows * 128u;
@@ -156,6 +158,7 @@ __device__ __forceinline__ void copy_tiles(const TcTree& p, uint64_t* bars, uint
     int b[4];                                  // block ids of tile t and the three after it
 #pragma unroll
     for (int i = 0; i < 4; ++i) b[i] = fetch(i);
+    if (r == 0) pdl_wait();                    // the cache rows of this step
     for (int t = 0; ok && t < n; ++t) {
       wait(empty + stg, par);
       if (!ok) break;
@@ -214,7 +217,7 @@ __device__ __forceinline__ void copy_tiles(const TcTree& p, uint64_t* bars, uint
 template <typename T, int D, int N, int MODE>
 __global__ void __launch_bounds__(kTreeThreads, 1) tree_few_kernel(const __grid_constant__ TcTree p) {
   using L = Layout<D, N>;
-  constexpr int H = L::kHalves, kKStages = L::kKStages, kVStages = L::kVStages;
+  constexpr int H = L::kHalves, kKStages = L::kKStages, kVStages = L::kVStages, kItemRing = L::kItemRing;
   constexpr int kWarps = 16;               // of the softmax
   constexpr int C = N / 4;                 // columns of a softmax thread
   // whole swizzle atoms, at an address known when linked
@@ -246,9 +249,9 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_few_kernel(const __grid_
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(FULL_MASK, *reinterpret_cast<volatile uint32_t*>(gbase + L::kBar + kTmemSlot), 0);
 
-  pdl_wait();      // the plan, and the cache rows of this step
-  pdl_trigger();
+  // (what the kernel before leaves is waited for where it is used)
   Item* ring_items = reinterpret_cast<Item*>(gbase + L::kItems);
+  if (pl.planned) pdl_wait();
 
   // registers: 512 x 104 + 128 x 56 = 60416 of the 61440 that 640 threads start with
   if (warp >= kWarps) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
@@ -257,13 +260,14 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_few_kernel(const __grid_
   } else if (warp == kVWarp) {
     copy_tiles<T, L, true>(p, bars, base, ring_items, lane);
   } else if (warp == kQWarp) {
-    tree_segments<L>(p, bars, base, ring_items, lane);
+    tree_segments<L>(p, bars, base, gbase, lane);
   } else if (warp == kMmaWarp) {
     // ---------------------------------------------------------------- MMA
     // S^T(n), n counting all tiles: Q and K have landed and S^T(n - 2), in the
     // same columns, was read.  PV(n): the weights, V, and for a segment's first
     // one the O^T of the segment before was read.  The whole warp walks through
     // this and one elected thread issues.
+    pdl_wait();          // (no bounded wait may run while the kernel before does)
     const bool leader = elect_one();
     constexpr uint32_t fmt = std::is_same<T, __nv_bfloat16>::value ? 1u : 0u;
     constexpr uint32_t id_s = tc_idesc(fmt, N, 0), id_pv = tc_idesc(fmt, N, 1) | (1u << 15), hi = desc_hi(1024);
@@ -332,6 +336,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_few_kernel(const __grid_
     wait_bounded(&bars[kDrain], 0);
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
+    pdl_wait();
+    pdl_trigger();
     // ------------------------------------------------------------ softmax
     // Every wait is bounded.  The warps meet at a named barrier, which does not
     // give up, but always brings all: each passes the same ones, a last one when
@@ -386,7 +392,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_few_kernel(const __grid_
     constexpr float kLift = kNarrow ? 7.f : 0.f, kFirst = kNarrow ? 4.f : 0.f, kLimit = kNarrow ? 15.f : 24.f;
     int n = 0;                                   // tiles so far, of all segments
     for (int r = 0; ok; ++r) {
-      ok = __all_sync(FULL_MASK, wait_item(&bars[kItemFull + r % kItemRing], (r / kItemRing) & 1));
+      ok = __all_sync(FULL_MASK, wait_item(&bars[kTreeFull + r % kItemRing], (r / kItemRing) & 1));
       if (!ok) break;
       const Item& it = ring_items[r % kItemRing];
       if (it.n < 0) break;
@@ -396,13 +402,15 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_few_kernel(const __grid_
       const int lo = uniform(it.lo), hi = uniform(it.hi), live = uniform(it.tokens * pl.group);
       // keys before this one may lie before some row's window (no position is past hi)
       const int wr_most = window_first(hi + 1, pl.window);
+      const uint32_t* rows_of = reinterpret_cast<const uint32_t*>(gbase + L::kTree + (r % kItemRing) * kTreeBytes);
+      const uint8_t* depth_of = reinterpret_cast<const uint8_t*>(rows_of) + 512;
       if (me < N) {
         const int c = min(me, live - 1), t = c / pl.group;
         ref[me] = -INFINITY;
         neg[me] = me < live ? kNoRef : -kNoRef;                // (no column: its scores never ask)
         most_of[me] = ordered(-INFINITY);
         if ((MODE & kBias) || pl.window > 0) {
-          pos[me] = cached + pl.depth[it.node0 + t];
+          pos[me] = cached + depth_of[t];
           slope[me] = bias_slope(p.mod, it.hk * pl.group + c - t * pl.group);
         }
       }
@@ -425,9 +433,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_few_kernel(const __grid_
         int at = key;
         if (tree || edge) {
           if (u >= 0 && seen) {
-            const int64_t k = (int64_t)it.seq * pl.max_q + u;
-            see &= pl.anc[k * 2 + c0 / 32] >> (c0 & 31);
-            if ((MODE & kBias) || edge) at = cached + pl.depth[k];
+            see &= rows_of[u * 2 + c0 / 32] >> (c0 & 31);
+            if ((MODE & kBias) || edge) at = cached + depth_of[u];
           }
           if (edge) {
             const int oldest = at + pl.window;               // of the positions that see it
@@ -475,10 +482,38 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_few_kernel(const __grid_
 #pragma unroll
           for (int c = 0; c < C; ++c) v[c] = (see >> c) & 1u ? v[c] : -INFINITY;
         }
-        // (a segment's first tile has no references yet)
-        bool rebase = j == 0;
+        // A segment's first tile has no references yet.  Where all rows see all of
+        // it they are the largest scores of 32 of its keys, another quarter of the
+        // tile for each quarter of the columns; a score far above asks as usual.
+        const bool sample = j == 0 && !(cut || tree || edge);
+        if (sample) {
+          float most = 0.f;              // lane e: of the e-th column of this quarter
+#pragma unroll
+          for (int s = 0; s < 4; ++s)
+            if (quarter == s) {
+#pragma unroll
+              for (int e = 0; e < C / 4; ++e) {
+                const float m = unordered(__reduce_max_sync(FULL_MASK, ordered(v[s * (C / 4) + e])));
+                most = lane == e ? m : most;
+              }
+            }
+          const int col = c0 + quarter * (C / 4) + lane;
+          if (lane < C / 4 && col < live && most > -INFINITY) {
+            const float now = most - kLift + kFirst;
+            ref[col] = now;
+            neg[col] = -now;
+          }
+          meet();
+          if (!ok) break;
+#pragma unroll
+          for (int c = 0; c < C; c += 4) {
+            const float4 s = *reinterpret_cast<const float4*>(neg + c0 + c);
+            less[c] = s.x, less[c + 1] = s.y, less[c + 2] = s.z, less[c + 3] = s.w;
+          }
+        }
+        bool rebase = j == 0 && !sample;
         float x[C];
-        if (j > 0) {
+        if (!rebase) {
           float top = -INFINITY;
 #pragma unroll
           for (int c = 0; c < C; c += 4) {
@@ -588,7 +623,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_few_kernel(const __grid_
         odd_keys(p, it, Sight(it, pl.window), kt_last - all + 1, kt_last, [&](int k, const uint16_t* v) {
           const float x = odd_value<T>(v + krow);
           uint32_t see = 0u;
-          if (k >= cached) see = pl.anc[((int64_t)it.seq * pl.max_q + k - cached) * 2 + c0 / 32] >> (c0 & 31);
+          if (k >= cached) see = rows_of[(k - cached) * 2 + c0 / 32] >> (c0 & 31);
 #pragma unroll
           for (int c = 0; c < C; ++c)
             if (k >= cached ? (see >> c) & 1u : pos[c0 + c] < k + pl.window) o[c] += x;

@@ -16,6 +16,8 @@
 
 namespace pkvd {
 
+constexpr int kOwnSeqs = 128;               // batches of at most as many: every CTA finds its own slice
+
 struct TreePlan {
   const int32_t* cu_q;
   const int32_t* cu_k;
@@ -28,10 +30,8 @@ struct TreePlan {
   // the workspace
   int64_t* starts;                          // [num_seqs + 1]: pieces before a sequence
   struct TreeStart* slice;                  // [grid]: where a slice begins
-  // [num_seqs][max_q][words]: a node's visible ancestors and itself, a bit each;
-  // by_key (at most 64 rows a tree): the rows of the nodes that see it, two words
-  uint32_t* anc;
-  int by_key;
+  int planned;                              // the plan kernel ran: the arrays above are there, and (for tree_tc.cu)
+  uint32_t* anc;                            // [num_seqs][max_q][words]: a node's visible ancestors and itself, a bit each
   int32_t* depth;                           // [num_seqs][max_q]
   float* rec;                               // [2 grid][unit_rows][D]: sums of a slice's first and last segment
   float2* rec_ml;                           // [2 grid][unit_rows]: maximum (log2 units), sum of weights
@@ -57,7 +57,7 @@ __device__ __forceinline__ TreeSeq tree_seq(const TreePlan& p, int q0, int n, in
   s.lo = p.window > 0 ? max(0, s.cached + 1 - p.window) : 0;
   s.lo_tile = s.lo / kTreeKeys;
   s.tiles = (s.klen - 1) / kTreeKeys - s.lo_tile + 1;
-  s.units = (s.n + p.unit_tokens - 1) / p.unit_tokens;
+  s.units = s.n <= p.unit_tokens ? 1 : (s.n + p.unit_tokens - 1) / p.unit_tokens;
   return s;
 }
 
@@ -85,6 +85,69 @@ struct __align__(16) TreeStart {
   int pad[2];
 };
 
+// The same found by a warp, without the plan: from the lengths alone, which are
+// inputs, so before the wait for the kernel before.  One launch less, 3 us of a
+// small call; and short code, because a kernel's first instructions come from far.
+struct OwnStart {
+  int64_t before[4], total;                 // pieces before sequences lane, lane + 32, .., in all
+  TreeStart first;
+  bool bad;                                 // one of them has lengths that cannot be
+  __device__ OwnStart(const TreePlan& p, int c, int lane) {
+    int64_t mine[4];
+    total = 0;
+    bad = false;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      before[e] = mine[e] = 0;
+      if (e * 32 >= p.num_seqs) continue;
+      const int i = e * 32 + lane;
+      if (i < p.num_seqs) {
+        const TreeSeq s = tree_seq(p, i);
+        bad |= s.n < 0;
+        mine[e] = s.pieces(p.hkv);
+      }
+      int64_t upto = mine[e];
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int64_t t = __shfl_up_sync(FULL_MASK, upto, o);
+        if (lane >= o) upto += t;
+      }
+      before[e] = total + upto - mine[e];
+      total += __shfl_sync(FULL_MASK, upto, 31);
+    }
+    const int64_t slices = tree_slices(p, total);
+    first.at = first.end = first.in = 0;
+    first.seq = first.q0 = first.n = first.klen = 0;
+    if (c >= slices) return;                // no piece for this CTA
+    if (total < (1 << 22)) {                // (a 64-bit division takes hundreds of clocks; c < 2^9)
+      first.at = (uint32_t)total * (uint32_t)c / (uint32_t)slices;
+      first.end = (uint32_t)total * (uint32_t)(c + 1) / (uint32_t)slices;
+    } else {
+      first.at = tree_slice_begin(total, slices, c);
+      first.end = tree_slice_begin(total, slices, c + 1);
+    }
+    int at = -1;                            // the sequence that has the first piece
+    int64_t in = 0;
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (before[e] <= first.at && first.at < before[e] + mine[e]) at = e * 32 + lane, in = first.at - before[e];
+    const int src = __ffs(__ballot_sync(FULL_MASK, at >= 0)) - 1;
+    first.in = __shfl_sync(FULL_MASK, in, src);
+    first.seq = __shfl_sync(FULL_MASK, at, src);
+    first.q0 = p.cu_q[first.seq];
+    first.n = p.cu_q[first.seq + 1] - first.q0;
+    first.klen = p.cu_k[first.seq + 1] - p.cu_k[first.seq];
+  }
+  // What the plan kernel would have said, by one warp of the grid, behind the wait.
+  static __device__ void tell(const TreePlan& p, int lane, int32_t* err, const int64_t (&before)[4], int64_t total, bool bad) {
+    if (bad) flag_error(err, PKVD_ERR_CONTEXT);
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (e * 32 + lane < p.num_seqs) p.starts[e * 32 + lane] = before[e];
+    if (lane == 0) p.starts[p.num_seqs] = total;
+  }
+};
+
 // One segment of a slice: tiles [t0, t1) of a (unit, head).
 struct TreeSegment {
   int seq, unit, head;
@@ -97,8 +160,7 @@ struct TreeWalk {
   int64_t at, end, begin, in;               // in: `at` within its sequence
   int cta, seq;
   TreeSeq s;
-  __device__ void start(const TreePlan& p, int c) {
-    const TreeStart f = p.slice[c];
+  __device__ void start(const TreePlan& p, int c, const TreeStart& f) {
     cta = c;
     at = begin = f.at;
     end = f.end;

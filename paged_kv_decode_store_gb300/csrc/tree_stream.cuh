@@ -29,7 +29,8 @@ enum : int {
 };
 constexpr uint32_t kBarBytes = 512, kTmemSlot = 8 * kNumBars;
 static_assert(kTmemSlot + 4 <= kBarBytes, "behind the barriers");
-constexpr int kItemRing = 4;
+constexpr int kTreeFull = kJoin;                  // tree_few.cu, two: a segment's tree_rows (its streams need not join)
+constexpr int kTreeBytes = 64 * 8 + 64;            // tree_rows
 constexpr int kItemUsers = 3 + 2 * kStreamWarps;   // K/V, two MMA and softmax warps
 
 struct TcTree {
@@ -37,6 +38,7 @@ struct TcTree {
   TreePlan plan;
   void* out;
   const int32_t* tables;
+  const int32_t* parents;
   int max_blocks;
   int block_size, block_shift;   // a power of two
   uint32_t block_limit;          // num_blocks, at most 2^31
@@ -60,7 +62,6 @@ struct __align__(16) Item {
   int qbuf, late;                // where a single Q tile lies; more than the unit's last tile, and that
   int odd, pad;                  // set by the copies of V: values that are no numbers (tidy_values)
 };
-constexpr uint32_t kItemBytes = sizeof(Item) * kItemRing;
 
 __device__ __forceinline__ int window_first(int c, int window) { return (window > 0 && c > window) ? c - window : 0; }
 
@@ -163,12 +164,13 @@ __device__ __forceinline__ void tree_init_barriers(uint64_t* bars) {
   fence_mbar_init();
 }
 
-// K and V (one warp).  Lane s copies segment s of a tile; K runs kAhead tiles
+// K and V (one warp; the block tables are inputs, read before the wait for the
+// kernel before).  Lane s copies segment s of a tile; K runs kAhead tiles
 // ahead of V.  A V tile with keys that not every row sees lands on a barrier of
 // its own (kVCut) and is released when tidy_values has seen to it.
 template <typename T, typename L>
 __device__ __forceinline__ void tree_copy_kv(const TcTree& p, uint64_t* bars, uint32_t base, Item* ring_items, int lane) {
-  constexpr int H = L::kHalves, kKStages = L::kKStages, kVStages = L::kVStages;
+  constexpr int H = L::kHalves, kKStages = L::kKStages, kVStages = L::kVStages, kItemRing = L::kItemRing;
   constexpr int kAhead = kKStages - 2;
   const uint32_t box = (uint32_t)p.seg_rows * 128u;
   const int nseg = kTcKeys / p.seg_rows;
@@ -233,6 +235,7 @@ __device__ __forceinline__ void tree_copy_kv(const TcTree& p, uint64_t* bars, ui
     int b[4];                                // block ids of V tile t and the three after it
 #pragma unroll
     for (int i = 0; i < 4; ++i) b[i] = fetch(i);
+    if (r == 0) pdl_wait();                  // the cache rows of this step
 #pragma unroll
     for (int i = 0; i < kAhead; ++i)
       if (i < n) copy_k(i, b[i]);
@@ -271,63 +274,139 @@ __device__ __forceinline__ void tree_copy_kv(const TcTree& p, uint64_t* bars, ui
   }
 }
 
+// A tree of at most 64 rows, by a warp: which rows see a node (64 bits), and its
+// depth.  Every node (lane's and lane + 32's parents: up) walks up to its root.
+__device__ __forceinline__ void tree_rows(const TcTree& p, int n, int (&up)[2], uint32_t* rows, uint8_t* depths, int lane) {
+  const TreePlan& pl = p.plan;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int t = i * 32 + lane;
+    if (up[i] < -1 || up[i] >= t) {
+      flag_error(p.err, PKVD_ERR_TREE);
+      up[i] = -1;
+    }
+    rows[2 * t] = rows[2 * t + 1] = 0u;
+  }
+  __syncwarp();
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int t = i * 32 + lane;
+    if (i * 32 >= n) break;
+    const uint64_t mine = t < n ? (pl.group == 64 ? ~0ull : (1ull << pl.group) - 1ull) << (t * pl.group) : 0ull;
+    int u = t < n ? t : -1, depth = -1;
+    while (__any_sync(FULL_MASK, u >= 0)) {
+      if (u >= 0) {
+        ++depth;
+        if (pl.window <= 0 || depth < pl.window) {
+          if ((uint32_t)mine) atomicOr(rows + 2 * u, (uint32_t)mine);
+          if (mine >> 32) atomicOr(rows + 2 * u + 1, (uint32_t)(mine >> 32));
+        }
+      }
+      const int a = __shfl_sync(FULL_MASK, up[0], u & 31), b = __shfl_sync(FULL_MASK, up[1], u & 31);
+      if (u >= 0) u = u < 32 ? a : b;
+    }
+    if (t < n) depths[t] = (uint8_t)depth;
+  }
+  __syncwarp();
+}
+
 // Segments and Q (one warp).  A Q tile's rows are one box per 64 columns (G heads
 // of tile_tokens nodes).  Two tiles of a unit fill both buffers; single ones take
-// them in turn (L::kQBufs), so the next is loaded while the last is in use.
+// them in turn (L::kQBufs), so the next is loaded while the last is in use.  The
+// first segments are there before the wait for the kernel before, where there is no
+// plan to wait for.
 template <typename L>
-__device__ __forceinline__ void tree_segments(const TcTree& p, uint64_t* bars, uint32_t base, Item* ring_items, int lane) {
-  constexpr int H = L::kHalves;
+__device__ __forceinline__ void tree_segments(const TcTree& p, uint64_t* bars, uint32_t base, uint8_t* gbase, int lane) {
+  constexpr int H = L::kHalves, kItemRing = L::kItemRing;
   const TreePlan& pl = p.plan;
+  Item* ring_items = reinterpret_cast<Item*>(gbase + L::kItems);
+  const bool own = !pl.planned;
   TreeWalk walk;
-  walk.start(pl, blockIdx.x);
-  if (lane == 0) {
-    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&p.tmap_q)) : "memory");
-    bool ok = true;
-    int used[2] = {0, 0}, turn = 0;
-    for (int r = 0; ok; ++r) {
-      const int slot = r % kItemRing;
-      if (r >= kItemRing) ok = wait_item(&bars[kItemFree + slot], ((r / kItemRing) - 1) & 1);
-      if (!ok) break;
-      Item it;
-      TreeSegment g;
-      it.n = -1;
-      if (walk.next(pl, g)) {
-        const int tb = g.unit * pl.unit_tokens;
-        it.seq = g.seq;
-        it.hk = g.head;
-        it.q0 = walk.s.q0 + tb;
-        it.tokens = min(pl.unit_tokens, walk.s.n - tb);
-        it.node0 = g.seq * pl.max_q + tb;
-        it.cached = walk.s.cached;
-        it.lo = walk.s.lo;
-        it.hi = walk.s.klen - 1;
-        it.kt_last = walk.s.lo_tile + g.t1 - 1;
-        it.n = g.t1 - g.t0;
-        it.slot = g.slot;
-        it.late = g.t1 == walk.s.tiles && it.n > 1;
-        it.odd = 0;
-        it.two = it.tokens > p.tile_tokens;
-        it.qbuf = turn;
-        if (!it.two && L::kQBufs == 2) turn ^= 1;
-      }
+  bool waited = !own;
+  if (lane == 0) asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&p.tmap_q)) : "memory");
+  int64_t before[4] = {}, total = 0;
+  bool bad = false;
+  if (own) {
+    const OwnStart s(pl, blockIdx.x, lane);
+    walk.start(pl, blockIdx.x, s.first);
+    if (blockIdx.x == 0) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) before[e] = s.before[e];
+      total = s.total;
+      bad = s.bad;
+    }
+  } else {                                   // (the kernel before, the plan, was waited for)
+    walk.start(pl, blockIdx.x, pl.slice[blockIdx.x]);
+  }
+  bool ok = true;
+  int used[2] = {0, 0}, turn = 0;
+  for (int r = 0; ok; ++r) {
+    const int slot = r % kItemRing;
+    if (r >= kItemRing) ok = __all_sync(FULL_MASK, wait_item(&bars[kItemFree + slot], ((r / kItemRing) - 1) & 1));
+    if (!ok) break;
+    Item it;
+    TreeSegment g;
+    it.n = -1;
+    if (walk.next(pl, g)) {
+      const int tb = g.unit * pl.unit_tokens;
+      it.seq = g.seq;
+      it.hk = g.head;
+      it.q0 = walk.s.q0 + tb;
+      it.tokens = min(pl.unit_tokens, walk.s.n - tb);
+      it.node0 = g.seq * pl.max_q + tb;
+      it.cached = walk.s.cached;
+      it.lo = walk.s.lo;
+      it.hi = walk.s.klen - 1;
+      it.kt_last = walk.s.lo_tile + g.t1 - 1;
+      it.n = g.t1 - g.t0;
+      it.slot = g.slot;
+      it.late = g.t1 == walk.s.tiles && it.n > 1;
+      it.odd = 0;
+      it.two = it.tokens > p.tile_tokens;
+      it.qbuf = turn;
+      if (!it.two && L::kQBufs == 2) turn ^= 1;
+    }
+    if (lane == 0) {
       ring_items[slot] = it;
       mbar_arrive(&bars[kItemFull + slot]);
-      if (it.n < 0) break;
+    }
+    __syncwarp();
+    if (it.n < 0) {
+      if (L::kTree > 0 && lane == 0) mbar_arrive(&bars[kTreeFull + slot]);
+      break;
+    }
+    int up[2];
 #pragma unroll
-      for (int g2 = 0; g2 < 2; ++g2) {
-        if (!ok || !(it.two || it.qbuf == g2)) continue;
-        if (used[g2] > 0) ok = wait_item(&bars[kQEmpty + g2], (used[g2] - 1) & 1);
-        if (!ok) continue;
+    for (int i = 0; i < 2; ++i)
+      up[i] = L::kTree > 0 && i * 32 + lane < it.tokens ? p.parents[it.q0 + i * 32 + lane] : -1;
+    if (!waited) pdl_wait();
+    waited = true;
+#pragma unroll
+    for (int g2 = 0; g2 < 2; ++g2) {
+      if (!ok || !(it.two || it.qbuf == g2)) continue;
+      if (used[g2] > 0) ok = __all_sync(FULL_MASK, wait_item(&bars[kQEmpty + g2], (used[g2] - 1) & 1));
+      if (!ok) continue;
+      if (lane == 0) {
         mbar_arrive_expect_tx(&bars[kQFull + g2], p.q_box * H);
         for (int h = 0; h < H; ++h)
           tma_load3(base + L::kQ + (g2 * H + h) * L::kQHalf, &p.tmap_q, h * 64, it.hk * pl.group,
                     it.q0 + (it.two ? g2 * p.tile_tokens : 0), &bars[kQFull + g2]);
-        ++used[g2];
       }
+      ++used[g2];
     }
-    if (!ok) flag_error(p.err, PKVD_ERR_TIMEOUT);
+    if constexpr (L::kTree > 0) {              // the unit is the whole tree
+      uint8_t* tree = gbase + L::kTree + slot * kTreeBytes;
+      tree_rows(p, it.tokens, up, reinterpret_cast<uint32_t*>(tree), tree + 512, lane);
+      if (lane == 0) mbar_arrive(&bars[kTreeFull + slot]);
+    }
+  }
+  if (!ok && lane == 0) flag_error(p.err, PKVD_ERR_TIMEOUT);
+  if (lane == 0)
     for (int g2 = 0; g2 < 2; ++g2)             // no copy is in flight when the CTA leaves
       if (used[g2] > 0) wait_bounded(&bars[kQFull + g2], (used[g2] - 1) & 1);
+  if (own && blockIdx.x == 0 && !pl.planned) { // for the merge
+    if (!waited) pdl_wait();
+    OwnStart::tell(pl, lane, p.err, before, total, bad);
   }
 }
 
@@ -347,6 +426,7 @@ inline bool tree_tc_params(const TreeArgs& a, const TreePlan& plan, int tile_tok
   prm->head_stride = c.head_stride;
   prm->out = a.out;
   prm->tables = a.block_tables;
+  prm->parents = a.parents;
   prm->max_blocks = a.max_blocks_per_seq;
   prm->block_limit = (uint32_t)(c.num_blocks < 0x80000000ll ? c.num_blocks : 0x80000000ll);
   prm->block_size = c.block_size;

@@ -47,7 +47,9 @@ struct Layout {
   static constexpr int kQBufs = 2, kJoinWarps = 4;                     // kJoin: a quarter of the rows, both streams
   static constexpr uint32_t kX = kBar + kBarBytes;                     // exchange: 1024 bytes a stream
   static constexpr uint32_t kItems = kX + 2048;                        // ring of segments
-  static constexpr uint32_t kGaveUp = kItems + kItemBytes;             // one word a pair of softmax warps
+  static constexpr int kItemRing = 4;
+  static constexpr uint32_t kTree = 0;                                 // (the plan's array is read)
+  static constexpr uint32_t kGaveUp = kItems + sizeof(Item) * kItemRing;             // one word a pair of softmax warps
   static constexpr uint32_t kEnd = kGaveUp + 32;
   // at least 120 KB so that one CTA (which holds all TMEM) is resident per SM
   static constexpr uint32_t kBytes = kEnd > 122880u ? kEnd : 122880u;
@@ -114,7 +116,7 @@ __device__ __forceinline__ void hide(float (&v)[kThreadKeys], uint32_t seen, flo
 template <typename T, int D, int MODE>
 __global__ void __launch_bounds__(kTreeThreads, 1) tree_tc_kernel(const __grid_constant__ TcTree p) {
   using L = Layout<D>;
-  constexpr int H = L::kHalves, kKStages = L::kKStages, kVStages = L::kVStages;
+  constexpr int H = L::kHalves, kKStages = L::kKStages, kVStages = L::kVStages, kItemRing = L::kItemRing;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* gbase = smem_raw;
   const uint32_t base = smem_u32(smem_raw);
@@ -134,16 +136,16 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_tc_kernel(const __grid_c
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(FULL_MASK, *reinterpret_cast<volatile uint32_t*>(gbase + L::kBar + kTmemSlot), 0);
 
-  pdl_wait();      // the plan, and the cache rows of this step
-  pdl_trigger();
+  // (what the kernels before leave is waited for where it is used)
   Item* ring_items = reinterpret_cast<Item*>(gbase + L::kItems);
+  if (pl.planned) pdl_wait();
 
   // registers: 512 x 104 + 128 x 56 = 60416 of the 61440 that 640 threads start with
   if (warp >= kKvWarp) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
   if (warp == kKvWarp) {
     tree_copy_kv<T, L>(p, bars, base, ring_items, lane);
   } else if (warp == kQWarp) {
-    tree_segments<L>(p, bars, base, ring_items, lane);
+    tree_segments<L>(p, bars, base, gbase, lane);
   } else if (warp == kMmaWarp || warp == kMmaWarp1) {
     // ---------------------------------------------------------------- MMA
     // S(n, h) of the stream, n counting all its K tiles, h = 1 (the newer 64
@@ -154,6 +156,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_tc_kernel(const __grid_c
     // use it waits for all the same, so that no phase of a stage is waited for
     // before the one before it is over.  The whole warp walks through this and one
     // elected thread issues.
+    pdl_wait();          // (no bounded wait may run while the kernel before does)
     const bool leader = elect_one();
     const int g = warp == kMmaWarp ? 0 : 1;
     constexpr uint32_t fmt = std::is_same<T, __nv_bfloat16>::value ? 1u : 0u;
@@ -281,6 +284,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1) tree_tc_kernel(const __grid_c
     wait_bounded(&bars[kDrain + g], 0);
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
+    pdl_wait();
+    pdl_trigger();
     // ------------------------------------------------------------ softmax
     // Every wait is bounded; a warp whose wait gives up leaves (the others'
     // then give up in turn).  The two warps of a quarter of a stream's rows meet
