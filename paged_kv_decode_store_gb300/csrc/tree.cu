@@ -180,20 +180,25 @@ __global__ void __launch_bounds__(kFmaThreads) tree_fma_kernel(const TreeFma p) 
   const TreePlan& pl = p.plan;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   TreeWalk walk;
-  if (pl.num_seqs <= kOwnSeqs) {
+  int64_t total;
+  if (!pl.planned) {
     const OwnStart own(pl, blockIdx.x, lane);
     pdl_wait();
     pdl_trigger();
     walk.start(pl, blockIdx.x, own.first);
-    if (blockIdx.x == 0 && warp == 0) OwnStart::tell(pl, lane, p.err, own.before, own.total, own.bad);
+    total = own.total;
+    if (own.bad && blockIdx.x == 0) flag_error(p.err, PKVD_ERR_CONTEXT);
   } else {
     pdl_wait();
     pdl_trigger();
     walk.start(pl, blockIdx.x, pl.slice[blockIdx.x]);
+    total = pl.starts[pl.num_seqs];
   }
   TreeSegment g;
   int tree_of = -1;                                 // whose ancestors are at hand
-  while (walk.next(pl, g)) {
+  bool more = walk.next(pl, g);
+  if (tid == 0) tell_join(pl, walk, g, more, total);
+  for (; more; more = walk.next(pl, g)) {
     const TreeSeq& s = walk.s;
     if (g.seq != tree_of) {
       tree_of = g.seq;
@@ -333,39 +338,40 @@ __global__ void __launch_bounds__(kFmaThreads) tree_fma_kernel(const TreeFma p) 
 // ------------------------------------------------------------------- merge
 // Joins the records of a (unit, head) that more than one CTA worked on:
 //   M = max m_k, out = sum 2^(m_k - M) acc_k / sum 2^(m_k - M) l_k.
+// CTA (c, group): what slice c continues and the one before began, as CTA c of the
+// kernel with the records left it (finding it here, for every unit of every
+// sequence, took divisions by every CTA: 312 instead of 308 us for 16 sequences of 64
+// nodes of 64 heads).
 // PARTS = 1: a warp has kMergeRows rows, whose records are on their way together
-// (one row a warp: 36 instead of see the table for 64 nodes of 8 heads a KV head,
-// where rows are cut in two or three).  PARTS = 8, for few rows cut into many
-// pieces: the CTA's eight warps share a row's records.
+// (one row a warp: 36 instead of 18 us for 64 nodes of 8 heads a KV head, where
+// rows are cut in two or three).  PARTS = 8, for few rows cut into many pieces:
+// the CTA's eight warps share a row's records.
 constexpr int kMergeRows = 4;
 
 template <typename T, int D, int PARTS>
 __global__ void __launch_bounds__(256) tree_merge_kernel(const TreePlan p, T* __restrict__ out) {
   constexpr int ROWS = PARTS == 1 ? kMergeRows : 1, R = PARTS == 1 ? 3 : 8;   // rows, records of each on their way
   __shared__ float part[PARTS == 1 ? 1 : 8 * (D + 2)];
-  // The plan was complete before the kernel with the records let this one start;
-  // its records come behind the wait.
-  const int seq = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int units = (p.max_q + p.unit_tokens - 1) / p.unit_tokens;
-  const int item = blockIdx.x % (units * p.hkv), group = blockIdx.x / (units * p.hkv);
-  const int unit = item / p.hkv, head = item % p.hkv;
-  if (!p.planned) pdl_wait();                            // (its first lines then come from that kernel too)
-  const int64_t total = __ldcg(reinterpret_cast<const long long*>(p.starts + p.num_seqs));
-  const int64_t start = __ldcg(reinterpret_cast<const long long*>(p.starts + seq));
-  const TreeSeq s = tree_seq(p, seq);
-  const int tb = unit * p.unit_tokens, rows = unit < s.units ? (min(tb + p.unit_tokens, s.n) - tb) * p.group : 0;
-  const int row0 = PARTS == 1 ? (group * 8 + warp) * ROWS : group;
-  int a = 0, b = 0;
-  int64_t slices = 0, f = 0;
-  if ((PARTS == 1 ? group * 8 * ROWS : group) < rows) {
-    slices = tree_slices(p, total);
-    f = start + ((int64_t)unit * p.hkv + head) * s.tiles;
-    a = (int)tree_slice_of(total, slices, f), b = (int)tree_slice_of(total, slices, f + s.tiles - 1);
-  }
-  if (p.planned) pdl_wait();
+  pdl_wait();
   pdl_trigger();
-  if (a == b) return;                                    // no rows, or one CTA had them all
-  const int slot_a = tree_slice_begin(total, slices, a) == f ? 0 : 1;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, group = blockIdx.y;
+  int c = blockIdx.x;
+  if constexpr (PARTS > 1) {           // few of the slices' begins have something to join: the x-th of those
+    int left = blockIdx.x;
+    c = -1;
+#pragma unroll 4
+    for (int base = 0; base < p.grid; base += 32) {
+      const uint32_t some = __ballot_sync(FULL_MASK, base + lane < p.grid && p.join[base + lane].rows > 0);
+      const int n = __popc(some);
+      if (c < 0 && left < n) c = base + __fns(some, 0, left + 1);
+      left -= n;
+    }
+    if (c < 0) return;
+  }
+  const TreeJoin j = p.join[c];
+  const int rows = j.rows, a = j.a, b = j.b;
+  const int row0 = PARTS == 1 ? (group * 8 + warp) * ROWS : group;
+  if ((PARTS == 1 ? group * 8 * ROWS : group) >= rows) return;
   constexpr int Q = D / 4, SUB = 32 / Q;                 // lanes of a row's float4 slices; records a warp takes at once
   const int d4 = lane % Q * 4, sub = lane / Q;
   const int step = SUB * PARTS, k_first = PARTS == 1 ? sub : warp * SUB + sub;
@@ -379,7 +385,7 @@ __global__ void __launch_bounds__(256) tree_merge_kernel(const TreePlan p, T* __
 #pragma unroll
     for (int e = 0; e < R; ++e) {
       const int k = k0 + e * step;
-      const int64_t at = (int64_t)(2 * k + (k == a ? slot_a : 0)) * p.unit_rows + row0;
+      const int64_t at = (int64_t)(k == a ? j.slot_a : 2 * k) * p.unit_rows + row0;
 #pragma unroll
       for (int i = 0; i < ROWS; ++i) {
         ml[e][i] = make_float2(-INFINITY, 0.f);
@@ -439,7 +445,7 @@ __global__ void __launch_bounds__(256) tree_merge_kernel(const TreePlan p, T* __
     const int row = row0 + i;
     if (row >= rows) break;
     const int t = row / p.group, gi = row % p.group;
-    T* dst = out + ((int64_t)(s.q0 + tb + t) * p.hq + (int64_t)head * p.group + gi) * D + d4;
+    T* dst = out + ((int64_t)(j.q0 + t) * p.hq + (int64_t)j.head * p.group + gi) * D + d4;
     const float inv = L[i] > 0.f ? 1.f / L[i] : 0.f;
     if constexpr (sizeof(T) == 2) {                      // out is 16-byte aligned, rows of 128 bytes and more
       *reinterpret_cast<uint2*>(dst) = make_uint2(Mma<T>::pack(o[i].x * inv, o[i].y * inv), Mma<T>::pack(o[i].z * inv, o[i].w * inv));
@@ -531,13 +537,14 @@ int unit_tokens_of(int path, int group, int max_q) {
 int grid_of(int path, int sms) { return path == PKVD_PATH_FMA ? 2 * sms : sms; }
 
 struct WorkspaceLayout {
-  size_t starts, slice, anc, depth, rec, rec_ml, bytes;
+  size_t starts, slice, join, anc, depth, rec, rec_ml, bytes;
   WorkspaceLayout(int path, int num_seqs, int group, int head_dim, int max_q, int sms) {
     const int words = words_of(max_q);
     const size_t rows = (size_t)2 * grid_of(path, sms) * unit_tokens_of(path, group, max_q) * group;
     starts = 0;
     slice = starts + up256(sizeof(int64_t) * ((size_t)num_seqs + 1));
-    anc = slice + up256(sizeof(TreeStart) * (size_t)grid_of(path, sms));
+    join = slice + up256(sizeof(TreeStart) * (size_t)grid_of(path, sms));
+    anc = join + up256(sizeof(TreeJoin) * (size_t)grid_of(path, sms));
     depth = anc + up256(sizeof(uint32_t) * (size_t)num_seqs * max_q * words);
     rec_ml = depth + up256(sizeof(int32_t) * (size_t)num_seqs * max_q);
     rec = rec_ml + up256(sizeof(float2) * rows);
@@ -559,8 +566,7 @@ cudaError_t launch_merge(const TreePlan& p, void* out, cudaStream_t stream) {
   const int rows = (p.max_q < p.unit_tokens ? p.max_q : p.unit_tokens) * p.group;
   // pieces of an item: about grid / items; a warp takes eight records a round
   const bool many = p.grid > 8 * items * p.num_seqs;
-  const int64_t groups = many ? rows : (rows + 8 * kMergeRows - 1) / (8 * kMergeRows);
-  const dim3 grid((unsigned)(items * groups), (unsigned)p.num_seqs);
+  const dim3 grid((unsigned)(many ? items * p.num_seqs : p.grid), (unsigned)(many ? rows : (rows + 8 * kMergeRows - 1) / (8 * kMergeRows)));
   return many ? launch_pdl(tree_merge_kernel<T, D, 8>, grid, dim3(256), 0, stream, p, static_cast<T*>(out))
               : launch_pdl(tree_merge_kernel<T, D, 1>, grid, dim3(256), 0, stream, p, static_cast<T*>(out));
 }
@@ -598,6 +604,7 @@ cudaError_t launch_tree(const TreeArgs& a, cudaStream_t stream) {
   p.planned = a.num_seqs > kOwnSeqs || (a.path == PKVD_PATH_TC && !few_rows(group, a.max_seqlen_q));
   p.starts = reinterpret_cast<int64_t*>(ws + lay.starts);
   p.slice = reinterpret_cast<TreeStart*>(ws + lay.slice);
+  p.join = reinterpret_cast<TreeJoin*>(ws + lay.join);
   p.anc = reinterpret_cast<uint32_t*>(ws + lay.anc);
   p.depth = reinterpret_cast<int32_t*>(ws + lay.depth);
   p.rec = reinterpret_cast<float*>(ws + lay.rec);

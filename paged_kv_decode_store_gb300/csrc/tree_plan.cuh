@@ -30,7 +30,8 @@ struct TreePlan {
   // the workspace
   int64_t* starts;                          // [num_seqs + 1]: pieces before a sequence
   struct TreeStart* slice;                  // [grid]: where a slice begins
-  int planned;                              // the plan kernel ran: the arrays above are there, and (for tree_tc.cu)
+  struct TreeJoin* join;                    // [grid]: what is to be joined across a slice's begin
+  int planned;                              // the plan kernel ran: starts and slice are there, and (for tree_tc.cu)
   uint32_t* anc;                            // [num_seqs][max_q][words]: a node's visible ancestors and itself, a bit each
   int32_t* depth;                           // [num_seqs][max_q]
   float* rec;                               // [2 grid][unit_rows][D]: sums of a slice's first and last segment
@@ -69,10 +70,14 @@ __device__ __forceinline__ TreeSeq tree_seq(const TreePlan& p, int i) {
 __device__ __forceinline__ int64_t tree_slices(const TreePlan& p, int64_t total) {
   return total < p.grid ? total : p.grid;
 }
-__device__ __forceinline__ int64_t tree_slice_begin(int64_t total, int64_t slices, int64_t c) { return total * c / slices; }
+// (in 32 bits where they hold it -- slices are fewer than 2^10 -- because a 64-bit
+// division takes hundreds of clocks)
+__device__ __forceinline__ int64_t tree_slice_begin(int64_t total, int64_t slices, int64_t c) {
+  return total < (1 << 22) ? (uint32_t)total * (uint32_t)c / (uint32_t)slices : total * c / slices;
+}
 // The slice that holds piece f.
 __device__ __forceinline__ int64_t tree_slice_of(int64_t total, int64_t slices, int64_t f) {
-  return ((f + 1) * slices - 1) / total;
+  return total < (1 << 22) ? ((uint32_t)(f + 1) * (uint32_t)slices - 1u) / (uint32_t)total : ((f + 1) * slices - 1) / total;
 }
 
 // Where a slice begins, as the plan kernel leaves it: one load instead of a
@@ -89,11 +94,11 @@ struct __align__(16) TreeStart {
 // inputs, so before the wait for the kernel before.  One launch less, 3 us of a
 // small call; and short code, because a kernel's first instructions come from far.
 struct OwnStart {
-  int64_t before[4], total;                 // pieces before sequences lane, lane + 32, .., in all
+  int64_t total;                            // pieces in all
   TreeStart first;
   bool bad;                                 // one of them has lengths that cannot be
   __device__ OwnStart(const TreePlan& p, int c, int lane) {
-    int64_t mine[4];
+    int64_t before[4], mine[4];             // pieces before sequences lane, lane + 32, .., and of them
     total = 0;
     bad = false;
 #pragma unroll
@@ -119,13 +124,8 @@ struct OwnStart {
     first.at = first.end = first.in = 0;
     first.seq = first.q0 = first.n = first.klen = 0;
     if (c >= slices) return;                // no piece for this CTA
-    if (total < (1 << 22)) {                // (a 64-bit division takes hundreds of clocks; c < 2^9)
-      first.at = (uint32_t)total * (uint32_t)c / (uint32_t)slices;
-      first.end = (uint32_t)total * (uint32_t)(c + 1) / (uint32_t)slices;
-    } else {
-      first.at = tree_slice_begin(total, slices, c);
-      first.end = tree_slice_begin(total, slices, c + 1);
-    }
+    first.at = tree_slice_begin(total, slices, c);
+    first.end = tree_slice_begin(total, slices, c + 1);
     int at = -1;                            // the sequence that has the first piece
     int64_t in = 0;
 #pragma unroll
@@ -137,14 +137,6 @@ struct OwnStart {
     first.q0 = p.cu_q[first.seq];
     first.n = p.cu_q[first.seq + 1] - first.q0;
     first.klen = p.cu_k[first.seq + 1] - p.cu_k[first.seq];
-  }
-  // What the plan kernel would have said, by one warp of the grid, behind the wait.
-  static __device__ void tell(const TreePlan& p, int lane, int32_t* err, const int64_t (&before)[4], int64_t total, bool bad) {
-    if (bad) flag_error(err, PKVD_ERR_CONTEXT);
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-      if (e * 32 + lane < p.num_seqs) p.starts[e * 32 + lane] = before[e];
-    if (lane == 0) p.starts[p.num_seqs] = total;
   }
 };
 
@@ -191,5 +183,31 @@ struct TreeWalk {
     return true;
   }
 };
+
+// A (unit, head) that slice c continues and the slice before it began: the records
+// of CTAs a = c - 1 to b, which the merge joins.  rows = 0: there is none.
+struct __align__(16) TreeJoin {
+  int q0, rows, head, slot_a;               // slot_a: of CTA a's record; the others' are 2 k
+  int a, b, pad[2];
+};
+
+// By one thread of a CTA, behind the wait.  g: the walk's first segment (any: there is one).
+__device__ __forceinline__ void tell_join(const TreePlan& p, const TreeWalk& walk, const TreeSegment& g, bool any, int64_t total) {
+  TreeJoin j = {};
+  if (any && g.t0 > 0) {
+    const int c = walk.cta;
+    const int64_t slices = tree_slices(p, total), begin = walk.begin - g.t0, before = tree_slice_begin(total, slices, c - 1);
+    if (begin >= before) {
+      const int tb = g.unit * p.unit_tokens;
+      j.q0 = walk.s.q0 + tb;
+      j.rows = min(p.unit_tokens, walk.s.n - tb) * p.group;
+      j.head = g.head;
+      j.slot_a = 2 * (c - 1) + (begin == before ? 0 : 1);
+      j.a = c - 1;
+      j.b = (int)tree_slice_of(total, slices, begin + walk.s.tiles - 1);
+    }
+  }
+  p.join[walk.cta] = j;
+}
 
 }  // namespace pkvd

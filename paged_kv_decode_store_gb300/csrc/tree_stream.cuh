@@ -324,19 +324,15 @@ __device__ __forceinline__ void tree_segments(const TcTree& p, uint64_t* bars, u
   TreeWalk walk;
   bool waited = !own;
   if (lane == 0) asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&p.tmap_q)) : "memory");
-  int64_t before[4] = {}, total = 0;
-  bool bad = false;
+  int64_t total = 0;
   if (own) {
     const OwnStart s(pl, blockIdx.x, lane);
     walk.start(pl, blockIdx.x, s.first);
-    if (blockIdx.x == 0) {
-#pragma unroll
-      for (int e = 0; e < 4; ++e) before[e] = s.before[e];
-      total = s.total;
-      bad = s.bad;
-    }
+    total = s.total;
+    if (s.bad && blockIdx.x == 0) flag_error(p.err, PKVD_ERR_CONTEXT);
   } else {                                   // (the kernel before, the plan, was waited for)
     walk.start(pl, blockIdx.x, pl.slice[blockIdx.x]);
+    total = pl.starts[pl.num_seqs];
   }
   bool ok = true;
   int used[2] = {0, 0}, turn = 0;
@@ -373,6 +369,10 @@ __device__ __forceinline__ void tree_segments(const TcTree& p, uint64_t* bars, u
     __syncwarp();
     if (it.n < 0) {
       if (L::kTree > 0 && lane == 0) mbar_arrive(&bars[kTreeFull + slot]);
+      if (r == 0) {
+        if (!waited) pdl_wait();
+        if (lane == 0) tell_join(pl, walk, g, false, total);
+      }
       break;
     }
     int up[2];
@@ -399,15 +399,12 @@ __device__ __forceinline__ void tree_segments(const TcTree& p, uint64_t* bars, u
       tree_rows(p, it.tokens, up, reinterpret_cast<uint32_t*>(tree), tree + 512, lane);
       if (lane == 0) mbar_arrive(&bars[kTreeFull + slot]);
     }
+    if (r == 0 && lane == 0) tell_join(pl, walk, g, true, total);
   }
   if (!ok && lane == 0) flag_error(p.err, PKVD_ERR_TIMEOUT);
   if (lane == 0)
     for (int g2 = 0; g2 < 2; ++g2)             // no copy is in flight when the CTA leaves
       if (used[g2] > 0) wait_bounded(&bars[kQFull + g2], (used[g2] - 1) & 1);
-  if (own && blockIdx.x == 0 && !pl.planned) { // for the merge
-    if (!waited) pdl_wait();
-    OwnStart::tell(pl, lane, p.err, before, total, bad);
-  }
 }
 
 // Host: the parameters, without the shape of a Q tile's rows.
