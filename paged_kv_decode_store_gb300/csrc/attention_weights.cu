@@ -9,7 +9,9 @@
 // (4 bytes a query head and key: 1 / 16 of the K/V bytes for 8 query heads a KV
 // head of 128 in 16 bits), the merge kernel the rows' statistics, and this kernel,
 // bound by bytes, turns scores into weights.  Each element has one thread, so
-// no atomics: the sums are the same in every run.
+// no atomics: the sums are the same in every run.  64 rows of up to 32,768 keys, 64
+// + 8 heads of 128 in bf16, take 408 us where the plain call takes 358 (floor 322): the
+// partition kernel 361, this one 40 for 137 MB of scores, which do not stay in L2.
 #include "attention_kernels.cuh"
 
 namespace pkvd {

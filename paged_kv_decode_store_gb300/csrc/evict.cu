@@ -18,7 +18,7 @@
 // no barrier an element.  Exact: whole-number arithmetic on the weights' bits.
 //
 // Bound by instructions (59 % of the issue slots) and the barriers between the
-// passes: 64 x 8 rows of 4,096 to 32,768 take 51 us, of which their bytes are 15;
+// passes: 64 x 8 rows of 4,096 to 32,768 take 50 us, of which their bytes are 15;
 // 62 with every pass over the whole row and rows in order.  The loops are short
 // code on purpose: a form with half of the weights in registers, its passes
 // written out, took 14 us for a row of 50 instead of 8: it waited for instructions.

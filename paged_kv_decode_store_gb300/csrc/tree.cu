@@ -1,5 +1,5 @@
 // Attention for trees of drafted tokens over the paged cache: the plan, the
-// fp32 kernel and the merge; and the walk that says which drafts stay.
+// CUDA-core kernel and the merge; and the walk that says which drafts stay.
 //
 // Node t of sequence i's tree is its drafted row t, stored behind the cached
 // tokens (position cached_i + t of the block table); parents[t] < t, or -1 for
@@ -9,14 +9,19 @@
 // over the cached keys (j < cached_i) and t's ancestors and t itself.  Token
 // positions are cached_i + depth; a window and a distance bias count those.
 //
-// The plan kernel turns parents into one bit a (node, ancestor) -- the window
-// applied, so that a set bit is a visible key and the number of bits above one
-// is its distance -- and sums up the batch's pieces (tree_plan.cuh).
-//
-// The fp32 kernel (fp32 caches, 16-bit ones whose layout the tensor cores'
-// copies cannot walk) keeps 32 keys of K and V in shared memory and four query
-// rows a warp: lane j scores key j, then owns D / 32 dims of the sums.  Bound by
-// shared-memory reads (eight per sixteen multiply-adds).
+// Parents become one bit a (node, ancestor) -- the window applied, so that a set
+// bit is a visible key and the number of bits above one is its distance.  Three
+// kernels compute the attention, chosen by type, layout and rows a tree (max_seqlen_q
+// times the query heads of a KV head):
+//   tree_few.cu, 16 bits, up to 64 rows: 32 sequences of 8 nodes, 48 + 8 heads of
+//     128 over 2,048 tokens take 62 us (71 in tree_tc.cu; of 64 dims 51.5,
+//     55.5 there; 24 sequences of up to 33 capped rows in a window 62, 64.5);
+//   tree_tc.cu, 16 bits, more rows: up to 16 nodes there take 75 us;
+//   below, fp32 and 16-bit caches whose layout the tensor copies cannot walk: four
+//     sequences of up to 5 nodes in 15 us, as much as its launches.
+// The last keeps 32 keys of K and V in shared memory and four query rows a warp:
+// lane j scores key j, then owns D / 32 dims of the sums.  Bound by shared-memory
+// reads (eight per sixteen multiply-adds).
 #include "score_mod.cuh"
 #include "tree_plan.cuh"
 

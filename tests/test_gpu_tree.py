@@ -121,6 +121,19 @@ def test_many_short_sequences(path):
     run_tree(pk, ("bf16", 4, 2, 64, 16, path), qlen, cached, (0.0, "geometric", 0), seed=8, every=5)
 
 
+@pytest.mark.parametrize("path", [1, 3])
+@pytest.mark.parametrize("seqs", [32, 33, 128, 129])
+def test_batches_around_a_warp_and_its_plan(seqs, path):
+    """Slices that every CTA finds by itself and those of a plan, with empty sequences at both ends and between."""
+    pk = require_gpu()
+    rng = np.random.default_rng(seqs)
+    qlen = rng.integers(0, 6, seqs)
+    qlen[[0, seqs // 2, seqs - 1]] = 0
+    qlen[1], qlen[seqs - 2] = 5, 3
+    cached = rng.integers(0, 600, seqs)
+    run_tree(pk, ("f16", 4, 2, 64, 16, path), qlen.tolist(), cached.tolist(), (0.0, None, 0), seed=seqs, every=3)
+
+
 def test_max_seqlen_above_every_tree():
     pk = require_gpu()
     run_tree(pk, ("bf16", 16, 2, 128, 16, 3), [3, 1], [50, 300], seed=9, max_q=256)
