@@ -19,7 +19,8 @@
 //
 // Bound by instructions (59 % of the issue slots) and the barriers between the
 // passes: 64 x 8 rows of 4,096 to 32,768 take 50 us, of which their bytes are 15;
-// 62 with every pass over the whole row and rows in order.  The loops are short
+// 62 with every pass over the whole row and rows in order (512 equal rows of
+// 16,384: 39; 43 with a weight a load instead of four).  The loops are short
 // code on purpose: a form with half of the weights in registers, its passes
 // written out, took 14 us for a row of 50 instead of 8: it waited for instructions.
 #include <climits>
@@ -58,60 +59,73 @@ struct Row {
   int lo, hi, left;                    // [lo, hi) compete for `left` places behind the first lo
 };
 
-// This warp's part: positions [first, n), 32 at a time; step i's of this thread is
-// held[i * kThreads] for i < kPer, behind that it is read where it lies.
+// This warp's part: words [from, n), of which word w is position first + w (the
+// first warp's may begin up to three before, on a boundary of 16 bytes); the first
+// kPer * 32 are held, what is behind is read where it lies.
 struct Part {
-  const float* src;                    // this lane's first
+  const float* src;                    // word 0
   uint32_t* held;
-  int first, mine, steps;              // positions from this lane's first to the end; steps: a multiple of four
-  __device__ Part(const Row& row, uint32_t* held, int warp, int lane) : held(held) {
-    const int span = row.hi - row.lo, seg = ((span + kWarps - 1) / kWarps + 31) / 32 * 32;
-    first = row.lo + (int)min((int64_t)warp * seg, (int64_t)span);
-    const int n = row.lo + (int)min((int64_t)warp * seg + seg, (int64_t)span);
-    src = row.w + first + lane;
-    mine = n - first - lane;
-    steps = ((n - first + 31) / 32 + 3) / 4 * 4;
+  int first, from, n, steps;           // steps of 32 words: a multiple of four
+  bool beyond;                         // are there parts with more than what is held?
+  __device__ Part(const Row& row, uint32_t* held, int warp) : held(held) {
+    const int ahead = (int)(reinterpret_cast<uintptr_t>(row.w + row.lo) / 4 % 4);
+    const int span = row.hi - row.lo + ahead, seg = ((span + kWarps - 1) / kWarps + 31) / 32 * 32;
+    const int begin = (int)min((int64_t)warp * seg, (int64_t)span);
+    first = row.lo - ahead + begin;
+    from = warp == 0 ? ahead : 0;
+    n = (int)min((int64_t)begin + seg, (int64_t)span) - begin;
+    src = row.w + first;
+    steps = ((n + 31) / 32 + 3) / 4 * 4;
+    beyond = seg > kPer * 32;
   }
   // 0 where there is none
-  __device__ uint32_t read(int i) const { return (int64_t)i * 32 < mine ? ordered_bits(__float_as_uint(src[(int64_t)i * 32])) : 0u; }
-  __device__ void ask() const {
-    const int n = min(steps, kPer);
-#pragma unroll 4
-    for (int i = 0; i < n; ++i) {
-      if (i * 32 < mine)
-        asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(held + i * kThreads)), "l"(src + i * 32)
-                     : "memory");
+  __device__ uint32_t read(int w) const { return w < n ? ordered_bits(__float_as_uint(src[w])) : 0u; }
+  __device__ void ask(int lane) const {
+#pragma unroll 1
+    for (int w = lane * 4; w < min(steps, kPer) * 32; w += 128) {
+      if (w >= from && w + 4 <= n) {
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(held + w)), "l"(src + w) : "memory");
+      } else {
+        for (int e = w; e < w + 4; ++e)
+          if (e >= from && e < n)
+            asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(held + e)), "l"(src + e) : "memory");
+      }
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   }
-  // what was asked for has come: f(bits in order) of every one
+  // What was asked for has come (each lane's own): f(bits in order) of every one, in
+  // no order.
   template <typename F>
-  __device__ void take_in(F f) const {
+  __device__ void take_in(int lane, F f) const {
     asm volatile("cp.async.wait_group 0;" ::: "memory");
-    const int n = min(steps, kPer);
-#pragma unroll 4
-    for (int i = 0; i < n; ++i) {
-      const uint32_t x = i * 32 < mine ? ordered_bits(held[i * kThreads]) : 0u;
-      held[i * kThreads] = x;
-      f(x);
+#pragma unroll 2
+    for (int w = lane * 4; w < min(steps, kPer) * 32; w += 128) {
+      uint4 x = *reinterpret_cast<const uint4*>(held + w);
+      uint32_t* const v = &x.x;
+      const bool whole = w >= from && w + 4 <= n;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        v[e] = whole || (w + e >= from && w + e < n) ? ordered_bits(v[e]) : 0u;
+        f(v[e]);
+      }
+      *reinterpret_cast<uint4*>(held + w) = x;
     }
 #pragma unroll 4
-    for (int i = kPer; i < steps; ++i) f(read(i));
+    for (int i = kPer; i < steps; ++i) f(read(i * 32 + lane));
   }
-  // f(step, bits in order), every lane of the warp alike
+  // The same again.
   template <typename F>
-  __device__ void each(F f) const {
-    const int n = min(steps, kPer);
-#pragma unroll 4
-    for (int i = 0; i < n; ++i) f(i, held[i * kThreads]);
-#pragma unroll 1
-    for (int i = kPer; i < steps; i += 4) {
-      uint32_t x[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) x[e] = read(i + e);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) f(i + e, x[e]);
+  __device__ void each(int lane, F f) const {
+#pragma unroll 2
+    for (int w = lane * 4; w < min(steps, kPer) * 32; w += 128) {
+      const uint4 x = *reinterpret_cast<const uint4*>(held + w);
+      f(x.x);
+      f(x.y);
+      f(x.z);
+      f(x.w);
     }
+#pragma unroll 4
+    for (int i = kPer; i < steps; ++i) f(read(i * 32 + lane));
   }
 };
 
@@ -139,14 +153,14 @@ __device__ __forceinline__ int by_length(const int32_t* __restrict__ lens, int n
 
 __global__ void __launch_bounds__(kThreads, 2) evict_select_kernel(const EvictArgs a, int ranked) {
   extern __shared__ __align__(16) uint32_t sm[];
-  __shared__ int warp_sum[2][kWarps];
+  __shared__ int warp_sum[2][kWarps], listed_by[kWarps];
   __shared__ uint32_t found_digit;
   __shared__ int found_left;
   uint32_t* const hist = sm;                               // [kBins][copies]
   const int seq = ranked ? by_length(a.context_lens, (int)gridDim.y, (int)blockIdx.y, reinterpret_cast<int*>(sm)) : (int)blockIdx.y;
   pdl_wait();          // (and no early trigger: counts are the next call's lengths, which it reads before it waits)
   const int h = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  uint32_t* const held = sm + kHist + tid;
+  uint32_t* const held = sm + kHist + warp * (kPer * 32);
   uint32_t* const list = sm + kBins + warp * kList;
   int c = a.context_lens[seq];
   if (c < 0 || c > a.length) {
@@ -182,14 +196,15 @@ __global__ void __launch_bounds__(kThreads, 2) evict_select_kernel(const EvictAr
   row.hi = c - recent;
   row.left = count - sink - recent;
   const bool selects = row.left > 0;
-  Part part(row, held, warp, lane);
+  Part part(row, held, warp);
   if (selects) {
-    part.ask();
+    part.ask(lane);
+    if (tid < kWarps) listed_by[tid] = 0;
     for (int i = tid; i < kBins * kCopies / 4; i += kThreads) reinterpret_cast<uint4*>(hist)[i] = make_uint4(0, 0, 0, 0);
   }
   // rows that are read again while they are written in place: the weights follow
   // when every position is known
-  const bool later = row.wo == row.w && selects && row.hi - row.lo > kPer * kThreads;
+  const bool later = row.wo == row.w && selects && part.beyond;
   if (row.wo != row.w) behind();
 #pragma unroll 1
   for (int j = count + tid; j < a.keep; j += kThreads) row.out[j] = -1;
@@ -213,7 +228,7 @@ __global__ void __launch_bounds__(kThreads, 2) evict_select_kernel(const EvictAr
       // counts nowhere, so that rows of few do not pile up there)
       if (pass == 0) {
         __syncthreads();               // (emptied above)
-        part.take_in([&](uint32_t x) {
+        part.take_in(lane, [&](uint32_t x) {
           const uint32_t k = key_of(x);
           if (k != 0u) atomicAdd(bins + (k >> 21) * kCopies, 1u);
         });
@@ -227,7 +242,7 @@ __global__ void __launch_bounds__(kThreads, 2) evict_select_kernel(const EvictAr
             if (k >> above == kth >> above) atomicAdd(hist + ((k >> shift) & digits), 1u);
           }
         } else {
-          part.each([&](int, uint32_t x) {
+          part.each(lane, [&](uint32_t x) {
             const uint32_t k = key_of(x);
             if (k != 0u && k >> above == kth >> above) atomicAdd(bins + ((k >> shift) & digits) * kCopies, 1u);
           });
@@ -277,15 +292,16 @@ __global__ void __launch_bounds__(kThreads, 2) evict_select_kernel(const EvictAr
       // two digits are looked for there.  (Digit 0 has what is no weight.)
       const uint32_t first = found_digit;
       if (first != 0u)
-        part.each([&](int, uint32_t x) {
+        part.each(lane, [&](uint32_t x) {
           const uint32_t k = key_of(x), d = k >> 21;
           more += d > first;
-          const uint32_t b = __ballot_sync(FULL_MASK, d == first);
-          if (b == 0u) return;
-          const int to = fill + __popc(b & ((1u << lane) - 1u));
-          if (d == first && to < kList) list[to] = k;
-          fill += __popc(b);
+          if (d == first) {            // (in whatever order: they are counted)
+            const int to = atomicAdd(&listed_by[warp], 1);
+            if (to < kList) list[to] = k;
+          }
         });
+      __syncwarp();
+      fill = listed_by[warp];
       listed = !__syncthreads_or(first == 0u || fill > kList);
     }
     // in order: what is larger, and of those equal to the last one the first `left`
@@ -293,7 +309,7 @@ __global__ void __launch_bounds__(kThreads, 2) evict_select_kernel(const EvictAr
       for (int i = lane; i < fill; i += 32) more += list[i] > kth, tie += list[i] == kth;
     } else {
       more = 0;
-      part.each([&](int, uint32_t x) {
+      part.each(lane, [&](uint32_t x) {
         const uint32_t k = key_of(x);
         more += k > kth;
         tie += k == kth;
@@ -344,15 +360,15 @@ __global__ void __launch_bounds__(kThreads, 2) evict_select_kernel(const EvictAr
     };
     if (more > 0 || (tie > 0 && rank < left)) {
       const int n = min(part.steps, kPer);
-      uint32_t next = part.held[0];    // (a step is 32 of this warp's: n > 0)
+      uint32_t next = held[lane];      // (a step is 32 of this warp's: n > 0)
 #pragma unroll 1
       for (int i = 0; i < n; ++i) {
         const uint32_t x = next;
-        next = part.held[min(i + 1, kPer - 1) * kThreads];
+        next = held[min(i + 1, kPer - 1) * 32 + lane];
         take(i, x);
       }
 #pragma unroll 1
-      for (int i = kPer; i < part.steps; ++i) take(i, part.read(i));
+      for (int i = kPer; i < part.steps; ++i) take(i, part.read(i * 32 + lane));
       flush();
     }
     if (later) {                       // position r comes from r or behind it: a stretch read before it is written

@@ -246,6 +246,17 @@ def test_select_of_many_rows(seqs):
     run_select(pk, w, ctx[::-1], 60, 3, 10, in_place=True)
 
 
+@pytest.mark.parametrize("more", [-1, 0, 1, 40])
+@pytest.mark.parametrize("sink", [0, 1, 2, 3, 4])
+def test_select_in_place_where_memory_on_the_chip_ends(sink, more):
+    """Rows about as long as what a row's kernel holds, beginning at every offset from a boundary of 16 bytes."""
+    pk = require_gpu()
+    n = 44 * 512 + sink + more
+    w = torch.empty(1, 2, n).exponential_(1.0, generator=torch.Generator().manual_seed(sink))
+    run_select(pk, w, [n], 20000, sink, 5, in_place=True)
+    run_select(pk, w, [n - 3], 300, sink, 0)
+
+
 def test_select_long_rows_of_other_strides():
     """Rows longer than one pass over shared memory would hold, inside a wider buffer at an odd offset."""
     pk = require_gpu()
