@@ -570,7 +570,8 @@ pkvd_status pkvd_prefill_attention_mod(void* out, const void* q, const pkvd_cach
  *         aligned; parents int32 [total_q]; cu_seqlens_q, cu_seqlens_k,
  *         block_tables as in pkvd_prefill_attention; max_seqlen_q >= every n_i.
  *         Cache rows before every node's window and past k_len_i are never
- *         weighed; drafted rows of the same tree must be stored (finite).
+ *         weighed; a tree's drafted rows must be stored.  What lies in a row that
+ *         a node does not see does not reach it, infinities and NaN included.
  * Output: out [total_q, num_q_heads, head_dim], 16-byte aligned, not q; rows t
  *         >= cu_seqlens_q[num_seqs] are not written.  Scores, softmax statistics
  *         and sums are fp32; PKVD_PATH_TC rounds the softmax weights to the cache's
