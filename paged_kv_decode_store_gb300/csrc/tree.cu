@@ -527,7 +527,7 @@ __global__ void __launch_bounds__(kAcceptWarps * 32) tree_accept_kernel(const Ac
 // ------------------------------------------------------------------- host
 size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 
-int words_of(int max_q) { return max_q <= 64 ? 2 : (max_q + 31) / 32; }   // an even number
+int words_of(int max_q) { return (max_q + 31) / 32; }
 
 bool few_rows(int group, int max_q) { return group * max_q <= kTreeFewRows; }
 
