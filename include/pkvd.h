@@ -686,7 +686,8 @@ pkvd_status pkvd_paged_decode_attention_weights(void* out, const void* q, const 
  * Inputs: weights f32 as above, rows of `length`; context_lens int32 [num_seqs]
  *         <= length; sink, recent >= 0, sink + recent <= keep.
  * Output: positions int32 [num_seqs, heads, keep], ascending, -1 behind; counts
- *         int32 [num_seqs] = min(context_lens[i], keep); weights_out (or NULL) at
+ *         int32 [num_seqs] = min(context_lens[i], keep), nowhere over context_lens
+ *         (PKVD_INVALID_ARG: other rows still read those); weights_out (or NULL) at
  *         the same strides: the weights that stay, closed up in the same order,
  *         zeros behind them up to `length`.  It may be weights (in place), else
  *         must not overlap it.

@@ -83,6 +83,12 @@ bool score_mod(const pkvd_score_mod* m, float scale, bool prefill, ScoreMod* out
   return true;
 }
 
+// Do two ranges of bytes meet?
+bool overlap(const void* a, size_t na, const void* b, size_t nb) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y + nb && y < x + na;
+}
+
 pkvd_status from_cuda(cudaError_t e) { return e == cudaSuccess ? PKVD_OK : PKVD_CUDA_ERROR; }
 
 }  // namespace
@@ -842,6 +848,8 @@ pkvd_status pkvd_evict_select(int32_t* positions, int32_t* counts, float* weight
   if (!positions || !counts || !weights || !context_lens) return PKVD_INVALID_ARG;
   if ((num_seqs > 1 && seq_stride < length) || (heads > 1 && head_stride < length)) return PKVD_INVALID_ARG;
   if (reinterpret_cast<uintptr_t>(weights) % 4 || reinterpret_cast<uintptr_t>(weights_out) % 4) return PKVD_UNSUPPORTED_SHAPE;
+  const size_t lens = (size_t)num_seqs * sizeof(int32_t);
+  if (overlap(counts, lens, context_lens, lens)) return PKVD_INVALID_ARG;   // a row's length is read where others' counts are written
   EvictArgs a;
   a.weights = weights;
   a.weights_out = weights_out;
