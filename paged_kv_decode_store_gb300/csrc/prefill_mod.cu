@@ -423,7 +423,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_mod_kernel(const __grid_c
         const int ks = key_of(t);
         if (t >= n || lane >= nseg || ks > hi || ks + p.seg_rows - 1 < lo) return kNone;
         if (ks >= hole && ks + p.seg_rows <= hole_end) return kNone;
-        return __ldg(table + (ks >> p.block_shift));
+        return max(__ldg(table + (ks >> p.block_shift)), -1);   // (no id is taken for kNone)
       };
       auto copy_k = [&](int t, int b) {
         wait(kKEmpty + kstg, kpar);

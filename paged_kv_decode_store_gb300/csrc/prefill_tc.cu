@@ -223,7 +223,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) prefill_tc_kernel(const __grid_
       if (tt >= n || lane >= nseg) return kNone;
       const int ks = (kt_first + tt) * kTcKeys + lane * p.seg_rows;
       if (ks > hi || ks + p.seg_rows - 1 < lo) return kNone;
-      return __ldg(table + ks / p.block_size);
+      return max(__ldg(table + ks / p.block_size), -1);         // (no id is taken for kNone)
     };
     // each lane's block id of tiles t .. t + 3
     int b0 = fetch(0), b1 = fetch(1), b2 = fetch(2), b3 = fetch(3);

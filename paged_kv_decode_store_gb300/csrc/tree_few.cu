@@ -156,7 +156,7 @@ __device__ __forceinline__ void copy_tiles(const TcTree& p, uint64_t* bars, uint
     auto fetch = [&](int t) -> int {
       const int ks = tile_at(kt_last, n, late, t) * kTcKeys + lane * p.seg_rows;
       if (t >= n || lane >= nseg || ks > hi || ks + p.seg_rows - 1 < lo) return kNone;
-      return __ldg(table + (ks >> p.block_shift));
+      return max(__ldg(table + (ks >> p.block_shift)), -1);     // (no id is taken for kNone)
     };
     int b[4];                                  // block ids of tile t and the three after it
 #pragma unroll

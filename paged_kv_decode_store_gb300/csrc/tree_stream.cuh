@@ -224,7 +224,7 @@ __device__ __forceinline__ void tree_copy_kv(const TcTree& p, uint64_t* bars, ui
     auto fetch = [&](int t) -> int {
       const int ks = key_of(t);
       if (t >= n || lane >= nseg || ks > hi || ks + p.seg_rows - 1 < lo) return kNone;
-      return __ldg(table + (ks >> p.block_shift));
+      return max(__ldg(table + (ks >> p.block_shift)), -1);     // (no id is taken for kNone)
     };
     auto copy_k = [&](int t, int b) {
       wait(kKEmpty + kstg, kpar);
