@@ -379,6 +379,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_mod_kernel(const __grid_c
     constexpr int kNone = INT_MIN;             // a segment of rows that are not read: nothing to load
     bool ok = true;
     int kstg = 0, vstg = 0, landed = 0;        // next stages; phases of kVCut
+    bool cutting = false;                      // a copy is under way to kVCut of the next V stage
     uint32_t kpar = 1, vpar = 1;               // parities of their release (nothing to wait for in the first round)
     auto wait = [&](int bar, uint32_t parity) {
       if (ok) ok = __all_sync(FULL_MASK, wait_bounded(&bars[bar], parity));
@@ -448,8 +449,9 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_mod_kernel(const __grid_c
         copy(&p.tmap_v, dst, (cut ? kVCut : kVFull) + vstg, kbase + lane * p.seg_rows, hk, b[0]);
         if (cut) {
           wait(kVCut + vstg, (landed >> vstg) & 1);
-          landed ^= 1 << vstg;
+          cutting = !ok;
           if (!ok) break;
+          landed ^= 1 << vstg;
           for (int rr = lane; rr < kTcKeys; rr += 32) {
             const int kp = kbase + rr;
             if (kp >= lo && kp <= hi && !(kp >= hole && kp < hole_end)) continue;
@@ -475,6 +477,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_mod_kernel(const __grid_c
       // (a stage's full barrier is behind its release, or one phase ahead of it)
       for (int u = 0; u < kKStages; ++u) wait_bounded(&bars[kKFull + u], (kpar ^ (u < kstg ? 0u : 1u)) ^ 1u);
       for (int u = 0; u < kVStages; ++u) wait_bounded(&bars[kVFull + u], (vpar ^ (u < vstg ? 0u : 1u)) ^ 1u);
+      if (cutting) wait_bounded(&bars[kVCut + vstg], (landed >> vstg) & 1);
     }
   } else if (warp == kQWarp) {
     // ------------------------------------------------- items and Q producer

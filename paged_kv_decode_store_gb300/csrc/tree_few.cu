@@ -141,6 +141,7 @@ __device__ __forceinline__ void copy_tiles(const TcTree& p, uint64_t* bars, uint
   constexpr int kNone = INT_MIN;               // a segment of rows that are not read: nothing to load
   bool ok = true;
   int stg = 0, landed = 0;                     // next stage; phases of kVCut
+  bool cutting = false;                        // a copy is under way to kVCut of the next stage
   uint32_t par = 1;                            // parity of its release (nothing to wait for in the first round)
   auto wait = [&](int bar, uint32_t parity) {
     if (ok) ok = __all_sync(FULL_MASK, wait_bounded(&bars[bar], parity));
@@ -193,8 +194,9 @@ __device__ __forceinline__ void copy_tiles(const TcTree& p, uint64_t* bars, uint
       }
       if (cut) {
         wait(kVCut + stg, (landed >> stg) & 1);
-        landed ^= 1 << stg;
+        cutting = !ok;
         if (!ok) break;
+        landed ^= 1 << stg;
         if (tidy_values<T, H>(tile, kbase, sight, lane) && lane == 0) cur.odd = 1;
         fence_proxy_async_smem();
         __syncwarp();
@@ -214,6 +216,7 @@ __device__ __forceinline__ void copy_tiles(const TcTree& p, uint64_t* bars, uint
     flag_error(p.err, PKVD_ERR_TIMEOUT);
     // (a stage's full barrier is behind its release, or one phase ahead of it)
     for (int u = 0; u < kStages; ++u) wait_bounded(&bars[full + u], (par ^ (u < stg ? 0u : 1u)) ^ 1u);
+    if (cutting) wait_bounded(&bars[kVCut + stg], (landed >> stg) & 1);
   }
 }
 

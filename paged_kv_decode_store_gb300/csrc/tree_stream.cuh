@@ -182,6 +182,7 @@ __device__ __forceinline__ void tree_copy_kv(const TcTree& p, uint64_t* bars, ui
   constexpr int kNone = INT_MIN;             // a segment of rows that are not read: nothing to load
   bool ok = true;
   int kstg = 0, vstg = 0, landed = 0;        // next stages; phases of kVCut
+  bool cutting = false;                      // a copy is under way to kVCut of the next V stage
   uint32_t kpar = 1, vpar = 1;               // parities of their release (nothing to wait for in the first round)
   auto wait = [&](int bar, uint32_t parity) {
     if (ok) ok = __all_sync(FULL_MASK, wait_bounded(&bars[bar], parity));
@@ -249,8 +250,9 @@ __device__ __forceinline__ void tree_copy_kv(const TcTree& p, uint64_t* bars, ui
       copy(&p.tmap_v, dst, (cut ? kVCut : kVFull) + vstg, kbase + lane * p.seg_rows, hk, b[0]);
       if (cut) {
         wait(kVCut + vstg, (landed >> vstg) & 1);
-        landed ^= 1 << vstg;
+        cutting = !ok;
         if (!ok) break;
+        landed ^= 1 << vstg;
         if (tidy_values<T, H>(dst, kbase, sight, lane) && lane == 0) cur.odd = 1;
         fence_proxy_async_smem();
         __syncwarp();
@@ -271,6 +273,7 @@ __device__ __forceinline__ void tree_copy_kv(const TcTree& p, uint64_t* bars, ui
     // (a stage's full barrier is behind its release, or one phase ahead of it)
     for (int u = 0; u < kKStages; ++u) wait_bounded(&bars[kKFull + u], (kpar ^ (u < kstg ? 0u : 1u)) ^ 1u);
     for (int u = 0; u < kVStages; ++u) wait_bounded(&bars[kVFull + u], (vpar ^ (u < vstg ? 0u : 1u)) ^ 1u);
+    if (cutting) wait_bounded(&bars[kVCut + vstg], (landed >> vstg) & 1);
   }
 }
 
