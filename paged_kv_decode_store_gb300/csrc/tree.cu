@@ -471,9 +471,9 @@ __global__ void __launch_bounds__(kAcceptWarps * 32) tree_accept_kernel(const Ac
   pdl_wait();          // the target's choices come from the sampler (no early trigger: counts may be lengths)
   const int i = blockIdx.x * kAcceptWarps + (threadIdx.x >> 5), lane = threadIdx.x & 31;
   if (i >= num_seqs) return;
-  const int q0 = a.cu_q[i], n = a.cu_q[i + 1] - q0, cached = a.cu_k[i + 1] - a.cu_k[i] - n;
+  const int q0 = a.cu_q[i], n = a.cu_q[i + 1] - q0, klen = a.cu_k[i + 1] - a.cu_k[i], cached = klen - n;
   int count = 0;
-  const bool ok = q0 >= 0 && n >= 0 && n <= kTreeMaxNodes && cached >= 0 && (int64_t)q0 + n <= a.total_q;
+  const bool ok = q0 >= 0 && n >= 0 && n <= kTreeMaxNodes && klen >= n && (int64_t)q0 + n <= a.total_q;
   if (!ok && lane == 0) flag_error(a.err, PKVD_ERR_CONTEXT);
   int32_t* pos = a.positions + (int64_t)i * a.max_path;
   int32_t* tok = a.tokens + (int64_t)i * a.max_path;

@@ -51,7 +51,8 @@ __device__ __forceinline__ TreeSeq tree_seq(const TreePlan& p, int q0, int n, in
   s.klen = klen;
   s.cached = s.klen - s.n;
   s.units = s.tiles = s.lo = s.lo_tile = 0;
-  const bool ok = s.q0 >= 0 && s.n >= 0 && s.n <= p.max_q && s.cached >= 0 && (int64_t)s.q0 + s.n <= p.total_q &&
+  // (not by the sign of cached: a length near -2^31 minus n is a large number again)
+  const bool ok = s.q0 >= 0 && s.n >= 0 && s.n <= p.max_q && s.klen >= s.n && (int64_t)s.q0 + s.n <= p.total_q &&
                   s.klen <= p.table_tokens;
   if (!ok) s.n = -1;
   if (s.n <= 0) return s;

@@ -64,3 +64,28 @@ def test_prefill(case, softcap):
     call = lambda t, err: pk.prefill_attention(q, kc, vc, t, cumulative(qlen), cumulative(klen), max(qlen), d ** -0.5, err=err,
                                                path=pk.PATH_TC, softcap=softcap)
     same_with_every_bad_id(pk, call, tables, [(0, 0), (0, 100), (0, 101), (0, 150), (1, 30)], zero)
+
+
+@pytest.mark.parametrize("klen", [-2 ** 31, -2 ** 31 + 3, -1, 0, 2, 2 ** 31 - 1])
+@pytest.mark.parametrize("case", [("bf16", 16, 3), ("bf16", 64, 3), ("f32", 4, 1)], ids=lambda c: "-".join(map(str, c)))
+def test_lengths_that_no_tree_has(case, klen):
+    """A k_len below the drafts' number or past the table, whatever its difference wraps to, leaves its sequence out."""
+    pk = require_gpu()
+    name, hq, path = case
+    dt = {"f32": torch.float32, "bf16": torch.bfloat16}[name]
+    kc, vc, tables, _ = cache_of([100, 60], 2, 64, 16, dt, 8)
+    n = 20 if hq == 64 else 3
+    q = torch.randn(2 * n, hq, 64, generator=torch.Generator().manual_seed(9)).to(dt).to(DEV)
+    err = torch.zeros(1, dtype=torch.int32, device=DEV)
+    chain = ints((list(range(-1, n - 1))) * 2)
+    cu_k = torch.tensor([-60, 0, klen], dtype=torch.int64).to(torch.int32).to(DEV)       # the first sequence is a good one
+    cu_q = cumulative([n, n])
+    out = torch.full_like(q, 7.0)
+    pk.tree_attention(q, kc, vc, tables, cu_q, cu_k, chain, n, 0.125, out=out, err=err, path=path)
+    assert err.item() == pk.ERR_CONTEXT
+    assert torch.all(out[n:] == 7.0) and torch.isfinite(out[:n]).all() and not torch.all(out[:n] == 7.0)
+    if klen != 2 ** 31 - 1:                                  # (the walk has no table: any length from n on is one)
+        err.zero_()
+        ids = torch.zeros(2 * n, dtype=torch.int32, device=DEV)
+        _, first, counts, _ = pk.tree_accept(ids, chain, ids, cu_q, cu_k, 4, err=err)
+        assert err.item() == pk.ERR_CONTEXT and counts.tolist() == [min(n, 4), 0] and first.tolist() == [60 - n, 0]
