@@ -405,7 +405,8 @@ __global__ void __launch_bounds__(256) tree_merge_kernel(const TreePlan p, T* __
     for (int e = 0; e < R; ++e)
 #pragma unroll
       for (int i = 0; i < ROWS; ++i) {
-        if (ml[e][i].x == -INFINITY) continue;           // saw none of the keys
+        // saw none of the keys (where all that it saw were NaN the sum is one, and no maximum was found either)
+        if (ml[e][i].y == 0.f) continue;
         const float Mn = fmaxf(M[i], ml[e][i].x), cs = exp2f(M[i] - Mn), cr = exp2f(ml[e][i].x - Mn);
         L[i] = L[i] * cs + ml[e][i].y * cr;
         o[i].x = o[i].x * cs + x[e][i].x * cr;
