@@ -132,9 +132,17 @@ struct SmemHdr {
 };
 
 // A row's statistics as the keys' weights need them: the maximum and one over
-// the sum; a row without a readable key gives its keys nothing.
+// the sum; a row without a readable key gives its keys nothing.  (Not l > 0: with
+// a NaN among the scores the sum is one, and so is every weight.)
 __device__ __forceinline__ float2 row_stats(float m, float l) {
-  return l > 0.f ? make_float2(m, 1.f / l) : make_float2(0.f, 0.f);
+  return l == 0.f ? make_float2(0.f, 0.f) : make_float2(m, 1.f / l);
+}
+// What the weights so far are taken against.  Where the scores are counted it is
+// a number even when none of them was one (or all were -inf), so that a sum of 0
+// means that no weight was seen: the merge leaves such records out, and no other.
+template <bool SCORES>
+__device__ __forceinline__ float weight_base(float top) {
+  return SCORES && top == -INFINITY ? 0.f : top;
 }
 
 // ----------------------------------------------------------- consumers
@@ -222,8 +230,9 @@ struct FmaConsumer {
           for (int g = 0; g < GMAX; ++g) {
             if (g < p.G) {
               const float mn = fmaxf(m[j][g], s[g]);
-              const float corr = exp2f(m[j][g] - mn);
-              const float pr = exp2f(s[g] - mn);
+              const float ref = weight_base<kScores>(mn);
+              const float corr = exp2f(m[j][g] - ref);
+              const float pr = exp2f(s[g] - ref);
               l[j][g] = l[j][g] * corr + pr;
 #pragma unroll
               for (int v = 0; v < VEC; ++v) acc[j][g][v] = fmaf(acc[j][g][v], corr, pr * vf[v]);
@@ -385,10 +394,11 @@ struct MmaConsumer {
         mx1 = fmaxf(mx1, __shfl_xor_sync(FULL_MASK, mx1, o));
       }
       const float mn0 = fmaxf(m[j][0], mx0), mn1 = fmaxf(m[j][1], mx1);
-      const float c0 = exp2f(m[j][0] - mn0), c1 = exp2f(m[j][1] - mn1);
+      const float r0 = weight_base<kScores>(mn0), r1 = weight_base<kScores>(mn1);
+      const float c0 = exp2f(m[j][0] - r0), c1 = exp2f(m[j][1] - r1);
       constexpr float lift = MOD ? kWeightLift<T> : 0.f;
-      const float p0 = exp2f(x0 - mn0 + lift), p1 = exp2f(x1 - mn1 + lift);
-      const float p2 = exp2f(x2 - mn0 + lift), p3 = exp2f(x3 - mn1 + lift);
+      const float p0 = exp2f(x0 - r0 + lift), p1 = exp2f(x1 - r1 + lift);
+      const float p2 = exp2f(x2 - r0 + lift), p3 = exp2f(x3 - r1 + lift);
       l[j][0] = l[j][0] * c0 + p0 + p2;
       l[j][1] = l[j][1] * c1 + p1 + p3;
       m[j][0] = mn0;
@@ -822,10 +832,10 @@ __global__ void __launch_bounds__(256) lse_merge_kernel(T* __restrict__ out, con
 #pragma unroll
       for (int e = 0; e < R; ++e) {
         const float m = mk[e];
-        if (m == -INFINITY) continue;
+        if (STATS ? lk[e] == 0.f : m == -INFINITY) continue;
         const float Mn = fmaxf(M, m);
         const float cs = (M == -INFINITY) ? 0.f : exp2f(M - Mn);
-        const float cr = exp2f(m - Mn);
+        const float cr = exp2f(m - weight_base<STATS>(Mn));
         L = L * cs + lk[e] * cr;
         o.x = o.x * cs + ak[e].x * cr;
         o.y = o.y * cs + ak[e].y * cr;
