@@ -572,8 +572,8 @@ pkvd_status pkvd_prefill_attention_mod(void* out, const void* q, const pkvd_cach
  *         Cache rows before every node's window and past k_len_i are never
  *         weighed; a tree's drafted rows must be stored.  What lies in a row that
  *         a node does not see does not reach it, infinities and NaN included.
- * Output: out [total_q, num_q_heads, head_dim], 16-byte aligned, not q; rows t
- *         >= cu_seqlens_q[num_seqs] are not written.  Scores, softmax statistics
+ * Output: out [total_q, num_q_heads, head_dim], 16-byte aligned, nowhere over q
+ *         (PKVD_INVALID_ARG); rows t >= cu_seqlens_q[num_seqs] are not written.  Scores, softmax statistics
  *         and sums are fp32; PKVD_PATH_TC rounds the softmax weights to the cache's
  *         type for the product with V (f16 ones keep their bits down to 2^-17 of
  *         the row's largest; bf16 ones are taken against a reference up to 2^24

@@ -675,7 +675,8 @@ pkvd_status pkvd_tree_attention(void* out, const void* q, const pkvd_cache* cach
   if (!out || !q || !block_tables || !cu_seqlens_q || !cu_seqlens_k || !parents || max_blocks_per_seq <= 0)
     return PKVD_INVALID_ARG;
   if (!aligned16(q) || !aligned16(out)) return PKVD_UNSUPPORTED_SHAPE;
-  if (out == q) return PKVD_INVALID_ARG;       // q rows are read again where others are written
+  const size_t rows = (size_t)total_q * num_q_heads * cache->head_dim * esize(cache->dtype);
+  if (overlap(out, rows, q, rows)) return PKVD_INVALID_ARG;       // q rows are read again where others are written
   TreeArgs a;
   a.sms = device_sm_count();
   if (a.sms <= 0) return PKVD_CUDA_ERROR;
