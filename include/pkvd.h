@@ -656,7 +656,8 @@ pkvd_status pkvd_compact_cache(const pkvd_cache* cache, const int32_t* block_tab
  * Entries from context_lens[i] on are left as they were.  A buffer that starts
  * with zeros adds up a sequence's decode steps; pkvd_evict_select reads it.
  * Inputs: weights f32, element (i, h, j) at i * seq_stride + h * head_stride + j,
- *         rows of at least max_context_len; mod as for the decode call.
+ *         rows of at least max_context_len that do not meet (PKVD_INVALID_ARG);
+ *         mod as for the decode call.
  * Output: out as the decode call's; weights_out at the same strides, may be
  *         weights (in place), else must not overlap it.  Sums are fp32 in a
  *         fixed order: the same bits in every run.
@@ -683,7 +684,8 @@ pkvd_status pkvd_paged_decode_attention_weights(void* out, const void* q, const 
  * a longer one its first `sink`, its last `recent` and the heaviest of the
  * others, keep in all, the lowest position first among equal weights (-0 equals
  * 0, a NaN is above all numbers).
- * Inputs: weights f32 as above, rows of `length`; context_lens int32 [num_seqs]
+ * Inputs: weights f32 as above, rows of `length` (which may meet only without
+ *         weights_out); context_lens int32 [num_seqs]
  *         <= length; sink, recent >= 0, sink + recent <= keep.
  * Output: positions int32 [num_seqs, heads, keep], ascending, -1 behind; counts
  *         int32 [num_seqs] = min(context_lens[i], keep), nowhere over context_lens

@@ -89,6 +89,24 @@ bool overlap(const void* a, size_t na, const void* b, size_t nb) {
   return x < y + nb && y < x + na;
 }
 
+// Do two of the rows [i * seq_stride + h * head_stride, .. + length), i < n, h < heads, meet?
+bool rows_meet(int64_t n, int64_t heads, int64_t seq_stride, int64_t head_stride, int64_t length) {
+  using wide = __int128;
+  if (n > 1 && seq_stride < length) return true;
+  if (heads > 1 && head_stride < length) return true;
+  if (n <= 1 || heads <= 1) return false;
+  if (seq_stride >= (wide)(heads - 1) * head_stride + length || head_stride >= (wide)(n - 1) * seq_stride + length)
+    return false;                       // sequence by sequence, or head by head
+  // sequence i's row 0 among the rows of sequence 0
+  for (int64_t i = 1; i < n; ++i) {
+    const wide at = (wide)i * seq_stride;
+    if (at >= (wide)(heads - 1) * head_stride + length) return false;
+    const wide rest = at % head_stride, next = at / head_stride + 1;
+    if (rest < length || (next < heads && head_stride - rest < length)) return true;
+  }
+  return false;
+}
+
 pkvd_status from_cuda(cudaError_t e) { return e == cudaSuccess ? PKVD_OK : PKVD_CUDA_ERROR; }
 
 }  // namespace
@@ -820,8 +838,7 @@ pkvd_status pkvd_paged_decode_attention_weights(void* out, const void* q, const 
   if (num_seqs == 0) return PKVD_OK;
   if (num_seqs > 65535) return PKVD_UNSUPPORTED_SHAPE;
   if (!weights || !weights_out || seq_stride < 0 || head_stride < 0) return PKVD_INVALID_ARG;
-  if ((num_seqs > 1 && seq_stride < max_context_len) || (weight_heads > 1 && head_stride < max_context_len))
-    return PKVD_INVALID_ARG;
+  if (rows_meet(num_seqs, weight_heads, seq_stride, head_stride, max_context_len)) return PKVD_INVALID_ARG;
   if (reinterpret_cast<uintptr_t>(weights) % 4 || reinterpret_cast<uintptr_t>(weights_out) % 4) return PKVD_UNSUPPORTED_SHAPE;
   const int64_t rows = (int64_t)num_seqs * num_q_heads;
   const WeightsLayout lay(records, rows, max_context_len);
@@ -848,6 +865,7 @@ pkvd_status pkvd_evict_select(int32_t* positions, int32_t* counts, float* weight
   if (num_seqs == 0) return PKVD_OK;
   if (!positions || !counts || !weights || !context_lens) return PKVD_INVALID_ARG;
   if ((num_seqs > 1 && seq_stride < length) || (heads > 1 && head_stride < length)) return PKVD_INVALID_ARG;
+  if (weights_out && rows_meet(num_seqs, heads, seq_stride, head_stride, length)) return PKVD_INVALID_ARG;
   if (reinterpret_cast<uintptr_t>(weights) % 4 || reinterpret_cast<uintptr_t>(weights_out) % 4) return PKVD_UNSUPPORTED_SHAPE;
   const size_t lens = (size_t)num_seqs * sizeof(int32_t);
   if (overlap(counts, lens, context_lens, lens)) return PKVD_INVALID_ARG;   // a row's length is read where others' counts are written

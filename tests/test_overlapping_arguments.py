@@ -38,3 +38,26 @@ def test_tree_outputs_over_queries(pk, off):
     q = 64 * P
     assert pk.lib().pkvd_tree_attention(q + off, q, ctypes.byref(c), P, 8, P, P, P, 2, 20, 9, 48, 0.1, 0, None, None, 0, None,
                                         None, 0) == INVALID
+
+
+ROWS = [  # sequences, heads, their strides: rows of 100 words that meet
+    (2, 2, 100, 100), (2, 3, 250, 200), (5, 2, 100, 400), (3, 3, 299, 200), (2, 2, 101, 200), (65535, 4, 150, 65534 * 150),
+]
+
+
+@pytest.mark.parametrize("seqs,heads,s_seq,s_head", ROWS)
+def test_rows_of_weights_that_meet(pk, seqs, heads, s_seq, s_head):
+    """Two of them would be written to the same words."""
+    used = set()
+    if seqs < 100:
+        for i in range(seqs):
+            for h in range(heads):
+                row = set(range(i * s_seq + h * s_head, i * s_seq + h * s_head + 100))
+                met = bool(used & row)
+                used |= row
+                if met:
+                    break
+            if met:
+                break
+        assert met
+    assert select(pk, 16 * P, 8 * P, seqs=seqs, heads=heads, s_seq=s_seq, s_head=s_head, w_out=32 * P) == INVALID
