@@ -44,7 +44,7 @@ struct pkvd_block_manager {
   int32_t head = -1, tail = -1, nfree = 0;
   std::vector<std::string> key_of;      // empty: not registered
   std::unordered_map<std::string, int32_t> cache;
-  std::vector<int32_t> uses;            // pkvd_bm_reorder's counts, all 0 between calls
+  std::vector<int32_t> uses;            // counts of pkvd_bm_reorder and held(), all 0 between calls
   std::vector<uint8_t> opaque;          // rows that are no prompt's (an eviction's, or behind such a block)
 
   pkvd_block_manager(int32_t n, int32_t b)
@@ -207,11 +207,16 @@ pkvd_status pkvd_bm_append(pkvd_block_manager* bm, const int32_t* tokens, int32_
   return PKVD_OK;
 }
 
-// Every block of a table is held.
-static bool held(const pkvd_block_manager* bm, const int32_t* block_table, int32_t n) {
-  for (int32_t i = 0; i < n; ++i)
-    if (block_table[i] < 0 || block_table[i] >= bm->nb || bm->ref[block_table[i]] <= 0) return false;
-  return true;
+// Every block of a sequence's table is held, and listed once.
+static bool held(pkvd_block_manager* bm, const int32_t* block_table, int32_t n) {
+  int32_t i = 0;
+  for (; i < n; ++i) {
+    const int32_t b = block_table[i];
+    if (b < 0 || b >= bm->nb || bm->ref[b] <= 0 || bm->uses[b] != 0) break;
+    bm->uses[b] = 1;
+  }
+  for (int32_t j = 0; j < i; ++j) bm->uses[block_table[j]] = 0;
+  return i >= n;
 }
 
 pkvd_status pkvd_bm_reserve(pkvd_block_manager* bm, int32_t num_tokens, int32_t drafts, int32_t* block_table,
