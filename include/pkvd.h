@@ -55,8 +55,8 @@
  *     early completion (griddepcontrol.launch_dependents) still runs.  Before
  *     waiting for it they read only inputs that no kernel of this library
  *     writes while a later one may start (context lengths, cu_seqlens, parents,
- *     block tables, rotary frequencies; pkvd_evict_select, whose counts are
- *     lengths, does not signal early); everything else (q, the cache,
+ *     block tables, rotary frequencies; pkvd_evict_select and pkvd_tree_accept,
+ *     whose counts are lengths, do not signal early); everything else (q, the cache,
  *     slot_mapping, outputs, workspaces) comes after the wait.  A caller's own
  *     kernel that signals early must not write those inputs of the call that
  *     follows it.

@@ -743,8 +743,9 @@ __global__ void __launch_bounds__(256) lse_merge_kernel(T* __restrict__ out, con
   // kernel -- and possibly the kernel before it, since the partition kernel
   // lets this grid start before its own dependency wait.  That is safe by the
   // input contract of the attention call: context_lens is written by no
-  // kernel that lets its dependents start early (the library's own kernels
-  // never write it).  The partial records are read after pdl_wait().
+  // kernel that lets its dependents start early.  (The library's kernels that
+  // write lengths, the counts of evict_select_kernel and tree_accept_kernel, do
+  // not, and must not begin to.)  The partial records are read after pdl_wait().
   long long before = 0, all = 0;
   for (int r = threadIdx.x; r < num_seqs; r += blockDim.x) {
     const int c = chunks_of(ctx, r, ctx_cap, window);

@@ -19,7 +19,6 @@ constexpr int kStreamWarps = 8;           // softmax warps of a stream
 constexpr int kKvWarp = 16, kMmaWarp = 17, kQWarp = 18, kMmaWarp1 = 19;
 constexpr uint32_t kTmemCols = 512;
 enum : int { kCap = 1, kBias = 2 };       // what a call modifies, known when compiled
-constexpr float kRebase = 8.f;            // a new reference when the maximum grows by > 2^8
 
 // mbarriers: five for each stage of K and V; those of a stream take + g, S, P and
 // PV + g + 2 half
