@@ -91,7 +91,7 @@ cudaError_t launch_attention_weights(const AttnArgs& a, const WeightArgs& w, cud
   const int span = kThreads * kPer;
   // rows are of all lengths: few CTAs each that walk it, rather than many of which most find nothing
   const int64_t rows = (int64_t)w.heads * a.num_seqs, most = (ctx_cap + span - 1) / span;
-  const int64_t each = 48 * 152 / rows + 1;
+  const int64_t each = 48 * (int64_t)device_sm_count() / rows + 1;
   const dim3 grid((unsigned)(each < most ? each : most), (unsigned)w.heads, (unsigned)a.num_seqs);
   return launch_pdl(add_weights_kernel, grid, dim3(kThreads), 0, stream, (const float*)a.scores, a.score_ld,
                     (const float2*)a.stats, lift, w.in, w.out, w.seq_stride, w.head_stride, a.context_lens, ctx_cap,
