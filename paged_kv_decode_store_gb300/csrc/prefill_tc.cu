@@ -218,12 +218,12 @@ __global__ void __launch_bounds__(kTcThreads, 1) prefill_tc_kernel(const __grid_
     bool ok = true;
     if (lane == 0) asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
     uint64_t t_start = globaltimer_ns();       // the last progress
-    constexpr int kNone = INT_MIN;             // a segment that misses [lo, hi]: nothing to load
+    constexpr int kNone = -1;                  // a segment that misses [lo, hi]: nothing to load
+    const uint32_t whole = (1u << nseg) - 1u;  // at most 16 segments
+    auto is_read = [&](int ks) { return lane < nseg && ks <= hi && ks + p.seg_rows - 1 >= lo; };
     auto fetch = [&](int tt) -> int {
-      if (tt >= n || lane >= nseg) return kNone;
       const int ks = (kt_first + tt) * kTcKeys + lane * p.seg_rows;
-      if (ks > hi || ks + p.seg_rows - 1 < lo) return kNone;
-      return max(__ldg(table + ks / p.block_size), -1);         // (no id is taken for kNone)
+      return tt < n && is_read(ks) ? __ldg(table + ks / p.block_size) : kNone;
     };
     // each lane's block id of tiles t .. t + 3
     int b0 = fetch(0), b1 = fetch(1), b2 = fetch(2), b3 = fetch(3);
@@ -239,15 +239,15 @@ __global__ void __launch_bounds__(kTcThreads, 1) prefill_tc_kernel(const __grid_
         break;
       }
       if (go == 0) continue;
-      const bool good = b0 != kNone && b0 >= 0 && b0 < p.num_blocks;
+      const bool good = b0 >= 0 && b0 < p.num_blocks;
       const uint32_t loaded = __ballot_sync(FULL_MASK, good);
-      if (!is_v && __ballot_sync(FULL_MASK, b0 != kNone && !good) && lane == 0) flag_error(p.err, PKVD_ERR_BLOCK_ID);
       const int stg = t % stages;
       uint64_t* bar = &bars[full0 + stg];
       const uint32_t dst0 = ring + stg * H * kHalf;
       const int kbase = (kt_first + t) * kTcKeys;
       // a segment with a bad block id reads as zeros (like the mma.sync path)
-      if (b0 != kNone && !good) {
+      if (loaded != whole && !good && is_read(kbase + lane * p.seg_rows)) {
+        if (!is_v) flag_error(p.err, PKVD_ERR_BLOCK_ID);
         for (int h = 0; h < H; ++h)
           for (uint32_t o = 0; o < box; o += 16) st_shared_v4(dst0 + h * kHalf + lane * box + o, make_uint4(0u, 0u, 0u, 0u));
         fence_proxy_async_smem();

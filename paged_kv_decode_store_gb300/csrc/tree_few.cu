@@ -138,10 +138,9 @@ __device__ __forceinline__ void copy_tiles(const TcTree& p, uint64_t* bars, uint
   const int nseg = kTcKeys / p.seg_rows;
   const uint32_t whole = (1u << nseg) - 1u;    // at most 16 segments
   if (lane == 0) asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
-  constexpr int kNone = INT_MIN;               // a segment of rows that are not read: nothing to load
+  constexpr int kNone = -1;                    // a segment of rows that are not read: nothing to load
   bool ok = true;
   int stg = 0, landed = 0;                     // next stage; phases of kVCut
-  bool cutting = false;                        // a copy is under way to kVCut of the next stage
   uint32_t par = 1;                            // parity of its release (nothing to wait for in the first round)
   auto wait = [&](int bar, uint32_t parity) {
     if (ok) ok = __all_sync(FULL_MASK, wait_bounded(&bars[bar], parity));
@@ -154,10 +153,10 @@ __device__ __forceinline__ void copy_tiles(const TcTree& p, uint64_t* bars, uint
     const Sight sight(cur, p.plan.window);
     const int32_t* table = p.tables + (int64_t)cur.seq * p.max_blocks;
     const int n = cur.n, hk = cur.hk, lo = cur.lo, hi = cur.hi, kt_last = cur.kt_last, late = cur.late;
+    auto is_read = [&](int ks) { return lane < nseg && ks <= hi && ks + p.seg_rows - 1 >= lo; };
     auto fetch = [&](int t) -> int {
       const int ks = tile_at(kt_last, n, late, t) * kTcKeys + lane * p.seg_rows;
-      if (t >= n || lane >= nseg || ks > hi || ks + p.seg_rows - 1 < lo) return kNone;
-      return max(__ldg(table + (ks >> p.block_shift)), -1);     // (no id is taken for kNone)
+      return t < n && is_read(ks) ? __ldg(table + (ks >> p.block_shift)) : kNone;
     };
     int b[4];                                  // block ids of tile t and the three after it
 #pragma unroll
@@ -175,7 +174,7 @@ __device__ __forceinline__ void copy_tiles(const TcTree& p, uint64_t* bars, uint
       uint32_t bytes = H * kHalf;
       if (loaded != whole) {
         bytes = (uint32_t)__popc(loaded) * box * H;
-        const uint32_t bad = __ballot_sync(FULL_MASK, b[0] != kNone && !good);
+        const uint32_t bad = __ballot_sync(FULL_MASK, !good && is_read(ks));
         if (bad) {                             // a bad block id reads as zeros
           if (lane == 0) flag_error(p.err, PKVD_ERR_BLOCK_ID);
           if ((bad >> lane) & 1u) {
@@ -194,7 +193,6 @@ __device__ __forceinline__ void copy_tiles(const TcTree& p, uint64_t* bars, uint
       }
       if (cut) {
         wait(kVCut + stg, (landed >> stg) & 1);
-        cutting = !ok;
         if (!ok) break;
         landed ^= 1 << stg;
         if (tidy_values<T, H>(tile, kbase, sight, lane) && lane == 0) cur.odd = 1;
@@ -216,7 +214,8 @@ __device__ __forceinline__ void copy_tiles(const TcTree& p, uint64_t* bars, uint
     flag_error(p.err, PKVD_ERR_TIMEOUT);
     // (a stage's full barrier is behind its release, or one phase ahead of it)
     for (int u = 0; u < kStages; ++u) wait_bounded(&bars[full + u], (par ^ (u < stg ? 0u : 1u)) ^ 1u);
-    if (cutting) wait_bounded(&bars[kVCut + stg], (landed >> stg) & 1);
+    // (a V tile on its way to the cut barrier; without one this runs into its limit, which costs a loop nothing)
+    if (IS_V) wait_bounded(&bars[kVCut + stg], (landed >> stg) & 1);
   }
 }
 

@@ -178,23 +178,22 @@ __device__ __forceinline__ void tree_copy_kv(const TcTree& p, uint64_t* bars, ui
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&p.tmap_k)) : "memory");
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&p.tmap_v)) : "memory");
   }
-  constexpr int kNone = INT_MIN;             // a segment of rows that are not read: nothing to load
+  constexpr int kNone = -1;                  // a segment of rows that are not read: nothing to load
   bool ok = true;
   int kstg = 0, vstg = 0, landed = 0;        // next stages; phases of kVCut
-  bool cutting = false;                      // a copy is under way to kVCut of the next V stage
   uint32_t kpar = 1, vpar = 1;               // parities of their release (nothing to wait for in the first round)
   auto wait = [&](int bar, uint32_t parity) {
     if (ok) ok = __all_sync(FULL_MASK, wait_bounded(&bars[bar], parity));
   };
   // one operand of a tile into a stage, whose block id is b in lane s
-  auto copy = [&](const CUtensorMap* map, uint32_t dst, int bar, int ks, int hk, int b) {
+  auto copy = [&](const CUtensorMap* map, uint32_t dst, int bar, int ks, int hk, int b, auto is_read) {
     const bool good = (uint32_t)b < p.block_limit;
     const uint32_t loaded = __ballot_sync(FULL_MASK, good);
     uint32_t bytes = H * kHalf;
     dst += lane * box;
     if (loaded != whole) {
       bytes = (uint32_t)__popc(loaded) * box * H;
-      const uint32_t bad = __ballot_sync(FULL_MASK, b != kNone && !good);
+      const uint32_t bad = __ballot_sync(FULL_MASK, !good && is_read(ks));
       if (bad) {                             // a bad block id reads as zeros
         if (lane == 0) flag_error(p.err, PKVD_ERR_BLOCK_ID);
         if ((bad >> lane) & 1u) {
@@ -221,15 +220,15 @@ __device__ __forceinline__ void tree_copy_kv(const TcTree& p, uint64_t* bars, ui
     const int n = cur.n, hk = cur.hk, lo = cur.lo, hi = cur.hi, kt_last = cur.kt_last;
     const Sight sight(cur, p.plan.window);
     auto key_of = [&](int t) { return (kt_last - t) * kTcKeys + lane * p.seg_rows; };
+    auto is_read = [&](int ks) { return lane < nseg && ks <= hi && ks + p.seg_rows - 1 >= lo; };
     auto fetch = [&](int t) -> int {
       const int ks = key_of(t);
-      if (t >= n || lane >= nseg || ks > hi || ks + p.seg_rows - 1 < lo) return kNone;
-      return max(__ldg(table + (ks >> p.block_shift)), -1);     // (no id is taken for kNone)
+      return t < n && is_read(ks) ? __ldg(table + (ks >> p.block_shift)) : kNone;
     };
     auto copy_k = [&](int t, int b) {
       wait(kKEmpty + kstg, kpar);
       if (!ok) return;
-      copy(&p.tmap_k, base + L::kK + kstg * H * kHalf, kKFull + kstg, key_of(t), hk, b);
+      copy(&p.tmap_k, base + L::kK + kstg * H * kHalf, kKFull + kstg, key_of(t), hk, b, is_read);
       if (++kstg == kKStages) kstg = 0, kpar ^= 1;
     };
     int b[4];                                // block ids of V tile t and the three after it
@@ -246,10 +245,9 @@ __device__ __forceinline__ void tree_copy_kv(const TcTree& p, uint64_t* bars, ui
       const int kbase = (kt_last - t) * kTcKeys;
       const bool cut = !sight.whole(kbase);
       const uint32_t dst = base + L::kV + vstg * H * kHalf;
-      copy(&p.tmap_v, dst, (cut ? kVCut : kVFull) + vstg, kbase + lane * p.seg_rows, hk, b[0]);
+      copy(&p.tmap_v, dst, (cut ? kVCut : kVFull) + vstg, kbase + lane * p.seg_rows, hk, b[0], is_read);
       if (cut) {
         wait(kVCut + vstg, (landed >> vstg) & 1);
-        cutting = !ok;
         if (!ok) break;
         landed ^= 1 << vstg;
         if (tidy_values<T, H>(dst, kbase, sight, lane) && lane == 0) cur.odd = 1;
@@ -272,7 +270,8 @@ __device__ __forceinline__ void tree_copy_kv(const TcTree& p, uint64_t* bars, ui
     // (a stage's full barrier is behind its release, or one phase ahead of it)
     for (int u = 0; u < kKStages; ++u) wait_bounded(&bars[kKFull + u], (kpar ^ (u < kstg ? 0u : 1u)) ^ 1u);
     for (int u = 0; u < kVStages; ++u) wait_bounded(&bars[kVFull + u], (vpar ^ (u < vstg ? 0u : 1u)) ^ 1u);
-    if (cutting) wait_bounded(&bars[kVCut + vstg], (landed >> vstg) & 1);
+    // (a V tile on its way to the cut barrier; without one this runs into its limit, which costs a loop nothing)
+    wait_bounded(&bars[kVCut + vstg], (landed >> vstg) & 1);
   }
 }
 
