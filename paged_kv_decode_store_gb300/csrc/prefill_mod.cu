@@ -51,7 +51,6 @@
 // clocks a round: beside four busy softmax warps it gets an instruction in about
 // every thirteenth clock), 18 items and Q.
 // Row = token * G + query head of the group, as in the plain kernel.
-#include <climits>
 #include <cmath>
 
 #include "common.cuh"

@@ -39,7 +39,6 @@
 // are read K-major (stride between 8-row groups 1024 B); V is read
 // MN-major (head_dim contiguous: 1024 B between 8-key groups, one half-tile
 // between 64-column halves).
-#include <climits>
 #include <cmath>
 
 #include "common.cuh"

@@ -3,7 +3,6 @@
 // of K, V and Q, and the barriers between them.
 #pragma once
 
-#include <climits>
 
 #include "common.cuh"
 #include "launch.h"
