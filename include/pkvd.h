@@ -435,7 +435,8 @@ pkvd_status pkvd_rope(void* q_out, int64_t q_out_stride, const void* q, int64_t 
 /*
  * pkvd_rope_store_paged -- pkvd_rope and pkvd_kv_store_paged in one kernel:
  * row i's query and key turn by the position of its newest token
- * (context_lens[i] - 1); the query goes to q_out, the key and the (unrotated)
+ * (context_lens[i] - 1: not for a sequence whose cache was cut by an eviction,
+ * see pkvd_evict_select); the query goes to q_out, the key and the (unrotated)
  * value to the token's cache slot.
  * Inputs: q, k, v rows at their strides (as pkvd_rope), cache dtype;
  *         block_tables, context_lens and slot_mapping as in
@@ -577,7 +578,9 @@ pkvd_status pkvd_prefill_attention_mod(void* out, const void* q, const pkvd_cach
  *         and sums are fp32; PKVD_PATH_TC rounds the softmax weights to the cache's
  *         type for the product with V (f16 ones keep their bits down to 2^-17 of
  *         the row's largest; bf16 ones are taken against a reference up to 2^24
- *         below the largest, so values should be below 2^80 in size).
+ *         below the largest, so values should be below 2^80 in size) and takes a
+ *         cap's tanh to 7.2e-6 of a score.  PKVD_PATH_FMA keeps fp32 weights, and
+ *         the tanh to 10^-6 (f32 caches: a few 2^-24).
  * workspace: pkvd_tree_workspace_bytes(...) bytes, 256-byte aligned, no
  *         initialisation; calls that share one must not overlap on the GPU.
  * path:   PKVD_PATH_TC (tcgen05; 16-bit caches with block_size >= 8 whose strides
@@ -666,6 +669,13 @@ pkvd_status pkvd_compact_cache(const pkvd_cache* cache, const int32_t* block_tab
  *         aligned, no initialisation; calls that share one must not overlap.
  * Requirements, status codes and device errors of the decode call; keys of a bad
  *         block are given 0.  PKVD_INVALID_ARG for other weight_heads.
+ * With a cap and a 16-bit cache a score is off by 10^-6 of itself, as in the
+ *         decode call, and its weight, relatively, by as much times the score.
+ * Only this call counts: what a prompt's rows (pkvd_prefill_attention) or drafted
+ *         ones (pkvd_tree_attention) give a position is not handed on.  Right after
+ *         a prompt, weights that started with zeros are equal, and
+ *         pkvd_evict_select keeps the lowest positions among equals: decode some
+ *         tokens first, or count the prompt's weights some other way.
  */
 pkvd_status pkvd_decode_weights_workspace_bytes(int32_t num_seqs, int32_t num_q_heads, int32_t head_dim,
                                                 int32_t max_context_len, int32_t sm_count, size_t* bytes);
@@ -695,6 +705,14 @@ pkvd_status pkvd_paged_decode_attention_weights(void* out, const void* q, const 
  *         must not overlap it.
  * Device errors: a length outside [0, length] sets PKVD_ERR_CONTEXT and is
  *         clamped.
+ * Afterwards a sequence's length counts rows, not tokens, and with a list for each
+ *         head a row is another token in each of them.  Calls that take a position
+ *         from a length or a row mean something else then:
+ *         pkvd_rope_store_paged turns q and the new key by context_lens[i] - 1,
+ *         which lies before tokens that were kept (give pkvd_rope the token's own
+ *         position and store with pkvd_kv_store_paged); a window and alibi_slopes
+ *         of the decode calls count rows (use neither); pkvd_tree_attention's
+ *         window and slopes likewise.
  */
 pkvd_status pkvd_evict_select(int32_t* positions, int32_t* counts, float* weights_out, const float* weights,
                               int64_t seq_stride, int64_t head_stride, int32_t length, const int32_t* context_lens,

@@ -10,8 +10,8 @@
 // so that softmax work and accumulators shrink with N, S^T has two buffers (the
 // next scores are there before the last weights are done) and one row of tiles
 // suffices: no second stream to join.  32 sequences of 8 nodes over 2,048
-// tokens, 48 + 8 heads of 128 in bf16: 62 us instead of 71, 275 MB of K and V at 0.66
-// of the copy rate (128 sequences: 188 us, 0.87; the rest is start, first and last
+// tokens, 48 + 8 heads of 128 in bf16: 62 us instead of 71, 275 MB of K and V at 0.65
+// of the copy rate (128 sequences: 188 us, 0.86; the rest is start, first and last
 // tiles and the merge).  A tile takes the larger of its copies, 2,600 clocks at
 // head_dim 128, and the chain from scores to weights, 2,200, which bounds head_dim 64.
 //

@@ -49,8 +49,10 @@ def paged_decode_attention_weights(q: torch.Tensor, k_cache: torch.Tensor, v_cac
     """paged_decode_attention that also counts what each cached position was given:
     (out, weights_out) with weights_out[i, h, j] = weights[i, h, j] + the softmax
     weights of position j summed over KV head h's query heads (all of them when
-    weights has one head).  weights: float32 [B, Hkv or 1, >= max_context_len];
-    weights_out: a tensor like it, by default weights itself."""
+    weights has one head).  weights: float32 [B, Hkv or 1, >= max_context_len], no
+    two rows over one another; weights_out: a tensor like it, by default weights
+    itself.  Only decoded tokens count: prefill_attention and tree_attention hand no
+    weights on, so right after a prompt all are equal."""
     B, Hq, D = q.shape if q.dim() == 3 else (0, 0, 0)
     dev = q.device
     c = cache_desc(k_cache, v_cache)
@@ -79,7 +81,12 @@ def evict_select(weights: torch.Tensor, context_lens: torch.Tensor, keep: int, s
     heaviest of the others (float32 weights [B, heads, length]), ascending, -1
     behind.  weights_out (a tensor like weights; weights itself: in place) gets
     the weights that stay, closed up, zeros behind.  Pass positions and counts to
-    compact_cache; counts are the new context_lens."""
+    compact_cache; counts are the new context_lens.
+
+    They count rows then, not tokens, and with a list for each head a row is another
+    token in each: give rope the tokens' own positions and store with kv_store_paged
+    (rope_store_paged turns by context_lens - 1), and decode without window and
+    alibi_slopes, which would count rows."""
     dev, B = weights.device, context_lens.shape[0]
     heads, length, s_seq, s_head, w = _weight_rows(weights, "weights", dev, B)
     with on_stream(stream, dev):

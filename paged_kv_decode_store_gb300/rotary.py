@@ -95,7 +95,9 @@ def rope_store_paged(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, block_ta
                      err: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """Decode step: row i's q and k turned by position context_lens[i] - 1, the
     key and the value stored in that token's cache slot (kv_store_paged), the
-    rotated q returned (q_out may be q; rows without a context get zeros)."""
+    rotated q returned (q_out may be q; rows without a context get zeros).  Not for
+    a sequence that evict_select has cut: its context_lens count rows, so rope with
+    the tokens' own positions and kv_store_paged."""
     c, dev, qshape, B, rows = _store(q, k, v, k_cache, v_cache)
     with on_stream(stream, dev):
         q_out, qos, qop = _out(q_out, q, qshape, "q_out")
