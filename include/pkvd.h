@@ -615,7 +615,8 @@ pkvd_status pkvd_tree_attention(void* out, const void* q, const pkvd_cache* cach
  *         (cached_i + node), -1 behind; first int32 [num_seqs] = cached_i; counts
  *         int32 [num_seqs], the path's nodes (0 for an empty tree); tokens int32
  *         [num_seqs, max_path] = target of the path's nodes, the new tokens of
- *         this step (the last one is the next tree's node 0), -1 behind.
+ *         this step (the last one is the next tree's node 0), -1 behind.  Outputs
+ *         must not overlap inputs or one another.
  *         pkvd_compact_cache(positions, first, counts) then moves the path's rows
  *         to where the sequence goes on.
  * Device errors: as pkvd_tree_attention (such a sequence gets counts 0, first 0).

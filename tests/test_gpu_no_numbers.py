@@ -91,7 +91,7 @@ def test_decode_with_weights(case, ctx):
 
 @pytest.mark.parametrize("case", DECODE, ids=lambda c: "-".join(map(str, c)))
 def test_keys_at_minus_infinity(case):
-    """Scores of -inf, by the pieceful: those keys weigh nothing, and the others what they do without them."""
+    """Scores of -inf, whole pieces of a row among them: those keys weigh nothing, the others what they do without them."""
     pk = require_gpu()
     name, hq, hkv, d, path = case
     dt, G, ctx = DT[name], hq // hkv, 1601
